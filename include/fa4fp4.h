@@ -63,7 +63,9 @@ typedef enum {
   FA4FP4_ERR_ALIGNMENT = 3,      /* a pointer is not 16-byte aligned */
   FA4FP4_ERR_CUDA = 4,           /* a CUDA runtime/driver call failed */
   FA4FP4_ERR_DEVICE_TIMEOUT = 5, /* a kernel's bounded wait expired */
-  FA4FP4_ERR_WORKSPACE = 6       /* workspace missing or too small */
+  FA4FP4_ERR_WORKSPACE = 6,      /* workspace missing or too small */
+  FA4FP4_ERR_DEVICE_INDEX = 7,   /* a cache call met a page index, length or count out of range */
+  FA4FP4_ERR_DEVICE_NONFINITE = 8 /* a NaN or infinity was given to the cache */
 } fa4fp4_status;
 
 typedef enum { FA4FP4_FMT_MXFP4 = 0, FA4FP4_FMT_MXFP8_E4M3 = 1 } fa4fp4_format;
@@ -295,9 +297,133 @@ FA4FP4_API fa4fp4_status fa4fp4_directp_codes(const float* s, int64_t n, float m
  * bounded-wait routine every kernel of the library uses (2 s limit). */
 FA4FP4_API fa4fp4_status fa4fp4_watchdog_selftest(int64_t limit_ns, void* stream);
 
+/* The 8-bit key/value cache: a paged pool of K and V as E4M3 codes with one
+ * E8M0 scale per page and head, the calls that fill it, attend over it, read
+ * it sparsely and cut it back.
+ *
+ * A pool has num_pages pages of `page` tokens (16, 32, 64 or 128) for Hkv heads
+ * of d (64 or 128):
+ *     k_codes, v_codes    [num_pages][Hkv][page][d] E4M3 bytes
+ *     k_scales, v_scales  [num_pages][Hkv] E8M0 bytes
+ *     k_bounds            [num_pages][Hkv][2][d] E4M3 bytes: the least and the
+ *                         greatest K code of the page's tokens, elementwise,
+ *                         under the page's K scale
+ * and holds any number of sequences: sequence b's token i lies in slot i % page
+ * of pool page page_table[b][i / page] (int32, [B][max_pages], device memory),
+ * and lens[b] (int32, device memory) is its number of tokens, at most
+ * max_pages * page.  Calls that only read may share pages among sequences;
+ * fa4fp4_cache_append and the destination of fa4fp4_cache_evict need pages of
+ * their own.  Code bytes in [0, lens) are finite (fa4fp4_cache_append writes no
+ * others); what lies behind a sequence's end may be anything.
+ *
+ * The lengths and page indexes are device data, so the host cannot check them.
+ * Every kernel does: a page index outside the pool, a length or count outside
+ * its range, or a token without room in the table is not followed (its keys
+ * count as absent, its tokens are not stored), nothing out of bounds is read or
+ * written, and the next fa4fp4_sync_status returns FA4FP4_ERR_DEVICE_INDEX.
+ *
+ * page_table, lens, q_lens, n_new, pages, weights and lse inputs need 4-byte
+ * alignment, all else 16-byte.  num_pages, max_pages >= 1; B <= 65535, Hkv <=
+ * 32767, max_pages * page <= 2^30, B * Hq * T < 2^31.  T == 0 is an empty
+ * problem too.  The calls read the structure during the call only. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  void* k_bounds;
+  int num_pages, Hkv, page, d;
+} fa4fp4_cache;
+
+/* Stores the new tokens k, v (bf16 [B][Hkv][T][d]) of every sequence behind its
+ * lens[b] tokens: n_new[b] <= T of them (NULL: T).  lens is not changed.  Per
+ * page, head and tensor: X = the least integer >= -127 with |x| <= 448 * 2^X
+ * for all new tokens x of the page, at least the page's exponent when the page
+ * already holds tokens (in slots before lens[b]); codes E4M3(x * 2^-X) rounded
+ * to nearest even; when X grows the older codes become E4M3(code * 2^(X_old -
+ * X)).  (The OCP exponent of fa4fp4_quantize would saturate magnitudes above
+ * 448 * 2^X.)  k_bounds follows.  Slots behind the new end are not touched.  A
+ * NaN is stored as 0, an infinity as the largest code of its sign; neither
+ * counts for X, and the next fa4fp4_sync_status returns
+ * FA4FP4_ERR_DEVICE_NONFINITE. */
+FA4FP4_API fa4fp4_status fa4fp4_cache_append(const fa4fp4_cache* cache, const void* k, const void* v,
+                                             const int* page_table, const int* lens, const int* n_new, int B,
+                                             int max_pages, int T, void* stream);
+
+/* Attention of T new query tokens per sequence over the cache.  q: bf16
+ * [B][Hq][T][d], query head h reads kv head h / (Hq / Hkv); lens counts the new
+ * tokens in (append first); sequence b has q_lens[b] <= T query tokens (NULL:
+ * T), its last ones: token t sees keys 0 .. lens[b] - q_lens[b] + t when
+ * causal, else all.  pages != NULL (int32 [B][Hkv][T][n_sel], as
+ * fa4fp4_cache_select writes it): token t of kv head hk sees, of those keys,
+ * only the ones in the pages listed for it (indexes into the sequence's row of
+ * page_table, -1 for none; a page listed twice counts twice); n_sel = 0
+ * without it.
+ *   s = softmax_scale * q.k, o = softmax(s) v, lse = ln sum e^s (nullable)
+ * o: [B][Hq][T][d], f32 or bf16 per out_dtype; lse: f32 [B][Hq][T].  A token
+ * that sees no key gets o = 0 and lse = -inf; rows t >= q_lens[b] are not
+ * written.  The products are exact in the codes; P is rounded to f16 under a
+ * factor 2^15 (f32 output: to the sum of two f16), the sums are FP32, the
+ * result does not depend on anything but the arguments.  `workspace`: at least
+ * fa4fp4_cache_fwd_workspace_bytes(...) bytes of device memory
+ * (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs. */
+FA4FP4_API size_t fa4fp4_cache_fwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page, int max_pages,
+                                                   int n_sel);
+FA4FP4_API fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void* q, const int* page_table,
+                                          const int* lens, const int* q_lens, const int* pages, int B, int Hq, int T,
+                                          int max_pages, int n_sel, float softmax_scale, int causal, void* o,
+                                          int out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/* The pages whose keys could score highest, for every query token and kv head.
+ * Among the pages that hold keys which token t sees (causal), the one with its
+ * last visible key is taken, and of the others those with the highest
+ *   sum over the kv head's query heads, sum over dims of max(q lo, q hi)
+ * (lo, hi: the page's bounds as values), ties to the lowest page, n_sel in all;
+ * all of them where there are no more.  pages (int32 [B][Hkv][T][n_sel])
+ * receives them in ascending order, then -1; rows t >= q_lens[b] are all -1.
+ * The set is that of the real-valued bounds: FP32 sums decide only where their
+ * error bounds allow it, the rest is evaluated in 64 bits.  max_pages <= 2^18,
+ * Hkv * T <= 65535.  `workspace` as for fa4fp4_cache_fwd. */
+FA4FP4_API size_t fa4fp4_cache_select_workspace_bytes(int B, int Hkv, int T, int max_pages);
+FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const void* q, const int* page_table,
+                                             const int* lens, const int* q_lens, int B, int Hq, int T, int max_pages,
+                                             int n_sel, int* pages, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/* The attention weight that every cached token received from these queries:
+ *   weight_out[b][hk][j] = weight_in[b][hk][j] + sum over the query heads of hk
+ *                          and the tokens t that see j of e^(s - lse)
+ * for j < lens[b], with fa4fp4_cache_fwd's arguments and the lse that it wrote
+ * (rows with lse = -inf add nothing).  weights: f32 [B][Hkv][max_pages * page];
+ * weight_out may be weight_in; entries j >= lens[b] are not written. */
+FA4FP4_API fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const float* lse,
+                                            const int* page_table, const int* lens, const int* q_lens, int B, int Hq,
+                                            int T, int max_pages, float softmax_scale, int causal,
+                                            const float* weight_in, float* weight_out, void* stream);
+
+/* Cuts every sequence back to `budget` tokens per kv head: the `recent` newest
+ * and of the others those with the largest weight (f32 [B][Hkv][max_pages *
+ * page]; NaN below everything), ties to the lowest position; all where there
+ * are no more than `budget`.  The kept tokens go, in order, into the pages
+ * dst_table[b][0 ..] (int32 [B][dst_pages] with dst_pages * page >= budget;
+ * pages of the same pool that no sequence of the call reads and no other row
+ * writes), fitted to the destination's scales by the append's rule.  Sequence b
+ * is then dst_table's row with new_lens[b] = min(lens[b], budget) tokens.
+ * kept: int32 [B][Hkv][budget], the kept positions in ascending order, then -1.
+ * weight_out (nullable): f32 [B][Hkv][dst_pages * page], the kept tokens'
+ * weights, then 0; not the weight array itself.  0 <= recent <= budget,
+ * budget >= 1. */
+FA4FP4_API fa4fp4_status fa4fp4_cache_evict(const fa4fp4_cache* cache, const int* page_table, const int* lens,
+                                            const float* weight, const int* dst_table, int B, int max_pages,
+                                            int dst_pages, int budget, int recent, int* new_lens, int* kept,
+                                            float* weight_out, void* stream);
+
 /* Synchronizes `stream`, then returns FA4FP4_ERR_CUDA for a pending CUDA error
- * or FA4FP4_ERR_DEVICE_TIMEOUT if any kernel's bounded wait expired since the
- * last call (the flag is cleared), else FA4FP4_OK. */
+ * or, for what kernels reported since the last call (the flags are cleared),
+ * FA4FP4_ERR_DEVICE_TIMEOUT if any bounded wait expired,
+ * FA4FP4_ERR_DEVICE_INDEX or FA4FP4_ERR_DEVICE_NONFINITE for what the cache
+ * calls met, else FA4FP4_OK. */
 FA4FP4_API fa4fp4_status fa4fp4_sync_status(void* stream);
 
 /* Static description of a status code. */

@@ -5,6 +5,8 @@
 #include <cstring>
 #include <mutex>
 #include "../../include/fa4fp4.h"
+#include "cache.h"
+#include "common.cuh"
 #include "internal.h"
 
 using namespace fa4;
@@ -101,6 +103,10 @@ fa4fp4_status check_dims(int B, int Hq, int Hkv, int N, int d) {
 
 }  // namespace
 
+namespace fa4 {
+unsigned* device_error_word() { return err_word(); }
+}  // namespace fa4
+
 extern "C" {
 
 const char* fa4fp4_status_string(int s) {
@@ -112,6 +118,8 @@ const char* fa4fp4_status_string(int s) {
     case FA4FP4_ERR_CUDA: return "CUDA error";
     case FA4FP4_ERR_DEVICE_TIMEOUT: return "device pipeline wait timed out";
     case FA4FP4_ERR_WORKSPACE: return "workspace missing or too small";
+    case FA4FP4_ERR_DEVICE_INDEX: return "a page index, length or count on the device is out of range";
+    case FA4FP4_ERR_DEVICE_NONFINITE: return "a NaN or infinity was given to the cache";
     default: return "unknown status";
   }
 }
@@ -421,6 +429,9 @@ fa4fp4_status fa4fp4_sync_status(void* stream) {
   if (host) {
     unsigned zero = 0;
     cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (host & FA4_DEVERR_TIMEOUT) return FA4FP4_ERR_DEVICE_TIMEOUT;
+    if (host & FA4_DEVERR_INDEX) return FA4FP4_ERR_DEVICE_INDEX;
+    if (host & FA4_DEVERR_NONFINITE) return FA4FP4_ERR_DEVICE_NONFINITE;
     return FA4FP4_ERR_DEVICE_TIMEOUT;
   }
   return FA4FP4_OK;

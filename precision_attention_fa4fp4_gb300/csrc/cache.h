@@ -1,0 +1,81 @@
+// cache.h -- host-side declarations of the 8-bit key/value cache kernels.  Not
+// part of the ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fa4 {
+
+// A paged pool and the sequences that live in it.  Page `p`, head `h`: codes
+// [page][d] at ((p * Hkv + h) * page) * d, one E8M0 scale byte at p * Hkv + h,
+// the K bounds [2][d] (elementwise least and greatest code) at
+// (p * Hkv + h) * 2 * d.
+struct CacheView {
+  uint8_t *k, *v, *ks, *vs, *kb;
+  const int* table;      // [B][max_pages]
+  const int* lens;       // [B]
+  int num_pages, Hkv, page, d, B, max_pages;
+  unsigned* err;
+};
+
+struct CacheAppendParams {
+  CacheView c;
+  const void *k, *v;     // bf16 [B][Hkv][T][d]
+  const int* n_new;      // [B] or nullptr (T)
+  int T;
+};
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t st);
+
+struct CacheFwdParams {
+  CacheView c;
+  const void* q;         // bf16 [B][Hq][T][d]
+  const int* q_lens;     // [B] or nullptr (T)
+  const int* pages;      // [B][Hkv][T][n_sel] selected pages, or nullptr (all pages)
+  void* o;
+  float* lse;
+  float* part;           // workspace: split partials
+  int Hq, T, n_sel, causal, out_bf16;
+  float scale, c2;       // softmax scale, fl32(scale * log2 e)
+};
+// Workspace of the split forward.
+size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages);
+cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st);
+
+struct CacheSelectParams {
+  CacheView c;
+  const void* q;
+  const int* q_lens;
+  int Hq, T, n_sel;
+  float2* score;         // workspace [B][Hkv][T][max_pages]: FP32 bound and its error
+  int* out;              // [B][Hkv][T][n_sel]
+};
+cudaError_t launch_cache_select(const CacheSelectParams& p, cudaStream_t st);
+
+struct CacheWeighParams {
+  CacheView c;
+  const void* q;
+  const float* lse;      // [B][Hq][T]
+  const int* q_lens;
+  const float* w_in;     // [B][Hkv][max_pages * page]
+  float* w_out;
+  int Hq, T, causal;
+  float c2;
+};
+cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st);
+
+struct CacheEvictParams {
+  CacheView c;
+  const float* w;        // [B][Hkv][max_pages * page]
+  const int* dst;        // [B][dst_pages]
+  int dst_pages, budget, recent;
+  int* new_lens;         // [B]
+  int* kept;             // [B][Hkv][budget]
+  float* w_out;          // [B][Hkv][dst_pages * page]
+};
+cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t st);
+
+// The library's device error word on the current device (nullptr on failure).
+unsigned* device_error_word();
+
+}  // namespace fa4

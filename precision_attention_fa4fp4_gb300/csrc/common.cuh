@@ -21,6 +21,8 @@
 // error codes written to the device error word (bit flags)
 enum : unsigned {
   FA4_DEVERR_TIMEOUT = 1u,
+  FA4_DEVERR_INDEX = 2u,       // cache: a page index, length or count outside its range
+  FA4_DEVERR_NONFINITE = 4u,   // cache: a NaN or infinity to be stored
 };
 
 namespace fa4 {
