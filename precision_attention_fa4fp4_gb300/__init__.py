@@ -13,6 +13,9 @@ def __getattr__(name):
     import importlib
     api = importlib.import_module(__name__ + ".api")
     try:
-        return getattr(api, name)
+        value = getattr(api, name)
     except AttributeError:
         raise AttributeError(name) from None
+    if callable(value):
+        globals()[name] = value     # later uses find it here
+    return value

@@ -609,9 +609,9 @@ class _on:
 
     def __init__(self, device):
         self.device = device.index
-        self.before = torch.cuda.current_device()
 
     def __enter__(self):
+        self.before = torch.cuda.current_device()
         if self.before != self.device:
             torch.cuda.set_device(self.device)
 
@@ -664,7 +664,8 @@ def _at(t):
 
 
 def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone: a torch.cuda.Stream object costs more than the launch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,

@@ -105,6 +105,10 @@ fa4fp4_status check_dims(int B, int Hq, int Hkv, int N, int d) {
 
 namespace fa4 {
 unsigned* device_error_word() { return err_word(); }
+bool make_rows_map(CUtensorMap* m, const void* base, int row_bytes, uint64_t rows, uint32_t box_rows) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, row_bytes, rows, 1, row_bytes, box_rows,
+                  row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
 }  // namespace fa4
 
 extern "C" {

@@ -74,6 +74,14 @@ FA4_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Raises the bytes that the current phase of an mbarrier waits for, before the
+// arrival that lets the phase end.
+FA4_DEV void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+FA4_DEV uint4 lds16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+FA4_DEV uint2 lds8(const void* p) { return *reinterpret_cast<const uint2*>(p); }
+
 // Transpose of an 8x8 matrix of 16-bit values held two to a lane.
 FA4_DEV uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;

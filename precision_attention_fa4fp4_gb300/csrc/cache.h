@@ -3,6 +3,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fa4 {
@@ -28,17 +29,19 @@ struct CacheAppendParams {
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t st);
 
 struct CacheFwdParams {
+  CUtensorMap tm_k, tm_v;  // codes as rows of d bytes, boxes of cache_fwd_box(page) rows
   CacheView c;
   const void* q;         // bf16 [B][Hq][T][d]
   const int* q_lens;     // [B] or nullptr (T)
   const int* pages;      // [B][Hkv][T][n_sel] selected pages, or nullptr (all pages)
   void* o;
   float* lse;
-  float* part;           // workspace: split partials
+  uint8_t* part;         // workspace: counter words, then split partials
   int Hq, T, n_sel, causal, out_bf16;
   float scale, c2;       // softmax scale, fl32(scale * log2 e)
 };
-// Workspace of the split forward.
+int cache_fwd_box(int page);
+// Workspace of the split forward; 0: more work than one call takes.
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages);
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st);
 
@@ -75,6 +78,9 @@ struct CacheEvictParams {
 };
 cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t st);
 
+// Tensor map of `rows` rows of `row_bytes` (64 or 128) bytes for boxes of
+// box_rows whole rows, swizzled over their whole width.
+bool make_rows_map(CUtensorMap* m, const void* base, int row_bytes, uint64_t rows, uint32_t box_rows);
 // The library's device error word on the current device (nullptr on failure).
 unsigned* device_error_word();
 

@@ -102,13 +102,19 @@ fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void* q, const i
   if (!aligned(q, 16) || !aligned(o, 16) || (lse && !aligned(lse, 16)) || (pages && !aligned(pages, 4)))
     return FA4FP4_ERR_ALIGNMENT;
   const size_t need = cache_fwd_workspace(B, Hq, cache->Hkv, T, cache->d, n_sel, cache->page, max_pages);
+  if (need == 0) return FA4FP4_ERR_UNSUPPORTED;       // 2^31 units of 128 keys and a row block, or more
   if (!workspace || workspace_bytes < need) return FA4FP4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return FA4FP4_ERR_ALIGNMENT;
   CacheFwdParams p;
   memset(&p, 0, sizeof(p));
   if (!view(&p.c, cache, page_table, lens, B, max_pages)) return FA4FP4_ERR_CUDA;
   p.q = q; p.q_lens = q_lens; p.pages = pages; p.o = o; p.lse = lse;
-  p.part = static_cast<float*>(workspace);
+  p.part = static_cast<uint8_t*>(workspace);
+  const uint64_t rows = (uint64_t)cache->num_pages * cache->Hkv * cache->page;
+  if (rows >= (1ull << 31)) return FA4FP4_ERR_UNSUPPORTED;
+  if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, rows, cache_fwd_box(cache->page)) ||
+      !make_rows_map(&p.tm_v, cache->v_codes, cache->d, rows, cache_fwd_box(cache->page)))
+    return FA4FP4_ERR_CUDA;
   p.Hq = Hq; p.T = T; p.n_sel = n_sel; p.causal = causal ? 1 : 0;
   p.out_bf16 = out_dtype == FA4FP4_OUT_BF16;
   p.scale = softmax_scale_of(softmax_scale, cache->d);

@@ -14,16 +14,24 @@
 // even as a batch of equal ones, and few rows over a long cache are split over
 // the whole GPU.  A share that covers a row block completely writes its
 // output; the others (at most two per CTA) leave (max, sum, unnormalized o) in
-// the workspace for the second kernel, which joins them in a fixed order.
+// the workspace, and the CTA that is the last to do so for a row block joins
+// them, in a fixed order.  It knows that it is the last from a counter word in
+// the workspace.  The words need no setting up: each carries a mark beside its
+// count, the first arrival that finds none puts it there, and the last leaves
+// the word marked and at zero for the next call.
 //
 // Inside a CTA four warps take 32 keys each of every unit and keep their own
 // running max and sum; they meet once, at the end of a share.
 //
 // Products: m16n8k16 with the keys as rows, so that eight queries fill the
-// instruction: S^T = K Q^T, O^T += V^T P.  The 8-bit rows go from global
-// memory into registers and are the A operand after one conversion (E4M3 ->
-// f16 is exact): no shared memory, no barrier in the loop.  For V^T the two
-// keys of an operand pair are interleaved with a byte permute.  The codes are
+// instruction: S^T = K Q^T, O^T += V^T P.  A lane reads 16 bytes of an 8-bit row
+// at a time and one conversion (E4M3 -> f16, exact) makes them A operands; for
+// V^T the two keys of an operand pair are interleaved with a byte permute.
+// Every warp has its own queue in shared memory, two or three steps of 32 keys
+// deep, filled by TMA (a 4 KB box of K and of V a step) and drained by the warp
+// alone: no barrier between warps in the loop, and far more in flight than
+// loads through L1 allow (16-byte asynchronous copies of the same bytes, and
+// loads into registers, both stopped at 4.8 TB/s).  The codes are
 // used unscaled: K's page scale multiplies the scores, V's page scale
 // multiplies the FP32 sum of the page's products.
 //
@@ -40,8 +48,29 @@ constexpr int NW = 4;                 // warps of a CTA
 constexpr int UNIT = 32 * NW;         // keys of a unit
 constexpr int kSMs = 152;             // GB300
 constexpr float P_BIAS = 15.f;        // log2 of the factor on P
+// the mark of a counter word, in its high 48 bits (no number, no pointer and no
+// pair of floats that a workspace could hold from other use)
+constexpr unsigned long long MARK = 0xfa4c0de5eed5ull;
 
+// Resident CTAs by registers (168 or 255 a thread), and the steps in flight
+// that fill the shared memory they leave.
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int stages(int d, int nt) { return d == 128 && nt == 1 ? 2 : 3; }
+
+// Order of the eight keys of an operand (its row i is key korder(i)), and of
+// the eight 16-byte words of a V row among the lanes: with the 128-byte swizzle
+// both reads are then free of bank conflicts (D = 128).  The 64-byte rows of
+// D = 64 are free of them for K in natural order, and two-way for V.
+template <int D>
+FA4_DEV constexpr int korder(int i) {
+  return D == 128 ? ((i & 1) << 2) | (i & 2) | (i >> 2) : i;
+}
+// Byte of row `row` and byte column `x` in a box of D-byte rows as TMA's swizzle
+// lays it out.
+template <int D>
+FA4_DEV int boxed(int row, int x) {
+  return D == 128 ? row * 128 + (x ^ ((row & 7) << 4)) : row * 64 + (x ^ (((row >> 1) & 3) << 4));
+}
 
 // Row blocks and units of the line.
 struct Line {
@@ -77,70 +106,95 @@ FA4_DEV int seq_units(const CacheFwdParams& p, int b) {
 }
 
 // Units of the sequences before `b` and of all sequences (whole warp).
-FA4_DEV void scan_units(const CacheFwdParams& p, int b, long long& before, long long& total) {
-  long long lo = 0, all = 0;
+FA4_DEV void scan_units(const CacheFwdParams& p, int b, unsigned& before, unsigned& total) {
+  unsigned lo = 0, all = 0;
   for (int i = threadIdx.x % 32; i < p.c.B; i += 32) {
-    const int u = seq_units(p, i);
+    const unsigned u = seq_units(p, i);
     all += u;
     if (i < b) lo += u;
   }
-#pragma unroll
-  for (int o = 16; o; o /= 2) {
-    lo += __shfl_xor_sync(0xffffffffu, lo, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  before = lo;
-  total = all;
+  before = __reduce_add_sync(0xffffffffu, lo);
+  total = __reduce_add_sync(0xffffffffu, all);
 }
 
-// CTAs that get a share: no more than there are units, so that no share is
-// empty (the join reads every slot from the first to the last).
-FA4_DEV int workers(long long total, int grid) { return (int)min((long long)grid, total); }
-// First unit of CTA i's share.
-FA4_DEV long long share_begin(long long total, int i, int n) { return total * i / n; }
-// CTA whose share holds unit u.
-FA4_DEV int share_of(long long u, long long total, int n) {
-  return (int)min((long long)n - 1, ((u + 1) * n - 1) / total);
+// CTAs that get a share.  No share is empty (the join reads every slot from
+// the first to the last), and no CTA is there only to make some shares shorter
+// than the longest: it would add a slot to the join and save nothing.
+FA4_DEV unsigned workers(unsigned total, unsigned grid) {
+  const unsigned longest = (total + grid - 1) / grid;
+  return (total + longest - 1) / longest;
 }
+// The line cut into n shares, the first `rem` of them one unit longer.
+struct Shares {
+  unsigned per, rem;
+  FA4_DEV Shares(unsigned total, unsigned n) : per(total / n), rem(total % n) {}
+  FA4_DEV unsigned begin(unsigned i) const { return i * per + min(i, rem); }
+  FA4_DEV unsigned of(unsigned u) const {          // the share that holds unit u
+    const unsigned cut = rem * (per + 1);
+    return u < cut ? u / (per + 1) : rem + (u - cut) / per;
+  }
+};
 
 template <int D, int NT>
 struct Slot {
   static constexpr int R = 8 * NT;
   static constexpr int FLOATS = R * D + 2 * R;     // o, then m, then l
+  // bytes of the counter words before the slots
+  __host__ __device__ static constexpr size_t counters(unsigned grid) { return ((size_t)grid * 8 + 15) / 16 * 16; }
+};
+
+template <int D, int NT>
+struct Queue {
+  static constexpr int S = stages(D, NT);
+  static constexpr int BYTES = 2 * 32 * D;                       // K and V of 32 keys
+  static constexpr int WARP = S * BYTES;
+  static constexpr int OS = D + 4;                               // row stride of the merge buffer
+  static constexpr int MERGE = NW * 8 * NT * (OS + 2) * 4;       // lies over the queues
+  static constexpr int OFF_BAR = NW * WARP > MERGE ? NW * WARP : MERGE;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NW * S;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;              // and the swizzle's alignment
 };
 
 template <int D, int NT, bool SPLIT, bool SMALLP>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+  using Q = Queue<D, NT>;
   constexpr int R = 8 * NT;
+  constexpr int S = Q::S;
   constexpr int NP = SMALLP ? 2 : 1;               // pages of a warp's 32 keys
-  constexpr int OS = D + 4;                        // row stride of the merge buffer
+  constexpr int OS = Q::OS;
   constexpr int VW = D / 32;                       // 32-bit words of V a lane holds per key
-  __shared__ float s_o[NW][R][OS];
-  __shared__ float s_m[NW][R], s_l[NW][R];
-  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float (*s_o)[R][OS] = reinterpret_cast<float (*)[R][OS]>(smem);
+  float (*s_m)[R] = reinterpret_cast<float (*)[R]>(smem + NW * R * OS * 4);
+  float (*s_l)[R] = s_m + NW;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Q::OFF_BAR) + threadIdx.x / 32 * S;
+  int* s_misc = reinterpret_cast<int*>(smem + Q::OFF_MISC);
+  volatile int* abort_flag = s_misc;
 
   const CacheView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t4 = lane % 4;
   const Line ln = make_line(p.Hq, c.Hkv, p.T, p.pages != nullptr);
   const int G = ln.G;
-  long long before, total;
+  unsigned before, total;
   scan_units(p, 0, before, total);
   total *= ln.nb;
-  const int ctas = workers(total, gridDim.x);
+  const unsigned ctas = workers(total, gridDim.x);
   if (blockIdx.x >= ctas) return;
-  long long at = share_begin(total, blockIdx.x, ctas);
-  const long long begin = at, end = share_begin(total, blockIdx.x + 1, ctas);
+  const Shares shares(total, ctas);
+  const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
+  unsigned at = begin;
   // the sequence that holds unit `at`
   int b = 0, units = 1;
-  long long seq0 = 0;                              // its first unit
+  unsigned seq0 = 0;                               // its first unit
   for (int base = 0;; base += 32) {
     const int i = base + lane;
-    const long long mine = i < c.B ? (long long)seq_units(p, i) * ln.nb : 0;
-    long long inc = mine;
+    const unsigned mine = i < c.B ? (unsigned)seq_units(p, i) * ln.nb : 0;
+    unsigned inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+      const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += up;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, seq0 + inc > at);
@@ -148,21 +202,44 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       const int src = __ffs(hit) - 1;
       b = base + src;
       seq0 += __shfl_sync(0xffffffffu, inc - mine, src);
+      units = __shfl_sync(0xffffffffu, mine, src) / ln.nb;
       break;
     }
     seq0 += __shfl_sync(0xffffffffu, inc, 31);
     if (base + 32 >= c.B) return;                  // cannot happen: at < total
   }
-  units = seq_units(p, b);
+  const int log_p = 31 - __clz(c.page);
+  uint8_t* queue = smem + warp * Q::WARP;
+  unsigned phases = 0;                             // parity of each step's barrier
+  if (lane == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  __syncthreads();
+  // byte offsets of the lane's words in a box of 16 keys
+  int ko[2][D / 64], vo[4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) ko[r][x] = boxed<D>(korder<D>(g) + 8 * r, 64 * x + 16 * t4);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    vo[r] = boxed<D>(korder<D>(2 * t4 + (r & 1)) + 8 * (r >> 1), (D / 8) * (D == 128 ? korder<D>(g) : g) & ~15) +
+            (D == 64 ? 8 * (g & 1) : 0);
+  const int v_dim = (D / 8) * (D == 128 ? korder<D>(g) : g);   // first head dimension of the lane's V bytes
 
   while (at < end) {
-    while (at >= seq0 + (long long)units * ln.nb) {
-      seq0 += (long long)units * ln.nb;
+    while (at >= seq0 + (unsigned)units * ln.nb) {
+      seq0 += (unsigned)units * ln.nb;
       units = seq_units(p, ++b);
     }
     const int rb = (int)((at - seq0) / units);     // row block of the sequence
     const int u0 = (int)((at - seq0) % units);
-    const int u1 = (int)min((long long)units, u0 + (end - at));
+    const int u1 = (int)min((unsigned)units, u0 + (end - at));
     const int h = rb / ln.per_head, sub = rb % ln.per_head;
     const int len = cache_len(c, b);
     const int q_len = cache_count(p.q_lens, b, p.T, c.err);
@@ -179,6 +256,60 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       return gg < G && t < q_len;
     };
     const int* sel = p.pages ? p.pages + (((long long)b * c.Hkv + h) * p.T + sub / ln.QG) * p.n_sel : nullptr;
+
+    // Pool page (-1: none) and first key position of the warp's keys of a
+    // unit; keys that are not there get a position that every query masks.
+    struct Where { int page[NP], pos[NP]; };
+    auto lookup = [&](int u) -> Where {
+      Where w;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int v = u * UNIT + 32 * warp + 16 * i;
+        int lp = v >> log_p;
+        w.page[i] = -1;
+        w.pos[i] = 0x40000000;
+        if (u < u1) {
+          if (sel) {
+            lp = lp < p.n_sel ? __ldg(sel + lp) : -1;
+            if (lp >= c.max_pages || lp < -1) { atomicOr(c.err, FA4_DEVERR_INDEX); lp = -1; }
+          }
+          if (lp >= 0 && ((long long)lp << log_p) < len) w.page[i] = cache_page(c, c.table, b, lp);
+          if (w.page[i] >= 0) w.pos[i] = (lp << log_p) + (v & (c.page - 1));
+        }
+      }
+      return w;
+    };
+    // What a step in flight still needs in registers.
+    struct Step { int pos[NP]; uint32_t ks[NP], vs[NP]; };
+    Step step[S];
+    auto issue = [&](int s, const Where& w) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        step[s].pos[i] = w.pos[i];
+        step[s].ks[i] = step[s].vs[i] = 0;
+        if (w.page[i] >= 0) {
+          const long long ph = (long long)w.page[i] * c.Hkv + h;
+          step[s].ks[i] = __ldg(c.ks + ph);
+          step[s].vs[i] = __ldg(c.vs + ph);
+          if (lane == 0) {
+            const int row = (int)(ph << log_p) + (w.pos[i] & (c.page - 1));
+            uint8_t* to = queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0);
+            // each box counts for itself: a step without a page has none
+            mbar_expect_tx(&bars[s], 2 * (32 / NP) * D);
+            tma_load_3d(to, &p.tm_k, &bars[s], 0, row, 0);
+            tma_load_3d(to + 32 * D, &p.tm_v, &bars[s], 0, row, 0);
+          }
+        }
+      }
+      if (lane == 0) mbar_arrive(&bars[s]);
+    };
+    Where next = lookup(u0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const Where w = next;
+      next = lookup(u0 + s + 1);
+      issue(s, w);
+    }
 
     QFrag<D> q[NT];
     float fx[NT][2];                               // log2-unit factor of columns 2 t4, 2 t4 + 1
@@ -215,72 +346,18 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       l[n][0] = l[n][1] = 0.f;
     }
 
-    // Pool offset (in tokens) and first key position of the warp's keys of a
-    // unit; keys that are not there get a position that every query masks.
-    auto lookup = [&](int u, long long (&tok)[NP], int (&pos)[NP]) {
+    auto body = [&](int st, int u) -> bool {
+      if (!mbar_wait(&bars[st], (phases >> st) & 1, abort_flag, c.err)) return false;
+      phases ^= 1u << st;
+      const uint8_t* from = queue + st * Q::BYTES;
+      int pos[NP];
+      float kxc[NP], vxc[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int v = u * UNIT + 32 * warp + 16 * i;
-        const int j = v / c.page, off = v % c.page;
-        int lp = j;
-        if (sel) {
-          lp = j < p.n_sel ? __ldg(sel + j) : -1;
-          if (lp >= c.max_pages || lp < -1) { atomicOr(c.err, FA4_DEVERR_INDEX); lp = -1; }
-        }
-        int pg = -1;
-        if (u < u1 && lp >= 0 && (long long)lp * c.page < len) pg = cache_page(c, c.table, b, lp);
-        pos[i] = pg >= 0 ? lp * c.page + off : 0x40000000;
-        tok[i] = ((long long)max(pg, 0) * c.Hkv + h) * c.page + off;
+        pos[i] = step[st].pos[i];
+        kxc[i] = e8m0_value(step[st].ks[i]);
+        vxc[i] = e8m0_value(step[st].vs[i]);
       }
-    };
-    uint4 kr[2][2][D / 64];
-    uint32_t vr[2][4][VW];
-    float kx[NP], vx[NP];
-    auto load_k = [&](const long long (&tok)[NP]) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const long long t = SMALLP ? tok[i % NP] : tok[0] + 16 * i;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int k = 0; k < D / 64; ++k)
-            kr[i][r][k] = __ldg(reinterpret_cast<const uint4*>(c.k + (t + g + 8 * r) * D + 64 * k + 16 * t4));
-      }
-    };
-    auto load_v = [&](const long long (&tok)[NP]) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const long long t = SMALLP ? tok[i % NP] : tok[0] + 16 * i;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* a = c.v + (t + 2 * t4 + (k & 1) + 8 * (k >> 1)) * D + (D / 8) * g;
-          if constexpr (VW == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(a));
-            vr[i][k][0] = x.x; vr[i][k][1] = x.y; vr[i][k][2] = x.z; vr[i][k][3] = x.w;
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(a));
-            vr[i][k][0] = x.x; vr[i][k][1] = x.y;
-          }
-        }
-      }
-    };
-    auto load_x = [&](const long long (&tok)[NP]) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const long long ph = tok[i] / c.page;
-        kx[i] = e8m0_value(__ldg(c.ks + ph));
-        vx[i] = e8m0_value(__ldg(c.vs + ph));
-      }
-    };
-
-    long long tok[NP], tok_n[NP];
-    int pos[NP], pos_n[NP];
-    lookup(u0, tok, pos);
-    load_k(tok);
-    load_x(tok);
-    load_v(tok);
-    lookup(u0 + 1, tok_n, pos_n);
-    for (int u = u0; u < u1; ++u) {
       // scores of 32 keys: rows g, g + 8 of each 16, columns 2 t4, 2 t4 + 1
       float s[NT][2][4];
 #pragma unroll
@@ -293,8 +370,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          const uint32_t lo[4] = {kr[i][0][k].x, kr[i][0][k].y, kr[i][0][k].z, kr[i][0][k].w};
-          const uint32_t hi[4] = {kr[i][1][k].x, kr[i][1][k].y, kr[i][1][k].z, kr[i][1][k].w};
+          const uint4 ka = lds16(from + i * 16 * D + ko[0][k]);
+          const uint4 kb = lds16(from + i * 16 * D + ko[1][k]);
+          const uint32_t lo[4] = {ka.x, ka.y, ka.z, ka.w};
+          const uint32_t hi[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t a0 = e4m3x2_to_f16x2(lo[w]), a2 = e4m3x2_hi_to_f16x2(lo[w]);
@@ -304,14 +383,6 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
               mma_16816(s[n][i], a0, a1, a2, a3, q[n].b[4 * k + w][0], q[n].b[4 * k + w][1]);
           }
         }
-      float kxc[NP], vxc[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) { kxc[i] = kx[i]; vxc[i] = vx[i]; }
-      const bool more = u + 1 < u1;
-      if (more) {
-        load_k(tok_n);
-        load_x(tok_n);
-      }
       bool full = true;
 #pragma unroll
       for (int i = 0; i < NP; ++i) full = full && pos[i] + 32 / NP <= vis_min;
@@ -326,7 +397,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
           for (int j = 0; j < 4; ++j) {
             float x = s[n][i][j] * kxc[i % NP] * fx[n][j & 1];
             if (!full) {
-              const int key = pos[i % NP] + (SMALLP ? 0 : 16 * i) + g + 8 * (j >> 1);
+              const int key = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1);
               if (key >= vis[n][j & 1]) x = -INFINITY;
             }
             s[n][i][j] = x;
@@ -373,13 +444,26 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
           }
         }
       }
+      uint32_t vr[2][4][VW];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (VW == 4) {
+            const uint4 x = lds16(from + (32 + 16 * i) * D + vo[r]);
+            vr[i][r][0] = x.x; vr[i][r][1] = x.y; vr[i][r][2] = x.z; vr[i][r][3] = x.w;
+          } else {
+            const uint2 x = lds8(from + (32 + 16 * i) * D + vo[r]);
+            vr[i][r][0] = x.x; vr[i][r][1] = x.y;
+          }
+        }
       // keys past the sequence's end hold anything: 0 * NaN must not happen
       if (!full) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int key = pos[i % NP] + (SMALLP ? 0 : 16 * i) + 2 * t4 + (k & 1) + 8 * (k >> 1);
+            const int key = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(2 * t4 + (k & 1)) + 8 * (k >> 1);
             if (key >= len)
 #pragma unroll
               for (int w = 0; w < VW; ++w) vr[i][k][w] = 0;
@@ -419,13 +503,34 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
             }
           }
         }
-      if (more) {
-        load_v(tok_n);
+      // the step's bytes are in registers: its place takes unit u + S
+      __syncwarp();
+      const Where w = next;
+      next = lookup(u + S + 1);
+      issue(st, w);
+      return true;
+    };
+    bool ok = true;
+    for (int u = u0; ok && u < u1; u += S) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) { tok[i] = tok_n[i]; pos[i] = pos_n[i]; }
-        lookup(u + 2, tok_n, pos_n);
+      for (int s = 0; s < S; ++s)
+        if (ok && u + s < u1) ok = body(s, u + s);
+    }
+    // the steps behind the last unit, empty but for their barriers' phases;
+    // after a wait that ran out, what is still in flight
+    if (!ok) {
+      volatile int none = 0;
+#pragma unroll
+      for (int s = 0; s < S; ++s) mbar_wait(&bars[s], (phases >> s) & 1, &none, c.err);
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        mbar_wait(&bars[s], (phases >> s) & 1, abort_flag, c.err);
+        phases ^= 1u << s;
       }
     }
+    __syncthreads();
+    if (*abort_flag) return;                       // the error word says why
 
     // the four warps' shares of the keys
 #pragma unroll
@@ -439,12 +544,27 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
         if (g == 0) { s_m[warp][col] = m[n][j]; s_l[warp][col] = l[n][j]; }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&s_o[warp][col][(D / 8) * g + 2 * i]) = make_float2(o[n][i][j], o[n][i][2 + j]);
+          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j], o[n][i][2 + j]);
       }
     }
     __syncthreads();
+    auto write = [&](int col, int x, const float4& a, float mt, float lt) {
+      int t, gg;
+      if (!row_of(col, t, gg)) return;
+      const long long row = ((long long)b * p.Hq + h * G + gg) * p.T + t;
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      if (p.out_bf16) {
+        __nv_bfloat162 z[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv)};
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + x) = *reinterpret_cast<uint2*>(z);
+      } else {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + row * D + x) =
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      }
+      if (x == 0 && p.lse) p.lse[row] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
+    };
     const bool whole = u0 == 0 && u1 == units;
-    float* slot = p.part + ((long long)blockIdx.x * 2 + (at == begin ? 0 : 1)) * Slot<D, NT>::FLOATS;
+    float* part = reinterpret_cast<float*>(p.part + Slot<D, NT>::counters(gridDim.x));
+    float* slot = part + (size_t)(blockIdx.x * 2 + (at == begin ? 0 : 1)) * Slot<D, NT>::FLOATS;
     for (int i = threadIdx.x; i < R * (D / 4); i += 32 * NW) {
       const int col = i / (D / 4), x = i % (D / 4) * 4;
       float mt = s_m[0][col];
@@ -459,87 +579,96 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
         lt = fmaf(f, s_l[w][col], lt);
         a.x = fmaf(f, y.x, a.x); a.y = fmaf(f, y.y, a.y); a.z = fmaf(f, y.z, a.z); a.w = fmaf(f, y.w, a.w);
       }
-      if (!whole) {
+      if (whole) {
+        write(col, x, a, mt, lt);
+      } else {
         *reinterpret_cast<float4*>(slot + col * D + x) = a;
         if (x == 0) { slot[R * D + col] = mt; slot[R * D + R + col] = lt; }
-        continue;
       }
-      int t, gg;
-      if (!row_of(col, t, gg)) continue;
-      const long long row = ((long long)b * p.Hq + h * G + gg) * p.T + t;
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
-      if (p.out_bf16) {
-        __nv_bfloat162 z[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv)};
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + x) = *reinterpret_cast<uint2*>(z);
-      } else {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + row * D + x) =
-            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-      }
-      if (x == 0 && p.lse) p.lse[row] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
     }
+    __syncthreads();
+    if (!whole) {
+      // the row block's units lie in the shares of CTAs c0 .. c1
+      const unsigned start = seq0 + (unsigned)rb * units;
+      const unsigned c0 = shares.of(start), c1 = shares.of(start + units - 1);
+      const int n = c1 - c0 + 1;
+      if (threadIdx.x == 0) {
+        __threadfence();
+        unsigned long long* word = reinterpret_cast<unsigned long long*>(p.part) + c0;
+        // one addition, unless the word holds anything but a marked count: then
+        // whoever swaps that for the mark and a count of one has arrived, and
+        // the others add again (a swap fails only when the word has changed,
+        // by another arrival)
+        unsigned long long had = atomicAdd(word, 1ull);
+        if ((had >> 16) != MARK) {
+          ++had;
+          for (;;) {
+            const unsigned long long was = atomicCAS(word, had, MARK << 16 | 1u);
+            if (was == had) { had = MARK << 16; break; }
+            had = was;
+            if ((had >> 16) == MARK) { had = atomicAdd(word, 1ull); break; }
+          }
+        }
+        const unsigned count = (unsigned)(had & 0xffffu) + 1;
+        if (count == (unsigned)n) atomicExch(word, MARK << 16);
+        __threadfence();
+        s_misc[1] = count == (unsigned)n;
+      }
+      __syncthreads();
+      if (s_misc[1]) {
+        // of the CTAs of a row block only the first may have come to it from
+        // another: its second slot
+        const int odd = shares.begin(c0) >= start ? 0 : 1;
+        auto slot_of = [&](int i) -> const float* {
+          return part + (size_t)((c0 + i) * 2 + (i == 0 ? odd : 0)) * Slot<D, NT>::FLOATS;
+        };
+        // 128 threads: D / 4 of them a row, four dimensions each, sixteen slots
+        // with their maxima and sums in flight at once
+        for (int j = threadIdx.x; j < R * (D / 4); j += 32 * NW) {
+          const int col = j / (D / 4), x = j % (D / 4) * 4;
+          int t, gg;
+          if (!row_of(col, t, gg)) continue;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          float mt = -INFINITY, lt = 0.f;
+          for (int i0 = 0; i0 < n; i0 += 16) {
+            float4 y[16];
+            float mi[16], li[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              mi[i] = -INFINITY;
+              li[i] = 0.f;
+              if (i0 + i < n) {
+                const float* from = slot_of(i0 + i);
+                y[i] = __ldcg(reinterpret_cast<const float4*>(from + col * D + x));
+                mi[i] = __ldcg(from + R * D + col);
+                li[i] = __ldcg(from + R * D + R + col);
+              }
+            }
+            float mx = mt;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, mi[i]);
+            const float back = mx == mt ? 1.f : ex2_approx(mt - mx);
+            mt = mx;
+            lt *= back;
+            a.x *= back; a.y *= back; a.z *= back; a.w *= back;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = mi[i] == mx ? 1.f : ex2_approx(mi[i] - mx);
+              lt = fmaf(f, li[i], lt);
+              a.x = fmaf(f, y[i].x, a.x); a.y = fmaf(f, y[i].y, a.y);
+              a.z = fmaf(f, y[i].z, a.z); a.w = fmaf(f, y[i].w, a.w);
+            }
+          }
+          write(col, x, a, mt, lt);
+        }
+      }
+    }
+    // the merge buffer makes room for the next row block's boxes
+    fence_proxy_async_smem();
     __syncthreads();
     at += u1 - u0;
   }
-}
-
-// Joins the partials of every row block that more than one CTA worked on: one
-// CTA per row block, one warp per row, a lane holding D / 32 dimensions.
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * 8 * NT) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int grid) {
-  constexpr int R = 8 * NT;
-  constexpr int E = D / 32;
-  const CacheView& c = p.c;
-  const Line ln = make_line(p.Hq, c.Hkv, p.T, p.pages != nullptr);
-  const int b = blockIdx.x / ln.nb, rb = blockIdx.x % ln.nb;
-  const int lane = threadIdx.x % 32, col = threadIdx.x / 32;
-  long long before, total;
-  scan_units(p, b, before, total);
-  total *= ln.nb;
-  const int ctas = workers(total, grid);
-  const int units = seq_units(p, b);
-  const long long start = before * ln.nb + (long long)rb * units;
-  const int c0 = share_of(start, total, ctas), c1 = share_of(start + units - 1, total, ctas);
-  if (c0 == c1) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = rb / ln.per_head, sub = rb % ln.per_head;
-  const int q_len = cache_count(p.q_lens, b, p.T, c.err);
-  int t, gg;
-  if (p.pages) { t = sub / ln.QG; gg = (sub % ln.QG) * R + col; }
-  else { const int r = sub * R + col; t = r / ln.G; gg = r % ln.G; }
-  if (gg >= ln.G || t >= q_len) return;
-  const int n = c1 - c0 + 1;
-  auto slot = [&](int i) -> const float* {
-    const int cta = c0 + i;
-    return p.part + ((long long)cta * 2 + (share_begin(total, cta, ctas) >= start ? 0 : 1)) * Slot<D, NT>::FLOATS;
-  };
-  float mt = -INFINITY;
-  for (int i = lane; i < n; i += 32) mt = fmaxf(mt, slot(i)[R * D + col]);
-#pragma unroll
-  for (int o = 16; o; o /= 2) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-  float lt = 0.f, a[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) a[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = slot(i);
-    const float mi = s[R * D + col];
-    const float f = mi == mt ? 1.f : ex2_approx(mi - mt);
-    lt = fmaf(f, s[R * D + R + col], lt);
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] = fmaf(f, s[col * D + lane * E + e], a[e]);
-  }
-  const long long row = ((long long)b * p.Hq + h * ln.G + gg) * p.T + t;
-  const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const long long i = row * D + lane * E + e;
-    if (p.out_bf16)
-      *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.o) + i) =
-          __floats2bfloat162_rn(a[e] * inv, a[e + 1] * inv);
-    else
-      *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.o) + i) = make_float2(a[e] * inv, a[e + 1] * inv);
-  }
-  if (lane == 0 && p.lse) p.lse[row] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
 }
 
 // CTAs of the fixed grid: the GPU's, or fewer where the cache's capacity gives
@@ -549,26 +678,19 @@ int grid_of(const Line& ln, int B, int n_sel, int page, int max_pages) {
   long long units = (keys + UNIT - 1) / UNIT;
   if (units < 1) units = 1;
   const long long all = units * ln.nb * B;
+  if (all >= (1LL << 31)) return 0;                // more than the line's 32 bits count
   const long long most = (long long)kSMs * ctas_per_sm(ln.R / 8);
   return (int)(all < most ? all : most);
 }
 
 template <int D, int NT, bool SPLIT>
-cudaError_t launch(const CacheFwdParams& p, const Line& ln, int grid, cudaStream_t st) {
-  if (p.c.page == 16) cache_fwd_kernel<D, NT, SPLIT, true><<<grid, 32 * NW, 0, st>>>(p);
-  else cache_fwd_kernel<D, NT, SPLIT, false><<<grid, 32 * NW, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch(const CacheFwdParams& p, int grid, cudaStream_t st) {
+  constexpr int smem = Queue<D, NT>::SMEM;
+  auto k = p.c.page == 16 ? cache_fwd_kernel<D, NT, SPLIT, true> : cache_fwd_kernel<D, NT, SPLIT, false>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ln.nb * p.c.B));
-  cfg.blockDim = dim3(32 * 8 * NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, NT>, p, grid);
+  k<<<grid, 32 * NW, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -576,15 +698,19 @@ cudaError_t launch(const CacheFwdParams& p, const Line& ln, int grid, cudaStream
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages) {
   const Line ln = make_line(Hq, Hkv, T, n_sel > 0);
   const size_t slot = (size_t)ln.R * (d + 2) * 4;
-  return 2 * slot * (size_t)grid_of(ln, B, n_sel, page, max_pages);
+  const size_t grid = (size_t)grid_of(ln, B, n_sel, page, max_pages);
+  return grid ? Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid : 0;
 }
+
+int cache_fwd_box(int page) { return page < 32 ? page : 32; }
 
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st) {
   const Line ln = make_line(p.Hq, p.c.Hkv, p.T, p.pages != nullptr);
   const int grid = grid_of(ln, p.c.B, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);
+  if (grid == 0) return cudaErrorInvalidValue;
   const bool split = !p.out_bf16;
 #define FA4_CASE(D, NT, S) \
-  if (p.c.d == D && ln.R == 8 * NT && split == S) return launch<D, NT, S>(p, ln, grid, st);
+  if (p.c.d == D && ln.R == 8 * NT && split == S) return launch<D, NT, S>(p, grid, st);
   FA4_CASE(64, 1, false) FA4_CASE(64, 1, true) FA4_CASE(64, 2, false) FA4_CASE(64, 2, true)
   FA4_CASE(128, 1, false) FA4_CASE(128, 1, true) FA4_CASE(128, 2, false) FA4_CASE(128, 2, true)
 #undef FA4_CASE

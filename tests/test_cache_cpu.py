@@ -100,6 +100,8 @@ def test_refusals_of_each_call(fa):
     assert c["fwd"](good, wb=need - 1) == WS
     assert c["fwd"](good, ws=odd4, wb=need) == ALIGN
     assert c["fwd"](good, T=1 << 30, Hq=4) == UNSUP
+    assert c["fwd"](cache(fa, H=64), B=65535, Hq=64, T=1, mp=1 << 20) == UNSUP     # 2^31 units or more
+    assert c["fwd"](cache(fa, n=1 << 24, H=8), Hq=8) == UNSUP                      # 2^31 pool rows or more
     assert c["fwd"](good, T=0, q=None, o=None, ws=None) == OK
     assert c["select"](good, n_sel=0) == INVALID
     assert c["select"](good, out=None) == INVALID
@@ -121,10 +123,12 @@ def test_refusals_of_each_call(fa):
 
 def test_workspace_sizes(fa):
     f = fa.cache_fwd_workspace_bytes
-    # one unit per kv head: two slots of eight rows (d values, max and sum) each
-    assert f(1, 8, 2, 1, 128, 64, 2, 0) == 2 * 2 * 8 * 130 * 4
+    # one unit per kv head: a counter word and two slots of eight rows (d
+    # values, max and sum) each
+    assert f(1, 8, 2, 1, 128, 64, 2, 0) == 2 * 8 + 2 * 2 * 8 * 130 * 4
     assert f(1, 8, 2, 1, 128, 64, 0, 0) == 0 and f(1, 8, 3, 1, 128, 64, 2, 0) == 0
     assert f(0, 8, 2, 1, 128, 64, 2, 0) == 0
+    assert f(65535, 64, 64, 1, 128, 128, 1 << 20, 0) == 0 and f(1, 8, 2, 1, 128, 64, 2, 1 << 25) == 0
     # bounded by the grid, whatever the batch
     assert f(512, 64, 8, 1, 128, 64, 4096, 0) == f(64, 64, 8, 1, 128, 64, 4096, 0) < (8 << 20)
     assert fa.cache_select_workspace_bytes(2, 3, 4, 5) == 2 * 3 * 4 * 5 * 8
