@@ -113,40 +113,55 @@ struct QFrag {
   uint32_t b[D / 16][2];
 };
 
-// Row pointer (nullptr: a row of zeros) of the query that this lane's column
-// g = lane / 4 stands for; returns 2^e for that column in every lane of the
-// quad.
+// The bf16 words of the query that a lane's column g = lane / 4 stands for, read
+// ahead of their use; nullptr: a row of zeros.
 template <int D>
-FA4_DEV float load_qfrag(QFrag<D>& q, const __nv_bfloat16* row, int t) {
+struct QRaw {
   uint2 w[D / 16];
+
+  FA4_DEV void fetch(const __nv_bfloat16* row, int t) {
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c)
+    for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row) x = __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 16 * t) + i);
-      w[4 * c + 2 * i] = make_uint2(x.x, x.y);
-      w[4 * c + 2 * i + 1] = make_uint2(x.z, x.w);
+      for (int i = 0; i < 2; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row) x = __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 16 * t) + i);
+        w[4 * c + 2 * i] = make_uint2(x.x, x.y);
+        w[4 * c + 2 * i + 1] = make_uint2(x.z, x.w);
+      }
+  }
+  // Exponent e of the row's scale, the same in every lane of the quad.
+  FA4_DEV int exponent() const {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      amax = max(amax, max((w[s].x << 16) & 0x7fffffffu, w[s].x & 0x7fff0000u));
+      amax = max(amax, max((w[s].y << 16) & 0x7fffffffu, w[s].y & 0x7fff0000u));
     }
-  uint32_t amax = 0;
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    amax = max(amax, max((w[s].x << 16) & 0x7fffffffu, w[s].x & 0x7fff0000u));
-    amax = max(amax, max((w[s].y << 16) & 0x7fffffffu, w[s].y & 0x7fff0000u));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // E - 127 - 7 for the largest's exponent field E, within what a normal FP32
+    // power of two can undo; zeros, infinities and NaN keep 0
+    const int E = (int)(amax >> 23);
+    return (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
   }
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // e = E - 127 - 7 for the largest's exponent field E, within what a normal
-  // FP32 power of two can undo; zeros, infinities and NaN keep 0
-  const int E = (int)(amax >> 23);
-  const int e = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
-  const float down = exp2i(-e);
+  // f16 operands of the scaled row; returns 2^e.
+  FA4_DEV float convert(QFrag<D>& q) const {
+    const int e = exponent();
+    const float down = exp2i(-e);
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    q.b[s][0] = pack_f16x2(__uint_as_float(w[s].x << 16) * down, __uint_as_float(w[s].x & 0xffff0000u) * down);
-    q.b[s][1] = pack_f16x2(__uint_as_float(w[s].y << 16) * down, __uint_as_float(w[s].y & 0xffff0000u) * down);
+    for (int s = 0; s < D / 16; ++s) {
+      q.b[s][0] = pack_f16x2(__uint_as_float(w[s].x << 16) * down, __uint_as_float(w[s].x & 0xffff0000u) * down);
+      q.b[s][1] = pack_f16x2(__uint_as_float(w[s].y << 16) * down, __uint_as_float(w[s].y & 0xffff0000u) * down);
+    }
+    return exp2i(e);
   }
-  return exp2i(e);
+};
+
+FA4_DEV unsigned long long atomic_add_acq_rel(unsigned long long* p, unsigned long long x) {
+  unsigned long long had;
+  asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(had) : "l"(p), "l"(x) : "memory");
+  return had;
 }
 
 }  // namespace fa4

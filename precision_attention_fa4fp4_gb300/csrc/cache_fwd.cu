@@ -32,45 +32,35 @@
 // alone: no barrier between warps in the loop, and far more in flight than
 // loads through L1 allow (16-byte asynchronous copies of the same bytes, and
 // loads into registers, both stopped at 4.8 TB/s).  The codes are
-// used unscaled: K's page scale multiplies the scores, V's page scale
-// multiplies the FP32 sum of the page's products.
+// used unscaled: K's page scale multiplies the scores, V's goes into the
+// exponent of P, relative to the accumulator's own exponent.
 //
 // Roundings: q to f16 under a power of two (2^-32 of the row's largest), P to
-// f16 under a factor 2^15 (half a step is 2^-12, and values keep it down to
-// 2^-29), or for FP32 output P as a sum of two f16 (2^-23).  The normalizer
+// f16 under a factor 2^11 (half a step is 2^-12, and values keep it down to
+// 2^-17 at least), or for FP32 output P as a sum of two f16 (2^-23).  The normalizer
 // sums the FP32 values of P.
-#include "cache.cuh"
+#include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
 
-constexpr int NW = 4;                 // warps of a CTA
-constexpr int UNIT = 32 * NW;         // keys of a unit
-constexpr int kSMs = 152;             // GB300
-constexpr float P_BIAS = 15.f;        // log2 of the factor on P
+constexpr int NW = LINE_WARPS;
+// log2 of the factor on P: the largest P is half of f16's largest power
+constexpr float P_BIAS = 15.f;
+// How far a step's greatest V exponent may lie below the accumulator's before
+// the accumulator's is lowered: P keeps half a step of 2^-12 (22 bits as a sum
+// of two) down to there.  Lowering is bounded, so that the accumulator stays
+// below 2^(40 + 80) (its terms: 2^15 * 448, fewer than 2^17 of them a warp).
+constexpr int v_down(bool split) { return split ? 8 : 24; }
+constexpr int V_LOWER = 80;
 // the mark of a counter word, in its high 48 bits (no number, no pointer and no
 // pair of floats that a workspace could hold from other use)
 constexpr unsigned long long MARK = 0xfa4c0de5eed5ull;
 
-// Resident CTAs by registers (168 or 255 a thread), and the steps in flight
-// that fill the shared memory they leave.
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
-constexpr int stages(int d, int nt) { return d == 128 && nt == 1 ? 2 : 3; }
-
-// Order of the eight keys of an operand (its row i is key korder(i)), and of
-// the eight 16-byte words of a V row among the lanes: with the 128-byte swizzle
-// both reads are then free of bank conflicts (D = 128).  The 64-byte rows of
-// D = 64 are free of them for K in natural order, and two-way for V.
-template <int D>
-FA4_DEV constexpr int korder(int i) {
-  return D == 128 ? ((i & 1) << 2) | (i & 2) | (i >> 2) : i;
-}
-// Byte of row `row` and byte column `x` in a box of D-byte rows as TMA's swizzle
-// lays it out.
-template <int D>
-FA4_DEV int boxed(int row, int x) {
-  return D == 128 ? row * 128 + (x ^ ((row & 7) << 4)) : row * 64 + (x ^ (((row >> 1) & 3) << 4));
-}
+// Resident CTAs by registers, and the steps in flight that fill the shared
+// memory they leave.
+constexpr int ctas_per_sm(int d, int nt) { return d == 128 && nt == 2 ? 2 : 3; }
+constexpr int stages(int d, int nt) { return d == 128 && nt == 1 ? 2 : d == 128 ? 3 : 4; }
 
 // Row blocks and units of the line.
 struct Line {
@@ -92,48 +82,13 @@ __host__ __device__ inline Line make_line(int Hq, int Hkv, int T, bool sparse) {
   return l;
 }
 
-// Units of one row block of a sequence of n tokens (at least one, which writes
-// the output of a row without keys).
-FA4_DEV int units_of(int n, int q_len, int n_sel, int page) {
-  long long keys = q_len > 0 ? n : 0;
-  // a list may name its pages in any order, with holes
-  if (n_sel > 0 && keys > 0) keys = (long long)n_sel * page;
-  return max(1, (int)((keys + UNIT - 1) / UNIT));
-}
-
+// Units of one row block of sequence b (one, which writes the output, where the
+// row has no keys).  A list of pages may name them in any order, with holes.
 FA4_DEV int seq_units(const CacheFwdParams& p, int b) {
-  return units_of(cache_len(p.c, b), cache_count(p.q_lens, b, p.T, p.c.err), p.pages ? p.n_sel : 0, p.c.page);
+  const int len = cache_len(p.c, b), q_len = cache_count(p.q_lens, b, p.T, p.c.err);
+  if (len == 0 || q_len == 0) return 1;
+  return units_of(p.pages ? (long long)p.n_sel * p.c.page : len);
 }
-
-// Units of the sequences before `b` and of all sequences (whole warp).
-FA4_DEV void scan_units(const CacheFwdParams& p, int b, unsigned& before, unsigned& total) {
-  unsigned lo = 0, all = 0;
-  for (int i = threadIdx.x % 32; i < p.c.B; i += 32) {
-    const unsigned u = seq_units(p, i);
-    all += u;
-    if (i < b) lo += u;
-  }
-  before = __reduce_add_sync(0xffffffffu, lo);
-  total = __reduce_add_sync(0xffffffffu, all);
-}
-
-// CTAs that get a share.  No share is empty (the join reads every slot from
-// the first to the last), and no CTA is there only to make some shares shorter
-// than the longest: it would add a slot to the join and save nothing.
-FA4_DEV unsigned workers(unsigned total, unsigned grid) {
-  const unsigned longest = (total + grid - 1) / grid;
-  return (total + longest - 1) / longest;
-}
-// The line cut into n shares, the first `rem` of them one unit longer.
-struct Shares {
-  unsigned per, rem;
-  FA4_DEV Shares(unsigned total, unsigned n) : per(total / n), rem(total % n) {}
-  FA4_DEV unsigned begin(unsigned i) const { return i * per + min(i, rem); }
-  FA4_DEV unsigned of(unsigned u) const {          // the share that holds unit u
-    const unsigned cut = rem * (per + 1);
-    return u < cut ? u / (per + 1) : rem + (u - cut) / per;
-  }
-};
 
 template <int D, int NT>
 struct Slot {
@@ -151,12 +106,13 @@ struct Queue {
   static constexpr int OS = D + 4;                               // row stride of the merge buffer
   static constexpr int MERGE = NW * 8 * NT * (OS + 2) * 4;       // lies over the queues
   static constexpr int OFF_BAR = NW * WARP > MERGE ? NW * WARP : MERGE;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * NW * S;
+  static constexpr int OFF_STEP = OFF_BAR + 8 * NW * S;          // 16 bytes a step: positions, scales
+  static constexpr int OFF_MISC = OFF_STEP + 16 * NW * S;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;              // and the swizzle's alignment
 };
 
 template <int D, int NT, bool SPLIT, bool SMALLP>
-__global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+__global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using Q = Queue<D, NT>;
   constexpr int R = 8 * NT;
   constexpr int S = Q::S;
@@ -169,6 +125,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
   float (*s_m)[R] = reinterpret_cast<float (*)[R]>(smem + NW * R * OS * 4);
   float (*s_l)[R] = s_m + NW;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Q::OFF_BAR) + threadIdx.x / 32 * S;
+  int4* steps = reinterpret_cast<int4*>(smem + Q::OFF_STEP) + threadIdx.x / 32 * S;
   int* s_misc = reinterpret_cast<int*>(smem + Q::OFF_MISC);
   volatile int* abort_flag = s_misc;
 
@@ -177,37 +134,16 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
   const int g = lane / 4, t4 = lane % 4;
   const Line ln = make_line(p.Hq, c.Hkv, p.T, p.pages != nullptr);
   const int G = ln.G;
-  unsigned before, total;
-  scan_units(p, 0, before, total);
-  total *= ln.nb;
+  auto seq = [&](int i) -> unsigned { return (unsigned)seq_units(p, i) * ln.nb; };
+  const unsigned total = line_total(c.B, seq);
   const unsigned ctas = workers(total, gridDim.x);
   if (blockIdx.x >= ctas) return;
   const Shares shares(total, ctas);
   const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
-  unsigned at = begin;
-  // the sequence that holds unit `at`
-  int b = 0, units = 1;
-  unsigned seq0 = 0;                               // its first unit
-  for (int base = 0;; base += 32) {
-    const int i = base + lane;
-    const unsigned mine = i < c.B ? (unsigned)seq_units(p, i) * ln.nb : 0;
-    unsigned inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, seq0 + inc > at);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      b = base + src;
-      seq0 += __shfl_sync(0xffffffffu, inc - mine, src);
-      units = __shfl_sync(0xffffffffu, mine, src) / ln.nb;
-      break;
-    }
-    seq0 += __shfl_sync(0xffffffffu, inc, 31);
-    if (base + 32 >= c.B) return;                  // cannot happen: at < total
-  }
+  unsigned at = begin, seq0;
+  int b;
+  if (!line_find(c.B, seq, at, b, seq0)) return;
+  int units = seq_units(p, b);
   const int log_p = 31 - __clz(c.page);
   uint8_t* queue = smem + warp * Q::WARP;
   unsigned phases = 0;                             // parity of each step's barrier
@@ -257,59 +193,39 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
     };
     const int* sel = p.pages ? p.pages + (((long long)b * c.Hkv + h) * p.T + sub / ln.QG) * p.n_sel : nullptr;
 
-    // Pool page (-1: none) and first key position of the warp's keys of a
-    // unit; keys that are not there get a position that every query masks.
-    struct Where { int page[NP], pos[NP]; };
-    auto lookup = [&](int u) -> Where {
-      Where w;
+    QRaw<D> raw[NT];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int v = u * UNIT + 32 * warp + 16 * i;
-        int lp = v >> log_p;
-        w.page[i] = -1;
-        w.pos[i] = 0x40000000;
-        if (u < u1) {
-          if (sel) {
-            lp = lp < p.n_sel ? __ldg(sel + lp) : -1;
-            if (lp >= c.max_pages || lp < -1) { atomicOr(c.err, FA4_DEVERR_INDEX); lp = -1; }
-          }
-          if (lp >= 0 && ((long long)lp << log_p) < len) w.page[i] = cache_page(c, c.table, b, lp);
-          if (w.page[i] >= 0) w.pos[i] = (lp << log_p) + (v & (c.page - 1));
-        }
-      }
-      return w;
-    };
-    // What a step in flight still needs in registers.
-    struct Step { int pos[NP]; uint32_t ks[NP], vs[NP]; };
-    Step step[S];
-    auto issue = [&](int s, const Where& w) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        step[s].pos[i] = w.pos[i];
-        step[s].ks[i] = step[s].vs[i] = 0;
-        if (w.page[i] >= 0) {
-          const long long ph = (long long)w.page[i] * c.Hkv + h;
-          step[s].ks[i] = __ldg(c.ks + ph);
-          step[s].vs[i] = __ldg(c.vs + ph);
-          if (lane == 0) {
-            const int row = (int)(ph << log_p) + (w.pos[i] & (c.page - 1));
-            uint8_t* to = queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0);
-            // each box counts for itself: a step without a page has none
-            mbar_expect_tx(&bars[s], 2 * (32 / NP) * D);
-            tma_load_3d(to, &p.tm_k, &bars[s], 0, row, 0);
-            tma_load_3d(to + 32 * D, &p.tm_v, &bars[s], 0, row, 0);
-          }
-        }
-      }
-      if (lane == 0) mbar_arrive(&bars[s]);
-    };
-    Where next = lookup(u0);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const Where w = next;
-      next = lookup(u0 + s + 1);
-      issue(s, w);
+    for (int n = 0; n < NT; ++n) {
+      int t, gg;
+      const bool in = row_of(8 * n + g, t, gg);
+      raw[n].fetch(in ? reinterpret_cast<const __nv_bfloat16*>(p.q) + (((long long)b * p.Hq + h * G + gg) * p.T + t) * D
+                      : nullptr, t4);
     }
+    Window<NP> window;
+    window.fill(c, b, h, len, sel, p.n_sel, u0, u1);
+    auto issue = [&](int s, int u) {
+      if (!window.has(u)) window.fill(c, b, h, len, sel, p.n_sel, u, u1);
+      int what[4] = {NOWHERE, 0, NOWHERE, 0};      // position, scales of each page
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const Entry w = window.get(u, i);
+        what[2 * i] = w.pos;
+        what[2 * i + 1] = w.ks | w.vs << 8;
+        if (w.page >= 0 && lane == 0) {
+          const int row = (int)(((long long)w.page * c.Hkv + h) << log_p) + (w.pos & (c.page - 1));
+          uint8_t* to = queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0);
+          // each box counts for itself: a step without a page has none
+          mbar_expect_tx(&bars[s], 2 * (32 / NP) * D);
+          tma_load_3d(to, &p.tm_k, &bars[s], 0, row, 0);
+          tma_load_3d(to + 32 * D, &p.tm_v, &bars[s], 0, row, 0);
+        }
+      }
+      if (lane == 0) {
+        steps[s] = make_int4(what[0], what[1], what[2], what[3]);
+        mbar_arrive(&bars[s]);
+      }
+    };
+    for (int s = 0; s < S; ++s) issue(s, u0 + s);
 
     QFrag<D> q[NT];
     float fx[NT][2];                               // log2-unit factor of columns 2 t4, 2 t4 + 1
@@ -318,11 +234,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       int t, gg;
-      const bool ok = row_of(8 * n + g, t, gg);
-      const __nv_bfloat16* row = ok ? reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                          (((long long)b * p.Hq + h * G + gg) * p.T + t) * D
-                                    : nullptr;
-      const float e = load_qfrag<D>(q[n], row, t4);
+      const float e = raw[n].convert(q[n]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         fx[n][j] = p.c2 * __shfl_sync(0xffffffffu, e, (2 * t4 + j) * 4);
@@ -336,6 +248,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
 
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];
+    int xo = -127;                                 // o is in units of 2^xo
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -350,13 +263,16 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       if (!mbar_wait(&bars[st], (phases >> st) & 1, abort_flag, c.err)) return false;
       phases ^= 1u << st;
       const uint8_t* from = queue + st * Q::BYTES;
+      const int4 what = steps[st];
       int pos[NP];
-      float kxc[NP], vxc[NP];
+      float kxc[NP];
+      int ev[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        pos[i] = step[st].pos[i];
-        kxc[i] = e8m0_value(step[st].ks[i]);
-        vxc[i] = e8m0_value(step[st].vs[i]);
+        pos[i] = i ? what.z : what.x;
+        const int sc = i ? what.w : what.y;
+        kxc[i] = e8m0_value(sc & 0xff);
+        ev[i] = pos[i] == NOWHERE ? -1000 : (sc >> 8) - 127;
       }
       // scores of 32 keys: rows g, g + 8 of each 16, columns 2 t4, 2 t4 + 1
       float s[NT][2][4];
@@ -386,6 +302,30 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       bool full = true;
 #pragma unroll
       for (int i = 0; i < NP; ++i) full = full && pos[i] + 32 / NP <= vis_min;
+
+      // V's exponents relative to the accumulator's go into P.  A page above it
+      // raises it, a step far below it lowers it
+      int ev_max = ev[0];
+#pragma unroll
+      for (int i = 1; i < NP; ++i) ev_max = max(ev_max, ev[i]);
+      if (ev_max > -1000 && (ev_max > xo || ev_max < xo - v_down(SPLIT))) {
+        const int to = max(ev_max, xo - V_LOWER);
+        const float by = pow2_any(xo - to);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][i][j] *= by;
+        xo = to;
+      }
+      float vd[NP], vu[NP];                        // exponent on P, and what undoes it for l
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int d = min(0, max(ev[i] - xo, -100));
+        vd[i] = (float)d;
+        vu[i] = exp2i(-d);
+      }
 
       uint32_t ph[NT][2][2], pl[NT][2][2];         // P^T as the B operand: [16 keys][k half]
 #pragma unroll
@@ -430,9 +370,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
         for (int i = 0; i < 2; ++i) {
           float e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = ex2_approx(s[n][i][j] - ((j & 1) ? r1 : r0));
-          l[n][0] += e[0] + e[2];
-          l[n][1] += e[1] + e[3];
+          for (int j = 0; j < 4; ++j) e[j] = ex2_approx(s[n][i][j] - (((j & 1) ? r1 : r0) - vd[i % NP]));
+          l[n][0] = fmaf(e[0] + e[2], vu[i % NP], l[n][0]);
+          l[n][1] = fmaf(e[1] + e[3], vu[i % NP], l[n][1]);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const uint32_t x = pack_f16x2(e[2 * r], e[2 * r + 1]);
@@ -471,50 +411,28 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       }
       // O^T += V^T P: lane rows (D / 8) g + 2 mt and + 1 of the head dimension
 #pragma unroll
-      for (int w = 0; w < VW; ++w)
+      for (int j = 0; j < D / 8; ++j) {
+        const int mt = j / 2, i = j % 2, w = mt / 2, pick = mt % 2 ? 0x7362 : 0x5140;
+        const uint32_t x = __byte_perm(vr[i][0][w], vr[i][1][w], pick);
+        const uint32_t y = __byte_perm(vr[i][2][w], vr[i][3][w], pick);
+        const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_hi_to_f16x2(x);
+        const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_hi_to_f16x2(y);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int mt = 2 * w + half;
-          float acc[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x = __byte_perm(vr[i][0][w], vr[i][1][w], half ? 0x7362 : 0x5140);
-            const uint32_t y = __byte_perm(vr[i][2][w], vr[i][3][w], half ? 0x7362 : 0x5140);
-            const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_hi_to_f16x2(x);
-            const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_hi_to_f16x2(y);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_16816(acc[n], a0, a1, a2, a3, ph[n][i][0], ph[n][i][1]);
-              if constexpr (SPLIT) mma_16816(acc[n], a0, a1, a2, a3, pl[n][i][0], pl[n][i][1]);
-            }
-            if (SMALLP || i == 1) {
-              const float x2 = vxc[i % NP];
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  o[n][mt][j] = fmaf(acc[n][j], x2, o[n][mt][j]);
-                  acc[n][j] = 0.f;
-                }
-            }
-          }
+        for (int n = 0; n < NT; ++n) {
+          mma_16816(o[n][mt], a0, a1, a2, a3, ph[n][i][0], ph[n][i][1]);
+          if constexpr (SPLIT) mma_16816(o[n][mt], a0, a1, a2, a3, pl[n][i][0], pl[n][i][1]);
         }
+      }
       // the step's bytes are in registers: its place takes unit u + S
       __syncwarp();
-      const Where w = next;
-      next = lookup(u + S + 1);
-      issue(st, w);
+      issue(st, u + S);
       return true;
     };
     bool ok = true;
-    for (int u = u0; ok && u < u1; u += S) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (ok && u + s < u1) ok = body(s, u + s);
+    int place = 0;                                 // in the queue
+    for (int u = u0; ok && u < u1; ++u) {
+      ok = body(place, u);
+      place = place + 1 == S ? 0 : place + 1;
     }
     // the steps behind the last unit, empty but for their barriers' phases;
     // after a wait that ran out, what is still in flight
@@ -533,6 +451,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
     if (*abort_flag) return;                       // the error word says why
 
     // the four warps' shares of the keys
+    const float unit = pow2_any(xo);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -544,7 +463,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
         if (g == 0) { s_m[warp][col] = m[n][j]; s_l[warp][col] = l[n][j]; }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j], o[n][i][2 + j]);
+          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j] * unit, o[n][i][2 + j] * unit);
       }
     }
     __syncthreads();
@@ -593,25 +512,29 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
       const unsigned c0 = shares.of(start), c1 = shares.of(start + units - 1);
       const int n = c1 - c0 + 1;
       if (threadIdx.x == 0) {
-        __threadfence();
+        // the barrier above and the release here order the CTA's slot before
+        // its arrival, the acquire the others' slots before the join
         unsigned long long* word = reinterpret_cast<unsigned long long*>(p.part) + c0;
         // one addition, unless the word holds anything but a marked count: then
         // whoever swaps that for the mark and a count of one has arrived, and
         // the others add again (a swap fails only when the word has changed,
         // by another arrival)
-        unsigned long long had = atomicAdd(word, 1ull);
+        unsigned long long had = atomic_add_acq_rel(word, 1ull);
         if ((had >> 16) != MARK) {
           ++had;
           for (;;) {
+            __threadfence();
             const unsigned long long was = atomicCAS(word, had, MARK << 16 | 1u);
             if (was == had) { had = MARK << 16; break; }
             had = was;
-            if ((had >> 16) == MARK) { had = atomicAdd(word, 1ull); break; }
+            if ((had >> 16) == MARK) { had = atomic_add_acq_rel(word, 1ull); break; }
           }
         }
         const unsigned count = (unsigned)(had & 0xffffu) + 1;
-        if (count == (unsigned)n) atomicExch(word, MARK << 16);
-        __threadfence();
+        if (count == (unsigned)n) {
+          atomicExch(word, MARK << 16);
+          __threadfence();
+        }
         s_misc[1] = count == (unsigned)n;
       }
       __syncthreads();
@@ -673,13 +596,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(NT)) cache_fwd_kernel(con
 
 // CTAs of the fixed grid: the GPU's, or fewer where the cache's capacity gives
 // fewer units.
-int grid_of(const Line& ln, int B, int n_sel, int page, int max_pages) {
-  const long long keys = (long long)(n_sel > 0 ? n_sel : max_pages) * page;
-  long long units = (keys + UNIT - 1) / UNIT;
-  if (units < 1) units = 1;
-  const long long all = units * ln.nb * B;
+int grid_of(const Line& ln, int B, int d, int n_sel, int page, int max_pages) {
+  const long long all = (long long)units_of((long long)(n_sel > 0 ? n_sel : max_pages) * page) * ln.nb * B;
   if (all >= (1LL << 31)) return 0;                // more than the line's 32 bits count
-  const long long most = (long long)kSMs * ctas_per_sm(ln.R / 8);
+  const long long most = (long long)kSMs * ctas_per_sm(d, ln.R / 8);
   return (int)(all < most ? all : most);
 }
 
@@ -698,7 +618,7 @@ cudaError_t launch(const CacheFwdParams& p, int grid, cudaStream_t st) {
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages) {
   const Line ln = make_line(Hq, Hkv, T, n_sel > 0);
   const size_t slot = (size_t)ln.R * (d + 2) * 4;
-  const size_t grid = (size_t)grid_of(ln, B, n_sel, page, max_pages);
+  const size_t grid = (size_t)grid_of(ln, B, d, n_sel, page, max_pages);
   return grid ? Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid : 0;
 }
 
@@ -706,7 +626,7 @@ int cache_fwd_box(int page) { return page < 32 ? page : 32; }
 
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st) {
   const Line ln = make_line(p.Hq, p.c.Hkv, p.T, p.pages != nullptr);
-  const int grid = grid_of(ln, p.c.B, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);
+  const int grid = grid_of(ln, p.c.B, p.c.d, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);
   if (grid == 0) return cudaErrorInvalidValue;
   const bool split = !p.out_bf16;
 #define FA4_CASE(D, NT, S) \

@@ -1,0 +1,148 @@
+// cache_line.cuh -- what the kernels that stream the cache share: the line of
+// work units and its equal shares, the window of looked-up pages, and the
+// layout of 8-bit rows as TMA's swizzle leaves them in shared memory.
+#pragma once
+#include "cache.cuh"
+
+namespace fa4 {
+
+constexpr int LINE_WARPS = 4;                // warps of a CTA
+constexpr int UNIT = 32 * LINE_WARPS;        // keys of a unit; a warp's step is 32
+constexpr int kSMs = 152;                    // GB300
+
+// Units of a run of keys (at least one).
+__host__ __device__ inline int units_of(long long keys) {
+  const long long u = (keys + UNIT - 1) / UNIT;
+  return u < 1 ? 1 : (int)u;
+}
+
+// CTAs that get a share.  No share is empty (a join reads every slot from the
+// first to the last), and no CTA is there only to make some shares shorter
+// than the longest: it would add a slot to the join and save nothing.
+FA4_DEV unsigned workers(unsigned total, unsigned grid) {
+  const unsigned longest = (total + grid - 1) / grid;
+  return (total + longest - 1) / longest;
+}
+
+// The line cut into n shares, the first `rem` of them one unit longer.
+struct Shares {
+  unsigned per, rem;
+  FA4_DEV Shares(unsigned total, unsigned n) : per(total / n), rem(total % n) {}
+  FA4_DEV unsigned begin(unsigned i) const { return i * per + min(i, rem); }
+  FA4_DEV unsigned of(unsigned u) const {          // the share that holds unit u
+    const unsigned cut = rem * (per + 1);
+    return u < cut ? u / (per + 1) : rem + (u - cut) / per;
+  }
+};
+
+// Units of all sequences (whole warp); units(b) is a sequence's.
+template <class F>
+FA4_DEV unsigned line_total(int B, F units) {
+  unsigned all = 0;
+  for (int i = threadIdx.x % 32; i < B; i += 32) all += units(i);
+  return __reduce_add_sync(0xffffffffu, all);
+}
+
+// The sequence b that holds unit `at` of the line and its first unit seq0
+// (whole warp).  Returns false if the line ends before (it does not).
+template <class F>
+FA4_DEV bool line_find(int B, F units, unsigned at, int& b, unsigned& seq0) {
+  const int lane = threadIdx.x % 32;
+  seq0 = 0;
+  for (int base = 0; base < B; base += 32) {
+    const unsigned mine = base + lane < B ? units(base + lane) : 0;
+    unsigned inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, seq0 + inc > at);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = base + src;
+      seq0 += __shfl_sync(0xffffffffu, inc - mine, src);
+      return true;
+    }
+    seq0 += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return false;
+}
+
+// A warp's keys of a unit lie in NP pages (one, or two of 16 keys).  The window
+// holds, one entry a lane, what is to be known of the next 32 / NP units: pool
+// page, position of the first key, scales.  Looking up 32 entries costs the
+// three dependent loads (list, table, scale) once.
+constexpr int NOWHERE = 0x40000000;          // a position that every query masks
+struct Entry {
+  int page, pos;                             // -1 and NOWHERE: no such keys
+  uint32_t ks, vs;
+};
+template <int NP>
+struct Window {
+  int first;                                 // unit of the first entry
+  Entry e;
+
+  // Entries of units u.. < end for this warp of a CTA: sequence b of len tokens,
+  // kv head h; sel: a list of n_sel pages to go through, or nullptr (all).
+  FA4_DEV void fill(const CacheView& c, int b, int h, int len, const int* sel, int n_sel, int u, int end) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int log_p = 31 - __clz(c.page);
+    first = u;
+    const int unit = u + lane / NP;
+    const int v = unit * UNIT + 32 * warp + 16 * (lane % NP);
+    int lp = v >> log_p;
+    e.page = -1;
+    e.pos = NOWHERE;
+    e.ks = e.vs = 0;
+    if (unit < end) {
+      if (sel) {
+        lp = lp < n_sel ? __ldg(sel + lp) : -1;
+        if (lp >= c.max_pages || lp < -1) { atomicOr(c.err, FA4_DEVERR_INDEX); lp = -1; }
+      }
+      if (lp >= 0 && ((long long)lp << log_p) < len) {
+        e.page = cache_page(c, c.table, b, lp);
+        if (e.page >= 0) {
+          const long long ph = (long long)e.page * c.Hkv + h;
+          e.ks = __ldg(c.ks + ph);
+          e.vs = __ldg(c.vs + ph);
+          e.pos = (lp << log_p) + (v & (c.page - 1));
+        }
+      }
+    }
+    __syncwarp();
+  }
+  FA4_DEV bool has(int u) const { return u < first + 32 / NP; }
+  FA4_DEV Entry get(int u, int i) const {
+    const int src = (u - first) * NP + i;
+    Entry r;
+    r.page = __shfl_sync(0xffffffffu, e.page, src);
+    r.pos = __shfl_sync(0xffffffffu, e.pos, src);
+    const uint32_t s = __shfl_sync(0xffffffffu, e.ks | e.vs << 8, src);
+    r.ks = s & 0xffu;
+    r.vs = s >> 8;
+    return r;
+  }
+};
+
+// Order of the eight keys of an operand (its row i is key korder(i)), and of
+// the eight 16-byte words of a V row among the lanes: with the 128-byte swizzle
+// both reads are then free of bank conflicts (D = 128).  The 64-byte rows of
+// D = 64 are free of them for K in natural order, and two-way for V.
+template <int D>
+FA4_DEV constexpr int korder(int i) {
+  return D == 128 ? ((i & 1) << 2) | (i & 2) | (i >> 2) : i;
+}
+// Byte of row `row` and byte column `x` in a box of D-byte rows as TMA's swizzle
+// lays it out.
+template <int D>
+FA4_DEV int boxed(int row, int x) {
+  return D == 128 ? row * 128 + (x ^ ((row & 7) << 4)) : row * 64 + (x ^ (((row >> 1) & 3) << 4));
+}
+
+// 2^x for x in [-382, 127]: the exact power, subnormal or zero where FP32 ends.
+FA4_DEV float pow2_any(int x) {
+  return x >= -126 ? exp2i(x) : (x >= -149 ? __uint_as_float(1u << (x + 149)) : 0.f);
+}
+
+}  // namespace fa4

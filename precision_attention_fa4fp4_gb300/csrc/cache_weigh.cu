@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(32 * NW) cache_weigh_kernel(const __grid_const
     if (rg < rows)
       row = reinterpret_cast<const __nv_bfloat16*>(p.q) +
             (((long long)b * p.Hq + h * G + rg % G) * p.T + rg / G) * D;
-    const float e = load_qfrag<D>(q, row, t4);
+    QRaw<D> raw;
+    raw.fetch(row, t4);
+    const float e = raw.convert(q);
     float fx[2], hi[2], lo[2];
     int vis[2];
 #pragma unroll
