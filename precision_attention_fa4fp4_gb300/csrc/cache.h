@@ -28,8 +28,11 @@ struct CacheAppendParams {
 };
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t st);
 
+// Rows of a TMA box of codes: a warp's 32 keys, or a page of 16.
+inline int cache_box(int page) { return page < 32 ? page : 32; }
+
 struct CacheFwdParams {
-  CUtensorMap tm_k, tm_v;  // codes as rows of d bytes, boxes of cache_fwd_box(page) rows
+  CUtensorMap tm_k, tm_v;  // codes as rows of d bytes, boxes of cache_box(page) rows
   CacheView c;
   const void* q;         // bf16 [B][Hq][T][d]
   const int* q_lens;     // [B] or nullptr (T)
@@ -40,7 +43,6 @@ struct CacheFwdParams {
   int Hq, T, n_sel, causal, out_bf16;
   float scale, c2;       // softmax scale, fl32(scale * log2 e)
 };
-int cache_fwd_box(int page);
 // Workspace of the split forward; 0: more work than one call takes.
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages);
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st);
@@ -56,6 +58,7 @@ struct CacheSelectParams {
 cudaError_t launch_cache_select(const CacheSelectParams& p, cudaStream_t st);
 
 struct CacheWeighParams {
+  CUtensorMap tm_k;
   CacheView c;
   const void* q;
   const float* lse;      // [B][Hq][T]
@@ -65,6 +68,7 @@ struct CacheWeighParams {
   int Hq, T, causal;
   float c2;
 };
+bool cache_weigh_fits(int B, int Hkv, int page, int max_pages);
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st);
 
 struct CacheEvictParams {

@@ -27,9 +27,13 @@ fa4fp4_status check_shape(int num_pages, int Hkv, int page, int d, int B, int Hq
   return FA4FP4_OK;
 }
 
+uint64_t pool_rows(const fa4fp4_cache* c) { return (uint64_t)c->num_pages * c->Hkv * c->page; }
+
 fa4fp4_status check_call(const fa4fp4_cache* c, int B, int Hq, int T, int max_pages) {
   if (!c) return FA4FP4_ERR_INVALID_ARG;
-  return check_shape(c->num_pages, c->Hkv, c->page, c->d, B, Hq, T, max_pages);
+  const fa4fp4_status s = check_shape(c->num_pages, c->Hkv, c->page, c->d, B, Hq, T, max_pages);
+  // a pool row (d codes of one token and head) is a 32-bit TMA coordinate
+  return s == FA4FP4_OK && pool_rows(c) >= (1ull << 31) ? FA4FP4_ERR_UNSUPPORTED : s;
 }
 
 // Pointers of the cache and of the sequences.
@@ -110,10 +114,8 @@ fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void* q, const i
   if (!view(&p.c, cache, page_table, lens, B, max_pages)) return FA4FP4_ERR_CUDA;
   p.q = q; p.q_lens = q_lens; p.pages = pages; p.o = o; p.lse = lse;
   p.part = static_cast<uint8_t*>(workspace);
-  const uint64_t rows = (uint64_t)cache->num_pages * cache->Hkv * cache->page;
-  if (rows >= (1ull << 31)) return FA4FP4_ERR_UNSUPPORTED;
-  if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, rows, cache_fwd_box(cache->page)) ||
-      !make_rows_map(&p.tm_v, cache->v_codes, cache->d, rows, cache_fwd_box(cache->page)))
+  if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, pool_rows(cache), cache_box(cache->page)) ||
+      !make_rows_map(&p.tm_v, cache->v_codes, cache->d, pool_rows(cache), cache_box(cache->page)))
     return FA4FP4_ERR_CUDA;
   p.Hq = Hq; p.T = T; p.n_sel = n_sel; p.causal = causal ? 1 : 0;
   p.out_bf16 = out_dtype == FA4FP4_OUT_BF16;
@@ -159,12 +161,15 @@ fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const
   if (s != FA4FP4_OK) return s;
   if (B == 0 || Hq == 0 || T == 0) return FA4FP4_OK;
   if ((s = check_cache(cache, page_table, lens, q_lens)) != FA4FP4_OK) return s;
+  if (!cache_weigh_fits(B, cache->Hkv, cache->page, max_pages)) return FA4FP4_ERR_UNSUPPORTED;
   if (!q || !lse || !weight_in || !weight_out) return FA4FP4_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weight_in, 4) || !aligned(weight_out, 4))
     return FA4FP4_ERR_ALIGNMENT;
   CacheWeighParams p;
   memset(&p, 0, sizeof(p));
   if (!view(&p.c, cache, page_table, lens, B, max_pages)) return FA4FP4_ERR_CUDA;
+  if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, pool_rows(cache), cache_box(cache->page)))
+    return FA4FP4_ERR_CUDA;
   p.q = q; p.lse = lse; p.q_lens = q_lens; p.w_in = weight_in; p.w_out = weight_out;
   p.Hq = Hq; p.T = T; p.causal = causal ? 1 : 0;
   p.c2 = log2_scale(softmax_scale_of(softmax_scale, cache->d));

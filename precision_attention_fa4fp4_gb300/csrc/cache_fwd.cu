@@ -622,8 +622,6 @@ size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int 
   return grid ? Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid : 0;
 }
 
-int cache_fwd_box(int page) { return page < 32 ? page : 32; }
-
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st) {
   const Line ln = make_line(p.Hq, p.c.Hkv, p.T, p.pages != nullptr);
   const int grid = grid_of(ln, p.c.B, p.c.d, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);

@@ -5,100 +5,365 @@
 // with the log-sum-exp that the attention wrote.  Every (kv head, token) has
 // one owner, so nothing is added in an order that changes.
 //
-// One query token: bound by HBM, d bytes of K and 8 bytes of weight per token
-// and kv head.  Many query tokens: bound by the m16n8k16 products and one
-// exponential per score; each warp converts its 32 keys once and keeps them as
-// f16 operands while it walks over the query rows.
-#include "cache.cuh"
+// Up to 16 query rows per kv head: bound by HBM, d bytes of K and 8 of weights
+// per token and kv head; K comes as in the attention, by TMA boxes into per-warp
+// queues, and a fixed grid shares one line of (sequence, head, 128 keys).
+//
+// More rows: bound by the matrix products and one exponential per score.  A
+// warp converts its 32 keys once and keeps them as f16 operands while it walks
+// over the rows, which the CTA prepares 64 at a time.  (The m16n8k32 E4M3
+// product would take the codes as they are, but is not a native instruction
+// here: it converts both operands at every use, and was five times slower.)
+#include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
 
-constexpr int NW = 4;
-constexpr int UNIT = 32 * NW;
+constexpr int NW = LINE_WARPS;
+
+// lse in log2 units as a float and the factor that makes up for its rounding;
+// rows that add nothing get (0, 0).
+FA4_DEV void reference(float lse, bool in, float& ref, float& fac) {
+  ref = 0.f;
+  fac = 0.f;
+  if (in && lse != -INFINITY) {
+    ref = lse * 1.4426950216293335f;
+    const float rest = fmaf(lse, 1.4426950216293335f, -ref) + lse * 1.9259629911266175e-8f;
+    fac = ex2_approx(-rest);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+template <int D, int NT>
+struct WQueue {
+  static constexpr int S = D == 128 ? 3 : 4;
+  static constexpr int BYTES = 32 * D;
+  static constexpr int WARP = S * BYTES;
+  static constexpr int OFF_BAR = NW * WARP;
+  static constexpr int OFF_STEP = OFF_BAR + 8 * NW * S;
+  static constexpr int OFF_MISC = OFF_STEP + 16 * NW * S;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+};
+
+constexpr int weigh_ctas(int nt) { return nt == 1 ? 4 : 3; }
+
+template <int D, int NT, bool SMALLP>
+__global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(const __grid_constant__ CacheWeighParams p) {
+  using Q = WQueue<D, NT>;
+  constexpr int S = Q::S;
+  constexpr int NP = SMALLP ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const CacheView& c = p.c;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, t4 = lane % 4;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Q::OFF_BAR) + warp * S;
+  int4* steps = reinterpret_cast<int4*>(smem + Q::OFF_STEP) + warp * S;
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + Q::OFF_MISC);
+  uint8_t* queue = smem + warp * Q::WARP;
+  const int G = p.Hq / c.Hkv;
+
+  auto seq = [&](int i) -> unsigned {
+    const int n = cache_len(c, i);
+    return n ? (unsigned)units_of(n) * c.Hkv : 0u;
+  };
+  const unsigned total = line_total(c.B, seq);
+  if (total == 0) return;
+  const unsigned ctas = workers(total, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const Shares shares(total, ctas);
+  const unsigned end = shares.begin(blockIdx.x + 1);
+  unsigned at = shares.begin(blockIdx.x), seq0;
+  int b;
+  if (!line_find(c.B, seq, at, b, seq0)) return;
+  const int log_p = 31 - __clz(c.page);
+  unsigned phases = 0;
+  if (lane == 0) {
+    tma_prefetch_desc(&p.tm_k);
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  __syncthreads();
+  int ko[2][D / 64];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) ko[r][x] = boxed<D>(korder<D>(g) + 8 * r, 64 * x + 16 * t4);
+  // of the eight sums of a quad's columns, the lane writes that of one key
+  const int my_i = t4 >> 1, my_key = 16 * (t4 >> 1) + 8 * (t4 & 1) + korder<D>(g);
+
+  bool ok = true;
+  int place = 0;
+  while (ok && at < end) {
+    while (at >= seq0 + seq(b)) seq0 += seq(b++);
+    const int len = cache_len(c, b), units = units_of(len);
+    const int q_len = cache_count(p.q_lens, b, p.T, c.err);
+    const int h = (int)((at - seq0) / units), u0 = (int)((at - seq0) % units);
+    const int u1 = (int)min((unsigned)units, u0 + (end - at));
+    const int rows = G * q_len;                    // <= 8 NT: row r is token r / G, head r % G
+    auto row_at = [&](int r) -> long long { return ((long long)b * p.Hq + h * G + r % G) * p.T + r / G; };
+    QRaw<D> raw[NT];
+    float lse[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + g;
+      raw[n].fetch(r < rows ? reinterpret_cast<const __nv_bfloat16*>(p.q) + row_at(r) * D : nullptr, t4);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int rc = 8 * n + 2 * t4 + j;
+        lse[n][j] = rc < rows ? __ldg(p.lse + row_at(rc)) : 0.f;
+      }
+    }
+    Window<NP> window;
+    window.fill(c, b, h, len, nullptr, 0, u0, u1);
+    auto issue = [&](int s, int u) {
+      if (!window.has(u)) window.fill(c, b, h, len, nullptr, 0, u, u1);
+      int what[4] = {NOWHERE, 0, NOWHERE, 0};
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const Entry w = window.get(u, i);
+        what[2 * i] = w.pos;
+        what[2 * i + 1] = w.ks;
+        if (w.page >= 0 && lane == 0) {
+          const int row = (int)(((long long)w.page * c.Hkv + h) << log_p) + (w.pos & (c.page - 1));
+          mbar_expect_tx(&bars[s], (32 / NP) * D);
+          tma_load_3d(queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0), &p.tm_k, &bars[s], 0, row, 0);
+        }
+      }
+      if (lane == 0) {
+        steps[s] = make_int4(what[0], what[1], what[2], what[3]);
+        mbar_arrive(&bars[s]);
+      }
+    };
+    // the queue goes on where the last head left it
+    for (int s = 0; s < S; ++s) issue((place + s) % S, u0 + s);
+
+    QFrag<D> q[NT];
+    float fx[NT][2], ref[NT][2], fac[NT][2];
+    int vis[NT][2], vis_min = 0x7fffffff;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float e = raw[n].convert(q[n]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * t4 + j;
+        const float f = __shfl_sync(0xffffffffu, e, (2 * t4 + j) * 4);
+        reference(lse[n][j], r < rows, ref[n][j], fac[n][j]);
+        fx[n][j] = fac[n][j] == 0.f ? 0.f : p.c2 * f;
+        vis[n][j] = p.causal ? max(0, min(len, len - q_len + r / G + 1)) : len;
+        if (r < rows) vis_min = min(vis_min, vis[n][j]);
+      }
+    }
+    vis_min = __reduce_min_sync(0xffffffffu, vis_min);
+
+    const long long w_row = ((long long)b * c.Hkv + h) * c.max_pages * c.page;
+    for (int u = u0; ok && u < u1; ++u) {
+      if (!mbar_wait(&bars[place], (phases >> place) & 1, abort_flag, c.err)) { ok = false; break; }
+      phases ^= 1u << place;
+      const uint8_t* from = queue + place * Q::BYTES;
+      const int4 what = steps[place];
+      int pos[NP];
+      float kx[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        pos[i] = i ? what.z : what.x;
+        kx[i] = e8m0_value(i ? what.w : what.y);
+      }
+      // the lane's key: its weight is read early
+      const int key = SMALLP ? (my_i ? pos[NP - 1] : pos[0]) + my_key - 16 * my_i : pos[0] + my_key;
+      const float had = key < len ? p.w_in[w_row + key] : 0.f;
+      float s[NT][2][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[n][i][j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const uint4 ka = lds16(from + i * 16 * D + ko[0][k]);
+          const uint4 kb = lds16(from + i * 16 * D + ko[1][k]);
+          const uint32_t lo[4] = {ka.x, ka.y, ka.z, ka.w};
+          const uint32_t hi[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = e4m3x2_to_f16x2(lo[w]), a2 = e4m3x2_hi_to_f16x2(lo[w]);
+            const uint32_t a1 = e4m3x2_to_f16x2(hi[w]), a3 = e4m3x2_hi_to_f16x2(hi[w]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_16816(s[n][i], a0, a1, a2, a3, q[n].b[4 * k + w][0], q[n].b[4 * k + w][1]);
+          }
+        }
+      __syncwarp();
+      issue(place, u + S);
+      place = place + 1 == S ? 0 : place + 1;
+
+      bool full = true;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) full = full && pos[i] + 32 / NP <= vis_min;
+      float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};    // keys g, g + 8 of each 16
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = s[n][i][j] * kx[i % NP];
+            float e = ex2_approx(fmaf(x, fx[n][j & 1], -ref[n][j & 1]));
+            if (!full) {
+              const int kk = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1);
+              if (kk >= vis[n][j & 1]) e = 0.f;
+            }
+            w[i][j >> 1] = fmaf(e, fac[n][j & 1], w[i][j >> 1]);
+          }
+      float mine = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 1);
+          w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 2);
+          if (t4 == 2 * i + r) mine = w[i][r];
+        }
+      if (key < len) p.w_out[w_row + key] = had + mine;
+    }
+    // the S steps behind the head's last unit have no boxes, only phases
+    if (ok) {
+      for (int s = 0; s < S; ++s) {
+        const int st = (place + s) % S;
+        ok = mbar_wait(&bars[st], (phases >> st) & 1, abort_flag, c.err) && ok;
+        phases ^= 1u << st;
+      }
+    }
+    at += u1 - u0;
+  }
+  if (!ok) {                                       // what is still in flight
+    volatile int none = 0;
+    for (int s = 0; s < S; ++s) mbar_wait(&bars[s], (phases >> s) & 1, &none, c.err);
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+constexpr int BLOCK = 64;                          // rows prepared at once
 
 template <int D>
-__global__ void __launch_bounds__(32 * NW) cache_weigh_kernel(const __grid_constant__ CacheWeighParams p) {
+__global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __grid_constant__ CacheWeighParams p) {
+  constexpr int QW = D / 32;                       // 16-byte words of a lane's query operand
+  __shared__ uint4 s_q[BLOCK / 8][QW][32];         // row tile, word, lane
+  __shared__ float s_fx[BLOCK], s_ref[BLOCK], s_fac[BLOCK];
   const CacheView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t4 = lane % 4;
   const int h = blockIdx.y, b = blockIdx.z;
   const int len = cache_len(c, b);
-  const int key0 = blockIdx.x * UNIT + 32 * warp;
-  if (key0 >= len) return;
+  const int cta0 = blockIdx.x * UNIT;
+  if (cta0 >= len) return;
+  const int key0 = cta0 + 32 * warp;
   const int q_len = cache_count(p.q_lens, b, p.T, c.err);
   const int G = p.Hq / c.Hkv;
+  const int rows = G * q_len;
+  auto row_at = [&](int r) -> long long { return ((long long)b * p.Hq + h * G + r % G) * p.T + r / G; };
 
   uint32_t ka[2][D / 16][4];
   float kx[2];
-  int end[2];                                        // keys of each 16 that are there: below it
+  int end[2];                                      // keys of each 16 that are there: below it
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int k = key0 + 16 * i;
+    const int key = key0 + 16 * i;
     int pg = -1;
-    if (k < len) pg = cache_page(c, c.table, b, k / c.page);
-    const long long ph = (long long)max(pg, 0) * c.Hkv + h;
-    const long long tok = ph * c.page + k % c.page;
-    kx[i] = e8m0_value(__ldg(c.ks + ph));
+    if (key < len) pg = cache_page(c, c.table, b, key / c.page);
     end[i] = pg < 0 ? 0 : len;
+    const long long ph = (long long)max(pg, 0) * c.Hkv + h;
+    kx[i] = e8m0_value(__ldg(c.ks + ph));
+    const uint8_t* at = c.k + (ph * c.page + key % c.page + g) * D + 16 * t4;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(c.k + (tok + g) * D + 64 * j + 16 * t4));
-      const uint4 hi = __ldg(reinterpret_cast<const uint4*>(c.k + (tok + g + 8) * D + 64 * j + 16 * t4));
+    for (int x = 0; x < D / 64; ++x) {
+      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(at + 64 * x));
+      const uint4 hi = __ldg(reinterpret_cast<const uint4*>(at + 8 * D + 64 * x));
       const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        ka[i][4 * j + w][0] = e4m3x2_to_f16x2(a[w]);
-        ka[i][4 * j + w][1] = e4m3x2_to_f16x2(e[w]);
-        ka[i][4 * j + w][2] = e4m3x2_hi_to_f16x2(a[w]);
-        ka[i][4 * j + w][3] = e4m3x2_hi_to_f16x2(e[w]);
+        ka[i][4 * x + w][0] = e4m3x2_to_f16x2(a[w]);
+        ka[i][4 * x + w][1] = e4m3x2_to_f16x2(e[w]);
+        ka[i][4 * x + w][2] = e4m3x2_hi_to_f16x2(a[w]);
+        ka[i][4 * x + w][3] = e4m3x2_hi_to_f16x2(e[w]);
       }
     }
   }
-  const int rows = q_len * G;
-  // the first token that sees any key of the warp
-  const int t_first = p.causal ? max(0, key0 - (len - q_len)) : 0;
-  float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};          // keys g, g + 8 of each 16
-  for (int r0 = t_first * G / 8 * 8; r0 < rows; r0 += 8) {
-    const int rg = r0 + g;
-    QFrag<D> q;
-    const __nv_bfloat16* row = nullptr;
-    if (rg < rows)
-      row = reinterpret_cast<const __nv_bfloat16*>(p.q) +
-            (((long long)b * p.Hq + h * G + rg % G) * p.T + rg / G) * D;
-    QRaw<D> raw;
-    raw.fetch(row, t4);
-    const float e = raw.convert(q);
-    float fx[2], hi[2], lo[2];
-    int vis[2];
+  float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+
+  // tokens before these see none of the CTA's keys, of the warp's
+  const int t_cta = p.causal ? max(0, cta0 - (len - q_len)) : 0;
+  const int t_warp = p.causal ? max(0, key0 - (len - q_len)) : 0;
+  const int first = (int)min((long long)rows, (long long)t_warp * G);
+  for (int r0 = (int)min((long long)rows, (long long)t_cta * G) / BLOCK * BLOCK; r0 < rows; r0 += BLOCK) {
+    QRaw<D> raw[BLOCK / 8 / NW];
+    float lse[BLOCK / 8 / NW];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = r0 + 2 * t4 + j;
-      fx[j] = p.c2 * __shfl_sync(0xffffffffu, e, (2 * t4 + j) * 4);
-      vis[j] = 0;
-      hi[j] = lo[j] = 0.f;
-      if (r < rows) {
-        const int t = r / G;
-        // lse * log2 e as a sum of two floats
-        const float z = __ldg(p.lse + ((long long)b * p.Hq + h * G + r % G) * p.T + t);
-        hi[j] = z * 1.4426950216293335f;
-        lo[j] = fmaf(z, 1.4426950216293335f, -hi[j]) + z * 1.9259629911266175e-8f;
-        if (z != -INFINITY) vis[j] = p.causal ? max(0, min(len, len - q_len + t + 1)) : len;
+    for (int j = 0; j < BLOCK / 8 / NW; ++j) {
+      const int r = r0 + 8 * (warp + j * NW) + g;
+      raw[j].fetch(r < rows ? reinterpret_cast<const __nv_bfloat16*>(p.q) + row_at(r) * D : nullptr, t4);
+      lse[j] = r < rows ? __ldg(p.lse + row_at(r)) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < BLOCK / 8 / NW; ++j) {
+      const int n = warp + j * NW;
+      QFrag<D> q;
+      const float e = raw[j].convert(q);
+#pragma unroll
+      for (int x = 0; x < QW; ++x)
+        s_q[n][x][lane] = make_uint4(q.b[2 * x][0], q.b[2 * x][1], q.b[2 * x + 1][0], q.b[2 * x + 1][1]);
+      if (t4 == 0) {
+        float ref, fac;
+        reference(lse[j], r0 + 8 * n + g < rows, ref, fac);
+        s_ref[8 * n + g] = ref;
+        s_fac[8 * n + g] = fac;
+        s_fx[8 * n + g] = fac == 0.f ? 0.f : p.c2 * e;
       }
     }
-    float s[2][4];
+    __syncthreads();
+    if (key0 >= len) continue;                     // the sequence's last keys: this warp has none
+    for (int n = max(0, (first - r0) / 8); n < BLOCK / 8 && r0 + 8 * n < rows; ++n) {
+      float s[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_16816(s[i], ka[i][k][0], ka[i][k][1], ka[i][k][2], ka[i][k][3], q.b[k][0], q.b[k][1]);
+      for (int x = 0; x < QW; ++x) {
+        const uint4 q = s_q[n][x][lane];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = key0 + 16 * i + g + 8 * (j >> 1);
-        const float x = s[i][j] * kx[i] * fx[j & 1];
-        if (key < min(end[i], vis[j & 1])) w[i][j >> 1] += ex2_approx((x - hi[j & 1]) - lo[j & 1]);
+        for (int i = 0; i < 2; ++i)
+          mma_16816(s[i], ka[i][2 * x][0], ka[i][2 * x][1], ka[i][2 * x][2], ka[i][2 * x][3], q.x, q.y);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          mma_16816(s[i], ka[i][2 * x + 1][0], ka[i][2 * x + 1][1], ka[i][2 * x + 1][2], ka[i][2 * x + 1][3], q.z, q.w);
+      }
+      const float2 fx = *reinterpret_cast<const float2*>(&s_fx[8 * n + 2 * t4]);
+      const float2 ref = *reinterpret_cast<const float2*>(&s_ref[8 * n + 2 * t4]);
+      const float2 fac = *reinterpret_cast<const float2*>(&s_fac[8 * n + 2 * t4]);
+      // the tile's first token sees the fewest keys
+      const int r_min = r0 + 8 * n;
+      const bool full = !p.causal || len - q_len + r_min / G + 1 >= key0 + 32;
+      int vis[2] = {len, len};
+      if (!full) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) vis[j] = len - q_len + (r_min + 2 * t4 + j) / G + 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f0 = kx[i] * fx.x, f1 = kx[i] * fx.y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float e = ex2_approx(fmaf(s[i][j], (j & 1) ? f1 : f0, (j & 1) ? -ref.y : -ref.x));
+          if (!full && key0 + 16 * i + g + 8 * (j >> 1) >= vis[j & 1]) e = 0.f;
+          w[i][j >> 1] = fmaf(e, (j & 1) ? fac.y : fac.x, w[i][j >> 1]);
+        }
       }
     }
   }
@@ -111,18 +376,37 @@ __global__ void __launch_bounds__(32 * NW) cache_weigh_kernel(const __grid_const
       const int key = key0 + 16 * i + 8 * r + g;
       if (t4 == 0 && key < len) {
         const long long at = ((long long)b * c.Hkv + h) * c.max_pages * c.page + key;
-        p.w_out[at] = p.w_in[at] + w[i][r];
+        p.w_out[at] = p.w_in[at] + (key < end[i] ? w[i][r] : 0.f);
       }
     }
 }
 
+template <int D, int NT>
+cudaError_t launch_few(const CacheWeighParams& p, cudaStream_t st) {
+  constexpr int smem = WQueue<D, NT>::SMEM;
+  auto k = p.c.page == 16 ? cache_weigh_kernel<D, NT, true> : cache_weigh_kernel<D, NT, false>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long all = (long long)units_of((long long)p.c.max_pages * p.c.page) * p.c.Hkv * p.c.B;
+  const long long most = (long long)kSMs * weigh_ctas(NT);
+  k<<<(unsigned)(all < most ? all : most), 32 * NW, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
+bool cache_weigh_fits(int B, int Hkv, int page, int max_pages) {
+  return (long long)units_of((long long)max_pages * page) * Hkv * B < (1LL << 31);
+}
+
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
+  const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
+  if (rows <= 8) return p.c.d == 128 ? launch_few<128, 1>(p, st) : launch_few<64, 1>(p, st);
+  if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const dim3 grid((unsigned)((cap + UNIT - 1) / UNIT), (unsigned)p.c.Hkv, (unsigned)p.c.B);
-  if (p.c.d == 128) cache_weigh_kernel<128><<<grid, 32 * NW, 0, st>>>(p);
-  else cache_weigh_kernel<64><<<grid, 32 * NW, 0, st>>>(p);
+  if (p.c.d == 128) cache_weigh_rows_kernel<128><<<grid, 32 * NW, 0, st>>>(p);
+  else cache_weigh_rows_kernel<64><<<grid, 32 * NW, 0, st>>>(p);
   return cudaGetLastError();
 }
 
