@@ -362,9 +362,11 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_append(const fa4fp4_cache* cache, const vo
  *   s = softmax_scale * q.k, o = softmax(s) v, lse = ln sum e^s (nullable)
  * o: [B][Hq][T][d], f32 or bf16 per out_dtype; lse: f32 [B][Hq][T].  A token
  * that sees no key gets o = 0 and lse = -inf; rows t >= q_lens[b] are not
- * written.  The products are exact in the codes; P is rounded to f16 under a
- * factor 2^15 (f32 output: to the sum of two f16), the sums are FP32, the
- * result does not depend on anything but the arguments.  `workspace`: at least
+ * written.  The products are exact in the codes, the sums FP32.  P is rounded
+ * to f16 (half a step: 2^-12) under a power of two that takes V's page scales
+ * in, so that a P far below the largest V of its 128 keys is off by 2^-36 of
+ * that V at most; f32 output takes P as a sum of two f16 (2^-23).  The result
+ * does not depend on anything but the arguments.  `workspace`: at least
  * fa4fp4_cache_fwd_workspace_bytes(...) bytes of device memory
  * (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs. */
 FA4FP4_API size_t fa4fp4_cache_fwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page, int max_pages,

@@ -35,10 +35,10 @@
 // used unscaled: K's page scale multiplies the scores, V's goes into the
 // exponent of P, relative to the accumulator's own exponent.
 //
-// Roundings: q to f16 under a power of two (2^-32 of the row's largest), P to
-// f16 under a factor 2^11 (half a step is 2^-12, and values keep it down to
-// 2^-17 at least), or for FP32 output P as a sum of two f16 (2^-23).  The normalizer
-// sums the FP32 values of P.
+// Roundings: q to f16 under a power of two (2^-32 of the row's largest); P to
+// f16 under a factor 2^15 and V's relative exponent (2^-12 of P, or 2^-36 of the
+// largest V of the 32 keys if that is more), for FP32 output as a sum of two f16
+// (2^-23, or the same 2^-36).  The normalizer sums the FP32 values of P.
 #include "cache_line.cuh"
 
 namespace fa4 {
@@ -48,11 +48,11 @@ constexpr int NW = LINE_WARPS;
 // log2 of the factor on P: the largest P is half of f16's largest power
 constexpr float P_BIAS = 15.f;
 // How far a step's greatest V exponent may lie below the accumulator's before
-// the accumulator's is lowered: P keeps half a step of 2^-12 (22 bits as a sum
-// of two) down to there.  Lowering is bounded, so that the accumulator stays
-// below 2^(40 + 80) (its terms: 2^15 * 448, fewer than 2^17 of them a warp).
-constexpr int v_down(bool split) { return split ? 8 : 24; }
-constexpr int V_LOWER = 80;
+// the accumulator's is lowered: P's smallest f16 step, 2^-24 under its factor
+// 2^15, is then at most 2^-35 of the step's largest V, its half 2^-36.  Lowering
+// is bounded, so that the accumulator stays below 2^(40 + 80) (its terms: 2^15 *
+// 448, fewer than 2^17 of them a warp).
+constexpr int V_DOWN = 4, V_LOWER = 80;
 // the mark of a counter word, in its high 48 bits (no number, no pointer and no
 // pair of floats that a workspace could hold from other use)
 constexpr unsigned long long MARK = 0xfa4c0de5eed5ull;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       int ev_max = ev[0];
 #pragma unroll
       for (int i = 1; i < NP; ++i) ev_max = max(ev_max, ev[i]);
-      if (ev_max > -1000 && (ev_max > xo || ev_max < xo - v_down(SPLIT))) {
+      if (ev_max > -1000 && (ev_max > xo || ev_max < xo - V_DOWN)) {
         const int to = max(ev_max, xo - V_LOWER);
         const float by = pow2_any(xo - to);
 #pragma unroll
@@ -622,7 +622,18 @@ size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int 
   return grid ? Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid : 0;
 }
 
+// Whether the kernel for many rows is the faster one.  Both take time in
+// proportion to the keys: per 128 of them, 1.3 us for each wave of its CTAs (256
+// rows of a kv head each) against 0.0048 us for each block of 16 rows here.
+static bool many_rows(const CacheFwdParams& p) {
+  if (p.pages || !p.out_bf16) return false;
+  const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T, heads = (long long)p.c.Hkv * p.c.B;
+  const long long waves = (((rows + 255) / 256) * heads + kSMs - 1) / kSMs;
+  return rows > 16 && 1.3 * waves < 0.0048 * (double)((rows + 15) / 16 * heads);
+}
+
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st) {
+  if (many_rows(p)) return launch_cache_chunk(p, st);
   const Line ln = make_line(p.Hq, p.c.Hkv, p.T, p.pages != nullptr);
   const int grid = grid_of(ln, p.c.B, p.c.d, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);
   if (grid == 0) return cudaErrorInvalidValue;

@@ -90,14 +90,15 @@ class Ref:
         return max(0, min(length, length - q_len + t + 1)) if causal else length
 
     def fwd(self, q, lens, q_lens, causal=True, scale=None, pages=None):
-        """q [B, Hq, T, d] float64.  Returns (o, lse, spread, eps): spread = sum
-        p |v| / sum p, eps = a bound of the error of a score per unit 2^-23 * d
-        (the greatest sum |q| |k| * scale)."""
+        """q [B, Hq, T, d] float64.  Returns (o, lse, spread, eps, small): spread
+        = sum p |v| / sum p, eps = a bound of the error of a score per unit
+        2^-23 * d (the greatest sum |q| |k| * scale), small = 2^-35 * keys * the
+        largest |v| of the sequence's head."""
         B, Hq, T, d = q.shape
         G = Hq // self.H
         scale = d ** -0.5 if scale is None else scale
         o, spread = np.zeros(q.shape), np.zeros(q.shape)
-        lse, eps = np.full((B, Hq, T), -np.inf), np.zeros((B, Hq, T))
+        lse, eps, small = np.full((B, Hq, T), -np.inf), np.zeros((B, Hq, T)), np.zeros((B, Hq, T))
         for b in range(B):
             L, n = int(lens[b]), int(q_lens[b])
             for hk in range(self.H):
@@ -117,7 +118,8 @@ class Ref:
                         spread[b, h, t] = p @ np.abs(V[see]) / p.sum()
                         lse[b, h, t] = m + np.log(p.sum())
                         eps[b, h, t] = (np.abs(K[see]) @ np.abs(q[b, h, t])).max() * scale
-        return o, lse, spread, eps
+                        small[b, h, t] = 2.0 ** -35 * see.sum() * np.abs(V).max()
+        return o, lse, spread, eps, small
 
     def select(self, q, lens, q_lens, n_sel):
         B, Hq, T, d = q.shape

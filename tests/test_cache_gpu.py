@@ -8,8 +8,12 @@ order) every weight is off by at most 2 eps + 2^-20 relative (the exponential,
 its argument and the running rescales), and P itself by 2^-12 (f16: half a step
 is 2^-12 for values in [1, 2) * 2^k) or 2^-22 (the sum of two f16).  Numerator
 and normalizer each carry the weights' error, so
-  |o - ref| <= (4 eps + 2^-19 + p_err) * spread + out_err * |ref|,
-spread = sum p |v| / sum p and out_err half a step of the output's type: 2^-9
+  |o - ref| <= (4 eps + 2^-19 + p_err) * spread + out_err * |ref| + 2^-35 n V,
+with n keys and V their largest |v|: P times 2^15 times the ratio of V's page
+scale to the accumulator's (at most 2^4 above the largest of the keys that are
+multiplied together) is a f16 number, whose smallest step is 2^-24; half of it
+is 2^-25 2^-15 2^4 = 2^-36 of a scale 2^X with 448 * 2^X < 2 V, and the weights'
+sum is at least 1.  spread = sum p |v| / sum p and out_err half a step of the output's type: 2^-9
 bf16 (eps 2^-7 relative to the binade's foot: 2^-8), 2^-24 FP32.
   |lse - ref| <= 2 eps + 2^-20 + 2^-22 |ref|."""
 import numpy as np
@@ -27,10 +31,10 @@ def f64(t):
 
 
 def check_fwd(o, lse, ref, d, f32, rows=None):
-    ro, rl, spread, eps = ref
+    ro, rl, spread, eps, small = ref
     e = eps * d * 2.0 ** -23
     tol = (4 * e + 2.0 ** -19 + (2.0 ** -22 if f32 else 2.0 ** -12))[..., None] * spread
-    tol += (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(ro) + 1e-37
+    tol += (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(ro) + small[..., None] + 1e-37
     o, lse = f64(o), f64(lse)
     rows = np.ones(rl.shape, bool) if rows is None else rows
     assert np.isfinite(o[rows]).all()
@@ -175,6 +179,75 @@ def test_fwd_split(lens, G, T, d, page):
     ob, _ = fa.cache_fwd(q, cache, table, ln)
     check_fwd(ob, lse, R.Ref.of(cache, table).fwd(f64(q), lens, ql), d, False)
     fa.sync_status()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,page,H,G,T", [(128, 64, 8, 4, 70), (128, 16, 8, 1, 300), (64, 128, 8, 5, 60), (64, 32, 16, 2, 129),
+                                          (128, 32, 8, 16, 20), (128, 128, 8, 3, 100)])
+def test_fwd_chunk(d, page, H, G, T, causal):
+    """Many query tokens per sequence and enough heads for the kernel that takes
+    256 rows at a time; contexts shorter than the chunk, none at all, ragged
+    query counts, NaN codes behind every end."""
+    fa = require_gpu()
+    lens = [T + 150, T, 0, T // 2, 515, T + 128 - T % 128]
+    q_lens = [T, T, T, T, T - 1, 3]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=40)
+    q = queries(len(lens), H * G, T, d, 41)
+    ql = torch.tensor(q_lens, dtype=torch.int32).cuda()
+    o = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    fa.cache_fwd(q, cache, table, ln, q_lens=ql, causal=causal, out=o, lse=lse)
+    fa.sync_status()
+    rows = np.broadcast_to(np.arange(T)[None, None, :] < np.array(q_lens)[:, None, None], lse.shape)
+    check_fwd(o, lse, R.Ref.of(cache, table).fwd(f64(q), lens, q_lens, causal), d, False, rows)
+    assert (f64(o)[~rows] == 7).all() and (f64(lse)[~rows] == 7).all()
+    o2, l2 = fa.cache_fwd(q, cache, table, ln, q_lens=ql, causal=causal, with_lse=False)
+    assert l2 is None and torch.equal(o2.cpu()[torch.tensor(rows)], o.cpu()[torch.tensor(rows)])
+
+
+def test_fwd_chunk_scales_far_apart():
+    """As below, through the kernel for many rows: pages whose V scales differ
+    by up to 2^77 and K scales by 4."""
+    fa = require_gpu()
+    d, page, H, G, T = 128, 16, 8, 4, 128
+    lens = [300, 300, 41]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=42)
+    g = torch.Generator().manual_seed(43)
+    k = torch.randn(3, H, 300, d, generator=g)
+    v = torch.randn(3, H, 300, d, generator=g)
+    for i in range(0, 300, page):
+        v[:, :, i:i + page] *= 2.0 ** (40 - 7 * (i // page % 12))
+        k[:, :, i:i + page] *= 2.0 ** (i // page % 3)
+    fa.cache_append(cache, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), table, torch.zeros_like(ln), n_new=ln)
+    q = queries(3, H * G, T, d, 44)
+    q[0, 5] *= 1e-20
+    q[1, 7] = 0
+    q[2, 9, 100, 3] = float("nan")
+    o, lse = fa.cache_fwd(q, cache, table, ln, softmax_scale=0.2)
+    fa.sync_status()
+    rows = np.ones(lse.shape, bool)
+    rows[2, 9, 100] = False
+    check_fwd(o, lse, R.Ref.of(cache, table).fwd(np.nan_to_num(f64(q)), lens, [T] * 3, scale=0.2), d, False, rows)
+    assert torch.isnan(o[2, 9, 100]).all()
+
+
+def test_fwd_chunk_bad_page():
+    fa = require_gpu()
+    d, page, H, G, T = 64, 32, 8, 4, 100
+    lens = [200, 300, 250]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=45)
+    q = queries(3, H * G, T, d, 46)
+    want = R.Ref.of(cache, table).fwd(f64(q), lens, [T] * 3)
+    t = table.clone()
+    t[1, 4] = cache.num_pages
+    o, lse = fa.cache_fwd(q, cache, t, ln)
+    with pytest.raises(fa.Fa4Fp4Error) as e:
+        fa.sync_status()
+    assert e.value.status == 7
+    rows = np.ones(lse.shape, bool)
+    rows[1] = False
+    check_fwd(o, lse, want, d, False, rows)
+    assert np.isfinite(f64(o)).all()
 
 
 @pytest.mark.parametrize("T", [1, 40, 200])
