@@ -385,8 +385,9 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void*
  * all of them where there are no more.  pages (int32 [B][Hkv][T][n_sel])
  * receives them in ascending order, then -1; rows t >= q_lens[b] are all -1.
  * The set is that of the real-valued bounds: FP32 sums decide only where their
- * error bounds allow it, the rest is evaluated in 64 bits.  max_pages <= 2^18,
- * Hkv * T <= 65535.  `workspace` as for fa4fp4_cache_fwd. */
+ * error bounds allow it, the rest is evaluated in 64 bits.  max_pages <= 2^18.
+ * `workspace` as for fa4fp4_cache_fwd; up to 16384 pages it needs none (its size
+ * is 0 and it may be NULL). */
 FA4FP4_API size_t fa4fp4_cache_select_workspace_bytes(int B, int Hkv, int T, int max_pages);
 FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const void* q, const int* page_table,
                                              const int* lens, const int* q_lens, int B, int Hq, int T, int max_pages,

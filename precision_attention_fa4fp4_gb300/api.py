@@ -749,10 +749,11 @@ def cache_select(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, lens
         _expect_on(cache, "out", out, shape, torch.int32)
     lib = load_library()
     with _on(cache.device):
-        ws = _cache_workspace(cache, workspace, B * cache.Hkv * T * max_pages * 8)
+        need = lib.fa4fp4_cache_select_workspace_bytes(B, cache.Hkv, T, max_pages)
+        ws = _cache_workspace(cache, workspace, need) if need or workspace is not None else None
         _check("fa4fp4_cache_select", lib.fa4fp4_cache_select(
             cache._struct, _at(q), _at(page_table), _at(lens), _at(q_lens), B, Hq, T, max_pages, shape[3], _at(out),
-            _at(ws), ws.numel(), _raw_stream(cache.device)))
+            _at(ws), ws.numel() if ws is not None else 0, _raw_stream(cache.device)))
     return out
 
 

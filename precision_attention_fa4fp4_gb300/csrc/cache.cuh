@@ -164,4 +164,24 @@ FA4_DEV unsigned long long atomic_add_acq_rel(unsigned long long* p, unsigned lo
   return had;
 }
 
+// E4M3 codes, four to a word, as unsigned bytes in the order of their values
+// (-0 just below 0), and back.
+FA4_DEV uint32_t e4m3_ordered(uint32_t x) {
+  const uint32_t neg = (x >> 7) & 0x01010101u;
+  return x ^ (neg * 0x7fu | 0x80808080u);
+}
+FA4_DEV uint32_t e4m3_unordered(uint32_t x) {
+  const uint32_t neg = (~x >> 7) & 0x01010101u;
+  return x ^ (neg * 0x7fu | 0x80808080u);
+}
+
+// Four codes times a power of two, rounded to nearest even (0 stays 0 whatever
+// the factor).
+FA4_DEV uint32_t e4m3_times(uint32_t x, float f) {
+  const uint32_t a = e4m3x2_to_f16x2(x), z = e4m3x2_hi_to_f16x2(x);
+  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z));
+  return pack_e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
+}
+
 }  // namespace fa4

@@ -55,8 +55,10 @@ struct CacheSelectParams {
   const int* q_lens;
   int Hq, T, n_sel;
   float2* score;         // workspace [B][Hkv][T][max_pages]: FP32 bound and its error
+                         // (unused where max_pages fits shared memory)
   int* out;              // [B][Hkv][T][n_sel]
 };
+size_t cache_select_workspace(int B, int Hkv, int T, int max_pages);
 cudaError_t launch_cache_select(const CacheSelectParams& p, cudaStream_t st);
 
 struct CacheWeighParams {

@@ -126,7 +126,7 @@ fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void* q, const i
 
 size_t fa4fp4_cache_select_workspace_bytes(int B, int Hkv, int T, int max_pages) {
   if (B < 0 || Hkv < 0 || T < 0 || max_pages < 1) return 0;
-  return (size_t)B * Hkv * T * max_pages * 8;
+  return cache_select_workspace(B, Hkv, T, max_pages);
 }
 
 fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const void* q, const int* page_table, const int* lens,
@@ -135,14 +135,13 @@ fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const void* q, cons
   fa4fp4_status s = check_call(cache, B, Hq, T, max_pages);
   if (s != FA4FP4_OK) return s;
   if (n_sel < 1) return FA4FP4_ERR_INVALID_ARG;
-  // one bit per page in shared memory; the rows in one grid dimension
-  if (max_pages > (1 << 18) || (long long)cache->Hkv * T > 65535) return FA4FP4_ERR_UNSUPPORTED;
+  if (max_pages > (1 << 18)) return FA4FP4_ERR_UNSUPPORTED;   // one bit per page in shared memory
   if (B == 0 || Hq == 0 || T == 0) return FA4FP4_OK;
   if ((s = check_cache(cache, page_table, lens, q_lens)) != FA4FP4_OK) return s;
   if (!q || !pages) return FA4FP4_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(pages, 4)) return FA4FP4_ERR_ALIGNMENT;
-  if (!workspace || workspace_bytes < fa4fp4_cache_select_workspace_bytes(B, cache->Hkv, T, max_pages))
-    return FA4FP4_ERR_WORKSPACE;
+  const size_t need = cache_select_workspace(B, cache->Hkv, T, max_pages);
+  if (need && (!workspace || workspace_bytes < need)) return FA4FP4_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return FA4FP4_ERR_ALIGNMENT;
   CacheSelectParams p;
   memset(&p, 0, sizeof(p));

@@ -3,9 +3,10 @@
 // Per sequence and kv head the `recent` newest tokens stay, and of the others
 // the heaviest, `budget` in all, ties to the lowest position.  Two kernels: the
 // first finds the cut among the weights by radix selection (one CTA per
-// sequence and head, four passes over the weights) and writes the kept
-// positions in ascending order with their weights; the second copies the
-// tokens into fresh pages, one CTA per (page, head, K or V).
+// sequence and head, three digits, the keys in registers while there are at
+// most 32768) and writes the kept positions in ascending order with their
+// weights; the second copies the tokens into fresh pages, one CTA per (page,
+// head).
 //
 // Tokens of pages with different scales meet in one page, so the codes are
 // fitted anew under the append's rule: X = the least integer >= -127 with every
@@ -14,7 +15,7 @@
 // e4m3(code) <= 448 2^e.  The codes then move by 2^(X_src - X), exact but for
 // codes that become subnormal.  Bound by HBM: d bytes read and written per kept
 // token, head and tensor, 4 bytes of weight read per token.
-#include "cache.cuh"
+#include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
@@ -28,10 +29,56 @@ FA4_DEV uint32_t weight_key(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+constexpr int WARPS1 = NT1 / 32;
+
+// Exclusive prefix over the CTA, in the order (chunk, thread), of flags: chunk
+// j's of this thread is bit j of `flags`; at(j) is what add() gets.  s_cnt has
+// EPT * 32 entries, s_tot 32.  Returns the total.
+template <int EPT, class F>
+FA4_DEV int block_places(uint32_t flags, int* s_cnt, int* s_tot, F add) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const unsigned v = __ballot_sync(0xffffffffu, (flags >> j) & 1u);
+    if (lane == 0) s_cnt[j * WARPS1 + warp] = __popc(v);
+  }
+  __syncthreads();
+  if (warp < EPT) {                                // chunk `warp`: prefix over its warps
+    const int v = s_cnt[warp * WARPS1 + lane];
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    s_cnt[warp * WARPS1 + lane] = inc - v;
+    if (lane == 31) s_tot[warp] = inc;
+  }
+  __syncthreads();
+  const int v = lane < EPT ? s_tot[lane] : 0;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  const int before = inc - v;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int base = __shfl_sync(0xffffffffu, before, j) + s_cnt[j * WARPS1 + warp];
+    const unsigned all = __ballot_sync(0xffffffffu, (flags >> j) & 1u);
+    add(j, base + __popc(all & ((1u << lane) - 1u)));
+  }
+  return __shfl_sync(0xffffffffu, inc, 31);
+}
+
+// EPT chunks of NT1 weights at a time; all of them at once (and kept) if ONCE.
+template <int EPT, bool ONCE>
 __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__ CacheEvictParams p) {
-  __shared__ unsigned s_hist[256];
-  __shared__ unsigned s_bin, s_rank;
-  __shared__ int s_warp[2][NT1 / 32];
+  __shared__ unsigned s_hist[2048];
+  __shared__ unsigned s_bin, s_rank, s_count;
+  __shared__ int s_cnt[EPT * WARPS1], s_tot[32];
   const CacheView& c = p.c;
   const int h = blockIdx.x, b = blockIdx.y;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -45,84 +92,94 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
   float* w_out = p.w_out ? p.w_out + ((long long)b * c.Hkv + h) * p.dst_pages * c.page : nullptr;
   if (h == 0 && threadIdx.x == 0) p.new_lens[b] = keep;
 
+  float x[EPT];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const int i = base + j * NT1 + threadIdx.x;
+      x[j] = i < len ? __ldg(w + i) : 0.f;
+    }
+  };
+  if (ONCE) load(0);
   uint32_t cut = 0;                                // keys above it stay, and `ties` of those on it
   unsigned ties = 0;
+  bool all_ties = true;                            // all of those on it
   if (k > 0 && k < n) {
     unsigned rank = k;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += NT1) s_hist[i] = 0;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      const uint32_t digit = d == 2 ? 1023u : 2047u;
+      const uint32_t mask = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffffc00u;
+      for (int i = threadIdx.x; i < 2048; i += NT1) s_hist[i] = 0;
       __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = threadIdx.x; i < n; i += NT1) {
-        const uint32_t key = weight_key(__ldg(w + i));
-        if ((key & mask) == cut) atomicAdd(&s_hist[(key >> shift) & 255u], 1u);
+      for (int base = 0; base < n; base += EPT * NT1) {
+        if (!ONCE) load(base);
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+          const uint32_t key = weight_key(x[j]);
+          if (base + j * NT1 + (int)threadIdx.x < n && (key & mask) == cut) atomicAdd(&s_hist[(key >> shift) & digit], 1u);
+        }
       }
       __syncthreads();
-      if (warp == 0) {
-        unsigned v[8], sum = 0;
+      // two bins a thread, from the top: where the rank falls
+      const unsigned v0 = s_hist[2047 - 2 * threadIdx.x], v1 = s_hist[2046 - 2 * threadIdx.x];
+      unsigned inc = v0 + v1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { v[i] = s_hist[255 - (lane * 8 + i)]; sum += v[i]; }
-        unsigned inc = sum;
+      for (int o = 1; o < 32; o *= 2) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) s_tot[warp] = (int)inc;
+      __syncthreads();
+      unsigned tot = (unsigned)s_tot[lane];
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += u;
-        }
-        unsigned before = inc - sum;
-        if (before < rank && rank <= inc) {
-          unsigned r = rank - before;
-          int i = 0;
-          while (i < 7 && r > v[i]) { r -= v[i]; ++i; }
-          s_bin = 255 - (lane * 8 + i);
-          s_rank = r;
-        }
+      for (int o = 1; o < 32; o *= 2) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, tot, o);
+        if (lane >= o) tot += up;
+      }
+      const unsigned before = (warp ? __shfl_sync(0xffffffffu, tot, warp - 1) : 0u) + inc - v0 - v1;
+      if (before < rank && rank <= before + v0 + v1) {
+        const bool first = rank <= before + v0;
+        s_bin = 2047 - 2 * threadIdx.x - (first ? 0 : 1);
+        s_rank = rank - before - (first ? 0 : v0);
+        s_count = first ? v0 : v1;
       }
       __syncthreads();
       cut |= s_bin << shift;
       rank = s_rank;
     }
     ties = rank;
+    all_ties = s_count == rank;
   }
   const bool all = k >= n, none = k == 0;
-  // ordered copy of what stays: positions above the cut, and the first `ties` on it
-  int done = 0;
-  unsigned seen = 0;
-  for (int base = 0; base < len; base += NT1) {
-    const int i = base + threadIdx.x;
-    bool above = false, on = false;
-    float x = 0.f;
-    if (i < len) {
-      x = __ldg(w + i);
-      const uint32_t key = weight_key(x);
-      above = i >= n || all || (!none && key > cut);
-      on = !above && !none && key == cut;
-    }
-    const unsigned bo = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) s_warp[0][warp] = __popc(bo);
-    __syncthreads();
-    unsigned before = seen, sum = 0;
+  int done = 0, seen = 0;
+  for (int base = 0; base < len; base += EPT * NT1) {
+    if (!ONCE) load(base);
+    uint32_t take = 0, on = 0;
 #pragma unroll
-    for (int j = 0; j < NT1 / 32; ++j) {
-      if (j < warp) before += s_warp[0][j];
-      sum += s_warp[0][j];
+    for (int j = 0; j < EPT; ++j) {
+      const int i = base + j * NT1 + threadIdx.x;
+      if (i < len) {
+        const uint32_t key = weight_key(x[j]);
+        if (i >= n || all || (!none && key > cut)) take |= 1u << j;
+        else if (!none && key == cut) on |= 1u << j;
+      }
     }
-    const bool take = above || (on && before + __popc(bo & ((1u << lane) - 1u)) < ties);
-    seen += sum;
-    const unsigned bt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) s_warp[1][warp] = __popc(bt);
-    __syncthreads();
-    int at = done, cnt = 0;
-#pragma unroll
-    for (int j = 0; j < NT1 / 32; ++j) {
-      if (j < warp) at += s_warp[1][j];
-      cnt += s_warp[1][j];
+    if (all_ties) take |= on;
+    else {
+      uint32_t more = 0;
+      seen += block_places<EPT>(on, s_cnt, s_tot, [&](int j, int place) {
+        if (((on >> j) & 1u) && seen + place < (int)ties) more |= 1u << j;
+      });
+      take |= more;
     }
-    at += __popc(bt & ((1u << lane) - 1u));
-    if (take && at < p.budget) {
-      kept[at] = i;
-      if (w_out) w_out[at] = x;
-    }
-    done += cnt;
+    done += block_places<EPT>(take, s_cnt, s_tot, [&](int j, int place) {
+      if (((take >> j) & 1u) && done + place < p.budget) {
+        kept[done + place] = base + j * NT1 + threadIdx.x;
+        if (w_out) w_out[done + place] = x[j];
+      }
+    });
   }
   for (int i = keep + threadIdx.x; i < p.budget; i += NT1) kept[i] = -1;
   if (w_out)
@@ -130,10 +187,6 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
 }
 
 constexpr int NT2 = 128;
-
-FA4_DEV float pow2_any(int x) {                    // 2^x for x in [-247, 127]
-  return x >= -126 ? exp2i(x) : (x >= -149 ? __uint_as_float(1u << (x + 149)) : 0.f);
-}
 
 // The least e with e4m3(code) <= 448 * 2^e for a magnitude 1..0x7e (448 =
 // 1.75 * 2^8): normal codes E - 15, plus one above a significand of 1.75;
@@ -145,14 +198,14 @@ FA4_DEV int code_exp(uint32_t mag) {
 
 template <int D, int P>
 __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__ CacheEvictParams p) {
-  constexpr int PARTS = D / 8;
-  constexpr int TOK = NT2 / PARTS;
+  constexpr int PARTS = D / 16;                    // 16-byte words of a token
+  constexpr int TOK = NT2 / PARTS;                 // tokens at once
   constexpr int N = (P + TOK - 1) / TOK;
-  __shared__ int s_x[NT2 / 32];
-  __shared__ float s_lo[NT2 / 32][D], s_hi[NT2 / 32][D];
+  __shared__ int s_x[2][NT2 / 32];
+  __shared__ uint4 s_lo[NT2 / 32][PARTS], s_hi[NT2 / 32][PARTS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const CacheView& c = p.c;
-  const int h = blockIdx.y >> 1, isv = blockIdx.y & 1, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int keep = min(cache_len(c, b), p.budget);
   const int first = blockIdx.x * P;
   if (first >= keep) return;
@@ -161,125 +214,129 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
     if (threadIdx.x == 0) atomicOr(c.err, FA4_DEVERR_INDEX);
     return;
   }
-  const uint8_t* pool = isv ? c.v : c.k;
-  const uint8_t* scales = isv ? c.vs : c.ks;
   const int* kept = p.kept + ((long long)b * c.Hkv + h) * p.budget + first;
   const int part = threadIdx.x % PARTS, tok = threadIdx.x / PARTS;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  uint2 w[N];
-  int xs[N];
-  long long at[N];
+  int src[N], row[N];                              // position; pool row of it (-1: none)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int s = tok + i * TOK;
-    at[i] = -1;
-    if (s < P && first + s < keep) {
-      const int src = kept[s];
-      const int pg = cache_page(c, c.table, b, src / P);
-      if (pg >= 0) at[i] = ((long long)pg * c.Hkv + h) * P + src % P;
-    }
-  }
-  int X = -127;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i] = make_uint2(0, 0);
-    xs[i] = 0;
-    if (at[i] >= 0) {
-      w[i] = __ldg(reinterpret_cast<const uint2*>(pool + at[i] * D + part * 8));
-      xs[i] = (int)__ldg(scales + at[i] / P) - 127;
-    }
+    src[i] = s < P && first + s < keep ? kept[s] : -1;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t a = __vmaxu4(w[i].x & 0x7f7f7f7fu, w[i].y & 0x7f7f7f7fu);
-    const uint32_t e = __vmaxu4(a, a >> 16);
-    const uint32_t mag = max(e & 0xffu, (e >> 8) & 0xffu);
-    if (mag) X = max(X, xs[i] + code_exp(mag));
+    row[i] = -1;
+    if (src[i] >= 0) {
+      const int pg = cache_page(c, c.table, b, src[i] / P);
+      if (pg >= 0) row[i] = (pg * c.Hkv + h) * P + src[i] % P;
+    }
   }
-  X = __reduce_max_sync(0xffffffffu, X);
-  if (lane == 0) s_x[warp] = X;
+  uint4 w[2][N];
+  int xs[2][N];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[kv][i] = make_uint4(0, 0, 0, 0);
+      xs[kv][i] = 0;
+      if (row[i] >= 0) {
+        w[kv][i] = __ldg(reinterpret_cast<const uint4*>((kv ? c.v : c.k) + (long long)row[i] * D) + part);
+        xs[kv][i] = (int)__ldg((kv ? c.vs : c.ks) + row[i] / P) - 127;
+      }
+    }
+  int X[2] = {-127, -127};
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint4 x = w[kv][i];
+      uint32_t a = __vmaxu4(__vmaxu4(x.x & 0x7f7f7f7fu, x.y & 0x7f7f7f7fu), __vmaxu4(x.z & 0x7f7f7f7fu, x.w & 0x7f7f7f7fu));
+      a = __vmaxu4(a, a >> 16);
+      const uint32_t mag = max(a & 0xffu, (a >> 8) & 0xffu);
+      if (mag) X[kv] = max(X[kv], xs[kv][i] + code_exp(mag));
+    }
+    X[kv] = __reduce_max_sync(0xffffffffu, X[kv]);
+    if (lane == 0) s_x[kv][warp] = X[kv];
+  }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NT2 / 32; ++i) X = max(X, s_x[i]);
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int i = 0; i < NT2 / 32; ++i) X[kv] = max(X[kv], s_x[kv][i]);
 
   const long long ph = (long long)dst * c.Hkv + h;
-  uint8_t* codes = (isv ? c.v : c.k) + ph * P * D;
-  float lo[8], hi[8];
+  uint32_t lo[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu}, hi[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) { lo[j] = 448.f; hi[j] = -448.f; }
+  for (int kv = 0; kv < 2; ++kv) {
+    uint4* to = reinterpret_cast<uint4*>((kv ? c.v : c.k) + ph * P * D) + part;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int s = tok + i * TOK;
-    if (s < P && first + s < keep) {
-      uint2 e = w[i];
-      float f[8];
-      const uint32_t u[2] = {e.x, e.y};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t a = e4m3x2_to_f16x2(u[j]), z = e4m3x2_hi_to_f16x2(u[j]);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&z));
-        f[4 * j] = x.x; f[4 * j + 1] = x.y; f[4 * j + 2] = y.x; f[4 * j + 3] = y.y;
+    for (int i = 0; i < N; ++i) {
+      if (src[i] < 0) continue;
+      uint4 x = w[kv][i];
+      if (xs[kv][i] != X[kv]) {
+        const float f = pow2_any(min(xs[kv][i] - X[kv], 127));
+        x = make_uint4(e4m3_times(x.x, f), e4m3_times(x.y, f), e4m3_times(x.z, f), e4m3_times(x.w, f));
       }
-      if (xs[i] != X) {
-        // zero codes may come from any exponent: keep the factor finite
-        const float mv = pow2_any(min(xs[i] - X, 127));
+      to[(tok + i * TOK) * PARTS] = x;
+      if (kv == 0) {
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] == 0.f ? f[j] : f[j] * mv;
-        e = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
-        if (!isv) {
-          const uint32_t r[2] = {e.x, e.y};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t a = e4m3x2_to_f16x2(r[j]), z = e4m3x2_hi_to_f16x2(r[j]);
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&z));
-            f[4 * j] = x.x; f[4 * j + 1] = x.y; f[4 * j + 2] = y.x; f[4 * j + 3] = y.y;
-          }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t o = e4m3_ordered(u[j]);
+          lo[j] = __vminu4(lo[j], o);
+          hi[j] = __vmaxu4(hi[j], o);
         }
       }
-      *reinterpret_cast<uint2*>(codes + (long long)s * D + part * 8) = e;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) { lo[j] = fminf(lo[j], f[j]); hi[j] = fmaxf(hi[j], f[j]); }
     }
   }
-  if (threadIdx.x == 0) ((isv ? c.vs : c.ks) + ph)[0] = (uint8_t)(X + 127);
-  if (isv) return;
+  if (threadIdx.x < 2) (threadIdx.x ? c.vs : c.ks)[ph] = (uint8_t)(X[threadIdx.x] + 127);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int o = PARTS; o < 32; o *= 2) {
-      lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
-      hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+      lo[j] = __vminu4(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      hi[j] = __vmaxu4(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
     }
   if (lane < PARTS) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) { s_lo[warp][part * 8 + j] = lo[j]; s_hi[warp][part * 8 + j] = hi[j]; }
+    s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    s_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
   __syncthreads();
   if (threadIdx.x < 2 * PARTS) {
     const bool up = threadIdx.x >= PARTS;
-    float f[8];
+    uint4 r = up ? s_hi[0][part] : s_lo[0][part];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[j] = up ? -448.f : 448.f;
-#pragma unroll
-      for (int i = 0; i < NT2 / 32; ++i)
-        f[j] = up ? fmaxf(f[j], s_hi[i][part * 8 + j]) : fminf(f[j], s_lo[i][part * 8 + j]);
+    for (int i = 1; i < NT2 / 32; ++i) {
+      const uint4 y = up ? s_hi[i][part] : s_lo[i][part];
+      r.x = up ? __vmaxu4(r.x, y.x) : __vminu4(r.x, y.x);
+      r.y = up ? __vmaxu4(r.y, y.y) : __vminu4(r.y, y.y);
+      r.z = up ? __vmaxu4(r.z, y.z) : __vminu4(r.z, y.z);
+      r.w = up ? __vmaxu4(r.w, y.w) : __vminu4(r.w, y.w);
     }
-    *reinterpret_cast<uint2*>(c.kb + ph * 2 * D + (up ? D : 0) + part * 8) =
-        make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+    reinterpret_cast<uint4*>(c.kb + ph * 2 * D + (up ? D : 0))[part] =
+        make_uint4(e4m3_unordered(r.x), e4m3_unordered(r.y), e4m3_unordered(r.z), e4m3_unordered(r.w));
   }
 }
 
 template <int D, int P>
 cudaError_t launch(const CacheEvictParams& p, cudaStream_t st) {
-  cache_keep_kernel<<<dim3((unsigned)p.c.Hkv, (unsigned)p.c.B), NT1, 0, st>>>(p);
+  const long long cap = (long long)p.c.max_pages * p.c.page;
+  const dim3 rows((unsigned)p.c.Hkv, (unsigned)p.c.B);
+  if (cap <= 8 * NT1) cache_keep_kernel<8, true><<<rows, NT1, 0, st>>>(p);
+  else if (cap <= 32 * NT1) cache_keep_kernel<32, true><<<rows, NT1, 0, st>>>(p);
+  else cache_keep_kernel<8, false><<<rows, NT1, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.budget + P - 1) / P), (unsigned)(2 * p.c.Hkv), (unsigned)p.c.B);
-  cache_copy_kernel<D, P><<<grid, NT2, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.budget + P - 1) / P), (unsigned)p.c.Hkv, (unsigned)p.c.B);
+  cfg.blockDim = dim3(NT2);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_copy_kernel<D, P>, p);
 }
 
 }  // namespace

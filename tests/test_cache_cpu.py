@@ -105,10 +105,10 @@ def test_refusals_of_each_call(fa):
     assert c["fwd"](good, T=0, q=None, o=None, ws=None) == OK
     assert c["select"](good, n_sel=0) == INVALID
     assert c["select"](good, out=None) == INVALID
-    assert c["select"](good, wb=1 * 2 * 2 * 3 * 8 - 1) == WS
-    assert c["select"](good, ws=None) == WS
+    assert c["select"](good, mp=16385, wb=1 * 2 * 2 * 16385 * 8 - 1) == WS
+    assert c["select"](good, mp=16385, ws=None) == WS
+    assert c["select"](good, mp=16385, ws=odd4) == ALIGN
     assert c["select"](cache(fa, page=16), mp=(1 << 18) + 1) == UNSUP
-    assert c["select"](good, T=40000) == UNSUP
     assert c["weigh"](good, lse=None) == INVALID
     assert c["weigh"](good, w=None) == INVALID
     assert c["weigh"](good, out=ODD) == ALIGN
@@ -131,7 +131,8 @@ def test_workspace_sizes(fa):
     assert f(65535, 64, 64, 1, 128, 128, 1 << 20, 0) == 0 and f(1, 8, 2, 1, 128, 64, 2, 1 << 25) == 0
     # bounded by the grid, whatever the batch
     assert f(512, 64, 8, 1, 128, 64, 4096, 0) == f(64, 64, 8, 1, 128, 64, 4096, 0) < (8 << 20)
-    assert fa.cache_select_workspace_bytes(2, 3, 4, 5) == 2 * 3 * 4 * 5 * 8
+    assert fa.cache_select_workspace_bytes(2, 3, 4, 16384) == 0
+    assert fa.cache_select_workspace_bytes(2, 3, 4, 16385) == 2 * 3 * 4 * 16385 * 8
 
 
 def test_binding_refuses_cpu_tensors(fa):

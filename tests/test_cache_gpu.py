@@ -337,7 +337,7 @@ def test_select_and_sparse_fwd(d, page, H, G, T, n_sel):
     fa.sync_status()
 
 
-@pytest.mark.parametrize("n_pages,n_sel", [(40, 9), (600, 300), (2000, 64)])
+@pytest.mark.parametrize("n_pages,n_sel", [(40, 9), (600, 300), (2000, 64), (16390, 5000)])
 def test_select_ties(n_pages, n_sel):
     """Equal pages tie to the lowest; hundreds of them are all undecided in
     FP32."""
@@ -417,11 +417,12 @@ def test_weigh(d, page, H, G, T, causal):
 # ------------------------------------------------------------------ eviction
 @pytest.mark.parametrize("d,page,budget,recent", [(64, 16, 40, 8), (128, 64, 64, 0), (128, 128, 130, 130), (64, 32, 1, 0),
                                                   (64, 32, 1, 1), (128, 16, 299, 17), (128, 64, 400, 5)])
-def test_evict(d, page, budget, recent):
+@pytest.mark.parametrize("room", [0, 9000, 33000])
+def test_evict(d, page, budget, recent, room):
     fa = require_gpu()
     H = 2
     lens = [0, 1, budget, budget + 1, 300, 2500]
-    cache, table, ln = R.make(fa, lens, H, d, page, seed=20, spare=len(lens) * (-(-budget // page) + 1))
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=20, spare=len(lens) * (-(-budget // page) + 1), room=room)
     # pages of very different scales meet in one destination page
     g = torch.Generator().manual_seed(21)
     x = torch.randn(1, H, 2500, d, generator=g) * 2.0 ** torch.randint(-12, 12, (1, 1, 2500, 1), generator=g).float()
