@@ -10,14 +10,18 @@
 // bounds, ties to the lowest page.
 //
 // The result is a set of whole numbers, so it has to be the right one.  One CTA
-// per (sequence, kv head, token) sums in FP32 and keeps, per page, the sum and a
-// bound of its rounding error (2 d + 1 bytes read a page); finds the cut among
-// the lower and the upper ends of these intervals by radix selection; and
-// evaluates only the pages that the intervals leave undecided in 64 bits:
-// usually one or two.  The intervals stay in shared memory (in the workspace
-// where there are more than 16384 pages), so one launch does it all: the same
-// work as two kernels, a wide one for the sums and one CTA a row for the cut,
-// took 22 us on 64 rows of 512 pages, against 9 us.
+// per (sequence, kv head, token) first takes the bounds as FP32 sums and keeps,
+// per page, the sum and a limit of its error (2 d + 1 bytes read a page); cuts
+// the sums at the last one to take, by radix selection; and evaluates only the
+// pages that the error leaves undecided in 64 bits: usually one or two.
+//
+// The sums are m16n8k16 products with 16 pages as rows, their codes as f16
+// (exact) and the coefficients as two f16 columns, hi + 2^-11 lo: a tenth of the
+// instructions of plain FP32 sums, which made this the longer part of the
+// kernel (6.7 of 12.5 us on 64 rows of 448 pages).
+//
+// The intervals stay in shared memory (in the workspace where there are more
+// than 16384 pages).
 #include "cache.cuh"
 
 namespace fa4 {
@@ -31,16 +35,10 @@ FA4_DEV uint32_t key32(float x) {
   const uint32_t u = __float_as_uint(x);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+FA4_DEV float key32_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
 FA4_DEV unsigned long long key64(double x) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(x);
   return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
-}
-
-// The ends of a page's interval as keys; what is not finite is undecided.
-FA4_DEV void ends(const float2 v, uint32_t& lo, uint32_t& hi) {
-  if (!(fabsf(v.x) <= 3.0e38f) || !(v.y <= 3.0e38f)) { lo = 0; hi = 0xffffffffu; return; }
-  lo = key32(__fsub_rd(v.x, v.y));
-  hi = key32(__fadd_ru(v.x, v.y));
 }
 
 constexpr int MAX_BORDER = 256;
@@ -76,15 +74,16 @@ FA4_DEV void find_bin(const unsigned* hist, unsigned& rank, unsigned& bin) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant__ CacheSelectParams p) {
-  constexpr int LN = D / 8;                        // lanes of a page: 16 bounds each
+__global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_constant__ CacheSelectParams p) {
   extern __shared__ __align__(16) uint32_t s_dyn[];
-  __shared__ unsigned s_hist[2][256];
-  __shared__ unsigned s_pre[2], s_rank[2];
+  constexpr int STEPS = D / 8;                     // of 16 bounds each: lo [D], then hi [D]
+  __shared__ unsigned s_hist[256];
+  __shared__ unsigned s_pre, s_rank, s_err;
   __shared__ double s_up[D], s_dn[D], s_score[MAX_BORDER];
-  __shared__ __align__(16) float s_w[2][D];        // dn against lo, up against hi
+  __shared__ __align__(16) float s_w[2 * D];       // dn against lo, up against hi
+  __shared__ __align__(16) uint32_t s_b[2][D];
   __shared__ int s_page[MAX_BORDER];
-  __shared__ int s_in, s_border, s_warp[NT / 32];
+  __shared__ int s_in, s_border;
   const CacheView& c = p.c;
   const int h = blockIdx.x / p.T % c.Hkv, t = blockIdx.x % p.T, b = blockIdx.x / (p.T * c.Hkv);
   int* out = p.out + (long long)blockIdx.x * p.n_sel;
@@ -99,13 +98,14 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
   const int m = n - 1;                             // pages to rank
   const unsigned k = p.n_sel - 1;                  // of which to take; k < m
   const int words = (n + 31) / 32;
-  // [words] pages taken, then (in shared memory or the workspace) the intervals
+  // pages taken by words of 32, their prefix counts, then (here or in the
+  // workspace) the sums with their errors
   uint32_t* s_bits = s_dyn;
   const int bit_words = (c.max_pages + 31) / 32;
-  float2* score = c.max_pages <= SMEM_PAGES ? reinterpret_cast<float2*>(s_dyn + (bit_words + 3) / 4 * 4)
+  float2* score = c.max_pages <= SMEM_PAGES ? reinterpret_cast<float2*>(s_dyn + (bit_words + 1) / 2 * 4)
                                             : p.score + (long long)blockIdx.x * c.max_pages;
   for (int i = threadIdx.x; i < words; i += NT) s_bits[i] = 0;
-  if (threadIdx.x == 0) { s_in = 0; s_border = 0; s_pre[0] = s_pre[1] = 0; s_rank[0] = k; s_rank[1] = k + 1; }
+  if (threadIdx.x == 0) { s_in = 0; s_border = 0; s_pre = 0; s_rank = k; s_err = 0; }
   const int G = p.Hq / c.Hkv;
   if (threadIdx.x < D) {
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
@@ -122,103 +122,142 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
     }
     s_up[threadIdx.x] = up;
     s_dn[threadIdx.x] = dn;
-    s_w[0][threadIdx.x] = fd;
-    s_w[1][threadIdx.x] = fu;
+    s_w[threadIdx.x] = fd;
+    s_w[D + threadIdx.x] = fu;
   }
   __syncthreads();
   if (k > 0) {
-    // lanes 0 .. LN / 2 - 1 of a page hold lo [D], the others hi [D]
-    const int ln = threadIdx.x % LN;
-    float w[16];
+    const int g = lane / 4, t4 = lane % 4;
+    // the coefficients' largest magnitude and their sum of magnitudes
+    uint32_t top = 0;
+    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 x = *reinterpret_cast<const float4*>(&s_w[ln / (LN / 2)][ln % (LN / 2) * 16 + 4 * j]);
-      w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
+    for (int i = 0; i < 2 * D / 32; ++i) {
+      const float x = fabsf(s_w[lane + 32 * i]);
+      top = max(top, __float_as_uint(x));
+      sum += x;
     }
-    // At most G - 1 roundings of a coefficient, 17 of the products and sums and
-    // 4 across the lanes, each 2^-24 of the sum of magnitudes (doubled for the
-    // second-order terms and the magnitudes' own rounding), and 2 D underflows.
-    const float rel = (float)(G + 24) * 0x1p-23f;
-    constexpr int PER = NT / LN;                   // pages at once
-    constexpr int ITER = 8;
-    for (int first = 0; first < m; first += PER * ITER) {
-      uint4 x[ITER];
-      uint32_t sc[ITER];
-      int pg[ITER];
+    top = __reduce_max_sync(0xffffffffu, top);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int pi = first + threadIdx.x / LN + i * PER;
-        pg[i] = pi < m ? cache_page(c, c.table, b, pi) : -1;
+    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int E = (int)(top >> 23);
+    const int e2 = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
+    // columns 0 and 1 of the B operand: hi and 2^11 lo, two coefficients a thread
+    if (threadIdx.x < D) {
+      const float2 w = *reinterpret_cast<const float2*>(&s_w[2 * threadIdx.x]);
+      const float down = exp2i(-e2);
+      const uint32_t hi = pack_f16x2(w.x * down, w.y * down);
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      s_b[0][threadIdx.x] = hi;
+      s_b[1][threadIdx.x] = pack_f16x2((w.x * down - y.x) * 2048.f, (w.y * down - y.y) * 2048.f);
+    }
+    __syncthreads();
+    // the sum over the bounds runs in the order in which 16-byte words fall to
+    // the lanes
+    uint2 wb[STEPS];
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) {
+      wb[x] = make_uint2(0, 0);
+      if (g < 2) wb[x] = *reinterpret_cast<const uint2*>(&s_b[g][32 * (x / 4) + 8 * t4 + 2 * (x % 4)]);
+    }
+    // Error: a coefficient is off by G - 1 roundings and 2^-22 (and 2^-35 of the
+    // largest, below 2^-36 of the sum per term); the products are exact and
+    // 2 D of them are added with 2^-23 of the sum of magnitudes each, whatever
+    // their order; doubled.  The sum of magnitudes is at most the largest code
+    // times the coefficients'.
+    const float rel = (float)(G + 2 * D + 16) * 0x1p-22f;
+    int pages[2];
+    auto look = [&](int first) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int pi = first + g + 8 * r;
+        pages[r] = pi < m ? cache_page(c, c.table, b, pi) : -1;
+      }
+    };
+    look(16 * warp);
+    for (int first = 16 * warp; first < m; first += 16 * (NT / 32)) {
+      long long ph[2];
+      uint4 x[2][D / 32];
+      uint32_t sc[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) ph[r] = pages[r] >= 0 ? (long long)pages[r] * c.Hkv + h : -1;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        sc[r] = ph[r] >= 0 ? __ldg(c.ks + ph[r]) : 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          x[r][i] = ph[r] >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.kb + ph[r] * 2 * D + 64 * i + 16 * t4))
+                               : make_uint4(0, 0, 0, 0);
+      }
+      look(first + 16 * (NT / 32));
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t big[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t u[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
+        const uint32_t v[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          mma_16816(w % 2 ? acc2 : acc, e4m3x2_to_f16x2(u[w]), e4m3x2_to_f16x2(v[w]), e4m3x2_hi_to_f16x2(u[w]),
+                    e4m3x2_hi_to_f16x2(v[w]), wb[4 * i + w].x, wb[4 * i + w].y);
+          big[0] = __vmaxu4(big[0], u[w] & 0x7f7f7f7fu);
+          big[1] = __vmaxu4(big[1], v[w] & 0x7f7f7f7fu);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        sc[i] = 0;
-        if (pg[i] >= 0) {
-          const long long ph = (long long)pg[i] * c.Hkv + h;
-          x[i] = __ldg(reinterpret_cast<const uint4*>(c.kb + ph * 2 * D + 16 * ln));
-          sc[i] = __ldg(c.ks + ph);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float s = 0.f, a = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t y[2] = {e4m3x2_to_f16x2(u[j]), e4m3x2_hi_to_f16x2(u[j])};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-            s = fmaf(v.x, w[4 * j + 2 * e], s);
-            s = fmaf(v.y, w[4 * j + 2 * e + 1], s);
-            a = fmaf(fabsf(v.x), fabsf(w[4 * j + 2 * e]), a);
-            a = fmaf(fabsf(v.y), fabsf(w[4 * j + 2 * e + 1]), a);
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < LN; o *= 2) {
-          s += __shfl_xor_sync(0xffffffffu, s, o);
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-        }
-        const int pi = first + threadIdx.x / LN + i * PER;
-        if (ln == 0 && pi < m) {
-          const float f = e8m0_value(sc[i]);
-          score[pi] = make_float2(s * f, __fmul_ru(__fmaf_ru(a, rel, 0x1p-140f), f));
+      for (int r = 0; r < 2; ++r) {
+        uint32_t z = __vmaxu4(big[r], __shfl_xor_sync(0xffffffffu, big[r], 1));
+        z = __vmaxu4(z, __shfl_xor_sync(0xffffffffu, z, 2));
+        z = __vmaxu4(z, z >> 16);
+        z = max(z & 0xffu, (z >> 8) & 0xffu);
+        const int pi = first + g + 8 * r;
+        if (t4 == 0 && pi < m) {
+          const float f = e8m0_value(sc[r]);
+          const float err = __fmul_ru(__fmaf_ru(__fmul_ru(e4m3_value(z), sum), rel, 0x1p-120f), f);
+          score[pi] = make_float2(
+              fmaf(acc[2 * r + 1] + acc2[2 * r + 1], 0x1p-11f, acc[2 * r] + acc2[2 * r]) * exp2i(e2) * f, err);
+          atomicMax(&s_err, __float_as_uint(err));
         }
       }
     }
     __syncthreads();
-    // the k-th largest lower end and the (k + 1)-th largest upper end
+    // the k-th largest sum
     for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 512; i += NT) (&s_hist[0][0])[i] = 0;
+      if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
       __syncthreads();
-      const unsigned p0 = s_pre[0], p1 = s_pre[1];
+      const unsigned pre = s_pre;
       const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
       for (int i = threadIdx.x; i < m; i += NT) {
-        uint32_t lo, hi;
-        ends(score[i], lo, hi);
-        if ((lo & mask) == p0) atomicAdd(&s_hist[0][(lo >> shift) & 255u], 1u);
-        if ((hi & mask) == p1) atomicAdd(&s_hist[1][(hi >> shift) & 255u], 1u);
+        const uint32_t key = key32(score[i].x);
+        if ((key & mask) == pre) atomicAdd(&s_hist[(key >> shift) & 255u], 1u);
       }
       __syncthreads();
-      if (warp < 2) {
-        unsigned rank = s_rank[warp], bin;
-        find_bin(s_hist[warp], rank, bin);
-        if (lane == 0) { s_rank[warp] = rank; s_pre[warp] |= bin << shift; }
+      if (warp == 0) {
+        unsigned rank = s_rank, bin;
+        find_bin(s_hist, rank, bin);
+        if (lane == 0) { s_rank = rank; s_pre |= bin << shift; }
       }
       __syncthreads();
     }
-    const uint32_t cut_lo = s_pre[0], cut_hi = s_pre[1];
-    // certainly in: the lower end above the (k + 1)-th largest upper end;
-    // certainly out: the upper end below the k-th largest lower end
+    // With err the largest error: k pages have a bound of at least cut - err, so
+    // a page is certainly out whose own is surely below; and at most k have one
+    // above cut + err (the others' sums are at most cut), so a page is certainly
+    // in whose own surely is.  Sums that are not finite decide nothing.
+    const float cut = key32_value(s_pre), err = __uint_as_float(s_err);
+    const float above = __fadd_ru(cut, err), below = __fsub_rd(cut, err);
+    const bool sane = fabsf(above) <= 3.0e38f && fabsf(below) <= 3.0e38f;
+    auto state = [&](int i) -> int {               // 1 in, -1 out, 0 undecided
+      const float2 v = score[i];
+      if (!sane || !(fabsf(v.x) <= 3.0e38f)) return 0;
+      if (__fsub_rd(v.x, v.y) > above) return 1;
+      return __fadd_ru(v.x, v.y) < below ? -1 : 0;
+    };
     for (int i = threadIdx.x; i < m; i += NT) {
-      uint32_t lo, hi;
-      ends(score[i], lo, hi);
-      if (lo > cut_hi) {
+      const int z = state(i);
+      if (z > 0) {
         atomicOr(&s_bits[i / 32], 1u << (i % 32));
         atomicAdd(&s_in, 1);
-      } else if (hi >= cut_lo) {
+      } else if (z == 0) {
         const int at = atomicAdd(&s_border, 1);
         if (at < MAX_BORDER) s_page[at] = i;
       }
@@ -241,11 +280,8 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
       return s == 0. ? 0. : s;
     };
     if (nb == need) {
-      for (int i = threadIdx.x; i < m; i += NT) {
-        uint32_t lo, hi;
-        ends(score[i], lo, hi);
-        if (!(lo > cut_hi) && hi >= cut_lo) atomicOr(&s_bits[i / 32], 1u << (i % 32));
-      }
+      for (int i = threadIdx.x; i < m; i += NT)
+        if (state(i) == 0) atomicOr(&s_bits[i / 32], 1u << (i % 32));
     } else if (nb <= MAX_BORDER) {
       for (int j = warp; j < nb; j += NT / 32) {
         const double s = exact(s_page[j]);
@@ -266,37 +302,35 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
       // of the FP32 pairs, and the need-th largest is found byte by byte
       double* wide = reinterpret_cast<double*>(score);
       for (int i = warp; i < m; i += NT / 32) {
-        uint32_t lo, hi;
-        ends(score[i], lo, hi);
-        const bool border = !(lo > cut_hi) && hi >= cut_lo;
+        const bool border = state(i) == 0;
         const double s = border ? exact(i) : 0.;
         __syncwarp();
         // what is decided already is kept apart by a NaN
         if (lane == 0) wide[i] = border && s == s ? s : __longlong_as_double(-1ll);
       }
       __syncthreads();
-      if (threadIdx.x == 0) s_rank[0] = need;
+      if (threadIdx.x == 0) s_rank = need;
       unsigned long long pre = 0;
       for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += NT) s_hist[0][i] = 0;
+        for (int i = threadIdx.x; i < 256; i += NT) s_hist[i] = 0;
         __syncthreads();
         const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8);
         for (int i = threadIdx.x; i < m; i += NT) {
           const double v = wide[i];
           const unsigned long long key = key64(v);
-          if (v == v && (key & mask) == pre) atomicAdd(&s_hist[0][(unsigned)(key >> shift) & 255u], 1u);
+          if (v == v && (key & mask) == pre) atomicAdd(&s_hist[(unsigned)(key >> shift) & 255u], 1u);
         }
         __syncthreads();
         if (warp == 0) {
-          unsigned rank = s_rank[0], bin;
-          find_bin(s_hist[0], rank, bin);
-          if (lane == 0) { s_rank[0] = rank; s_pre[0] = bin; }
+          unsigned rank = s_rank, bin;
+          find_bin(s_hist, rank, bin);
+          if (lane == 0) { s_rank = rank; s_pre = bin; }
         }
         __syncthreads();
-        pre |= (unsigned long long)s_pre[0] << shift;
+        pre |= (unsigned long long)s_pre << shift;
       }
-      // all above the cut, and of those on it the first s_rank[0]
-      const int ties = (int)s_rank[0];
+      // all above the cut, and of those on it the first s_rank
+      const int ties = (int)s_rank;
       for (int i = threadIdx.x; i < m; i += NT)
         if (wide[i] == wide[i] && key64(wide[i]) > pre) atomicOr(&s_bits[i / 32], 1u << (i % 32));
       __syncthreads();
@@ -317,41 +351,36 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
   __syncthreads();
   if (threadIdx.x == 0) s_bits[m / 32] |= 1u << (m % 32);   // the query's own page
   __syncthreads();
-  // the taken pages in ascending order
-  int done = 0;
-  for (int base = 0; base < words; base += NT) {
-    const int i = base + threadIdx.x;
-    uint32_t bits = i < words ? s_bits[i] : 0u;
-    const int cnt = __popc(bits);
-    int inc = cnt;
+  // the taken pages in ascending order: words' prefix, then a page a thread
+  int* s_before = reinterpret_cast<int*>(s_bits + bit_words);
+  if (warp == 0) {
+    int done = 0;
+    for (int base = 0; base < words; base += 32) {
+      const int cnt = base + lane < words ? __popc(s_bits[base + lane]) : 0;
+      int inc = cnt;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
+      for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (base + lane < words) s_before[base + lane] = done + inc - cnt;
+      done += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    int at = done + inc - cnt;
-    int all = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) at += s_warp[w];
-      all += s_warp[w];
-    }
-    while (bits) {
-      if (at < p.n_sel) out[at] = 32 * i + __ffs(bits) - 1;
-      ++at;
-      bits &= bits - 1;
-    }
-    done += all;
-    __syncthreads();
+    if (lane == 0) s_in = done;
   }
-  for (int i = done + threadIdx.x; i < p.n_sel; i += NT) out[i] = -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint32_t bits = s_bits[i / 32];
+    const int at = s_before[i / 32] + __popc(bits & ((1u << (i % 32)) - 1u));
+    if (((bits >> (i % 32)) & 1u) && at < p.n_sel) out[at] = i;
+  }
+  for (int i = s_in + threadIdx.x; i < p.n_sel; i += NT) out[i] = -1;
 }
 
 template <int D>
 cudaError_t launch(const CacheSelectParams& p, cudaStream_t st) {
   const int bit_words = (p.c.max_pages + 31) / 32;
-  size_t smem = (size_t)(bit_words + 3) / 4 * 16;
+  size_t smem = (size_t)(bit_words + 1) / 2 * 16;
   if (p.c.max_pages <= SMEM_PAGES) smem += (size_t)p.c.max_pages * 8;
   if (smem > 32 * 1024) {
     const cudaError_t e =
