@@ -32,12 +32,6 @@ class Fa4Fp4Error(RuntimeError):
 _lib = None
 
 
-class _CacheStruct(ctypes.Structure):
-    """fa4fp4_cache of include/fa4fp4.h."""
-    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "k_bounds")] + \
-               [(n, ctypes.c_int) for n in ("num_pages", "Hkv", "page", "d")]
-
-
 def library_path() -> str:
     return _LIB_PATH
 
@@ -82,21 +76,10 @@ def load_library():
         lib.fa4bf16_fwd.argtypes = [vp, vp, vp, i, i, i, i, i, f, i, vp, i, vp, vp]
         lib.fa4fp4_directp_codes.restype = i
         lib.fa4fp4_directp_codes.argtypes = [vp, ctypes.c_int64, f, f, i, vp, vp]
-        cp = ctypes.POINTER(_CacheStruct)
-        lib.fa4fp4_cache_append.restype = i
-        lib.fa4fp4_cache_append.argtypes = [cp] + [vp] * 5 + [i, i, i, vp]
         lib.fa4fp4_cache_fwd_workspace_bytes.restype = sz
         lib.fa4fp4_cache_fwd_workspace_bytes.argtypes = [i] * 8
-        lib.fa4fp4_cache_fwd.restype = i
-        lib.fa4fp4_cache_fwd.argtypes = [cp] + [vp] * 5 + [i] * 5 + [f, i, vp, i, vp, vp, sz, vp]
         lib.fa4fp4_cache_select_workspace_bytes.restype = sz
         lib.fa4fp4_cache_select_workspace_bytes.argtypes = [i] * 4
-        lib.fa4fp4_cache_select.restype = i
-        lib.fa4fp4_cache_select.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp, vp, sz, vp]
-        lib.fa4fp4_cache_weigh.restype = i
-        lib.fa4fp4_cache_weigh.argtypes = [cp] + [vp] * 5 + [i] * 4 + [f, i, vp, vp, vp]
-        lib.fa4fp4_cache_evict.restype = i
-        lib.fa4fp4_cache_evict.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp] * 4
         lib.fa4fp4_sync_status.restype = i
         lib.fa4fp4_sync_status.argtypes = [vp]
         _lib = lib
@@ -571,234 +554,41 @@ def bwd_noalloc(q4: QTensor, k4: QTensor, q8c: QTensor, k8c: QTensor, v8r: QTens
 
 
 # ----------------------------------------------------------------------------
-# the 8-bit key/value cache
+# the 8-bit key/value cache: the calls are in the native module _cache_binding
+# (csrc/cache_binding.cpp), loaded by the first use of one of its names
 # ----------------------------------------------------------------------------
-class KVCache:
-    """A paged pool of K and V as E4M3 codes with one E8M0 scale per page and
-    head (fa4fp4_cache of include/fa4fp4.h): uint8 CUDA tensors k, v
-    [num_pages, Hkv, page, d], ks, vs [num_pages, Hkv] and kb
-    [num_pages, Hkv, 2, d] (K bounds).  cache_alloc makes an empty one."""
-
-    def __init__(self, k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor, vs: torch.Tensor, kb: torch.Tensor):
-        if k.dim() != 4:
-            raise ValueError("k: expected [num_pages, Hkv, page, d]")
-        n, H, page, d = k.shape
-        u8 = torch.uint8
-        for name, t, shape in (("k", k, (n, H, page, d)), ("v", v, (n, H, page, d)), ("ks", ks, (n, H)),
-                               ("vs", vs, (n, H)), ("kb", kb, (n, H, 2, d))):
-            if t.shape != shape or t.dtype != u8:
-                raise ValueError(f"{name}: expected shape {shape} and dtype torch.uint8, got {tuple(t.shape)} {t.dtype}")
-            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
-                raise ValueError("fa4fp4: a cache's tensors must be contiguous CUDA tensors of one device")
-        self.k, self.v, self.ks, self.vs, self.kb = k, v, ks, vs, kb
-        self.num_pages, self.Hkv, self.page, self.d = n, H, page, d
-        self.device = k.device
-        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kb.data_ptr(),
-                                    n, H, page, d)
+_CACHE_NAMES = ("KVCache", "cache_append", "cache_fwd", "cache_select", "cache_weigh", "cache_evict")
 
 
-def cache_alloc(num_pages: int, Hkv: int, d: int, page: int = 64, device="cuda") -> KVCache:
-    """An empty cache of num_pages pages of `page` tokens."""
+def __getattr__(name):
+    if name not in _CACHE_NAMES:
+        raise AttributeError(name)
+    import importlib.machinery
+    import importlib.util
+    load_library()
+    path = os.path.join(HERE, "_cache_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"native binding not built: {path} (run __graft_entry__.build())")
+    loader = importlib.machinery.ExtensionFileLoader("_cache_binding", path)
+    binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache_binding", loader))
+    loader.exec_module(binding)
+    binding.set_error(Fa4Fp4Error)
+    for n in _CACHE_NAMES:
+        globals()[n] = getattr(binding, n)
+    return globals()[name]
+
+
+def cache_alloc(num_pages: int, Hkv: int, d: int, page: int = 64, device="cuda"):
+    """An empty KVCache of num_pages pages of `page` tokens."""
     z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=device)
-    return KVCache(z(num_pages, Hkv, page, d), z(num_pages, Hkv, page, d), z(num_pages, Hkv), z(num_pages, Hkv),
-                   z(num_pages, Hkv, 2, d))
-
-
-class _on:
-    """The device of the cache as the current one during a call."""
-
-    def __init__(self, device):
-        self.device = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.before != self.device:
-            torch.cuda.set_device(self.before)
-
-
-def _expect_sequences(cache, page_table, lens, counts, counts_name):
-    """Checks what every cache call is given; returns (B, max_pages)."""
-    if not isinstance(cache, KVCache):
-        raise ValueError("cache: expected a KVCache")
-    if page_table.dim() != 2:
-        raise ValueError("page_table: expected [B, max_pages]")
-    B, max_pages = page_table.shape
-    i32 = torch.int32
-    for name, t, shape in (("page_table", page_table, (B, max_pages)), ("lens", lens, (B,)), (counts_name, counts, (B,))):
-        if t is None and name == counts_name:
-            continue
-        if t.shape != shape or t.dtype != i32 or not t.is_cuda or not t.is_contiguous() or t.device != cache.device:
-            raise ValueError(f"{name}: expected a contiguous int32 tensor {shape} on the cache's device")
-    return B, max_pages
-
-
-def _expect_on(cache, name, t, shape, dtype):
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.device != cache.device:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {shape} on the cache's device, "
-                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-
-
-def _expect_queries(cache, q, B):
-    if q.dim() != 4:
-        raise ValueError("q: expected [B, Hq, T, d]")
-    _, Hq, T, _ = q.shape
-    _expect_on(cache, "q", q, (B, Hq, T, cache.d), torch.bfloat16)
-    return Hq, T
-
-
-def _cache_workspace(cache, workspace, need):
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
-    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() \
-            or workspace.device != cache.device:
-        raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
-    return workspace
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(device):
-    # the handle alone: a torch.cuda.Stream object costs more than the launch
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
-                 n_new: torch.Tensor | None = None) -> None:
-    """Store new tokens k, v (bf16 [B, Hkv, T, d]) behind the lens[b] tokens of
-    every sequence (fa4fp4_cache_append): n_new[b] of them, or all T.  lens is
-    not changed."""
-    B, max_pages = _expect_sequences(cache, page_table, lens, n_new, "n_new")
-    if k.dim() != 4:
-        raise ValueError("k: expected [B, Hkv, T, d]")
-    shape = (B, cache.Hkv, k.shape[2], cache.d)
-    _expect_on(cache, "k", k, shape, torch.bfloat16)
-    _expect_on(cache, "v", v, shape, torch.bfloat16)
-    with _on(cache.device):
-        _check("fa4fp4_cache_append", load_library().fa4fp4_cache_append(
-            cache._struct, _at(k), _at(v), _at(page_table), _at(lens), _at(n_new), B, max_pages, k.shape[2],
-            _raw_stream(cache.device)))
+    new = globals().get("KVCache") or __getattr__("KVCache")
+    return new(z(num_pages, Hkv, page, d), z(num_pages, Hkv, page, d), z(num_pages, Hkv), z(num_pages, Hkv),
+               z(num_pages, Hkv, 2, d))
 
 
 def cache_fwd_workspace_bytes(B, Hq, Hkv, T, d, page, max_pages, n_sel=0) -> int:
     return int(load_library().fa4fp4_cache_fwd_workspace_bytes(B, Hq, Hkv, T, d, page, max_pages, n_sel))
 
 
-def cache_fwd(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor,
-              q_lens: torch.Tensor | None = None, causal: bool = True, softmax_scale: float = 0.0,
-              out_dtype: int = OUT_BF16, with_lse: bool = True, out=None, lse=None,
-              pages: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
-    """Attention of the T newest tokens of every sequence, q bf16 [B, Hq, T, d],
-    over the cache (fa4fp4_cache_fwd); lens counts them in.  pages (from
-    cache_select) restricts every token to its own pages.  Rows t >= q_lens[b]
-    of out and lse are not written.  Returns (o, lse or None)."""
-    B, max_pages = _expect_sequences(cache, page_table, lens, q_lens, "q_lens")
-    Hq, T = _expect_queries(cache, q, B)
-    if out_dtype not in (OUT_F32, OUT_BF16):
-        raise ValueError("out_dtype must be OUT_F32 or OUT_BF16")
-    dtype = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
-    dev = cache.device
-    # rows that the call does not write hold zeros, not what the allocator left
-    new = torch.empty if q_lens is None else torch.zeros
-    if out is None:
-        out = new((B, Hq, T, cache.d), dtype=dtype, device=dev)
-    else:
-        _expect_on(cache, "out", out, (B, Hq, T, cache.d), dtype)
-    if not with_lse:
-        lse = None
-    elif lse is None:
-        lse = new((B, Hq, T), dtype=torch.float32, device=dev)
-    else:
-        _expect_on(cache, "lse", lse, (B, Hq, T), torch.float32)
-    n_sel = 0
-    if pages is not None:
-        n_sel = pages.shape[-1]
-        _expect_on(cache, "pages", pages, (B, cache.Hkv, T, n_sel), torch.int32)
-    lib = load_library()
-    with _on(dev):
-        ws = _cache_workspace(cache, workspace, 0 if workspace is not None else lib.fa4fp4_cache_fwd_workspace_bytes(
-            B, Hq, cache.Hkv, T, cache.d, cache.page, max_pages, n_sel))
-        _check("fa4fp4_cache_fwd", lib.fa4fp4_cache_fwd(
-            cache._struct, _at(q), _at(page_table), _at(lens), _at(q_lens), _at(pages), B, Hq, T, max_pages, n_sel,
-            softmax_scale, 1 if causal else 0, _at(out), out_dtype, _at(lse), _at(ws), ws.numel(), _raw_stream(dev)))
-    return out, lse
-
-
 def cache_select_workspace_bytes(B, Hkv, T, max_pages) -> int:
     return int(load_library().fa4fp4_cache_select_workspace_bytes(B, Hkv, T, max_pages))
-
-
-def cache_select(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, n_pages: int,
-                 q_lens: torch.Tensor | None = None, out=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """The n_pages pages whose keys could score highest for every query token
-    and kv head (fa4fp4_cache_select): int32 [B, Hkv, T, n_pages], ascending
-    indexes into the sequence's row of page_table, then -1."""
-    B, max_pages = _expect_sequences(cache, page_table, lens, q_lens, "q_lens")
-    Hq, T = _expect_queries(cache, q, B)
-    shape = (B, cache.Hkv, T, int(n_pages))
-    if n_pages < 1:
-        raise ValueError("n_pages must be at least 1")
-    if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
-    else:
-        _expect_on(cache, "out", out, shape, torch.int32)
-    lib = load_library()
-    with _on(cache.device):
-        need = lib.fa4fp4_cache_select_workspace_bytes(B, cache.Hkv, T, max_pages)
-        ws = _cache_workspace(cache, workspace, need) if need or workspace is not None else None
-        _check("fa4fp4_cache_select", lib.fa4fp4_cache_select(
-            cache._struct, _at(q), _at(page_table), _at(lens), _at(q_lens), B, Hq, T, max_pages, shape[3], _at(out),
-            _at(ws), ws.numel() if ws is not None else 0, _raw_stream(cache.device)))
-    return out
-
-
-def cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor,
-                weight: torch.Tensor, q_lens: torch.Tensor | None = None, causal: bool = True,
-                softmax_scale: float = 0.0, out: torch.Tensor | None = None) -> torch.Tensor:
-    """weight plus the attention weight that every cached token received from
-    the queries (fa4fp4_cache_weigh), with the lse of cache_fwd: f32
-    [B, Hkv, max_pages * page], written to `out` (default: into weight itself),
-    positions behind a sequence's end untouched."""
-    B, max_pages = _expect_sequences(cache, page_table, lens, q_lens, "q_lens")
-    Hq, T = _expect_queries(cache, q, B)
-    _expect_on(cache, "lse", lse, (B, Hq, T), torch.float32)
-    shape = (B, cache.Hkv, max_pages * cache.page)
-    _expect_on(cache, "weight", weight, shape, torch.float32)
-    if out is None:
-        out = weight
-    else:
-        _expect_on(cache, "out", out, shape, torch.float32)
-    with _on(cache.device):
-        _check("fa4fp4_cache_weigh", load_library().fa4fp4_cache_weigh(
-            cache._struct, _at(q), _at(lse), _at(page_table), _at(lens), _at(q_lens), B, Hq, T, max_pages,
-            softmax_scale, 1 if causal else 0, _at(weight), _at(out), _raw_stream(cache.device)))
-    return out
-
-
-def cache_evict(cache: KVCache, page_table: torch.Tensor, lens: torch.Tensor, weight: torch.Tensor,
-                dst_table: torch.Tensor, budget: int, recent: int = 0):
-    """Cut every sequence back to its `recent` newest and otherwise heaviest
-    tokens, `budget` in all per kv head, copied into the pages of dst_table
-    (int32 [B, dst_pages], fresh pages of the same cache; fa4fp4_cache_evict).
-    Returns (new lens int32 [B], kept positions int32 [B, Hkv, budget] with -1
-    behind, their weights f32 [B, Hkv, dst_pages * page] with 0 behind)."""
-    B, max_pages = _expect_sequences(cache, page_table, lens, None, "lens")
-    H, dev = cache.Hkv, cache.device
-    _expect_on(cache, "weight", weight, (B, H, max_pages * cache.page), torch.float32)
-    if dst_table.dim() != 2:
-        raise ValueError("dst_table: expected [B, dst_pages]")
-    dst_pages = dst_table.shape[1]
-    _expect_on(cache, "dst_table", dst_table, (B, dst_pages), torch.int32)
-    new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    kept = torch.empty((B, H, max(int(budget), 0)), dtype=torch.int32, device=dev)
-    w_out = torch.empty((B, H, dst_pages * cache.page), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check("fa4fp4_cache_evict", load_library().fa4fp4_cache_evict(
-            cache._struct, _at(page_table), _at(lens), _at(weight), _at(dst_table), B, max_pages, dst_pages,
-            int(budget), int(recent), _at(new_lens), _at(kept), _at(w_out), _raw_stream(dev)))
-    return new_lens, kept, w_out

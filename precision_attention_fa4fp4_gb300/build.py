@@ -1,5 +1,7 @@
 """Compile the CUDA library in-tree for sm_103a: every .cu under csrc/ with
-nvcc in parallel, then one shared library ``libfa4fp4.so`` next to this file.
+nvcc in parallel, then one shared library ``libfa4fp4.so`` next to this file, and
+beside it the native Python binding of the cache calls, ``_cache_binding.so``
+(g++, against the installed torch).
 Run ``python -m precision_attention_fa4fp4_gb300.build`` or call ``build()``."""
 from __future__ import annotations
 
@@ -16,9 +18,15 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hid
          "--expt-relaxed-constexpr"]
 
 
+BINDING = os.path.join(HERE, "_cache_binding.so")
+
+
+def _cuda_home() -> str:
+    return os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
 def _nvcc() -> str:
-    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    p = os.path.join(cuda, "bin", "nvcc")
+    p = os.path.join(_cuda_home(), "bin", "nvcc")
     return p if os.path.exists(p) else "nvcc"
 
 
@@ -33,6 +41,29 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_commands(force: bool, header: str) -> tuple[list[str] | None, list[str] | None, str]:
+    """The binding's compile and link commands where they are needed, and the
+    torch version it is built against."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "cache_binding.cpp")
+    obj = os.path.join(OUT_DIR, "cache_binding.o")
+    stamp = os.path.join(OUT_DIR, "cache_binding.torch")
+    root = os.path.dirname(torch.__file__)
+    built = open(stamp).read() if os.path.exists(stamp) else ""
+    fresh = not force and built == torch.__version__ and not _stale(obj, [src, header])
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(_cuda_home(), "include"), "-c", src, "-o", obj]
+    lib = os.path.join(root, "lib")
+    link = ["g++", "-shared", "-o", BINDING + f".{os.getpid()}.tmp", obj, "-L" + HERE, "-lfa4fp4", "-L" + lib,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    return (None if fresh else compile_), (None if fresh and not _stale(BINDING, [obj]) else link), torch.__version__
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
@@ -45,20 +76,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", src, "-o", obj])
+    compile_binding, link_binding, torch_version = _binding_commands(force, headers[-1])
+    relink = force or bool(jobs)
+    if compile_binding:
+        jobs.insert(0, compile_binding)
     if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+        with cf.ThreadPoolExecutor(max_workers=min(12, len(jobs))) as ex:
             for res in ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs):
                 if res.returncode != 0:
-                    raise RuntimeError("nvcc failed:\n" + " ".join(res.args) + "\n" + res.stderr)
+                    raise RuntimeError("compilation failed:\n" + " ".join(res.args) + "\n" + res.stderr)
                 if verbose and res.stderr:
                     print(res.stderr)
-    if force or jobs or _stale(LIB, objs):
+    if relink or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("link failed:\n" + res.stderr)
         os.replace(tmp, LIB)
+    if link_binding:
+        res = subprocess.run(link_binding, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("link failed:\n" + res.stderr)
+        os.replace(link_binding[3], BINDING)
+        with open(os.path.join(OUT_DIR, "cache_binding.torch"), "w") as f:
+            f.write(torch_version)
     return LIB
 
 

@@ -1,6 +1,7 @@
 """Host-side checks of the 8-bit cache's entry points that need no GPU: what
 they refuse, empty problems, workspace sizes, and the reference's own pins."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -23,13 +24,20 @@ def fa():
 
 
 def cache(fa, ptrs=(4096,) * 5, n=8, H=2, page=64, d=128):
-    return fa._CacheStruct(*ptrs, n, H, page, d)
+    """The C structure, as bytes."""
+    return struct.pack("@5P4i", *(p or 0 for p in ptrs), n, H, page, d)
 
 
 def calls(fa):
     """Every call with good arguments for B = 1, Hq = 4, T = 2, three pages;
     keyword arguments replace one."""
     lib = fa.load_library()
+    cp, vp, i, f, sz = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.fa4fp4_cache_append.argtypes = [cp] + [vp] * 5 + [i, i, i, vp]
+    lib.fa4fp4_cache_fwd.argtypes = [cp] + [vp] * 5 + [i] * 5 + [f, i, vp, i, vp, vp, sz, vp]
+    lib.fa4fp4_cache_select.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp, vp, sz, vp]
+    lib.fa4fp4_cache_weigh.argtypes = [cp] + [vp] * 5 + [i] * 4 + [f, i, vp, vp, vp]
+    lib.fa4fp4_cache_evict.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp] * 4
 
     def append(c, k=P, v=P, table=P, lens=P, n_new=None, B=1, mp=3, T=2):
         return lib.fa4fp4_cache_append(c, k, v, table, lens, n_new, B, mp, T, None)
@@ -141,9 +149,16 @@ def test_binding_refuses_cpu_tensors(fa):
         fa.KVCache(z, z, z[:, :, 0, 0].contiguous(), z[:, :, 0, 0].contiguous(), z[:, :, :2].contiguous())
     with pytest.raises(ValueError):
         fa.KVCache(z[0], z, z, z, z)
+    with pytest.raises(ValueError):
+        fa.KVCache(*[None] * 5)
     t = torch.zeros((1, 4), dtype=torch.int32)
     with pytest.raises(ValueError):
         fa.cache_append(None, z, z, t, t[:, 0])
+    for args, kw in (((), {}), ((None,) * 7, {}), ((None,) * 5, dict(lens=t)), ((None,) * 5, dict(tokens=t))):
+        with pytest.raises(TypeError):
+            fa.cache_append(*args, **kw)
+    with pytest.raises(TypeError):
+        fa.KVCache(z)
 
 
 def test_status_strings(fa):
