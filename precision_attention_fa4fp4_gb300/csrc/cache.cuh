@@ -9,9 +9,18 @@
 
 namespace fa4 {
 
+// Every kernel of the cache may be launched while the one before it in the
+// stream still runs (launch_next below).  It lets its own successor start right
+// away, and waits here, in every thread and before it touches global memory, for
+// everything before it; so the order of the stream holds however many calls
+// follow each other.  What other calls write is read by plain loads: a
+// non-coherent load would need it unchanged from the kernel's start.
+FA4_DEV void grid_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+FA4_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Length of sequence b: a value outside [0, capacity] is flagged and clamped.
 FA4_DEV int cache_len(const CacheView& c, int b) {
-  const int n = __ldg(c.lens + b);
+  const int n = *(c.lens + b);
   const long long cap = (long long)c.max_pages * c.page;
   if (n < 0 || n > cap) {
     atomicOr(c.err, FA4_DEVERR_INDEX);
@@ -23,7 +32,7 @@ FA4_DEV int cache_len(const CacheView& c, int b) {
 // A per-sequence count in [0, most] (nullptr: most), flagged and clamped.
 FA4_DEV int cache_count(const int* n, int b, int most, unsigned* err) {
   if (!n) return most;
-  const int x = __ldg(n + b);
+  const int x = *(n + b);
   if (x < 0 || x > most) {
     atomicOr(err, FA4_DEVERR_INDEX);
     return x < 0 ? 0 : most;
@@ -34,7 +43,7 @@ FA4_DEV int cache_count(const int* n, int b, int most, unsigned* err) {
 // Pool page of a sequence's page lp in [0, max_pages): -1 (flagged) where the
 // table's entry is no page of the pool.
 FA4_DEV int cache_page(const CacheView& c, const int* table, int b, int lp) {
-  const int p = __ldg(table + (long long)b * c.max_pages + lp);
+  const int p = *(table + (long long)b * c.max_pages + lp);
   if (p < 0 || p >= c.num_pages) {
     atomicOr(c.err, FA4_DEVERR_INDEX);
     return -1;
@@ -125,7 +134,7 @@ struct QRaw {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (row) x = __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 16 * t) + i);
+        if (row) x = reinterpret_cast<const uint4*>(row + 64 * c + 16 * t)[i];
         w[4 * c + 2 * i] = make_uint2(x.x, x.y);
         w[4 * c + 2 * i + 1] = make_uint2(x.z, x.w);
       }
@@ -182,6 +191,22 @@ FA4_DEV uint32_t e4m3_times(uint32_t x, float f) {
   const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z));
   return pack_e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
+}
+
+// Launches a kernel that begins with grid_start and grid_wait.
+template <class P>
+cudaError_t launch_next(void (*kernel)(const P), dim3 grid, int threads, size_t smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace fa4

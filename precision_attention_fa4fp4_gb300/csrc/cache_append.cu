@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const __grid_constant_
   constexpr int PARTS = D / 8;                    // 16-byte words of a token
   constexpr int TOK = NT / PARTS;                 // tokens the CTA covers at once
   constexpr int N = (P + TOK - 1) / TOK;          // words a thread holds
+  grid_start();
+  grid_wait();
   const int h = blockIdx.y >> 1, isv = blockIdx.y & 1, b = blockIdx.z;
   const CacheView& c = p.c;
   const int len = cache_len(c, b);
@@ -82,14 +84,14 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const __grid_constant_
   const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(isv ? p.v : p.k) +
                              (((long long)b * c.Hkv + h) * p.T + (first - len)) * D + part * 8;
 
-  const int X_old = s0 > 0 ? (int)__ldg(scale) - 127 : -127;
+  const int X_old = s0 > 0 ? (int)*(scale) - 127 : -127;
   uint4 w[N];
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int s = tok + i * TOK;
     w[i] = make_uint4(0, 0, 0, 0);
-    if (s >= s0 && s < s1) w[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)s * D));
+    if (s >= s0 && s < s1) w[i] = *(reinterpret_cast<const uint4*>(src + (long long)s * D));
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -213,8 +215,7 @@ template <int D, int P>
 cudaError_t launch(const CacheAppendParams& p, cudaStream_t st) {
   // T tokens behind any length touch at most (T + P - 2) / P + 1 pages
   const dim3 grid((unsigned)((p.T + P - 2) / P + 1), (unsigned)(2 * p.c.Hkv), (unsigned)p.c.B);
-  cache_append_kernel<D, P><<<grid, NT, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(cache_append_kernel<D, P>, grid, NT, 0, st, p);
 }
 
 }  // namespace

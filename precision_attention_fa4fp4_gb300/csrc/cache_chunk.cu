@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   using L = SmemC<D>;
   constexpr int STAGES = L::STAGES;
   constexpr uint32_t COL_O0 = L::COL_O0;
+  grid_start();
+  grid_wait();
   const CacheView& c = p.c;
   const int h = blockIdx.y, b = blockIdx.z;
   const int G = p.Hq / c.Hkv;
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         int pg = -1;
         if (lane < 8 && key < len) pg = cache_page(c, c.table, b, lp);
         const long long ph = (long long)max(pg, 0) * c.Hkv + h;
-        const float kx = e8m0_value(__ldg(c.ks + ph));
-        const int ev = (int)__ldg(c.vs + ph) - 127;
+        const float kx = e8m0_value(*(c.ks + ph));
+        const int ev = (int)*(c.vs + ph) - 127;
         Meta& m = metas[j % METAS];
         if (j > 0 && !mbar_wait(k8_empty, (j - 1) & 1, abort_flag, c.err)) break;
         int top = pg >= 0 ? ev : -1000;
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       uint4 w[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        w[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        w[i] = valid ? *(src + i) : make_uint4(0, 0, 0, 0);
         const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) amax = max(amax, max((u[k] << 16) & 0x7fffffffu, u[k] & 0x7fff0000u));
@@ -503,8 +505,7 @@ cudaError_t launch(const CacheFwdParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
   const dim3 grid((unsigned)((rows + 2 * BM - 1) / (2 * BM)), (unsigned)p.c.Hkv, (unsigned)p.c.B);
-  k<<<grid, NTHREADS, SmemC<D>::BYTES, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(k, grid, NTHREADS, SmemC<D>::BYTES, st, p);
 }
 
 }  // namespace

@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
   __shared__ unsigned s_hist[BINS];
   __shared__ unsigned s_bin, s_rank, s_count, s_lo, s_hi, s_few;
   __shared__ int s_cnt[EPT * WARPS1], s_tot[32];
+  grid_start();
+  grid_wait();
   const CacheView& c = p.c;
   const int h = blockIdx.x, b = blockIdx.y;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
       const int i = base + j * NT1 + threadIdx.x;
-      x[j] = i < len ? __ldg(w + i) : 0.f;
+      x[j] = i < len ? *(w + i) : 0.f;
     }
   };
   if (ONCE) load(0);
@@ -251,13 +253,14 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
   constexpr int N = (P + TOK - 1) / TOK;
   __shared__ int s_x[2][NT2 / 32];
   __shared__ uint4 s_lo[NT2 / 32][PARTS], s_hi[NT2 / 32][PARTS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_start();
+  grid_wait();
   const CacheView& c = p.c;
   const int h = blockIdx.y, b = blockIdx.z;
   const int keep = min(cache_len(c, b), p.budget);
   const int first = blockIdx.x * P;
   if (first >= keep) return;
-  const int dst = __ldg(p.dst + (long long)b * p.dst_pages + blockIdx.x);
+  const int dst = *(p.dst + (long long)b * p.dst_pages + blockIdx.x);
   if (dst < 0 || dst >= c.num_pages) {
     if (threadIdx.x == 0) atomicOr(c.err, FA4_DEVERR_INDEX);
     return;
@@ -288,8 +291,8 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
       w[kv][i] = make_uint4(0, 0, 0, 0);
       xs[kv][i] = 0;
       if (row[i] >= 0) {
-        w[kv][i] = __ldg(reinterpret_cast<const uint4*>((kv ? c.v : c.k) + (long long)row[i] * D) + part);
-        xs[kv][i] = (int)__ldg((kv ? c.vs : c.ks) + row[i] / P) - 127;
+        w[kv][i] = *(reinterpret_cast<const uint4*>((kv ? c.v : c.k) + (long long)row[i] * D) + part);
+        xs[kv][i] = (int)*((kv ? c.vs : c.ks) + row[i] / P) - 127;
       }
     }
   int X[2] = {-127, -127};
@@ -370,21 +373,12 @@ template <int D, int P>
 cudaError_t launch(const CacheEvictParams& p, cudaStream_t st) {
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const dim3 rows((unsigned)p.c.Hkv, (unsigned)p.c.B);
-  if (cap <= 8 * NT1) cache_keep_kernel<8, true><<<rows, NT1, 0, st>>>(p);
-  else if (cap <= 32 * NT1) cache_keep_kernel<32, true><<<rows, NT1, 0, st>>>(p);
-  else cache_keep_kernel<8, false><<<rows, NT1, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  auto keep = cap <= 8 * NT1 ? cache_keep_kernel<8, true>
+              : cap <= 32 * NT1 ? cache_keep_kernel<32, true> : cache_keep_kernel<8, false>;
+  const cudaError_t e = launch_next(keep, rows, NT1, 0, st, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.budget + P - 1) / P), (unsigned)p.c.Hkv, (unsigned)p.c.B);
-  cfg.blockDim = dim3(NT2);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_copy_kernel<D, P>, p);
+  const dim3 pages((unsigned)((p.budget + P - 1) / P), (unsigned)p.c.Hkv, (unsigned)p.c.B);
+  return launch_next(cache_copy_kernel<D, P>, pages, NT2, 0, st, p);
 }
 
 }  // namespace

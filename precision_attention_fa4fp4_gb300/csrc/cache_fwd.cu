@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
   using Q = Queue<D, NT>;
   constexpr int R = 8 * NT;
   constexpr int S = Q::S;
+  grid_start();
   constexpr int NP = SMALLP ? 2 : 1;               // pages of a warp's 32 keys
   constexpr int OS = Q::OS;
   constexpr int VW = D / 32;                       // 32-bit words of V a lane holds per key
@@ -134,16 +135,6 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
   const int g = lane / 4, t4 = lane % 4;
   const Line ln = make_line(p.Hq, c.Hkv, p.T, p.pages != nullptr);
   const int G = ln.G;
-  auto seq = [&](int i) -> unsigned { return (unsigned)seq_units(p, i) * ln.nb; };
-  const unsigned total = line_total(c.B, seq);
-  const unsigned ctas = workers(total, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const Shares shares(total, ctas);
-  const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
-  unsigned at = begin, seq0;
-  int b;
-  if (!line_find(c.B, seq, at, b, seq0)) return;
-  int units = seq_units(p, b);
   const int log_p = 31 - __clz(c.page);
   uint8_t* queue = smem + warp * Q::WARP;
   unsigned phases = 0;                             // parity of each step's barrier
@@ -167,6 +158,18 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     vo[r] = boxed<D>(korder<D>(2 * t4 + (r & 1)) + 8 * (r >> 1), (D / 8) * (D == 128 ? korder<D>(g) : g) & ~15) +
             (D == 64 ? 8 * (g & 1) : 0);
   const int v_dim = (D / 8) * (D == 128 ? korder<D>(g) : g);   // first head dimension of the lane's V bytes
+
+  auto seq = [&](int i) -> unsigned { return (unsigned)seq_units(p, i) * ln.nb; };
+  grid_wait();
+  const unsigned total = line_total(c.B, seq);
+  const unsigned ctas = workers(total, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const Shares shares(total, ctas);
+  const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
+  unsigned at = begin, seq0;
+  int b;
+  if (!line_find(c.B, seq, at, b, seq0)) return;
+  int units = seq_units(p, b);
 
   while (at < end) {
     while (at >= seq0 + (unsigned)units * ln.nb) {
@@ -609,8 +612,7 @@ cudaError_t launch(const CacheFwdParams& p, int grid, cudaStream_t st) {
   auto k = p.c.page == 16 ? cache_fwd_kernel<D, NT, SPLIT, true> : cache_fwd_kernel<D, NT, SPLIT, false>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k<<<grid, 32 * NW, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(k, dim3((unsigned)grid), 32 * NW, smem, st, p);
 }
 
 }  // namespace

@@ -97,15 +97,15 @@ struct Window {
     e.ks = e.vs = 0;
     if (unit < end) {
       if (sel) {
-        lp = lp < n_sel ? __ldg(sel + lp) : -1;
+        lp = lp < n_sel ? *(sel + lp) : -1;
         if (lp >= c.max_pages || lp < -1) { atomicOr(c.err, FA4_DEVERR_INDEX); lp = -1; }
       }
       if (lp >= 0 && ((long long)lp << log_p) < len) {
         e.page = cache_page(c, c.table, b, lp);
         if (e.page >= 0) {
           const long long ph = (long long)e.page * c.Hkv + h;
-          e.ks = __ldg(c.ks + ph);
-          e.vs = __ldg(c.vs + ph);
+          e.ks = *(c.ks + ph);
+          e.vs = *(c.vs + ph);
           e.pos = (lp << log_p) + (v & (c.page - 1));
         }
       }

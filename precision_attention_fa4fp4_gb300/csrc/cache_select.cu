@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
   __shared__ __align__(16) uint32_t s_b[2][D];
   __shared__ int s_page[MAX_BORDER];
   __shared__ int s_in, s_border;
+  grid_start();
+  grid_wait();
   const CacheView& c = p.c;
   const int h = blockIdx.x / p.T % c.Hkv, t = blockIdx.x % p.T, b = blockIdx.x / (p.T * c.Hkv);
   int* out = p.out + (long long)blockIdx.x * p.n_sel;
@@ -183,10 +185,10 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
       for (int r = 0; r < 2; ++r) ph[r] = pages[r] >= 0 ? (long long)pages[r] * c.Hkv + h : -1;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        sc[r] = ph[r] >= 0 ? __ldg(c.ks + ph[r]) : 0;
+        sc[r] = ph[r] >= 0 ? *(c.ks + ph[r]) : 0;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          x[r][i] = ph[r] >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.kb + ph[r] * 2 * D + 64 * i + 16 * t4))
+          x[r][i] = ph[r] >= 0 ? *(reinterpret_cast<const uint4*>(c.kb + ph[r] * 2 * D + 64 * i + 16 * t4))
                                : make_uint4(0, 0, 0, 0);
       }
       look(first + 16 * (NT / 32));
@@ -387,8 +389,7 @@ cudaError_t launch(const CacheSelectParams& p, cudaStream_t st) {
         cudaFuncSetAttribute(cache_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  cache_select_kernel<D><<<(unsigned)p.c.B * p.c.Hkv * p.T, NT, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(cache_select_kernel<D>, dim3((unsigned)p.c.B * p.c.Hkv * p.T), NT, smem, st, p);
 }
 
 }  // namespace

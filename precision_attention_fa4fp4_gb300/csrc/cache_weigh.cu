@@ -51,6 +51,7 @@ template <int D, int NT, bool SMALLP>
 __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(const __grid_constant__ CacheWeighParams p) {
   using Q = WQueue<D, NT>;
   constexpr int S = Q::S;
+  grid_start();
   constexpr int NP = SMALLP ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -63,19 +64,6 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
   uint8_t* queue = smem + warp * Q::WARP;
   const int G = p.Hq / c.Hkv;
 
-  auto seq = [&](int i) -> unsigned {
-    const int n = cache_len(c, i);
-    return n ? (unsigned)units_of(n) * c.Hkv : 0u;
-  };
-  const unsigned total = line_total(c.B, seq);
-  if (total == 0) return;
-  const unsigned ctas = workers(total, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const Shares shares(total, ctas);
-  const unsigned end = shares.begin(blockIdx.x + 1);
-  unsigned at = shares.begin(blockIdx.x), seq0;
-  int b;
-  if (!line_find(c.B, seq, at, b, seq0)) return;
   const int log_p = 31 - __clz(c.page);
   unsigned phases = 0;
   if (lane == 0) {
@@ -93,6 +81,21 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
     for (int x = 0; x < D / 64; ++x) ko[r][x] = boxed<D>(korder<D>(g) + 8 * r, 64 * x + 16 * t4);
   // of the eight sums of a quad's columns, the lane writes that of one key
   const int my_i = t4 >> 1, my_key = 16 * (t4 >> 1) + 8 * (t4 & 1) + korder<D>(g);
+
+  auto seq = [&](int i) -> unsigned {
+    const int n = cache_len(c, i);
+    return n ? (unsigned)units_of(n) * c.Hkv : 0u;
+  };
+  grid_wait();
+  const unsigned total = line_total(c.B, seq);
+  if (total == 0) return;
+  const unsigned ctas = workers(total, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const Shares shares(total, ctas);
+  const unsigned end = shares.begin(blockIdx.x + 1);
+  unsigned at = shares.begin(blockIdx.x), seq0;
+  int b;
+  if (!line_find(c.B, seq, at, b, seq0)) return;
 
   bool ok = true;
   int place = 0;
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int rc = 8 * n + 2 * t4 + j;
-        lse[n][j] = rc < rows ? __ldg(p.lse + row_at(rc)) : 0.f;
+        lse[n][j] = rc < rows ? *(p.lse + row_at(rc)) : 0.f;
       }
     }
     Window<NP> window;
@@ -255,6 +258,8 @@ __global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __gr
   constexpr int QW = D / 32;                       // 16-byte words of a lane's query operand
   __shared__ uint4 s_q[BLOCK / 8][QW][32];         // row tile, word, lane
   __shared__ float s_fx[BLOCK], s_ref[BLOCK], s_fac[BLOCK];
+  grid_start();
+  grid_wait();
   const CacheView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t4 = lane % 4;
@@ -278,12 +283,12 @@ __global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __gr
     if (key < len) pg = cache_page(c, c.table, b, key / c.page);
     end[i] = pg < 0 ? 0 : len;
     const long long ph = (long long)max(pg, 0) * c.Hkv + h;
-    kx[i] = e8m0_value(__ldg(c.ks + ph));
+    kx[i] = e8m0_value(*(c.ks + ph));
     const uint8_t* at = c.k + (ph * c.page + key % c.page + g) * D + 16 * t4;
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
-      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(at + 64 * x));
-      const uint4 hi = __ldg(reinterpret_cast<const uint4*>(at + 8 * D + 64 * x));
+      const uint4 lo = *(reinterpret_cast<const uint4*>(at + 64 * x));
+      const uint4 hi = *(reinterpret_cast<const uint4*>(at + 8 * D + 64 * x));
       const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __gr
     for (int j = 0; j < BLOCK / 8 / NW; ++j) {
       const int r = r0 + 8 * (warp + j * NW) + g;
       raw[j].fetch(r < rows ? reinterpret_cast<const __nv_bfloat16*>(p.q) + row_at(r) * D : nullptr, t4);
-      lse[j] = r < rows ? __ldg(p.lse + row_at(r)) : 0.f;
+      lse[j] = r < rows ? *(p.lse + row_at(r)) : 0.f;
     }
     __syncthreads();
 #pragma unroll
@@ -389,8 +394,7 @@ cudaError_t launch_few(const CacheWeighParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long all = (long long)units_of((long long)p.c.max_pages * p.c.page) * p.c.Hkv * p.c.B;
   const long long most = (long long)kSMs * weigh_ctas(NT);
-  k<<<(unsigned)(all < most ? all : most), 32 * NW, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(k, dim3((unsigned)(all < most ? all : most)), 32 * NW, smem, st, p);
 }
 
 }  // namespace
@@ -405,9 +409,7 @@ cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const dim3 grid((unsigned)((cap + UNIT - 1) / UNIT), (unsigned)p.c.Hkv, (unsigned)p.c.B);
-  if (p.c.d == 128) cache_weigh_rows_kernel<128><<<grid, 32 * NW, 0, st>>>(p);
-  else cache_weigh_rows_kernel<64><<<grid, 32 * NW, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_next(p.c.d == 128 ? cache_weigh_rows_kernel<128> : cache_weigh_rows_kernel<64>, grid, 32 * NW, 0, st, p);
 }
 
 }  // namespace fa4
