@@ -7,12 +7,6 @@
 // positions in ascending order with their weights; the second copies the tokens
 // into fresh pages, one CTA per (page, head).
 //
-// The cut: the keys' range is divided evenly into 2048 bins, which spreads
-// weights of any scale; the bin with the cut usually holds a few keys, which are
-// ranked by counting, else it is divided again (three times at most).  Digits of
-// the keys instead crowd the weights into few bins, and counting them costs 1.4
-// to 3 us a digit; halving the range by comparisons 0.6 to 2 us a step.
-//
 // Tokens of pages with different scales meet in one page, so the codes are
 // fitted anew under the append's rule: X = the least integer >= -127 with every
 // kept value <= 448 2^X.  A code's magnitude fixes that integer by itself, so
@@ -25,7 +19,7 @@
 namespace fa4 {
 namespace {
 
-constexpr int NT1 = 1024;
+constexpr int NT1 = KTH_THREADS;
 
 // Unsigned keys in the order of the weights; NaN lowest, -0 as 0.
 FA4_DEV uint32_t weight_key(float x) {
@@ -35,8 +29,6 @@ FA4_DEV uint32_t weight_key(float x) {
 }
 
 constexpr int WARPS1 = NT1 / 32;
-constexpr int BINS = 2048;
-constexpr unsigned FEW = 256;
 
 // Exclusive prefix over the CTA, in the order (chunk, thread), of flags: chunk
 // j's of this thread is bit j of `flags`; at(j) is what add() gets.  s_cnt has
@@ -83,8 +75,7 @@ FA4_DEV int block_places(uint32_t flags, int* s_cnt, int* s_tot, F add) {
 // EPT chunks of NT1 weights at a time; all of them at once (and kept) if ONCE.
 template <int EPT, bool ONCE>
 __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__ CacheEvictParams p) {
-  __shared__ unsigned s_hist[BINS];
-  __shared__ unsigned s_bin, s_rank, s_count, s_lo, s_hi, s_few;
+  __shared__ KthShared s_kth;
   __shared__ int s_cnt[EPT * WARPS1], s_tot[32];
   grid_start();
   grid_wait();
@@ -114,93 +105,17 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
   unsigned ties = 0;
   bool all_ties = true;                            // all of those on it
   if (k > 0 && k < n) {
-    // the keys' range
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    auto each = [&](auto f) {
+    const Cut r = kth_largest(s_kth, (unsigned)k, [&](auto f) {
       for (int base = 0; base < n; base += EPT * NT1) {
         if (!ONCE) load(base);
 #pragma unroll
         for (int j = 0; j < EPT; ++j)
           if (base + j * NT1 + (int)threadIdx.x < n) f(weight_key(x[j]));
       }
-    };
-    if (threadIdx.x == 0) { s_lo = 0xffffffffu; s_hi = 0u; s_few = 0u; }
-    each([&](uint32_t key) { lo = min(lo, key); hi = max(hi, key); });
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    __syncthreads();
-    if (lane == 0) { atomicMin(&s_lo, lo); atomicMax(&s_hi, hi); }
-    unsigned rank = k;
-    for (int turn = 0;; ++turn) {
-      for (int i = threadIdx.x; i < BINS; i += NT1) s_hist[i] = 0;
-      __syncthreads();
-      if (turn == 0) { lo = s_lo; hi = s_hi; }
-      const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);   // 2048 bins cover lo .. hi
-      each([&](uint32_t key) {
-        if (key >= lo && key <= hi) atomicAdd(&s_hist[(key - lo) >> shift], 1u);
-      });
-      __syncthreads();
-      // two bins a thread, from the top: where the rank falls
-      const unsigned v0 = s_hist[BINS - 1 - 2 * threadIdx.x], v1 = s_hist[BINS - 2 - 2 * threadIdx.x];
-      unsigned inc = v0 + v1;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-      }
-      if (lane == 31) s_tot[warp] = (int)inc;
-      __syncthreads();
-      unsigned tot = (unsigned)s_tot[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const unsigned up = __shfl_up_sync(0xffffffffu, tot, o);
-        if (lane >= o) tot += up;
-      }
-      const unsigned before = (warp ? __shfl_sync(0xffffffffu, tot, warp - 1) : 0u) + inc - v0 - v1;
-      if (before < rank && rank <= before + v0 + v1) {
-        const bool first = rank <= before + v0;
-        s_bin = BINS - 1 - 2 * threadIdx.x - (first ? 0 : 1);
-        s_rank = rank - before - (first ? 0 : v0);
-        s_count = first ? v0 : v1;
-      }
-      __syncthreads();
-      lo += s_bin << shift;
-      hi = lo + (1u << shift) - 1u;
-      rank = s_rank;
-      const unsigned count = s_count;
-      cut = lo;
-      if (count == rank) break;                    // the whole bin stays
-      if (shift == 0) {                            // the bin is one key
-        ties = rank;
-        all_ties = false;
-        break;
-      }
-      if (count <= FEW) {                          // the bin's keys, ranked by counting
-        each([&](uint32_t key) {
-          if (key >= lo && key <= hi) s_hist[atomicAdd(&s_few, 1u)] = key;
-        });
-        __syncthreads();
-        if (threadIdx.x < count) {
-          const uint32_t mine = s_hist[threadIdx.x];
-          unsigned more = 0, same = 0;
-          for (unsigned i = 0; i < count; ++i) {
-            const uint32_t o = s_hist[i];
-            more += o > mine ? 1u : 0u;
-            same += o == mine ? 1u : 0u;
-          }
-          if (more < rank && rank <= more + same) {
-            s_lo = mine;
-            s_rank = rank - more;
-            s_count = same;
-          }
-        }
-        __syncthreads();
-        cut = s_lo;
-        ties = s_rank;
-        all_ties = s_count == ties;
-        break;
-      }
-    }
+    });
+    cut = r.key;
+    ties = r.ties;
+    all_ties = r.all;
   }
   const bool all = k >= n, none = k == 0;
   int done = 0, seen = 0;

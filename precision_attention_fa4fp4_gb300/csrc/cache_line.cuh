@@ -145,4 +145,101 @@ FA4_DEV float pow2_any(int x) {
   return x >= -126 ? exp2i(x) : (x >= -149 ? __uint_as_float(1u << (x + 149)) : 0.f);
 }
 
+// ----------------------------------------------------------------------------
+// The rank-th largest (1 = largest) of a CTA's unsigned keys, 1024 threads.
+// The keys' range is divided evenly into 2048 bins, which spreads values of any
+// scale; the bin with the rank usually holds a few keys, which are ranked by
+// counting, else it is divided again (three times at most).  Digits of the keys
+// instead crowd them into few bins, and counting those costs 1.4 to 3 us a
+// digit of 8192 weights; halving the range by comparisons 0.6 to 2 us a step.
+constexpr int KTH_THREADS = 1024, KTH_BINS = 2048;
+constexpr unsigned KTH_FEW = 256;
+struct KthShared {
+  unsigned hist[KTH_BINS];
+  unsigned bin, rank, count, lo, hi, few, tot[32];
+};
+// `key`: fewer than `rank` keys are above it if not `all`, and of those equal to
+// it `ties` belong to the rank-th largest; `all`: exactly `rank` keys reach it.
+struct Cut {
+  uint32_t key;
+  unsigned ties;
+  bool all;
+};
+// each(f) calls f(key) for every key of the thread; 0 < rank <= keys.
+template <class EACH>
+FA4_DEV Cut kth_largest(KthShared& s, unsigned rank, EACH each) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  if (threadIdx.x == 0) { s.lo = 0xffffffffu; s.hi = 0u; s.few = 0u; }
+  each([&](uint32_t key) { lo = min(lo, key); hi = max(hi, key); });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  __syncthreads();
+  if (lane == 0) { atomicMin(&s.lo, lo); atomicMax(&s.hi, hi); }
+  for (int turn = 0;; ++turn) {
+    for (int i = threadIdx.x; i < KTH_BINS; i += KTH_THREADS) s.hist[i] = 0;
+    __syncthreads();
+    if (turn == 0) { lo = s.lo; hi = s.hi; }
+    const int shift = max(0, 32 - __clz((int)(hi - lo)) - 11);     // 2048 bins cover lo .. hi
+    each([&](uint32_t key) {
+      if (key >= lo && key <= hi) atomicAdd(&s.hist[(key - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // two bins a thread, from the top: where the rank falls
+    const unsigned v0 = s.hist[KTH_BINS - 1 - 2 * threadIdx.x], v1 = s.hist[KTH_BINS - 2 - 2 * threadIdx.x];
+    unsigned inc = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) s.tot[warp] = inc;
+    __syncthreads();
+    unsigned tot = s.tot[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, tot, o);
+      if (lane >= o) tot += up;
+    }
+    const unsigned sum = __shfl_sync(0xffffffffu, tot, max(warp - 1, 0));
+    const unsigned before = (warp ? sum : 0u) + inc - v0 - v1;
+    if (before < rank && rank <= before + v0 + v1) {
+      const bool first = rank <= before + v0;
+      s.bin = KTH_BINS - 1 - 2 * threadIdx.x - (first ? 0 : 1);
+      s.rank = rank - before - (first ? 0 : v0);
+      s.count = first ? v0 : v1;
+    }
+    __syncthreads();
+    lo += s.bin << shift;
+    hi = lo + ((1u << shift) - 1u);
+    rank = s.rank;
+    const unsigned count = s.count;
+    if (count == rank) return {lo, 0u, true};        // the whole bin
+    if (shift == 0) return {lo, rank, false};        // the bin is one key
+    if (count <= KTH_FEW) {                          // the bin's keys, ranked by counting
+      each([&](uint32_t key) {
+        if (key >= lo && key <= hi) s.hist[atomicAdd(&s.few, 1u)] = key;
+      });
+      __syncthreads();
+      if (threadIdx.x < count) {
+        const uint32_t mine = s.hist[threadIdx.x];
+        unsigned more = 0, same = 0;
+        for (unsigned i = 0; i < count; ++i) {
+          const uint32_t o = s.hist[i];
+          more += o > mine ? 1u : 0u;
+          same += o == mine ? 1u : 0u;
+        }
+        if (more < rank && rank <= more + same) {
+          s.lo = mine;
+          s.rank = rank - more;
+          s.count = same;
+        }
+      }
+      __syncthreads();
+      return {s.lo, s.rank, s.count == s.rank};
+    }
+    __syncthreads();                                 // all have read bin, rank, count
+  }
+}
+
 }  // namespace fa4

@@ -22,12 +22,12 @@
 //
 // The intervals stay in shared memory (in the workspace where there are more
 // than 16384 pages).
-#include "cache.cuh"
+#include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
 
-constexpr int NT = 512;
+constexpr int NT = KTH_THREADS;
 constexpr int SMEM_PAGES = 16384;
 
 // Unsigned keys in the order of the floats (NaN above everything).
@@ -74,10 +74,9 @@ FA4_DEV void find_bin(const unsigned* hist, unsigned& rank, unsigned& bin) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_constant__ CacheSelectParams p) {
+__global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant__ CacheSelectParams p) {
   extern __shared__ __align__(16) uint32_t s_dyn[];
-  constexpr int STEPS = D / 8;                     // of 16 bounds each: lo [D], then hi [D]
-  __shared__ unsigned s_hist[256];
+    __shared__ KthShared s_kth;
   __shared__ unsigned s_pre, s_rank, s_err;
   __shared__ double s_up[D], s_dn[D], s_score[MAX_BORDER];
   __shared__ __align__(16) float s_w[2 * D];       // dn against lo, up against hi
@@ -107,8 +106,35 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
   float2* score = c.max_pages <= SMEM_PAGES ? reinterpret_cast<float2*>(s_dyn + (bit_words + 1) / 2 * 4)
                                             : p.score + (long long)blockIdx.x * c.max_pages;
   for (int i = threadIdx.x; i < words; i += NT) s_bits[i] = 0;
-  if (threadIdx.x == 0) { s_in = 0; s_border = 0; s_pre = 0; s_rank = k; s_err = 0; }
+  if (threadIdx.x == 0) { s_in = 0; s_border = 0; s_err = 0; }
   const int G = p.Hq / c.Hkv;
+  // A warp sums up 16 pages at a time, lane (g, t4) reading 16-byte words of
+  // pages g and g + 8; the first pages' bounds are on their way while the
+  // coefficients are formed.
+  const int g = lane / 4, t4 = lane % 4;
+  int raw[2];
+  uint4 x[2][D / 32];
+  uint32_t sc[2];
+  auto look = [&](int first) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int pi = first + g + 8 * r;
+      raw[r] = pi < m ? c.table[(long long)b * c.max_pages + pi] : -1;
+    }
+  };
+  auto load = [&](int first) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool in = raw[r] >= 0 && raw[r] < c.num_pages;
+      if (!in && first + g + 8 * r < m) atomicOr(c.err, FA4_DEVERR_INDEX);
+      const long long ph = in ? (long long)raw[r] * c.Hkv + h : 0;
+      sc[r] = in ? c.ks[ph] : 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        x[r][i] = in ? *reinterpret_cast<const uint4*>(c.kb + ph * 2 * D + 64 * i + 16 * t4) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (k > 0) look(16 * warp);
   if (threadIdx.x < D) {
     const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) +
                              (((long long)b * p.Hq + h * G) * p.T + t) * D + threadIdx.x;
@@ -127,9 +153,9 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
     s_w[threadIdx.x] = fd;
     s_w[D + threadIdx.x] = fu;
   }
-  __syncthreads();
   if (k > 0) {
-    const int g = lane / 4, t4 = lane % 4;
+    load(16 * warp);
+    __syncthreads();
     // the coefficients' largest magnitude and their sum of magnitudes
     uint32_t top = 0;
     float sum = 0.f;
@@ -154,43 +180,13 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
       s_b[1][threadIdx.x] = pack_f16x2((w.x * down - y.x) * 2048.f, (w.y * down - y.y) * 2048.f);
     }
     __syncthreads();
-    // the sum over the bounds runs in the order in which 16-byte words fall to
-    // the lanes
-    uint2 wb[STEPS];
-#pragma unroll
-    for (int x = 0; x < STEPS; ++x) {
-      wb[x] = make_uint2(0, 0);
-      if (g < 2) wb[x] = *reinterpret_cast<const uint2*>(&s_b[g][32 * (x / 4) + 8 * t4 + 2 * (x % 4)]);
-    }
     // Error: a coefficient is off by G - 1 roundings and 2^-22 (and 2^-35 of the
     // largest, below 2^-36 of the sum per term); the products are exact and
     // 2 D of them are added with 2^-23 of the sum of magnitudes each, whatever
     // their order; doubled.  The sum of magnitudes is at most the largest code
     // times the coefficients'.
     const float rel = (float)(G + 2 * D + 16) * 0x1p-22f;
-    int pages[2];
-    auto look = [&](int first) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int pi = first + g + 8 * r;
-        pages[r] = pi < m ? cache_page(c, c.table, b, pi) : -1;
-      }
-    };
-    look(16 * warp);
     for (int first = 16 * warp; first < m; first += 16 * (NT / 32)) {
-      long long ph[2];
-      uint4 x[2][D / 32];
-      uint32_t sc[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) ph[r] = pages[r] >= 0 ? (long long)pages[r] * c.Hkv + h : -1;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sc[r] = ph[r] >= 0 ? *(c.ks + ph[r]) : 0;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          x[r][i] = ph[r] >= 0 ? *(reinterpret_cast<const uint4*>(c.kb + ph[r] * 2 * D + 64 * i + 16 * t4))
-                               : make_uint4(0, 0, 0, 0);
-      }
       look(first + 16 * (NT / 32));
       float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
       uint32_t big[2] = {0, 0};
@@ -200,8 +196,11 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
         const uint32_t v[4] = {x[1][i].x, x[1][i].y, x[1][i].z, x[1][i].w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
+          // the sum runs in the order in which 16-byte words fall to the lanes
+          uint2 wb = make_uint2(0, 0);
+          if (g < 2) wb = *reinterpret_cast<const uint2*>(&s_b[g][32 * i + 8 * t4 + 2 * w]);
           mma_16816(w % 2 ? acc2 : acc, e4m3x2_to_f16x2(u[w]), e4m3x2_to_f16x2(v[w]), e4m3x2_hi_to_f16x2(u[w]),
-                    e4m3x2_hi_to_f16x2(v[w]), wb[4 * i + w].x, wb[4 * i + w].y);
+                    e4m3x2_hi_to_f16x2(v[w]), wb.x, wb.y);
           big[0] = __vmaxu4(big[0], u[w] & 0x7f7f7f7fu);
           big[1] = __vmaxu4(big[1], v[w] & 0x7f7f7f7fu);
         }
@@ -221,31 +220,18 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
           atomicMax(&s_err, __float_as_uint(err));
         }
       }
+      if (first + 16 * (NT / 32) < m) load(first + 16 * (NT / 32));
     }
     __syncthreads();
-    // the k-th largest sum
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
-      __syncthreads();
-      const unsigned pre = s_pre;
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = threadIdx.x; i < m; i += NT) {
-        const uint32_t key = key32(score[i].x);
-        if ((key & mask) == pre) atomicAdd(&s_hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        unsigned rank = s_rank, bin;
-        find_bin(s_hist, rank, bin);
-        if (lane == 0) { s_rank = rank; s_pre |= bin << shift; }
-      }
-      __syncthreads();
-    }
+    // the k-th largest sum, or a value that exactly k reach
+    const Cut kth = kth_largest(s_kth, k, [&](auto f) {
+      for (int i = threadIdx.x; i < m; i += NT) f(key32(score[i].x));
+    });
     // With err the largest error: k pages have a bound of at least cut - err, so
     // a page is certainly out whose own is surely below; and at most k have one
     // above cut + err (the others' sums are at most cut), so a page is certainly
     // in whose own surely is.  Sums that are not finite decide nothing.
-    const float cut = key32_value(s_pre), err = __uint_as_float(s_err);
+    const float cut = key32_value(kth.key), err = __uint_as_float(s_err);
     const float above = __fadd_ru(cut, err), below = __fsub_rd(cut, err);
     const bool sane = fabsf(above) <= 3.0e38f && fabsf(below) <= 3.0e38f;
     auto state = [&](int i) -> int {               // 1 in, -1 out, 0 undecided
@@ -314,18 +300,18 @@ __global__ void __launch_bounds__(NT, 1) cache_select_kernel(const __grid_consta
       if (threadIdx.x == 0) s_rank = need;
       unsigned long long pre = 0;
       for (int shift = 56; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += NT) s_hist[i] = 0;
+        for (int i = threadIdx.x; i < 256; i += NT) s_kth.hist[i] = 0;
         __syncthreads();
         const unsigned long long mask = shift == 56 ? 0ull : ~0ull << (shift + 8);
         for (int i = threadIdx.x; i < m; i += NT) {
           const double v = wide[i];
           const unsigned long long key = key64(v);
-          if (v == v && (key & mask) == pre) atomicAdd(&s_hist[(unsigned)(key >> shift) & 255u], 1u);
+          if (v == v && (key & mask) == pre) atomicAdd(&s_kth.hist[(unsigned)(key >> shift) & 255u], 1u);
         }
         __syncthreads();
         if (warp == 0) {
           unsigned rank = s_rank, bin;
-          find_bin(s_hist, rank, bin);
+          find_bin(s_kth.hist, rank, bin);
           if (lane == 0) { s_rank = rank; s_pre = bin; }
         }
         __syncthreads();
