@@ -399,11 +399,15 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const vo
  *                          and the tokens t that see j of e^(s - lse)
  * for j < lens[b], with fa4fp4_cache_fwd's arguments and the lse that it wrote
  * (rows with lse = -inf add nothing).  weights: f32 [B][Hkv][max_pages * page];
- * weight_out may be weight_in; entries j >= lens[b] are not written. */
+ * weight_out may be weight_in; entries j >= lens[b] are not written.  `workspace`
+ * as for fa4fp4_cache_fwd; below 64 query rows per kv head (Hq / Hkv * T) it
+ * needs none (its size is 0 and it may be NULL). */
+FA4FP4_API size_t fa4fp4_cache_weigh_workspace_bytes(int B, int Hq, int Hkv, int T, int d);
 FA4FP4_API fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const float* lse,
                                             const int* page_table, const int* lens, const int* q_lens, int B, int Hq,
                                             int T, int max_pages, float softmax_scale, int causal,
-                                            const float* weight_in, float* weight_out, void* stream);
+                                            const float* weight_in, float* weight_out, void* workspace,
+                                            size_t workspace_bytes, void* stream);
 
 /* Cuts every sequence back to `budget` tokens per kv head: the `recent` newest
  * and of the others those with the largest weight (f32 [B][Hkv][max_pages *

@@ -80,6 +80,8 @@ def load_library():
         lib.fa4fp4_cache_fwd_workspace_bytes.argtypes = [i] * 8
         lib.fa4fp4_cache_select_workspace_bytes.restype = sz
         lib.fa4fp4_cache_select_workspace_bytes.argtypes = [i] * 4
+        lib.fa4fp4_cache_weigh_workspace_bytes.restype = sz
+        lib.fa4fp4_cache_weigh_workspace_bytes.argtypes = [i] * 5
         lib.fa4fp4_sync_status.restype = i
         lib.fa4fp4_sync_status.argtypes = [vp]
         _lib = lib
@@ -592,3 +594,7 @@ def cache_fwd_workspace_bytes(B, Hq, Hkv, T, d, page, max_pages, n_sel=0) -> int
 
 def cache_select_workspace_bytes(B, Hkv, T, max_pages) -> int:
     return int(load_library().fa4fp4_cache_select_workspace_bytes(B, Hkv, T, max_pages))
+
+
+def cache_weigh_workspace_bytes(B, Hq, Hkv, T, d) -> int:
+    return int(load_library().fa4fp4_cache_weigh_workspace_bytes(B, Hq, Hkv, T, d))

@@ -109,6 +109,9 @@ bool make_rows_map(CUtensorMap* m, const void* base, int row_bytes, uint64_t row
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, row_bytes, rows, 1, row_bytes, box_rows,
                   row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
+bool make_f16_rows_map(CUtensorMap* m, const void* base, int d, uint64_t rows) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, d, rows, 1, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 }  // namespace fa4
 
 extern "C" {

@@ -62,8 +62,9 @@ size_t cache_select_workspace(int B, int Hkv, int T, int max_pages);
 cudaError_t launch_cache_select(const CacheSelectParams& p, cudaStream_t st);
 
 struct CacheWeighParams {
-  CUtensorMap tm_k;
+  CUtensorMap tm_k, tm_q;    // codes; the prepared rows (many rows only)
   CacheView c;
+  uint8_t *rows, *metas;     // workspace: prepared rows, their constants
   const void* q;
   const float* lse;      // [B][Hq][T]
   const int* q_lens;
@@ -74,6 +75,10 @@ struct CacheWeighParams {
 };
 bool cache_weigh_fits(int B, int Hkv, int page, int max_pages);
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st);
+// The same for many rows (query heads of a kv head x T), with a workspace.
+constexpr int WEIGH_MANY = 64;
+size_t cache_weigh_rows_bytes(int B, int Hq, int Hkv, int T, int d, size_t* all);
+cudaError_t launch_cache_weigh_rows(const CacheWeighParams& p, cudaStream_t st);
 
 struct CacheEvictParams {
   CacheView c;
@@ -89,6 +94,8 @@ cudaError_t launch_cache_evict(const CacheEvictParams& p, cudaStream_t st);
 // Tensor map of `rows` rows of `row_bytes` (64 or 128) bytes for boxes of
 // box_rows whole rows, swizzled over their whole width.
 bool make_rows_map(CUtensorMap* m, const void* base, int row_bytes, uint64_t rows, uint32_t box_rows);
+// ... of f16 rows of d values, for boxes of 64 values x 128 rows.
+bool make_f16_rows_map(CUtensorMap* m, const void* base, int d, uint64_t rows);
 // The library's device error word on the current device (nullptr on failure).
 unsigned* device_error_word();
 

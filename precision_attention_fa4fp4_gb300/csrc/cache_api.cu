@@ -152,10 +152,18 @@ fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const void* q, cons
   return status_of(launch_cache_select(p, static_cast<cudaStream_t>(stream)));
 }
 
+size_t fa4fp4_cache_weigh_workspace_bytes(int B, int Hq, int Hkv, int T, int d) {
+  if (check_shape(1, Hkv, 16, d, B, Hq, T, 1) != FA4FP4_OK || B == 0 || Hq == 0 || T == 0) return 0;
+  if ((long long)(Hq / Hkv) * T < WEIGH_MANY) return 0;
+  size_t all;
+  cache_weigh_rows_bytes(B, Hq, Hkv, T, d, &all);
+  return all;
+}
+
 fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const float* lse, const int* page_table,
                                  const int* lens, const int* q_lens, int B, int Hq, int T, int max_pages,
                                  float softmax_scale, int causal, const float* weight_in, float* weight_out,
-                                 void* stream) {
+                                 void* workspace, size_t workspace_bytes, void* stream) {
   fa4fp4_status s = check_call(cache, B, Hq, T, max_pages);
   if (s != FA4FP4_OK) return s;
   if (B == 0 || Hq == 0 || T == 0) return FA4FP4_OK;
@@ -164,11 +172,23 @@ fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const
   if (!q || !lse || !weight_in || !weight_out) return FA4FP4_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(weight_in, 4) || !aligned(weight_out, 4))
     return FA4FP4_ERR_ALIGNMENT;
+  const size_t need = fa4fp4_cache_weigh_workspace_bytes(B, Hq, cache->Hkv, T, cache->d);
+  if (need && (!workspace || workspace_bytes < need)) return FA4FP4_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return FA4FP4_ERR_ALIGNMENT;
+  // a prepared row is a 32-bit TMA coordinate
+  if (need / (2 * (size_t)cache->d) >= (1ull << 31)) return FA4FP4_ERR_UNSUPPORTED;
   CacheWeighParams p;
   memset(&p, 0, sizeof(p));
   if (!view(&p.c, cache, page_table, lens, B, max_pages)) return FA4FP4_ERR_CUDA;
-  if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, pool_rows(cache), cache_box(cache->page)))
+  if (need) {
+    size_t all;
+    p.rows = static_cast<uint8_t*>(workspace);
+    const size_t rows = cache_weigh_rows_bytes(B, Hq, cache->Hkv, T, cache->d, &all);
+    p.metas = p.rows + rows;
+    if (!make_f16_rows_map(&p.tm_q, p.rows, cache->d, rows / (2 * (size_t)cache->d))) return FA4FP4_ERR_CUDA;
+  } else if (!make_rows_map(&p.tm_k, cache->k_codes, cache->d, pool_rows(cache), cache_box(cache->page))) {
     return FA4FP4_ERR_CUDA;
+  }
   p.q = q; p.lse = lse; p.q_lens = q_lens; p.w_in = weight_in; p.w_out = weight_out;
   p.Hq = Hq; p.T = T; p.causal = causal ? 1 : 0;
   p.c2 = log2_scale(softmax_scale_of(softmax_scale, cache->d));

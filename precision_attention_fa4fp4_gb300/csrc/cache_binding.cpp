@@ -117,6 +117,15 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index, bool zer
   return zero ? at::zeros(shape, o) : at::empty(shape, o);
 }
 
+// The caller's workspace, or a fresh one of `need` bytes (none for 0).
+at::Tensor workspace(PyObject* x, int index, size_t need) {
+  if (!given(x)) return need ? fresh({(int64_t)need}, at::kByte, index) : at::Tensor();
+  const at::Tensor& t = as_tensor(x, "workspace");
+  if (t.scalar_type() != at::kByte || !t.is_cuda() || t.get_device() != index || !t.is_contiguous())
+    refuse("workspace: expected a contiguous uint8 tensor on the cache's device");
+  return t;
+}
+
 // ---------------------------------------------------------------- KVCache
 struct Cache {
   PyObject_HEAD
@@ -300,16 +309,8 @@ PyObject* fwd(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
       pages = ints(a[11], "pages", q.index, {q.B, c->Hkv, r.T, m});
       n_sel = (int)m;
     }
-    at::Tensor ws;
-    if (given(a[12])) {
-      ws = as_tensor(a[12], "workspace");
-      if (ws.scalar_type() != at::kByte || !ws.is_cuda() || ws.get_device() != q.index || !ws.is_contiguous())
-        refuse("workspace: expected a contiguous uint8 tensor on the cache's device");
-    } else {
-      const size_t need =
-          fa4fp4_cache_fwd_workspace_bytes(q.B, r.Hq, c->Hkv, r.T, c->d, c->page, q.max_pages, n_sel);
-      ws = fresh({(int64_t)(need ? need : 16)}, at::kByte, q.index);
-    }
+    const size_t need = fa4fp4_cache_fwd_workspace_bytes(q.B, r.Hq, c->Hkv, r.T, c->d, c->page, q.max_pages, n_sel);
+    const at::Tensor ws = workspace(a[12], q.index, need ? need : 16);
     launch("fa4fp4_cache_fwd", q.index, [&](void* st) {
       return fa4fp4_cache_fwd(c, r.q, q.table, q.lens, q.counts, pages, q.B, r.Hq, r.T, q.max_pages, n_sel, scale,
                               causal, o.data_ptr(), out_dtype, with_lse ? static_cast<float*>(l.data_ptr()) : nullptr,
@@ -342,14 +343,8 @@ PyObject* select(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     if (n_sel < 1) refuse("n_pages must be at least 1");
     const at::Tensor out = given(a[6]) ? expect(a[6], "out", q.index, at::kInt, {q.B, c->Hkv, r.T, n_sel})
                                        : fresh({q.B, c->Hkv, r.T, n_sel}, at::kInt, q.index);
-    at::Tensor ws;
-    if (given(a[7])) {
-      ws = as_tensor(a[7], "workspace");
-      if (ws.scalar_type() != at::kByte || !ws.is_cuda() || ws.get_device() != q.index || !ws.is_contiguous())
-        refuse("workspace: expected a contiguous uint8 tensor on the cache's device");
-    } else if (const size_t need = fa4fp4_cache_select_workspace_bytes(q.B, c->Hkv, r.T, q.max_pages)) {
-      ws = fresh({(int64_t)need}, at::kByte, q.index);
-    }
+    const at::Tensor ws =
+        workspace(a[7], q.index, fa4fp4_cache_select_workspace_bytes(q.B, c->Hkv, r.T, q.max_pages));
     launch("fa4fp4_cache_select", q.index, [&](void* st) {
       return fa4fp4_cache_select(c, r.q, q.table, q.lens, q.counts, q.B, r.Hq, r.T, q.max_pages, n_sel,
                                  static_cast<int*>(out.data_ptr()), ws.defined() ? ws.data_ptr() : nullptr,
@@ -361,10 +356,10 @@ PyObject* select(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
 
 PyObject* weigh(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
-    static const Signature s = {"cache_weigh", 10, 6,
+    static const Signature s = {"cache_weigh", 11, 6,
                                 {"q", "lse", "cache", "page_table", "lens", "weight", "q_lens", "causal",
-                                 "softmax_scale", "out"}};
-    PyObject* a[10];
+                                 "softmax_scale", "out", "workspace"}};
+    PyObject* a[11];
     parse(s, args, n, kw, a);
     const Sequences q(a[2], a[3], a[4], a[6], "q_lens");
     const Queries r(q, a[0]);
@@ -376,9 +371,11 @@ PyObject* weigh(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     float* out = static_cast<float*>(expect(po, "out", q.index, at::kFloat, {q.B, c->Hkv, L}).data_ptr());
     const bool causal = as_bool(a[7], true);
     const float scale = as_float(a[8]);
+    const at::Tensor ws =
+        workspace(a[10], q.index, fa4fp4_cache_weigh_workspace_bytes(q.B, r.Hq, c->Hkv, r.T, c->d));
     launch("fa4fp4_cache_weigh", q.index, [&](void* st) {
       return fa4fp4_cache_weigh(c, r.q, lse, q.table, q.lens, q.counts, q.B, r.Hq, r.T, q.max_pages, scale, causal, w,
-                                out, st);
+                                out, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, st);
     });
     return Py_NewRef(po);
   });
@@ -439,7 +436,7 @@ PyMethodDef methods[] = {
      "page_table, then -1."},
     {"cache_weigh", FA4_METHOD(weigh),
      "cache_weigh(q, lse, cache, page_table, lens, weight, q_lens=None, causal=True, softmax_scale=0.0,\n"
-     "            out=None) -> out\n\n"
+     "            out=None, workspace=None) -> out\n\n"
      "weight plus the attention weight that every cached token received from the queries\n"
      "(fa4fp4_cache_weigh), with the lse of cache_fwd: f32 [B, Hkv, max_pages * page], written to out\n"
      "(default: into weight itself), positions behind a sequence's end untouched."},

@@ -51,7 +51,7 @@ struct alignas(16) Meta {
 template <int D>
 struct SmemC {
   static constexpr int STAGES = 2;
-  static constexpr int CH = 128 * 128;              // one [128 rows][128 B] chunk (64 f16)
+  static constexpr int CH = F16_CHUNK;
   static constexpr int TILE = (D / 64) * CH;        // a tile of 128 f16 rows
   static constexpr int BYTES8 = 128 * D;            // a staged tile of codes
   static constexpr int OFF_Q = 0;
@@ -68,29 +68,6 @@ struct SmemC {
   static_assert(COL_O0 + 2 * D <= TMEM_COLS, "tensor memory");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-
-FA4_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// Sixteen codes to f16 into the two 16-byte units of a row that they fill.
-// Lanes of the odd half store the units in the other order: eight lanes at a
-// time then touch every bank once.
-template <int D>
-FA4_DEV void store16(uint8_t* tile, int row, int part, const uint4& x) {
-  const uint4 lo = make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x), e4m3x2_to_f16x2(x.y),
-                              e4m3x2_hi_to_f16x2(x.y));
-  const uint4 hi = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_hi_to_f16x2(x.z), e4m3x2_to_f16x2(x.w),
-                              e4m3x2_hi_to_f16x2(x.w));
-  uint8_t* at = tile + part / 4 * SmemC<D>::CH + row * 128;
-  const int u = 2 * (part % 4);
-  const bool odd = part >= 4;
-  *reinterpret_cast<uint4*>(at + (((u + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-  *reinterpret_cast<uint4*>(at + (((u + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
-}
 
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_constant__ CacheFwdParams p) {
@@ -113,7 +90,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   const int nt = (see_last + BN - 1) / BN;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + smem_pad(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_full = bars;
   uint64_t* k8_full = bars + 1;              // staged bytes
@@ -323,30 +300,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     // the row of q: largest magnitude, then f16 under a power of two
     float f_row;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D);
-      uint32_t amax = 0;
-      uint4 w[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        w[i] = valid ? *(src + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max((u[k] << 16) & 0x7fffffffu, u[k] & 0x7fff0000u));
-      }
-      const int E = (int)(amax >> 23);
-      const int e = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
-      const float down = exp2i(-e);
-      f_row = p.c2 * exp2i(e);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t z[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          z[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xffff0000u) * down);
-        *reinterpret_cast<uint4*>(smem + L::OFF_Q + x * L::TILE + i / 8 * L::CH + rt * 128 +
-                                  (((i % 8) ^ (rt & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
-      }
+      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D;
+      f_row = p.c2 * exp2i(store_query_row<D, D / 8>(smem + L::OFF_Q + x * L::TILE, rt, valid ? src : nullptr));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);

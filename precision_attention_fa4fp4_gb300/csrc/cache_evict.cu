@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
   grid_wait();
   const CacheView& c = p.c;
   const int h = blockIdx.x, b = blockIdx.y;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int len = cache_len(c, b);
   const int keep = min(len, p.budget);
   const int recent = min(p.recent, keep);

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
   constexpr int OS = Q::OS;
   constexpr int VW = D / 32;                       // 32-bit words of V a lane holds per key
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + smem_pad(smem_raw);
   float (*s_o)[R][OS] = reinterpret_cast<float (*)[R][OS]>(smem);
   float (*s_m)[R] = reinterpret_cast<float (*)[R]>(smem + NW * R * OS * 4);
   float (*s_l)[R] = s_m + NW;

@@ -242,4 +242,87 @@ FA4_DEV Cut kth_largest(KthShared& s, unsigned rank, EACH each) {
   }
 }
 
+// A contiguous copy into shared memory, counted on an mbarrier.
+FA4_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// ----------------------------------------------------------------------------
+// Tiles of f16 rows in shared memory as the products of tcgen05 read them: 128
+// rows, 64 values (128 bytes, swizzled) a chunk.
+constexpr int F16_CHUNK = 128 * 128;
+
+// Sixteen codes to f16 into the two 16-byte units of a row that they fill.
+// Lanes of the odd half store the units in the other order: eight lanes at a
+// time then touch every bank once.
+template <int D>
+FA4_DEV void store16(uint8_t* tile, int row, int part, const uint4& x) {
+  const uint4 lo = make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x), e4m3x2_to_f16x2(x.y),
+                              e4m3x2_hi_to_f16x2(x.y));
+  const uint4 hi = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_hi_to_f16x2(x.z), e4m3x2_to_f16x2(x.w),
+                              e4m3x2_hi_to_f16x2(x.w));
+  uint8_t* at = tile + part / 4 * F16_CHUNK + row * 128;
+  const int u = 2 * (part % 4);
+  const bool odd = part >= 4;
+  *reinterpret_cast<uint4*>(at + (((u + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+  *reinterpret_cast<uint4*>(at + (((u + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+}
+
+// A row of q (nullptr: zeros) as f16 under a power of two into row `row` of such
+// a tile: the largest magnitude comes into [2^7, 2^8), as in QRaw.  Returns the
+// exponent that undoes it.  HALF words of 16 bytes are held at a time.
+template <int D, int HALF>
+FA4_DEV int store_query_row(uint8_t* tile, int row, const __nv_bfloat16* src_row) {
+  const uint4* src = reinterpret_cast<const uint4*>(src_row);
+  uint4 w[HALF];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int p = D / 8 - HALF; p >= 0; p -= HALF) {    // ends with the first words in registers
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) w[i] = src ? src[p + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) amax = max(amax, max((u[k] << 16) & 0x7fffffffu, u[k] & 0x7fff0000u));
+    }
+  }
+  const int E = (int)(amax >> 23);
+  const int e = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
+  const float down = exp2i(-e);
+#pragma unroll
+  for (int p = 0; p < D / 8; p += HALF) {
+    if (p > 0) {
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) w[i] = src ? src[p + i] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t z[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        z[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xffff0000u) * down);
+      *reinterpret_cast<uint4*>(tile + (p + i) / 8 * F16_CHUNK + row * 128 + ((((p + i) % 8) ^ (row & 7)) << 4)) =
+          make_uint4(z[0], z[1], z[2], z[3]);
+    }
+  }
+  return e;
+}
+
+// lse in log2 units as a float and the factor that makes up for its rounding;
+// rows that add nothing get (0, 0).
+FA4_DEV void reference(float lse, bool in, float& ref, float& fac) {
+  ref = 0.f;
+  fac = 0.f;
+  if (in && lse != -INFINITY) {
+    ref = lse * 1.4426950216293335f;
+    const float rest = fmaf(lse, 1.4426950216293335f, -ref) + lse * 1.9259629911266175e-8f;
+    fac = ex2_approx(-rest);
+  }
+}
+
 }  // namespace fa4

@@ -21,18 +21,6 @@ namespace {
 
 constexpr int NW = LINE_WARPS;
 
-// lse in log2 units as a float and the factor that makes up for its rounding;
-// rows that add nothing get (0, 0).
-FA4_DEV void reference(float lse, bool in, float& ref, float& fac) {
-  ref = 0.f;
-  fac = 0.f;
-  if (in && lse != -INFINITY) {
-    ref = lse * 1.4426950216293335f;
-    const float rest = fmaf(lse, 1.4426950216293335f, -ref) + lse * 1.9259629911266175e-8f;
-    fac = ex2_approx(-rest);
-  }
-}
-
 // ---------------------------------------------------------------- few rows
 template <int D, int NT>
 struct WQueue {
@@ -54,7 +42,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
   grid_start();
   constexpr int NP = SMALLP ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + smem_pad(smem_raw);
   const CacheView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t4 = lane % 4;
@@ -407,6 +395,7 @@ cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
   if (rows <= 8) return p.c.d == 128 ? launch_few<128, 1>(p, st) : launch_few<64, 1>(p, st);
   if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
+  if (rows >= WEIGH_MANY) return launch_cache_weigh_rows(p, st);
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const dim3 grid((unsigned)((cap + UNIT - 1) / UNIT), (unsigned)p.c.Hkv, (unsigned)p.c.B);
   return launch_next(p.c.d == 128 ? cache_weigh_rows_kernel<128> : cache_weigh_rows_kernel<64>, grid, 32 * NW, 0, st, p);

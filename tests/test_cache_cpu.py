@@ -36,7 +36,7 @@ def calls(fa):
     lib.fa4fp4_cache_append.argtypes = [cp] + [vp] * 5 + [i, i, i, vp]
     lib.fa4fp4_cache_fwd.argtypes = [cp] + [vp] * 5 + [i] * 5 + [f, i, vp, i, vp, vp, sz, vp]
     lib.fa4fp4_cache_select.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp, vp, sz, vp]
-    lib.fa4fp4_cache_weigh.argtypes = [cp] + [vp] * 5 + [i] * 4 + [f, i, vp, vp, vp]
+    lib.fa4fp4_cache_weigh.argtypes = [cp] + [vp] * 5 + [i] * 4 + [f, i, vp, vp, vp, sz, vp]
     lib.fa4fp4_cache_evict.argtypes = [cp] + [vp] * 4 + [i] * 5 + [vp] * 4
 
     def append(c, k=P, v=P, table=P, lens=P, n_new=None, B=1, mp=3, T=2):
@@ -50,8 +50,9 @@ def calls(fa):
     def select(c, q=P, table=P, lens=P, q_lens=None, B=1, Hq=4, T=2, mp=3, n_sel=2, out=P, ws=P, wb=BIG):
         return lib.fa4fp4_cache_select(c, q, table, lens, q_lens, B, Hq, T, mp, n_sel, out, ws, wb, None)
 
-    def weigh(c, q=P, lse=P, table=P, lens=P, q_lens=None, B=1, Hq=4, T=2, mp=3, w=P, out=P):
-        return lib.fa4fp4_cache_weigh(c, q, lse, table, lens, q_lens, B, Hq, T, mp, 0.0, 1, w, out, None)
+    def weigh(c, q=P, lse=P, table=P, lens=P, q_lens=None, B=1, Hq=4, T=2, mp=3, w=P, out=P, ws=None,
+              wb=0):
+        return lib.fa4fp4_cache_weigh(c, q, lse, table, lens, q_lens, B, Hq, T, mp, 0.0, 1, w, out, ws, wb, None)
 
     def evict(c, table=P, lens=P, w=P, dst=P, B=1, mp=3, dp=2, budget=100, recent=4, nl=P, kept=P, wo=None):
         return lib.fa4fp4_cache_evict(c, table, lens, w, dst, B, mp, dp, budget, recent, nl, kept, wo, None)
@@ -120,6 +121,9 @@ def test_refusals_of_each_call(fa):
     assert c["weigh"](good, lse=None) == INVALID
     assert c["weigh"](good, w=None) == INVALID
     assert c["weigh"](good, out=ODD) == ALIGN
+    need = fa.cache_weigh_workspace_bytes(1, 4, 2, 32, 128)
+    assert c["weigh"](good, T=32) == WS and c["weigh"](good, T=32, ws=P, wb=need - 1) == WS
+    assert c["weigh"](good, T=32, ws=odd4, wb=need) == ALIGN
     assert c["evict"](good, budget=0) == INVALID
     assert c["evict"](good, budget=129) == INVALID        # more than two pages of 64 hold
     assert c["evict"](good, recent=101) == INVALID
@@ -139,6 +143,9 @@ def test_workspace_sizes(fa):
     assert f(65535, 64, 64, 1, 128, 128, 1 << 20, 0) == 0 and f(1, 8, 2, 1, 128, 64, 2, 1 << 25) == 0
     # bounded by the grid, whatever the batch
     assert f(512, 64, 8, 1, 128, 64, 4096, 0) == f(64, 64, 8, 1, 128, 64, 4096, 0) < (8 << 20)
+    # tiles of 128 rows of f16 and 16 bytes of constants a row, from 64 rows on
+    assert fa.cache_weigh_workspace_bytes(1, 4, 2, 31, 128) == 0
+    assert fa.cache_weigh_workspace_bytes(3, 4, 2, 65, 64) == 3 * 2 * 2 * 128 * (64 * 2 + 16)
     assert fa.cache_select_workspace_bytes(2, 3, 4, 16384) == 0
     assert fa.cache_select_workspace_bytes(2, 3, 4, 16385) == 2 * 3 * 4 * 16385 * 8
 
