@@ -91,8 +91,7 @@ FA4_DEV void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 // Bytes from p to the next multiple of 1024 (the swizzle's period).  Added to the
 // array itself, so that the compiler still sees shared memory: through an
 // address rounded as an integer every access became a generic one, with the
-// latency of a global load (four times the time of an epilogue that reads its
-// constants there).
+// latency of a global load.
 FA4_DEV uint32_t smem_pad(const void* p) { return (0u - smem_u32(p)) & 1023u; }
 FA4_DEV uint4 lds16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 FA4_DEV uint2 lds8(const void* p) { return *reinterpret_cast<const uint2*>(p); }

@@ -159,26 +159,64 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
             (D == 64 ? 8 * (g & 1) : 0);
   const int v_dim = (D / 8) * (D == 128 ? korder<D>(g) : g);   // first head dimension of the lane's V bytes
 
-  auto seq = [&](int i) -> unsigned { return (unsigned)seq_units(p, i) * ln.nb; };
   grid_wait();
-  const unsigned total = line_total(c.B, seq);
-  const unsigned ctas = workers(total, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const Shares shares(total, ctas);
-  const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
-  unsigned at = begin, seq0;
+  // Few row blocks: the shares are cut at their ends, into parts of at most `cut`
+  // units, so that no CTA has to finish one row block and begin another.  The
+  // shortest cut that leaves no more parts than CTAs is searched from below.
+  // (lane i keeps the units of sequence i where there are no more than 32)
+  const unsigned mine = lane < c.B ? (unsigned)seq_units(p, lane) : 0u;
+  auto lane_units = [&](int i) -> unsigned { return i < 32 ? mine : (unsigned)seq_units(p, i); };   // i % 32 == lane
+  const unsigned total = line_total(c.B, [&](int i) -> unsigned { return lane_units(i) * ln.nb; });
+  unsigned cut = 0;
+  if (2LL * ln.nb * c.B <= gridDim.x) {
+    cut = (total + gridDim.x - 1) / gridDim.x;
+    while (cut > 1 &&
+           line_total(c.B, [&](int i) -> unsigned { return (lane_units(i) + cut - 1) / cut * ln.nb; }) > gridDim.x)
+      cut += cut / 16 + 1;
+  }
+  // a sequence's stretch of the line: parts, or units
+  auto stretch = [&](unsigned u) -> unsigned { return (cut > 1 ? (u + cut - 1) / cut : u) * ln.nb; };
+  const Shares shares(total, workers(total, gridDim.x));
+  unsigned at, end, seq0;
+  if (cut) {
+    at = blockIdx.x;
+    end = at + 1;
+  } else {
+    if (blockIdx.x >= workers(total, gridDim.x)) return;
+    at = shares.begin(blockIdx.x);
+    end = shares.begin(blockIdx.x + 1);
+  }
+  const unsigned begin = at;
   int b;
-  if (!line_find(c.B, seq, at, b, seq0)) return;
+  if (!line_find(c.B, [&](int i) -> unsigned { return stretch(lane_units(i)); }, at, b, seq0))
+    return;                                        // more CTAs than parts
   int units = seq_units(p, b);
 
   while (at < end) {
-    while (at >= seq0 + (unsigned)units * ln.nb) {
-      seq0 += (unsigned)units * ln.nb;
+    while (at >= seq0 + stretch(units)) {
+      seq0 += stretch(units);
       units = seq_units(p, ++b);
     }
-    const int rb = (int)((at - seq0) / units);     // row block of the sequence
-    const int u0 = (int)((at - seq0) % units);
-    const int u1 = (int)min((unsigned)units, u0 + (end - at));
+    // row block, its units u0 .. u1, and where its slots lie: those of n CTAs
+    // from c0, the first of them perhaps its second
+    int rb, u0, u1, n, odd = 0;
+    unsigned c0;
+    if (cut) {
+      n = (units + cut - 1) / cut;
+      rb = (int)((at - seq0) / n);
+      const unsigned part = (at - seq0) % n;
+      u0 = (int)((unsigned long long)units * part / n);
+      u1 = (int)((unsigned long long)units * (part + 1) / n);
+      c0 = seq0 + (unsigned)rb * n;
+    } else {
+      rb = (int)((at - seq0) / units);
+      u0 = (int)((at - seq0) % units);
+      u1 = (int)min((unsigned)units, u0 + (end - at));
+      const unsigned start = seq0 + (unsigned)rb * units;
+      c0 = shares.of(start);
+      n = (int)(shares.of(start + units - 1) - c0) + 1;
+      odd = shares.begin(c0) >= start ? 0 : 1;
+    }
     const int h = rb / ln.per_head, sub = rb % ln.per_head;
     const int len = cache_len(c, b);
     const int q_len = cache_count(p.q_lens, b, p.T, c.err);
@@ -206,16 +244,15 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     }
     Window<NP> window;
     window.fill(c, b, h, len, sel, p.n_sel, u0, u1);
+    // A step's boxes; then, apart, what it needs besides them: the boxes are not
+    // to wait for the scales' loads.
     auto issue = [&](int s, int u) {
       if (!window.has(u)) window.fill(c, b, h, len, sel, p.n_sel, u, u1);
-      int what[4] = {NOWHERE, 0, NOWHERE, 0};      // position, scales of each page
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const Entry w = window.get(u, i);
-        what[2 * i] = w.pos;
-        what[2 * i + 1] = w.ks | w.vs << 8;
-        if (w.page >= 0 && lane == 0) {
-          const int row = (int)(((long long)w.page * c.Hkv + h) << log_p) + (w.pos & (c.page - 1));
+        const int page = window.page(u, i), pos = window.pos(u, i);
+        if (page >= 0 && lane == 0) {
+          const int row = (int)(((long long)page * c.Hkv + h) << log_p) + (pos & (c.page - 1));
           uint8_t* to = queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0);
           // each box counts for itself: a step without a page has none
           mbar_expect_tx(&bars[s], 2 * (32 / NP) * D);
@@ -223,12 +260,16 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
           tma_load_3d(to + 32 * D, &p.tm_v, &bars[s], 0, row, 0);
         }
       }
-      if (lane == 0) {
-        steps[s] = make_int4(what[0], what[1], what[2], what[3]);
-        mbar_arrive(&bars[s]);
-      }
+      if (lane == 0) mbar_arrive(&bars[s]);
     };
+    auto note = [&](int s, int u) {
+      int4 what = make_int4(window.pos(u, 0), window.scales(u, 0), NOWHERE, 0);
+      if (NP == 2) { what.z = window.pos(u, NP - 1); what.w = window.scales(u, NP - 1); }
+      if (lane == 0) steps[s] = what;
+    };
+    // (the first S units lie in the first window)
     for (int s = 0; s < S; ++s) issue(s, u0 + s);
+    for (int s = 0; s < S; ++s) note(s, u0 + s);
 
     QFrag<D> q[NT];
     float fx[NT][2];                               // log2-unit factor of columns 2 t4, 2 t4 + 1
@@ -265,6 +306,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     auto body = [&](int st, int u) -> bool {
       if (!mbar_wait(&bars[st], (phases >> st) & 1, abort_flag, c.err)) return false;
       phases ^= 1u << st;
+      __syncwarp();
       const uint8_t* from = queue + st * Q::BYTES;
       const int4 what = steps[st];
       int pos[NP];
@@ -429,6 +471,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       // the step's bytes are in registers: its place takes unit u + S
       __syncwarp();
       issue(st, u + S);
+      note(st, u + S);
       return true;
     };
     bool ok = true;
@@ -510,10 +553,6 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     }
     __syncthreads();
     if (!whole) {
-      // the row block's units lie in the shares of CTAs c0 .. c1
-      const unsigned start = seq0 + (unsigned)rb * units;
-      const unsigned c0 = shares.of(start), c1 = shares.of(start + units - 1);
-      const int n = c1 - c0 + 1;
       if (threadIdx.x == 0) {
         // the barrier above and the release here order the CTA's slot before
         // its arrival, the acquire the others' slots before the join
@@ -542,9 +581,6 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       }
       __syncthreads();
       if (s_misc[1]) {
-        // of the CTAs of a row block only the first may have come to it from
-        // another: its second slot
-        const int odd = shares.begin(c0) >= start ? 0 : 1;
         auto slot_of = [&](int i) -> const float* {
           return part + (size_t)((c0 + i) * 2 + (i == 0 ? odd : 0)) * Slot<D, NT>::FLOATS;
         };
@@ -593,7 +629,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     // the merge buffer makes room for the next row block's boxes
     fence_proxy_async_smem();
     __syncthreads();
-    at += u1 - u0;
+    at += cut ? 1 : u1 - u0;
   }
 }
 

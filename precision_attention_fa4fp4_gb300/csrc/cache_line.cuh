@@ -113,15 +113,11 @@ struct Window {
     __syncwarp();
   }
   FA4_DEV bool has(int u) const { return u < first + 32 / NP; }
-  FA4_DEV Entry get(int u, int i) const {
-    const int src = (u - first) * NP + i;
-    Entry r;
-    r.page = __shfl_sync(0xffffffffu, e.page, src);
-    r.pos = __shfl_sync(0xffffffffu, e.pos, src);
-    const uint32_t s = __shfl_sync(0xffffffffu, e.ks | e.vs << 8, src);
-    r.ks = s & 0xffu;
-    r.vs = s >> 8;
-    return r;
+  FA4_DEV int page(int u, int i) const { return __shfl_sync(0xffffffffu, e.page, (u - first) * NP + i); }
+  FA4_DEV int pos(int u, int i) const { return __shfl_sync(0xffffffffu, e.pos, (u - first) * NP + i); }
+  // K's scale byte, and V's above it
+  FA4_DEV int scales(int u, int i) const {
+    return __shfl_sync(0xffffffffu, (int)(e.ks | e.vs << 8), (u - first) * NP + i);
   }
 };
 

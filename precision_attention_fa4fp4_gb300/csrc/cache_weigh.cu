@@ -111,25 +111,25 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
     window.fill(c, b, h, len, nullptr, 0, u0, u1);
     auto issue = [&](int s, int u) {
       if (!window.has(u)) window.fill(c, b, h, len, nullptr, 0, u, u1);
-      int what[4] = {NOWHERE, 0, NOWHERE, 0};
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const Entry w = window.get(u, i);
-        what[2 * i] = w.pos;
-        what[2 * i + 1] = w.ks;
-        if (w.page >= 0 && lane == 0) {
-          const int row = (int)(((long long)w.page * c.Hkv + h) << log_p) + (w.pos & (c.page - 1));
+        const int page = window.page(u, i), pos = window.pos(u, i);
+        if (page >= 0 && lane == 0) {
+          const int row = (int)(((long long)page * c.Hkv + h) << log_p) + (pos & (c.page - 1));
           mbar_expect_tx(&bars[s], (32 / NP) * D);
           tma_load_3d(queue + s * Q::BYTES + (SMALLP ? i * 16 * D : 0), &p.tm_k, &bars[s], 0, row, 0);
         }
       }
-      if (lane == 0) {
-        steps[s] = make_int4(what[0], what[1], what[2], what[3]);
-        mbar_arrive(&bars[s]);
-      }
+      if (lane == 0) mbar_arrive(&bars[s]);
+    };
+    auto note = [&](int s, int u) {
+      int4 what = make_int4(window.pos(u, 0), window.scales(u, 0), NOWHERE, 0);
+      if (NP == 2) { what.z = window.pos(u, NP - 1); what.w = window.scales(u, NP - 1); }
+      if (lane == 0) steps[s] = what;
     };
     // the queue goes on where the last head left it
     for (int s = 0; s < S; ++s) issue((place + s) % S, u0 + s);
+    for (int s = 0; s < S; ++s) note((place + s) % S, u0 + s);
 
     QFrag<D> q[NT];
     float fx[NT][2], ref[NT][2], fac[NT][2];
@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
     for (int u = u0; ok && u < u1; ++u) {
       if (!mbar_wait(&bars[place], (phases >> place) & 1, abort_flag, c.err)) { ok = false; break; }
       phases ^= 1u << place;
+      __syncwarp();
       const uint8_t* from = queue + place * Q::BYTES;
       const int4 what = steps[place];
       int pos[NP];
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         pos[i] = i ? what.z : what.x;
-        kx[i] = e8m0_value(i ? what.w : what.y);
+        kx[i] = e8m0_value((i ? what.w : what.y) & 0xff);
       }
       // the lane's key: its weight is read early
       const int key = SMALLP ? (my_i ? pos[NP - 1] : pos[0]) + my_key - 16 * my_i : pos[0] + my_key;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
         }
       __syncwarp();
       issue(place, u + S);
+      note(place, u + S);
       place = place + 1 == S ? 0 : place + 1;
 
       bool full = true;
