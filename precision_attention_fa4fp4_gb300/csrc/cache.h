@@ -46,7 +46,9 @@ struct CacheFwdParams {
 // Workspace of the split forward; 0: more work than one call takes.
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages);
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st);
-// The same for many rows, all pages and bf16 output; needs no workspace.
+// The same for many rows, all pages and bf16 output, with a workspace of its own
+// size.
+size_t cache_chunk_workspace(int B, int Hq, int Hkv, int T, int d, int page, int max_pages);
 cudaError_t launch_cache_chunk(const CacheFwdParams& p, cudaStream_t st);
 
 struct CacheSelectParams {

@@ -39,6 +39,34 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr float P_BIAS = 15.f;
 constexpr int V_DOWN = 4, V_LOWER = 80;      // as in the kernel for few rows
 constexpr int METAS = 4;
+constexpr int MIN_SHARE = 4;                 // tiles of a share: a start and a join cost two
+
+// Row blocks of 256 of a kv head's rows.
+__host__ __device__ inline int row_blocks(int G, int T) { return (int)(((long long)G * T + 2 * BM - 1) / (2 * BM)); }
+
+// Partial of a cut row block: o / l [d / 4][256][4], then m, l.
+template <int D>
+struct PartC {
+  static constexpr int FLOATS = 2 * BM * (D + 2);
+};
+
+// Row block `i` of all (sequence, row block) pairs: what it is and the tiles of
+// keys that its last token sees.
+struct Block {
+  int b, r0, rows, len, q_len, nt;
+  FA4_DEV Block(const CacheFwdParams& p, int G, int RB, int i) {
+    b = i / RB;
+    r0 = (i - b * RB) * 2 * BM;
+    len = cache_len(p.c, b);
+    q_len = cache_count(p.q_lens, b, p.T, p.c.err);
+    rows = G * q_len;
+    const int t_last = (min(rows, r0 + 2 * BM) - 1) / G;
+    const int see = p.causal ? max(0, min(len, len - q_len + t_last + 1)) : len;
+    nt = r0 < rows ? (see + BN - 1) / BN : 0;
+  }
+  // units of the line: one where rows see no keys
+  FA4_DEV int units() const { return r0 < rows ? max(nt, 1) : 0; }
+};
 
 // Scales of a 128-key tile, by groups of 16 keys.
 struct alignas(16) Meta {
@@ -61,13 +89,26 @@ struct SmemC {
   static constexpr int OFF_V8 = OFF_K8 + BYTES8;
   static constexpr int OFF_META = OFF_V8 + BYTES8;
   static constexpr int OFF_BAR = (OFF_META + METAS * (int)sizeof(Meta) + 7) / 8 * 8;
-  static constexpr int NBAR = 1 + 4 + 4 * STAGES + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 + 4 + 4 * STAGES + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t COL_O0 = 256;
   static_assert(COL_O0 + 2 * D <= TMEM_COLS, "tensor memory");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
+
+FA4_DEV void store_bf16_32(__nv_bfloat16* dst, const float (&y)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 z = __floats2bfloat162_rn(y[8 * i + 2 * e], y[8 * i + 2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&z);
+    }
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_constant__ CacheFwdParams p) {
@@ -77,27 +118,47 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   grid_start();
   grid_wait();
   const CacheView& c = p.c;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int G = p.Hq / c.Hkv;
-  const int len = cache_len(c, b);
-  const int q_len = cache_count(p.q_lens, b, p.T, c.err);
-  const int rows = G * q_len;
-  const int r0 = (int)blockIdx.x * 2 * BM;
-  if (r0 >= rows) return;
-  // keys that the CTA's last token sees, in tiles
-  const int t_last = (min(rows, r0 + 2 * BM) - 1) / G;
-  const int see_last = p.causal ? max(0, min(len, len - q_len + t_last + 1)) : len;
-  const int nt = (see_last + BN - 1) / BN;
+  const int G = p.Hq / c.Hkv, RB = row_blocks(G, p.T), blocks = c.B * RB;
+  // the line: (sequence, row block), kv head, tile
+  auto units = [&](int i) -> unsigned { return (unsigned)(Block(p, G, RB, i).units() * c.Hkv); };
+  const unsigned total = line_total(blocks, units);
+  if (total == 0) return;
+  const unsigned n_shares = workers(total, min((unsigned)gridDim.x, (total + MIN_SHARE - 1) / MIN_SHARE));
+  if (blockIdx.x >= n_shares) return;
+  const Shares shares(total, n_shares);
+  const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
+  // the part of a row block of a kv head that starts at unit `at` (whole warp)
+  struct Seg {
+    int b, h, r0, rows, len, q_len, t0, tiles, nx;
+    unsigned item, all;                      // the row block's first unit, its units
+    unsigned next;                           // where the next part starts
+  };
+  auto segment = [&](unsigned at) -> Seg {
+    int i = 0;
+    unsigned seq0 = 0;
+    line_find(blocks, units, at, i, seq0);
+    const Block k(p, G, RB, i);
+    Seg g;
+    g.b = k.b; g.r0 = k.r0; g.rows = k.rows; g.len = k.len; g.q_len = k.q_len;
+    g.all = (unsigned)max(k.units(), 1);
+    g.h = min((int)((at - seq0) / g.all), c.Hkv - 1);
+    g.item = seq0 + (unsigned)g.h * g.all;
+    g.t0 = (int)(at - g.item);
+    g.next = min(end, g.item + g.all);
+    g.tiles = k.nt == 0 ? 0 : (int)(g.next - at);
+    g.nx = k.rows - k.r0 > BM ? 2 : 1;       // tile B may have no rows
+    return g;
+  };
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + smem_pad(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_full = bars;
-  uint64_t* k8_full = bars + 1;              // staged bytes
-  uint64_t* k8_empty = bars + 2;
-  uint64_t* v8_full = bars + 3;
-  uint64_t* v8_empty = bars + 4;
-  uint64_t* k_full = bars + 5;               // f16 tiles
+  uint64_t* q_full = bars;                  // by tile
+  uint64_t* k8_full = bars + 2;              // staged bytes
+  uint64_t* k8_empty = bars + 3;
+  uint64_t* v8_full = bars + 4;
+  uint64_t* v8_empty = bars + 5;
+  uint64_t* k_full = bars + 6;               // f16 tiles
   uint64_t* k_empty = k_full + STAGES;
   uint64_t* v_full = k_empty + STAGES;
   uint64_t* v_empty = v_full + STAGES;
@@ -107,11 +168,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   uint64_t* mma_done = o_done + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  volatile int* last_one = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 8);
   Meta* metas = reinterpret_cast<Meta*>(smem + L::OFF_META);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 8);
     mbar_init(k8_full, 1); mbar_init(k8_empty, 4);
     mbar_init(v8_full, 1); mbar_init(v8_empty, 4);
     for (int s = 0; s < STAGES; ++s) {
@@ -119,6 +180,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       mbar_init(&v_full[s], 4); mbar_init(&v_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 4);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_done[x], 1);
@@ -138,40 +200,46 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     if (warp == W_LOAD) {
       // ---------------------------------------------------------- pages
       const int log_p = 31 - __clz(c.page);
-      int issued = 0;
-      for (int j = 0; j < nt; ++j) {
-        // lane i < 8: group i of 16 keys; the first lane of a page copies it
-        const int key = j * BN + 16 * (lane & 7);
-        const int lp = key >> log_p;
-        int pg = -1;
-        if (lane < 8 && key < len) pg = cache_page(c, c.table, b, lp);
-        const long long ph = (long long)max(pg, 0) * c.Hkv + h;
-        const float kx = e8m0_value(*(c.ks + ph));
-        const int ev = (int)*(c.vs + ph) - 127;
-        Meta& m = metas[j % METAS];
-        if (j > 0 && !mbar_wait(k8_empty, (j - 1) & 1, abort_flag, c.err)) break;
-        int top = pg >= 0 ? ev : -1000;
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
-        if (lane < 8) {
-          m.kx[lane] = kx;
-          m.ev[lane] = ev;
-          if (lane == 0) { m.ev_max = top; m.absent = ~there & 0xffu; }
+      int issued = 0, n = 0;                 // n: tiles so far
+      bool ok = true;
+      for (unsigned at = begin; ok && at < end;) {
+        const Seg sg = segment(at);
+        at = sg.next;
+        for (int j = sg.t0; j < sg.t0 + sg.tiles; ++j, ++n) {
+          // lane i < 8: group i of 16 keys; the first lane of a page copies it
+          const int key = j * BN + 16 * (lane & 7);
+          const int lp = key >> log_p;
+          int pg = -1;
+          if (lane < 8 && key < sg.len) pg = cache_page(c, c.table, sg.b, lp);
+          const long long ph = (long long)max(pg, 0) * c.Hkv + sg.h;
+          const float kx = e8m0_value(*(c.ks + ph));
+          const int ev = (int)*(c.vs + ph) - 127;
+          Meta& m = metas[n % METAS];
+          if (n > 0 && !mbar_wait(k8_empty, (n - 1) & 1, abort_flag, c.err)) { ok = false; break; }
+          int top = pg >= 0 ? ev : -1000;
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+          if (lane < 8) {
+            m.kx[lane] = kx;
+            m.ev[lane] = ev;
+            if (lane == 0) { m.ev_max = top; m.absent = ~there & 0xffu; }
+          }
+          __syncwarp();
+          const bool copies = lane < 8 && pg >= 0 && ((16 * lane) & (c.page - 1)) == 0;
+          const uint32_t bytes = (uint32_t)c.page * D;
+          const uint32_t all = (uint32_t)__popc(__ballot_sync(0xffffffffu, copies)) * bytes;
+          if (lane == 0) mbar_arrive_expect_tx(k8_full, all);
+          __syncwarp();
+          if (copies) bulk_load(smem + L::OFF_K8 + 16 * lane * D, c.k + (ph << log_p) * D, bytes, k8_full);
+          issued = 2 * n + 1;
+          if (n > 0 && !mbar_wait(v8_empty, (n - 1) & 1, abort_flag, c.err)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(v8_full, all);
+          __syncwarp();
+          if (copies) bulk_load(smem + L::OFF_V8 + 16 * lane * D, c.v + (ph << log_p) * D, bytes, v8_full);
+          issued = 2 * n + 2;
         }
-        __syncwarp();
-        const bool copies = lane < 8 && pg >= 0 && ((16 * lane) & (c.page - 1)) == 0;
-        const uint32_t bytes = (uint32_t)c.page * D;
-        const uint32_t all = (uint32_t)__popc(__ballot_sync(0xffffffffu, copies)) * bytes;
-        if (lane == 0) mbar_arrive_expect_tx(k8_full, all);
-        __syncwarp();
-        if (copies) bulk_load(smem + L::OFF_K8 + 16 * lane * D, c.k + (ph << log_p) * D, bytes, k8_full);
-        if (j > 0 && !mbar_wait(v8_empty, (j - 1) & 1, abort_flag, c.err)) { issued = 2 * j + 1; break; }
-        if (lane == 0) mbar_arrive_expect_tx(v8_full, all);
-        __syncwarp();
-        if (copies) bulk_load(smem + L::OFF_V8 + 16 * lane * D, c.v + (ph << log_p) * D, bytes, v8_full);
-        issued = 2 * j + 2;
       }
       if (*abort_flag) {                     // what is still in flight lands first
         volatile int none = 0;
@@ -180,15 +248,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         if (nv) mbar_wait(v8_full, (nv - 1) & 1, &none, c.err);
       }
       __syncwarp();
-    } else if (warp == W_MMA && nt > 0) {
+    } else if (warp == W_MMA) {
       // ---------------------------------------------------------- products
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, false, false, false);
       const uint32_t idesc_o = idesc_f16(BM, D, false, false, true);   // A from TMEM, V MN-major
       const uint32_t sq = smem_u32(smem + L::OFF_Q);
-      bool ok = mbar_wait(q_full, 0, abort_flag, c.err);
-      tc_fence_after();
-      auto issue_qk = [&](int x, int t) -> bool {
+      bool ok = true;
+      // t: the CTA's tile, for the stages; u: the tile's (0: A, 1: B) own count
+      auto issue_qk = [&](int x, int t, bool last) -> bool {
         const int st = t % STAGES;
         if (x == 0 && !mbar_wait(&k_full[st], (t / STAGES) & 1, abort_flag, c.err)) return false;
         tc_fence_after();
@@ -202,36 +270,46 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
                     make_sdesc(sk + off, 16, 1024, SW_128B), idesc_s, k > 0);
           }
           mma_commit(&s_full[x]);
-          if (x == 1) mma_commit(&k_empty[st]);
+          if (last) mma_commit(&k_empty[st]);
         }
         __syncwarp();
         return true;
       };
-      auto issue_pv = [&](int x, int t) -> bool {
+      auto issue_pv = [&](int x, int t, int u, bool first, bool last) -> bool {
         const int st = t % STAGES;
         if (x == 0 && !mbar_wait(&v_full[st], (t / STAGES) & 1, abort_flag, c.err)) return false;
-        if (!mbar_wait(&p_full[x], t & 1, abort_flag, c.err)) return false;
+        if (!mbar_wait(&p_full[x], u & 1, abort_flag, c.err)) return false;
         tc_fence_after();
         const uint32_t sv = smem_u32(smem + L::OFF_V + st * L::TILE);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
             mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + 128 * x + 8 * k,
-                           make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, t > 0 || k > 0);
+                           make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, !first || k > 0);
           mma_commit(&o_done[x]);
-          if (x == 1) mma_commit(&v_empty[st]);
+          if (last) mma_commit(&v_empty[st]);
         }
         __syncwarp();
         return true;
       };
       // each tile's next Q K^T follows its own P V, so the pipe has read P_X
       // before it overwrites S_X
-      if (ok) ok = issue_qk(0, 0) && issue_qk(1, 0);
-      for (int j = 0; ok && j < nt; ++j) {
-        if (!issue_pv(0, j)) { ok = false; break; }
-        if (j + 1 < nt && !issue_qk(0, j + 1)) { ok = false; break; }
-        if (!issue_pv(1, j)) { ok = false; break; }
-        if (j + 1 < nt && !issue_qk(1, j + 1)) { ok = false; break; }
+      int n = 0, nb = 0, pa = 0, pb = 0;     // tiles and parts so far, those of B among them
+      for (unsigned at = begin; ok && at < end;) {
+        const Seg sg = segment(at);
+        at = sg.next;
+        if (sg.tiles == 0) continue;
+        const bool two = sg.nx == 2;
+        ok = mbar_wait(&q_full[0], pa++ & 1, abort_flag, c.err) && (!two || mbar_wait(&q_full[1], pb++ & 1, abort_flag, c.err));
+        tc_fence_after();
+        ok = ok && issue_qk(0, n, !two) && (!two || issue_qk(1, n, true));
+        for (int j = 0; ok && j < sg.tiles; ++j) {
+          const bool more = j + 1 < sg.tiles;
+          ok = issue_pv(0, n + j, n + j, j == 0, !two) && (!more || issue_qk(0, n + j + 1, !two));
+          if (two) ok = ok && issue_pv(1, n + j, nb + j, j == 0, true) && (!more || issue_qk(1, n + j + 1, true));
+        }
+        n += sg.tiles;
+        if (two) nb += sg.tiles;
       }
       if (leader) mma_commit(mma_done);
       __syncwarp();
@@ -246,42 +324,49 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     constexpr int RSTEP = 128 / PARTS;       // rows at once
     const int tid = threadIdx.x - 32 * W_CONV;
     const int part = tid % PARTS, row0 = tid / PARTS;
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % STAGES;
-      const int left = len - j * BN;         // keys of the tile that are there
-      const uint32_t parity = (j / STAGES - 1) & 1;
+    int n = 0;
+    bool ok = true;
+    for (unsigned at = begin; ok && at < end;) {
+      const Seg sg = segment(at);
+      at = sg.next;
+      for (int j = sg.t0; ok && j < sg.t0 + sg.tiles; ++j, ++n) {
+        const int st = n % STAGES;
+        const int left = sg.len - j * BN;    // keys of the tile that are there
+        const uint32_t parity = (n / STAGES - 1) & 1;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint64_t* full8 = kv ? v8_full : k8_full;
-        uint64_t* empty8 = kv ? v8_empty : k8_empty;
-        uint64_t* empty = kv ? &v_empty[st] : &k_empty[st];
-        uint64_t* full = kv ? &v_full[st] : &k_full[st];
-        if (!mbar_wait(full8, j & 1, abort_flag, c.err)) break;
-        const uint8_t* from = smem + (kv ? L::OFF_V8 : L::OFF_K8) + row0 * D + part * 16;
-        uint4 x[128 / RSTEP];
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* full8 = kv ? v8_full : k8_full;
+          uint64_t* empty8 = kv ? v8_empty : k8_empty;
+          uint64_t* empty = kv ? &v_empty[st] : &k_empty[st];
+          uint64_t* full = kv ? &v_full[st] : &k_full[st];
+          ok = ok && mbar_wait(full8, n & 1, abort_flag, c.err);
+          if (!ok) break;
+          const uint8_t* from = smem + (kv ? L::OFF_V8 : L::OFF_K8) + row0 * D + part * 16;
+          uint4 x[128 / RSTEP];
 #pragma unroll
-        for (int i = 0; i < 128 / RSTEP; ++i) x[i] = lds16(from + i * RSTEP * D);
-        const uint32_t absent = metas[j % METAS].absent;
-        // what is not there is zero: a score is masked by its place, but 0 * NaN
-        // must not happen to P V
-        if (left < BN || absent) {
+          for (int i = 0; i < 128 / RSTEP; ++i) x[i] = lds16(from + i * RSTEP * D);
+          const uint32_t absent = metas[n % METAS].absent;
+          // what is not there is zero: a score is masked by its place, but 0 * NaN
+          // must not happen to P V
+          if (left < BN || absent) {
 #pragma unroll
-          for (int i = 0; i < 128 / RSTEP; ++i) {
-            const int row = row0 + i * RSTEP;
-            if (row >= left || ((absent >> (row / 16)) & 1)) x[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 128 / RSTEP; ++i) {
+              const int row = row0 + i * RSTEP;
+              if (row >= left || ((absent >> (row / 16)) & 1)) x[i] = make_uint4(0, 0, 0, 0);
+            }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty8);
-        if (j >= STAGES && !mbar_wait(empty, parity, abort_flag, c.err)) break;
-        uint8_t* tile = smem + (kv ? L::OFF_V : L::OFF_K) + st * L::TILE;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty8);
+          if (n >= STAGES) ok = mbar_wait(empty, parity, abort_flag, c.err);
+          if (!ok) break;
+          uint8_t* tile = smem + (kv ? L::OFF_V : L::OFF_K) + st * L::TILE;
 #pragma unroll
-        for (int i = 0; i < 128 / RSTEP; ++i) store16<D>(tile, row0 + i * RSTEP, part, x[i]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
+          for (int i = 0; i < 128 / RSTEP; ++i) store16<D>(tile, row0 + i * RSTEP, part, x[i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
       }
-      if (*abort_flag) break;
     }
   } else {
     setmaxnreg_inc<REG_SOFT>();
@@ -289,163 +374,227 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     const int x = warp >> 2;
     const int quad = warp & 3;
     const int rt = quad * 32 + lane;         // row within the tile
-    const int r = r0 + x * BM + rt;
-    const bool valid = r < rows;
-    const int t = valid ? r / G : 0, gg = valid ? r % G : 0;
-    const long long orow = ((long long)b * p.Hq + h * G + gg) * p.T + t;
+    const int mate = BM * x + rt;            // row of the block
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const uint32_t col_s = 128 * x, col_o = COL_O0 + D * x;
-    const int vis = !valid ? 0 : p.causal ? max(0, min(len, len - q_len + t + 1)) : len;
-
-    // the row of q: largest magnitude, then f16 under a power of two
-    float f_row;
-    {
-      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D;
-      f_row = p.c2 * exp2i(store_query_row<D, D / 8>(smem + L::OFF_Q + x * L::TILE, rt, valid ? src : nullptr));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
-
-    float m = -INFINITY, l = 0.f;
-    int xo = -127;                           // o is in units of 2^xo
+    // After a wait that ran out a warp computes no more, but comes to the
+    // barriers of every join.
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      if (!mbar_wait(&s_full[x], j & 1, abort_flag, c.err)) { ok = false; break; }
-      tc_fence_after();
-      float s[4][32];
-      {
-        uint32_t v[4][32];
+    int n = 0, m0 = 0;                       // tiles so far of X, of the CTA
+    for (unsigned at = begin; at < end;) {
+      const Seg sg = segment(at);
+      const bool cut = shares.of(sg.item) != shares.of(sg.item + sg.all - 1);
+      const int tiles = x < sg.nx ? sg.tiles : 0;
+      const int r = sg.r0 + mate;
+      const bool valid = r < sg.rows;
+      const int t = valid ? r / G : 0, gg = valid ? r - t * G : 0;
+      const long long orow = ((long long)sg.b * p.Hq + sg.h * G + gg) * p.T + t;
+      const int vis = !valid ? 0 : p.causal ? max(0, min(sg.len, sg.len - sg.q_len + t + 1)) : sg.len;
+
+      // the row of q: largest magnitude, then f16 under a power of two
+      float f_row = 0.f;
+      if (tiles > 0) {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D;
+        f_row = p.c2 * exp2i(store_query_row<D, D / 8>(smem + L::OFF_Q + x * L::TILE, rt, valid ? src : nullptr));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[x]);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      int xo = -127;                         // o is in units of 2^xo
+      for (int j = 0; ok && j < tiles; ++j, ++n) {
+        ok = mbar_wait(&s_full[x], n & 1, abort_flag, c.err);
+        if (!ok) break;
+        tc_fence_after();
+        float s[4][32];
+        {
+          uint32_t v[4][32];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32(lane_base + col_s + 32 * g, v[g]);
-        tmem_ld_wait();
+          for (int g = 0; g < 4; ++g) tmem_ld32(lane_base + col_s + 32 * g, v[g]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            reg_fence32(v[g]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[g][i] = __uint_as_float(v[g][i]);
+          }
+        }
+        const Meta& meta = metas[(m0 + j) % METAS];
+        const uint32_t absent = meta.absent;
+        const int left = vis - (sg.t0 + j) * BN;
+        if (__any_sync(0xffffffffu, left < BN) || absent) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * g + i >= left || ((absent >> (2 * g + i / 16)) & 1)) s[g][i] = -INFINITY;
+        }
+        // exponent of V against the accumulator's
+        const int ev_max = meta.ev_max;
+        float back = 1.f;
+        if (ev_max > -1000 && (ev_max > xo || ev_max < xo - V_DOWN)) {
+          const int to = j == 0 ? ev_max : max(ev_max, xo - V_LOWER);
+          back = pow2_any(xo - to);
+          xo = to;
+        }
+        // max by groups of 16 keys, each with its K scale
+        float F[8];
+        {
+          const float4 k0 = *reinterpret_cast<const float4*>(meta.kx), k1 = *reinterpret_cast<const float4*>(meta.kx + 4);
+          F[0] = k0.x * f_row; F[1] = k0.y * f_row; F[2] = k0.z * f_row; F[3] = k0.w * f_row;
+          F[4] = k1.x * f_row; F[5] = k1.y * f_row; F[6] = k1.z * f_row; F[7] = k1.w * f_row;
+        }
+        float m_new = m;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float a[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) a[i] = s[g / 2][16 * (g % 2) + i];
+          float top = fmax3(a[0], a[1], a[2]);
+          float top2 = fmax3(a[3], a[4], a[5]);
+          top = fmax3(top, a[6], a[7]);
+          top2 = fmax3(top2, a[8], a[9]);
+          top = fmax3(top, a[10], a[11]);
+          top2 = fmax3(top2, a[12], a[13]);
+          top = fmax3(top, a[14], a[15]);
+          m_new = fmaxf(m_new, fmaxf(top, top2) * F[g]);
+        }
+        const float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
+        float l_new = 0.f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          reg_fence32(v[g]);
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[g][i] = __uint_as_float(v[g][i]);
-        }
-      }
-      const Meta& meta = metas[j % METAS];
-      const uint32_t absent = meta.absent;
-      const int left = vis - j * BN;
-      if (__any_sync(0xffffffffu, left < BN) || absent) {
+          for (int hf = 0; hf < 2; ++hf) {
+            const int gr = 2 * g + hf;
+            const int d = min(0, max(meta.ev[gr] - xo, -100));
+            const float Fg = F[gr], add = (float)d - ref;
+            float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * g + i >= left || ((absent >> (2 * g + i / 16)) & 1)) s[g][i] = -INFINITY;
-      }
-      // exponent of V against the accumulator's
-      const int ev_max = meta.ev_max;
-      float back = 1.f;
-      if (ev_max > -1000 && (ev_max > xo || ev_max < xo - V_DOWN)) {
-        const int to = j == 0 ? ev_max : max(ev_max, xo - V_LOWER);
-        back = pow2_any(xo - to);
-        xo = to;
-      }
-      // max by groups of 16 keys, each with its K scale
-      float F[8];
-      {
-        const float4 k0 = *reinterpret_cast<const float4*>(meta.kx), k1 = *reinterpret_cast<const float4*>(meta.kx + 4);
-        F[0] = k0.x * f_row; F[1] = k0.y * f_row; F[2] = k0.z * f_row; F[3] = k0.w * f_row;
-        F[4] = k1.x * f_row; F[5] = k1.y * f_row; F[6] = k1.z * f_row; F[7] = k1.w * f_row;
-      }
-      float m_new = m;
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        float a[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = s[g / 2][16 * (g % 2) + i];
-        float top = fmax3(a[0], a[1], a[2]);
-        float top2 = fmax3(a[3], a[4], a[5]);
-        top = fmax3(top, a[6], a[7]);
-        top2 = fmax3(top2, a[8], a[9]);
-        top = fmax3(top, a[10], a[11]);
-        top2 = fmax3(top2, a[12], a[13]);
-        top = fmax3(top, a[14], a[15]);
-        m_new = fmaxf(m_new, fmaxf(top, top2) * F[g]);
-      }
-      const float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
-      float l_new = 0.f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int gr = 2 * g + hf;
-          const int d = min(0, max(meta.ev[gr] - xo, -100));
-          const float Fg = F[gr], add = (float)d - ref;
-          float2 ls = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int k = 16 * hf + 2 * i;
-            const float2 e = ffma2(make_float2(s[g][k], s[g][k + 1]), make_float2(Fg, Fg), make_float2(add, add));
-            const float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            ls = fadd2(ls, pp);
-            pk[8 * hf + i] = pack_f16x2(pp.x, pp.y);
-          }
-          l_new = fmaf(ls.x + ls.y, exp2i(-d), l_new);
-        }
-        tmem_st16(lane_base + col_s + 16 * g, pk);
-      }
-      const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
-      if (j > 0) {
-        if (!mbar_wait(&o_done[x], (j - 1) & 1, abort_flag, c.err)) { ok = false; break; }
-        tc_fence_after();
-        const float by = alpha * back;
-        if (__any_sync(0xffffffffu, by != 1.f)) {
-#pragma unroll
-          for (int g = 0; g < D / 32; ++g) {
-            uint32_t ov[32];
-            tmem_ld32(lane_base + col_o + 32 * g, ov);
-            tmem_ld_wait();
-            reg_fence32(ov);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = fmul2(make_float2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), make_float2(by, by));
-              ov[i] = __float_as_uint(y.x);
-              ov[i + 1] = __float_as_uint(y.y);
+            for (int i = 0; i < 8; ++i) {
+              const int k = 16 * hf + 2 * i;
+              const float2 e = ffma2(make_float2(s[g][k], s[g][k + 1]), make_float2(Fg, Fg), make_float2(add, add));
+              const float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              ls = fadd2(ls, pp);
+              pk[8 * hf + i] = pack_f16x2(pp.x, pp.y);
             }
-            tmem_st32(lane_base + col_o + 32 * g, ov);
+            l_new = fmaf(ls.x + ls.y, exp2i(-d), l_new);
+          }
+          tmem_st16(lane_base + col_s + 16 * g, pk);
+        }
+        const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
+        if (j > 0) {
+          ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
+          if (!ok) break;
+          tc_fence_after();
+          const float by = alpha * back;
+          if (__any_sync(0xffffffffu, by != 1.f)) {
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g) {
+              uint32_t ov[32];
+              tmem_ld32(lane_base + col_o + 32 * g, ov);
+              tmem_ld_wait();
+              reg_fence32(ov);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = fmul2(make_float2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), make_float2(by, by));
+                ov[i] = __float_as_uint(y.x);
+                ov[i + 1] = __float_as_uint(y.y);
+              }
+              tmem_st32(lane_base + col_o + 32 * g, ov);
+            }
           }
         }
+        l = fmaf(alpha, l, l_new);
+        m = m_new;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      l = fmaf(alpha, l, l_new);
-      m = m_new;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
-    }
-    if (ok && (nt == 0 || mbar_wait(&o_done[x], (nt - 1) & 1, abort_flag, c.err))) {
+      if (ok && tiles > 0) ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
       tc_fence_after();
       // a row without keys: whatever the accumulator holds counts for nothing
       const bool none = l == 0.f;
-      const float inv = none ? 0.f : 1.f / l, unit = pow2_any(xo);
+      float4* part = reinterpret_cast<float4*>(p.part + (gridDim.x * 8 + 15) / 16 * 16);
+      float4* slot = part + (size_t)(2 * blockIdx.x + (at == begin ? 0 : 1)) * (PartC<D>::FLOATS / 4);
+      if (ok && x < sg.nx) {
+        const float inv = none ? 0.f : 1.f / l, unit = pow2_any(xo);
 #pragma unroll 1
-      for (int g = 0; g < D / 32; ++g) {
-        uint32_t v[32];
-        tmem_ld32(lane_base + col_o + 32 * g, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-        if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + orow * D + 32 * g);
+        for (int g = 0; g < D / 32; ++g) {
+          uint32_t v[32];
+          tmem_ld32(lane_base + col_o + 32 * g, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+          if (!valid) continue;
+          float y[32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 32; ++i) y[i] = none ? 0.f : __uint_as_float(v[i]) * unit * inv;
+          if (cut) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = none ? 0.f : __uint_as_float(v[8 * i + 2 * e]) * unit * inv;
-              const float z = none ? 0.f : __uint_as_float(v[8 * i + 2 * e + 1]) * unit * inv;
-              const __nv_bfloat162 y = __floats2bfloat162_rn(a, z);
-              w[e] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 8; ++i)
+              slot[(8 * g + i) * 2 * BM + mate] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else {
+            store_bf16_32(reinterpret_cast<__nv_bfloat16*>(p.o) + orow * D + 32 * g, y);
           }
         }
+        if (valid && cut) {
+          float* ml = reinterpret_cast<float*>(slot) + 2 * BM * D + mate;
+          ml[0] = m;
+          ml[2 * BM] = l;
+        } else if (valid && p.lse) {
+          p.lse[orow] = none ? -INFINITY : fmaf(m - P_BIAS, 0.69314718f, logf(l));
+        }
       }
-      if (valid && p.lse) p.lse[orow] = none ? -INFINITY : fmaf(m - P_BIAS, 0.69314718f, logf(l));
+      if (cut) {
+        // The block's parts meet: whoever is the last to have written one joins
+        // them.  The barrier and the release order the CTA's part before its
+        // arrival, the acquire the others' parts before the join.
+        const unsigned c0 = shares.of(sg.item), parts = shares.of(sg.item + sg.all - 1) - c0 + 1;
+        const int odd = shares.begin(c0) != sg.item;
+        named_bar(1, 2 * BM);
+        if (threadIdx.x == 0) *last_one = !*abort_flag && marked_arrive(reinterpret_cast<unsigned long long*>(p.part) + c0, parts);
+        named_bar(1, 2 * BM);
+        if (*last_one && valid) {
+          auto slot_of = [&](unsigned i) { return part + (size_t)(2 * (c0 + i) + (i == 0 ? odd : 0)) * (PartC<D>::FLOATS / 4); };
+          auto stat = [&](unsigned i, int which) {
+            return __ldcg(reinterpret_cast<const float*>(slot_of(i)) + 2 * BM * (D + which) + mate);
+          };
+          float mt = -INFINITY, lt = 0.f;
+          for (unsigned i = 0; i < parts; ++i) mt = fmaxf(mt, stat(i, 0));
+          for (unsigned i = 0; i < parts; ++i) {
+            const float li = stat(i, 1);
+            if (li != 0.f) lt = fmaf(li, ex2_approx(stat(i, 0) - mt), lt);
+          }
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll 1
+          for (int g = 0; g < D / 32; ++g) {
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = 0.f;
+            for (unsigned i = 0; i < parts; ++i) {
+              const float4* from = slot_of(i) + 16 * g * BM + mate;
+              const float li = stat(i, 1), w = li == 0.f ? 0.f : li * inv * ex2_approx(stat(i, 0) - mt);
+              float4 z[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] = __ldcg(from + e * 2 * BM);
+              if (w == 0.f) continue;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                y[4 * e] = fmaf(w, z[e].x, y[4 * e]);
+                y[4 * e + 1] = fmaf(w, z[e].y, y[4 * e + 1]);
+                y[4 * e + 2] = fmaf(w, z[e].z, y[4 * e + 2]);
+                y[4 * e + 3] = fmaf(w, z[e].w, y[4 * e + 3]);
+              }
+            }
+            store_bf16_32(reinterpret_cast<__nv_bfloat16*>(p.o) + orow * D + 32 * g, y);
+          }
+          if (p.lse) p.lse[orow] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
+        }
+      }
+      m0 += sg.tiles;
+      at = sg.next;
     }
   }
   tc_fence_before();
@@ -453,17 +602,32 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
+// CTAs of the fixed grid: the GPU's, or fewer where the cache's capacity gives
+// fewer tiles; 0: more than the line's 32 bits count.
+int grid_of(int B, int Hq, int Hkv, int T, int page, int max_pages) {
+  const long long blocks = (long long)row_blocks(Hq / Hkv, T) * B;
+  const long long tiles = ((long long)max_pages * page + BN - 1) / BN;
+  if (blocks * Hkv >= (1LL << 31) / (tiles < 1 ? 1 : tiles)) return 0;
+  const long long all = blocks * Hkv * (tiles < 1 ? 1 : tiles);
+  return (int)(all < kSMs ? all : kSMs);
+}
+
 template <int D>
 cudaError_t launch(const CacheFwdParams& p, cudaStream_t st) {
   auto k = cache_chunk_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemC<D>::BYTES);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
-  const dim3 grid((unsigned)((rows + 2 * BM - 1) / (2 * BM)), (unsigned)p.c.Hkv, (unsigned)p.c.B);
-  return launch_next(k, grid, NTHREADS, SmemC<D>::BYTES, st, p);
+  const int grid = grid_of(p.c.B, p.Hq, p.c.Hkv, p.T, p.c.page, p.c.max_pages);
+  if (grid == 0) return cudaErrorInvalidValue;
+  return launch_next(k, dim3((unsigned)grid), NTHREADS, SmemC<D>::BYTES, st, p);
 }
 
 }  // namespace
+
+size_t cache_chunk_workspace(int B, int Hq, int Hkv, int T, int d, int page, int max_pages) {
+  const size_t grid = (size_t)grid_of(B, Hq, Hkv, T, page, max_pages);
+  return (grid * 8 + 15) / 16 * 16 + 2 * grid * 4 * (size_t)(d == 128 ? PartC<128>::FLOATS : PartC<64>::FLOATS);
+}
 
 cudaError_t launch_cache_chunk(const CacheFwdParams& p, cudaStream_t st) {
   return p.c.d == 128 ? launch<128>(p, st) : launch<64>(p, st);

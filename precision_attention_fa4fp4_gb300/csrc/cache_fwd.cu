@@ -53,9 +53,7 @@ constexpr float P_BIAS = 15.f;
 // is bounded, so that the accumulator stays below 2^(40 + 80) (its terms: 2^15 *
 // 448, fewer than 2^17 of them a warp).
 constexpr int V_DOWN = 4, V_LOWER = 80;
-// the mark of a counter word, in its high 48 bits (no number, no pointer and no
-// pair of floats that a workspace could hold from other use)
-constexpr unsigned long long MARK = 0xfa4c0de5eed5ull;
+constexpr int MANY_ROWS = 48;
 
 // Resident CTAs by registers, and the steps in flight that fill the shared
 // memory they leave.
@@ -557,27 +555,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
         // the barrier above and the release here order the CTA's slot before
         // its arrival, the acquire the others' slots before the join
         unsigned long long* word = reinterpret_cast<unsigned long long*>(p.part) + c0;
-        // one addition, unless the word holds anything but a marked count: then
-        // whoever swaps that for the mark and a count of one has arrived, and
-        // the others add again (a swap fails only when the word has changed,
-        // by another arrival)
-        unsigned long long had = atomic_add_acq_rel(word, 1ull);
-        if ((had >> 16) != MARK) {
-          ++had;
-          for (;;) {
-            __threadfence();
-            const unsigned long long was = atomicCAS(word, had, MARK << 16 | 1u);
-            if (was == had) { had = MARK << 16; break; }
-            had = was;
-            if ((had >> 16) == MARK) { had = atomic_add_acq_rel(word, 1ull); break; }
-          }
-        }
-        const unsigned count = (unsigned)(had & 0xffffu) + 1;
-        if (count == (unsigned)n) {
-          atomicExch(word, MARK << 16);
-          __threadfence();
-        }
-        s_misc[1] = count == (unsigned)n;
+        s_misc[1] = marked_arrive(word, (unsigned)n);
       }
       __syncthreads();
       if (s_misc[1]) {
@@ -653,25 +631,24 @@ cudaError_t launch(const CacheFwdParams& p, int grid, cudaStream_t st) {
 
 }  // namespace
 
+// Whether the kernel for many rows is the faster one.
+static bool many_rows(int Hq, int Hkv, int T) {
+  return (long long)(Hq / Hkv) * T > MANY_ROWS;
+}
+
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d, int n_sel, int page, int max_pages) {
   const Line ln = make_line(Hq, Hkv, T, n_sel > 0);
   const size_t slot = (size_t)ln.R * (d + 2) * 4;
   const size_t grid = (size_t)grid_of(ln, B, d, n_sel, page, max_pages);
-  return grid ? Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid : 0;
-}
-
-// Whether the kernel for many rows is the faster one.  Both take time in
-// proportion to the keys: per 128 of them, 1.3 us for each wave of its CTAs (256
-// rows of a kv head each) against 0.0048 us for each block of 16 rows here.
-static bool many_rows(const CacheFwdParams& p) {
-  if (p.pages || !p.out_bf16) return false;
-  const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T, heads = (long long)p.c.Hkv * p.c.B;
-  const long long waves = (((rows + 255) / 256) * heads + kSMs - 1) / kSMs;
-  return rows > 16 && 1.3 * waves < 0.0048 * (double)((rows + 15) / 16 * heads);
+  if (!grid) return 0;
+  const size_t few = Slot<64, 1>::counters((unsigned)grid) + 2 * slot * grid;
+  // either, as the output's type decides
+  const size_t many = n_sel == 0 && many_rows(Hq, Hkv, T) ? cache_chunk_workspace(B, Hq, Hkv, T, d, page, max_pages) : 0;
+  return many > few ? many : few;
 }
 
 cudaError_t launch_cache_fwd(const CacheFwdParams& p, cudaStream_t st) {
-  if (many_rows(p)) return launch_cache_chunk(p, st);
+  if (!p.pages && p.out_bf16 && many_rows(p.Hq, p.c.Hkv, p.T)) return launch_cache_chunk(p, st);
   const Line ln = make_line(p.Hq, p.c.Hkv, p.T, p.pages != nullptr);
   const int grid = grid_of(ln, p.c.B, p.c.d, p.pages ? p.n_sel : 0, p.c.page, p.c.max_pages);
   if (grid == 0) return cudaErrorInvalidValue;

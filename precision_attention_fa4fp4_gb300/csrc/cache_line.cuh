@@ -69,6 +69,35 @@ FA4_DEV bool line_find(int B, F units, unsigned at, int& b, unsigned& seq0) {
   return false;
 }
 
+// The mark of a counter word, in its high 48 bits (no number, no pointer and no
+// pair of floats that a workspace could hold from other use).
+constexpr unsigned long long MARK = 0xfa4c0de5eed5ull;
+// One arrival at a counter word: whether it is the last of n, which leaves the
+// word marked and at zero for the next call.  Release before, acquire after.
+FA4_DEV bool marked_arrive(unsigned long long* word, unsigned n) {
+  // one addition, unless the word holds anything but a marked count: then
+  // whoever swaps that for the mark and a count of one has arrived, and the
+  // others add again (a swap fails only when the word has changed, by another
+  // arrival)
+  unsigned long long had = atomic_add_acq_rel(word, 1ull);
+  if ((had >> 16) != MARK) {
+    ++had;
+    for (;;) {
+      __threadfence();
+      const unsigned long long was = atomicCAS(word, had, MARK << 16 | 1u);
+      if (was == had) { had = MARK << 16; break; }
+      had = was;
+      if ((had >> 16) == MARK) { had = atomic_add_acq_rel(word, 1ull); break; }
+    }
+  }
+  const bool last = (unsigned)(had & 0xffffu) + 1 == n;
+  if (last) {
+    atomicExch(word, MARK << 16);
+    __threadfence();
+  }
+  return last;
+}
+
 // A warp's keys of a unit lie in NP pages (one, or two of 16 keys).  The window
 // holds, one entry a lane, what is to be known of the next 32 / NP units: pool
 // page, position of the first key, scales.  Looking up 32 entries costs the
