@@ -36,8 +36,13 @@ constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13;
 // registers after setmaxnreg: 2 x 192 + 80 + 48 = 512 of 512 (x 128 threads)
 constexpr int REG_SOFT = 192, REG_CONV = 80, REG_MISC = 48;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr float P_BIAS = 15.f;
-constexpr int V_DOWN = 4, V_LOWER = 80;      // as in the kernel for few rows
+// log2 of the factor on P, and how far a row's maximum may pass the reference of
+// its exponents before the reference follows: P stays below 2^15.
+constexpr float P_BIAS = 12.f, M_UP = 3.f;
+// V_DOWN: f16's smallest step 2^-24 is then 2^-35 of a tile's largest V.  The
+// accumulator's exponent is lowered by V_LOWER at most at once, as in the kernel
+// for few rows.
+constexpr int V_DOWN = 1, V_LOWER = 80;
 constexpr int METAS = 4;
 constexpr int MIN_SHARE = 4;                 // tiles of a share: a start and a join cost two
 
@@ -89,7 +94,7 @@ struct SmemC {
   static constexpr int OFF_V8 = OFF_K8 + BYTES8;
   static constexpr int OFF_META = OFF_V8 + BYTES8;
   static constexpr int OFF_BAR = (OFF_META + METAS * (int)sizeof(Meta) + 7) / 8 * 8;
-  static constexpr int NBAR = 2 + 4 + 4 * STAGES + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 + 4 + 4 * STAGES + 2 + 4 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;
   static constexpr uint32_t COL_O0 = 256;
@@ -163,8 +168,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   uint64_t* v_full = k_empty + STAGES;
   uint64_t* v_empty = v_full + STAGES;
   uint64_t* s_full = v_empty + STAGES;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
+  uint64_t* p_full = s_full + 2;            // by tile, half of its keys
+  uint64_t* o_done = p_full + 4;
   uint64_t* mma_done = o_done + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 4);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[2 * x], 4); mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&o_done[x], 1);
     }
     mbar_init(mma_done, 1);
@@ -278,18 +283,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       auto issue_pv = [&](int x, int t, int u, bool first, bool last) -> bool {
         const int st = t % STAGES;
         if (x == 0 && !mbar_wait(&v_full[st], (t / STAGES) & 1, abort_flag, c.err)) return false;
-        if (!mbar_wait(&p_full[x], u & 1, abort_flag, c.err)) return false;
-        tc_fence_after();
         const uint32_t sv = smem_u32(smem + L::OFF_V + st * L::TILE);
-        if (leader) {
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + 128 * x + 8 * k,
-                           make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, !first || k > 0);
-          mma_commit(&o_done[x]);
-          if (last) mma_commit(&v_empty[st]);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(&p_full[2 * x + half], u & 1, abort_flag, c.err)) return false;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = BN / 32 * half; k < BN / 32 * (half + 1); ++k)
+              mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + 128 * x + 8 * k,
+                             make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, !first || k > 0);
+            if (half) {
+              mma_commit(&o_done[x]);
+              if (last) mma_commit(&v_empty[st]);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         return true;
       };
       // each tile's next Q K^T follows its own P V, so the pipe has read P_X
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           F[0] = k0.x * f_row; F[1] = k0.y * f_row; F[2] = k0.z * f_row; F[3] = k0.w * f_row;
           F[4] = k1.x * f_row; F[5] = k1.y * f_row; F[6] = k1.z * f_row; F[7] = k1.w * f_row;
         }
-        float m_new = m;
+        float top_all = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           float a[16];
@@ -458,9 +468,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           top = fmax3(top, a[10], a[11]);
           top2 = fmax3(top2, a[12], a[13]);
           top = fmax3(top, a[14], a[15]);
-          m_new = fmaxf(m_new, fmaxf(top, top2) * F[g]);
+          top_all = fmaxf(top_all, fmaxf(top, top2) * F[g]);
         }
+        const float m_new = top_all > m + M_UP ? top_all : m;
         const float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
+        const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
         float l_new = 0.f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -482,36 +494,38 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
             l_new = fmaf(ls.x + ls.y, exp2i(-d), l_new);
           }
           tmem_st16(lane_base + col_s + 16 * g, pk);
-        }
-        const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
-        if (j > 0) {
-          ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
-          if (!ok) break;
-          tc_fence_after();
-          const float by = alpha * back;
-          if (__any_sync(0xffffffffu, by != 1.f)) {
+          if (g == 1 && j > 0) {
+            ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
+            if (!ok) break;
+            tc_fence_after();
+            const float by = alpha * back;
+            if (__any_sync(0xffffffffu, by != 1.f)) {
 #pragma unroll
-            for (int g = 0; g < D / 32; ++g) {
-              uint32_t ov[32];
-              tmem_ld32(lane_base + col_o + 32 * g, ov);
-              tmem_ld_wait();
-              reg_fence32(ov);
+              for (int og = 0; og < D / 32; ++og) {
+                uint32_t ov[32];
+                tmem_ld32(lane_base + col_o + 32 * og, ov);
+                tmem_ld_wait();
+                reg_fence32(ov);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = fmul2(make_float2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), make_float2(by, by));
-                ov[i] = __float_as_uint(y.x);
-                ov[i + 1] = __float_as_uint(y.y);
+                for (int i = 0; i < 32; i += 2) {
+                  const float2 y = fmul2(make_float2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), make_float2(by, by));
+                  ov[i] = __float_as_uint(y.x);
+                  ov[i + 1] = __float_as_uint(y.y);
+                }
+                tmem_st32(lane_base + col_o + 32 * og, ov);
               }
-              tmem_st32(lane_base + col_o + 32 * g, ov);
             }
           }
+          if (g & 1) {                       // P V of 64 keys may go
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * x + g / 2]);
+          }
         }
+        if (!ok) break;
         l = fmaf(alpha, l, l_new);
         m = m_new;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (ok && tiles > 0) ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
       tc_fence_after();
