@@ -73,11 +73,12 @@ struct Block {
   FA4_DEV int units() const { return r0 < rows ? max(nt, 1) : 0; }
 };
 
-// Scales of a 128-key tile, by groups of 16 keys.
+// Factors of a 128-key tile, by groups of 16 keys.
 struct alignas(16) Meta {
-  float kx[8];
-  int ev[8];                                 // V's exponents
-  int ev_max;
+  float kx[8];                               // K's scales
+  float vd[8], vu[8];                        // V's exponents against the accumulator's, and 2^-vd
+  float back;                                // what the accumulator's own change multiplies it with
+  int xo;                                    // its exponent
   uint32_t absent;                           // groups without a page
 };
 
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   uint64_t* v_full = k_empty + STAGES;
   uint64_t* v_empty = v_full + STAGES;
   uint64_t* s_full = v_empty + STAGES;
-  uint64_t* p_full = s_full + 2;            // by tile, half of its keys
+  uint64_t* p_full = s_full + 2;            // by tile: 96 keys, 32
   uint64_t* o_done = p_full + 4;
   uint64_t* mma_done = o_done + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       for (unsigned at = begin; ok && at < end;) {
         const Seg sg = segment(at);
         at = sg.next;
+        int xo = -127;
         for (int j = sg.t0; j < sg.t0 + sg.tiles; ++j, ++n) {
           // lane i < 8: group i of 16 keys; the first lane of a page copies it
           const int key = j * BN + 16 * (lane & 7);
@@ -225,11 +227,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = __shfl_sync(0xffffffffu, top, 0);
+          // the accumulator's exponent: at least the tile's largest, and not far
+          // above it
+          float back = 1.f;
+          if (top > -1000 && (top > xo || top < xo - V_DOWN)) {
+            const int to = j == sg.t0 ? top : max(top, xo - V_LOWER);
+            back = pow2_any(xo - to);
+            xo = to;
+          }
           const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane < 8) {
+            const int d = min(0, max(ev - xo, -100));
             m.kx[lane] = kx;
-            m.ev[lane] = ev;
-            if (lane == 0) { m.ev_max = top; m.absent = ~there & 0xffu; }
+            m.vd[lane] = (float)d;
+            m.vu[lane] = exp2i(-d);
+            if (lane == 0) { m.back = back; m.xo = xo; m.absent = ~there & 0xffu; }
           }
           __syncwarp();
           const bool copies = lane < 8 && pg >= 0 && ((16 * lane) & (c.page - 1)) == 0;
@@ -290,7 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int k = BN / 32 * half; k < BN / 32 * (half + 1); ++k)
+            for (int k = half ? 6 : 0; k < (half ? 8 : 6); ++k)
               mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + 128 * x + 8 * k,
                              make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, !first || k > 0);
             if (half) {
@@ -440,21 +453,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
             for (int i = 0; i < 32; ++i)
               if (32 * g + i >= left || ((absent >> (2 * g + i / 16)) & 1)) s[g][i] = -INFINITY;
         }
-        // exponent of V against the accumulator's
-        const int ev_max = meta.ev_max;
-        float back = 1.f;
-        if (ev_max > -1000 && (ev_max > xo || ev_max < xo - V_DOWN)) {
-          const int to = j == 0 ? ev_max : max(ev_max, xo - V_LOWER);
-          back = pow2_any(xo - to);
-          xo = to;
-        }
         // max by groups of 16 keys, each with its K scale
-        float F[8];
-        {
-          const float4 k0 = *reinterpret_cast<const float4*>(meta.kx), k1 = *reinterpret_cast<const float4*>(meta.kx + 4);
-          F[0] = k0.x * f_row; F[1] = k0.y * f_row; F[2] = k0.z * f_row; F[3] = k0.w * f_row;
-          F[4] = k1.x * f_row; F[5] = k1.y * f_row; F[6] = k1.z * f_row; F[7] = k1.w * f_row;
+        float F[8], add[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          *reinterpret_cast<float4*>(F + 4 * g) = *reinterpret_cast<const float4*>(meta.kx + 4 * g);
+          *reinterpret_cast<float4*>(add + 4 * g) = *reinterpret_cast<const float4*>(meta.vd + 4 * g);
         }
+        const float back = meta.back;
+        xo = meta.xo;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) F[g] *= f_row;
         float top_all = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
@@ -472,26 +481,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         }
         const float m_new = top_all > m + M_UP ? top_all : m;
         const float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) add[g] -= ref;
         const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
         float l_new = 0.f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          const float2 undo = *reinterpret_cast<const float2*>(meta.vu + 2 * g);
           uint32_t pk[16];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int gr = 2 * g + hf;
-            const int d = min(0, max(meta.ev[gr] - xo, -100));
-            const float Fg = F[gr], add = (float)d - ref;
             float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int k = 16 * hf + 2 * i;
-              const float2 e = ffma2(make_float2(s[g][k], s[g][k + 1]), make_float2(Fg, Fg), make_float2(add, add));
+              const float2 e = ffma2(make_float2(s[g][k], s[g][k + 1]), make_float2(F[gr], F[gr]), make_float2(add[gr], add[gr]));
               const float2 pp = make_float2(ex2_approx(e.x), ex2_approx(e.y));
               ls = fadd2(ls, pp);
               pk[8 * hf + i] = pack_f16x2(pp.x, pp.y);
             }
-            l_new = fmaf(ls.x + ls.y, exp2i(-d), l_new);
+            l_new = fmaf(ls.x + ls.y, hf ? undo.y : undo.x, l_new);
           }
           tmem_st16(lane_base + col_s + 16 * g, pk);
           if (g == 1 && j > 0) {
@@ -516,11 +526,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
               }
             }
           }
-          if (g & 1) {                       // P V of 64 keys may go
+          if (g >= 2) {                      // P V of 96 keys may go, of all
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * x + g / 2]);
+            if (lane == 0) mbar_arrive(&p_full[2 * x + g - 2]);
           }
         }
         if (!ok) break;
