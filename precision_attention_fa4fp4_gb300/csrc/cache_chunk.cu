@@ -5,19 +5,26 @@
 //
 // Bound by the tensor cores (4 d flop per row and key): tcgen05.  The query
 // heads of a kv head share its keys, so rows are (token, head of the group),
-// token major; one CTA takes 256 rows of a kv head as two tiles A and B, which
-// share every converted key tile.  16 warps:
+// token major; a block is 256 rows of a kv head as two tiles A and B, which share
+// every converted key tile (B is left out where it has no rows).  All blocks'
+// key tiles form a line that is cut into equal shares, one per SM; a block that
+// is cut leaves partials in the workspace, and the last CTA to do so joins them
+// (whole blocks instead of shares: 256 blocks on 152 SMs took two rounds, 270
+// against 257 us).  16 warps:
 //   0-3, 4-7  softmax of tile A, of tile B: one thread per row.  At the start it
 //             brings its row of q to f16 under a power of two (a largest
 //             magnitude in [2^7, 2^8): 2^-32 of it at most is lost); then exact
-//             online softmax, P to f16 under a factor 2^15 into tensor memory
-//             over the scores, o rescaled in tensor memory when the max grows.
+//             online softmax, P to f16 into tensor memory over the scores.  The
+//             reference of a row's exponents follows its maximum only when that
+//             has grown by 2^M_UP: o in tensor memory is rescaled in a few tiles
+//             instead of most (10 us of 257).
 //   8-11      conversion of the 128-key tiles: E4M3 -> f16 is exact, unscaled,
 //             from the staged bytes into the swizzled layout that the products
 //             read.
-//   12        issues the products (kind::f16): S_X = Q_X K^T, O_X += P_X V.
-//   13        looks the pages up and stages their bytes by bulk copies; writes
-//             the tile's scales for the softmax.
+//   12        issues the products (kind::f16): S_X = Q_X K^T, O_X += P_X V, the
+//             latter's first 96 keys while the last 32 are still in the making.
+//   13        looks the pages up, stages their bytes by bulk copies, and works
+//             the tile's factors out for the softmax.
 // K's page scale multiplies the scores (folded into the exponent's FMA), V's
 // goes into the exponent of P relative to the accumulator's own exponent, which
 // is at most V_DOWN above the tile's largest: half of P's smallest f16 step is
@@ -25,6 +32,14 @@
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).  Two f16 stages of
 // K and of V beside both query tiles leave room for one staged tile of bytes
 // each: the copy of tile j + 1 runs while tile j is multiplied.
+//
+// 2 x 1024 tokens over 8192, 32 / 8 heads of 128: 225 us, 1.15 PFLOP/s, 0.62 of
+// the measured cuBLAS rate.  Four fifths of that are the tiles' loop, 3300 clocks
+// for both tiles: a tile's own chain of softmax (2150) and products (1100), with
+// the other tile's in between; the tensor cores are busy in 2050 of them and
+// shared memory, from which they read, in 2500.  The rest are the starts and
+// ends of a share's two or three blocks.  Two threads a row (24 warps) shorten
+// the chain but add instructions: 294 us when one thread took 271.
 #include "cache_line.cuh"
 
 namespace fa4 {
@@ -44,7 +59,9 @@ constexpr float P_BIAS = 12.f, M_UP = 3.f;
 // for few rows.
 constexpr int V_DOWN = 1, V_LOWER = 80;
 constexpr int METAS = 4;
-constexpr int MIN_SHARE = 4;                 // tiles of a share: a start and a join cost two
+// Tiles of a share at least.  64 tokens over 8192, 32 / 8 heads: shares of 4
+// tiles 55 us, of 8 43 us; over 1024 they are 26 and 23 us.
+constexpr int MIN_SHARE = 8;
 
 // Row blocks of 256 of a kv head's rows.
 __host__ __device__ inline int row_blocks(int G, int T) { return (int)(((long long)G * T + 2 * BM - 1) / (2 * BM)); }
@@ -97,7 +114,8 @@ struct SmemC {
   static constexpr int OFF_BAR = (OFF_META + METAS * (int)sizeof(Meta) + 7) / 8 * 8;
   static constexpr int NBAR = 2 + 4 + 4 * STAGES + 2 + 4 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int OFF_SEG = (OFF_MISC + 16 + 15) / 16 * 16;    // 64 bytes a softmax warp
+  static constexpr int BYTES = OFF_SEG + 8 * 64 + 1024;
   static constexpr uint32_t COL_O0 = 256;
   static_assert(COL_O0 + 2 * D <= TMEM_COLS, "tensor memory");
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -404,21 +422,37 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     // barriers of every join.
     bool ok = true;
     int n = 0, m0 = 0;                       // tiles so far of X, of the CTA
-    for (unsigned at = begin; at < end;) {
-      const Seg sg = segment(at);
-      const bool cut = shares.of(sg.item) != shares.of(sg.item + sg.all - 1);
-      const int tiles = x < sg.nx ? sg.tiles : 0;
-      const int r = sg.r0 + mate;
-      const bool valid = r < sg.rows;
-      const int t = valid ? r / G : 0, gg = valid ? r - t * G : 0;
-      const long long orow = ((long long)sg.b * p.Hq + sg.h * G + gg) * p.T + t;
-      const int vis = !valid ? 0 : p.causal ? max(0, min(sg.len, sg.len - sg.q_len + t + 1)) : sg.len;
+    // What is needed again after the tiles waits in shared memory: the tiles'
+    // loop needs the registers.
+    enum { E_B, E_H, E_R0, E_ROWS, E_NX, E_TILES, E_FIRST, E_C0, E_PARTS, E_ODD, E_NEXT };
+    volatile unsigned* rec = reinterpret_cast<volatile unsigned*>(smem + L::OFF_SEG + 64 * warp);
+    for (unsigned at = begin; at < end; at = rec[E_NEXT]) {
+      int tiles, left0;                      // left0: keys that the row sees from the first tile on
+      const __nv_bfloat16* src = nullptr;
+      {
+        const Seg sg = segment(at);
+        tiles = x < sg.nx ? sg.tiles : 0;
+        const int r = sg.r0 + mate;
+        const bool valid = r < sg.rows;
+        const int t = valid ? r / G : 0, gg = valid ? r - t * G : 0;
+        const long long orow = ((long long)sg.b * p.Hq + sg.h * G + gg) * p.T + t;
+        const int vis = !valid ? 0 : p.causal ? max(0, min(sg.len, sg.len - sg.q_len + t + 1)) : sg.len;
+        left0 = vis - sg.t0 * BN;
+        if (valid) src = reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D;
+        const unsigned c0 = shares.of(sg.item), c1 = shares.of(sg.item + sg.all - 1);
+        __syncwarp();
+        if (lane == 0) {
+          rec[E_B] = sg.b; rec[E_H] = sg.h; rec[E_R0] = sg.r0; rec[E_ROWS] = sg.rows; rec[E_NX] = sg.nx;
+          rec[E_TILES] = sg.tiles; rec[E_FIRST] = at == begin; rec[E_C0] = c0; rec[E_PARTS] = c1 - c0 + 1;
+          rec[E_ODD] = shares.begin(c0) != sg.item; rec[E_NEXT] = sg.next;
+        }
+        __syncwarp();
+      }
 
       // the row of q: largest magnitude, then f16 under a power of two
       float f_row = 0.f;
       if (tiles > 0) {
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + orow * D;
-        f_row = p.c2 * exp2i(store_query_row<D, D / 8>(smem + L::OFF_Q + x * L::TILE, rt, valid ? src : nullptr));
+        f_row = p.c2 * exp2i(store_query_rows<D>(smem + L::OFF_Q + x * L::TILE, 32 * quad, src));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
@@ -445,7 +479,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         }
         const Meta& meta = metas[(m0 + j) % METAS];
         const uint32_t absent = meta.absent;
-        const int left = vis - (sg.t0 + j) * BN;
+        const int left = left0 - j * BN;
         if (__any_sync(0xffffffffu, left < BN) || absent) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -541,9 +575,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       tc_fence_after();
       // a row without keys: whatever the accumulator holds counts for nothing
       const bool none = l == 0.f;
+      const int nx = (int)rec[E_NX], r0 = (int)rec[E_R0], rows = (int)rec[E_ROWS], sb = (int)rec[E_B], sh = (int)rec[E_H];
+      const unsigned parts = rec[E_PARTS], c0 = rec[E_C0];
+      const bool cut = parts > 1, valid = r0 + mate < rows;
+      auto out_row = [&](int r) -> long long {
+        return ((long long)sb * p.Hq + sh * G + r % G) * p.T + r / G;
+      };
+      const long long orow = valid ? out_row(r0 + mate) : 0;
       float4* part = reinterpret_cast<float4*>(p.part + (gridDim.x * 8 + 15) / 16 * 16);
-      float4* slot = part + (size_t)(2 * blockIdx.x + (at == begin ? 0 : 1)) * (PartC<D>::FLOATS / 4);
-      if (ok && x < sg.nx) {
+      float4* slot = part + (size_t)(2 * blockIdx.x + (rec[E_FIRST] ? 0 : 1)) * (PartC<D>::FLOATS / 4);
+      if (ok && x < nx) {
         const float inv = none ? 0.f : 1.f / l, unit = pow2_any(xo);
 #pragma unroll 1
         for (int g = 0; g < D / 32; ++g) {
@@ -575,50 +616,74 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         // The block's parts meet: whoever is the last to have written one joins
         // them.  The barrier and the release order the CTA's part before its
         // arrival, the acquire the others' parts before the join.
-        const unsigned c0 = shares.of(sg.item), parts = shares.of(sg.item + sg.all - 1) - c0 + 1;
-        const int odd = shares.begin(c0) != sg.item;
+        const unsigned odd = rec[E_ODD];
         named_bar(1, 2 * BM);
         if (threadIdx.x == 0) *last_one = !*abort_flag && marked_arrive(reinterpret_cast<unsigned long long*>(p.part) + c0, parts);
         named_bar(1, 2 * BM);
-        if (*last_one && valid) {
+        // all eight warps: rows of two tiles, or the two halves of one tile's
+        // dimensions; four parts' words in flight
+        const int row = nx == 2 ? mate : rt, jr = r0 + row;
+        if (*last_one && jr < rows) {
           auto slot_of = [&](unsigned i) { return part + (size_t)(2 * (c0 + i) + (i == 0 ? odd : 0)) * (PartC<D>::FLOATS / 4); };
           auto stat = [&](unsigned i, int which) {
-            return __ldcg(reinterpret_cast<const float*>(slot_of(i)) + 2 * BM * (D + which) + mate);
+            return __ldcg(reinterpret_cast<const float*>(slot_of(i)) + 2 * BM * (D + which) + row);
           };
           float mt = -INFINITY, lt = 0.f;
-          for (unsigned i = 0; i < parts; ++i) mt = fmaxf(mt, stat(i, 0));
-          for (unsigned i = 0; i < parts; ++i) {
-            const float li = stat(i, 1);
-            if (li != 0.f) lt = fmaf(li, ex2_approx(stat(i, 0) - mt), lt);
+#pragma unroll 1
+          for (unsigned i0 = 0; i0 < parts; i0 += 4) {
+            float mi[4], li[4], mx = mt;
+#pragma unroll
+            for (unsigned k = 0; k < 4; ++k) {
+              mi[k] = stat(min(i0 + k, parts - 1), 0);
+              li[k] = i0 + k < parts ? stat(i0 + k, 1) : 0.f;
+            }
+#pragma unroll
+            for (unsigned k = 0; k < 4; ++k) mx = fmaxf(mx, mi[k]);
+            if (lt != 0.f) lt *= ex2_approx(mt - mx);
+            mt = mx;
+#pragma unroll
+            for (unsigned k = 0; k < 4; ++k)
+              if (li[k] != 0.f) lt = fmaf(li[k], ex2_approx(mi[k] - mt), lt);
           }
           const float inv = lt == 0.f ? 0.f : 1.f / lt;
+          const long long to = out_row(jr);
+          const int from_g = nx == 2 ? 0 : x * (D / 64), to_g = nx == 2 ? D / 32 : from_g + D / 64;
 #pragma unroll 1
-          for (int g = 0; g < D / 32; ++g) {
+          for (int g = from_g; g < to_g; ++g) {
             float y[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = 0.f;
-            for (unsigned i = 0; i < parts; ++i) {
-              const float4* from = slot_of(i) + 16 * g * BM + mate;
-              const float li = stat(i, 1), w = li == 0.f ? 0.f : li * inv * ex2_approx(stat(i, 0) - mt);
-              float4 z[8];
+#pragma unroll 1
+            for (unsigned i0 = 0; i0 < parts; i0 += 4) {
+              float4 z[4][8];
+              float w[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = __ldcg(from + e * 2 * BM);
-              if (w == 0.f) continue;
+              for (unsigned k = 0; k < 4; ++k) {
+                const unsigned i = min(i0 + k, parts - 1);
+                const float4* from = slot_of(i) + 16 * g * BM + row;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                y[4 * e] = fmaf(w, z[e].x, y[4 * e]);
-                y[4 * e + 1] = fmaf(w, z[e].y, y[4 * e + 1]);
-                y[4 * e + 2] = fmaf(w, z[e].z, y[4 * e + 2]);
-                y[4 * e + 3] = fmaf(w, z[e].w, y[4 * e + 3]);
+                for (int e = 0; e < 8; ++e) z[k][e] = __ldcg(from + e * 2 * BM);
+                const float li = stat(i, 1);
+                w[k] = li == 0.f || i0 + k >= parts ? 0.f : li * inv * ex2_approx(stat(i, 0) - mt);
+              }
+#pragma unroll
+              for (unsigned k = 0; k < 4; ++k) {
+                if (w[k] == 0.f) continue;             // 0 * inf
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  y[4 * e] = fmaf(w[k], z[k][e].x, y[4 * e]);
+                  y[4 * e + 1] = fmaf(w[k], z[k][e].y, y[4 * e + 1]);
+                  y[4 * e + 2] = fmaf(w[k], z[k][e].z, y[4 * e + 2]);
+                  y[4 * e + 3] = fmaf(w[k], z[k][e].w, y[4 * e + 3]);
+                }
               }
             }
-            store_bf16_32(reinterpret_cast<__nv_bfloat16*>(p.o) + orow * D + 32 * g, y);
+            store_bf16_32(reinterpret_cast<__nv_bfloat16*>(p.o) + to * D + 32 * g, y);
           }
-          if (p.lse) p.lse[orow] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
+          if (p.lse && from_g == 0) p.lse[to] = lt == 0.f ? -INFINITY : fmaf(mt - P_BIAS, 0.69314718f, logf(lt));
         }
       }
-      m0 += sg.tiles;
-      at = sg.next;
+      m0 += (int)rec[E_TILES];
     }
   }
   tc_fence_before();

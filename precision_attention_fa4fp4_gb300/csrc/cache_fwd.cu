@@ -36,9 +36,9 @@
 // exponent of P, relative to the accumulator's own exponent.
 //
 // Roundings: q to f16 under a power of two (2^-32 of the row's largest); P to
-// f16 under a factor 2^15 and V's relative exponent (2^-12 of P, or 2^-36 of the
+// f16 under a factor 2^15 and V's relative exponent (2^-11 of P, or 2^-36 of the
 // largest V of the 32 keys if that is more), for FP32 output as a sum of two f16
-// (2^-23, or the same 2^-36).  The normalizer sums the FP32 values of P.
+// (2^-22, or the same 2^-36).  The normalizer sums the FP32 values of P.
 #include "cache_line.cuh"
 
 namespace fa4 {
@@ -53,7 +53,14 @@ constexpr float P_BIAS = 15.f;
 // is bounded, so that the accumulator stays below 2^(40 + 80) (its terms: 2^15 *
 // 448, fewer than 2^17 of them a warp).
 constexpr int V_DOWN = 4, V_LOWER = 80;
-constexpr int MANY_ROWS = 48;
+// Rows of a kv head above which the kernel for many rows takes over.  It takes
+// the same time for 1 to 128 of them, this one in proportion to blocks of 16.
+// Keys x sequences, heads of 128, 8 kv heads, us here / there:
+//   2048 x 16:  64 rows 60 / 59,  128 rows 107 / 51,  256 rows 195 / 63
+//   8192 x 1:   64 rows 25 / 32,  128 rows 35 / 32,   256 rows 55 / 43
+//   1024 x 1:   64 rows 15 / 22,  256 rows 18 / 23 (the price of one rule)
+// heads of 64, 4096 x 16: 64 rows 64 / 69, 96 rows 90 / 69.
+constexpr int MANY_ROWS = 64;
 
 // Resident CTAs by registers, and the steps in flight that fill the shared
 // memory they leave.
@@ -631,7 +638,6 @@ cudaError_t launch(const CacheFwdParams& p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-// Whether the kernel for many rows is the faster one.
 static bool many_rows(int Hq, int Hkv, int T) {
   return (long long)(Hq / Hkv) * T > MANY_ROWS;
 }

@@ -296,46 +296,48 @@ FA4_DEV void store16(uint8_t* tile, int row, int part, const uint4& x) {
   *reinterpret_cast<uint4*>(at + (((u + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
 }
 
-// A row of q (nullptr: zeros) as f16 under a power of two into row `row` of such
-// a tile: the largest magnitude comes into [2^7, 2^8), as in QRaw.  Returns the
-// exponent that undoes it.  HALF words of 16 bytes are held at a time.
-template <int D, int HALF>
-FA4_DEV int store_query_row(uint8_t* tile, int row, const __nv_bfloat16* src_row) {
-  const uint4* src = reinterpret_cast<const uint4*>(src_row);
-  uint4 w[HALF];
-  uint32_t amax = 0;
+// Each lane's row of q (nullptr: zeros) as f16 under a power of two into rows
+// row0..+31 of such a tile (whole warp): the largest magnitude comes into
+// [2^7, 2^8), as in QRaw.  Returns the exponent that undoes it.  D / 8 lanes
+// read a row, whole lines at a time.  A loop: the code runs once or twice in a
+// kernel's life, and straight-line code waits for its own instructions then.
+template <int D>
+FA4_DEV int store_query_rows(uint8_t* tile, int row0, const __nv_bfloat16* mine) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR, AT_ONCE = 32 / RPI;
+  const int lane = threadIdx.x % 32, word = lane % LPR;
+  int e_mine = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 32; i0 += RPI * AT_ONCE) {
+    uint4 w[AT_ONCE];
 #pragma unroll
-  for (int p = D / 8 - HALF; p >= 0; p -= HALF) {    // ends with the first words in registers
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const unsigned long long src =
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), i0 + RPI * i + lane / LPR);
+      w[i] = src ? reinterpret_cast<const uint4*>(src)[word] : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < HALF; ++i) w[i] = src ? src[p + i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < HALF; ++i) {
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int row = i0 + RPI * i + lane / LPR;
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t amax = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) amax = max(amax, max((u[k] << 16) & 0x7fffffffu, u[k] & 0x7fff0000u));
-    }
-  }
-  const int E = (int)(amax >> 23);
-  const int e = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
-  const float down = exp2i(-e);
 #pragma unroll
-  for (int p = 0; p < D / 8; p += HALF) {
-    if (p > 0) {
-#pragma unroll
-      for (int i = 0; i < HALF; ++i) w[i] = src ? src[p + i] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < HALF; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      for (int o = 1; o < LPR; o *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int E = (int)(amax >> 23);
+      const int e = (E == 0 || E == 255) ? 0 : max(-120, min(120, E - 134));
+      const float down = exp2i(-e);
       uint32_t z[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         z[k] = pack_f16x2(__uint_as_float(u[k] << 16) * down, __uint_as_float(u[k] & 0xffff0000u) * down);
-      *reinterpret_cast<uint4*>(tile + (p + i) / 8 * F16_CHUNK + row * 128 + ((((p + i) % 8) ^ (row & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(tile + word / 8 * F16_CHUNK + (row0 + row) * 128 + ((word % 8 ^ (row & 7)) << 4)) =
           make_uint4(z[0], z[1], z[2], z[3]);
+      const int theirs = __shfl_sync(0xffffffffu, e, lane % RPI * LPR);
+      if (lane / RPI == i0 / RPI + i) e_mine = theirs;
     }
   }
-  return e;
+  return e_mine;
 }
 
 // lse in log2 units as a float and the factor that makes up for its rounding;

@@ -395,9 +395,9 @@ bool cache_weigh_fits(int B, int Hkv, int page, int max_pages) {
 
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
+  if (rows >= WEIGH_MANY) return launch_cache_weigh_rows(p, st);   // as the host decided on the tensor map
   if (rows <= 8) return p.c.d == 128 ? launch_few<128, 1>(p, st) : launch_few<64, 1>(p, st);
   if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
-  if (rows >= WEIGH_MANY) return launch_cache_weigh_rows(p, st);
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const dim3 grid((unsigned)((cap + UNIT - 1) / UNIT), (unsigned)p.c.Hkv, (unsigned)p.c.B);
   return launch_next(p.c.d == 128 ? cache_weigh_rows_kernel<128> : cache_weigh_rows_kernel<64>, grid, 32 * NW, 0, st, p);
