@@ -189,14 +189,29 @@ FA4_DEV uint32_t e4m3_unordered(uint32_t x) {
   return x ^ (neg * 0x7fu | 0x80808080u);
 }
 
-// Four codes times a power of two, rounded to nearest even (0 stays 0 whatever
-// the factor).
-FA4_DEV uint32_t e4m3_times(uint32_t x, float f) {
-  const uint32_t a = e4m3x2_to_f16x2(x), z = e4m3x2_hi_to_f16x2(x);
-  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z));
-  return pack_e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
+// Least and greatest by 16-bit halves (one instruction each; by bytes they are
+// made of several).  A half's high byte is then right whatever the low one is.
+FA4_DEV uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+FA4_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest magnitude among codes, in two words whose high bytes hold it.
+struct MaxCode {
+  uint32_t odd = 0, even = 0;
+  FA4_DEV void add(uint32_t x) {
+    const uint32_t m = x & 0x7f7f7f7fu;
+    odd = max_u16x2(odd, m);
+    even = max_u16x2(even, m << 8);
+  }
+  FA4_DEV uint32_t halves() const { return max_u16x2(odd, even); }
+  static FA4_DEV uint32_t of(uint32_t halves) { return max(halves >> 24, (halves >> 8) & 0xffu); }
+};
 
 // Launches a kernel that begins with grid_start and grid_wait.
 template <class P>

@@ -152,6 +152,15 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
 
 constexpr int NT2 = 128;
 
+// Four codes times a power of two, rounded to nearest even (0 stays 0 whatever
+// the factor).
+FA4_DEV uint32_t e4m3_times(uint32_t x, float f) {
+  const uint32_t a = e4m3x2_to_f16x2(x), z = e4m3x2_hi_to_f16x2(x);
+  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z));
+  return pack_e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
+}
+
 // The least e with e4m3(code) <= 448 * 2^e for a magnitude 1..0x7e (448 =
 // 1.75 * 2^8): normal codes E - 15, plus one above a significand of 1.75;
 // subnormal codes m * 2^-9.
@@ -215,9 +224,9 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint4 x = w[kv][i];
-      uint32_t a = __vmaxu4(__vmaxu4(x.x & 0x7f7f7f7fu, x.y & 0x7f7f7f7fu), __vmaxu4(x.z & 0x7f7f7f7fu, x.w & 0x7f7f7f7fu));
-      a = __vmaxu4(a, a >> 16);
-      const uint32_t mag = max(a & 0xffu, (a >> 8) & 0xffu);
+      MaxCode most;
+      most.add(x.x); most.add(x.y); most.add(x.z); most.add(x.w);
+      const uint32_t mag = MaxCode::of(most.halves());
       if (mag) X[kv] = max(X[kv], xs[kv][i] + code_exp(mag));
     }
     X[kv] = __reduce_max_sync(0xffffffffu, X[kv]);
@@ -230,7 +239,10 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
     for (int i = 0; i < NT2 / 32; ++i) X[kv] = max(X[kv], s_x[kv][i]);
 
   const long long ph = (long long)dst * c.Hkv + h;
-  uint32_t lo[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu}, hi[4] = {0u, 0u, 0u, 0u};
+  // odd bytes, then even ones in the odd place
+  uint32_t lo2[2][4], hi2[2][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) { lo2[j / 4][j % 4] = 0xffffffffu; hi2[j / 4][j % 4] = 0u; }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     uint4* to = reinterpret_cast<uint4*>((kv ? c.v : c.k) + ph * P * D) + part;
@@ -248,13 +260,21 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t o = e4m3_ordered(u[j]);
-          lo[j] = __vminu4(lo[j], o);
-          hi[j] = __vmaxu4(hi[j], o);
+          lo2[0][j] = min_u16x2(lo2[0][j], o);
+          hi2[0][j] = max_u16x2(hi2[0][j], o);
+          lo2[1][j] = min_u16x2(lo2[1][j], o << 8);
+          hi2[1][j] = max_u16x2(hi2[1][j], o << 8);
         }
       }
     }
   }
   if (threadIdx.x < 2) (threadIdx.x ? c.vs : c.ks)[ph] = (uint8_t)(X[threadIdx.x] + 127);
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    lo[j] = (lo2[0][j] & 0xff00ff00u) | ((lo2[1][j] >> 8) & 0x00ff00ffu);
+    hi[j] = (hi2[0][j] & 0xff00ff00u) | ((hi2[1][j] >> 8) & 0x00ff00ffu);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
     for (int first = 16 * warp; first < m; first += 16 * (NT / 32)) {
       look(first + 16 * (NT / 32));
       float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t big[2] = {0, 0};
+      MaxCode big[2];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t u[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
@@ -201,16 +201,16 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
           if (g < 2) wb = *reinterpret_cast<const uint2*>(&s_b[g][32 * i + 8 * t4 + 2 * w]);
           mma_16816(w % 2 ? acc2 : acc, e4m3x2_to_f16x2(u[w]), e4m3x2_to_f16x2(v[w]), e4m3x2_hi_to_f16x2(u[w]),
                     e4m3x2_hi_to_f16x2(v[w]), wb.x, wb.y);
-          big[0] = __vmaxu4(big[0], u[w] & 0x7f7f7f7fu);
-          big[1] = __vmaxu4(big[1], v[w] & 0x7f7f7f7fu);
+          big[0].add(u[w]);
+          big[1].add(v[w]);
         }
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        uint32_t z = __vmaxu4(big[r], __shfl_xor_sync(0xffffffffu, big[r], 1));
-        z = __vmaxu4(z, __shfl_xor_sync(0xffffffffu, z, 2));
-        z = __vmaxu4(z, z >> 16);
-        z = max(z & 0xffu, (z >> 8) & 0xffu);
+        uint32_t z = big[r].halves();
+        z = max_u16x2(z, __shfl_xor_sync(0xffffffffu, z, 1));
+        z = max_u16x2(z, __shfl_xor_sync(0xffffffffu, z, 2));
+        z = MaxCode::of(z);
         const int pi = first + g + 8 * r;
         if (t4 == 0 && pi < m) {
           const float f = e8m0_value(sc[r]);
