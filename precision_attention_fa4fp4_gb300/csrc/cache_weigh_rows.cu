@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __g
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
 
-  float sum = 0.f;
+  float sum = 0.f, before = 0.f;             // of a key; what it had
+  bool there = false;                        // its page
   if (warp == W_MMA) {
     // -------------------------------------------------------------- products
     if (nt > 0) {
@@ -217,22 +218,23 @@ __global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __g
     constexpr int PARTS = D / 16, RSTEP = 128 / PARTS;
     const int tid = threadIdx.x - 32 * W_CONV;
     const int part = tid % PARTS;
+    constexpr int N = 128 / RSTEP;
+    int pg[N];                               // all rows' loads in flight, one after the other's pages
 #pragma unroll
-    for (int i0 = 0; i0 < 128 / RSTEP; i0 += 4) {
-      uint4 x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = tid / PARTS + (i0 + i) * RSTEP, key = key0 + row;
-        int pg = -1;
-        if (key < len) pg = cache_page(c, c.table, b, key / c.page);
-        x[i] = make_uint4(0, 0, 0, 0);               // what is not there is zero
-        if (pg >= 0)
-          x[i] = reinterpret_cast<const uint4*>(c.k + (((long long)pg * c.Hkv + h) * c.page + key % c.page) * D)[part];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store16<D>(smem + L::OFF_K, tid / PARTS + (i0 + i) * RSTEP, part, x[i]);
+    for (int i = 0; i < N; ++i) {
+      const int key = key0 + tid / PARTS + i * RSTEP;
+      pg[i] = key < len ? cache_page(c, c.table, b, key / c.page) : -1;
     }
+    uint4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int key = key0 + tid / PARTS + i * RSTEP;
+      x[i] = make_uint4(0, 0, 0, 0);         // what is not there is zero
+      if (pg[i] >= 0)
+        x[i] = reinterpret_cast<const uint4*>(c.k + (((long long)pg[i] * c.Hkv + h) * c.page + key % c.page) * D)[part];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) store16<D>(smem + L::OFF_K, tid / PARTS + i * RSTEP, part, x[i]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(k_full);
@@ -243,7 +245,9 @@ __global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __g
     float kx = 0.f;
     if (key < len) {
       const int pg = cache_page(c, c.table, b, key / c.page);
-      if (pg >= 0) kx = e8m0_value(c.ks[(long long)pg * c.Hkv + h]);
+      there = pg >= 0;
+      if (there) kx = e8m0_value(c.ks[(long long)pg * c.Hkv + h]);
+      if (half == 0) before = p.w_in[((long long)b * c.Hkv + h) * c.max_pages * c.page + key];
     }
     const float2 kx2 = make_float2(kx, kx);
     const uint32_t base = tbase + ((uint32_t)(32 * quad) << 16) + 64 * half;
@@ -299,9 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __g
   if (warp < 4 && key < len) {
     const long long at = ((long long)b * c.Hkv + h) * c.max_pages * c.page + key;
     // a page that is not there adds nothing
-    const int pg = c.table[(long long)b * c.max_pages + key / c.page];
-    const float add = pg >= 0 && pg < c.num_pages ? sum + s_sum[threadIdx.x] : 0.f;
-    if (!*abort_flag) p.w_out[at] = p.w_in[at] + add;
+    if (!*abort_flag) p.w_out[at] = before + (there ? sum + s_sum[threadIdx.x] : 0.f);
   }
 }
 
