@@ -121,9 +121,9 @@ def test_refusals_of_each_call(fa):
     assert c["weigh"](good, lse=None) == INVALID
     assert c["weigh"](good, w=None) == INVALID
     assert c["weigh"](good, out=ODD) == ALIGN
-    need = fa.cache_weigh_workspace_bytes(1, 4, 2, 32, 128)
-    assert c["weigh"](good, T=32) == WS and c["weigh"](good, T=32, ws=P, wb=need - 1) == WS
-    assert c["weigh"](good, T=32, ws=odd4, wb=need) == ALIGN
+    need = fa.cache_weigh_workspace_bytes(1, 4, 2, 64, 128)
+    assert c["weigh"](good, T=64) == WS and c["weigh"](good, T=64, ws=P, wb=need - 1) == WS
+    assert c["weigh"](good, T=64, ws=odd4, wb=need) == ALIGN
     assert c["evict"](good, budget=0) == INVALID
     assert c["evict"](good, budget=129) == INVALID        # more than two pages of 64 hold
     assert c["evict"](good, recent=101) == INVALID
