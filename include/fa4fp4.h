@@ -365,8 +365,9 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_append(const fa4fp4_cache* cache, const vo
  * written.  The products are exact in the codes, the sums FP32.  P is rounded
  * to f16 (half a step: 2^-11) under a power of two that takes V's page scales
  * in, so that a P far below the largest V of its 128 keys is off by 2^-36 of
- * that V at most; f32 output takes P as a sum of two f16 (2^-22).  The result
- * does not depend on anything but the arguments.  `workspace`: at least
+ * that V at most; f32 output takes P as a sum of two f16 (2^-22).  Scores up to
+ * 2^22 in magnitude; beyond, the rounding of their maximum takes P out of its
+ * range.  The result does not depend on anything but the arguments.  `workspace`: at least
  * fa4fp4_cache_fwd_workspace_bytes(...) bytes of device memory
  * (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs. */
 FA4FP4_API size_t fa4fp4_cache_fwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page, int max_pages,

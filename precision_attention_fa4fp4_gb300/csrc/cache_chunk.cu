@@ -151,15 +151,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
   if (blockIdx.x >= n_shares) return;
   const Shares shares(total, n_shares);
   const unsigned begin = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
-  // the part of a row block of a kv head that starts at unit `at` (whole warp)
+  // the part of a row block of a kv head that starts at unit `at` (whole warp);
+  // i, seq0: of the part before it
   struct Seg {
     int b, h, r0, rows, len, q_len, t0, tiles, nx;
     unsigned item, all;                      // the row block's first unit, its units
     unsigned next;                           // where the next part starts
   };
-  auto segment = [&](unsigned at) -> Seg {
-    int i = 0;
-    unsigned seq0 = 0;
+  auto segment = [&](unsigned at, int& i, unsigned& seq0) -> Seg {
     line_find(blocks, units, at, i, seq0);
     const Block k(p, G, RB, i);
     Seg g;
@@ -224,10 +223,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     if (warp == W_LOAD) {
       // ---------------------------------------------------------- pages
       const int log_p = 31 - __clz(c.page);
+      int li = 0;
+      unsigned lseq = 0;
       int issued = 0, n = 0;                 // n: tiles so far
       bool ok = true;
       for (unsigned at = begin; ok && at < end;) {
-        const Seg sg = segment(at);
+        const Seg sg = segment(at, li, lseq);
         at = sg.next;
         int xo = -127;
         for (int j = sg.t0; j < sg.t0 + sg.tiles; ++j, ++n) {
@@ -335,9 +336,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       };
       // each tile's next Q K^T follows its own P V, so the pipe has read P_X
       // before it overwrites S_X
+      int li = 0;
+      unsigned lseq = 0;
       int n = 0, nb = 0, pa = 0, pb = 0;     // tiles and parts so far, those of B among them
       for (unsigned at = begin; ok && at < end;) {
-        const Seg sg = segment(at);
+        const Seg sg = segment(at, li, lseq);
         at = sg.next;
         if (sg.tiles == 0) continue;
         const bool two = sg.nx == 2;
@@ -365,10 +368,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     constexpr int RSTEP = 128 / PARTS;       // rows at once
     const int tid = threadIdx.x - 32 * W_CONV;
     const int part = tid % PARTS, row0 = tid / PARTS;
+    int li = 0;
+    unsigned lseq = 0;
     int n = 0;
     bool ok = true;
     for (unsigned at = begin; ok && at < end;) {
-      const Seg sg = segment(at);
+      const Seg sg = segment(at, li, lseq);
       at = sg.next;
       for (int j = sg.t0; ok && j < sg.t0 + sg.tiles; ++j, ++n) {
         const int st = n % STAGES;
@@ -424,13 +429,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
     int n = 0, m0 = 0;                       // tiles so far of X, of the CTA
     // What is needed again after the tiles waits in shared memory: the tiles'
     // loop needs the registers.
-    enum { E_B, E_H, E_R0, E_ROWS, E_NX, E_TILES, E_FIRST, E_C0, E_PARTS, E_ODD, E_NEXT };
+    enum { E_B, E_H, E_R0, E_ROWS, E_NX, E_TILES, E_FIRST, E_C0, E_PARTS, E_ODD, E_NEXT, E_I, E_SEQ0 };
     volatile unsigned* rec = reinterpret_cast<volatile unsigned*>(smem + L::OFF_SEG + 64 * warp);
+    if (lane == 0) { rec[E_I] = 0; rec[E_SEQ0] = 0; }
+    __syncwarp();
     for (unsigned at = begin; at < end; at = rec[E_NEXT]) {
       int tiles, left0;                      // left0: keys that the row sees from the first tile on
       const __nv_bfloat16* src = nullptr;
       {
-        const Seg sg = segment(at);
+        int li = (int)rec[E_I];
+        unsigned lseq = rec[E_SEQ0];
+        const Seg sg = segment(at, li, lseq);
         tiles = x < sg.nx ? sg.tiles : 0;
         const int r = sg.r0 + mate;
         const bool valid = r < sg.rows;
@@ -445,6 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           rec[E_B] = sg.b; rec[E_H] = sg.h; rec[E_R0] = sg.r0; rec[E_ROWS] = sg.rows; rec[E_NX] = sg.nx;
           rec[E_TILES] = sg.tiles; rec[E_FIRST] = at == begin; rec[E_C0] = c0; rec[E_PARTS] = c1 - c0 + 1;
           rec[E_ODD] = shares.begin(c0) != sg.item; rec[E_NEXT] = sg.next;
+          rec[E_I] = li; rec[E_SEQ0] = lseq;
         }
         __syncwarp();
       }

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
   // a sequence's stretch of the line: parts, or units
   auto stretch = [&](unsigned u) -> unsigned { return (cut > 1 ? (u + cut - 1) / cut : u) * ln.nb; };
   const Shares shares(total, workers(total, gridDim.x));
-  unsigned at, end, seq0;
+  unsigned at, end, seq0 = 0;
   if (cut) {
     at = blockIdx.x;
     end = at + 1;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     end = shares.begin(blockIdx.x + 1);
   }
   const unsigned begin = at;
-  int b;
+  int b = 0;
   if (!line_find(c.B, [&](int i) -> unsigned { return stretch(lane_units(i)); }, at, b, seq0))
     return;                                        // more CTAs than parts
   int units = seq_units(p, b);

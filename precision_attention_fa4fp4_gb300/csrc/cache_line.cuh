@@ -44,12 +44,12 @@ FA4_DEV unsigned line_total(int B, F units) {
 }
 
 // The sequence b that holds unit `at` of the line and its first unit seq0
-// (whole warp).  Returns false if the line ends before (it does not).
+// (whole warp), looked for from the given b and seq0 on (0 and 0, or an earlier
+// answer).  Returns false if the line ends before.
 template <class F>
 FA4_DEV bool line_find(int B, F units, unsigned at, int& b, unsigned& seq0) {
   const int lane = threadIdx.x % 32;
-  seq0 = 0;
-  for (int base = 0; base < B; base += 32) {
+  for (int base = b; base < B; base += 32) {
     const unsigned mine = base + lane < B ? units(base + lane) : 0;
     unsigned inc = mine;
 #pragma unroll

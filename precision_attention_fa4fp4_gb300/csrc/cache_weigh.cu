@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
   if (blockIdx.x >= ctas) return;
   const Shares shares(total, ctas);
   const unsigned end = shares.begin(blockIdx.x + 1);
-  unsigned at = shares.begin(blockIdx.x), seq0;
-  int b;
+  unsigned at = shares.begin(blockIdx.x), seq0 = 0;
+  int b = 0;
   if (!line_find(c.B, seq, at, b, seq0)) return;
 
   bool ok = true;

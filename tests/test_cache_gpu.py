@@ -267,6 +267,29 @@ def test_fwd_chunk_cut(d, page, H, G, T, causal):
     fa.sync_status()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_fwd_chunk_many_sequences(causal):
+    """More sequences and blocks of rows than a warp looks up at once, with and
+    without queries, shorter and longer than their queries."""
+    fa = require_gpu()
+    d, page, H, G, T, B = 64, 32, 2, 8, 40, 150
+    g = torch.Generator().manual_seed(72)
+    lens = torch.randint(0, 300, (B,), generator=g).tolist()
+    q_lens = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    q_lens[40:110] = [0] * 70
+    lens[45] = 0
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=73)
+    q = queries(B, H * G, T, d, 74)
+    ql = torch.tensor(q_lens, dtype=torch.int32).cuda()
+    o = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    fa.cache_fwd(q, cache, table, ln, q_lens=ql, causal=causal, out=o, lse=lse)
+    fa.sync_status()
+    rows = np.broadcast_to(np.arange(T)[None, None, :] < np.array(q_lens)[:, None, None], lse.shape)
+    check_fwd(o, lse, R.Ref.of(cache, table).fwd(f64(q), lens, q_lens, causal), d, False, rows)
+    assert (f64(o)[~rows] == 7).all() and (f64(lse)[~rows] == 7).all()
+
+
 def test_fwd_chunk_bad_page():
     fa = require_gpu()
     d, page, H, G, T = 64, 32, 8, 4, 100
@@ -284,6 +307,38 @@ def test_fwd_chunk_bad_page():
     rows[1] = False
     check_fwd(o, lse, want, d, False, rows)
     assert np.isfinite(f64(o)).all()
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("T", [1, 3, 60])
+def test_fwd_large_scores(T, f32):
+    """Scores that are multiples of 2^19, up to 7 * 2^19: of a row's keys only
+    those with the largest count, all alike.  Their weights are 2^x with the same
+    x, which the rounding of the reference (at most 2^-2 at 2^22) leaves within
+    the range of P: the mean of their values, to the roundings of P (2^-11 or
+    2^-22, the same for all), of the sums and of the output."""
+    fa = require_gpu()
+    d, page, H, G, n = 128, 16, 1, 4, 600
+    cache, table, ln = R.make(fa, [n], H, d, page, seed=75)
+    g = torch.Generator().manual_seed(76)
+    j = torch.randint(0, 8, (n,), generator=g)
+    v = torch.randint(-8, 9, (1, H, n, d), generator=g)
+    k = (j.view(1, 1, n, 1) * torch.ones(1, H, n, d)).bfloat16().cuda()
+    fa.cache_append(cache, k, v.bfloat16().cuda(), table, torch.zeros_like(ln), n_new=ln)
+    q = torch.full((1, H * G, T, d), 4096.0).bfloat16().cuda()
+    o, lse = fa.cache_fwd(q, cache, table, ln, softmax_scale=1.0, out_dtype=fa.OUT_F32 if f32 else fa.OUT_BF16)
+    fa.sync_status()
+    o, lse = f64(o), f64(lse)
+    for t in range(T):
+        see = n - T + t + 1
+        top = (j[:see] == j[:see].max()).numpy()
+        want = v[0, 0, :see].numpy()[top].mean(0)
+        tol = (2.0 ** -10 if not f32 else 2.0 ** -16) * np.abs(v[0, 0, :see].numpy()[top]).mean(0)
+        tol = tol + (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(want)
+        assert (np.abs(o[0, :, t] - want) <= tol).all()
+        # a unit in the last place of 2^22 is 2^-1: the roundings of log2 e, of the
+        # score in log2 units, of ln 2 and of the result are half of one each
+        assert (np.abs(lse[0, :, t] - int(j[:see].max()) * 2.0 ** 19 - np.log(top.sum())) <= 2.0).all()
 
 
 @pytest.mark.parametrize("T", [1, 40, 200])
