@@ -3,56 +3,58 @@
 //   out[j] = in[j] + sum over rows r that see j of  e^(scale q_r.k_j - lse_r)
 //
 // 2 d flop and one exponential per row and key: tcgen05 for the products, with
-// the keys as rows of the accumulator (S^T = K Q^T), so that a thread of the
-// epilogue owns a key and its sum runs along its own tensor-memory lane: no
-// exchange between threads until the end.
+// the rows of q as rows of the accumulator (S = Q K^T).  A thread of the sums
+// owns a row, whose constants stay in its registers, and keeps a sum for each of
+// 32 keys while the rows go by; the rows' sums meet once, at the end of a key
+// tile.  (With the keys as rows nothing has to meet, but every warp reads every
+// row's constants from shared memory: 30 us where this takes TODO.)
 //
 // A first kernel brings the rows to f16 under a power of two, in the order
-// (token, head) and with what the epilogue needs of each, into the workspace:
-// every CTA of the second reads them all, and reading and converting bf16 rows
-// there took 4.9 us per 128 rows (91 us for 2 x 256 tokens over 4096) against
-// the 0.6 us in which they are multiplied and summed.
+// (token, head) and with what the sums need of each, into the workspace: every
+// CTA of the second reads them all, and reading and converting bf16 rows there
+// took 4.9 us per 128 rows (91 us for 2 x 256 tokens over 4096) against the 0.6
+// us in which they are multiplied and summed.
 //
-// The second kernel: one CTA takes 128 keys of a kv head, converted to f16 once
-// (exactly), and walks over the rows 128 at a time, two CTAs to an SM.  14 warps:
-//   0-7   epilogue: lane quadrant warp % 4 (32 keys), columns 64 (warp / 4)..;
-//         two score tiles in tensor memory, so the products of one run while the
-//         other is summed.
-//   8-11  conversion of K.
-//   12    issues the products.
-//   13    loads the rows by TMA, and their constants by bulk copies.
-// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 36 us (5 of them the first
-// kernel's), 0.46 PFLOP/s.  The sums bound it: an exponential per score, and the
-// rows' constants read from shared memory by every warp.
+// The second kernel: one CTA per SM goes through tiles of 128 keys of a kv head,
+// converted to f16 once (exactly) while the tile before is at work, and walks
+// over the rows 128 at a time.  22 warps:
+//   0-15  sums: rows 32 (warp % 4).., keys 32 (warp / 4).. of a tile; four score
+//         tiles in tensor memory, so that the products run ahead.
+//   16-19 conversion of K.
+//   20    issues the products.
+//   21    loads the rows by TMA.
 #include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
 
-constexpr int NTHREADS = 448;
-constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13;
-constexpr uint32_t TMEM_COLS = 256;
-constexpr int METAS = 6;                     // rows are loaded at most four tiles ahead of the sums
+constexpr int NTHREADS = 704;
+constexpr int W_CONV = 16, W_MMA = 20, W_LOAD = 21;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int QS = 3, KS = 2, SB = 4;        // tiles of rows, of keys, of scores
+constexpr int KX = 8;                        // key tiles whose scales are kept: the conversion is at
+                                             // most KS + SB ahead of the sums
+constexpr int METAS = 8;                     // rows are loaded at most QS + SB tiles ahead of the sums
 
-// What the epilogue needs of 128 rows; pairs of columns side by side.
+// What the sums need of 128 rows.
 struct alignas(16) RowMeta {
-  float4 fx_ref[64];                         // fx, fx', -ref, -ref'
-  float2 fac[64];
-  int vis[128];
+  float fx[128], nref[128], fac[128];        // factor of a score; -reference; what its rounding makes up for
+  int vis[128];                              // keys that it sees
 };
 
 template <int D>
 struct SmemW {
   static constexpr int TILE = (D / 64) * F16_CHUNK;
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_Q = TILE;
-  static constexpr int OFF_META = OFF_Q + 2 * TILE;
-  static constexpr int OFF_BAR = OFF_META + METAS * (int)sizeof(RowMeta);
-  static constexpr int NBAR = 1 + 2 + 2 + 2 + 2;
+  static constexpr int OFF_Q = KS * TILE;
+  static constexpr int OFF_META = OFF_Q + QS * TILE;
+  static constexpr int OFF_KX = OFF_META + METAS * (int)sizeof(RowMeta);   // [KX][8] scales of 16 keys; 0: no page
+  static constexpr int OFF_SUM = OFF_KX + KX * 8 * 4;        // [2][4][128] sums of 32 rows
+  static constexpr int OFF_BAR = OFF_SUM + 2 * 4 * 128 * 4;
+  static constexpr int NBAR = 2 * KS + 2 * QS + 2 * SB + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int OFF_SUM = OFF_MISC + 24;
-  static constexpr int BYTES = OFF_SUM + 128 * 4 + 1024;
-  static_assert(2 * (BYTES + 1024) <= 228 * 1024, "two CTAs to an SM");
+  static constexpr int BYTES = OFF_MISC + 16 + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 // Workspace of one (sequence, kv head): its rows in tiles of 128, zeros behind
@@ -100,54 +102,58 @@ __global__ void __launch_bounds__(NT_PREP) cache_rows_kernel(const __grid_consta
     const int i = r % 128;
     float ref, fac;
     reference(lse, true, ref, fac);
-    float* fr = reinterpret_cast<float*>(&m.fx_ref[i / 2]) + i % 2;
-    fr[0] = fac == 0.f ? 0.f : p.c2 * exp2i(e);
-    fr[2] = -ref;
-    reinterpret_cast<float*>(m.fac)[i] = fac;
+    m.fx[i] = fac == 0.f ? 0.f : p.c2 * exp2i(e);
+    m.nref[i] = -ref;
+    m.fac[i] = fac;
     m.vis[i] = p.causal ? len - q_len + t + 1 : len;
   }
 }
 
+// A tile of 128 keys and the row tiles that see any of them.
+struct KeyTile {
+  int b, h, key0, len, j0, nt;
+  FA4_DEV KeyTile(const CacheWeighParams& p, int G, unsigned tiles, unsigned i) {
+    const int bh = (int)(i / tiles);
+    b = bh / p.c.Hkv;
+    h = bh - b * p.c.Hkv;
+    key0 = (int)(i - (unsigned)bh * tiles) * 128;
+    len = cache_len(p.c, b);
+    const int q_len = cache_count(p.q_lens, b, p.T, p.c.err), rows = G * q_len;
+    // tokens before this one see none of the keys
+    const int t_first = p.causal ? max(0, key0 - (len - q_len)) : 0;
+    j0 = (int)min((long long)rows, (long long)t_first * G) / 128;
+    nt = key0 < len ? max(0, (rows + 127) / 128 - j0) : 0;
+  }
+};
+
 template <int D>
-__global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __grid_constant__ CacheWeighParams p) {
+__global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __grid_constant__ CacheWeighParams p) {
   using L = SmemW<D>;
   grid_start();
-  grid_wait();
   const CacheView& c = p.c;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int len = cache_len(c, b);
-  const int key0 = blockIdx.x * 128;
-  if (key0 >= len) return;
-  const int q_len = cache_count(p.q_lens, b, p.T, c.err);
   const int G = p.Hq / c.Hkv;
-  const int rows = G * q_len;
-  // tokens before this one see none of the CTA's keys
-  const int t_first = p.causal ? max(0, key0 - (len - q_len)) : 0;
-  const int j0 = (int)min((long long)rows, (long long)t_first * G) / 128;
-  const int nt = max(0, (rows + 127) / 128 - j0);
+  const unsigned key_tiles = (unsigned)(((long long)c.max_pages * c.page + 127) / 128);
+  const unsigned items = key_tiles * c.Hkv * c.B;    // below 2^31: the call checks
+  const int r_tiles = row_tiles(G, p.T);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + smem_pad(smem_raw);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_full = k_full + 1;
-  uint64_t* q_empty = q_full + 2;
-  uint64_t* s_full = q_empty + 2;
-  uint64_t* s_empty = s_full + 2;
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* q_full = k_empty + KS;
+  uint64_t* q_empty = q_full + QS;
+  uint64_t* s_full = q_empty + QS;
+  uint64_t* s_empty = s_full + SB;
+  uint64_t* mma_done = s_empty + SB;
+  RowMeta* metas = reinterpret_cast<RowMeta*>(smem + L::OFF_META);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  uint64_t* mma_done = reinterpret_cast<uint64_t*>(smem + L::OFF_MISC + 8);
-  RowMeta* metas = reinterpret_cast<RowMeta*>(smem + L::OFF_META);
-  float* s_sum = reinterpret_cast<float*>(smem + L::OFF_SUM);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    mbar_init(k_full, 4);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], 8);
-    }
+    for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 4); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
+    for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 16); }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -157,157 +163,199 @@ __global__ void __launch_bounds__(NTHREADS, 2) cache_weigh_rows_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  grid_wait();
 
-  float sum = 0.f, before = 0.f;             // of a key; what it had
-  bool there = false;                        // its page
   if (warp == W_MMA) {
     // -------------------------------------------------------------- products
-    if (nt > 0) {
-      const bool leader = elect_one();
-      const uint32_t idesc = idesc_f16(128, 128, false, false, false);
-      const uint32_t sk = smem_u32(smem + L::OFF_K);
-      bool ok = mbar_wait(k_full, 0, abort_flag, c.err);
-      for (int j = 0; ok && j < nt; ++j) {
-        const int s = j & 1;
-        const uint32_t phase = (j >> 1) & 1;
-        if (!mbar_wait(&q_full[s], phase, abort_flag, c.err)) break;
-        if (j >= 2 && !mbar_wait(&s_empty[s], phase ^ 1, abort_flag, c.err)) break;
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_f16(128, 128, false, false, false);
+    bool ok = true;
+    int n = 0, t = 0;                        // key tiles and row tiles so far
+    for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const KeyTile k(p, G, key_tiles, i);
+      if (k.nt == 0) continue;
+      const uint32_t sk = smem_u32(smem + L::OFF_K + n % KS * L::TILE);
+      ok = mbar_wait(&k_full[n % KS], (n / KS) & 1, abort_flag, c.err);
+      for (int j = 0; ok && j < k.nt; ++j, ++t) {
+        const int qs = t % QS, sb = t % SB;
+        ok = mbar_wait(&q_full[qs], (t / QS) & 1, abort_flag, c.err) &&
+             (t < SB || mbar_wait(&s_empty[sb], (t / SB - 1) & 1, abort_flag, c.err));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t sq = smem_u32(smem + L::OFF_Q + s * L::TILE);
+        const uint32_t sq = smem_u32(smem + L::OFF_Q + qs * L::TILE);
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * F16_CHUNK + (k % 4) * 32;
-            mma_f16(tbase + 128 * s, make_sdesc(sk + off, 16, 1024, SW_128B), make_sdesc(sq + off, 16, 1024, SW_128B),
-                    idesc, k > 0);
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = (x / 4) * F16_CHUNK + (x % 4) * 32;
+            mma_f16(tbase + 128 * sb, make_sdesc(sq + off, 16, 1024, SW_128B), make_sdesc(sk + off, 16, 1024, SW_128B),
+                    idesc, x > 0);
           }
-          mma_commit(&s_full[s]);
-          mma_commit(&q_empty[s]);
+          mma_commit(&s_full[sb]);
+          mma_commit(&q_empty[qs]);
+          if (j + 1 == k.nt) mma_commit(&k_empty[n % KS]);
         }
         __syncwarp();
       }
-      if (leader) mma_commit(mma_done);
-      __syncwarp();
-      volatile int none = 0;
-      mbar_wait(mma_done, 0, &none, c.err);
-      __syncwarp();
+      ++n;
     }
+    if (leader) mma_commit(mma_done);
+    __syncwarp();
+    volatile int none = 0;
+    mbar_wait(mma_done, 0, &none, c.err);
+    __syncwarp();
   } else if (warp == W_LOAD) {
     // -------------------------------------------------------------- rows of q
     if (lane == 0) {
       tma_prefetch_desc(&p.tm_q);
-      const long long bh = (long long)b * c.Hkv + h;
-      const int tiles = row_tiles(G, p.T);
-      int issued = 0;
-      for (int j = 0; j < nt; ++j) {
-        const int s = j & 1;
-        if (j >= 2 && !mbar_wait(&q_empty[s], ((j >> 1) & 1) ^ 1, abort_flag, c.err)) break;
-        mbar_arrive_expect_tx(&q_full[s], L::TILE + (uint32_t)sizeof(RowMeta));
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_3d(smem + L::OFF_Q + s * L::TILE + x * F16_CHUNK, &p.tm_q, &q_full[s], 64 * x,
-                      (int)((bh * tiles + j0 + j) * 128), 0);
-        bulk_load(&metas[j % METAS], reinterpret_cast<const RowMeta*>(p.metas) + bh * tiles + j0 + j,
-                  (uint32_t)sizeof(RowMeta), &q_full[s]);
-        issued = j + 1;
+      bool ok = true;
+      int t = 0;
+      for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        const KeyTile k(p, G, key_tiles, i);
+        const long long bh = (long long)k.b * c.Hkv + k.h;
+        for (int j = 0; j < k.nt; ++j, ++t) {
+          const int s = t % QS;
+          ok = t < QS || mbar_wait(&q_empty[s], (t / QS - 1) & 1, abort_flag, c.err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[s], L::TILE + (uint32_t)sizeof(RowMeta));
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(smem + L::OFF_Q + s * L::TILE + x * F16_CHUNK, &p.tm_q, &q_full[s], 64 * x,
+                        (int)((bh * r_tiles + k.j0 + j) * 128), 0);
+          bulk_load(&metas[t % METAS], reinterpret_cast<const RowMeta*>(p.metas) + bh * r_tiles + k.j0 + j,
+                    (uint32_t)sizeof(RowMeta), &q_full[s]);
+        }
       }
       if (*abort_flag) {                             // what is still in flight lands first
         volatile int none = 0;
-        for (int j = max(0, issued - 2); j < issued; ++j) mbar_wait(&q_full[j & 1], (j >> 1) & 1, &none, c.err);
+        for (int j = max(0, t - QS); j < t; ++j) mbar_wait(&q_full[j % QS], (j / QS) & 1, &none, c.err);
       }
     }
     __syncwarp();
   } else if (warp >= W_CONV) {
     // -------------------------------------------------------------- K
-    constexpr int PARTS = D / 16, RSTEP = 128 / PARTS;
+    constexpr int PARTS = D / 16, RSTEP = 128 / PARTS, N = 128 / RSTEP;
     const int tid = threadIdx.x - 32 * W_CONV;
-    const int part = tid % PARTS;
-    constexpr int N = 128 / RSTEP;
-    int pg[N];                               // all rows' loads in flight, one after the other's pages
+    const int part = tid % PARTS, row0 = tid / PARTS;
+    bool ok = true;
+    int n = 0;
+    for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const KeyTile k(p, G, key_tiles, i);
+      if (k.nt == 0) continue;
+      // all rows' loads in flight, one after the other's pages
+      const int* table = c.table + (long long)k.b * c.max_pages;
+      int pg[N + 1];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int key = key0 + tid / PARTS + i * RSTEP;
-      pg[i] = key < len ? cache_page(c, c.table, b, key / c.page) : -1;
+      for (int e = 0; e <= N; ++e) {         // the last: group tid of 16 keys, for its scale
+        const int key = k.key0 + (e < N ? row0 + e * RSTEP : 16 * (tid & 7));
+        pg[e] = key < k.len ? table[key / c.page] : -1;
+        if (key < k.len && (pg[e] < 0 || pg[e] >= c.num_pages)) pg[e] = -2;
+      }
+      uint4 x[N];
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int key = k.key0 + row0 + e * RSTEP;
+        x[e] = make_uint4(0, 0, 0, 0);       // what is not there is zero
+        bad = bad || pg[e] == -2;
+        if (pg[e] >= 0)
+          x[e] = reinterpret_cast<const uint4*>(c.k + (((long long)pg[e] * c.Hkv + k.h) * c.page + key % c.page) * D)[part];
+      }
+      if (bad) atomicOr(c.err, FA4_DEVERR_INDEX);
+      const float kx = pg[N] >= 0 ? e8m0_value(c.ks[(long long)pg[N] * c.Hkv + k.h]) : 0.f;
+      ok = n < KS || mbar_wait(&k_empty[n % KS], (n / KS - 1) & 1, abort_flag, c.err);
+      if (!ok) break;
+      uint8_t* tile = smem + L::OFF_K + n % KS * L::TILE;
+#pragma unroll
+      for (int e = 0; e < N; ++e) store16<D>(tile, row0 + e * RSTEP, part, x[e]);
+      if (tid < 8) reinterpret_cast<float*>(smem + L::OFF_KX)[n % KX * 8 + tid] = kx;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[n % KS]);
+      ++n;
     }
-    uint4 x[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int key = key0 + tid / PARTS + i * RSTEP;
-      x[i] = make_uint4(0, 0, 0, 0);         // what is not there is zero
-      if (pg[i] >= 0)
-        x[i] = reinterpret_cast<const uint4*>(c.k + (((long long)pg[i] * c.Hkv + h) * c.page + key % c.page) * D)[part];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) store16<D>(smem + L::OFF_K, tid / PARTS + i * RSTEP, part, x[i]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(k_full);
   } else {
     // -------------------------------------------------------------- sums
-    const int quad = warp & 3, half = warp >> 2;
-    const int key = key0 + 32 * quad + lane;
-    float kx = 0.f;
-    if (key < len) {
-      const int pg = cache_page(c, c.table, b, key / c.page);
-      there = pg >= 0;
-      if (there) kx = e8m0_value(c.ks[(long long)pg * c.Hkv + h]);
-      if (half == 0) before = p.w_in[((long long)b * c.Hkv + h) * c.max_pages * c.page + key];
-    }
-    const float2 kx2 = make_float2(kx, kx);
-    const uint32_t base = tbase + ((uint32_t)(32 * quad) << 16) + 64 * half;
-    float2 acc = make_float2(0.f, 0.f);
-    for (int j = 0; j < nt; ++j) {
-      const int s = j & 1;
-      if (!mbar_wait(&s_full[s], (j >> 1) & 1, abort_flag, c.err)) break;
-      tc_fence_after();
-      const RowMeta& m = metas[j % METAS];
-      const int r0 = (j0 + j) * 128;
-      // the tile's first token sees the fewest keys
-      const bool full = !p.causal || len - q_len + r0 / G + 1 >= key0 + 128;
+    const int quad = warp & 3, part = warp >> 2;
+    const int row = 32 * quad + lane;
+    const uint32_t base = tbase + ((uint32_t)(32 * quad) << 16) + 32 * part;
+    float* s_sum = reinterpret_cast<float*>(smem + L::OFF_SUM);
+    // after a wait that ran out a warp computes no more, but comes to the barriers
+    bool ok = true;
+    int n = 0, t = 0, turn = 0;
+    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
+      const KeyTile k(p, G, key_tiles, i);
+      if (k.key0 >= k.len) continue;
+      const long long bh = (long long)k.b * c.Hkv + k.h;
+      const int my_key = k.key0 + 32 * part + lane;    // of the quadrant that writes the sums
+      float before = 0.f;
+      if (quad == 0 && my_key < k.len) before = p.w_in[bh * c.max_pages * c.page + my_key];
+      float2 kx = make_float2(0.f, 0.f);
+      float2 acc[16];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t v[32];
-        tmem_ld32(base + 128 * s + 32 * g, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-        if (g == 1) {
+      for (int e = 0; e < 16; ++e) acc[e] = make_float2(0.f, 0.f);
+      if (k.nt > 0) {
+        for (int j = 0; ok && j < k.nt; ++j, ++t) {
+          const int sb = t % SB;
+          ok = mbar_wait(&s_full[sb], (t / SB) & 1, abort_flag, c.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (j == 0) kx = *reinterpret_cast<const float2*>(smem + L::OFF_KX + (n % KX * 8 + 2 * part) * 4);
+          uint32_t v[32];
+          tmem_ld32(base + 128 * sb, v);
+          const RowMeta& m = metas[t % METAS];
+          const float fx = m.fx[row], nref = m.nref[row], fac = m.fac[row];
+          const float F[2] = {fx * kx.x, fx * kx.y};
+          const float2 nr = make_float2(nref, nref), fc = make_float2(fac, fac);
+          const int left = m.vis[row] - k.key0 - 32 * part;      // keys of these that the row sees
+          tmem_ld_wait();
+          reg_fence32(v);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[s]);
+          if (lane == 0) mbar_arrive(&s_empty[sb]);
+          auto add = [&](bool full) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 f2 = make_float2(F[e / 8], F[e / 8]);
+              const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, nr);
+              float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              if (!full) {
+                if (2 * e >= left) w.x = 0.f;
+                if (2 * e + 1 >= left) w.y = 0.f;
+              }
+              acc[e] = ffma2(w, fc, acc[e]);
+            }
+          };
+          if (__all_sync(0xffffffffu, left >= 32)) add(true);
+          else add(false);
         }
-        const int c0 = 32 * half + 16 * g;           // pairs of columns
-        if (full) {
+        ++n;
+      }
+      // the 32 rows' sums: lanes hand half of their keys over, five times; lane i
+      // then has key i's
+      float a[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 fr = m.fx_ref[c0 + i];
-            const float2 x = fmul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kx2);
-            const float2 y = ffma2(x, make_float2(fr.x, fr.y), make_float2(fr.z, fr.w));
-            acc = ffma2(make_float2(ex2_approx(y.x), ex2_approx(y.y)), m.fac[c0 + i], acc);
-          }
-        } else {
+      for (int e = 0; e < 16; ++e) { a[2 * e] = acc[e].x; a[2 * e + 1] = acc[e].y; }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 fr = m.fx_ref[c0 + i];
-            const float2 x = fmul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kx2);
-            const float2 y = ffma2(x, make_float2(fr.x, fr.y), make_float2(fr.z, fr.w));
-            const int2 vis = reinterpret_cast<const int2*>(m.vis)[c0 + i];
-            acc = ffma2(make_float2(key < vis.x ? ex2_approx(y.x) : 0.f, key < vis.y ? ex2_approx(y.y) : 0.f),
-                        m.fac[c0 + i], acc);
-          }
+      for (int o = 16; o > 0; o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int e = 0; e < o; ++e) {
+          const float mine = up ? a[e + o] : a[e], theirs = up ? a[e] : a[e + o];
+          a[e] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
         }
       }
+      float* sums = s_sum + (turn++ & 1) * 512 + 32 * part + lane;
+      sums[128 * quad] = a[0];
+      named_bar(1 + part, 128);
+      if (quad == 0 && my_key < k.len && !*abort_flag) {
+        const float sum = (a[0] + sums[128]) + (sums[256] + sums[384]);
+        // a page that is not there adds nothing
+        p.w_out[bh * c.max_pages * c.page + my_key] = before + ((lane < 16 ? kx.x : kx.y) == 0.f ? 0.f : sum);
+      }
     }
-    sum = acc.x + acc.y;
-    if (half == 1) s_sum[32 * quad + lane] = sum;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
-  const int key = key0 + (int)threadIdx.x;
-  if (warp < 4 && key < len) {
-    const long long at = ((long long)b * c.Hkv + h) * c.max_pages * c.page + key;
-    // a page that is not there adds nothing
-    if (!*abort_flag) p.w_out[at] = before + (there ? sum + s_sum[threadIdx.x] : 0.f);
-  }
 }
 
 template <int D>
@@ -320,8 +368,8 @@ cudaError_t launch(const CacheWeighParams& p, cudaStream_t st) {
   auto k = cache_weigh_rows_kernel<D>;
   e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemW<D>::BYTES);
   if (e != cudaSuccess) return e;
-  const long long cap = (long long)p.c.max_pages * p.c.page;
-  return launch_next(k, dim3((unsigned)((cap + 127) / 128), H, B), NTHREADS, SmemW<D>::BYTES, st, p);
+  const long long items = ((long long)p.c.max_pages * p.c.page + 127) / 128 * H * B;
+  return launch_next(k, dim3((unsigned)(items < kSMs ? items : kSMs)), NTHREADS, SmemW<D>::BYTES, st, p);
 }
 
 }  // namespace
