@@ -299,33 +299,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
           if (!ok) break;
           tc_fence_after();
           if (j == 0) kx = *reinterpret_cast<const float2*>(smem + L::OFF_KX + (n % KX * 8 + 2 * part) * 4);
-          uint32_t v[32];
-          tmem_ld32(base + 128 * sb, v);
           const RowMeta& m = metas[t % METAS];
           const float fx = m.fx[row], nref = m.nref[row], fac = m.fac[row];
-          const float F[2] = {fx * kx.x, fx * kx.y};
           const float2 nr = make_float2(nref, nref), fc = make_float2(fac, fac);
           const int left = m.vis[row] - k.key0 - 32 * part;      // keys of these that the row sees
-          tmem_ld_wait();
-          reg_fence32(v);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[sb]);
-          auto add = [&](bool full) {
+          const bool all = __all_sync(0xffffffffu, left >= 32);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 f2 = make_float2(F[e / 8], F[e / 8]);
-              const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, nr);
-              float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              if (!full) {
-                if (2 * e >= left) w.x = 0.f;
-                if (2 * e + 1 >= left) w.y = 0.f;
-              }
-              acc[e] = ffma2(w, fc, acc[e]);
+          for (int hf = 0; hf < 2; ++hf) {                       // 16 keys, of one scale
+            uint32_t v[16];
+            tmem_ld16(base + 128 * sb + 16 * hf, v);
+            const float F = fx * (hf ? kx.y : kx.x);
+            const float2 f2 = make_float2(F, F);
+            tmem_ld_wait();
+            reg_fence16(v);
+            if (hf) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_empty[sb]);
             }
-          };
-          if (__all_sync(0xffffffffu, left >= 32)) add(true);
-          else add(false);
+            auto add = [&](bool full) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, nr);
+                float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                if (!full) {
+                  if (16 * hf + 2 * e >= left) w.x = 0.f;
+                  if (16 * hf + 2 * e + 1 >= left) w.y = 0.f;
+                }
+                acc[8 * hf + e] = ffma2(w, fc, acc[8 * hf + e]);
+              }
+            };
+            if (all) add(true);
+            else add(false);
+          }
         }
         ++n;
       }
