@@ -401,7 +401,7 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const vo
  * for j < lens[b], with fa4fp4_cache_fwd's arguments and the lse that it wrote
  * (rows with lse = -inf add nothing).  weights: f32 [B][Hkv][max_pages * page];
  * weight_out may be weight_in; entries j >= lens[b] are not written.  `workspace`
- * as for fa4fp4_cache_fwd; below 128 query rows per kv head (Hq / Hkv * T) it
+ * as for fa4fp4_cache_fwd; below 80 query rows per kv head (Hq / Hkv * T) it
  * needs none (its size is 0 and it may be NULL). */
 FA4FP4_API size_t fa4fp4_cache_weigh_workspace_bytes(int B, int Hq, int Hkv, int T, int d);
 FA4FP4_API fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const void* q, const float* lse,

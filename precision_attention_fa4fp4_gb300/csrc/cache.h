@@ -79,10 +79,10 @@ bool cache_weigh_fits(int B, int Hkv, int page, int max_pages);
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st);
 // The same for many rows (query heads of a kv head x T), with a workspace.
 // Keys x sequences, heads of 128, 8 kv heads, us by mma.sync / by tcgen05:
-//   2048 x 16:  32 rows 22 / 48,  96 rows 42 / 48,  128 rows 49 / 48,  256 rows 90 / 59
-//   8192 x 1:   32 rows 7 / 15,   96 rows 14 / 15,  128 rows 16 / 15,  256 rows 28 / 18
-// heads of 64, 4096 x 16: 96 rows 59 / 66, 128 rows 71 / 67.
-constexpr int WEIGH_MANY = 128;
+//   2048 x 16:  32 rows 22 / 31,  64 rows 29 / 31,  96 rows 42 / 31,  256 rows 90 / 39
+//   8192 x 1:   32 rows 7 / 13,   64 rows 10 / 13,  96 rows 14 / 13,  256 rows 28 / 15
+// heads of 64, 4096 x 16: 64 rows 43 / 49, 96 rows 59 / 49.
+constexpr int WEIGH_MANY = 80;
 size_t cache_weigh_rows_bytes(int B, int Hq, int Hkv, int T, int d, size_t* all);
 cudaError_t launch_cache_weigh_rows(const CacheWeighParams& p, cudaStream_t st);
 

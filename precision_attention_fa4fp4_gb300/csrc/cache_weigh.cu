@@ -10,7 +10,7 @@
 // queues, and a fixed grid shares one line of (sequence, head, 128 keys): 16
 // sequences of 4001..8192, 32 / 8 heads of 128, 23.2 us, 4.5 TB/s.
 //
-// Up to 127 rows: bound by the matrix products and one exponential per score.  A
+// Up to 79 rows: bound by the matrix products and one exponential per score.  A
 // warp converts its 32 keys once and keeps them as f16 operands while it walks
 // over the rows, which the CTA prepares 64 at a time: 32 rows of 8 heads of 128,
 // 16 sequences of 2048, 22 us.  (The m16n8k32 E4M3 product would take the codes

@@ -7,7 +7,7 @@
 // owns a row, whose constants stay in its registers, and keeps a sum for each of
 // 32 keys while the rows go by; the rows' sums meet once, at the end of a key
 // tile.  (With the keys as rows nothing has to meet, but every warp reads every
-// row's constants from shared memory: 30 us where this takes TODO.)
+// row's constants from shared memory: 36 us where this takes 27.)
 //
 // A first kernel brings the rows to f16 under a power of two, in the order
 // (token, head) and with what the sums need of each, into the workspace: every
@@ -17,23 +17,28 @@
 //
 // The second kernel: one CTA per SM goes through tiles of 128 keys of a kv head,
 // converted to f16 once (exactly) while the tile before is at work, and walks
-// over the rows 128 at a time.  22 warps:
+// over the rows 128 at a time.  23 warps:
 //   0-15  sums: rows 32 (warp % 4).., keys 32 (warp / 4).. of a tile; four score
 //         tiles in tensor memory, so that the products run ahead.
 //   16-19 conversion of K.
 //   20    issues the products.
-//   21    loads the rows by TMA.
+//   21    loads the rows by TMA, and their constants by bulk copies.
+//   22    looks the pages up and stages K's bytes by bulk copies (the conversion's
+//         own loads, page after table after length, took 4 us a key tile).
+// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 26.6 us (5 of them the first
+// kernel's), 0.62 PFLOP/s.  Latency bounds it: 512 key tiles are 3.4 an SM, so
+// four rounds of eight row tiles, and of the 1500 clocks of a step 470 are sums.
 #include "cache_line.cuh"
 
 namespace fa4 {
 namespace {
 
-constexpr int NTHREADS = 704;
-constexpr int W_CONV = 16, W_MMA = 20, W_LOAD = 21;
+constexpr int NTHREADS = 736;
+constexpr int W_CONV = 16, W_MMA = 20, W_LOAD = 21, W_PAGE = 22;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int QS = 3, KS = 2, SB = 4;        // tiles of rows, of keys, of scores
-constexpr int KX = 8;                        // key tiles whose scales are kept: the conversion is at
-                                             // most KS + SB ahead of the sums
+constexpr int KX = 16;                       // key tiles whose scales are kept: they are looked up at
+                                             // most 2 KS + SB tiles ahead of the sums
 constexpr int METAS = 8;                     // rows are loaded at most QS + SB tiles ahead of the sums
 
 // What the sums need of 128 rows.
@@ -48,10 +53,11 @@ struct SmemW {
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = KS * TILE;
   static constexpr int OFF_META = OFF_Q + QS * TILE;
-  static constexpr int OFF_KX = OFF_META + METAS * (int)sizeof(RowMeta);   // [KX][8] scales of 16 keys; 0: no page
+  static constexpr int OFF_K8 = OFF_META + METAS * (int)sizeof(RowMeta);   // staged codes
+  static constexpr int OFF_KX = OFF_K8 + KS * 128 * D;       // [KX][8] scales of 16 keys; 0: no page
   static constexpr int OFF_SUM = OFF_KX + KX * 8 * 4;        // [2][4][128] sums of 32 rows
   static constexpr int OFF_BAR = OFF_SUM + 2 * 4 * 128 * 4;
-  static constexpr int NBAR = 2 * KS + 2 * QS + 2 * SB + 1;
+  static constexpr int NBAR = 4 * KS + 2 * QS + 2 * SB + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory");
@@ -140,18 +146,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
   uint8_t* smem = smem_raw + smem_pad(smem_raw);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* k_empty = k_full + KS;
-  uint64_t* q_full = k_empty + KS;
+  uint64_t* k8_full = k_empty + KS;
+  uint64_t* k8_empty = k8_full + KS;
+  uint64_t* q_full = k8_empty + KS;
   uint64_t* q_empty = q_full + QS;
   uint64_t* s_full = q_empty + QS;
   uint64_t* s_empty = s_full + SB;
   uint64_t* mma_done = s_empty + SB;
+  float* s_kx = reinterpret_cast<float*>(smem + L::OFF_KX);
   RowMeta* metas = reinterpret_cast<RowMeta*>(smem + L::OFF_META);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 4); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], 4); mbar_init(&k_empty[s], 1);
+      mbar_init(&k8_full[s], 1); mbar_init(&k8_empty[s], 4);
+    }
     for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
     for (int s = 0; s < SB; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 16); }
     mbar_init(mma_done, 1);
@@ -230,6 +242,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
       }
     }
     __syncwarp();
+  } else if (warp == W_PAGE) {
+    // -------------------------------------------------------------- pages
+    const int log_p = 31 - __clz(c.page);
+    bool ok = true;
+    int n = 0;
+    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
+      const KeyTile k(p, G, key_tiles, i);
+      if (k.nt == 0) continue;
+      // lane i < 8: group i of 16 keys; the first lane of a page copies it
+      const int key = k.key0 + 16 * (lane & 7);
+      int pg = -1;
+      if (lane < 8 && key < k.len) pg = cache_page(c, c.table, k.b, key >> log_p);
+      const long long ph = (long long)max(pg, 0) * c.Hkv + k.h;
+      const float kx = pg >= 0 ? e8m0_value(*(c.ks + ph)) : 0.f;
+      ok = n < KS || mbar_wait(&k8_empty[n % KS], (n / KS - 1) & 1, abort_flag, c.err);
+      if (!ok) break;
+      if (lane < 8) s_kx[n % KX * 8 + lane] = kx;
+      __syncwarp();
+      const bool copies = lane < 8 && pg >= 0 && ((16 * lane) & (c.page - 1)) == 0;
+      const uint32_t bytes = (uint32_t)c.page * D;
+      const uint32_t all = (uint32_t)__popc(__ballot_sync(0xffffffffu, copies)) * bytes;
+      if (lane == 0) mbar_arrive_expect_tx(&k8_full[n % KS], all);
+      __syncwarp();
+      if (copies)
+        bulk_load(smem + L::OFF_K8 + n % KS * 128 * D + 16 * lane * D, c.k + (ph << log_p) * D, bytes, &k8_full[n % KS]);
+      __syncwarp();
+      ++n;
+    }
+    if (*abort_flag) {                               // what is still in flight lands first
+      volatile int none = 0;
+      for (int j = max(0, n - KS); j < n; ++j) mbar_wait(&k8_full[j % KS], (j / KS) & 1, &none, c.err);
+    }
+    __syncwarp();
   } else if (warp >= W_CONV) {
     // -------------------------------------------------------------- K
     constexpr int PARTS = D / 16, RSTEP = 128 / PARTS, N = 128 / RSTEP;
@@ -240,33 +285,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const KeyTile k(p, G, key_tiles, i);
       if (k.nt == 0) continue;
-      // all rows' loads in flight, one after the other's pages
-      const int* table = c.table + (long long)k.b * c.max_pages;
-      int pg[N + 1];
-#pragma unroll
-      for (int e = 0; e <= N; ++e) {         // the last: group tid of 16 keys, for its scale
-        const int key = k.key0 + (e < N ? row0 + e * RSTEP : 16 * (tid & 7));
-        pg[e] = key < k.len ? table[key / c.page] : -1;
-        if (key < k.len && (pg[e] < 0 || pg[e] >= c.num_pages)) pg[e] = -2;
-      }
+      ok = mbar_wait(&k8_full[n % KS], (n / KS) & 1, abort_flag, c.err);
+      if (!ok) break;
+      const uint8_t* from = smem + L::OFF_K8 + n % KS * 128 * D + row0 * D + part * 16;
       uint4 x[N];
-      bool bad = false;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int key = k.key0 + row0 + e * RSTEP;
-        x[e] = make_uint4(0, 0, 0, 0);       // what is not there is zero
-        bad = bad || pg[e] == -2;
-        if (pg[e] >= 0)
-          x[e] = reinterpret_cast<const uint4*>(c.k + (((long long)pg[e] * c.Hkv + k.h) * c.page + key % c.page) * D)[part];
+        const int row = row0 + e * RSTEP;
+        x[e] = lds16(from + e * RSTEP * D);
+        // what is not there is zero
+        if (k.key0 + row >= k.len || s_kx[n % KX * 8 + row / 16] == 0.f) x[e] = make_uint4(0, 0, 0, 0);
       }
-      if (bad) atomicOr(c.err, FA4_DEVERR_INDEX);
-      const float kx = pg[N] >= 0 ? e8m0_value(c.ks[(long long)pg[N] * c.Hkv + k.h]) : 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k8_empty[n % KS]);
       ok = n < KS || mbar_wait(&k_empty[n % KS], (n / KS - 1) & 1, abort_flag, c.err);
       if (!ok) break;
       uint8_t* tile = smem + L::OFF_K + n % KS * L::TILE;
 #pragma unroll
       for (int e = 0; e < N; ++e) store16<D>(tile, row0 + e * RSTEP, part, x[e]);
-      if (tid < 8) reinterpret_cast<float*>(smem + L::OFF_KX)[n % KX * 8 + tid] = kx;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[n % KS]);
@@ -298,7 +334,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
           ok = mbar_wait(&s_full[sb], (t / SB) & 1, abort_flag, c.err);
           if (!ok) break;
           tc_fence_after();
-          if (j == 0) kx = *reinterpret_cast<const float2*>(smem + L::OFF_KX + (n % KX * 8 + 2 * part) * 4);
+          if (j == 0) kx = *reinterpret_cast<const float2*>(s_kx + n % KX * 8 + 2 * part);
           const RowMeta& m = metas[t % METAS];
           const float fx = m.fx[row], nref = m.nref[row], fac = m.fac[row];
           const float2 nr = make_float2(nref, nref), fc = make_float2(fac, fac);

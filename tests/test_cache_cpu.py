@@ -143,7 +143,7 @@ def test_workspace_sizes(fa):
     assert f(65535, 64, 64, 1, 128, 128, 1 << 20, 0) == 0 and f(1, 8, 2, 1, 128, 64, 2, 1 << 25) == 0
     # bounded by the grid, whatever the batch
     assert f(512, 64, 8, 1, 128, 64, 4096, 0) == f(64, 64, 8, 1, 128, 64, 4096, 0) < (8 << 20)
-    # tiles of 128 rows of f16 and 16 bytes of constants a row, from 64 rows on
+    # tiles of 128 rows of f16 and 16 bytes of constants a row, from 80 rows on
     assert fa.cache_weigh_workspace_bytes(1, 4, 2, 31, 128) == 0
     assert fa.cache_weigh_workspace_bytes(3, 4, 2, 65, 64) == 3 * 2 * 2 * 128 * (64 * 2 + 16)
     assert fa.cache_select_workspace_bytes(2, 3, 4, 16384) == 0

@@ -471,7 +471,7 @@ def test_select_near_ties():
 # ------------------------------------------------------------------ weights
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("d,page,H,G,T", [(64, 16, 2, 1, 1), (128, 64, 2, 4, 1), (128, 128, 1, 3, 7), (64, 32, 2, 5, 40),
-                                          (128, 64, 1, 4, 100), (128, 16, 2, 1, 300), (64, 16, 1, 8, 15),
+                                          (128, 64, 1, 4, 100), (128, 16, 2, 1, 300), (64, 16, 1, 8, 15), (128, 64, 1, 1, 79), (64, 32, 1, 4, 20),
                                           (128, 32, 2, 2, 63), (128, 32, 1, 1, 128), (64, 128, 1, 2, 9)])
 def test_weigh(d, page, H, G, T, causal):
     """|out - ref| <= (2 eps + 2^-19 + 2^-21 |lse|) * received + 2^-22 * ref:
