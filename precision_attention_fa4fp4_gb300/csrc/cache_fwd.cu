@@ -39,7 +39,7 @@
 // is missing to a copy's 6.7 are the first 5 us of a launch and the ends of row
 // blocks.  One of 1000: 9.0 us (start 2, lens and pages 1.5, first keys 2, join
 // 2-3).  With 9 to 16 rows and FP32 output instructions bound it: 4 sequences of
-// 16001..32760, 8 heads of 64, 37 us, 2.7 TB/s.
+// 16001..32760, 8 heads of 64, 39 us, 2.6 TB/s.
 //
 // Roundings: q to f16 under a power of two (2^-32 of the row's largest); P to
 // f16 under a factor 2^15 and V's relative exponent (2^-11 of P, or 2^-36 of the
@@ -465,7 +465,11 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
               for (int w = 0; w < VW; ++w) vr[i][k][w] = 0;
           }
       }
-      // O^T += V^T P: lane rows (D / 8) g + 2 mt and + 1 of the head dimension
+      // O^T += V^T P: lane rows (D / 8) g + 2 mt and + 1 of the head dimension.
+      // The products' accumulators are cut, not rounded: for FP32 output a step's
+      // sum is taken by itself and added with rounding (over 16001..32760 keys the
+      // output is off by 1.2e-6 of its norm without and 6.7e-7 with, for 2 us of 37)
+      float part[SPLIT ? NT : 1][4];
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         const int mt = j / 2, i = j % 2, w = mt / 2, pick = mt % 2 ? 0x7362 : 0x5140;
@@ -475,8 +479,16 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
         const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_hi_to_f16x2(y);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_16816(o[n][mt], a0, a1, a2, a3, ph[n][i][0], ph[n][i][1]);
-          if constexpr (SPLIT) mma_16816(o[n][mt], a0, a1, a2, a3, pl[n][i][0], pl[n][i][1]);
+          if constexpr (SPLIT) {
+            if (i == 0) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
+            mma_16816(part[n], a0, a1, a2, a3, pl[n][i][0], pl[n][i][1]);
+            mma_16816(part[n], a0, a1, a2, a3, ph[n][i][0], ph[n][i][1]);
+            if (i == 1)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[n][mt][k] += part[n][k];
+          } else {
+            mma_16816(o[n][mt], a0, a1, a2, a3, ph[n][i][0], ph[n][i][1]);
+          }
         }
       }
       // the step's bytes are in registers: its place takes unit u + S
