@@ -39,7 +39,7 @@
 // is missing to a copy's 6.7 are the first 5 us of a launch and the ends of row
 // blocks.  One of 1000: 9.0 us (start 2, lens and pages 1.5, first keys 2, join
 // 2-3).  With 9 to 16 rows and FP32 output instructions bound it: 4 sequences of
-// 16001..32760, 8 heads of 64, 39 us, 2.6 TB/s.
+// 16001..32760, 8 heads of 64, 40 us, 2.5 TB/s.
 //
 // Roundings: q to f16 under a power of two (2^-32 of the row's largest); P to
 // f16 under a factor 2^15 and V's relative exponent (2^-11 of P, or 2^-36 of the
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
+          float half[SPLIT ? NT : 1][4];
           const uint4 ka = lds16(from + i * 16 * D + ko[0][k]);
           const uint4 kb = lds16(from + i * 16 * D + ko[1][k]);
           const uint32_t lo[4] = {ka.x, ka.y, ka.z, ka.w};
@@ -351,8 +352,17 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
             const uint32_t a0 = e4m3x2_to_f16x2(lo[w]), a2 = e4m3x2_hi_to_f16x2(lo[w]);
             const uint32_t a1 = e4m3x2_to_f16x2(hi[w]), a3 = e4m3x2_hi_to_f16x2(hi[w]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_16816(s[n][i], a0, a1, a2, a3, q[n].b[4 * k + w][0], q[n].b[4 * k + w][1]);
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (SPLIT) {
+                if (w % 2 == 0) half[n][0] = half[n][1] = half[n][2] = half[n][3] = 0.f;
+                mma_16816(half[n], a0, a1, a2, a3, q[n].b[4 * k + w][0], q[n].b[4 * k + w][1]);
+                if (w % 2)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) s[n][i][e] += half[n][e];
+              } else {
+                mma_16816(s[n][i], a0, a1, a2, a3, q[n].b[4 * k + w][0], q[n].b[4 * k + w][1]);
+              }
+            }
           }
         }
       bool full = true;
@@ -375,12 +385,14 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
             for (int j = 0; j < 4; ++j) o[n][i][j] *= by;
         xo = to;
       }
-      float vd[NP], vu[NP];                        // exponent on P, and what undoes it for l
+      // exponent on P, what undoes it for l, and P's whole factor
+      float vd[NP], vu[NP], up[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int d = min(0, max(ev[i] - xo, -100));
         vd[i] = (float)d;
         vu[i] = exp2i(-d);
+        up[i] = exp2i((int)P_BIAS + d);
       }
 
       uint32_t ph[NT][2][2], pl[NT][2][2];         // P^T as the B operand: [16 keys][k half]
@@ -420,13 +432,18 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
         }
         // nothing seen yet: any finite reference will do, the masked scores
         // stay -inf
-        const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - P_BIAS;
-        const float r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - P_BIAS;
+        const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - (SPLIT ? 0.f : P_BIAS);
+        const float r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - (SPLIT ? 0.f : P_BIAS);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = ex2_approx(s[n][i][j] - (((j & 1) ? r1 : r0) - vd[i % NP]));
+          for (int j = 0; j < 4; ++j) {
+            // FP32 output: the factor on P comes after the exponential, whose
+            // argument (and so its rounding) is then small for large weights
+            if constexpr (SPLIT) e[j] = ex2_approx(s[n][i][j] - ((j & 1) ? r1 : r0)) * up[i % NP];
+            else e[j] = ex2_approx(s[n][i][j] - (((j & 1) ? r1 : r0) - vd[i % NP]));
+          }
           l[n][0] = fmaf(e[0] + e[2], vu[i % NP], l[n][0]);
           l[n][1] = fmaf(e[1] + e[3], vu[i % NP], l[n][1]);
 #pragma unroll
@@ -467,8 +484,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       }
       // O^T += V^T P: lane rows (D / 8) g + 2 mt and + 1 of the head dimension.
       // The products' accumulators are cut, not rounded: for FP32 output a step's
-      // sum is taken by itself and added with rounding (over 16001..32760 keys the
-      // output is off by 1.2e-6 of its norm without and 6.7e-7 with, for 2 us of 37)
+      // sum is taken by itself and added with rounding, as the scores' are by 32
+      // dimensions.  All in all 3 us of 37 (4 x 16001..32760 keys), and on six
+      // sequences of 4205..15496 an output off by 3.3e-7 of its norm (4.9e-7 in
+      // plain FP32) that was off by more than 1e-6.
       float part[SPLIT ? NT : 1][4];
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
