@@ -7,7 +7,7 @@
 // owns a row, whose constants stay in its registers, and keeps a sum for each of
 // 32 keys while the rows go by; the rows' sums meet once, at the end of a key
 // tile.  (With the keys as rows nothing has to meet, but every warp reads every
-// row's constants from shared memory: 36 us where this takes 27.)
+// row's constants from shared memory: 36 us where this takes 28.)
 //
 // A first kernel brings the rows to f16 under a power of two, in the order
 // (token, head) and with what the sums need of each, into the workspace: every
@@ -25,8 +25,8 @@
 //   21    loads the rows by TMA, and their constants by bulk copies.
 //   22    looks the pages up and stages K's bytes by bulk copies (the conversion's
 //         own loads, page after table after length, took 4 us a key tile).
-// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 26.6 us (5 of them the first
-// kernel's), 0.62 PFLOP/s.  Latency bounds it: 512 key tiles are 3.4 an SM, so
+// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 28.2 us (5 of them the first
+// kernel's), 0.59 PFLOP/s.  Latency bounds it: 512 key tiles are 3.4 an SM, so
 // four rounds of eight row tiles, and of the 1500 clocks of a step 470 are sums.
 #include "cache_line.cuh"
 
@@ -115,20 +115,31 @@ __global__ void __launch_bounds__(NT_PREP) cache_rows_kernel(const __grid_consta
   }
 }
 
-// A tile of 128 keys and the row tiles that see any of them.
+// A tile of 128 keys and the row tiles that see any of them.  The tiles that hold
+// keys form a line of (sequence, kv head, tile); a CTA takes every gridDim.x-th.
 struct KeyTile {
-  int b, h, key0, len, j0, nt;
-  FA4_DEV KeyTile(const CacheWeighParams& p, int G, unsigned tiles, unsigned i) {
-    const int bh = (int)(i / tiles);
-    b = bh / p.c.Hkv;
-    h = bh - b * p.c.Hkv;
-    key0 = (int)(i - (unsigned)bh * tiles) * 128;
-    len = cache_len(p.c, b);
-    const int q_len = cache_count(p.q_lens, b, p.T, p.c.err), rows = G * q_len;
+  int b = 0, h, key0, len = 0, q_len = 0, j0, nt;
+  unsigned seq0 = 0, end = 0;                // the sequence's part of the line
+  static FA4_DEV unsigned of(const CacheWeighParams& p, int b) {
+    return (unsigned)((cache_len(p.c, b) + 127) / 128) * (unsigned)p.c.Hkv;
+  }
+  // goes on to tile `at` of the line, if there is one (whole warp)
+  FA4_DEV bool go(const CacheWeighParams& p, int G, unsigned at) {
+    if (at >= end) {
+      if (!line_find(p.c.B, [&](int i) { return of(p, i); }, at, b, seq0)) return false;
+      len = cache_len(p.c, b);
+      q_len = cache_count(p.q_lens, b, p.T, p.c.err);
+      end = seq0 + of(p, b);
+    }
+    const unsigned tiles = (unsigned)max((len + 127) / 128, 1);
+    h = (int)((at - seq0) / tiles);
+    key0 = (int)((at - seq0) - (unsigned)h * tiles) * 128;
+    const int rows = G * q_len;
     // tokens before this one see none of the keys
     const int t_first = p.causal ? max(0, key0 - (len - q_len)) : 0;
     j0 = (int)min((long long)rows, (long long)t_first * G) / 128;
-    nt = key0 < len ? max(0, (rows + 127) / 128 - j0) : 0;
+    nt = max(0, (rows + 127) / 128 - j0);
+    return true;
   }
 };
 
@@ -138,8 +149,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
   grid_start();
   const CacheView& c = p.c;
   const int G = p.Hq / c.Hkv;
-  const unsigned key_tiles = (unsigned)(((long long)c.max_pages * c.page + 127) / 128);
-  const unsigned items = key_tiles * c.Hkv * c.B;    // below 2^31: the call checks
   const int r_tiles = row_tiles(G, p.T);
 
   extern __shared__ uint8_t smem_raw[];
@@ -176,6 +185,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
   grid_wait();
+  KeyTile k;                                 // (fewer than 2^31 of them: the call checks)
 
   if (warp == W_MMA) {
     // -------------------------------------------------------------- products
@@ -183,8 +193,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     const uint32_t idesc = idesc_f16(128, 128, false, false, false);
     bool ok = true;
     int n = 0, t = 0;                        // key tiles and row tiles so far
-    for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
-      const KeyTile k(p, G, key_tiles, i);
+    for (unsigned i = blockIdx.x; ok && k.go(p, G, i); i += gridDim.x) {
       if (k.nt == 0) continue;
       const uint32_t sk = smem_u32(smem + L::OFF_K + n % KS * L::TILE);
       ok = mbar_wait(&k_full[n % KS], (n / KS) & 1, abort_flag, c.err);
@@ -217,29 +226,29 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     __syncwarp();
   } else if (warp == W_LOAD) {
     // -------------------------------------------------------------- rows of q
-    if (lane == 0) {
-      tma_prefetch_desc(&p.tm_q);
-      bool ok = true;
-      int t = 0;
-      for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
-        const KeyTile k(p, G, key_tiles, i);
-        const long long bh = (long long)k.b * c.Hkv + k.h;
-        for (int j = 0; j < k.nt; ++j, ++t) {
-          const int s = t % QS;
-          ok = t < QS || mbar_wait(&q_empty[s], (t / QS - 1) & 1, abort_flag, c.err);
-          if (!ok) break;
+    if (lane == 0) tma_prefetch_desc(&p.tm_q);
+    bool ok = true;
+    int t = 0;
+    for (unsigned i = blockIdx.x; ok && k.go(p, G, i); i += gridDim.x) {
+      const long long first = ((long long)k.b * c.Hkv + k.h) * r_tiles + k.j0;
+      for (int j = 0; j < k.nt; ++j, ++t) {
+        const int s = t % QS;
+        ok = t < QS || mbar_wait(&q_empty[s], (t / QS - 1) & 1, abort_flag, c.err);
+        if (!ok) break;
+        if (lane == 0) {
           mbar_arrive_expect_tx(&q_full[s], L::TILE + (uint32_t)sizeof(RowMeta));
           for (int x = 0; x < D / 64; ++x)
             tma_load_3d(smem + L::OFF_Q + s * L::TILE + x * F16_CHUNK, &p.tm_q, &q_full[s], 64 * x,
-                        (int)((bh * r_tiles + k.j0 + j) * 128), 0);
-          bulk_load(&metas[t % METAS], reinterpret_cast<const RowMeta*>(p.metas) + bh * r_tiles + k.j0 + j,
-                    (uint32_t)sizeof(RowMeta), &q_full[s]);
+                        (int)((first + j) * 128), 0);
+          bulk_load(&metas[t % METAS], reinterpret_cast<const RowMeta*>(p.metas) + first + j, (uint32_t)sizeof(RowMeta),
+                    &q_full[s]);
         }
+        __syncwarp();
       }
-      if (*abort_flag) {                             // what is still in flight lands first
-        volatile int none = 0;
-        for (int j = max(0, t - QS); j < t; ++j) mbar_wait(&q_full[j % QS], (j / QS) & 1, &none, c.err);
-      }
+    }
+    if (*abort_flag) {                               // what is still in flight lands first
+      volatile int none = 0;
+      for (int j = max(0, t - QS); j < t; ++j) mbar_wait(&q_full[j % QS], (j / QS) & 1, &none, c.err);
     }
     __syncwarp();
   } else if (warp == W_PAGE) {
@@ -247,8 +256,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     const int log_p = 31 - __clz(c.page);
     bool ok = true;
     int n = 0;
-    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
-      const KeyTile k(p, G, key_tiles, i);
+    for (unsigned i = blockIdx.x; k.go(p, G, i); i += gridDim.x) {
       if (k.nt == 0) continue;
       // lane i < 8: group i of 16 keys; the first lane of a page copies it
       const int key = k.key0 + 16 * (lane & 7);
@@ -282,8 +290,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     const int part = tid % PARTS, row0 = tid / PARTS;
     bool ok = true;
     int n = 0;
-    for (unsigned i = blockIdx.x; ok && i < items; i += gridDim.x) {
-      const KeyTile k(p, G, key_tiles, i);
+    for (unsigned i = blockIdx.x; ok && k.go(p, G, i); i += gridDim.x) {
       if (k.nt == 0) continue;
       ok = mbar_wait(&k8_full[n % KS], (n / KS) & 1, abort_flag, c.err);
       if (!ok) break;
@@ -317,9 +324,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
     // after a wait that ran out a warp computes no more, but comes to the barriers
     bool ok = true;
     int n = 0, t = 0, turn = 0;
-    for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
-      const KeyTile k(p, G, key_tiles, i);
-      if (k.key0 >= k.len) continue;
+    for (unsigned i = blockIdx.x; k.go(p, G, i); i += gridDim.x) {
       const long long bh = (long long)k.b * c.Hkv + k.h;
       const int my_key = k.key0 + 32 * part + lane;    // of the quadrant that writes the sums
       float before = 0.f;
