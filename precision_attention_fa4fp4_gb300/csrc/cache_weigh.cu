@@ -13,7 +13,7 @@
 // Up to 79 rows: bound by the matrix products and one exponential per score.  A
 // warp converts its 32 keys once and keeps them as f16 operands while it walks
 // over the rows, which the CTA prepares 64 at a time: 32 rows of 8 heads of 128,
-// 16 sequences of 2048, 22 us.  (The m16n8k32 E4M3 product would take the codes
+// 16 sequences of 2048, 25 us.  (The m16n8k32 E4M3 product would take the codes
 // as they are, but is made of conversions and other products here: 631
 // instructions a row tile, 175 us where this took 99.)
 #include "cache_line.cuh"
@@ -255,127 +255,132 @@ __global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __gr
   const CacheView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t4 = lane % 4;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int len = cache_len(c, b);
-  const int cta0 = blockIdx.x * UNIT;
-  if (cta0 >= len) return;
-  const int key0 = cta0 + 32 * warp;
-  const int q_len = cache_count(p.q_lens, b, p.T, c.err);
-  const int G = p.Hq / c.Hkv;
-  const int rows = G * q_len;
-  auto row_at = [&](int r) -> long long { return ((long long)b * p.Hq + h * G + r % G) * p.T + r / G; };
+  // every gridDim.x-th of the line of (sequence, head, 128 keys that are there)
+  int b = 0;
+  unsigned seq0 = 0;
+  auto units = [&](int i) { return (unsigned)((cache_len(c, i) + UNIT - 1) / UNIT) * (unsigned)c.Hkv; };
+  for (unsigned u = blockIdx.x; line_find(c.B, units, u, b, seq0); u += gridDim.x) {
+    const int len = cache_len(c, b);
+    const unsigned per = (unsigned)(len + UNIT - 1) / UNIT;
+    const int h = (int)((u - seq0) / per), cta0 = (int)((u - seq0) % per) * UNIT;
+    const int key0 = cta0 + 32 * warp;
+    const int q_len = cache_count(p.q_lens, b, p.T, c.err);
+    const int G = p.Hq / c.Hkv;
+    const int rows = G * q_len;
+    auto row_at = [&](int r) -> long long { return ((long long)b * p.Hq + h * G + r % G) * p.T + r / G; };
 
-  uint32_t ka[2][D / 16][4];
-  float kx[2];
-  int end[2];                                      // keys of each 16 that are there: below it
+    uint32_t ka[2][D / 16][4];
+    float kx[2];
+    int end[2];                                      // keys of each 16 that are there: below it
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int key = key0 + 16 * i;
-    int pg = -1;
-    if (key < len) pg = cache_page(c, c.table, b, key / c.page);
-    end[i] = pg < 0 ? 0 : len;
-    const long long ph = (long long)max(pg, 0) * c.Hkv + h;
-    kx[i] = e8m0_value(*(c.ks + ph));
-    const uint8_t* at = c.k + (ph * c.page + key % c.page + g) * D + 16 * t4;
+    for (int i = 0; i < 2; ++i) {
+      const int key = key0 + 16 * i;
+      int pg = -1;
+      if (key < len) pg = cache_page(c, c.table, b, key / c.page);
+      end[i] = pg < 0 ? 0 : len;
+      const long long ph = (long long)max(pg, 0) * c.Hkv + h;
+      kx[i] = e8m0_value(*(c.ks + ph));
+      const uint8_t* at = c.k + (ph * c.page + key % c.page + g) * D + 16 * t4;
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) {
-      const uint4 lo = *(reinterpret_cast<const uint4*>(at + 64 * x));
-      const uint4 hi = *(reinterpret_cast<const uint4*>(at + 8 * D + 64 * x));
-      const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
+      for (int x = 0; x < D / 64; ++x) {
+        const uint4 lo = *(reinterpret_cast<const uint4*>(at + 64 * x));
+        const uint4 hi = *(reinterpret_cast<const uint4*>(at + 8 * D + 64 * x));
+        const uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, e[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        ka[i][4 * x + w][0] = e4m3x2_to_f16x2(a[w]);
-        ka[i][4 * x + w][1] = e4m3x2_to_f16x2(e[w]);
-        ka[i][4 * x + w][2] = e4m3x2_hi_to_f16x2(a[w]);
-        ka[i][4 * x + w][3] = e4m3x2_hi_to_f16x2(e[w]);
-      }
-    }
-  }
-  float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-
-  // tokens before these see none of the CTA's keys, of the warp's
-  const int t_cta = p.causal ? max(0, cta0 - (len - q_len)) : 0;
-  const int t_warp = p.causal ? max(0, key0 - (len - q_len)) : 0;
-  const int first = (int)min((long long)rows, (long long)t_warp * G);
-  for (int r0 = (int)min((long long)rows, (long long)t_cta * G) / BLOCK * BLOCK; r0 < rows; r0 += BLOCK) {
-    QRaw<D> raw[BLOCK / 8 / NW];
-    float lse[BLOCK / 8 / NW];
-#pragma unroll
-    for (int j = 0; j < BLOCK / 8 / NW; ++j) {
-      const int r = r0 + 8 * (warp + j * NW) + g;
-      raw[j].fetch(r < rows ? reinterpret_cast<const __nv_bfloat16*>(p.q) + row_at(r) * D : nullptr, t4);
-      lse[j] = r < rows ? *(p.lse + row_at(r)) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < BLOCK / 8 / NW; ++j) {
-      const int n = warp + j * NW;
-      QFrag<D> q;
-      const float e = raw[j].convert(q);
-#pragma unroll
-      for (int x = 0; x < QW; ++x)
-        s_q[n][x][lane] = make_uint4(q.b[2 * x][0], q.b[2 * x][1], q.b[2 * x + 1][0], q.b[2 * x + 1][1]);
-      if (t4 == 0) {
-        float ref, fac;
-        reference(lse[j], r0 + 8 * n + g < rows, ref, fac);
-        s_ref[8 * n + g] = ref;
-        s_fac[8 * n + g] = fac;
-        s_fx[8 * n + g] = fac == 0.f ? 0.f : p.c2 * e;
-      }
-    }
-    __syncthreads();
-    if (key0 >= len) continue;                     // the sequence's last keys: this warp has none
-    for (int n = max(0, (first - r0) / 8); n < BLOCK / 8 && r0 + 8 * n < rows; ++n) {
-      float s[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll
-      for (int x = 0; x < QW; ++x) {
-        const uint4 q = s_q[n][x][lane];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          mma_16816(s[i], ka[i][2 * x][0], ka[i][2 * x][1], ka[i][2 * x][2], ka[i][2 * x][3], q.x, q.y);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          mma_16816(s[i], ka[i][2 * x + 1][0], ka[i][2 * x + 1][1], ka[i][2 * x + 1][2], ka[i][2 * x + 1][3], q.z, q.w);
-      }
-      const float2 fx = *reinterpret_cast<const float2*>(&s_fx[8 * n + 2 * t4]);
-      const float2 ref = *reinterpret_cast<const float2*>(&s_ref[8 * n + 2 * t4]);
-      const float2 fac = *reinterpret_cast<const float2*>(&s_fac[8 * n + 2 * t4]);
-      // the tile's first token sees the fewest keys
-      const int r_min = r0 + 8 * n;
-      const bool full = !p.causal || len - q_len + r_min / G + 1 >= key0 + 32;
-      int vis[2] = {len, len};
-      if (!full) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) vis[j] = len - q_len + (r_min + 2 * t4 + j) / G + 1;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f0 = kx[i] * fx.x, f1 = kx[i] * fx.y;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float e = ex2_approx(fmaf(s[i][j], (j & 1) ? f1 : f0, (j & 1) ? -ref.y : -ref.x));
-          if (!full && key0 + 16 * i + g + 8 * (j >> 1) >= vis[j & 1]) e = 0.f;
-          w[i][j >> 1] = fmaf(e, (j & 1) ? fac.y : fac.x, w[i][j >> 1]);
+        for (int w = 0; w < 4; ++w) {
+          ka[i][4 * x + w][0] = e4m3x2_to_f16x2(a[w]);
+          ka[i][4 * x + w][1] = e4m3x2_to_f16x2(e[w]);
+          ka[i][4 * x + w][2] = e4m3x2_hi_to_f16x2(a[w]);
+          ka[i][4 * x + w][3] = e4m3x2_hi_to_f16x2(e[w]);
         }
       }
     }
-  }
+    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+
+    // tokens before these see none of the CTA's keys, of the warp's
+    const int t_cta = p.causal ? max(0, cta0 - (len - q_len)) : 0;
+    const int t_warp = p.causal ? max(0, key0 - (len - q_len)) : 0;
+    const int first = (int)min((long long)rows, (long long)t_warp * G);
+    for (int r0 = (int)min((long long)rows, (long long)t_cta * G) / BLOCK * BLOCK; r0 < rows; r0 += BLOCK) {
+      QRaw<D> raw[BLOCK / 8 / NW];
+      float lse[BLOCK / 8 / NW];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < BLOCK / 8 / NW; ++j) {
+        const int r = r0 + 8 * (warp + j * NW) + g;
+        raw[j].fetch(r < rows ? reinterpret_cast<const __nv_bfloat16*>(p.q) + row_at(r) * D : nullptr, t4);
+        lse[j] = r < rows ? *(p.lse + row_at(r)) : 0.f;
+      }
+      __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 1);
-      w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 2);
-      const int key = key0 + 16 * i + 8 * r + g;
-      if (t4 == 0 && key < len) {
-        const long long at = ((long long)b * c.Hkv + h) * c.max_pages * c.page + key;
-        p.w_out[at] = p.w_in[at] + (key < end[i] ? w[i][r] : 0.f);
+      for (int j = 0; j < BLOCK / 8 / NW; ++j) {
+        const int n = warp + j * NW;
+        QFrag<D> q;
+        const float e = raw[j].convert(q);
+#pragma unroll
+        for (int x = 0; x < QW; ++x)
+          s_q[n][x][lane] = make_uint4(q.b[2 * x][0], q.b[2 * x][1], q.b[2 * x + 1][0], q.b[2 * x + 1][1]);
+        if (t4 == 0) {
+          float ref, fac;
+          reference(lse[j], r0 + 8 * n + g < rows, ref, fac);
+          s_ref[8 * n + g] = ref;
+          s_fac[8 * n + g] = fac;
+          s_fx[8 * n + g] = fac == 0.f ? 0.f : p.c2 * e;
+        }
+      }
+      __syncthreads();
+      if (key0 >= len) continue;                     // the sequence's last keys: this warp has none
+      for (int n = max(0, (first - r0) / 8); n < BLOCK / 8 && r0 + 8 * n < rows; ++n) {
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll
+        for (int x = 0; x < QW; ++x) {
+          const uint4 q = s_q[n][x][lane];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mma_16816(s[i], ka[i][2 * x][0], ka[i][2 * x][1], ka[i][2 * x][2], ka[i][2 * x][3], q.x, q.y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mma_16816(s[i], ka[i][2 * x + 1][0], ka[i][2 * x + 1][1], ka[i][2 * x + 1][2], ka[i][2 * x + 1][3], q.z, q.w);
+        }
+        const float2 fx = *reinterpret_cast<const float2*>(&s_fx[8 * n + 2 * t4]);
+        const float2 ref = *reinterpret_cast<const float2*>(&s_ref[8 * n + 2 * t4]);
+        const float2 fac = *reinterpret_cast<const float2*>(&s_fac[8 * n + 2 * t4]);
+        // the tile's first token sees the fewest keys
+        const int r_min = r0 + 8 * n;
+        const bool full = !p.causal || len - q_len + r_min / G + 1 >= key0 + 32;
+        int vis[2] = {len, len};
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) vis[j] = len - q_len + (r_min + 2 * t4 + j) / G + 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f0 = kx[i] * fx.x, f1 = kx[i] * fx.y;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float e = ex2_approx(fmaf(s[i][j], (j & 1) ? f1 : f0, (j & 1) ? -ref.y : -ref.x));
+            if (!full && key0 + 16 * i + g + 8 * (j >> 1) >= vis[j & 1]) e = 0.f;
+            w[i][j >> 1] = fmaf(e, (j & 1) ? fac.y : fac.x, w[i][j >> 1]);
+          }
+        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 1);
+        w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 2);
+        const int key = key0 + 16 * i + 8 * r + g;
+        if (t4 == 0 && key < len) {
+          const long long at = ((long long)b * c.Hkv + h) * c.max_pages * c.page + key;
+          p.w_out[at] = p.w_in[at] + (key < end[i] ? w[i][r] : 0.f);
+        }
+      }
+  }
 }
 
 template <int D, int NT>
@@ -401,7 +406,8 @@ cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   if (rows <= 8) return p.c.d == 128 ? launch_few<128, 1>(p, st) : launch_few<64, 1>(p, st);
   if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
   const long long cap = (long long)p.c.max_pages * p.c.page;
-  const dim3 grid((unsigned)((cap + UNIT - 1) / UNIT), (unsigned)p.c.Hkv, (unsigned)p.c.B);
+  const long long all = (cap + UNIT - 1) / UNIT * p.c.Hkv * p.c.B, most = 4LL * kSMs;
+  const dim3 grid((unsigned)(all < most ? all : most));
   return launch_next(p.c.d == 128 ? cache_weigh_rows_kernel<128> : cache_weigh_rows_kernel<64>, grid, 32 * NW, 0, st, p);
 }
 
