@@ -79,9 +79,9 @@ bool cache_weigh_fits(int B, int Hkv, int page, int max_pages);
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st);
 // The same for many rows (query heads of a kv head x T), with a workspace.
 // Keys x sequences, heads of 128, 8 kv heads, us by mma.sync / by tcgen05:
-//   2048 x 16:  32 rows 22 / 31,  64 rows 29 / 31,  96 rows 42 / 31,  256 rows 90 / 39
-//   8192 x 1:   32 rows 7 / 13,   64 rows 10 / 13,  96 rows 14 / 13,  256 rows 28 / 15
-// heads of 64, 4096 x 16: 64 rows 43 / 49, 96 rows 59 / 49.
+//   2048 x 16:  32 rows 25 / 42,  64 rows 34 / 42,  96 rows 49 / 42,  256 rows 106 / 48
+//   8192 x 1:   32 rows 8 / 14,   64 rows 11 / 14,  96 rows 14 / 14,  256 rows 29 / 16
+// heads of 64, 4096 x 16: 64 rows 49 / 58, 96 rows 68 / 58.
 constexpr int WEIGH_MANY = 80;
 size_t cache_weigh_rows_bytes(int B, int Hq, int Hkv, int T, int d, size_t* all);
 cudaError_t launch_cache_weigh_rows(const CacheWeighParams& p, cudaStream_t st);
