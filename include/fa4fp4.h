@@ -364,8 +364,9 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_append(const fa4fp4_cache* cache, const vo
  * that sees no key gets o = 0 and lse = -inf; rows t >= q_lens[b] are not
  * written.  The products are exact in the codes, the sums FP32.  P is rounded
  * to f16 (half a step: 2^-11) under a power of two that takes V's page scales
- * in, so that a P far below the largest V of its 128 keys is off by 2^-36 of
- * that V at most; f32 output takes P as a sum of two f16 (2^-22).  Scores up to
+ * in, so that a P far below the largest V of its 128 keys (seen or not) is off by
+ * 2^-36 of that V at most, or by 2^-90 of a far larger sum that it is added to;
+ * f32 output takes P as a sum of two f16 (2^-22).  Scores up to
  * 2^22 in magnitude; beyond, the rounding of their maximum takes P out of its
  * range.  The result does not depend on anything but the arguments.  `workspace`: at least
  * fa4fp4_cache_fwd_workspace_bytes(...) bytes of device memory

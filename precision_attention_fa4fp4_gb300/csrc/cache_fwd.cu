@@ -33,18 +33,19 @@
 // loads through L1 allow (16-byte asynchronous copies of the same bytes, and
 // loads into registers, both stopped at 4.8 TB/s).  The codes are used
 // unscaled: K's page scale multiplies the scores, V's goes into the exponent of
-// P, relative to the accumulator's own exponent.
+// P, relative to that of the row's accumulator.
 //
 // 64 sequences of 1..8192 tokens, 32 / 8 heads of 128: 107-110 us, 5.2 TB/s; what
 // is missing to a copy's 6.7 are the first 5 us of a launch and the ends of row
 // blocks.  One of 1000: 9.0 us (start 2, lens and pages 1.5, first keys 2, join
 // 2-3).  With 9 to 16 rows and FP32 output instructions bound it: 4 sequences of
-// 16001..32760, 8 heads of 64, 40 us, 2.5 TB/s.
+// 16001..32760, 8 heads of 64, 42 us, 2.4 TB/s.
 //
 // Roundings: q to f16 under a power of two (2^-32 of the row's largest); P to
 // f16 under a factor 2^15 and V's relative exponent (2^-11 of P, or 2^-36 of the
-// largest V of the 32 keys if that is more), for FP32 output as a sum of two f16
-// (2^-22, or the same 2^-36).  The normalizer sums the FP32 values of P.
+// largest V of the 32 keys or 2^-90 of the row's own sum if that is more), for FP32
+// output as a sum of two f16 (2^-22, or the same).  The normalizer sums the FP32
+// values of P.
 #include "cache_line.cuh"
 
 namespace fa4 {
@@ -53,12 +54,18 @@ namespace {
 constexpr int NW = LINE_WARPS;
 // log2 of the factor on P: the largest P is half of f16's largest power
 constexpr float P_BIAS = 15.f;
-// How far a step's greatest V exponent may lie below the accumulator's before
-// the accumulator's is lowered: P's smallest f16 step, 2^-24 under its factor
-// 2^15, is then at most 2^-35 of the step's largest V, its half 2^-36.  Lowering
-// is bounded, so that the accumulator stays below 2^(40 + 80) (its terms: 2^15 *
-// 448, fewer than 2^17 of them a warp).
-constexpr int V_DOWN = 4, V_LOWER = 80;
+// How far a step's greatest V exponent may lie below that of a row's accumulator
+// before the latter is lowered: P's smallest f16 step, 2^-24 under its factor 2^15,
+// is then at most 2^-35 of the step's largest V, its half 2^-36.  It is lowered only
+// as far as leaves the row's sums below 2^O_MOST, beside which later terms (2^15 *
+// 448, fewer than 2^20 of them a warp) are none: what a page far below loses then
+// is 2^-90 of the row's own sum.  Rows have exponents of their own, as the sums of
+// rows over the same keys may lie as far apart as V does.
+constexpr int V_DOWN = 4, O_MOST = 100;
+// A factor of 2^-P_NONE leaves no f16 of P.
+constexpr float P_NONE = 48.f;
+// 2^x for a whole number x in [-126, 127]: x + 127 is read off the significand.
+FA4_DEV float exp2f_whole(float x) { return __uint_as_float(__float_as_uint(x + (12582912.f + 127.f)) << 23); }
 // Rows of a kv head above which the kernel for many rows takes over.  It takes
 // the same time for 1 to 128 of them, this one in proportion to blocks of 16.
 // Keys x sequences, heads of 128, 8 kv heads, us here / there:
@@ -303,9 +310,15 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
 
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];
-    int xo = -127;                                 // o is in units of 2^xo
+    // o is in units of 2^xo; the first step's to begin with
+    float first = -127.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (window.page(u0, i) >= 0) first = fmaxf(first, (float)((window.scales(u0, i) >> 8) - 127));
+    float xo[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      xo[n][0] = xo[n][1] = first;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -322,13 +335,13 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       const int4 what = steps[st];
       int pos[NP];
       float kxc[NP];
-      int ev[NP];
+      float ev[NP];                                // V's exponents
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         pos[i] = i ? what.z : what.x;
         const int sc = i ? what.w : what.y;
         kxc[i] = e8m0_value(sc & 0xff);
-        ev[i] = pos[i] == NOWHERE ? -1000 : (sc >> 8) - 127;
+        ev[i] = pos[i] == NOWHERE ? -1000.f : (float)((sc >> 8) - 127);
       }
       // scores of 32 keys: rows g, g + 8 of each 16, columns 2 t4, 2 t4 + 1
       float s[NT][2][4];
@@ -369,31 +382,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
 #pragma unroll
       for (int i = 0; i < NP; ++i) full = full && pos[i] + 32 / NP <= vis_min;
 
-      // V's exponents relative to the accumulator's go into P.  A page above it
-      // raises it, a step far below it lowers it
-      int ev_max = ev[0];
+      float ev_max = ev[0];
 #pragma unroll
-      for (int i = 1; i < NP; ++i) ev_max = max(ev_max, ev[i]);
-      if (ev_max > -1000 && (ev_max > xo || ev_max < xo - V_DOWN)) {
-        const int to = max(ev_max, xo - V_LOWER);
-        const float by = pow2_any(xo - to);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[n][i][j] *= by;
-        xo = to;
-      }
-      // exponent on P, what undoes it for l, and P's whole factor
-      float vd[NP], vu[NP], up[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int d = min(0, max(ev[i] - xo, -100));
-        vd[i] = (float)d;
-        vu[i] = exp2i(-d);
-        up[i] = exp2i((int)P_BIAS + d);
-      }
+      for (int i = 1; i < NP; ++i) ev_max = fmaxf(ev_max, ev[i]);
 
       uint32_t ph[NT][2][2], pl[NT][2][2];         // P^T as the B operand: [16 keys][k half]
 #pragma unroll
@@ -430,6 +421,40 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
             }
           }
         }
+        // V's exponents relative to the accumulators' go into P.  A page above an
+        // accumulator raises it, a step far below lowers it
+        auto off = [&](float x) { return ev_max > x || ev_max < x - V_DOWN; };
+        if (ev_max > -1000.f && __any_sync(0xffffffffu, off(xo[n][0]) || off(xo[n][1]))) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t most = 0;                     // of the row's sums, over the lanes that hold it
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              most = max(most, max(__float_as_uint(o[n][i][j]) & 0x7fffffffu, __float_as_uint(o[n][i][2 + j]) & 0x7fffffffu));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 4));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+            const int x = (int)xo[n][j], e = (int)ev_max;
+            const int room = max(0, O_MOST + 126 - (int)(most >> 23));      // up to 226
+            const int to = !off(xo[n][j]) ? x : most == 0 ? e : max(e, x - room);
+            const int up = most == 0 ? 0 : x - to;
+            const float by = pow2_any(min(up, 100)), more = exp2i(max(up - 100, 0));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[n][i][j] = o[n][i][j] * by * more;
+              o[n][i][2 + j] = o[n][i][2 + j] * by * more;
+            }
+            xo[n][j] = (float)to;
+          }
+        }
+        float vd[2][NP], up[2][NP];                // exponent on P, its whole factor
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            vd[j][i] = fmaxf(ev[i] - xo[n][j], -P_NONE);
+            up[j][i] = exp2f_whole(P_BIAS + vd[j][i]);
+          }
         // nothing seen yet: any finite reference will do, the masked scores
         // stay -inf
         const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - (SPLIT ? 0.f : P_BIAS);
@@ -441,11 +466,11 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
           for (int j = 0; j < 4; ++j) {
             // FP32 output: the factor on P comes after the exponential, whose
             // argument (and so its rounding) is then small for large weights
-            if constexpr (SPLIT) e[j] = ex2_approx(s[n][i][j] - ((j & 1) ? r1 : r0)) * up[i % NP];
-            else e[j] = ex2_approx(s[n][i][j] - (((j & 1) ? r1 : r0) - vd[i % NP]));
+            if constexpr (SPLIT) e[j] = ex2_approx(s[n][i][j] - ((j & 1) ? r1 : r0)) * up[j & 1][i % NP];
+            else e[j] = ex2_approx(s[n][i][j] - (((j & 1) ? r1 : r0) - vd[j & 1][i % NP]));
           }
-          l[n][0] = fmaf(e[0] + e[2], vu[i % NP], l[n][0]);
-          l[n][1] = fmaf(e[1] + e[3], vu[i % NP], l[n][1]);
+          l[n][0] = fmaf(e[0] + e[2], exp2f_whole(-vd[0][i % NP]), l[n][0]);
+          l[n][1] = fmaf(e[1] + e[3], exp2f_whole(-vd[1][i % NP]), l[n][1]);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const uint32_t x = pack_f16x2(e[2 * r], e[2 * r + 1]);
@@ -539,9 +564,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     if (*abort_flag) return;                       // the error word says why
 
     // the four warps' shares of the keys
-    const float unit = pow2_any(xo);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      const float unit[2] = {pow2_any((int)xo[n][0]), pow2_any((int)xo[n][1])};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
@@ -551,7 +576,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
         if (g == 0) { s_m[warp][col] = m[n][j]; s_l[warp][col] = l[n][j]; }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j] * unit, o[n][i][2 + j] * unit);
+          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j] * unit[j], o[n][i][2 + j] * unit[j]);
       }
     }
     __syncthreads();

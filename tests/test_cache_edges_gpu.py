@@ -1,0 +1,190 @@
+"""The 8-bit cache at the ends of its range: runs of zero tokens, scales that
+fall or rise by hundreds of powers of two, values close to the largest bf16.
+
+The attention's bound is that of the other cache tests (weights and P relative,
+the output's half step), but for what P loses as a f16 number: with U the unit of
+128 keys (of a token's own list) and V_U its largest |v|, seen or not,
+
+  |o - ref| <= (4 eps + 2^-19 + p_err) * spread + out_err * |ref|
+               + 2^-35 * sum over U of 128 V_U e^min(0, M_U - m)
+
+M_U being the largest score seen up to the end of U: a lost part of P shrinks with
+everything else when a larger score comes later.  (A P times 2^15 and the ratio of
+V's page scale to the accumulator's, at most 2^4 above that of its keys, is off by
+half of f16's smallest step 2^-24: 2^-36 of a scale whose 448 is below 2 V_U.  2^12
+and 2^1 in the kernel for many rows: the same.  An accumulator that holds values
+more than 2^60 above is not brought down to a unit's own scale: that leaves 2^-96 of
+those, which the terms of their own units contain.)"""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as R
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def queries(B, Hq, T, d, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(B, Hq, T, d, generator=g) * scale).to(torch.bfloat16).cuda()
+
+
+def cache_of(fa, k, v, page, seed, first=0, stale=0xff):
+    """A cache of the sequences k, v: [B][H, n_b, d] float tensors."""
+    lens = [x.shape[1] for x in k]
+    H, d = k[0].shape[0], k[0].shape[2]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=seed, first=first, stale=stale)
+    T = max(lens)
+    pad = lambda xs: torch.stack([torch.nn.functional.pad(x, (0, 0, 0, T - x.shape[1])) for x in xs])
+    fa.cache_append(cache, pad(k).bfloat16().cuda(), pad(v).bfloat16().cuda(), table, torch.zeros_like(ln), n_new=ln)
+    return cache, table, ln, lens
+
+
+def reference(ref, q, lens, T, f32, causal=True, scale=None, pages=None, heads=None):
+    """o, lse and their bounds for T query tokens of every sequence (and the first
+    `heads` kv heads)."""
+    G, P = q.shape[1] // ref.H, ref.page
+    q = q[:, :G * (heads or ref.H)]
+    B, Hq, _, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    o, lse, tol = np.zeros(q.shape), np.full((B, Hq, T), -np.inf), np.zeros(q.shape)
+    lse_tol = np.zeros((B, Hq, T))
+    for b in range(B):
+        L = int(lens[b])
+        for hk in range(Hq // G):
+            K, V = ref.read("k", b, hk, L), ref.read("v", b, hk, L)
+            for t in range(T):
+                n = ref.sees(L, T, t, causal)
+                at = np.arange(L)
+                if pages is not None:
+                    at = np.concatenate([np.arange(p * P, min(p * P + P, L)) for p in pages[b, hk, t] if p >= 0] or [at[:0]])
+                    unit = np.concatenate([np.arange(i * P, i * P + min(P, L - p * P)) // 128
+                                           for i, p in enumerate(pages[b, hk, t]) if p >= 0] or [at[:0]])
+                else:
+                    unit = at // 128
+                see = at < n
+                if not see.any():
+                    continue
+                k, v = K[at], V[at]
+                top = np.abs(v).max(1)
+                for h in range(hk * G, hk * G + G):
+                    s = np.where(see, k @ q[b, h, t] * scale, -np.inf)
+                    m = s.max()
+                    p = np.exp(s - m)
+                    o[b, h, t] = p @ v / p.sum()
+                    lse[b, h, t] = m + np.log(p.sum())
+                    e = (np.abs(k) @ np.abs(q[b, h, t]))[see].max() * scale * d * 2.0 ** -23
+                    lost, upto = 0.0, -np.inf
+                    for u in np.unique(unit):
+                        upto = max(upto, s[unit == u].max())
+                        if upto > -np.inf:
+                            lost += 2.0 ** -35 * 128 * top[unit == u].max() * np.exp(min(0.0, upto - m))
+                    tol[b, h, t] = (4 * e + 2.0 ** -19 + (2.0 ** -22 if f32 else 2.0 ** -11)) * (p @ np.abs(v) / p.sum())
+                    tol[b, h, t] += (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(o[b, h, t]) + lost + 1e-37
+                    lse_tol[b, h, t] = 2 * e + 2.0 ** -20 + 2.0 ** -22 * abs(lse[b, h, t])
+    return o, lse, tol, lse_tol
+
+
+def check(fa, q, cache, table, ln, lens, f32, causal=True, scale=None, pages=None, heads=None):
+    o, lse = fa.cache_fwd(q, cache, table, ln, causal=causal, softmax_scale=scale or 0.0, pages=pages,
+                          out_dtype=fa.OUT_F32 if f32 else fa.OUT_BF16)
+    fa.sync_status()
+    ref = R.Ref.of(cache, table)
+    want, wl, tol, lt = reference(ref, f64(q), lens, q.shape[2], f32, causal, scale,
+                                  None if pages is None else pages.cpu().numpy(), heads)
+    o, lse = f64(o[:, :wl.shape[1]]), f64(lse[:, :wl.shape[1]])
+    assert np.isfinite(o).all()
+    bad = np.abs(o - want) - tol
+    assert bad.max() <= 0, f"o off by {bad.max():.3g} over its bound"
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isneginf(lse), ~seen) and not o[~seen].any()
+    assert (np.abs(lse - wl)[seen] <= lt[seen]).all()
+
+
+# ------------------------------------------------------------------ V's exponents, few rows
+def zero_runs(H, d, seed, alike=1):
+    """V is zero over 1, 2, 3 and 5 blocks of 128 tokens between others and at the
+    end; and the same in sequences of few tokens.  `alike` times as many heads: with
+    enough of them one CTA goes through several units of a head."""
+    g = torch.Generator().manual_seed(seed)
+    k, v = [], []
+    for runs in ([128, -128, 128, -256, 100, -384, 130, -640, 60], [256, -1300], [-300, 200, -1024, 300, -700],
+                 [3, -500], [-513], [16, -17, 5]):
+        n = sum(abs(r) for r in runs)
+        k.append(torch.randn(H, n, d, generator=g))
+        x = torch.randn(H, n, d, generator=g)
+        at = 0
+        for r in runs:
+            if r < 0:
+                x[:, at:at - r] = 0
+            at += abs(r)
+        v.append(x)
+    return [x.repeat(alike, 1, 1) for x in k], [x.repeat(alike, 1, 1) for x in v]
+
+
+def falling(H, d, seed, first, last, keys, steps, alike=1):
+    """|v| falls (or rises) from 2^first to 2^last in equal steps of `keys` tokens."""
+    g = torch.Generator().manual_seed(seed)
+    n = keys * steps
+    k = torch.randn(H, n, d, generator=g)
+    v = torch.randn(H, n, d, generator=g)
+    for i in range(steps):
+        v[:, i * keys:(i + 1) * keys] *= 2.0 ** (first + (last - first) * i / max(steps - 1, 1))
+    return [k.repeat(alike, 1, 1)], [v.repeat(alike, 1, 1)]
+
+
+FEW = [(64, 16, 2, 3, 1, False), (64, 64, 1, 1, 5, True), (128, 32, 2, 4, 1, False), (128, 128, 1, 3, 4, True),
+       (128, 16, 1, 2, 8, False), (64, 128, 2, 4, 16, False), (128, 64, 1, 1, 1, True)]
+
+
+@pytest.mark.parametrize("alike", [1, 60])
+@pytest.mark.parametrize("d,page,H,G,T,f32", FEW)
+def test_fwd_runs_of_zero_v(d, page, H, G, T, f32, alike):
+    fa = require_gpu()
+    k, v = zero_runs(H, d, 1, alike)
+    cache, table, ln, lens = cache_of(fa, k, v, page, 2)
+    q = queries(len(lens), H * alike * G, T, d, 3)
+    for causal in (True, False):
+        check(fa, q, cache, table, ln, lens, f32, causal, heads=H)
+    sel = fa.cache_select(q, cache, table, ln, 700 // page + 1)
+    check(fa, q, cache, table, ln, lens, f32, pages=sel, heads=H)
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("first,last", [(100, -100), (-100, 100), (70, -126), (0, -120)])
+@pytest.mark.parametrize("T,keys,steps,alike", [(1, 128, 5, 1), (1, 128, 5, 240), (3, 256, 9, 1), (2, 256, 9, 240),
+                                                (1, 640, 2, 240), (12, 64, 21, 1), (4, 64, 21, 240)])
+def test_fwd_v_falls_and_rises(T, keys, steps, alike, first, last, f32):
+    fa = require_gpu()
+    d, page, G = 128, 32, 4
+    k, v = falling(1, d, 4, first, last, keys, steps, alike)
+    cache, table, ln, lens = cache_of(fa, k, v, page, 5)
+    q = queries(1, alike * G, T, d, 6)
+    check(fa, q, cache, table, ln, lens, f32, heads=1)
+    all_pages = torch.arange(table.shape[1], dtype=torch.int32, device="cuda").expand(1, alike, T, -1).contiguous()
+    check(fa, q, cache, table, ln, lens, f32, pages=all_pages, heads=1)
+
+
+@pytest.mark.parametrize("T,f32", [(1, True), (1, False), (4, True), (4, False)])
+def test_fwd_large_v_without_weight(T, f32):
+    """Far larger values whose weight a later score takes away from some of the
+    rows only: those rows' small values keep their accuracy, the others theirs."""
+    fa = require_gpu()
+    d, page, H, G, n = 64, 16, 480, 4, 1700
+    g = torch.Generator().manual_seed(7)
+    k = (torch.randn(1, n, d, generator=g) * 0.1).repeat(H, 1, 1)
+    v = torch.randn(1, n, d, generator=g).repeat(H, 1, 1)
+    v[:, :300] *= 2.0 ** 100
+    v[:, 300:800] *= 2.0 ** 40
+    v[:, 1200:] *= 2.0 ** -30
+    k[:, 800:, 0] = 60.0                  # scores 60 q_0: 0 or 300
+    cache, table, ln, lens = cache_of(fa, [k], [v], page, 8)
+    q = queries(1, H * G, T, d, 9)
+    q[:, :, :, 0] = 0
+    q[:, ::2, :, 0] = 5
+    check(fa, q, cache, table, ln, lens, f32, scale=1.0, heads=1)
