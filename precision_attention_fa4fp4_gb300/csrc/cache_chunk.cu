@@ -26,14 +26,14 @@
 //   13        looks the pages up, stages their bytes by bulk copies, and works
 //             the tile's factors out for the softmax.
 // K's page scale multiplies the scores (folded into the exponent's FMA), V's
-// goes into the exponent of P relative to the accumulator's own exponent, which
+// goes into the exponent of P relative to that of the row's accumulator, which
 // is at most V_DOWN above the tile's largest: half of P's smallest f16 step is
-// then 2^-36 of a tile's largest V.
+// then 2^-36 of a tile's largest V (or 2^-90 of what is in the accumulator already).
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).  Two f16 stages of
 // K and of V beside both query tiles leave room for one staged tile of bytes
 // each: the copy of tile j + 1 runs while tile j is multiplied.
 //
-// 2 x 1024 tokens over 8192, 32 / 8 heads of 128: 225 us, 1.15 PFLOP/s, 0.62 of
+// 2 x 1024 tokens over 8192, 32 / 8 heads of 128: 227 us, 1.14 PFLOP/s, 0.61 of
 // the measured cuBLAS rate.  Four fifths of that are the tiles' loop, 3300 clocks
 // for both tiles: a tile's own chain of softmax (2150) and products (1100), with
 // the other tile's in between; the tensor cores are busy in 2050 of them and
@@ -54,10 +54,16 @@ constexpr uint32_t TMEM_COLS = 512;
 // log2 of the factor on P, and how far a row's maximum may pass the reference of
 // its exponents before the reference follows: P stays below 2^15.
 constexpr float P_BIAS = 12.f, M_UP = 3.f;
-// V_DOWN: f16's smallest step 2^-24 is then 2^-35 of a tile's largest V.  The
-// accumulator's exponent is lowered by V_LOWER at most at once, as in the kernel
-// for few rows.
-constexpr int V_DOWN = 1, V_LOWER = 80;
+// V_DOWN: f16's smallest step 2^-24 is then 2^-35 of a tile's largest V.  The loader
+// gives a tile's exponent; a row whose accumulator would pass 2^O_MOST on the way
+// there stops above it, and P takes the difference.  The bound of an accumulator is
+// counted instead of read: a tile adds at most 2^O_TILE (2^15 * 448 * 128), and fewer
+// than 2^23 of them are added.
+constexpr int V_DOWN = 1;
+constexpr float O_MOST = 100.f, O_TILE = 31.f;
+// A factor of 2^-P_NONE leaves no f16 of P, and two of them leave FP32 the weights
+// from 2^-40 on for the normalizer.
+constexpr int P_NONE = 48;
 constexpr int METAS = 4;
 // Tiles of a share at least.  64 tokens over 8192, 32 / 8 heads: shares of 4
 // tiles 55 us, of 8 43 us; over 1024 they are 26 and 23 us.
@@ -93,9 +99,9 @@ struct Block {
 // Factors of a 128-key tile, by groups of 16 keys.
 struct alignas(16) Meta {
   float kx[8];                               // K's scales
-  float vd[8], vu[8];                        // V's exponents against the accumulator's, and 2^-vd
-  float back;                                // what the accumulator's own change multiplies it with
-  int xo;                                    // its exponent
+  float vd[8], vu[8];                        // V's exponents against the tile's, and 2^-vd
+  int xo;                                    // the tile's exponent
+  int moved;                                 // the exponent of the tile before less it
   uint32_t absent;                           // groups without a page
 };
 
@@ -247,21 +253,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = __shfl_sync(0xffffffffu, top, 0);
-          // the accumulator's exponent: at least the tile's largest, and not far
-          // above it
-          float back = 1.f;
-          if (top > -1000 && (top > xo || top < xo - V_DOWN)) {
-            const int to = j == sg.t0 ? top : max(top, xo - V_LOWER);
-            back = pow2_any(xo - to);
-            xo = to;
-          }
+          // the exponent: at least the tile's largest, and not far above it
+          const int had = xo;
+          if (top > -1000 && (top > xo || top < xo - V_DOWN)) xo = top;
           const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane < 8) {
-            const int d = min(0, max(ev - xo, -100));
+            const int d = min(0, max(ev - xo, -P_NONE));
             m.kx[lane] = kx;
             m.vd[lane] = (float)d;
             m.vu[lane] = exp2i(-d);
-            if (lane == 0) { m.back = back; m.xo = xo; m.absent = ~there & 0xffu; }
+            if (lane == 0) { m.xo = xo; m.moved = had - xo; m.absent = ~there & 0xffu; }
           }
           __syncwarp();
           const bool copies = lane < 8 && pg >= 0 && ((16 * lane) & (c.page - 1)) == 0;
@@ -469,7 +470,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       }
 
       float m = -INFINITY, l = 0.f;
-      int xo = -127;                         // o is in units of 2^xo
+      // o is in units of 2^(xo + above), xo being the tile's exponent; `apart`: above
+      // is not 0 in all rows of the warp.  With m_grown the row's maximum, o was below
+      // 2^(grown + 23) when it last changed its unit.  What is rarely needed stays out
+      // of the registers.
+      int xo = -127;
+      bool apart = false;
+      enum { ABOVE, GROWN, M_GROWN, BY, UNDO };
+      volatile float rare[5] = {0.f, O_TILE, -INFINITY, 1.f, 1.f};
       for (int j = 0; ok && j < tiles; ++j, ++n) {
         ok = mbar_wait(&s_full[x], n & 1, abort_flag, c.err);
         if (!ok) break;
@@ -504,8 +512,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           *reinterpret_cast<float4*>(F + 4 * g) = *reinterpret_cast<const float4*>(meta.kx + 4 * g);
           *reinterpret_cast<float4*>(add + 4 * g) = *reinterpret_cast<const float4*>(meta.vd + 4 * g);
         }
-        const float back = meta.back;
+        const int moved = meta.moved;
         xo = meta.xo;
+        const bool refit = j > 0 && (moved != 0 || apart);
 #pragma unroll
         for (int g = 0; g < 8; ++g) F[g] *= f_row;
         float top_all = -INFINITY;
@@ -524,7 +533,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           top_all = fmaxf(top_all, fmaxf(top, top2) * F[g]);
         }
         const float m_new = top_all > m + M_UP ? top_all : m;
-        const float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
+        float ref = (m_new == -INFINITY ? 0.f : m_new) - P_BIAS;
+        if (refit) {
+          // what bounds the accumulator after this tile's alpha; before the row's first
+          // key it holds zeros (and of a NaN fmaxf takes the other)
+          const bool empty = m_new == -INFINITY;
+          const float now = fmaxf(rare[GROWN] + (rare[M_GROWN] - m), O_TILE) + (m - m_new);
+          const float x = (float)moved + rare[ABOVE];                // above the tile's exponent
+          const float to = empty ? 0.f : fmaxf(0.f, x - floorf(fmaxf(O_MOST - now, 0.f)));
+          rare[BY] = empty ? 1.f : ex2_approx((m_new == m ? 0.f : m - m_new) + (x - to));
+          rare[GROWN] = fmaxf(O_TILE, now + (x - to));
+          rare[M_GROWN] = m_new;
+          rare[ABOVE] = to;
+          const int n_above = (int)fminf(to, (float)P_NONE);
+          ref += (float)n_above;
+          rare[UNDO] = exp2i(n_above);
+          apart = __any_sync(0xffffffffu, to != 0.f);
+        }
 #pragma unroll
         for (int g = 0; g < 8; ++g) add[g] -= ref;
         const float alpha = (j == 0 || m_new == m) ? 1.f : ex2_approx(m - m_new);
@@ -552,7 +577,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
             ok = mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, c.err);
             if (!ok) break;
             tc_fence_after();
-            const float by = alpha * back;
+            float by = alpha;
+            if (refit) by = rare[BY];
             if (__any_sync(0xffffffffu, by != 1.f)) {
 #pragma unroll
               for (int og = 0; og < D / 32; ++og) {
@@ -578,6 +604,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           }
         }
         if (!ok) break;
+        if (refit) l_new *= rare[UNDO];
         l = fmaf(alpha, l, l_new);
         m = m_new;
       }
@@ -595,7 +622,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
       float4* part = reinterpret_cast<float4*>(p.part + (gridDim.x * 8 + 15) / 16 * 16);
       float4* slot = part + (size_t)(2 * blockIdx.x + (rec[E_FIRST] ? 0 : 1)) * (PartC<D>::FLOATS / 4);
       if (ok && x < nx) {
-        const float inv = none ? 0.f : 1.f / l, unit = pow2_any(xo);
+        const float inv = none ? 0.f : 1.f / l, unit = pow2_any(xo + (int)rare[ABOVE]);
 #pragma unroll 1
         for (int g = 0; g < D / 32; ++g) {
           uint32_t v[32];

@@ -103,7 +103,7 @@ def check(fa, q, cache, table, ln, lens, f32, causal=True, scale=None, pages=Non
     assert bad.max() <= 0, f"o off by {bad.max():.3g} over its bound"
     seen = np.isfinite(wl)
     assert np.array_equal(np.isneginf(lse), ~seen) and not o[~seen].any()
-    assert (np.abs(lse - wl)[seen] <= lt[seen]).all()
+    assert (np.abs(lse[seen] - wl[seen]) <= lt[seen]).all()
 
 
 # ------------------------------------------------------------------ V's exponents, few rows
@@ -188,3 +188,45 @@ def test_fwd_large_v_without_weight(T, f32):
     q[:, :, :, 0] = 0
     q[:, ::2, :, 0] = 5
     check(fa, q, cache, table, ln, lens, f32, scale=1.0, heads=1)
+
+
+# ------------------------------------------------------------------ V's exponents, many rows
+@pytest.mark.parametrize("d,page,H,G,T", [(64, 16, 2, 3, 40), (128, 64, 1, 2, 200), (128, 16, 1, 4, 70), (64, 128, 1, 1, 300)])
+def test_fwd_chunk_runs_of_zero_v(d, page, H, G, T):
+    fa = require_gpu()
+    k, v = zero_runs(H, d, 11)
+    cache, table, ln, lens = cache_of(fa, k, v, page, 12)
+    q = queries(len(lens), H * G, T, d, 13)
+    for causal in (True, False):
+        check(fa, q, cache, table, ln, lens, False, causal)
+    check(fa, q, cache, table, ln, lens, True)
+
+
+@pytest.mark.parametrize("first,last", [(100, -100), (-100, 100), (70, -126), (0, -120)])
+@pytest.mark.parametrize("d,T,keys,steps", [(128, 70, 128, 5), (64, 80, 256, 9), (128, 65, 640, 2), (64, 200, 64, 21)])
+def test_fwd_chunk_v_falls_and_rises(d, T, keys, steps, first, last):
+    fa = require_gpu()
+    k, v = falling(1, d, 14, first, last, keys, steps)
+    cache, table, ln, lens = cache_of(fa, k, v, 32, 15)
+    q = queries(1, 2, T, d, 16)
+    check(fa, q, cache, table, ln, lens, False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fwd_chunk_large_v_without_weight(d):
+    """As above: 70 rows of a head side by side, every second of which loses the
+    large values' weight."""
+    fa = require_gpu()
+    page, H, G, T, n = 64, 1, 2, 70, 1700
+    g = torch.Generator().manual_seed(17)
+    k = torch.randn(H, n, d, generator=g) * 0.1
+    v = torch.randn(H, n, d, generator=g)
+    v[:, :300] *= 2.0 ** 100
+    v[:, 300:800] *= 2.0 ** 40
+    v[:, 1200:] *= 2.0 ** -30
+    k[:, 800:, 0] = 60.0
+    cache, table, ln, lens = cache_of(fa, [k], [v], page, 18)
+    q = queries(1, H * G, T, d, 19)
+    q[..., 0] = 0
+    q[:, :, ::2, 0] = 5
+    check(fa, q, cache, table, ln, lens, False, scale=1.0)
