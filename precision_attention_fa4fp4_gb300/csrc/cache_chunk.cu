@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           int pg = -1;
           if (lane < 8 && key < sg.len) pg = cache_page(c, c.table, sg.b, lp);
           const long long ph = (long long)max(pg, 0) * c.Hkv + sg.h;
-          const float kx = e8m0_value(*(c.ks + ph));
+          const float kx = pg >= 0 ? e8m0_value(*(c.ks + ph)) : 1.f;      // (what is absent is masked)
           const int ev = (int)*(c.vs + ph) - 127;
           Meta& m = metas[n % METAS];
           if (n > 0 && !mbar_wait(k8_empty, (n - 1) & 1, abort_flag, c.err)) { ok = false; break; }
@@ -515,8 +515,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
         const int moved = meta.moved;
         xo = meta.xo;
         const bool refit = j > 0 && (moved != 0 || apart);
+        // (a masked score is -inf, which must not meet a factor of 0: 2^-126 more changes
+        // a score of up to 2^24 units by 2^-102 at most)
 #pragma unroll
-        for (int g = 0; g < 8; ++g) F[g] *= f_row;
+        for (int g = 0; g < 8; ++g) F[g] = fmaf(F[g], f_row, 0x1p-126f);
         float top_all = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {

@@ -230,3 +230,25 @@ def test_fwd_chunk_large_v_without_weight(d):
     q[..., 0] = 0
     q[:, :, ::2, 0] = 5
     check(fa, q, cache, table, ln, lens, False, scale=1.0)
+
+
+# ------------------------------------------------------------------ small queries, zero keys, many rows
+@pytest.mark.parametrize("d,page,H,G,T,scale", [(128, 64, 2, 2, 70, None), (64, 16, 1, 3, 100, None), (128, 128, 1, 1, 90, 1e-12),
+                                                (64, 32, 2, 1, 66, 1e-6)])
+def test_fwd_chunk_small_queries(d, page, H, G, T, scale):
+    """Pool page 0 unused, its scale byte 0 (2^-127), keys that end inside a tile, and
+    pages of zero keys at the causal edge: rows of q down to the smallest bf16."""
+    fa = require_gpu()
+    g = torch.Generator().manual_seed(21)
+    lens = [T + 5, 3 * T + 1, 128, 7, 300]
+    k = [torch.randn(H, n, d, generator=g) for n in lens]
+    k[1][:, 2 * T:] = 0
+    k[4][:] = 0
+    k[2][:, 100:] *= 2.0 ** -120
+    v = [torch.randn(H, n, d, generator=g) for n in lens]
+    cache, table, ln, lens = cache_of(fa, k, v, page, 22, first=1)
+    assert int(cache.ks[0].max()) == 0 and int(table.min()) > 0
+    q = queries(len(lens), H * G, T, d, 23)
+    q *= (2.0 ** -(torch.arange(T) % 14 * 10).float()).view(1, 1, T, 1).cuda()      # down to 2^-130
+    for causal in (True, False):
+        check(fa, q, cache, table, ln, lens, False, causal, scale)
