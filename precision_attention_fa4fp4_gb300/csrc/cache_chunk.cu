@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_chunk_kernel(const __grid_c
           if (!valid) continue;
           float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = none ? 0.f : __uint_as_float(v[i]) * unit * inv;
+          for (int i = 0; i < 32; ++i) y[i] = none ? 0.f : __uint_as_float(v[i]) * inv * unit;    // in this order: it may be near FP32's end
           if (cut) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -108,6 +108,13 @@ FA4_DEV int seq_units(const CacheFwdParams& p, int b) {
   return units_of(p.pages ? (long long)p.n_sel * p.c.page : len);
 }
 
+// Sums of V that leave the registers are in units of 2^HIGH where their exponent
+// lies above FROM (the sum of many values near bf16's end would pass FP32's), and
+// their sum of weights l is then negative.
+constexpr float FROM = -40.f;
+constexpr int HIGH = 48;             // |o| <= l * 2^128 with l < 2^15 * 2^30
+constexpr float TO_HIGH = 0x1p-48f, FROM_HIGH = 0x1p48f;
+
 template <int D, int NT>
 struct Slot {
   static constexpr int R = 8 * NT;
@@ -566,25 +573,26 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
     // the four warps' shares of the keys
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float unit[2] = {pow2_any((int)xo[n][0]), pow2_any((int)xo[n][1])};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
         l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
         l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
         const int col = 8 * n + 2 * t4 + j;
-        if (g == 0) { s_m[warp][col] = m[n][j]; s_l[warp][col] = l[n][j]; }
+        const bool high = xo[n][j] > FROM;
+        if (g == 0) { s_m[warp][col] = m[n][j]; s_l[warp][col] = high ? -l[n][j] : l[n][j]; }
+        const float unit = pow2_any((int)xo[n][j] - (high ? HIGH : 0));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j] * unit[j], o[n][i][2 + j] * unit[j]);
+          *reinterpret_cast<float2*>(&s_o[warp][col][v_dim + 2 * i]) = make_float2(o[n][i][j] * unit, o[n][i][2 + j] * unit);
       }
     }
     __syncthreads();
-    auto write = [&](int col, int x, const float4& a, float mt, float lt) {
+    auto write = [&](int col, int x, const float4& a, bool high, float mt, float lt) {
       int t, gg;
       if (!row_of(col, t, gg)) return;
       const long long row = ((long long)b * p.Hq + h * G + gg) * p.T + t;
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;
+      const float inv = lt == 0.f ? 0.f : (high ? FROM_HIGH : 1.f) / lt;
       if (p.out_bf16) {
         __nv_bfloat162 z[2] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv)};
         *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + x) = *reinterpret_cast<uint2*>(z);
@@ -604,18 +612,23 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       for (int w = 1; w < NW; ++w) mt = fmaxf(mt, s_m[w][col]);
       float lt = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      bool high = false;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) high = high || s_l[w][col] < 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float f = s_m[w][col] == mt ? 1.f : ex2_approx(s_m[w][col] - mt);
+        float f = s_m[w][col] == mt ? 1.f : ex2_approx(s_m[w][col] - mt);
         const float4 y = *reinterpret_cast<const float4*>(&s_o[w][col][x]);
-        lt = fmaf(f, s_l[w][col], lt);
+        const float lw = s_l[w][col];
+        lt = fmaf(f, fabsf(lw), lt);
+        if (high && !(lw < 0.f)) f *= TO_HIGH;
         a.x = fmaf(f, y.x, a.x); a.y = fmaf(f, y.y, a.y); a.z = fmaf(f, y.z, a.z); a.w = fmaf(f, y.w, a.w);
       }
       if (whole) {
-        write(col, x, a, mt, lt);
+        write(col, x, a, high, mt, lt);
       } else {
         *reinterpret_cast<float4*>(slot + col * D + x) = a;
-        if (x == 0) { slot[R * D + col] = mt; slot[R * D + R + col] = lt; }
+        if (x == 0) { slot[R * D + col] = mt; slot[R * D + R + col] = high ? -lt : lt; }
       }
     }
     __syncthreads();
@@ -639,6 +652,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
           if (!row_of(col, t, gg)) continue;
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
           float mt = -INFINITY, lt = 0.f;
+          bool high = false;
           for (int i0 = 0; i0 < n; i0 += 16) {
             float4 y[16];
             float mi[16], li[16];
@@ -657,19 +671,24 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
             float mx = mt;
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, mi[i]);
-            const float back = mx == mt ? 1.f : ex2_approx(mt - mx);
+            float back = mx == mt ? 1.f : ex2_approx(mt - mx);
             mt = mx;
             lt *= back;
+            const bool was = high;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) high = high || li[i] < 0.f;
+            if (high && !was) back *= TO_HIGH;
             a.x *= back; a.y *= back; a.z *= back; a.w *= back;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float f = mi[i] == mx ? 1.f : ex2_approx(mi[i] - mx);
-              lt = fmaf(f, li[i], lt);
+              float f = mi[i] == mx ? 1.f : ex2_approx(mi[i] - mx);
+              lt = fmaf(f, fabsf(li[i]), lt);
+              if (high && !(li[i] < 0.f)) f *= TO_HIGH;
               a.x = fmaf(f, y[i].x, a.x); a.y = fmaf(f, y[i].y, a.y);
               a.z = fmaf(f, y[i].z, a.z); a.w = fmaf(f, y[i].w, a.w);
             }
           }
-          write(col, x, a, mt, lt);
+          write(col, x, a, high, mt, lt);
         }
       }
     }

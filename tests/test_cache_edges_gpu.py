@@ -252,3 +252,25 @@ def test_fwd_chunk_small_queries(d, page, H, G, T, scale):
     q *= (2.0 ** -(torch.arange(T) % 14 * 10).float()).view(1, 1, T, 1).cuda()      # down to 2^-130
     for causal in (True, False):
         check(fa, q, cache, table, ln, lens, False, causal, scale)
+
+
+# ------------------------------------------------------------------ V close to the largest bf16
+@pytest.mark.parametrize("d,page,H,G,T,f32", FEW + [(128, 64, 1, 2, 70, False), (64, 16, 1, 3, 90, False), (64, 16, 1, 3, 90, True)])
+def test_fwd_largest_values(d, page, H, G, T, f32):
+    """A mean of values up to 2^127.99 is one itself; so are keys of nearly equal
+    weight in great number, and a row whose keys are cut among CTAs."""
+    fa = require_gpu()
+    g = torch.Generator().manual_seed(31)
+    big = float(torch.finfo(torch.bfloat16).max)
+    lens = [1, 40, 513, 6000]
+    k = [torch.randn(H, n, d, generator=g) * 0.01 for n in lens]
+    v = [torch.rand(H, n, d, generator=g) * 0.9 * big for n in lens]
+    for x in v:
+        x[:, :, ::2] *= -1
+        x[:, :, 1] *= 2.0 ** -30
+    cache, table, ln, lens = cache_of(fa, k, v, page, 32)
+    q = queries(len(lens), H * G, T, d, 33)
+    check(fa, q, cache, table, ln, lens, f32)
+    small = [x * 2.0 ** -200 for x in v]
+    cache, table, ln, lens = cache_of(fa, k, small, page, 34)
+    check(fa, q, cache, table, ln, lens, f32)
