@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
         pos[i] = i ? what.z : what.x;
         kx[i] = e8m0_value((i ? what.w : what.y) & 0xff);
       }
-      // the lane's key: its weight is read early
-      const int key = SMALLP ? (my_i ? pos[NP - 1] : pos[0]) + my_key - 16 * my_i : pos[0] + my_key;
+      // the lane's key: its weight is read early (and written back as it was where
+      // its page is not there)
+      const int key = u * UNIT + 32 * warp + my_key;
+      const bool there = (my_i ? pos[NP - 1] : pos[0]) != NOWHERE;
       const float had = key < len ? p.w_in[w_row + key] : 0.f;
       float s[NT][2][4];
 #pragma unroll
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
           w[i][r] += __shfl_xor_sync(0xffffffffu, w[i][r], 2);
           if (t4 == 2 * i + r) mine = w[i][r];
         }
-      if (key < len) p.w_out[w_row + key] = had + mine;
+      if (key < len) p.w_out[w_row + key] = had + (there ? mine : 0.f);
     }
     // the S steps behind the head's last unit have no boxes, only phases
     if (ok) {

@@ -274,3 +274,32 @@ def test_fwd_largest_values(d, page, H, G, T, f32):
     small = [x * 2.0 ** -200 for x in v]
     cache, table, ln, lens = cache_of(fa, k, small, page, 34)
     check(fa, q, cache, table, ln, lens, f32)
+
+
+# ------------------------------------------------------------------ received weights
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (64, 128)])
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 4), (4, 10), (4, 40)])
+def test_weigh_bad_page(d, page, G, T):
+    """The keys of a page that is not in the pool receive nothing; their old
+    weights arrive all the same, in every kernel."""
+    fa = require_gpu()
+    H, lens = 2, [3 * page + 5, 300, 2 * page]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=25)
+    q = queries(3, H * G, T, d, 26)
+    ql = torch.tensor([T, T, 0], dtype=torch.int32).cuda()
+    _, lse = fa.cache_fwd(q, cache, table, ln, q_lens=ql, out_dtype=fa.OUT_F32)
+    w = torch.rand(3, H, table.shape[1] * page, device="cuda")
+    good, out = torch.full_like(w, 5.0), torch.full_like(w, 5.0)
+    fa.cache_weigh(q, lse, cache, table, ln, w, q_lens=ql, out=good)
+    fa.sync_status()
+    bad = table.clone()
+    bad[0, 1], bad[1, 0], bad[2, 1] = cache.num_pages, -1, 1 << 30
+    fa.cache_weigh(q, lse, cache, bad, ln, w, q_lens=ql, out=out)
+    with pytest.raises(fa.Fa4Fp4Error) as e:
+        fa.sync_status()
+    assert e.value.status == 7
+    for b, p in ((0, 1), (1, 0), (2, 1)):
+        at = slice(p * page, min((p + 1) * page, lens[b]))
+        assert torch.equal(out[b, :, at], w[b, :, at])
+        good[b, :, at] = w[b, :, at]
+    assert torch.equal(out, good)
