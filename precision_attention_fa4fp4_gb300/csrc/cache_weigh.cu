@@ -210,12 +210,11 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float x = s[n][i][j] * kx[i % NP];
-            float e = ex2_approx(fmaf(x, fx[n][j & 1], -ref[n][j & 1]));
-            if (!full) {
-              const int kk = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1);
-              if (kk >= vis[n][j & 1]) e = 0.f;
-            }
-            w[i][j >> 1] = fmaf(e, fac[n][j & 1], w[i][j >> 1]);
+            const float e = ex2_approx(fmaf(x, fx[n][j & 1], -ref[n][j & 1]));
+            // (a row that does not see the key must not reach it as 0 * NaN either)
+            bool sees = true;
+            if (!full) sees = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1) < vis[n][j & 1];
+            if (sees) w[i][j >> 1] = fmaf(e, fac[n][j & 1], w[i][j >> 1]);
           }
       float mine = 0.f;
 #pragma unroll
@@ -363,9 +362,9 @@ __global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __gr
           const float f0 = kx[i] * fx.x, f1 = kx[i] * fx.y;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float e = ex2_approx(fmaf(s[i][j], (j & 1) ? f1 : f0, (j & 1) ? -ref.y : -ref.x));
-            if (!full && key0 + 16 * i + g + 8 * (j >> 1) >= vis[j & 1]) e = 0.f;
-            w[i][j >> 1] = fmaf(e, (j & 1) ? fac.y : fac.x, w[i][j >> 1]);
+            const float e = ex2_approx(fmaf(s[i][j], (j & 1) ? f1 : f0, (j & 1) ? -ref.y : -ref.x));
+            if (full || key0 + 16 * i + g + 8 * (j >> 1) < vis[j & 1])
+              w[i][j >> 1] = fmaf(e, (j & 1) ? fac.y : fac.x, w[i][j >> 1]);
           }
         }
       }

@@ -362,12 +362,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cache_weigh_rows_kernel(const __g
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, nr);
-                float2 w = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                if (!full) {
-                  if (16 * hf + 2 * e >= left) w.x = 0.f;
-                  if (16 * hf + 2 * e + 1 >= left) w.y = 0.f;
-                }
-                acc[8 * hf + e] = ffma2(w, fc, acc[8 * hf + e]);
+                const float2 sum = ffma2(make_float2(ex2_approx(y.x), ex2_approx(y.y)), fc, acc[8 * hf + e]);
+                // (a row that does not see the key must not reach it as 0 * NaN either)
+                if (full || 16 * hf + 2 * e < left) acc[8 * hf + e].x = sum.x;
+                if (full || 16 * hf + 2 * e + 1 < left) acc[8 * hf + e].y = sum.y;
               }
             };
             if (all) add(true);

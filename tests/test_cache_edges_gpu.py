@@ -303,3 +303,33 @@ def test_weigh_bad_page(d, page, G, T):
         assert torch.equal(out[b, :, at], w[b, :, at])
         good[b, :, at] = w[b, :, at]
     assert torch.equal(out, good)
+
+
+WEIGH = [(64, 16, 1, 7), (128, 64, 2, 8), (128, 32, 2, 20), (64, 128, 1, 79), (128, 64, 2, 100)]
+
+
+def weigh_with(fa, d, page, G, T, value):
+    """Weights with one row's lse set to `value`, and with the row left out."""
+    H, lens = 2, [T + 150, T, 129]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=27)
+    q = queries(3, H * G, T, d, 28)
+    _, lse = fa.cache_fwd(q, cache, table, ln, out_dtype=fa.OUT_F32)
+    w = torch.rand(3, H, table.shape[1] * page, device="cuda")
+    t = T // 2
+    none, some = lse.clone(), lse.clone()
+    none[:, 0, t] = float("-inf")
+    some[:, 0, t] = value
+    want = fa.cache_weigh(q, none, cache, table, ln, w, out=w.clone())
+    got = fa.cache_weigh(q, some, cache, table, ln, w, out=w.clone())
+    fa.sync_status()
+    return got, want, [max(0, min(n, n - T + t + 1)) for n in lens]
+
+
+@pytest.mark.parametrize("d,page,G,T", WEIGH)
+def test_weigh_row_of_nan(d, page, G, T):
+    """A token whose lse is not a number says nothing about the keys that it does
+    not see."""
+    got, want, sees = weigh_with(require_gpu(), d, page, G, T, float("nan"))
+    for b, n in enumerate(sees):
+        assert torch.isnan(got[b, 0, :n]).all()
+        assert torch.equal(got[b, 0, n:], want[b, 0, n:]) and torch.equal(got[b, 1:], want[b, 1:])
