@@ -341,11 +341,11 @@ FA4_DEV int store_query_rows(uint8_t* tile, int row0, const __nv_bfloat16* mine)
 }
 
 // lse in log2 units as a float and the factor that makes up for its rounding;
-// rows that add nothing get (0, 0).
+// rows that add nothing (e^-inf for every key if lse is infinite) get (0, 0).
 FA4_DEV void reference(float lse, bool in, float& ref, float& fac) {
   ref = 0.f;
   fac = 0.f;
-  if (in && lse != -INFINITY) {
+  if (in && !isinf(lse)) {
     ref = lse * 1.4426950216293335f;
     const float rest = fmaf(lse, 1.4426950216293335f, -ref) + lse * 1.9259629911266175e-8f;
     fac = ex2_approx(-rest);

@@ -333,3 +333,10 @@ def test_weigh_row_of_nan(d, page, G, T):
     for b, n in enumerate(sees):
         assert torch.isnan(got[b, 0, :n]).all()
         assert torch.equal(got[b, 0, n:], want[b, 0, n:]) and torch.equal(got[b, 1:], want[b, 1:])
+
+
+@pytest.mark.parametrize("d,page,G,T", WEIGH)
+def test_weigh_row_of_infinite_lse(d, page, G, T):
+    """e^(s - inf) = 0 for every key."""
+    got, want, _ = weigh_with(require_gpu(), d, page, G, T, float("inf"))
+    assert torch.equal(got, want)
