@@ -29,7 +29,7 @@ namespace fa4 {
 namespace {
 
 constexpr int NT = KTH_THREADS;
-constexpr int SMEM_PAGES = 16384;
+constexpr int SMEM_PAGES = 16384, MAX_PAGES = 1 << 18;    // (the call refuses more)
 
 // Unsigned keys in the order of the floats (NaN above everything).
 FA4_DEV uint32_t key32(float x) {
@@ -366,14 +366,22 @@ __global__ void __launch_bounds__(NT) cache_select_kernel(const __grid_constant_
   for (int i = s_in + threadIdx.x; i < p.n_sel; i += NT) out[i] = -1;
 }
 
+constexpr size_t smem_bytes(int max_pages) {
+  const size_t bit_words = ((size_t)max_pages + 31) / 32;
+  return (bit_words + 1) / 2 * 16 + (max_pages <= SMEM_PAGES ? (size_t)max_pages * 8 : 0);
+}
+
 template <int D>
 cudaError_t launch(const CacheSelectParams& p, cudaStream_t st) {
-  const int bit_words = (p.c.max_pages + 31) / 32;
-  size_t smem = (size_t)(bit_words + 1) / 2 * 16;
-  if (p.c.max_pages <= SMEM_PAGES) smem += (size_t)p.c.max_pages * 8;
+  const size_t smem = smem_bytes(p.c.max_pages);
   if (smem > 32 * 1024) {
+    // One limit for the kernel on a device, so every call sets the same (the most
+    // that any needs): another thread's smaller one between here and the launch
+    // would refuse it.
+    constexpr size_t most = smem_bytes(SMEM_PAGES);
+    static_assert(most >= smem_bytes(MAX_PAGES), "the limit covers the largest table");
     const cudaError_t e =
-        cudaFuncSetAttribute(cache_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(cache_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   return launch_next(cache_select_kernel<D>, dim3((unsigned)p.c.B * p.c.Hkv * p.T), NT, smem, st, p);

@@ -340,3 +340,36 @@ def test_weigh_row_of_infinite_lse(d, page, G, T):
     """e^(s - inf) = 0 for every key."""
     got, want, _ = weigh_with(require_gpu(), d, page, G, T, float("inf"))
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ calls from several threads
+def test_select_from_two_threads():
+    """Tables of different lengths at once, each on its own stream: the kernel's
+    limit of shared memory is one for the whole process."""
+    import threading
+    fa = require_gpu()
+    d, page, H = 64, 16, 1
+    caches = [R.make(fa, [n], H, d, page, seed=35, room=room) for n, room in ((5000, 16 * 9000), (5000, 16 * 16000))]
+    q = queries(1, 2, 1, d, 36)
+    want = [fa.cache_select(q, c, t, ln, 20) for c, t, ln in caches]
+    fa.sync_status()
+    errors = []
+
+    def run(i):
+        try:
+            c, t, ln = caches[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3000):
+                    got = fa.cache_select(q, c, t, ln, 20)
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(got, want[i])
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i % 2,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    fa.sync_status()
+    assert not errors, errors
