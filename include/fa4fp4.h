@@ -429,10 +429,10 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_evict(const fa4fp4_cache* cache, const int
                                             float* weight_out, void* stream);
 
 /* Synchronizes `stream`, then returns FA4FP4_ERR_CUDA for a pending CUDA error
- * or, for what kernels reported since the last call (the flags are cleared),
- * FA4FP4_ERR_DEVICE_TIMEOUT if any bounded wait expired,
- * FA4FP4_ERR_DEVICE_INDEX or FA4FP4_ERR_DEVICE_NONFINITE for what the cache
- * calls met, else FA4FP4_OK. */
+ * or, for what kernels reported, FA4FP4_ERR_DEVICE_TIMEOUT if any bounded wait
+ * expired, FA4FP4_ERR_DEVICE_INDEX or FA4FP4_ERR_DEVICE_NONFINITE for what the
+ * cache calls met, else FA4FP4_OK.  One kind a call, in this order: what a call
+ * returns is cleared by it, the other kinds are returned by the next ones. */
 FA4FP4_API fa4fp4_status fa4fp4_sync_status(void* stream);
 
 /* Static description of a status code. */

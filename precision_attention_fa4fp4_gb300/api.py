@@ -521,7 +521,9 @@ def watchdog_selftest(limit_ns: int = 50_000_000, device=None):
 
 
 def sync_status(device=None):
-    """Synchronize the current stream and raise on a device watchdog error."""
+    """Synchronize the current stream and raise for what kernels reported: a wait
+    that ran out, a bad page index, length or count, a NaN or infinity given to the
+    cache.  One kind a call, which clears it; the next call raises the next kind."""
     _check("fa4fp4_sync_status", load_library().fa4fp4_sync_status(_stream(device)))
 
 

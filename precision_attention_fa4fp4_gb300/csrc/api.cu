@@ -433,14 +433,18 @@ fa4fp4_status fa4fp4_sync_status(void* stream) {
   if (!w) return FA4FP4_ERR_CUDA;
   unsigned host = 0;
   if (cudaMemcpy(&host, w, sizeof(host), cudaMemcpyDeviceToHost) != cudaSuccess) return FA4FP4_ERR_CUDA;
-  if (host) {
-    unsigned zero = 0;
-    cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    if (host & FA4_DEVERR_TIMEOUT) return FA4FP4_ERR_DEVICE_TIMEOUT;
-    if (host & FA4_DEVERR_INDEX) return FA4FP4_ERR_DEVICE_INDEX;
-    if (host & FA4_DEVERR_NONFINITE) return FA4FP4_ERR_DEVICE_NONFINITE;
-    return FA4FP4_ERR_DEVICE_TIMEOUT;
-  }
+  // one kind at a time: the others wait for the next calls
+  const struct { unsigned bit; fa4fp4_status status; } kinds[] = {
+      {FA4_DEVERR_TIMEOUT, FA4FP4_ERR_DEVICE_TIMEOUT},
+      {FA4_DEVERR_INDEX, FA4FP4_ERR_DEVICE_INDEX},
+      {FA4_DEVERR_NONFINITE, FA4FP4_ERR_DEVICE_NONFINITE}};
+  for (const auto& kind : kinds)
+    if (host & kind.bit) {
+      if (launch_clear_errors(w, kind.bit, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+          cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return FA4FP4_ERR_CUDA;
+      return kind.status;
+    }
   return FA4FP4_OK;
 }
 

@@ -61,6 +61,7 @@ cudaError_t launch_directp_codes(const float* s, long long n, float m, float c, 
                                  int native, uint8_t* codes, cudaStream_t st);
 
 cudaError_t launch_watchdog_selftest(unsigned* err, unsigned long long limit_ns, cudaStream_t st);
+cudaError_t launch_clear_errors(unsigned* err, unsigned bits, cudaStream_t st);
 
 // ---------------------------------------------------------------- BF16 fwd
 struct FwdBf16Params {

@@ -300,6 +300,9 @@ int grid_for(long long work, int per_cta) {
 
 // One CTA waits, with a bounded wait, on an mbarrier that nothing arrives at:
 // the wait must expire, flag the device error word and return.
+// (what another stream's kernels report meanwhile stays)
+__global__ void clear_errors_kernel(unsigned* err, unsigned bits) { atomicAnd(err, ~bits); }
+
 __global__ void watchdog_selftest_kernel(unsigned* err, unsigned long long limit_ns) {
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
@@ -354,6 +357,11 @@ cudaError_t launch_quantize_nvfp4(const void* x, long long n, void* codes, void*
 
 cudaError_t launch_watchdog_selftest(unsigned* err, unsigned long long limit_ns, cudaStream_t st) {
   watchdog_selftest_kernel<<<1, 32, 0, st>>>(err, limit_ns);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_clear_errors(unsigned* err, unsigned bits, cudaStream_t st) {
+  clear_errors_kernel<<<1, 1, 0, st>>>(err, bits);
   return cudaGetLastError();
 }
 

@@ -373,3 +373,25 @@ def test_select_from_two_threads():
         t.join()
     fa.sync_status()
     assert not errors, errors
+
+
+# ------------------------------------------------------------------ status
+def test_every_kind_of_error_is_reported():
+    """Errors of different kinds between two looks at the status: each is
+    reported, the more serious first, and then none."""
+    fa = require_gpu()
+    cache, table, ln = R.make(fa, [0, 0], 2, 64, 16, room=20)
+    zero = torch.zeros_like(ln)
+    x = queries(2, 2, 3, 64, 37)
+    x[0, 0, 1, 5] = float("nan")
+    bad = table.clone()
+    bad[1, 0] = -1
+    fa.sync_status()
+    fa.watchdog_selftest(1_000_000)
+    fa.cache_append(cache, x, x, bad, zero)
+    fa.cache_append(cache, x, x, bad, zero)
+    for status in (5, 7, 8):
+        with pytest.raises(fa.Fa4Fp4Error) as e:
+            fa.sync_status()
+        assert e.value.status == status
+    fa.sync_status()
