@@ -174,7 +174,10 @@ void cache_dealloc(PyObject* self) {
 }
 
 PyObject* cache_device(PyObject* self, void*) {
-  return PyObject_GetAttrString(reinterpret_cast<Cache*>(self)->k, "device");
+  PyObject* k = reinterpret_cast<Cache*>(self)->k;
+  if (k) return PyObject_GetAttrString(k, "device");
+  PyErr_SetString(PyExc_AttributeError, "device");
+  return nullptr;
 }
 
 PyMemberDef cache_members[] = {
