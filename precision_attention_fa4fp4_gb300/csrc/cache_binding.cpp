@@ -128,12 +128,26 @@ at::Tensor workspace(PyObject* x, int index, size_t need) {
 }
 
 // ---------------------------------------------------------------- KVCache
+// It keeps the tensors and their sizes, no addresses: a tensor may have been given
+// other memory (resize_, set_) since.
 struct Cache {
   PyObject_HEAD
   PyObject *k, *v, *ks, *vs, *kb;
-  int index;
-  fa4fp4_cache c;
+  int index, num_pages, Hkv, page, d;
 };
+
+// The structure of a call, from tensors that have (still) the cache's sizes.
+fa4fp4_cache structure(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, PyObject* kb, int index, int64_t n, int64_t H,
+                       int64_t page, int64_t d) {
+  fa4fp4_cache c;
+  c.k_codes = expect(k, "k", index, at::kByte, {n, H, page, d}).data_ptr();
+  c.v_codes = expect(v, "v", index, at::kByte, {n, H, page, d}).data_ptr();
+  c.k_scales = expect(ks, "ks", index, at::kByte, {n, H}).data_ptr();
+  c.v_scales = expect(vs, "vs", index, at::kByte, {n, H}).data_ptr();
+  c.k_bounds = expect(kb, "kb", index, at::kByte, {n, H, 2, d}).data_ptr();
+  c.num_pages = (int)n; c.Hkv = (int)H; c.page = (int)page; c.d = (int)d;
+  return c;
+}
 
 int cache_init(PyObject* self, PyObject* args, PyObject* kwargs) {
   Cache* o = reinterpret_cast<Cache*>(self);
@@ -146,18 +160,12 @@ int cache_init(PyObject* self, PyObject* args, PyObject* kwargs) {
     if (!tk.is_cuda()) refuse("fa4fp4: a cache's tensors must be CUDA tensors");
     const int index = tk.get_device();
     if (n > INT_MAX || H > INT_MAX || page > INT_MAX || d > INT_MAX) refuse("k: too large");
-    fa4fp4_cache c;
-    c.k_codes = expect(k, "k", index, at::kByte, {n, H, page, d}).data_ptr();
-    c.v_codes = expect(v, "v", index, at::kByte, {n, H, page, d}).data_ptr();
-    c.k_scales = expect(ks, "ks", index, at::kByte, {n, H}).data_ptr();
-    c.v_scales = expect(vs, "vs", index, at::kByte, {n, H}).data_ptr();
-    c.k_bounds = expect(kb, "kb", index, at::kByte, {n, H, 2, d}).data_ptr();
-    c.num_pages = (int)n; c.Hkv = (int)H; c.page = (int)page; c.d = (int)d;
+    structure(k, v, ks, vs, kb, index, n, H, page, d);
     PyObject* had[] = {o->k, o->v, o->ks, o->vs, o->kb};
     Py_INCREF(k); Py_INCREF(v); Py_INCREF(ks); Py_INCREF(vs); Py_INCREF(kb);
     o->k = k; o->v = v; o->ks = ks; o->vs = vs; o->kb = kb;
     o->index = index;
-    o->c = c;
+    o->num_pages = (int)n; o->Hkv = (int)H; o->page = (int)page; o->d = (int)d;
     for (PyObject* x : had) Py_XDECREF(x);
     return 0;
   } catch (const Refused&) {
@@ -186,10 +194,10 @@ PyMemberDef cache_members[] = {
     {"ks", T_OBJECT_EX, offsetof(Cache, ks), READONLY, "K scales, uint8 [num_pages, Hkv]"},
     {"vs", T_OBJECT_EX, offsetof(Cache, vs), READONLY, "V scales, uint8 [num_pages, Hkv]"},
     {"kb", T_OBJECT_EX, offsetof(Cache, kb), READONLY, "K bounds, uint8 [num_pages, Hkv, 2, d]"},
-    {"num_pages", T_INT, offsetof(Cache, c) + offsetof(fa4fp4_cache, num_pages), READONLY, "pages of the pool"},
-    {"Hkv", T_INT, offsetof(Cache, c) + offsetof(fa4fp4_cache, Hkv), READONLY, "kv heads"},
-    {"page", T_INT, offsetof(Cache, c) + offsetof(fa4fp4_cache, page), READONLY, "tokens of a page"},
-    {"d", T_INT, offsetof(Cache, c) + offsetof(fa4fp4_cache, d), READONLY, "head dimension"},
+    {"num_pages", T_INT, offsetof(Cache, num_pages), READONLY, "pages of the pool"},
+    {"Hkv", T_INT, offsetof(Cache, Hkv), READONLY, "kv heads"},
+    {"page", T_INT, offsetof(Cache, page), READONLY, "tokens of a page"},
+    {"d", T_INT, offsetof(Cache, d), READONLY, "head dimension"},
     {nullptr}};
 PyGetSetDef cache_getset[] = {{"device", cache_device, nullptr, "the tensors' device", nullptr}, {nullptr}};
 
@@ -198,14 +206,15 @@ PyTypeObject cache_type = {PyVarObject_HEAD_INIT(nullptr, 0)};
 // ---------------------------------------------------------------- calls
 // The sequences that every call is given.
 struct Sequences {
-  Cache* cache;
+  fa4fp4_cache c;
   int index, B, max_pages;
   const int *table, *lens, *counts;
 
   Sequences(PyObject* cache_, PyObject* table_, PyObject* lens_, PyObject* counts_, const char* counts_name) {
     if (Py_TYPE(cache_) != &cache_type || !reinterpret_cast<Cache*>(cache_)->k) refuse("cache: expected a KVCache");
-    cache = reinterpret_cast<Cache*>(cache_);
-    index = cache->index;
+    const Cache* o = reinterpret_cast<Cache*>(cache_);
+    index = o->index;
+    c = structure(o->k, o->v, o->ks, o->vs, o->kb, index, o->num_pages, o->Hkv, o->page, o->d);
     const at::Tensor& t = as_tensor(table_, "page_table");
     const int64_t b = dim(t, "page_table", 2, 0), m = t.size(1);
     if (b > INT_MAX || m > INT_MAX) refuse("page_table: too large");
@@ -226,7 +235,7 @@ struct Queries {
     const at::Tensor& t = as_tensor(q_, "q");
     const int64_t h = dim(t, "q", 4, 1), n = t.size(2);
     if (h > INT_MAX || n > INT_MAX) refuse("q: too large");
-    q = expect(q_, "q", s.index, at::kBFloat16, {s.B, h, n, s.cache->c.d}).data_ptr();
+    q = expect(q_, "q", s.index, at::kBFloat16, {s.B, h, n, s.c.d}).data_ptr();
     Hq = (int)h;
     T = (int)n;
   }
@@ -270,7 +279,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     PyObject* a[6];
     parse(s, args, n, kw, a);
     const Sequences q(a[0], a[3], a[4], a[5], "n_new");
-    const fa4fp4_cache* c = &q.cache->c;
+    const fa4fp4_cache* c = &q.c;
     const int64_t T = dim(as_tensor(a[1], "k"), "k", 4, 2);
     if (T > INT_MAX) refuse("k: too large");
     const void* k = expect(a[1], "k", q.index, at::kBFloat16, {q.B, c->Hkv, T, c->d}).data_ptr();
@@ -291,7 +300,7 @@ PyObject* fwd(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     parse(s, args, n, kw, a);
     const Sequences q(a[1], a[2], a[3], a[4], "q_lens");
     const Queries r(q, a[0]);
-    const fa4fp4_cache* c = &q.cache->c;
+    const fa4fp4_cache* c = &q.c;
     const bool causal = as_bool(a[5], true), with_lse = as_bool(a[8], true);
     const float scale = as_float(a[6]);
     const int out_dtype = a[7] ? as_int(a[7], "out_dtype") : FA4FP4_OUT_BF16;
@@ -342,7 +351,7 @@ PyObject* select(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     parse(s, args, n, kw, a);
     const Sequences q(a[1], a[2], a[3], a[5], "q_lens");
     const Queries r(q, a[0]);
-    const fa4fp4_cache* c = &q.cache->c;
+    const fa4fp4_cache* c = &q.c;
     const int n_sel = as_int(a[4], "n_pages");
     if (n_sel < 1) refuse("n_pages must be at least 1");
     const at::Tensor out = given(a[6]) ? expect(a[6], "out", q.index, at::kInt, {q.B, c->Hkv, r.T, n_sel})
@@ -367,7 +376,7 @@ PyObject* weigh(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     parse(s, args, n, kw, a);
     const Sequences q(a[2], a[3], a[4], a[6], "q_lens");
     const Queries r(q, a[0]);
-    const fa4fp4_cache* c = &q.cache->c;
+    const fa4fp4_cache* c = &q.c;
     const float* lse = static_cast<float*>(expect(a[1], "lse", q.index, at::kFloat, {q.B, r.Hq, r.T}).data_ptr());
     const int64_t L = (int64_t)q.max_pages * c->page;
     const float* w = static_cast<float*>(expect(a[5], "weight", q.index, at::kFloat, {q.B, c->Hkv, L}).data_ptr());
@@ -392,7 +401,7 @@ PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
     PyObject* a[7];
     parse(s, args, n, kw, a);
     const Sequences q(a[0], a[1], a[2], nullptr, "");
-    const fa4fp4_cache* c = &q.cache->c;
+    const fa4fp4_cache* c = &q.c;
     const int64_t L = (int64_t)q.max_pages * c->page;
     const float* w = static_cast<float*>(expect(a[3], "weight", q.index, at::kFloat, {q.B, c->Hkv, L}).data_ptr());
     const int64_t m = dim(as_tensor(a[4], "dst_table"), "dst_table", 2, 1);

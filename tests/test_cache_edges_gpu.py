@@ -395,3 +395,37 @@ def test_every_kind_of_error_is_reported():
             fa.sync_status()
         assert e.value.status == status
     fa.sync_status()
+
+
+# ------------------------------------------------------------------ the cache's tensors
+def test_cache_tensors_with_other_memory():
+    """A call uses the memory that the cache's tensors have then, and refuses
+    tensors that have lost the cache's shape."""
+    fa = require_gpu()
+    cache, table, ln = R.make(fa, [40, 70], 2, 64, 16, seed=40)
+    q = queries(2, 4, 1, 64, 41)
+    want = fa.cache_fwd(q, cache, table, ln)[0]
+    old = {n: getattr(cache, n).clone() for n in ("k", "v", "ks", "vs", "kb")}
+    for name in old:
+        t = getattr(cache, name)
+        t.set_(t.clone())
+    fa.sync_status()
+    for name in old:
+        getattr(cache, name).copy_(old[name])
+    assert torch.equal(fa.cache_fwd(q, cache, table, ln)[0], want)
+    zero = torch.zeros_like(ln)
+    new = queries(2, 2, 3, 64, 42)
+    fa.cache_append(cache, new, new, table, zero)
+    assert not torch.equal(cache.k, old["k"])              # stored in the new memory
+    for name, t in old.items():
+        getattr(cache, name).copy_(t)
+    v = cache.v
+    for change in (lambda: v.set_(v[:-1].clone()), lambda: v.set_(old["v"].transpose(2, 3))):
+        change()
+        with pytest.raises(ValueError, match="v: expected"):
+            fa.cache_fwd(q, cache, table, ln)
+        with pytest.raises(ValueError, match="v: expected"):
+            fa.cache_append(cache, new, new, table, zero)
+        v.set_(old["v"].clone())
+    assert torch.equal(fa.cache_fwd(q, cache, table, ln)[0], want)
+    fa.sync_status()
