@@ -1,13 +1,16 @@
 """Compile the CUDA library in-tree for sm_103a: every .cu under csrc/ with
 nvcc in parallel, then one shared library ``libfa4fp4.so`` next to this file, and
 beside it the native Python binding of the cache calls, ``_cache_binding.so``
-(g++, against the installed torch).
+(g++, against the installed torch; left out, with a note, where torch or Python's
+headers are not installed: the library itself needs neither).
 Run ``python -m precision_attention_fa4fp4_gb300.build`` or call ``build()``."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +22,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hid
 
 
 BINDING = os.path.join(HERE, "_cache_binding.so")
+STAMP = os.path.join(OUT_DIR, "cache_binding.torch")
 
 
 def _cuda_home() -> str:
@@ -42,26 +46,35 @@ def _stale(out: str, deps: list[str]) -> bool:
 
 
 def _binding_commands(force: bool, header: str) -> tuple[list[str] | None, list[str] | None, str]:
-    """The binding's compile and link commands where they are needed, and the
-    torch version it is built against."""
-    import sysconfig
-
-    import torch
+    """The binding's compile and link commands where they are needed, and what it
+    is built against."""
+    include = sysconfig.get_paths()["include"]
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    if torch is None or not os.path.exists(os.path.join(include, "Python.h")):
+        print("the Python binding of the cache calls is left out: "
+              + ("torch is not installed" if torch is None else f"no Python.h in {include}"), file=sys.stderr)
+        return None, None, ""
     src = os.path.join(CSRC, "cache_binding.cpp")
     obj = os.path.join(OUT_DIR, "cache_binding.o")
-    stamp = os.path.join(OUT_DIR, "cache_binding.torch")
     root = os.path.dirname(torch.__file__)
-    built = open(stamp).read() if os.path.exists(stamp) else ""
-    fresh = not force and built == torch.__version__ and not _stale(obj, [src, header])
+    against = torch.__version__
+    built = ""
+    if os.path.exists(STAMP):
+        with open(STAMP) as f:
+            built = f.read()
+    fresh = not force and built == against and not _stale(obj, [src, header])
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+                "-I", include, "-isystem", os.path.join(root, "include"),
                 "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 "-isystem", os.path.join(_cuda_home(), "include"), "-c", src, "-o", obj]
     lib = os.path.join(root, "lib")
     link = ["g++", "-shared", "-o", BINDING + f".{os.getpid()}.tmp", obj, "-L" + HERE, "-lfa4fp4", "-L" + lib,
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
-    return (None if fresh else compile_), (None if fresh and not _stale(BINDING, [obj]) else link), torch.__version__
+    return (None if fresh else compile_), (None if fresh and not _stale(BINDING, [obj]) else link), against
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -76,7 +89,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", src, "-o", obj])
-    compile_binding, link_binding, torch_version = _binding_commands(force, headers[-1])
+    compile_binding, link_binding, against = _binding_commands(force, headers[-1])
     relink = force or bool(jobs)
     if compile_binding:
         jobs.insert(0, compile_binding)
@@ -99,8 +112,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError("link failed:\n" + res.stderr)
         os.replace(link_binding[3], BINDING)
-        with open(os.path.join(OUT_DIR, "cache_binding.torch"), "w") as f:
-            f.write(torch_version)
+        with open(STAMP, "w") as f:
+            f.write(against)
     return LIB
 
 
