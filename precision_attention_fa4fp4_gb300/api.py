@@ -569,8 +569,9 @@ def __getattr__(name):
         raise AttributeError(name)
     import importlib.machinery
     import importlib.util
+
+    from .build import BINDING as path
     load_library()
-    path = os.path.join(HERE, "_cache_binding.so")
     if not os.path.exists(path):
         raise RuntimeError(f"native binding not built: {path} (run __graft_entry__.build())")
     loader = importlib.machinery.ExtensionFileLoader("_cache_binding", path)

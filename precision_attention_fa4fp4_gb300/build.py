@@ -1,8 +1,9 @@
 """Compile the CUDA library in-tree for sm_103a: every .cu under csrc/ with
 nvcc in parallel, then one shared library ``libfa4fp4.so`` next to this file, and
-beside it the native Python binding of the cache calls, ``_cache_binding.so``
-(g++, against the installed torch; left out, with a note, where torch or Python's
-headers are not installed: the library itself needs neither).
+beside it the native Python binding of the cache calls, ``_cache_binding`` with
+the running Python's suffix (g++, against the installed torch; left out, with a
+note, where torch or Python's headers are not installed: the library itself needs
+neither).
 Run ``python -m precision_attention_fa4fp4_gb300.build`` or call ``build()``."""
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hid
          "--expt-relaxed-constexpr"]
 
 
-BINDING = os.path.join(HERE, "_cache_binding.so")
+BINDING = os.path.join(HERE, "_cache_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 STAMP = os.path.join(OUT_DIR, "cache_binding.torch")
 
 
@@ -60,7 +61,7 @@ def _binding_commands(force: bool, header: str) -> tuple[list[str] | None, list[
     src = os.path.join(CSRC, "cache_binding.cpp")
     obj = os.path.join(OUT_DIR, "cache_binding.o")
     root = os.path.dirname(torch.__file__)
-    against = torch.__version__
+    against = f"torch {torch.__version__}, {os.path.basename(BINDING)}"
     built = ""
     if os.path.exists(STAMP):
         with open(STAMP) as f:

@@ -3,6 +3,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -12,6 +13,10 @@ from precision_attention_fa4fp4_gb300 import build as b
 @pytest.fixture(scope="module")
 def built():
     return b.build()
+
+
+def header():
+    return os.path.join(os.path.dirname(b.HERE), "include", "fa4fp4.h")
 
 
 def test_library_builds_without_torch(built, tmp_path):
@@ -29,3 +34,16 @@ def test_library_builds_without_torch(built, tmp_path):
     assert run.returncode == 0, run.stderr
     assert "torch is not installed" in run.stderr
     assert (package / os.path.basename(b.LIB)).exists() and not (package / os.path.basename(b.BINDING)).exists()
+
+
+def test_binding_is_for_one_python_and_one_torch(built, monkeypatch, tmp_path):
+    assert b.BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and os.path.exists(b.BINDING)
+    assert b._binding_commands(False, header())[:2] == (None, None)
+    with open(b.STAMP) as f:
+        stamp = f.read()
+    for other in (stamp.replace("torch ", "torch 0."), stamp.replace("cpython-3", "cpython-2"), "2.11.0"):
+        path = tmp_path / "stamp"
+        path.write_text(other)
+        monkeypatch.setattr(b, "STAMP", str(path))
+        compile_, link, against = b._binding_commands(False, header())
+        assert compile_ and link and against == stamp
