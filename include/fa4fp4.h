@@ -418,7 +418,8 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_weigh(const fa4fp4_cache* cache, const voi
  * dst_table[b][0 ..] (int32 [B][dst_pages] with dst_pages * page >= budget;
  * pages of the same pool that no sequence of the call reads and no other row
  * writes), fitted to the destination's scales by the append's rule.  Sequence b
- * is then dst_table's row with new_lens[b] = min(lens[b], budget) tokens.
+ * is then dst_table's row with new_lens[b] = min(lens[b], budget) tokens (new_lens
+ * may be lens).
  * kept: int32 [B][Hkv][budget], the kept positions in ascending order, then -1.
  * weight_out (nullable): f32 [B][Hkv][dst_pages * page], the kept tokens'
  * weights, then 0; not the weight array itself.  0 <= recent <= budget,

@@ -94,7 +94,6 @@ __global__ void __launch_bounds__(NT1) cache_keep_kernel(const __grid_constant__
   const float* w = p.w + ((long long)b * c.Hkv + h) * c.max_pages * c.page;
   int* kept = p.kept + ((long long)b * c.Hkv + h) * p.budget;
   float* w_out = p.w_out ? p.w_out + ((long long)b * c.Hkv + h) * p.dst_pages * c.page : nullptr;
-  if (h == 0 && threadIdx.x == 0) p.new_lens[b] = keep;
 
   float x[EPT];
   auto load = [&](int base) {
@@ -186,6 +185,9 @@ __global__ void __launch_bounds__(NT2) cache_copy_kernel(const __grid_constant__
   const CacheView& c = p.c;
   const int h = blockIdx.y, b = blockIdx.z;
   const int keep = min(cache_len(c, b), p.budget);
+  // here, where a length already cut back gives the same: new_lens may be lens, and
+  // the first kernel's CTAs need the old ones
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.new_lens[b] = keep;
   const int first = blockIdx.x * P;
   if (first >= keep) return;
   const int dst = *(p.dst + (long long)b * p.dst_pages + blockIdx.x);

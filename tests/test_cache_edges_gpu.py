@@ -429,3 +429,35 @@ def test_cache_tensors_with_other_memory():
         v.set_(old["v"].clone())
     assert torch.equal(fa.cache_fwd(q, cache, table, ln)[0], want)
     fa.sync_status()
+
+
+# ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("d,page,budget", [(64, 16, 20), (64, 64, 1)])
+def test_evict_lengths_in_place(d, page, budget):
+    """new_lens may be lens itself, with more heads than the GPU works on at
+    once: every head is cut back from the old length."""
+    import ctypes
+    import struct
+    fa = require_gpu()
+    H, B, recent = 700, 2, 1
+    lens = [100, 37]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=38, spare=2 * (-(-budget // page)))
+    used = set(table.flatten().tolist())
+    per = -(-budget // page)
+    dst = torch.tensor([p for p in range(cache.num_pages) if p not in used][:B * per], dtype=torch.int32).view(B, per).cuda()
+    w = torch.rand(B, H, table.shape[1] * page, generator=torch.Generator().manual_seed(39)).cuda()
+    want_lens, want_kept, want_w = fa.cache_evict(cache, table, ln, w, dst, budget, recent)
+    fa.sync_status()
+    kept, out = torch.full_like(want_kept, -7), torch.full_like(want_w, -7)
+    c = struct.pack("@5P4i", *(t.data_ptr() for t in (cache.k, cache.v, cache.ks, cache.vs, cache.kb)), cache.num_pages, H,
+                    page, d)
+    lib = fa.load_library()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    call = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, *[ctypes.c_void_p] * 4, *[ctypes.c_int] * 5,
+                            *[ctypes.c_void_p] * 4)(("fa4fp4_cache_evict", lib))
+    in_place = ln.clone()
+    torch.cuda.synchronize()
+    assert call(c, p(table), p(in_place), p(w), p(dst), B, table.shape[1], per, budget, recent, p(in_place), p(kept), p(out),
+                ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    fa.sync_status()
+    assert torch.equal(in_place, want_lens) and torch.equal(kept, want_kept) and torch.equal(out, want_w)
