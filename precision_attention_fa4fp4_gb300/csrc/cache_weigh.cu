@@ -403,6 +403,7 @@ bool cache_weigh_fits(int B, int Hkv, int page, int max_pages) {
 
 cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   const long long rows = (long long)(p.Hq / p.c.Hkv) * p.T;
+  static_assert(WEIGH_MANY > 16, "below it the call makes the tensor map that the kernel for few rows reads");
   if (rows >= WEIGH_MANY) return launch_cache_weigh_rows(p, st);   // as the host decided on the tensor map
   if (rows <= 8) return p.c.d == 128 ? launch_few<128, 1>(p, st) : launch_few<64, 1>(p, st);
   if (rows <= 16) return p.c.d == 128 ? launch_few<128, 2>(p, st) : launch_few<64, 2>(p, st);
