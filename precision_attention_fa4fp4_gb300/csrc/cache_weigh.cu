@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
 constexpr int BLOCK = 64;                          // rows prepared at once
 
 template <int D>
-__global__ void __launch_bounds__(32 * NW, 4) cache_weigh_rows_kernel(const __grid_constant__ CacheWeighParams p) {
+__global__ void __launch_bounds__(32 * NW, 4) cache_weigh_block_kernel(const __grid_constant__ CacheWeighParams p) {
   constexpr int QW = D / 32;                       // 16-byte words of a lane's query operand
   __shared__ uint4 s_q[BLOCK / 8][QW][32];         // row tile, word, lane
   __shared__ float s_fx[BLOCK], s_ref[BLOCK], s_fac[BLOCK];
@@ -410,7 +410,7 @@ cudaError_t launch_cache_weigh(const CacheWeighParams& p, cudaStream_t st) {
   const long long cap = (long long)p.c.max_pages * p.c.page;
   const long long all = (cap + UNIT - 1) / UNIT * p.c.Hkv * p.c.B, most = 4LL * kSMs;
   const dim3 grid((unsigned)(all < most ? all : most));
-  return launch_next(p.c.d == 128 ? cache_weigh_rows_kernel<128> : cache_weigh_rows_kernel<64>, grid, 32 * NW, 0, st, p);
+  return launch_next(p.c.d == 128 ? cache_weigh_block_kernel<128> : cache_weigh_block_kernel<64>, grid, 32 * NW, 0, st, p);
 }
 
 }  // namespace fa4
