@@ -461,3 +461,115 @@ def test_evict_lengths_in_place(d, page, budget):
                 ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
     fa.sync_status()
     assert torch.equal(in_place, want_lens) and torch.equal(kept, want_kept) and torch.equal(out, want_w)
+
+
+# ------------------------------------------------------------------ what else the calls allow
+def fa_values(cache):
+    """|v| of every finite code in the pages, under their scales."""
+    v = np.abs(np.nan_to_num(R.E4M3[cache.v.cpu().numpy()]))
+    used = (cache.vs.cpu().numpy() != 200)[:, :, None, None]
+    return np.where(used, v * 2.0 ** (cache.vs.cpu().numpy().astype(np.float64) - 127)[:, :, None, None], 0)
+
+
+@pytest.mark.parametrize("f32", [True, False])
+def test_pages_listed_twice(f32):
+    """A page that is listed twice counts twice: o is the mean over the doubled
+    keys, and lse of pages that are all listed twice is ln 2 higher."""
+    fa = require_gpu()
+    d, page, H, G, T = 64, 16, 2, 4, 2
+    cache, table, ln = R.make(fa, [150, 70], H, d, page, seed=43)
+    q = queries(2, H * G, T, d, 44)
+    once = torch.tensor([0, 2, 3], dtype=torch.int32).expand(2, H, T, 3).contiguous().cuda()
+    twice = torch.tensor([2, 0, 3, 3, 2, 0], dtype=torch.int32).expand(2, H, T, 6).contiguous().cuda()
+    mixed = torch.tensor([3, 0, 3, 2, -1], dtype=torch.int32).expand(2, H, T, 5).contiguous().cuda()
+    dt = fa.OUT_F32 if f32 else fa.OUT_BF16
+    o1, l1 = fa.cache_fwd(q, cache, table, ln, pages=once, out_dtype=dt)
+    o2, l2 = fa.cache_fwd(q, cache, table, ln, pages=twice, out_dtype=dt)
+    fa.sync_status()
+    # The scores are the same.  Each side's weights carry the exponential (2^-19 of the
+    # spread) and P's f16 (2^-22 or 2^-11), each output half a step; |v| < 8
+    assert float(fa_values(cache).max()) < 8
+    tol = 2 * 8 * (2.0 ** -19 + (2.0 ** -22 + 2.0 ** -24 if f32 else 2.0 ** -11 + 2.0 ** -8))
+    assert np.abs(f64(o1) - f64(o2)).max() <= tol and np.abs(f64(l2) - f64(l1) - np.log(2)).max() <= 2 * 2.0 ** -18
+    check(fa, q, cache, table, ln, [150, 70], f32, pages=mixed)
+
+
+@pytest.mark.parametrize("B,H", [(100, 1), (300, 2)])
+@pytest.mark.parametrize("G,T", [(4, 1), (2, 7)])
+def test_many_sequences_few_rows(B, H, G, T):
+    """More sequences than a warp has lanes, few enough to be cut at their ends and
+    too many for that: attention, received weights and selection, with lengths of
+    zero in runs, queries that are none, and room in the table."""
+    fa = require_gpu()
+    d, page = 64, 32
+    g = torch.Generator().manual_seed(45)
+    lens = torch.randint(0, 700, (B,), generator=g)
+    lens[10:60] = 0
+    lens[70:90] = torch.arange(20)
+    q_lens = torch.randint(0, T + 1, (B,), generator=g)
+    cache, table, ln = R.make(fa, lens.tolist(), H, d, page, seed=46, room=500)
+    q = queries(B, H * G, T, d, 47)
+    ql = q_lens.int().cuda()
+    o = torch.full(q.shape, 7.0, device="cuda")
+    lse = torch.full(q.shape[:3], 7.0, device="cuda")
+    fa.cache_fwd(q, cache, table, ln, q_lens=ql, out=o, lse=lse, out_dtype=fa.OUT_F32)
+    w = torch.rand(B, H, table.shape[1] * page, device="cuda")
+    got = fa.cache_weigh(q, lse, cache, table, ln, w, q_lens=ql, out=torch.full_like(w, 5.0))
+    sel = fa.cache_select(q, cache, table, ln, 4, q_lens=ql)
+    fa.sync_status()
+    ref = R.Ref.of(cache, table)
+    wo, wl, spread, eps, small = ref.fwd(f64(q), lens, q_lens)
+    e = eps * d * 2.0 ** -23
+    rows = np.broadcast_to(np.arange(T)[None, None] < q_lens.numpy()[:, None, None], wl.shape)
+    tol = (4 * e + 2.0 ** -19 + 2.0 ** -22)[..., None] * spread + 2.0 ** -24 * np.abs(wo) + small[..., None]
+    assert (np.abs(f64(o) - wo) <= tol)[rows].all() and (f64(o)[~rows] == 7).all() and (f64(lse)[~rows] == 7).all()
+    assert np.array_equal(np.isneginf(f64(lse))[rows], np.isneginf(wl)[rows])
+    assert np.array_equal(sel.cpu().numpy(), ref.select(f64(q), lens, q_lens, 4))
+    want = ref.weigh(f64(q), np.where(rows, f64(lse), -np.inf), lens, q_lens, f64(w))
+    for b, n in enumerate(lens.tolist()):
+        recv = want[b, :, :n] - f64(w)[b, :, :n]
+        # as in the weights' own test: 2^-16 + 2^-21 |lse| with |lse| <= 16
+        tol = (2 * e[b].max(initial=0) + 2.0 ** -15) * recv + 2.0 ** -22 * want[b, :, :n]
+        assert (np.abs(f64(got[b, :, :n]) - want[b, :, :n]) <= tol).all() and (got[b, :, n:] == 5).all()
+
+
+def test_full_cache_and_no_new_tokens():
+    """Sequences at the table's capacity: nothing to append is no error."""
+    fa = require_gpu()
+    d, page, H = 64, 16, 2
+    cache, table, ln = R.make(fa, [48, 48, 20], H, d, page, seed=48)
+    before = [t.clone() for t in (cache.k, cache.v, cache.ks, cache.vs, cache.kb)]
+    x = queries(3, H, 5, d, 49)
+    fa.cache_append(cache, x, x, table, ln, n_new=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    fa.sync_status()
+    for a, b in zip(before, (cache.k, cache.v, cache.ks, cache.vs, cache.kb)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("G,T", [(4, 1), (4, 30)])
+def test_padded_rows_hold_anything(G, T):
+    """NaN and infinities in query rows behind q_lens and in their lse reach
+    nothing."""
+    fa = require_gpu()
+    d, page, H = 128, 64, 2
+    lens, q_lens = [200, 90, 131], [T, 0, (T + 1) // 2]
+    cache, table, ln = R.make(fa, lens, H, d, page, seed=50)
+    ql = torch.tensor(q_lens, dtype=torch.int32).cuda()
+    q = queries(3, H * G, T, d, 51)
+    bad = q.clone()
+    for b, n in enumerate(q_lens):
+        bad[b, :, n:] = float("nan") if b else float("inf")
+    w = torch.rand(3, H, table.shape[1] * page, device="cuda")
+    for f32 in (False, True):
+        dt = fa.OUT_F32 if f32 else fa.OUT_BF16
+        o1, l1 = fa.cache_fwd(q, cache, table, ln, q_lens=ql, out_dtype=dt)
+        o2, l2 = fa.cache_fwd(bad, cache, table, ln, q_lens=ql, out_dtype=dt)
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    nan = l1.clone()
+    for b, n in enumerate(q_lens):
+        nan[b, :, n:] = float("nan")
+    a = fa.cache_weigh(q, l1, cache, table, ln, w, q_lens=ql, out=w.clone())
+    b = fa.cache_weigh(bad, nan, cache, table, ln, w, q_lens=ql, out=w.clone())
+    assert torch.equal(a, b)
+    assert torch.equal(fa.cache_select(q, cache, table, ln, 2, q_lens=ql), fa.cache_select(bad, cache, table, ln, 2, q_lens=ql))
+    fa.sync_status()
