@@ -368,9 +368,12 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_append(const fa4fp4_cache* cache, const vo
  * 2^-36 of that V at most, or by 2^-90 of a far larger sum that it is added to;
  * f32 output takes P as a sum of two f16 (2^-22).  Scores up to
  * 2^22 in magnitude; beyond, the rounding of their maximum takes P out of its
- * range.  The result does not depend on anything but the arguments.  `workspace`: at least
+ * range.  The result does not depend on anything but the arguments.  (More than
+ * 64 rows Hq / Hkv * T are fastest with bf16 output and without pages: f32 output
+ * reads the keys again for every 16 rows.)  `workspace`: at least
  * fa4fp4_cache_fwd_workspace_bytes(...) bytes of device memory
- * (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs. */
+ * (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs; it needs no
+ * initialisation, but after FA4FP4_ERR_DEVICE_TIMEOUT zeros before its next use. */
 FA4FP4_API size_t fa4fp4_cache_fwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int page, int max_pages,
                                                    int n_sel);
 FA4FP4_API fa4fp4_status fa4fp4_cache_fwd(const fa4fp4_cache* cache, const void* q, const int* page_table,
@@ -400,7 +403,9 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const vo
  *   weight_out[b][hk][j] = weight_in[b][hk][j] + sum over the query heads of hk
  *                          and the tokens t that see j of e^(s - lse)
  * for j < lens[b], with fa4fp4_cache_fwd's arguments and the lse that it wrote
- * (rows with lse = -inf add nothing).  weights: f32 [B][Hkv][max_pages * page];
+ * (rows with an infinite lse add nothing).  The scores are sums of exact products
+ * in the tensor cores' FP32, which cuts where it adds, and the exponential is the
+ * native one: what is received is off by about 2^-23 of itself.  weights: f32 [B][Hkv][max_pages * page];
  * weight_out may be weight_in; entries j >= lens[b] are not written.  `workspace`
  * as for fa4fp4_cache_fwd; below 80 query rows per kv head (Hq / Hkv * T) it
  * needs none (its size is 0 and it may be NULL). */

@@ -17,8 +17,8 @@
 // HBM is the floor: d bytes read and written per kept token, head and tensor, 4
 // bytes of weight read per token.  16 sequences of 4001..8192 tokens to 4096, 8
 // heads of 128: 11 us of selection (its passes over the keys' bits, one after
-// the other) and 52 us of copy, 5.2 TB/s: instructions, most of them for the
-// exponents and the K bounds, keep it from more.  One of 4096 to 1000: 11.2 us.
+// the other) and 51 us of copy, 5.3 TB/s: instructions, most of them for the
+// exponents and the K bounds, keep it from more.  One of 4096 to 1000: 10.9 us.
 #include "cache_line.cuh"
 
 namespace fa4 {

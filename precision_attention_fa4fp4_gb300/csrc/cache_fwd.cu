@@ -35,9 +35,9 @@
 // unscaled: K's page scale multiplies the scores, V's goes into the exponent of
 // P, relative to that of the row's accumulator.
 //
-// 64 sequences of 1..8192 tokens, 32 / 8 heads of 128: 107-110 us, 5.2 TB/s; what
+// 64 sequences of 1..8192 tokens, 32 / 8 heads of 128: 110 us, 5.1 TB/s; what
 // is missing to a copy's 6.7 are the first 5 us of a launch and the ends of row
-// blocks.  One of 1000: 9.0 us (start 2, lens and pages 1.5, first keys 2, join
+// blocks.  One of 1000: 9.2 us (start 2, lens and pages 1.5, first keys 2, join
 // 2-3).  With 9 to 16 rows and FP32 output instructions bound it: 4 sequences of
 // 16001..32760, 8 heads of 64, 42 us, 2.4 TB/s.
 //
@@ -69,10 +69,11 @@ FA4_DEV float exp2f_whole(float x) { return __uint_as_float(__float_as_uint(x + 
 // Rows of a kv head above which the kernel for many rows takes over.  It takes
 // the same time for 1 to 128 of them, this one in proportion to blocks of 16.
 // Keys x sequences, heads of 128, 8 kv heads, us here / there:
-//   2048 x 16:  64 rows 60 / 59,  128 rows 107 / 51,  256 rows 195 / 63
-//   8192 x 1:   64 rows 25 / 32,  128 rows 35 / 32,   256 rows 55 / 43
-//   1024 x 1:   64 rows 15 / 22,  256 rows 18 / 23 (the price of one rule)
-// heads of 64, 4096 x 16: 64 rows 64 / 69, 96 rows 90 / 69.
+//   2048 x 16:  64 rows 63 / 60,  128 rows 114 / 52,  256 rows 208 / 64
+//   8192 x 1:   64 rows 26 / 32,  128 rows 36 / 31,   256 rows 58 / 41
+//   1024 x 1:   64 rows 16 / 22,  256 rows 19 / 23 (the price of one rule)
+// heads of 64, 4096 x 16: 64 rows 69 / 72, 96 rows 98 / 72.
+// FP32 output always comes here: 2048 x 16, 128 rows 142, 256 rows 265.
 constexpr int MANY_ROWS = 64;
 
 // Resident CTAs by registers, and the steps in flight that fill the shared
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
       // O^T += V^T P: lane rows (D / 8) g + 2 mt and + 1 of the head dimension.
       // The products' accumulators are cut, not rounded: for FP32 output a step's
       // sum is taken by itself and added with rounding, as the scores' are by 32
-      // dimensions.  All in all 3 us of 37 (4 x 16001..32760 keys), and on six
+      // dimensions.  All in all 3 us of 42 (4 x 16001..32760 keys), and on six
       // sequences of 4205..15496 an output off by 3.3e-7 of its norm (4.9e-7 in
       // plain FP32) that was off by more than 1e-6.
       float part[SPLIT ? NT : 1][4];

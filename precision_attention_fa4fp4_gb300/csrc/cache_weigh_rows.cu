@@ -25,7 +25,7 @@
 //   21    loads the rows by TMA, and their constants by bulk copies.
 //   22    looks the pages up and stages K's bytes by bulk copies (the conversion's
 //         own loads, page after table after length, took 4 us a key tile).
-// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 28.2 us (5 of them the first
+// 2 x 256 tokens over 4096, 32 / 8 heads of 128: 28.5 us (5 of them the first
 // kernel's), 0.59 PFLOP/s.  Latency bounds it: 512 key tiles are 3.4 an SM, so
 // four rounds of eight row tiles, and of the 1500 clocks of a step 470 are sums.
 #include "cache_line.cuh"
