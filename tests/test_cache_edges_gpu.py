@@ -573,3 +573,23 @@ def test_padded_rows_hold_anything(G, T):
     assert torch.equal(a, b)
     assert torch.equal(fa.cache_select(q, cache, table, ln, 2, q_lens=ql), fa.cache_select(bad, cache, table, ln, 2, q_lens=ql))
     fa.sync_status()
+
+
+@pytest.mark.parametrize("d,page,H,G,T,f32", FEW)
+def test_fwd_small_queries(d, page, H, G, T, f32):
+    """As in the kernel for many rows: query rows down to the smallest bf16 over pages
+    of zero keys and of very small ones, with pool page 0 unused."""
+    fa = require_gpu()
+    g = torch.Generator().manual_seed(52)
+    lens = [T + 5, 300, 128, 7, 290]
+    k = [torch.randn(H, n, d, generator=g) for n in lens]
+    k[1][:, 100:] = 0
+    k[2][:, 60:] *= 2.0 ** -120
+    k[4][:] = 0
+    v = [torch.randn(H, n, d, generator=g) for n in lens]
+    cache, table, ln, lens = cache_of(fa, k, v, page, 53, first=1)
+    q = queries(len(lens), H * G, T, d, 54)
+    q *= (2.0 ** -(torch.arange(H * G) % 14 * 10).float()).view(1, H * G, 1, 1).cuda()
+    for causal in (True, False):
+        for scale in (None, 1e-12):
+            check(fa, q, cache, table, ln, lens, f32, causal, scale)
