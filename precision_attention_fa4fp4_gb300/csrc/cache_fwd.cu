@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm(D, NT)) cache_fwd_kernel(
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float x = s[n][i][j] * kxc[i % NP] * fx[n][j & 1];
+            // (the factors first: K's times the sum alone may pass FP32's end)
+            float x = s[n][i][j] * (kxc[i % NP] * fx[n][j & 1]);
             if (!full) {
               const int key = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1);
               if (key >= vis[n][j & 1]) x = -INFINITY;

@@ -593,3 +593,24 @@ def test_fwd_small_queries(d, page, H, G, T, f32):
     for causal in (True, False):
         for scale in (None, 1e-12):
             check(fa, q, cache, table, ln, lens, f32, causal, scale)
+
+
+# ------------------------------------------------------------------ keys and queries far apart
+def around_one(*shape, seed):
+    """Magnitudes in [0.5, 2): exact under any power of two that bf16 has."""
+    g = torch.Generator().manual_seed(seed)
+    return (torch.rand(*shape, generator=g) * 1.5 + 0.5).bfloat16().float() * (torch.randint(0, 2, shape, generator=g) * 2 - 1)
+
+
+@pytest.mark.parametrize("k_up,q_up", [(120, -112), (-112, 120)])
+@pytest.mark.parametrize("d,page,H,G,T,f32", FEW + [(128, 64, 1, 2, 70, False), (64, 16, 1, 3, 90, True)])
+def test_fwd_keys_and_queries_far_apart(d, page, H, G, T, f32, k_up, q_up):
+    """Keys near one end of bf16's range under queries near the other, of scores of
+    ordinary size."""
+    fa = require_gpu()
+    lens = [T, 150, 700]
+    k = [around_one(H, n, d, seed=55 + i) * 2.0 ** k_up for i, n in enumerate(lens)]
+    v = [around_one(H, n, d, seed=60 + i) for i, n in enumerate(lens)]
+    cache, table, ln, lens = cache_of(fa, k, v, page, 56)
+    q = (around_one(len(lens), H * G, T, d, seed=57) * 2.0 ** q_up).bfloat16().cuda()
+    check(fa, q, cache, table, ln, lens, f32, scale=2.0 ** -7)
