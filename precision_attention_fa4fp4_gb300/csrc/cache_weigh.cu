@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(32 * NW, weigh_ctas(NT)) cache_weigh_kernel(co
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float x = s[n][i][j] * kx[i % NP];
-            const float e = ex2_approx(fmaf(x, fx[n][j & 1], -ref[n][j & 1]));
+            // (the factors first: K's times the sum alone may pass FP32's end)
+            const float e = ex2_approx(fmaf(s[n][i][j], kx[i % NP] * fx[n][j & 1], -ref[n][j & 1]));
             // (a row that does not see the key must not reach it as 0 * NaN either)
             bool sees = true;
             if (!full) sees = pos[i % NP] + (SMALLP ? 0 : 16 * i) + korder<D>(g) + 8 * (j >> 1) < vis[n][j & 1];

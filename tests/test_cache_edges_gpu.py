@@ -614,3 +614,24 @@ def test_fwd_keys_and_queries_far_apart(d, page, H, G, T, f32, k_up, q_up):
     cache, table, ln, lens = cache_of(fa, k, v, page, 56)
     q = (around_one(len(lens), H * G, T, d, seed=57) * 2.0 ** q_up).bfloat16().cuda()
     check(fa, q, cache, table, ln, lens, f32, scale=2.0 ** -7)
+
+
+@pytest.mark.parametrize("k_up,q_up", [(120, -112), (-112, 120)])
+@pytest.mark.parametrize("d,page,G,T", WEIGH)
+def test_weigh_keys_and_queries_far_apart(d, page, G, T, k_up, q_up):
+    """The same weights, bit for bit, as under keys and queries of ordinary size, whose
+    scores differ by nothing but powers of two that cancel."""
+    fa = require_gpu()
+    H, lens = 2, [T + 150, T, 129]
+    k = [around_one(H, n, d, seed=58 + i) for i, n in enumerate(lens)]
+    q = around_one(3, H * G, T, d, seed=59)
+    got = []
+    for ku, qu in ((k_up + q_up, 0), (k_up, q_up)):
+        cache, table, ln, _ = cache_of(fa, [x * 2.0 ** ku for x in k], k, page, 60)
+        x, scale = (q * 2.0 ** qu).bfloat16().cuda(), 0.03
+        w = torch.zeros(3, H, table.shape[1] * page, device="cuda")
+        if not got:
+            _, lse = fa.cache_fwd(x, cache, table, ln, softmax_scale=scale, out_dtype=fa.OUT_F32)
+        got.append(fa.cache_weigh(x, lse, cache, table, ln, w, softmax_scale=scale))
+    fa.sync_status()
+    assert torch.equal(*got)
