@@ -405,7 +405,8 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_select(const fa4fp4_cache* cache, const vo
  * for j < lens[b], with fa4fp4_cache_fwd's arguments and the lse that it wrote
  * (rows with an infinite lse add nothing).  The scores are sums of exact products
  * in the tensor cores' FP32, which cuts where it adds, and the exponential is the
- * native one: what is received is off by about 2^-23 of itself.  weights: f32 [B][Hkv][max_pages * page];
+ * native one: for scores of ordinary size what is received is off by 2^-23 of its
+ * norm, a single weight by up to 2^-20.  weights: f32 [B][Hkv][max_pages * page];
  * weight_out may be weight_in; entries j >= lens[b] are not written.  `workspace`
  * as for fa4fp4_cache_fwd; below 80 query rows per kv head (Hq / Hkv * T) it
  * needs none (its size is 0 and it may be NULL). */
