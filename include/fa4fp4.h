@@ -435,6 +435,111 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_evict(const fa4fp4_cache* cache, const int
                                             int dst_pages, int budget, int recent, int* new_lens, int* kept,
                                             float* weight_out, void* stream);
 
+/* Operators around the attention calls: norm and rotation of queries and keys,
+ * and attention of queries to keys of another length.  Their tensors may be
+ * strided views (slices of a fused projection, transposes of [B][N][H][d]):
+ * logical [B][H][N][d], element (b, h, n, i) at ptr + b stride_b + h stride_h + n
+ * stride_n + i, strides in elements.  The last dimension is dense; ptr is 16-byte
+ * aligned, and so is every row: strides (of dimensions larger than 1) are
+ * multiples of 16 bytes, at least 0 and at most 2^40 bytes.  An input may have
+ * strides of 0 (a broadcast).  The rows of an output do not overlap. */
+typedef struct {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_n;
+} fa4fp4_heads;
+
+/* The rotation by position.  Channel pair i < d / 2 is (i, i + d / 2), or (2i,
+ * 2i + 1) when interleaved, and turns by positions[axis(i)] * freqs[i] radians;
+ * the first sections[0] pairs belong to axis 0, the next sections[1] to axis 1 and
+ * so on (1 to 4 axes, sections sum to d / 2).  positions: int32 in DEVICE memory,
+ * [B][axes][N], or [axes][N] for all sequences when shared, 4-byte aligned, of any
+ * sign.  sections and freqs (64-bit, d / 2 of them, finite) are HOST arrays, read
+ * during the call only.  Angles are reduced to a turn in 64-bit integers, so they
+ * are as exact at far positions as at near ones: for |freqs[i]| <= 2 pi they are
+ * off by |position| 2^-52 and 2^-30 at most. */
+typedef struct {
+  const int* positions;
+  int shared;
+  int axes;
+  const int* sections;
+  const double* freqs;
+  int interleaved;
+} fa4fp4_rotation;
+
+/* The norm of every row of d channels: n = x w / sqrt(mean(x^2) + eps), w the
+ * weight of its tensor ([d], f32 or bf16 by weight_dtype (fa4fp4_out_dtype), device
+ * memory, 16-byte aligned; NULL: ones).  eps >= 0. */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  int weight_dtype;
+  float eps;
+} fa4fp4_norm;
+
+/* Norm and rotation of queries and keys in one pass: q bf16 [B][Hq][N][d], k bf16
+ * [B][Hkv][N][d] (NULL: queries alone; Hkv is then 0), norm NULL for the rotation
+ * alone, rotation NULL for the norm alone (not both NULL).  All arithmetic is FP32
+ * (the angles as above), rounded once to bf16.  q_out may be q and k_out may be k.
+ * Hq and Hkv need not divide each other. */
+FA4FP4_API fa4fp4_status fa4fp4_norm_rope(const fa4fp4_heads* q, const fa4fp4_heads* k, int B, int Hq, int Hkv,
+                                          int N, int d, const fa4fp4_norm* norm,
+                                          const fa4fp4_rotation* rotation, const fa4fp4_heads* q_out,
+                                          const fa4fp4_heads* k_out, void* stream);
+
+/* Its gradients: from q, k as they went in and the outputs' gradients dq_out,
+ * dk_out (f32, as fa4fp4_bwd writes them, or bf16, by dout_dtype), with g the
+ * gradient turned back, r = 1 / sqrt(mean(x^2) + eps), u = g w:
+ *   dx = r (u - x r mean(u x r)),  dw = sum over b, h, n of g x r
+ * dq, dk: bf16; dq_weight, dk_weight: f32 [d] (NULL where not wanted; without a
+ * norm they must be NULL).  All sums are FP32, in an order that depends on the
+ * shapes and the GPU's number of multiprocessors alone.  `workspace`: at least
+ * fa4fp4_norm_rope_bwd_workspace_bytes(...) bytes of device memory (its size is 0,
+ * and it may be NULL, for an empty problem), for this call alone while it runs; it
+ * needs no initialisation.  Without a dq_weight or dk_weight it is not used and may
+ * be NULL. */
+FA4FP4_API size_t fa4fp4_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
+FA4FP4_API fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const fa4fp4_heads* dk_out, int dout_dtype,
+                                              const fa4fp4_heads* q, const fa4fp4_heads* k, int B, int Hq, int Hkv,
+                                              int N, int d, const fa4fp4_norm* norm,
+                                              const fa4fp4_rotation* rotation, const fa4fp4_heads* dq,
+                                              const fa4fp4_heads* dk, float* dq_weight, float* dk_weight,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* BF16 attention of queries to keys of another length (cross attention to an
+ * encoder's states), beside fa4bf16_fwd: q bf16 [B][Hq][Nq][d], k and v bf16
+ * [B][Hkv][Nk][d], query head h reads kv head h / (Hq / Hkv), no causal mask.
+ * kv_lens (int32 [B], device memory, 4-byte aligned; NULL: Nk) is each sequence's
+ * number of keys; keys behind it may be anything, NaN too.  A length outside 0 ..
+ * Nk is taken as the nearer end and the next fa4fp4_sync_status returns
+ * FA4FP4_ERR_DEVICE_INDEX.
+ *   s = softmax_scale * q.k, o = softmax(s) v, lse = ln sum e^s (nullable)
+ * o: bf16; lse: f32 [B][Hq][Nq], dense.  Without a key o = 0 and lse = -inf.
+ * Products are exact, sums FP32; P is rounded to bf16 (half a step: 2^-9) for the
+ * product with V, its sum is taken before that.  Nq and Nk may be 0 (k and v are
+ * then not read; no query is an empty problem). */
+FA4FP4_API fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, const fa4fp4_heads* v,
+                                           const int* kv_lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                           float softmax_scale, const fa4fp4_heads* o, float* lse, void* stream);
+
+/* Its gradients, from the o and lse that it wrote and the gradient dout of o
+ * (bf16): with P = e^(s - lse), dP = dO V^T, D = rowsum(dO o), dS = P (dP - D),
+ *   dV = P^T dO, dK = softmax_scale dS^T Q, dQ = softmax_scale dS K
+ * dV and dK summed over the query heads of their kv head.  dq, dk, dv: bf16, fully
+ * written (zeros for keys behind kv_lens and for queries without a key).  P and dS
+ * are rounded to bf16 for the products, the sums are FP32 and are added in an order
+ * that depends on the shapes and the GPU's number of multiprocessors alone.
+ * `workspace`: at least fa4bf16_cross_bwd_workspace_bytes(...) bytes of device
+ * memory (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs; it
+ * needs no initialisation.  Nq == 0 gives zeros for dk and dv, Nk == 0 zeros for
+ * dq. */
+FA4FP4_API size_t fa4bf16_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+FA4FP4_API fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, const fa4fp4_heads* v,
+                                           const fa4fp4_heads* o, const fa4fp4_heads* dout, const float* lse,
+                                           const int* kv_lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                           float softmax_scale, const fa4fp4_heads* dq, const fa4fp4_heads* dk,
+                                           const fa4fp4_heads* dv, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
 /* Synchronizes `stream`, then returns FA4FP4_ERR_CUDA for a pending CUDA error
  * or, for what kernels reported, FA4FP4_ERR_DEVICE_TIMEOUT if any bounded wait
  * expired, FA4FP4_ERR_DEVICE_INDEX or FA4FP4_ERR_DEVICE_NONFINITE for what the

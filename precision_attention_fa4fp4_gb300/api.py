@@ -82,6 +82,10 @@ def load_library():
         lib.fa4fp4_cache_select_workspace_bytes.argtypes = [i] * 4
         lib.fa4fp4_cache_weigh_workspace_bytes.restype = sz
         lib.fa4fp4_cache_weigh_workspace_bytes.argtypes = [i] * 5
+        lib.fa4fp4_norm_rope_bwd_workspace_bytes.restype = sz
+        lib.fa4fp4_norm_rope_bwd_workspace_bytes.argtypes = [i] * 5
+        lib.fa4bf16_cross_bwd_workspace_bytes.restype = sz
+        lib.fa4bf16_cross_bwd_workspace_bytes.argtypes = [i] * 6
         lib.fa4fp4_sync_status.restype = i
         lib.fa4fp4_sync_status.argtypes = [vp]
         _lib = lib
@@ -558,14 +562,16 @@ def bwd_noalloc(q4: QTensor, k4: QTensor, q8c: QTensor, k8c: QTensor, v8r: QTens
 
 
 # ----------------------------------------------------------------------------
-# the 8-bit key/value cache: the calls are in the native module _cache_binding
-# (csrc/cache_binding.cpp), loaded by the first use of one of its names
+# the 8-bit key/value cache, norm and rotation, cross attention: the calls are in
+# the native module _cache_binding (csrc/cache_binding.cpp), loaded by the first
+# use of one of its names
 # ----------------------------------------------------------------------------
-_CACHE_NAMES = ("KVCache", "cache_append", "cache_fwd", "cache_select", "cache_weigh", "cache_evict")
+_NATIVE_NAMES = ("KVCache", "cache_append", "cache_fwd", "cache_select", "cache_weigh", "cache_evict",
+                "qk_norm_rope", "qk_norm_rope_bwd", "cross_fwd", "cross_bwd")
 
 
 def __getattr__(name):
-    if name not in _CACHE_NAMES:
+    if name not in _NATIVE_NAMES:
         raise AttributeError(name)
     import importlib.machinery
     import importlib.util
@@ -578,7 +584,7 @@ def __getattr__(name):
     binding = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache_binding", loader))
     loader.exec_module(binding)
     binding.set_error(Fa4Fp4Error)
-    for n in _CACHE_NAMES:
+    for n in _NATIVE_NAMES:
         globals()[n] = getattr(binding, n)
     return globals()[name]
 
@@ -601,3 +607,23 @@ def cache_select_workspace_bytes(B, Hkv, T, max_pages) -> int:
 
 def cache_weigh_workspace_bytes(B, Hq, Hkv, T, d) -> int:
     return int(load_library().fa4fp4_cache_weigh_workspace_bytes(B, Hq, Hkv, T, d))
+
+
+def rope_freqs(d: int, sections=None, base: float = 10000.0) -> torch.Tensor:
+    """The rotation's usual frequencies, radians a position, for qk_norm_rope:
+    float64 [d / 2] on the CPU.  Every axis of n channel pairs (sections; one axis of
+    d / 2 by default) has its own ladder base^(-i / n), i < n."""
+    sections = [d // 2] if sections is None else list(sections)
+    if d < 2 or d % 2 or min(sections, default=-1) < 0 or sum(sections) != d // 2:
+        raise ValueError(f"sections: expected numbers of channel pairs, {d // 2} in all")
+    if not base > 0:
+        raise ValueError("base must be positive")
+    return torch.cat([float(base) ** (-torch.arange(n, dtype=torch.float64) / max(n, 1)) for n in sections])
+
+
+def qk_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d) -> int:
+    return int(load_library().fa4fp4_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d))
+
+
+def cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d) -> int:
+    return int(load_library().fa4bf16_cross_bwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))

@@ -1,7 +1,7 @@
 """Compile the CUDA library in-tree for sm_103a: every .cu under csrc/ with
 nvcc in parallel, then one shared library ``libfa4fp4.so`` next to this file, and
-beside it the native Python binding of the cache calls, ``_cache_binding`` with
-the running Python's suffix (g++, against the installed torch; left out, with a
+beside it the native Python binding of the calls of every layer (cache, norm and
+rotation, cross attention), ``_cache_binding`` with the running Python's suffix (g++, against the installed torch; left out, with a
 note, where torch or Python's headers are not installed: the library itself needs
 neither).
 Run ``python -m precision_attention_fa4fp4_gb300.build`` or call ``build()``."""
@@ -55,7 +55,7 @@ def _binding_commands(force: bool, header: str) -> tuple[list[str] | None, list[
     except ImportError:
         torch = None
     if torch is None or not os.path.exists(os.path.join(include, "Python.h")):
-        print("the Python binding of the cache calls is left out: "
+        print("the native Python binding is left out: "
               + ("torch is not installed" if torch is None else f"no Python.h in {include}"), file=sys.stderr)
         return None, None, ""
     src = os.path.join(CSRC, "cache_binding.cpp")
@@ -66,7 +66,8 @@ def _binding_commands(force: bool, header: str) -> tuple[list[str] | None, list[
     if os.path.exists(STAMP):
         with open(STAMP) as f:
             built = f.read()
-    fresh = not force and built == against and not _stale(obj, [src, header])
+    parts = [os.path.join(CSRC, f) for f in ("binding.h", "cross_binding.h")]
+    fresh = not force and built == against and not _stale(obj, [src, header, *parts])
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                 "-I", include, "-isystem", os.path.join(root, "include"),

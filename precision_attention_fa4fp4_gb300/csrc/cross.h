@@ -1,0 +1,25 @@
+// cross.h -- host-side declarations of the cross attention kernels.  Not part of
+// the ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include "rope.h"
+
+namespace fa4 {
+
+struct CrossParams {
+  Strided q, k, v, o, dout, dq, dk, dv;   // the last four: backward only
+  float* lse;                             // [B][Hq][Nq]; nullable forward
+  const int* lens;                        // [B] or nullptr (Nk)
+  unsigned* err;
+  int B, Hq, Hkv, Nq, Nk, d;
+  float scale, c;                         // softmax scale, fl32(scale * log2 e)
+  uint8_t* work;                          // backward workspace
+};
+cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st);
+size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st);
+
+}  // namespace fa4

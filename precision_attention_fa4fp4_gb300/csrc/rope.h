@@ -1,0 +1,39 @@
+// rope.h -- host-side declarations of the norm and rotation kernels.  Not part
+// of the ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fa4 {
+
+// A strided [B][H][N][d] tensor: element strides, the last dimension dense.
+struct Strided {
+  void* p;
+  long long b, h, n;
+};
+
+struct RopeTensor {            // q or k
+  Strided x, dy, out;          // dy: backward only
+  const void* w;               // norm weight [d] or nullptr
+  float* part;                 // backward: weight gradient partials [CTAs of the tensor][d]
+  float* dw;                   // backward: weight gradient [d] or nullptr
+  int H;
+};
+struct RopeParams {
+  RopeTensor t[2];
+  const int* pos;              // [B or 1][axes][N], or nullptr: no rotation
+  long long pos_b;             // its stride between sequences
+  uint64_t turn[64];           // turns a position of each channel pair, 0.64 fixed point
+  uint8_t axis[64];            // axis of each channel pair
+  int B, N, d, norm, w_bf16, pairs, dy_f32;
+  int ctas[2];                 // backward: CTAs of each tensor
+  float eps;
+};
+cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t st);
+
+// CTAs that the backward gives q and k (a rule of shapes and SMs).
+void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas);
+cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st);
+
+}  // namespace fa4
