@@ -13,12 +13,21 @@ FA4_DEV __nv_bfloat16* at(const Strided& t, int b, int h, int n) {
 
 // Keys of sequence b; a length outside 0 .. Nk is reported and taken as the nearer
 // end.
-FA4_DEV int key_count(const CrossParams& p, int b) {
+FA4_DEV int key_count(const CrossParams& p, int b, bool report = true) {
   if (!p.lens) return p.Nk;
   const int len = p.lens[b];
   if (len >= 0 && len <= p.Nk) return len;
-  atomicOr(p.err, FA4_DEVERR_INDEX);
+  if (report) atomicOr(p.err, FA4_DEVERR_INDEX);
   return len < 0 ? 0 : p.Nk;
+}
+
+// A box at channel c, row n, head h, sequence b.
+FA4_DEV void tma_heads(void* dst, const HeadsMap& m, uint64_t* bar, int c, int n, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(&m.map)), "r"(smem_u32(bar)), "r"(c), "r"(n), "r"(h * m.own_h), "r"(b * m.own_b)
+      : "memory");
 }
 
 // x . row, x in shared memory.

@@ -18,6 +18,16 @@ struct CrossParams {
   float scale, c;                         // softmax scale, fl32(scale * log2 e)
   uint8_t* work;                          // backward workspace
 };
+
+// A tiled map of one of the tensors, and whether its heads and sequences have
+// places of their own (0: broadcast, all at coordinate 0).
+struct HeadsMap {
+  CUtensorMap map;
+  int own_h, own_b;
+};
+bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads);
+int sm_count();
+
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st);
 size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st);

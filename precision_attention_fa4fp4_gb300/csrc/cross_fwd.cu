@@ -1,58 +1,464 @@
-// cross_fwd.cu -- attention of queries to keys of another length, one warp per
-// query row: 32 keys at a time, a lane's score each, an online softmax over the
-// lanes, then the 32 rows of V with d / 32 channels a lane.
+// cross_fwd.cu -- BF16 attention of many query rows to keys of another length
+// (tcgen05), a persistent grid.
+//
+// A tile is 128 query rows of one kv head: 128 rows of a query head, or, where
+// the heads have up to 64 rows, as many of its query heads as fit.  A work item is two
+// neighbouring tiles A and B, which share K and V.  The CTAs take the items in turn
+// (item i goes to CTA i mod grid), so that those at work at a time read the
+// same K and V.  12 warps:
+//   warps 0-3  softmax of tile A, warps 4-7 of tile B: a thread per row.  P =
+//              2^(c s - c m) rounded to bf16 into tensor memory over S, the
+//              normalizer from P before the rounding; the reference m follows the
+//              running maximum only when that passes it by 2^8 (P stays within
+//              bf16's range and relative precision), and only then O is rescaled.
+//              Then O / l to the row's place, 32 bytes at a time.
+//   warp 8     producer: Q tiles through one ring, K and V tiles through another,
+//              ahead of the item at work.
+//   warp 9     issues the products: S = Q K^T, O += P V (P from tensor memory, V
+//              MN-major).  The next S of a tile follows its P V, across items too.
+// Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "cross.cuh"
+#include "internal.h"
 
 namespace fa4 {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int BM = 128, BN = 128;
+constexpr int NTHREADS = 384;
+constexpr int W_PROD = 8, W_MMA = 9;
+constexpr int REG_SOFT = 208, REG_MISC = 88;   // 2 x 208 + 88 = 504 of 512
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
+constexpr float TAU = 8.f;                     // log2 units
+
+struct Params {
+  CrossParams p;
+  HeadsMap q, k, v;
+  int tiles;        // per (sequence, kv head)
+  int per_head;     // tiles of a query head (1 where heads share a tile)
+  int heads;        // query heads of a tile
+  int pairs;        // items per (sequence, kv head)
+  int items;
+  int box;          // rows that a Q box brings
+  int o32;          // rows of O begin on 32 bytes
+};
 
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) cross_fwd_kernel(const __grid_constant__ CrossParams p) {
-  constexpr int C = D / 32;
-  __shared__ float qs[WARPS][D];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const long long row = (long long)blockIdx.x * WARPS + warp;
-  if (row >= (long long)p.B * p.Hq * p.Nq) return;
-  const int n = (int)(row % p.Nq), bh = (int)(row / p.Nq), h = bh % p.Hq, b = bh / p.Hq, hk = h / (p.Hq / p.Hkv);
-  const int len = key_count(p, b);
-  const __nv_bfloat16* q = at(p.q, b, h, n);
-  for (int i = lane; i < D; i += 32) qs[warp][i] = __bfloat162float(q[i]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[C] = {};
-  for (int j0 = 0; j0 < len; j0 += 32) {
-    const int j = j0 + lane;
-    const float s = j < len ? dot<D>(qs[warp], at(p.k, b, hk, j)) * p.c : -INFINITY;
-    float top = s;
-    for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float now = fmaxf(m, top);
-    const float e = j < len ? exp2f(s - now) : 0.f;
-    const float a = m == -INFINITY ? 0.f : exp2f(m - now);
-    m = now;
-    l = l * a + e;
-    for (int i = 0; i < C; ++i) o[i] *= a;
-    for (int x = 0; x < min(32, len - j0); ++x) {
-      const float w = __shfl_sync(0xffffffffu, e, x);
-      const __nv_bfloat16* v = at(p.v, b, hk, j0 + x) + lane * C;
-      for (int i = 0; i < C; ++i) o[i] = fmaf(w, __bfloat162float(v[i]), o[i]);
+struct Smem {
+  static constexpr int CH = 128 * 128;              // [128 rows][64 channels]
+  static constexpr int TILE = (D / 64) * CH;
+  static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
+  static constexpr int OFF_Q = 0, OFF_KV = OFF_Q + QS * TILE;
+  static constexpr int OFF_BAR = OFF_KV + KS * TILE;
+  static constexpr int NBAR = 2 * QS + 2 * KS + 6 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+  static constexpr int BYTES = OFF_MISC + 16 + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory budget");
+};
+
+// Where an item lies.
+struct Item {
+  int b, hk, tile0, len, nt;
+  bool two;
+};
+
+// The next item of this CTA from `i` on that has keys (skipping the others, which
+// the softmax warps alone see to); `len` is kept from item to item.
+struct Walk {
+  int i, b = -1, len = 0;
+  FA4_DEV Walk() : i(blockIdx.x) {}
+  FA4_DEV bool at(const Params& a, Item& it, bool report) {
+    if (i >= a.items) return false;
+    const int bh = i / a.pairs;
+    it.b = bh / a.p.Hkv;
+    it.hk = bh % a.p.Hkv;
+    it.tile0 = 2 * (i % a.pairs);
+    it.two = it.tile0 + 1 < a.tiles;
+    if (it.b != b) {
+      b = it.b;
+      len = key_count(a.p, b, report);
+    }
+    it.len = len;
+    it.nt = (len + BN - 1) / BN;
+    return true;
+  }
+  FA4_DEV void next() { i += gridDim.x; }
+  FA4_DEV bool with_keys(const Params& a, Item& it, bool report) {
+    while (at(a, it, report)) {
+      if (it.nt > 0) return true;
+      next();
+    }
+    return false;
+  }
+};
+
+FA4_DEV float rowmax128(const float (&s)[4][32]) {
+  float a[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a[i] = fmax3(s[0][i], s[1][i], fmaxf(s[2][i], s[3][i]));
+#pragma unroll
+  for (int n = 32; n > 1; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) a[i] = fmaxf(a[i], a[i + n / 2]);
+  return a[0];
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_constant__ Params a) {
+  using L = Smem<D>;
+  constexpr int QS = L::QS, KS = L::KS;
+  const CrossParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* q_empty = q_full + QS;
+  uint64_t* kv_full = q_empty + QS;
+  uint64_t* kv_empty = kv_full + KS;
+  uint64_t* s_full = kv_empty + KS;          // [X]: S_X is there
+  uint64_t* p_full = s_full + 2;             // [X]: P_X is there, O_X rescaled
+  uint64_t* o_done = p_full + 2;             // [X]: P_X V is in O_X
+  uint64_t* mma_done = o_done + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
+    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int x = 0; x < 2; ++x) { mbar_init(&s_full[x], 1); mbar_init(&p_full[x], 4); mbar_init(&o_done[x], 1); }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+
+  if (warp >= W_PROD) {
+    setmaxnreg_dec<REG_MISC>();
+    if (warp == W_PROD) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        tma_prefetch_desc(&a.q.map);
+        tma_prefetch_desc(&a.k.map);
+        tma_prefetch_desc(&a.v.map);
+        const int G = p.Hq / p.Hkv;
+        int qn = 0, kn = 0;                  // tiles issued into each ring
+        auto load_q = [&](const Item& it, int tile) -> bool {
+          const int st = qn % QS;
+          if (qn >= QS && !mbar_wait(&q_empty[st], (qn / QS - 1) & 1, abort_flag, p.err)) return false;
+          mbar_arrive_expect_tx(&q_full[st], a.box * 2 * D);
+          const int h = it.hk * G + tile / a.per_head * a.heads, n = tile % a.per_head * BM;
+          for (int c = 0; c < D / 64; ++c)
+            tma_heads(smem + L::OFF_Q + st * L::TILE + c * L::CH, a.q, &q_full[st], 64 * c, n, h, it.b);
+          ++qn;
+          return true;
+        };
+        auto load_kv = [&](const HeadsMap& m, const Item& it, int j) -> bool {
+          const int st = kn % KS;
+          if (kn >= KS && !mbar_wait(&kv_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
+          mbar_arrive_expect_tx(&kv_full[st], L::TILE);
+          for (int c = 0; c < D / 64; ++c)
+            tma_heads(smem + L::OFF_KV + st * L::TILE + c * L::CH, m, &kv_full[st], 64 * c, j * BN, it.hk, it.b);
+          ++kn;
+          return true;
+        };
+        Walk w;
+        Item it;
+        bool ok = true;
+        for (; ok && w.with_keys(a, it, true); w.next()) {
+          ok = load_q(it, it.tile0) && load_kv(a.k, it, 0) && (!it.two || load_q(it, it.tile0 + 1)) &&
+               load_kv(a.v, it, 0);
+          for (int j = 1; ok && j < it.nt; ++j) ok = load_kv(a.k, it, j) && load_kv(a.v, it, j);
+        }
+        if (*abort_flag) {
+          volatile int no_abort = 0;
+          for (int i = max(0, qn - QS); i < qn; ++i) mbar_wait(&q_full[i % QS], (i / QS) & 1, &no_abort, p.err);
+          for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait(&kv_full[i % KS], (i / KS) & 1, &no_abort, p.err);
+        }
+      }
+      __syncwarp();
+    } else if (warp == W_MMA) {
+      // ---------------------------------------------------------- products
+      const bool leader = elect_one();
+      const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
+      const uint32_t idesc_o = idesc_f16(BM, D, true, false, true);
+      // a key tile of an item, and where its operands are
+      struct Step {
+        Item it;
+        int j, kv, q;                        // key tile; ring positions of its K, and of the item's Q tiles
+      };
+      Walk w;
+      int qn = 0, kn = 0;
+      auto first = [&](Step& s) -> bool {
+        if (!w.with_keys(a, s.it, false)) return false;
+        s.j = 0;
+        s.kv = kn;
+        s.q = qn;
+        return true;
+      };
+      auto after = [&](const Step& s, Step& n) -> bool {
+        kn = s.kv + 2;
+        if (s.j + 1 < s.it.nt) {
+          n = s;
+          ++n.j;
+          n.kv = kn;
+          return true;
+        }
+        qn = s.q + (s.it.two ? 2 : 1);
+        w.next();
+        return first(n);
+      };
+      int pn[2] = {0, 0};                    // P V issued of each tile
+      auto issue_qk = [&](int x, const Step& s) -> bool {
+        const int ks = s.kv % KS, q = s.q + x, qs = q % QS;
+        if (s.j == 0 && !mbar_wait(&q_full[qs], (q / QS) & 1, abort_flag, p.err)) return false;
+        if (!mbar_wait(&kv_full[ks], (s.kv / KS) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+        const uint32_t sq = smem_u32(smem + L::OFF_Q + qs * L::TILE), sk = smem_u32(smem + L::OFF_KV + ks * L::TILE);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * L::CH + (k % 4) * 32;
+            mma_f16(tbase + COL_S0 + 128 * x, make_sdesc(sq + off, 16, 1024, SW_128B),
+                    make_sdesc(sk + off, 16, 1024, SW_128B), idesc_s, k > 0);
+          }
+          mma_commit(&s_full[x]);
+          if (x == 1 || !s.it.two) mma_commit(&kv_empty[ks]);
+          if (s.j == s.it.nt - 1) mma_commit(&q_empty[qs]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int x, const Step& s) -> bool {
+        const int seq = s.kv + 1, st = seq % KS;
+        uint8_t* v = smem + L::OFF_KV + st * L::TILE;
+        if (x == 0) {
+          if (!mbar_wait(&kv_full[st], (seq / KS) & 1, abort_flag, p.err)) return false;
+          // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not
+          const int keep = s.it.len - s.j * BN;
+          if (keep < BN && s.it.len < p.Nk) {
+            for (int c = 0; c < D / 64; ++c)
+              for (int i = keep * 8 + lane; i < BN * 8; i += 32)
+                reinterpret_cast<uint4*>(v + c * L::CH)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!mbar_wait(&p_full[x], pn[x] & 1, abort_flag, p.err)) return false;
+        ++pn[x];
+        tc_fence_after();
+        const uint32_t sv = smem_u32(v);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + COL_S0 + 128 * x + 8 * k,
+                           make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, s.j > 0 || k > 0);
+          mma_commit(&o_done[x]);
+          if (x == 1 || !s.it.two) mma_commit(&kv_empty[st]);
+        }
+        __syncwarp();
+        return true;
+      };
+      Step cur, nxt;
+      bool more = first(cur);
+      bool ok = !more || (issue_qk(0, cur) && (!cur.it.two || issue_qk(1, cur)));
+      while (ok && more) {
+        const bool then = after(cur, nxt);
+        ok = issue_pv(0, cur) && (!then || issue_qk(0, nxt)) && (!cur.it.two || issue_pv(1, cur)) &&
+             (!then || !nxt.it.two || issue_qk(1, nxt));
+        more = then;
+        cur = nxt;
+      }
+      if (leader) mma_commit(mma_done);
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait(mma_done, 0, &no_abort, p.err);
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<REG_SOFT>();
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
+    const uint32_t col_s = COL_S0 + 128 * x, col_o = COL_O0 + D * x;
+    const float c = p.c;
+    const int G = p.Hq / p.Hkv;
+    int n = 0;                               // key tiles of this warp's tile so far
+    bool ok = true;
+    Walk w;
+    Item it;
+    for (; ok && w.at(a, it, false); w.next()) {
+      if (x == 1 && !it.two) continue;
+      const int tile = it.tile0 + x;
+      int g, row;
+      if (a.heads > 1) {
+        g = tile * a.heads + r / p.Nq;
+        row = r % p.Nq;
+        if (r >= a.heads * p.Nq) g = G;
+      } else {
+        g = tile / a.per_head;
+        row = tile % a.per_head * BM + r;
+      }
+      const bool valid = g < G && row < p.Nq;
+      float m = 0.f, mc = 0.f, l = 0.f;
+      for (int j = 0; j < it.nt; ++j, ++n) {
+        if (!mbar_wait(&s_full[x], n & 1, abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
+        float s[4][32];
+        {
+          uint32_t v[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(lane_base + col_s + 32 * q, v[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            reg_fence32(v[q]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[q][i] = __uint_as_float(v[q][i]);
+          }
+        }
+        const int keep = it.len - j * BN;
+        if (keep < BN) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i >= keep) s[q][i] = -INFINITY;
+        }
+        const float top = rowmax128(s);
+        // the reference: the first tile's maximum, then only where a maximum passes it by far
+        const bool lift = j == 0 || (top - m) * c > TAU;
+        const float was = mc;
+        if (lift) {
+          m = top > -INFINITY ? top : 0.f;
+          mc = m * c;
+        }
+        float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = ffma2(make_float2(s[q][2 * i], s[q][2 * i + 1]), make_float2(c, c), make_float2(-mc, -mc));
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            ls = fadd2(ls, e);
+            __nv_bfloat162 t = __floats2bfloat162_rn(e.x, e.y);
+            pk[i] = *reinterpret_cast<uint32_t*>(&t);
+          }
+          tmem_st16(lane_base + col_s + 16 * q, pk);
+        }
+        if (j > 0 && __any_sync(0xffffffffu, lift)) {
+          const float f = lift ? ex2_approx(was - mc) : 1.f;
+          if (!mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t ov[32];
+            tmem_ld32(lane_base + col_o + 32 * q, ov);
+            tmem_ld_wait();
+            reg_fence32(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+            tmem_st32(lane_base + col_o + 32 * q, ov);
+          }
+          l *= f;
+        }
+        l += ls.x + ls.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      const int h = it.hk * G + g;
+      if (valid && p.lse)
+        p.lse[((long long)it.b * p.Hq + h) * p.Nq + row] =
+            it.nt > 0 ? (mc + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      __nv_bfloat16* dst = valid ? at(p.o, it.b, h, row) : nullptr;
+      if (it.nt == 0) {
+        if (valid)
+          for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (!mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+      tc_fence_after();
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32], pk[16];
+        tmem_ld32(lane_base + col_o + 32 * q, v);
+        tmem_ld_wait();
+        reg_fence32(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+          pk[i] = *reinterpret_cast<uint32_t*>(&t);
+        }
+        if (valid && a.o32) {
+          st_global_v8(dst + 32 * q, pk);
+          st_global_v8(dst + 32 * q + 16, pk + 8);
+        } else if (valid) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(dst + 32 * q)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
     }
   }
-  for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
-  __nv_bfloat16* out = at(p.o, b, h, n) + lane * C;
-  for (int i = 0; i < C; ++i) out[i] = __float2bfloat16(len > 0 ? o[i] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[row] = len > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
 }  // namespace
 
+bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads) {
+  m->own_b = t.b != 0;
+  m->own_h = t.h != 0;
+  const uint64_t dims[3] = {(uint64_t)N, m->own_h ? (uint64_t)H : 1, m->own_b ? (uint64_t)B : 1};
+  const int64_t strides[3] = {t.n, t.h, t.b};
+  return make_heads_map(&m->map, t.p, d, dims, strides, (uint32_t)rows, (uint32_t)heads);
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
+}
+
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {
-  const long long rows = (long long)p.B * p.Hq * p.Nq;
-  const unsigned grid = (unsigned)((rows + WARPS - 1) / WARPS);
-  if (p.d == 128) cross_fwd_kernel<128><<<grid, WARPS * 32, 0, st>>>(p);
-  else cross_fwd_kernel<64><<<grid, WARPS * 32, 0, st>>>(p);
+  Params a;
+  a.p = p;
+  const int G = p.Hq / p.Hkv;
+  a.heads = p.Nq <= 64 && p.q.h != 0 ? (128 / p.Nq < G ? 128 / p.Nq : G) : 1;
+  a.per_head = (p.Nq + BM - 1) / BM;
+  a.tiles = a.heads > 1 ? (G + a.heads - 1) / a.heads : G * a.per_head;
+  a.pairs = (a.tiles + 1) / 2;
+  const long long items = (long long)p.B * p.Hkv * a.pairs;
+  a.items = (int)items;
+  a.box = a.heads > 1 ? a.heads * p.Nq : BM;
+  a.o32 = (reinterpret_cast<uintptr_t>(p.o.p) & 31) == 0 && ((p.o.b | p.o.h | p.o.n) & 15) == 0;
+  if (!heads_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, a.heads > 1 ? p.Nq : BM, a.heads)) return cudaErrorInvalidValue;
+  if (p.Nk > 0) {
+    if (!heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, BN, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, BN, 1))
+      return cudaErrorInvalidValue;
+  } else {
+    a.k = a.v = a.q;       // never loaded from
+  }
+  const int sms = sm_count(), grid = a.items < sms ? a.items : sms;
+  const int smem = p.d == 128 ? Smem<128>::BYTES : Smem<64>::BYTES;
+  auto k = p.d == 128 ? cross_fwd_kernel<128> : cross_fwd_kernel<64>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k<<<grid, NTHREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
 

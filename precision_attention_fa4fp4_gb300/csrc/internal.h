@@ -8,6 +8,11 @@
 
 namespace fa4 {
 
+// Tiled map of a strided bf16 [B][H][N][d] tensor: boxes of 64 channels (128-byte
+// swizzle) x `rows` x `heads`; dims, strides (elements): N, H, B.
+bool make_heads_map(CUtensorMap* m, const void* base, int d, const uint64_t (&dims)[3], const int64_t (&strides)[3],
+                    uint32_t rows, uint32_t heads);
+
 struct Thresh { float v[7]; };
 
 // Round N up to the padded key length of the along-N layouts.
