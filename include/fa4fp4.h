@@ -513,7 +513,9 @@ FA4FP4_API fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const 
  * Nk is taken as the nearer end and the next fa4fp4_sync_status returns
  * FA4FP4_ERR_DEVICE_INDEX.
  *   s = softmax_scale * q.k, o = softmax(s) v, lse = ln sum e^s (nullable)
- * o: bf16; lse: f32 [B][Hq][Nq], dense.  Without a key o = 0 and lse = -inf.
+ * o: bf16; lse: f32 [B][Hq][Nq], dense.  Without a key o = 0 and lse = -inf.  The
+ * rows of q, k and v do not overlap (stride_n >= d; FA4FP4_ERR_UNSUPPORTED); heads
+ * and sequences may be broadcast.
  * Products are exact, sums FP32; P is rounded to bf16 (half a step: 2^-9) for the
  * product with V, its sum is taken before that.  Nq and Nk may be 0 (k and v are
  * then not read; no query is an empty problem). */

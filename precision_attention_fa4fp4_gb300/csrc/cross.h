@@ -28,6 +28,9 @@ struct HeadsMap {
 bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads);
 int sm_count();
 
+// Up to CROSS_TOKEN_ROWS query rows of a kv head (Hq / Hkv * Nq).
+constexpr int CROSS_TOKEN_ROWS = 32;
+cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st);
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st);
 size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st);

@@ -92,6 +92,11 @@ void set_rotation(RopeParams* p, const fa4fp4_norm* norm, const fa4fp4_rotation*
     }
 }
 
+// Cross attention reads rows by TMA boxes: they may not lie on each other.
+fa4fp4_status check_rows(const Strided& t, int N, int d) {
+  return N > 1 && t.n < d ? FA4FP4_ERR_UNSUPPORTED : FA4FP4_OK;
+}
+
 float softmax_scale_of(float s, int d) { return s > 0.f ? s : (float)(1.0 / std::sqrt((double)d)); }
 
 fa4fp4_status check_cross(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
@@ -212,6 +217,9 @@ fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
   if (!aligned(kv_lens, 4) || !aligned(lse, 16)) return FA4FP4_ERR_ALIGNMENT;
   p.q = strided(q, B, Hq, Nq);
   p.o = strided(o, B, Hq, Nq);
+  if ((s = check_rows(p.q, Nq, d)) != FA4FP4_OK || (s = check_rows(p.k, Nk, d)) != FA4FP4_OK ||
+      (s = check_rows(p.v, Nk, d)) != FA4FP4_OK)
+    return s;
   p.lse = lse;
   p.lens = kv_lens;
   p.err = device_error_word();
@@ -219,7 +227,8 @@ fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.d = d;
   p.scale = softmax_scale_of(softmax_scale, d);
   p.c = (float)((double)p.scale * 1.4426950408889634);
-  return status_of(launch_cross_fwd(p, static_cast<cudaStream_t>(stream)));
+  const bool few = (long long)(Hq / Hkv) * Nq <= CROSS_TOKEN_ROWS;
+  return status_of((few ? launch_cross_token : launch_cross_fwd)(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fa4bf16_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
@@ -247,6 +256,7 @@ fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
     if ((s = check_heads(dq, B, Hq, Nq, 2, true)) != FA4FP4_OK) return s;
     p.dq = strided(dq, B, Hq, Nq);
     if (!lse) return FA4FP4_ERR_INVALID_ARG;
+    if ((s = check_rows(p.q, Nq, d)) != FA4FP4_OK || (s = check_rows(p.dout, Nq, d)) != FA4FP4_OK) return s;
   }
   if (Nk > 0) {
     const fa4fp4_heads* in[] = {k, v, dk, dv};
@@ -255,6 +265,7 @@ fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
       if ((s = check_heads(in[i], B, Hkv, Nk, 2, i >= 2)) != FA4FP4_OK) return s;
       *to[i] = strided(in[i], B, Hkv, Nk);
     }
+    if ((s = check_rows(p.k, Nk, d)) != FA4FP4_OK || (s = check_rows(p.v, Nk, d)) != FA4FP4_OK) return s;
   }
   if (!aligned(kv_lens, 4) || !aligned(lse, 16)) return FA4FP4_ERR_ALIGNMENT;
   const size_t need = cross_bwd_workspace(B, Hq, Hkv, Nq, Nk, d);

@@ -1,0 +1,359 @@
+// cross_token.cu -- cross attention of few query rows (up to 32 per kv head: the
+// new tokens of a decoding step, all query heads of a kv head together).
+//
+// Bound by reading K and V once.  A CTA (4 warps) works on one (sequence, kv head)
+// or on a part of its keys: a cluster of up to 16 CTAs shares them where there are
+// fewer heads than multiprocessors.  Blocks of keys go round the cluster's warps;
+// each warp has a ring of its own in shared memory, filled by TMA boxes, so no warp
+// waits for another.  The rows are the m16n8k16 products' A operand, held in
+// registers (mma.sync: 16 rows have no use for a 128-row tensor memory tile, and the
+// bytes of K and V, not the products, bound this kernel); a warp keeps its running
+// maximum, sum and O.  The warps' results are joined in shared memory, the
+// cluster's through distributed shared memory, each CTA taking a share of the
+// outputs.
+#include <cstring>
+#include <cuda_bf16.h>
+#include "common.cuh"
+#include "cross.cuh"
+#include "internal.h"
+
+namespace fa4 {
+namespace {
+
+constexpr int WARPS = 4, STAGES = 3;
+
+struct Params {
+  CrossParams p;
+  HeadsMap k, v;
+  int splits;                    // CTAs of a cluster
+};
+
+// 8 KB of K and V a block: 16 keys at d = 128, 32 at d = 64.
+template <int D>
+constexpr int KEYS = 2048 / D;
+
+FA4_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+FA4_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+// A float in the shared memory of CTA `rank` of the cluster, at this CTA's place `x`.
+FA4_DEV float peer_float(const float* x, uint32_t rank) {
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+               : "=f"(v)
+               : "r"(smem_u32(x)), "r"(rank)
+               : "memory");
+  return v;
+}
+
+FA4_DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+FA4_DEV void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+FA4_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+FA4_DEV uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&t);
+}
+
+template <int D, int MT>
+struct Smem {
+  static constexpr int CHUNK = KEYS<D> * 128;              // [keys][64 channels], 128-byte swizzle
+  static constexpr int TILE = (D / 64) * CHUNK;            // 4 KB
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int RING = WARPS * STAGES * STAGE;      // 96 KB
+  // after the loop the rings' place holds the warps' (m, l) and O, then the CTA's
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int WARP_F = ROWS * (D + 2);            // floats of one warp: O [ROWS][D], m, l
+  static constexpr int OFF_CTA = WARPS * WARP_F * 4;
+  static_assert(OFF_CTA + WARP_F * 4 <= RING, "join fits the rings");
+  static constexpr int OFF_BAR = RING;
+  static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8 + 16 + 1024;
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_constant__ Params a) {
+  using L = Smem<D, MT>;
+  constexpr int NK = KEYS<D>;
+  const CrossParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + WARPS * STAGES);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = a.splits > 1 ? (int)cluster_rank() : 0;
+  const int bh = blockIdx.x / a.splits, b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int G = p.Hq / p.Hkv, R = G * p.Nq;
+  uint64_t* full = bars + warp * STAGES;
+  uint8_t* ring = smem + warp * STAGES * L::STAGE;
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int len = key_count(p, b, threadIdx.x == 0 && rank == 0);
+  const int blocks = (len + NK - 1) / NK;
+  // this warp's blocks: me, me + step, ...
+  const int me = rank * WARPS + warp, step = a.splits * WARPS;
+  const int mine = me < blocks ? (blocks - me + step - 1) / step : 0;
+  auto load = [&](int i) {
+    const int st = i % STAGES, key = (me + i * step) * NK;
+    mbar_arrive_expect_tx(&full[st], L::STAGE);
+    for (int c = 0; c < D / 64; ++c) {
+      tma_heads(ring + st * L::STAGE + c * L::CHUNK, a.k, &full[st], 64 * c, key, hk, b);
+      tma_heads(ring + st * L::STAGE + L::TILE + c * L::CHUNK, a.v, &full[st], 64 * c, key, hk, b);
+    }
+  };
+  if (lane == 0)
+    for (int i = 0; i < min(mine, STAGES); ++i) load(i);
+
+  // the rows as A fragments: rows lane / 4 and + 8 of each 16, channels 2 (lane % 4) and + 8 of each 16
+  uint32_t qf[MT][D / 16][4];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = 16 * t + lane / 4 + 8 * half;
+      const __nv_bfloat16* q = r < R ? at(p.q, b, hk * G + r / p.Nq, r % p.Nq) + 2 * (lane % 4) : nullptr;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[t][k][half] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+        qf[t][k][2 + half] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+      }
+    }
+  float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+  }
+  // ldmatrix rows of this lane: K: matrices (keys 0-7, channels 0-7), (keys 0-7, 8-15), (keys 8-15, 0-7), (8-15, 8-15)
+  const int krow = (lane & 7) + ((lane & 16) >> 1), kcol = (lane >> 3) & 1;
+  // V, transposed: (keys 0-7, channels 0-7), (keys 8-15, 0-7), (keys 0-7, 8-15), (keys 8-15, 8-15)
+  const int vrow = lane & 15, vcol = lane >> 4;
+
+  for (int i = 0; i < mine; ++i) {
+    const int st = i % STAGES;
+    if (!mbar_wait(&full[st], (i / STAGES) & 1, abort_flag, p.err)) break;
+    uint8_t* kt = ring + st * L::STAGE;
+    uint8_t* vt = kt + L::TILE;
+    const int keep = len - (me + i * step) * NK;
+    if (keep < NK && len < p.Nk) {
+      // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not
+      for (int x = keep * 8 + lane; x < NK * 8; x += 32)
+        for (int c = 0; c < D / 64; ++c) reinterpret_cast<uint4*>(vt + c * L::CHUNK)[x] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    const uint32_t ks = smem_u32(kt), vs = smem_u32(vt);
+    float s[MT][NK / 8][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int n = 0; n < NK / 8; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < NK / 16; ++n) {
+        const int row = 16 * n + krow;
+        uint32_t kf[4];
+        ldsm4(ks + (k / 4) * L::CHUNK + row * 128 + ((2 * (k % 4) + kcol) ^ (row & 7)) * 16, kf);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          mma_bf16(s[t][2 * n], qf[t][k], kf[0], kf[1]);
+          mma_bf16(s[t][2 * n + 1], qf[t][k], kf[2], kf[3]);
+        }
+      }
+    uint32_t pf[MT][NK / 16][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if (keep < NK) {
+#pragma unroll
+        for (int n = 0; n < NK / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * n + 2 * (lane % 4) + (e & 1) >= keep) s[t][n][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NK / 8; ++n) top = fmaxf(top, fmaxf(s[t][n][2 * half], s[t][n][2 * half + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float now = fmaxf(m[t][half], top * p.c);
+        const float ref = now > -INFINITY ? now : 0.f;
+        if (__any_sync(0xffffffffu, now != m[t][half])) {
+          const float f = ex2_approx(m[t][half] - ref);
+          l[t][half] *= f;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[t][n][2 * half] *= f;
+            o[t][n][2 * half + 1] *= f;
+          }
+        }
+        m[t][half] = now;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NK / 8; ++n) {
+          const float e0 = ex2_approx(fmaf(s[t][n][2 * half], p.c, -ref));
+          const float e1 = ex2_approx(fmaf(s[t][n][2 * half + 1], p.c, -ref));
+          sum += e0 + e1;
+          pf[t][n / 2][(n & 1) * 2 + half] = pack2(e0, e1);
+        }
+        l[t][half] += sum;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NK / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        const int row = 16 * k + vrow;
+        uint32_t vf[4];
+        ldsm4_t(vs + (n / 4) * L::CHUNK + row * 128 + ((2 * (n % 4) + vcol) ^ (row & 7)) * 16, vf);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          mma_bf16(o[t][2 * n], pf[t][k], vf[0], vf[1]);
+          mma_bf16(o[t][2 * n + 1], pf[t][k], vf[2], vf[3]);
+        }
+      }
+    __syncwarp();
+    if (i + STAGES < mine && lane == 0) load(i + STAGES);
+  }
+  if (*abort_flag) {                           // (a wait ran out: let the loads in flight land)
+    volatile int no_abort = 0;
+    for (int s = 0; s < min(mine, STAGES); ++s)
+      for (int ph = 0; ph < 2; ++ph) mbar_wait_ns(&full[s], ph, &no_abort, p.err, 100000000ull);
+  }
+
+  // join: every warp leaves O [ROWS][D], m and l where the rings were
+  __syncthreads();
+  float* mem = reinterpret_cast<float*>(smem);
+  float* my = mem + warp * L::WARP_F;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = 16 * t + lane / 4 + 8 * half;
+      l[t][half] += __shfl_xor_sync(0xffffffffu, l[t][half], 1);
+      l[t][half] += __shfl_xor_sync(0xffffffffu, l[t][half], 2);
+      if (lane % 4 == 0) {
+        my[L::ROWS * D + r] = m[t][half];
+        my[L::ROWS * D + L::ROWS + r] = l[t][half];
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(my + r * D + 8 * n + 2 * (lane % 4)) =
+            make_float2(o[t][n][2 * half], o[t][n][2 * half + 1]);
+    }
+  __syncthreads();
+  // this CTA's O (not divided), m and l
+  float* cta = a.splits > 1 ? reinterpret_cast<float*>(smem + L::OFF_CTA) : nullptr;
+  auto store = [&](int r, int i, float v0, float v1, float top, float sum) {
+    if (r >= R) return;
+    const int h = hk * G + r / p.Nq, n = r % p.Nq;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint32_t*>(at(p.o, b, h, n) + i) = pack2(v0 * inv, v1 * inv);
+    if (i == 0 && p.lse)
+      p.lse[((long long)b * p.Hq + h) * p.Nq + n] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  };
+  for (int x = threadIdx.x; x < L::ROWS * (D / 2); x += WARPS * 32) {
+    const int r = x / (D / 2), i = x % (D / 2) * 2;
+    if (r >= R) break;
+    float top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, mem[w * L::WARP_F + L::ROWS * D + r]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float* from = mem + w * L::WARP_F;
+      const float f = top > -INFINITY ? ex2_approx(from[L::ROWS * D + r] - top) : 0.f;
+      const float2 v = *reinterpret_cast<const float2*>(from + r * D + i);
+      sum = fmaf(from[L::ROWS * D + L::ROWS + r], f, sum);
+      v0 = fmaf(v.x, f, v0);
+      v1 = fmaf(v.y, f, v1);
+    }
+    if (!cta) {
+      store(r, i, v0, v1, top, sum);
+    } else {
+      *reinterpret_cast<float2*>(cta + r * D + i) = make_float2(v0, v1);
+      if (i == 0) {
+        cta[L::ROWS * D + r] = top;
+        cta[L::ROWS * D + L::ROWS + r] = sum;
+      }
+    }
+  }
+  if (!cta) return;
+  cluster_sync();
+  // the cluster's: pairs of outputs in turn
+  for (int x = rank * WARPS * 32 + threadIdx.x; x < R * (D / 2); x += a.splits * WARPS * 32) {
+    const int r = x / (D / 2), i = x % (D / 2) * 2;
+    float top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
+    for (int c = 0; c < a.splits; ++c) top = fmaxf(top, peer_float(cta + L::ROWS * D + r, c));
+    for (int c = 0; c < a.splits; ++c) {
+      const float f = top > -INFINITY ? ex2_approx(peer_float(cta + L::ROWS * D + r, c) - top) : 0.f;
+      sum = fmaf(peer_float(cta + L::ROWS * D + L::ROWS + r, c), f, sum);
+      v0 = fmaf(peer_float(cta + r * D + i, c), f, v0);
+      v1 = fmaf(peer_float(cta + r * D + i + 1, c), f, v1);
+    }
+    store(r, i, v0, v1, top, sum);
+  }
+  cluster_sync();          // no CTA leaves while another reads its memory
+}
+
+}  // namespace
+
+cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st) {
+  Params a;
+  a.p = p;
+  const int nk = 2048 / p.d;
+  if (p.Nk > 0) {
+    if (!heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, nk, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, nk, 1))
+      return cudaErrorInvalidValue;
+  } else {
+    memset(&a.k, 0, sizeof(a.k));          // never loaded from
+    a.v = a.k;
+  }
+  // a cluster shares a head's keys while there are more multiprocessors than CTAs
+  // and at least two blocks for each of its warps
+  const long long heads = (long long)p.B * p.Hkv;
+  const int sms = sm_count();
+  a.splits = 1;
+  while (a.splits < 16 && heads * a.splits * 2 <= 2LL * sms && p.Nk >= a.splits * 2 * WARPS * 2 * nk) a.splits *= 2;
+  const bool two = p.Hq / p.Hkv * p.Nq > 16;
+  auto k = p.d == 128 ? (two ? cross_token_kernel<128, 2> : cross_token_kernel<128, 1>)
+                      : (two ? cross_token_kernel<64, 2> : cross_token_kernel<64, 1>);
+  const int smem = p.d == 128 ? (two ? Smem<128, 2>::BYTES : Smem<128, 1>::BYTES)
+                              : (two ? Smem<64, 2>::BYTES : Smem<64, 1>::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && a.splits > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(heads * a.splits));
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+}  // namespace fa4
