@@ -100,9 +100,13 @@ def cross_bwd(q, k, v, o, dout, lse, lens=None, scale=0.0):
     p = torch.exp((Q @ K.transpose(2, 3) * scale - L).masked_fill(~use, -float("inf")))
     ep = p * ((Q.abs() @ K.abs().transpose(2, 3) * scale) * (d * 2.0 ** -23) + 2.0 ** -19 * (1 + L.abs().nan_to_num(posinf=0.0)))
     dp, D = G @ V.transpose(2, 3), (G * O).sum(-1, keepdim=True)
+    # below 2^-126 the native exponential gives 0, and so may the rounding of dS: P is off by 2^-126 more, dS by that
+    # and by what the P makes of it (d S = P (dP - D))
+    least = use * 2.0 ** -126
+    ep = ep + least
     edp = ((G.abs() @ V.abs().transpose(2, 3)) + (G * O).abs().sum(-1, keepdim=True)) * (d * 2.0 ** -23)
     ds = p * (dp - D)
-    eds = U * ds.abs() + (1 + U) * (ep * (dp - D).abs() + p * edp)
+    eds = U * ds.abs() + (1 + U) * (ep * (dp - D).abs() + p * edp) + least
     few = 1 + 2.0 ** -10        # sums in FP32
     out = []
     for x, e, y in ((ds, eds, K), (ds.transpose(2, 3), eds.transpose(2, 3), Q)):
