@@ -108,6 +108,7 @@ fa4fp4_status check_cross(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   if (Nq > (1 << 30) || Nk > (1 << 30) || (long long)B * Hq * Nq > (1LL << 31) - 1 ||
       (long long)B * Hkv * Nk > (1LL << 31) - 1 || (long long)B * Hq > (1LL << 24))
     return FA4FP4_ERR_UNSUPPORTED;
+  if ((long long)B * Hq * ((Nq + 127) / 128) > (1LL << 36) / ((Nk + 127) / 128 + 1)) return FA4FP4_ERR_UNSUPPORTED;
   return FA4FP4_OK;
 }
 

@@ -16,12 +16,14 @@
 // cross_dq_kernel: persistent, a query tile at a time.  Warps 0-7: a thread per
 //   row and half of the keys: P from S while dP runs, dS as bf16 into tensor memory
 //   (the A operand of dQ).  S of the next key tile runs as soon as S has been read.
-//   D is summed by the same threads from dO and o, and kept in the workspace.
+//   D is summed by the same threads from o and the dO tile, and kept in the
+//   workspace; an item's o is on its way while the item before ends.  Two warps issue
+//   the products: S; dP and dQ.
 // cross_dkv_kernel: persistent over the steps (key tile, query tile), cut into
 //   equal ranges.  Rows are keys: P^T and dS^T go over S^T and dP^T as A operands of
-//   dV and dK, which are summed in tensor memory (512 columns in all).  The
-//   products' order dV, next S^T, dK, next dP^T leaves each half of the element-wise
-//   work two products to hide behind.  A range that starts or ends inside a key
+//   dV and dK, which are summed in tensor memory (512 columns in all).  Two warps
+//   issue the products, S^T and dV the one, dP^T and dK the other (one warp was the
+//   bound: a product takes 512 cycles, its waits, instructions and commits 700).  A range that starts or ends inside a key
 //   tile leaves FP32 partials in the workspace.
 // cross_join_kernel: sums those in the ranges' order; zeros for keys behind kv_lens.
 #include <cuda_bf16.h>
@@ -34,16 +36,16 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NTHREADS = 384;
-constexpr int W_PROD = 8, W_MMA = 9, W_STAT = 10;
+constexpr int W_PROD = 8, W_MMA = 9, W_MMA_B = 10, W_STAT = 11;
 constexpr int REG_SOFT = 208, REG_MISC = 88;   // 2 x 208 + 88 = 504 of 512
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float L2E = 1.4426950408889634f;
-constexpr int CH = 128 * 128;                  // [128 rows][64 channels] of bf16
 
 struct Params {
   CrossParams p;
   HeadsMap q, dout, k, v;
-  int tiles, per_head, heads, box;             // query tiles of a kv head, as in the forward
+  int tiles, heads, box;                       // query tiles of a kv head, as in the forward
+  Divisor per_head, per_kv, hkv, nq;           // (per_kv: tiles)
   int key_tiles;                               // of Nk
   int items;                                   // query tiles in all
   int ctas;                                    // of the dK, dV kernel
@@ -55,11 +57,11 @@ struct Params {
 // Row r of a query tile: query head within the group (G: none) and position.
 FA4_DEV void tile_row(const Params& a, int tile, int r, int G, int& g, int& n) {
   if (a.heads > 1) {
-    g = r < a.heads * a.p.Nq ? min(G, tile * a.heads + r / a.p.Nq) : G;
-    n = r % a.p.Nq;
+    divide(r, a.nq, g, n);
+    g = r < a.heads * a.p.Nq ? min(G, tile * a.heads + g) : G;
   } else {
-    g = tile / a.per_head;
-    n = tile % a.per_head * BM + r;
+    divide(tile, a.per_head, g, n);
+    n = n * BM + r;
     if (n >= a.p.Nq) g = G;
   }
 }
@@ -84,24 +86,6 @@ FA4_DEV void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float f, bool 
   }
 }
 
-// A K-major product of 128 x 128 over D channels, both operands in shared memory.
-template <int D>
-FA4_DEV void product_kk(uint32_t acc, uint32_t sa, uint32_t sb, uint32_t idesc) {
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint32_t off = (k / 4) * CH + (k % 4) * 32;
-    mma_f16(acc, make_sdesc(sa + off, 16, 1024, SW_128B), make_sdesc(sb + off, 16, 1024, SW_128B), idesc, k > 0);
-  }
-}
-// ... over 128 rows of B (MN-major), A packed in tensor memory: the first 64
-// of them in columns [a0, a0 + 32), the others in [a1, a1 + 32).
-FA4_DEV void product_tmem(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t idesc, bool add) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    mma_f16_tmem_a(acc, (k < 4 ? a0 : a1) + 8 * (k % 4), make_sdesc(sb + k * 16 * 128, CH, 1024, SW_128B), idesc,
-                   add || k > 0);
-}
-
 // ---------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------
@@ -110,11 +94,11 @@ struct SmemQ {
   static constexpr int TILE = (D / 64) * CH;
   static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0, OFF_KV = QS * TILE;
-  static constexpr int OFF_DEL = OFF_KV + KS * TILE;        // float [2][128]
-  static constexpr int OFF_BAR = OFF_DEL + 1024;
+  static constexpr int OFF_DEL = OFF_KV + KS * TILE;        // [2 items][2 halves][128]: shares of D
+  static constexpr int OFF_BAR = OFF_DEL + 2 * 1024;
   static constexpr int NBAR = 2 * QS + 2 * KS + 6;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -126,10 +110,9 @@ struct WalkQ {
   FA4_DEV WalkQ() : i(blockIdx.x) {}
   FA4_DEV bool at(const Params& a, ItemQ& it, bool report) {
     if (i >= a.items) return false;
-    const int bh = i / a.tiles;
-    it.b = bh / a.p.Hkv;
-    it.hk = bh % a.p.Hkv;
-    it.tile = i % a.tiles;
+    int bh;
+    divide(i, a.per_kv, bh, it.tile);
+    divide(bh, a.hkv, it.b, it.hk);
     if (it.b != b) {
       b = it.b;
       len = key_count(a.p, b, report);
@@ -154,9 +137,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   constexpr int QS = L::QS, KS = L::KS;
   constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DS = 384;
   const CrossParams& p = a.p;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* del_half = reinterpret_cast<float*>(smem + L::OFF_DEL);
+  // (no room to align it by hand: nothing else is in shared memory, so it begins on its alignment)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023) {
+    atomicOr(p.err, FA4_DEVERR_TIMEOUT);
+    return;
+  }
+  float* shares = reinterpret_cast<float*>(smem + L::OFF_DEL);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_empty = q_full + QS;
   uint64_t* kv_full = q_empty + QS;
@@ -172,14 +159,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
+    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 9); }
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 8);
     mbar_init(dq_done, 1);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -203,7 +190,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           const int st = qn % QS;
           if (qn >= QS && !mbar_wait(&q_empty[st], (qn / QS - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(&q_full[st], a.box * 2 * D);
-          const int h = it.hk * G + it.tile / a.per_head * a.heads, n = it.tile % a.per_head * BM;
+          int g, n;
+          divide(it.tile, a.per_head, g, n);
+          const int h = it.hk * G + g * a.heads;
+          n *= BM;
           for (int c = 0; c < D / 64; ++c)
             tma_heads(smem + L::OFF_Q + st * L::TILE + c * CH, m, &q_full[st], 64 * c, n, h, it.b);
           ++qn;
@@ -233,94 +223,81 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       }
       __syncwarp();
     } else if (warp == W_MMA) {
+      // S of every step, as soon as the one before has been read
+      const bool leader = elect_one();
+      const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
+      WalkQ w;
+      ItemQ it;
+      int kv = 0, q = 0, n = 0;
+      bool ok = true;
+      for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
+        const uint32_t sq = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
+        ok = mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
+        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += 2) {
+          ok = mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err) &&
+               (n == 0 || mbar_wait(s_free, (n - 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+          // rows of K behind the sequence's keys may be anything: dS is 0 there, and 0 x NaN is not
+          uint8_t* k = smem + L::OFF_KV + kv % KS * L::TILE;
+          if (it.len - j * BN < BN && it.len < p.Nk) clear_rows<D>(k, it.len - j * BN, lane);
+          tc_fence_after();
+          if (leader) {
+            product_rows<D>(tbase + COL_S, sq, smem_u32(k), idesc_s);
+            mma_commit(s_full);
+            if (j == it.nt - 1) mma_commit(&q_empty[q % QS]);
+          }
+          __syncwarp();
+        }
+      }
+      if (leader) mma_commit(mma_done);
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait(mma_done, 0, &no_abort, p.err);
+      __syncwarp();
+    } else if (warp == W_MMA_B) {
+      // dP of every step; dQ of the step before it first
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_q = idesc_f16(BM, D, true, false, true);
-      struct Step {
-        ItemQ it;
-        int j, kv, q;                    // key tile; ring positions of its K, and of the item's Q
-      };
       WalkQ w;
-      int qn = 0, kn = 0, done = 0;      // done: steps whose dQ is issued
-      auto first = [&](Step& s) -> bool {
-        if (!w.with_keys(a, s.it, false)) return false;
-        s.j = 0;
-        s.kv = kn;
-        s.q = qn;
+      ItemQ it;
+      int kv = 0, q = 1, n = 0;
+      bool ok = true, add = false;
+      // dQ += dS K of step n - 1, whose K is at ring position k; last: of its item
+      auto issue_dq = [&](int k, bool last) -> bool {
+        if (!mbar_wait(ds_full, (n - 1) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+        const uint32_t sk = smem_u32(smem + L::OFF_KV + k % KS * L::TILE);
+        if (leader) {
+          product_cols(tbase + COL_DQ, tbase + COL_DS, tbase + COL_DS + 32, sk, idesc_q, add);
+          mma_commit(&kv_empty[k % KS]);
+          if (last) mma_commit(dq_done);
+        }
+        __syncwarp();
+        add = !last;
         return true;
       };
-      auto after = [&](const Step& s, Step& n) -> bool {
-        kn = s.kv + 2;
-        if (s.j + 1 < s.it.nt) {
-          n = s;
-          ++n.j;
-          n.kv = kn;
-          return true;
-        }
-        qn = s.q + 2;
-        w.next();
-        return first(n);
-      };
-      auto tile_kv = [&](int seq) { return smem + L::OFF_KV + seq % KS * L::TILE; };
-      auto issue_s = [&](const Step& s) -> bool {
-        if (s.j == 0 && !mbar_wait(&q_full[s.q % QS], (s.q / QS) & 1, abort_flag, p.err)) return false;
-        if (!mbar_wait(&kv_full[s.kv % KS], (s.kv / KS) & 1, abort_flag, p.err)) return false;
-        // rows of K behind the sequence's keys may be anything: dS is 0 there, and 0 x NaN is not
-        const int keep = s.it.len - s.j * BN;
-        uint8_t* k = tile_kv(s.kv);
-        if (keep < BN && s.it.len < p.Nk) {
-          for (int c = 0; c < D / 64; ++c)
-            for (int i = keep * 8 + lane; i < BN * 8; i += 32)
-              reinterpret_cast<uint4*>(k + c * CH)[i] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
+      for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
+        const uint32_t sdo = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
+        for (int j = 0; ok && j < it.nt; ++j, kv += 2) {
+          const int v = kv + 1;
+          if (n > 0) ok = issue_dq(kv - 2, j == 0);
+          if (j == 0) ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
+          ok = ok && mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sv = smem_u32(smem + L::OFF_KV + v % KS * L::TILE);
+          if (leader) {
+            product_rows<D>(tbase + COL_DP, sdo, sv, idesc_s);
+            mma_commit(dp_full);
+            mma_commit(&kv_empty[v % KS]);
+            if (j == it.nt - 1) mma_commit(&q_empty[q % QS]);
+          }
           __syncwarp();
+          ++n;
         }
-        tc_fence_after();
-        if (leader) {
-          product_kk<D>(tbase + COL_S, smem_u32(smem + L::OFF_Q + s.q % QS * L::TILE), smem_u32(k), idesc_s);
-          mma_commit(s_full);
-          if (s.j == s.it.nt - 1) mma_commit(&q_empty[s.q % QS]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_dp = [&](const Step& s) -> bool {
-        const int q = s.q + 1, v = s.kv + 1;
-        if (s.j == 0 && !mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err)) return false;
-        if (!mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err)) return false;
-        tc_fence_after();
-        if (leader) {
-          product_kk<D>(tbase + COL_DP, smem_u32(smem + L::OFF_Q + q % QS * L::TILE), smem_u32(tile_kv(v)), idesc_s);
-          mma_commit(dp_full);
-          mma_commit(&kv_empty[v % KS]);
-          if (s.j == s.it.nt - 1) mma_commit(&q_empty[q % QS]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_dq = [&](const Step& s) -> bool {
-        if (!mbar_wait(ds_full, done & 1, abort_flag, p.err)) return false;
-        tc_fence_after();
-        if (leader) {
-          product_tmem(tbase + COL_DQ, tbase + COL_DS, tbase + COL_DS + 32, smem_u32(tile_kv(s.kv)), idesc_q, s.j > 0);
-          mma_commit(&kv_empty[s.kv % KS]);
-          if (s.j == s.it.nt - 1) mma_commit(dq_done);
-        }
-        __syncwarp();
-        return true;
-      };
-      Step cur, nxt;
-      bool more = first(cur);
-      bool ok = !more || (issue_s(cur) && issue_dp(cur));
-      while (ok && more) {
-        const bool then = after(cur, nxt);
-        if (then) ok = mbar_wait(s_free, done & 1, abort_flag, p.err) && issue_s(nxt);
-        ok = ok && issue_dq(cur);
-        ++done;
-        if (then) ok = ok && issue_dp(nxt);
-        more = then;
-        cur = nxt;
       }
+      if (ok && n > 0) issue_dq(kv - 2, true);
       if (leader) mma_commit(mma_done);
       __syncwarp();
       volatile int no_abort = 0;
@@ -332,41 +309,66 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     const int half = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
-    int n = 0, items = 0;
+    int n = 0, items = 0;                  // key tiles, items with keys so far
     bool ok = true;
     WalkQ w;
     ItemQ it;
-    // (a warp whose wait ran out still meets the others at the barriers of later items)
-    for (; w.at(a, it, false); w.next()) {
-      int g, row;
-      tile_row(a, it.tile, r, G, g, row);
-      const bool valid = g < G;
-      const int h = it.hk * G + (valid ? g : 0);
-      const long long flat = ((long long)it.b * p.Hq + h) * p.Nq + row;
-      // this half's share of D, both halves' sum
-      float del = 0.f, lse = INFINITY;
+    // an item's row, and this thread's half of its o: on its way while the item before ends
+    bool valid = false;
+    int h = 0, row = 0;
+    float lse = INFINITY;
+    uint4 u[D / 16];
+    auto fetch = [&](const ItemQ& x) {
+      int g;
+      tile_row(a, x.tile, r, G, g, row);
+      valid = g < G;
+      h = x.hk * G + g;
+      lse = INFINITY;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) u[i] = make_uint4(0, 0, 0, 0);
       if (valid) {
-        const __nv_bfloat16 *x = at(p.dout, it.b, h, row) + half * (D / 2), *y = at(p.o, it.b, h, row) + half * (D / 2);
+        const uint4* o = reinterpret_cast<const uint4*>(at(p.o, x.b, h, row) + half * (D / 2));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 u = reinterpret_cast<const uint4*>(x)[i], v = reinterpret_cast<const uint4*>(y)[i];
-          const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < D / 16; ++i) u[i] = o[i];
+        lse = p.lse[((long long)x.b * p.Hq + h) * p.Nq + row];
+      }
+    };
+    bool more = w.at(a, it, false);
+    if (more) fetch(it);
+    while (more) {
+      float del = 0.f, z = INFINITY;       // (a row without keys: P = 2^-inf = 0)
+      if (lse > -INFINITY) z = lse * L2E;
+      if (it.nt > 0) {
+        // D: this half's share from o and the dO tile, then both halves'.  (A warp whose wait ran out still meets the
+        // others at the barrier.)
+        const int q = 2 * items;
+        ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err) &&
+             mbar_wait(&q_full[(q + 1) % QS], ((q + 1) / QS) & 1, abort_flag, p.err);
+        if (ok) {
+          const uint8_t* tile = smem + L::OFF_Q + (q + 1) % QS * L::TILE + r * 128;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            del = fmaf(__uint_as_float(uw[e] << 16), __uint_as_float(vw[e] << 16), del);
-            del = fmaf(__uint_as_float(uw[e] & 0xffff0000u), __uint_as_float(vw[e] & 0xffff0000u), del);
+          for (int i = 0; i < D / 16; ++i) {
+            const int x = half * (D / 16) + i;
+            const uint4 y = *reinterpret_cast<const uint4*>(tile + x / 8 * CH + ((x % 8) ^ (r & 7)) * 16);
+            const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              del = fmaf(__uint_as_float(uw[e] << 16), __uint_as_float(yw[e] << 16), del);
+              del = fmaf(__uint_as_float(uw[e] & 0xffff0000u), __uint_as_float(yw[e] & 0xffff0000u), del);
+            }
           }
         }
-        const float z = p.lse[flat];
-        if (z > -INFINITY) lse = z * L2E;          // a row without keys: P = 2^-inf = 0
+        float* mine = shares + (items & 1) * 256;
+        mine[half * 128 + r] = del;
+        named_bar(1, 256);
+        del += mine[(half ^ 1) * 128 + r];
+        if (lane == 0) {
+          mbar_arrive(&q_empty[q % QS]);
+          mbar_arrive(&q_empty[(q + 1) % QS]);
+        }
+        if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
       }
-      del_half[half * 128 + r] = del;
-      named_bar(1, 256);
-      del += del_half[(half ^ 1) * 128 + r];
-      named_bar(1, 256);
-      if (!ok) continue;
-      if (valid && half == 0) a.del[flat] = del;
-      for (int j = 0; j < it.nt; ++j, ++n) {
+      for (int j = 0; ok && j < it.nt; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         float e[2][32];
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -lse));
+            for (int i = 0; i < 32; ++i) e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -z));
         }
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
@@ -416,15 +418,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      if (!ok) continue;
-      __nv_bfloat16* dst = valid ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
-      if (it.nt == 0) {
-        if (valid)
+      // the next item's o sets out before this one's dQ is awaited
+      const bool keys = it.nt > 0, here = valid;
+      __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
+      w.next();
+      more = w.at(a, it, false);
+      if (more) fetch(it);
+      if (!keys) {
+        if (here)
           for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      if (!mbar_wait(dq_done, items & 1, abort_flag, p.err)) { ok = false; continue; }
+      ok = ok && mbar_wait(dq_done, items & 1, abort_flag, p.err);
       ++items;
+      if (!ok) continue;
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         tmem_ld32(lane_base + COL_DQ + half * (D / 2) + 32 * q, v);
         tmem_ld_wait();
         reg_fence32(v);
-        if (valid) store32(dst + 32 * q, v, p.scale, a.dq32);
+        if (here) store32(dst + 32 * q, v, p.scale, a.dq32);
       }
       tc_fence_before();
     }
@@ -462,17 +469,17 @@ struct SmemK {
 // line's steps are the kv head's query tiles.  The CTAs get equal ranges of all
 // steps.
 struct Lines {
-  int b, nt, i;                // sequence, its key tiles, line within it
+  int b, hk, tile;             // sequence, kv head, key tile
+  int nt, len;                 // the sequence's key tiles and keys
   int t;                       // step within the line
-  long long left;              // steps of the range from here on
-  int len;
-  FA4_DEV int hk() const { return i / nt; }
-  FA4_DEV int tile() const { return i % nt; }
+  int left;                    // steps of the range from here on
   // to the next line (the range has more)
   FA4_DEV void line(const Params& a) {
     t = 0;
-    if (++i < a.p.Hkv * nt) return;
-    i = 0;
+    if (++tile < nt) return;
+    tile = 0;
+    if (++hk < a.p.Hkv) return;
+    hk = 0;
     do {
       ++b;
       len = key_count(a.p, b, false);
@@ -483,40 +490,21 @@ struct Lines {
 
 FA4_DEV int tiles_of(const Params& a, int b) { return (key_count(a.p, b, false) + BN - 1) / BN; }
 
-// Key tiles that hold keys, of the sequences before `b` and in all (one warp).
-FA4_DEV void count_tiles(const Params& a, int b, int lane, long long& before, long long& all) {
-  if (!a.p.lens) {
-    before = (long long)b * a.key_tiles;
-    all = (long long)a.p.B * a.key_tiles;
-    return;
-  }
-  before = all = 0;
-  for (int x = lane; x < a.p.B; x += 32) {
-    const int n = tiles_of(a, x);
-    all += n;
-    if (x < b) before += n;
-  }
-  for (int o = 16; o > 0; o /= 2) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
+// Key tiles that hold keys, of all sequences (one warp).
+FA4_DEV long long all_tiles(const Params& a, int lane) {
+  if (!a.p.lens) return (long long)a.p.B * a.key_tiles;
+  long long all = 0;
+  for (int x = lane; x < a.p.B; x += 32) all += tiles_of(a, x);
+  for (int o = 16; o > 0; o /= 2) all += __shfl_xor_sync(0xffffffffu, all, o);
+  return all;
 }
 
 // The first step of CTA `cta` of `total` steps.
 FA4_DEV long long range_start(const Params& a, long long total, int cta) { return total * cta / a.ctas; }
 
-// This CTA's range (one warp).
-FA4_DEV Lines find_range(const Params& a, int lane) {
-  Lines x;
-  long long before, all;
-  count_tiles(a, 0, lane, before, all);
-  const long long total = all * a.p.Hkv * a.tiles;
-  const long long s0 = range_start(a, total, blockIdx.x), s1 = range_start(a, total, blockIdx.x + 1);
-  x.left = s1 - s0;
-  x.b = x.nt = x.i = x.t = x.len = 0;
-  if (x.left == 0) return x;
-  long long line = s0 / a.tiles;
-  x.t = (int)(s0 % a.tiles);
+// The sequence, kv head and key tile of a line (one warp).
+FA4_DEV void find_line(const Params& a, long long line, int lane, Lines& x) {
+  x.b = 0;
   if (!a.p.lens) {
     x.b = (int)(line / ((long long)a.p.Hkv * a.key_tiles));
     line -= (long long)x.b * a.p.Hkv * a.key_tiles;
@@ -539,9 +527,22 @@ FA4_DEV Lines find_range(const Params& a, int lane) {
       line -= __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  x.i = (int)line;
   x.len = key_count(a.p, x.b, false);
   x.nt = (x.len + BN - 1) / BN;
+  x.hk = (int)line / x.nt;
+  x.tile = (int)line % x.nt;
+}
+
+// This CTA's range (one warp).
+FA4_DEV Lines find_range(const Params& a, int lane) {
+  Lines x;
+  const long long total = all_tiles(a, lane) * a.p.Hkv * a.tiles;
+  const long long s0 = range_start(a, total, blockIdx.x), s1 = range_start(a, total, blockIdx.x + 1);
+  x.left = (int)(s1 - s0);
+  x.b = x.hk = x.tile = x.nt = x.t = x.len = 0;
+  if (x.left == 0) return x;
+  x.t = (int)(s0 % a.tiles);
+  find_line(a, s0 / a.tiles, lane, x);
   return x;
 }
 
@@ -579,14 +580,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     mbar_init(k_full, 1); mbar_init(k_empty, 1); mbar_init(v_full, 1); mbar_init(v_empty, 1);
-    for (int s = 0; s < RS; ++s) { mbar_init(&r_full[s], 1); mbar_init(&r_empty[s], 1); }
+    for (int s = 0; s < RS; ++s) { mbar_init(&r_full[s], 1); mbar_init(&r_empty[s], 2); }
     for (int s = 0; s < 2; ++s) { mbar_init(&st_full[s], 1); mbar_init(&st_empty[s], 8); }
     mbar_init(s_full, 1);
     mbar_init(p_full, 8);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 8);
-    mbar_init(acc_done, 1);
-    mbar_init(mma_done, 1);
+    mbar_init(acc_done, 2);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           if (ln > 0 && !mbar_wait(empty, (ln - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(full, L::TILE);
           for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + off + c * CH, m, full, 64 * c, at_.tile() * BN, at_.hk(), at_.b);
+            tma_heads(smem + off + c * CH, m, full, 64 * c, at_.tile * BN, at_.hk, at_.b);
           ++count;
           return true;
         };
@@ -628,7 +629,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           const int st = rn % RS;
           if (rn >= RS && !mbar_wait(&r_empty[st], (rn / RS - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(&r_full[st], a.box * 2 * D);
-          const int h = at_.hk() * G + at_.t / a.per_head * a.heads, n = at_.t % a.per_head * BM;
+          int g, n;
+          divide(at_.t, a.per_head, g, n);
+          const int h = at_.hk * G + g * a.heads;
+          n *= BM;
           for (int c = 0; c < D / 64; ++c)
             tma_heads(smem + L::OFF_R + st * L::TILE + c * CH, m, &r_full[st], 64 * c, n, h, at_.b);
           ++rn;
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           z[i] = INFINITY;
           d4[i] = 0.f;
           if (g < G) {
-            const long long flat = ((long long)at_.b * p.Hq + at_.hk() * G + g) * p.Nq + n;
+            const long long flat = ((long long)at_.b * p.Hq + at_.hk * G + g) * p.Nq + n;
             const float v = p.lse[flat];
             if (v > -INFINITY) z[i] = v * L2E;
             d4[i] = a.del[flat];
@@ -686,70 +690,58 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         if (++at_.t == a.tiles) at_.line(a);
         fetch();
       }
-    } else if (warp == W_MMA) {
+    } else if (warp == W_MMA || warp == W_MMA_B) {
+      // the first warp issues S^T and dV, the second dP^T and dK.  Each overwrites, in its own order, what its own
+      // product before has read: S^T the P^T, dP^T the dS^T.
+      const int x = warp == W_MMA ? 0 : 1;
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_a = idesc_f16(BM, D, true, false, true);
-      const uint32_t sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
-      auto ring = [&](int seq) { return smem_u32(smem + L::OFF_R + seq % RS * L::TILE); };
-      auto arrived = [&](int seq) { return mbar_wait(&r_full[seq % RS], (seq / RS) & 1, abort_flag, p.err); };
-      const long long steps = at_.left;
-      // step n: the first or last of its line?  (t counts on from the range's start)
-      auto first_of = [&](long long n) { return n == 0 || (at_.t + n) % a.tiles == 0; };
-      auto last_of = [&](long long n) { return n == steps - 1 || (at_.t + n + 1) % a.tiles == 0; };
-      int ls = 0, lp = 0;                  // lines begun by S^T, by dP^T
-      auto issue_s = [&](int n) -> bool {
-        if (first_of(n)) {
-          if (!mbar_wait(k_full, ls & 1, abort_flag, p.err)) return false;
-          ++ls;
+      const uint32_t fixed = smem_u32(smem + (x ? L::OFF_V : L::OFF_K));
+      const uint32_t col = tbase + (x ? COL_DP : COL_S), sum = tbase + (x ? COL_DK : COL_DV);
+      uint64_t *full = x ? v_full : k_full, *empty = x ? v_empty : k_empty;
+      uint64_t *there = x ? dp_full : s_full, *ready = x ? ds_full : p_full;
+      const int steps = at_.left;
+      int t = at_.t, lines = 0;              // the next step's place in its line; lines begun
+      auto issue = [&](int n, bool first, bool last) -> bool {
+        const int seq = 2 * n + x;           // Q for S^T, dO for dP^T
+        if (first) {
+          if (!mbar_wait(full, lines & 1, abort_flag, p.err)) return false;
+          ++lines;
         }
-        if (!arrived(2 * n)) return false;
+        if (!mbar_wait(&r_full[seq % RS], (seq / RS) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
+        const uint32_t b = smem_u32(smem + L::OFF_R + seq % RS * L::TILE);
         if (leader) {
-          product_kk<D>(tbase + COL_S, sk, ring(2 * n), idesc_s);
-          mma_commit(s_full);
-          if (last_of(n)) mma_commit(k_empty);
+          product_rows<D>(col, fixed, b, idesc_s);
+          mma_commit(there);
+          mma_commit(&r_empty[seq % RS]);
+          if (last) mma_commit(empty);
         }
         __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int n) -> bool {
-        if (first_of(n)) {
-          if (!mbar_wait(v_full, lp & 1, abort_flag, p.err)) return false;
-          ++lp;
-        }
-        if (!arrived(2 * n + 1)) return false;
-        tc_fence_after();
-        if (leader) {
-          product_kk<D>(tbase + COL_DP, sv, ring(2 * n + 1), idesc_s);
-          mma_commit(dp_full);
-          if (last_of(n)) mma_commit(v_empty);
-        }
-        __syncwarp();
-        return true;
-      };
-      bool ok = steps == 0 || (issue_s(0) && issue_dp(0));
+      // of the step whose product is awaited: is it the first, the last here of its line?
+      bool first = true, last = steps == 1 || t + 1 == a.tiles;
+      bool ok = steps == 0 || issue(0, true, last);
       for (int n = 0; ok && n < steps; ++n) {
-        const bool add = !first_of(n);
-        ok = mbar_wait(p_full, n & 1, abort_flag, p.err);
+        t = t + 1 == a.tiles ? 0 : t + 1;
+        const bool next_last = n + 2 == steps || t + 1 == a.tiles;
+        const int seq = 2 * n + 1 - x;       // dO for dV, Q for dK (it has arrived: the step's scores are there)
+        ok = mbar_wait(&r_full[seq % RS], (seq / RS) & 1, abort_flag, p.err) &&
+             mbar_wait(ready, n & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t b = smem_u32(smem + L::OFF_R + seq % RS * L::TILE);
         if (leader) {
-          product_tmem(tbase + COL_DV, tbase + COL_S, tbase + COL_S + 64, ring(2 * n + 1), idesc_a, add);
-          mma_commit(&r_empty[(2 * n + 1) % RS]);
+          product_cols(sum, col, col + 64, b, idesc_a, !first);
+          mma_commit(&r_empty[seq % RS]);
+          if (last) mma_commit(acc_done);
         }
         __syncwarp();
-        if (n + 1 < steps && !issue_s(n + 1)) { ok = false; break; }
-        ok = mbar_wait(ds_full, n & 1, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          product_tmem(tbase + COL_DK, tbase + COL_DP, tbase + COL_DP + 64, ring(2 * n), idesc_a, add);
-          mma_commit(&r_empty[(2 * n) % RS]);
-          if (last_of(n)) mma_commit(acc_done);
-        }
-        __syncwarp();
-        if (n + 1 < steps && !issue_dp(n + 1)) { ok = false; break; }
+        if (n + 1 < steps) ok = issue(n + 1, last, next_last);
+        first = last;
+        last = next_last;
       }
       if (leader) mma_commit(mma_done);
       __syncwarp();
@@ -765,7 +757,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
     int n = 0, lines = 0;
     bool ok = true;
     while (ok && at_.left > 0) {
-      const int s0 = at_.t, s1 = (int)min((long long)a.tiles, s0 + at_.left);
+      const int s0 = at_.t, s1 = min(a.tiles, s0 + at_.left);
       for (; at_.t < s1; ++at_.t, ++n) {
         const int st = n & 1;
         const float* stat = reinterpret_cast<const float*>(smem + L::OFF_ST + st * 1024) + 64 * half;
@@ -837,10 +829,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       if (!mbar_wait(acc_done, lines & 1, abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
       const bool whole = s0 == 0 && s1 == a.tiles;
-      const int key = at_.tile() * BN + r;
+      const int key = at_.tile * BN + r;
       const bool mine = key < p.Nk;
       const float f = key < at_.len ? (half ? p.scale : 1.f) : 0.f;
-      __nv_bfloat16* dst = mine ? at(half ? p.dk : p.dv, at_.b, at_.hk(), key) : nullptr;
+      __nv_bfloat16* dst = mine ? at(half ? p.dk : p.dv, at_.b, at_.hk, key) : nullptr;
       // partials: slot 0 for the range's first line, 1 for its last
       float* part = a.part + ((((long long)blockIdx.x * 2 + (lines > 0)) * 2 + half) * BN + r) * D;
 #pragma unroll
@@ -873,62 +865,63 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
-// A CTA per key tile of Nk, kv head and sequence (x), and dV or dK (y).
+// dV (y = 0) and dK (y = 1) of the key tiles whose steps lie in several ranges: the x
+// below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside a key tile's steps
+// and began at or before their first.  Then, where sequences have lengths, zeros for the
+// key tiles behind them: an x for each sequence and kv head.
+constexpr int JOIN_PARTS = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
   const CrossParams& p = a.p;
-  __shared__ long long counts[2];
-  const int jt = blockIdx.x % a.key_tiles, bh = blockIdx.x / a.key_tiles, hk = bh % p.Hkv, b = bh / p.Hkv;
   const int which = blockIdx.y;
-  const int len = key_count(p, b), nt = (len + BN - 1) / BN;
   const Strided& out = which ? p.dk : p.dv;
-  const bool live = jt < nt;
-  long long first = 0;
-  int c0 = 0, c1 = 0;
-  if (live) {
-    if (threadIdx.x < 32) {
-      long long before, all;
-      count_tiles(a, b, threadIdx.x, before, all);
-      if (threadIdx.x == 0) { counts[0] = before; counts[1] = all; }
-    }
-    __syncthreads();
-    const long long line = counts[0] * p.Hkv + (long long)hk * nt + jt, total = counts[1] * p.Hkv * a.tiles;
-    first = line * a.tiles;
-    const long long end = first + a.tiles;
-    // the CTAs whose ranges meet [first, end)
-    auto owner = [&](long long s) {
-      int c = (int)(s * a.ctas / total);
-      while (c + 1 < a.ctas && range_start(a, total, c + 1) <= s) ++c;
-      while (c > 0 && range_start(a, total, c) > s) --c;
-      return c;
-    };
-    c0 = owner(first);
-    c1 = owner(end - 1);
-    if (c0 == c1) return;                       // written whole
-    // of each range, slot 0 unless it began in a line before
-    for (int x = threadIdx.x; x < BN * (D / 8); x += 256) {
-      const int r = x / (D / 8), i = x % (D / 8) * 8, key = jt * BN + r;
-      if (key >= p.Nk) break;
-      float v[8] = {};
-      for (int c = c0; c <= c1; ++c) {
-        const long long s = range_start(a, total, c);
-        if (range_start(a, total, c + 1) == s) continue;
-        const float* from = a.part + ((((long long)c * 2 + (s < first)) * 2 + which) * BN + r) * D + i;
-        const float4 u = *reinterpret_cast<const float4*>(from), w = *reinterpret_cast<const float4*>(from + 4);
-        v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
-        v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
-      }
-      const float f = which ? p.scale : 1.f;
-      *reinterpret_cast<uint4*>(at(out, b, hk, key) + i) =
-          make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
-                     pack2(v[6] * f, v[7] * f));
-    }
+  if ((int)blockIdx.x >= a.ctas) {
+    int b, hk;
+    divide((int)blockIdx.x - a.ctas, a.hkv, b, hk);
+    const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
+    for (long long x = blockIdx.z * 256 + threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += JOIN_PARTS * 256)
+      *reinterpret_cast<uint4*>(at(out, b, hk, from + (int)(x / (D / 8))) + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
-  for (int x = threadIdx.x; x < BN * (D / 8); x += 256) {
-    const int r = x / (D / 8), i = x % (D / 8) * 8, key = jt * BN + r;
+  const int c0 = blockIdx.x;
+  __shared__ Lines place;
+  __shared__ long long sum;
+  if (threadIdx.x < 32) {
+    const long long total = all_tiles(a, threadIdx.x) * p.Hkv * a.tiles;
+    const long long end = range_start(a, total, c0 + 1);
+    Lines x;
+    x.left = 0;
+    // (a range that ends with its key tile's steps, or began inside them, joins nothing)
+    if (end > range_start(a, total, c0) && end % a.tiles != 0 && range_start(a, total, c0) <= end / a.tiles * a.tiles) {
+      x.left = 1;
+      find_line(a, end / a.tiles, threadIdx.x, x);
+    }
+    if (threadIdx.x == 0) {
+      place = x;
+      sum = total;
+    }
+  }
+  __syncthreads();
+  if (!place.left) return;
+  const long long total = sum, first = range_start(a, total, c0 + 1) / a.tiles * a.tiles;
+  for (int x = blockIdx.z * 256 + threadIdx.x; x < BN * (D / 8); x += JOIN_PARTS * 256) {
+    const int r = x / (D / 8), i = x % (D / 8) * 8, key = place.tile * BN + r;
     if (key >= p.Nk) break;
-    *reinterpret_cast<uint4*>(at(out, b, hk, key) + i) = make_uint4(0, 0, 0, 0);
+    float v[8] = {};
+    for (int c = c0; c < a.ctas; ++c) {
+      const long long s = range_start(a, total, c);
+      if (s >= first + a.tiles) break;
+      if (range_start(a, total, c + 1) == s) continue;
+      // slot 0, unless the range began in a line before
+      const float* from = a.part + ((((long long)c * 2 + (s < first)) * 2 + which) * BN + r) * D + i;
+      const float4 u = *reinterpret_cast<const float4*>(from), w = *reinterpret_cast<const float4*>(from + 4);
+      v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+      v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+    }
+    const float f = which ? p.scale : 1.f;
+    *reinterpret_cast<uint4*>(at(out, place.b, place.hk, key) + i) =
+        make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
+                   pack2(v[6] * f, v[7] * f));
   }
 }
 
@@ -952,8 +945,11 @@ cudaError_t zero(const Strided& t, int B, int H, int N, int d, cudaStream_t st) 
 void plan(Params& a, int B, int Hq, int Hkv, int Nq, int Nk, bool share) {
   const int G = Hq / Hkv;
   a.heads = share && Nq <= 64 ? (128 / Nq < G ? 128 / Nq : G) : 1;
-  a.per_head = (Nq + BM - 1) / BM;
-  a.tiles = a.heads > 1 ? (G + a.heads - 1) / a.heads : G * a.per_head;
+  a.per_head = Divisor((Nq + BM - 1) / BM);
+  a.tiles = a.heads > 1 ? (G + a.heads - 1) / a.heads : G * a.per_head.d;
+  a.per_kv = Divisor(a.tiles);
+  a.hkv = Divisor(Hkv);
+  a.nq = Divisor(Nq);
   a.box = a.heads > 1 ? a.heads * Nq : BM;
   a.items = (int)((long long)B * Hkv * a.tiles);
   a.key_tiles = (Nk + BN - 1) / BN;
@@ -1002,7 +998,7 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
       !heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, BN, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, BN, 1))
     return cudaErrorInvalidValue;
   const int sms = sm_count();
-  const dim3 gq(a.items < sms ? a.items : sms), gk(a.ctas), gj(p.B * p.Hkv * a.key_tiles, 2);
+  const dim3 gq(a.items < sms ? a.items : sms), gk(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 2, JOIN_PARTS);
   cudaError_t e;
   if (p.d == 128) {
     e = start(cross_dq_kernel<128>, gq, SmemQ<128>::BYTES, a, st);

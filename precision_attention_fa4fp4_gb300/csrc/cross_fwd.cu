@@ -14,8 +14,10 @@
 //              Then O / l to the row's place, 32 bytes at a time.
 //   warp 8     producer: Q tiles through one ring, K and V tiles through another,
 //              ahead of the item at work.
-//   warp 9     issues the products: S = Q K^T, O += P V (P from tensor memory, V
-//              MN-major).  The next S of a tile follows its P V, across items too.
+//   warps 9-10 issue the products of tile A and of tile B: S = Q K^T, O += P V (P
+//              from tensor memory, V MN-major).  The next S of a tile follows its
+//              P V, across items too.  (One warp for both tiles was the bound: a
+//              product takes 512 cycles, its waits, instructions and commits 600.)
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).
 #include <cuda_bf16.h>
 #include "common.cuh"
@@ -27,7 +29,7 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NTHREADS = 384;
-constexpr int W_PROD = 8, W_MMA = 9;
+constexpr int W_PROD = 8, W_MMA = 9, W_MMA_B = 10;
 constexpr int REG_SOFT = 208, REG_MISC = 88;   // 2 x 208 + 88 = 504 of 512
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
@@ -37,9 +39,10 @@ struct Params {
   CrossParams p;
   HeadsMap q, k, v;
   int tiles;        // per (sequence, kv head)
-  int per_head;     // tiles of a query head (1 where heads share a tile)
   int heads;        // query heads of a tile
-  int pairs;        // items per (sequence, kv head)
+  Divisor per_head; // tiles of a query head (1 where heads share a tile)
+  Divisor pairs;    // items per (sequence, kv head)
+  Divisor hkv, nq;
   int items;
   int box;          // rows that a Q box brings
   int o32;          // rows of O begin on 32 bytes
@@ -47,7 +50,6 @@ struct Params {
 
 template <int D>
 struct Smem {
-  static constexpr int CH = 128 * 128;              // [128 rows][64 channels]
   static constexpr int TILE = (D / 64) * CH;
   static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0, OFF_KV = OFF_Q + QS * TILE;
@@ -71,10 +73,10 @@ struct Walk {
   FA4_DEV Walk() : i(blockIdx.x) {}
   FA4_DEV bool at(const Params& a, Item& it, bool report) {
     if (i >= a.items) return false;
-    const int bh = i / a.pairs;
-    it.b = bh / a.p.Hkv;
-    it.hk = bh % a.p.Hkv;
-    it.tile0 = 2 * (i % a.pairs);
+    int bh, pair;
+    divide(i, a.pairs, bh, pair);
+    divide(bh, a.hkv, it.b, it.hk);
+    it.tile0 = 2 * pair;
     it.two = it.tile0 + 1 < a.tiles;
     if (it.b != b) {
       b = it.b;
@@ -126,9 +128,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
     for (int x = 0; x < 2; ++x) { mbar_init(&s_full[x], 1); mbar_init(&p_full[x], 4); mbar_init(&o_done[x], 1); }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -152,9 +154,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           const int st = qn % QS;
           if (qn >= QS && !mbar_wait(&q_empty[st], (qn / QS - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(&q_full[st], a.box * 2 * D);
-          const int h = it.hk * G + tile / a.per_head * a.heads, n = tile % a.per_head * BM;
+          int g, n;
+          divide(tile, a.per_head, g, n);
+          const int h = it.hk * G + g * a.heads;
+          n *= BM;
           for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_Q + st * L::TILE + c * L::CH, a.q, &q_full[st], 64 * c, n, h, it.b);
+            tma_heads(smem + L::OFF_Q + st * L::TILE + c * CH, a.q, &q_full[st], 64 * c, n, h, it.b);
           ++qn;
           return true;
         };
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           if (kn >= KS && !mbar_wait(&kv_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(&kv_full[st], L::TILE);
           for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_KV + st * L::TILE + c * L::CH, m, &kv_full[st], 64 * c, j * BN, it.hk, it.b);
+            tma_heads(smem + L::OFF_KV + st * L::TILE + c * CH, m, &kv_full[st], 64 * c, j * BN, it.hk, it.b);
           ++kn;
           return true;
         };
@@ -182,97 +187,77 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
         }
       }
       __syncwarp();
-    } else if (warp == W_MMA) {
+    } else if (warp == W_MMA || warp == W_MMA_B) {
       // ---------------------------------------------------------- products
+      const int x = warp == W_MMA ? 0 : 1;
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_o = idesc_f16(BM, D, true, false, true);
-      // a key tile of an item, and where its operands are
-      struct Step {
-        Item it;
-        int j, kv, q;                        // key tile; ring positions of its K, and of the item's Q tiles
-      };
+      const uint32_t col_s = tbase + COL_S0 + 128 * x, col_o = tbase + COL_O0 + D * x;
+      auto tile_q = [&](int seq) { return smem_u32(smem + L::OFF_Q + seq % QS * L::TILE); };
+      auto tile_kv = [&](int seq) { return smem + L::OFF_KV + seq % KS * L::TILE; };
+      auto arrived = [&](int seq) { return mbar_wait(&kv_full[seq % KS], (seq / KS) & 1, abort_flag, p.err); };
       Walk w;
-      int qn = 0, kn = 0;
-      auto first = [&](Step& s) -> bool {
-        if (!w.with_keys(a, s.it, false)) return false;
-        s.j = 0;
-        s.kv = kn;
-        s.q = qn;
-        return true;
-      };
-      auto after = [&](const Step& s, Step& n) -> bool {
-        kn = s.kv + 2;
-        if (s.j + 1 < s.it.nt) {
-          n = s;
-          ++n.j;
-          n.kv = kn;
-          return true;
-        }
-        qn = s.q + (s.it.two ? 2 : 1);
-        w.next();
-        return first(n);
-      };
-      int pn[2] = {0, 0};                    // P V issued of each tile
-      auto issue_qk = [&](int x, const Step& s) -> bool {
-        const int ks = s.kv % KS, q = s.q + x, qs = q % QS;
-        if (s.j == 0 && !mbar_wait(&q_full[qs], (q / QS) & 1, abort_flag, p.err)) return false;
-        if (!mbar_wait(&kv_full[ks], (s.kv / KS) & 1, abort_flag, p.err)) return false;
+      Item it;
+      int kv = 0, qn = 0, n = 0;             // ring positions of K_j and of the item's Q_A; tiles done
+      bool ok = true, ahead = false;         // ahead: S of this item's first key tile is issued
+      // S = Q K_j^T; the item's last one lets go of Q
+      auto issue_s = [&](int q, int k, bool first, bool last) -> bool {
+        if (first && !mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err)) return false;
+        if (!arrived(k)) return false;
         tc_fence_after();
-        const uint32_t sq = smem_u32(smem + L::OFF_Q + qs * L::TILE), sk = smem_u32(smem + L::OFF_KV + ks * L::TILE);
+        const uint32_t sq = tile_q(q), sk = smem_u32(tile_kv(k));
         if (leader) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * L::CH + (k % 4) * 32;
-            mma_f16(tbase + COL_S0 + 128 * x, make_sdesc(sq + off, 16, 1024, SW_128B),
-                    make_sdesc(sk + off, 16, 1024, SW_128B), idesc_s, k > 0);
-          }
+          product_rows<D>(col_s, sq, sk, idesc_s);
           mma_commit(&s_full[x]);
-          if (x == 1 || !s.it.two) mma_commit(&kv_empty[ks]);
-          if (s.j == s.it.nt - 1) mma_commit(&q_empty[qs]);
+          mma_commit(&kv_empty[k % KS]);
+          if (last) mma_commit(&q_empty[q % QS]);
         }
         __syncwarp();
         return true;
       };
-      auto issue_pv = [&](int x, const Step& s) -> bool {
-        const int seq = s.kv + 1, st = seq % KS;
-        uint8_t* v = smem + L::OFF_KV + st * L::TILE;
-        if (x == 0) {
-          if (!mbar_wait(&kv_full[st], (seq / KS) & 1, abort_flag, p.err)) return false;
-          // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not
-          const int keep = s.it.len - s.j * BN;
-          if (keep < BN && s.it.len < p.Nk) {
-            for (int c = 0; c < D / 64; ++c)
-              for (int i = keep * 8 + lane; i < BN * 8; i += 32)
-                reinterpret_cast<uint4*>(v + c * L::CH)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        if (!mbar_wait(&p_full[x], pn[x] & 1, abort_flag, p.err)) return false;
-        ++pn[x];
-        tc_fence_after();
-        const uint32_t sv = smem_u32(v);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_f16_tmem_a(tbase + COL_O0 + D * x, tbase + COL_S0 + 128 * x + 8 * k,
-                           make_sdesc(sv + k * 16 * 128, L::CH, 1024, SW_128B), idesc_o, s.j > 0 || k > 0);
-          mma_commit(&o_done[x]);
-          if (x == 1 || !s.it.two) mma_commit(&kv_empty[st]);
-        }
-        __syncwarp();
-        return true;
-      };
-      Step cur, nxt;
-      bool more = first(cur);
-      bool ok = !more || (issue_qk(0, cur) && (!cur.it.two || issue_qk(1, cur)));
+      bool more = w.with_keys(a, it, false);
       while (ok && more) {
-        const bool then = after(cur, nxt);
-        ok = issue_pv(0, cur) && (!then || issue_qk(0, nxt)) && (!cur.it.two || issue_pv(1, cur)) &&
-             (!then || !nxt.it.two || issue_qk(1, nxt));
-        more = then;
-        cur = nxt;
+        const int nt = it.nt, len = it.len;
+        const bool mine = x == 0 || it.two;
+        const int q = qn + x, k0 = kv;
+        if (mine && !ahead) ok = issue_s(q, k0, true, nt == 1);
+        ahead = false;
+        qn += it.two ? 2 : 1;
+        kv += 2 * nt;
+        w.next();
+        for (int j = 0; ok && j < nt; ++j) {
+          const int k = k0 + 2 * j, v = k + 1;
+          if (!mine) {                       // tile A alone: only let go of K and V
+            ok = arrived(k) && arrived(v);
+            if (leader) { mbar_arrive(&kv_empty[k % KS]); mbar_arrive(&kv_empty[v % KS]); }
+            __syncwarp();
+            continue;
+          }
+          ok = arrived(v);
+          if (!ok) break;
+          // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not (both issuing
+          // warps write the same zeros)
+          if (len - j * BN < BN && len < p.Nk) clear_rows<D>(tile_kv(v), len - j * BN, lane);
+          ok = mbar_wait(&p_full[x], n & 1, abort_flag, p.err);
+          if (!ok) break;
+          ++n;
+          tc_fence_after();
+          const uint32_t sv = smem_u32(tile_kv(v));
+          if (leader) {
+            product_cols(col_o, col_s, col_s + 32, sv, idesc_o, j > 0);
+            mma_commit(&o_done[x]);
+            mma_commit(&kv_empty[v % KS]);
+          }
+          __syncwarp();
+          if (j + 1 < nt) ok = issue_s(q, k + 2, false, j + 2 == nt);
+        }
+        // the next item's first S, while this one's last tile is at its softmax's end
+        more = ok && w.with_keys(a, it, false);
+        if (more && mine && (x == 0 || it.two)) {
+          ok = issue_s(qn + x, kv, true, it.nt == 1);
+          ahead = true;
+        }
       }
       if (leader) mma_commit(mma_done);
       __syncwarp();
@@ -298,12 +283,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
       const int tile = it.tile0 + x;
       int g, row;
       if (a.heads > 1) {
-        g = tile * a.heads + r / p.Nq;
-        row = r % p.Nq;
-        if (r >= a.heads * p.Nq) g = G;
+        divide(r, a.nq, g, row);
+        g = r < a.heads * p.Nq ? tile * a.heads + g : G;
       } else {
-        g = tile / a.per_head;
-        row = tile % a.per_head * BM + r;
+        divide(tile, a.per_head, g, row);
+        row = row * BM + r;
       }
       const bool valid = g < G && row < p.Nq;
       float m = 0.f, mc = 0.f, l = 0.f;
@@ -439,10 +423,12 @@ cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {
   a.p = p;
   const int G = p.Hq / p.Hkv;
   a.heads = p.Nq <= 64 && p.q.h != 0 ? (128 / p.Nq < G ? 128 / p.Nq : G) : 1;
-  a.per_head = (p.Nq + BM - 1) / BM;
-  a.tiles = a.heads > 1 ? (G + a.heads - 1) / a.heads : G * a.per_head;
-  a.pairs = (a.tiles + 1) / 2;
-  const long long items = (long long)p.B * p.Hkv * a.pairs;
+  a.per_head = Divisor((p.Nq + BM - 1) / BM);
+  a.tiles = a.heads > 1 ? (G + a.heads - 1) / a.heads : G * a.per_head.d;
+  a.pairs = Divisor((a.tiles + 1) / 2);
+  a.hkv = Divisor(p.Hkv);
+  a.nq = Divisor(p.Nq);
+  const long long items = (long long)p.B * p.Hkv * a.pairs.d;
   a.items = (int)items;
   a.box = a.heads > 1 ? a.heads * p.Nq : BM;
   a.o32 = (reinterpret_cast<uintptr_t>(p.o.p) & 31) == 0 && ((p.o.b | p.o.h | p.o.n) & 15) == 0;
