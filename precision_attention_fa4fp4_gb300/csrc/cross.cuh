@@ -36,6 +36,19 @@ FA4_DEV void tma_heads(void* dst, const HeadsMap& m, uint64_t* bar, int c, int n
       : "memory");
 }
 
+// A box from shared memory, by one lane; rows behind the tensor's are left out.
+FA4_DEV void tma_heads_store(const HeadsMap& m, const void* src, int c, int n, int h, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(&m.map)),
+               "r"(smem_u32(src)), "r"(c), "r"(n), "r"(h * m.own_h), "r"(b * m.own_b)
+               : "memory");
+}
+
+// 16-byte word x (of D / 8) of a row of a tile.
+FA4_DEV uint4* tile_word(uint8_t* tile, int r, int x) {
+  return reinterpret_cast<uint4*>(tile + x / 8 * (128 * 128) + r * 128 + ((x % 8) ^ (r & 7)) * 16);
+}
+
 // ---------------------------------------------------------------- products
 // Tiles are [128 rows][64 channels] of bf16 with the 128-byte swizzle, D / 64 of
 // them.  Their descriptors differ in the low word alone (address, leading

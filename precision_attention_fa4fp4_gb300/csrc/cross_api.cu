@@ -257,7 +257,9 @@ fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
     if ((s = check_heads(dq, B, Hq, Nq, 2, true)) != FA4FP4_OK) return s;
     p.dq = strided(dq, B, Hq, Nq);
     if (!lse) return FA4FP4_ERR_INVALID_ARG;
-    if ((s = check_rows(p.q, Nq, d)) != FA4FP4_OK || (s = check_rows(p.dout, Nq, d)) != FA4FP4_OK) return s;
+    if ((s = check_rows(p.q, Nq, d)) != FA4FP4_OK || (s = check_rows(p.dout, Nq, d)) != FA4FP4_OK ||
+        (s = check_rows(p.o, Nq, d)) != FA4FP4_OK || (s = check_rows(p.dq, Nq, d)) != FA4FP4_OK)
+      return s;
   }
   if (Nk > 0) {
     const fa4fp4_heads* in[] = {k, v, dk, dv};

@@ -16,9 +16,9 @@
 // cross_dq_kernel: persistent, a query tile at a time.  Warps 0-7: a thread per
 //   row and half of the keys: P from S while dP runs, dS as bf16 into tensor memory
 //   (the A operand of dQ).  S of the next key tile runs as soon as S has been read.
-//   D is summed by the same threads from o and the dO tile, and kept in the
-//   workspace; an item's o is on its way while the item before ends.  Two warps issue
-//   the products: S; dP and dQ.
+//   D is summed by the same threads from the o and dO tiles, and kept in the
+//   workspace; dQ leaves through the dO tile's place.  Two warps issue the products:
+//   S; dP and dQ.
 // cross_dkv_kernel: persistent over the steps (key tile, query tile), cut into
 //   equal ranges.  Rows are keys: P^T and dS^T go over S^T and dP^T as A operands of
 //   dV and dK, which are summed in tensor memory (512 columns in all).  Two warps
@@ -43,7 +43,8 @@ constexpr float L2E = 1.4426950408889634f;
 
 struct Params {
   CrossParams p;
-  HeadsMap q, dout, k, v;
+  HeadsMap q, dout, o, k, v;
+  HeadsMap dq;                                 // boxes of 32 rows, where heads share no tile
   int tiles, heads, box;                       // query tiles of a kv head, as in the forward
   Divisor per_head, per_kv, hkv, nq;           // (per_kv: tiles)
   int key_tiles;                               // of Nk
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   uint64_t* kv_full = q_empty + QS;
   uint64_t* kv_empty = kv_full + KS;
   uint64_t* s_full = kv_empty + KS;      // S is there
-  uint64_t* s_free = s_full + 1;         // S has been read
+  uint64_t* s_free = s_full + 1;         // S has been read, and dP is there
   uint64_t* dp_full = s_free + 1;        // dP is there
   uint64_t* ds_full = dp_full + 1;       // dS is there, dP has been read
   uint64_t* dq_done = ds_full + 1;       // the item's dQ is there
@@ -199,12 +200,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           ++qn;
           return true;
         };
-        auto load_kv = [&](const HeadsMap& m, const ItemQ& it, int j) -> bool {
+        auto load_kv = [&](const HeadsMap& m, int rows, int n, int h, int b) -> bool {
           const int st = kn % KS;
           if (kn >= KS && !mbar_wait(&kv_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
-          mbar_arrive_expect_tx(&kv_full[st], L::TILE);
+          mbar_arrive_expect_tx(&kv_full[st], rows * 2 * D);
           for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_KV + st * L::TILE + c * CH, m, &kv_full[st], 64 * c, j * BN, it.hk, it.b);
+            tma_heads(smem + L::OFF_KV + st * L::TILE + c * CH, m, &kv_full[st], 64 * c, n, h, b);
           ++kn;
           return true;
         };
@@ -212,8 +213,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         ItemQ it;
         bool ok = true;
         for (; ok && w.with_keys(a, it, true); w.next()) {
-          ok = load_q(a.q, it) && load_kv(a.k, it, 0) && load_q(a.dout, it) && load_kv(a.v, it, 0);
-          for (int j = 1; ok && j < it.nt; ++j) ok = load_kv(a.k, it, j) && load_kv(a.v, it, j);
+          int g, n;
+          divide(it.tile, a.per_head, g, n);
+          ok = load_q(a.q, it) && load_kv(a.k, BN, 0, it.hk, it.b) && load_q(a.dout, it) &&
+               load_kv(a.o, a.box, n * BM, it.hk * G + g * a.heads, it.b) && load_kv(a.v, BN, 0, it.hk, it.b);
+          for (int j = 1; ok && j < it.nt; ++j)
+            ok = load_kv(a.k, BN, j * BN, it.hk, it.b) && load_kv(a.v, BN, j * BN, it.hk, it.b);
         }
         if (*abort_flag) {
           volatile int no_abort = 0;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       }
       __syncwarp();
     } else if (warp == W_MMA) {
-      // S of every step, as soon as the one before has been read
+      // S of every step, once the one before has been read and dP of that step is there
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       WalkQ w;
@@ -233,7 +238,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
         const uint32_t sq = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
         ok = mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
-        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += 2) {
+        // (an item's tiles in the K, V ring: K_0, o, V_0, K_1, V_1, ...)
+        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += j == 1 ? 3 : 2) {
           ok = mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err) &&
                (n == 0 || mbar_wait(s_free, (n - 1) & 1, abort_flag, p.err));
           if (!ok) break;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       const uint32_t idesc_q = idesc_f16(BM, D, true, false, true);
       WalkQ w;
       ItemQ it;
-      int kv = 0, q = 1, n = 0;
+      int k = 0, k_before = 0, q = 1, n = 0;   // K of this step and of the one before it
       bool ok = true, add = false;
       // dQ += dS K of step n - 1, whose K is at ring position k; last: of its item
       auto issue_dq = [&](int k, bool last) -> bool {
@@ -279,9 +285,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       };
       for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
         const uint32_t sdo = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
-        for (int j = 0; ok && j < it.nt; ++j, kv += 2) {
-          const int v = kv + 1;
-          if (n > 0) ok = issue_dq(kv - 2, j == 0);
+        for (int j = 0; ok && j < it.nt; ++j) {
+          const int v = k + (j == 0 ? 2 : 1);
+          if (n > 0) ok = issue_dq(k_before, j == 0);
           if (j == 0) ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
           ok = ok && mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err);
           if (!ok) break;
@@ -295,9 +301,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           }
           __syncwarp();
           ++n;
+          k_before = k;
+          k = v + 1;
         }
       }
-      if (ok && n > 0) issue_dq(kv - 2, true);
+      if (ok && n > 0) issue_dq(k_before, true);
       if (leader) mma_commit(mma_done);
       __syncwarp();
       volatile int no_abort = 0;
@@ -313,44 +321,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     bool ok = true;
     WalkQ w;
     ItemQ it;
-    // an item's row, and this thread's half of its o: on its way while the item before ends
+    int kv = 0;                            // ring position of the item's K_0
+    bool leaving = false;                  // a dQ is on its way out of shared memory
+    // an item's row: its lse is on its way while the item before ends
     bool valid = false;
     int h = 0, row = 0;
     float lse = INFINITY;
-    uint4 u[D / 16];
     auto fetch = [&](const ItemQ& x) {
       int g;
       tile_row(a, x.tile, r, G, g, row);
       valid = g < G;
       h = x.hk * G + g;
-      lse = INFINITY;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) u[i] = make_uint4(0, 0, 0, 0);
-      if (valid) {
-        const uint4* o = reinterpret_cast<const uint4*>(at(p.o, x.b, h, row) + half * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) u[i] = o[i];
-        lse = p.lse[((long long)x.b * p.Hq + h) * p.Nq + row];
-      }
+      lse = valid ? p.lse[((long long)x.b * p.Hq + h) * p.Nq + row] : INFINITY;
     };
     bool more = w.at(a, it, false);
     if (more) fetch(it);
     while (more) {
       float del = 0.f, z = INFINITY;       // (a row without keys: P = 2^-inf = 0)
       if (lse > -INFINITY) z = lse * L2E;
+      const int q = 2 * items, o = kv + 1;
+      uint8_t* tile = smem + L::OFF_Q + (q + 1) % QS * L::TILE;      // dO, in the end dQ
       if (it.nt > 0) {
-        // D: this half's share from o and the dO tile, then both halves'.  (A warp whose wait ran out still meets the
-        // others at the barrier.)
-        const int q = 2 * items;
+        // D: this half's share from the o and dO tiles, then both halves'.  (A warp whose wait ran out still meets the
+        // others at the barriers.)
         ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err) &&
-             mbar_wait(&q_full[(q + 1) % QS], ((q + 1) / QS) & 1, abort_flag, p.err);
+             mbar_wait(&q_full[(q + 1) % QS], ((q + 1) / QS) & 1, abort_flag, p.err) &&
+             mbar_wait(&kv_full[o % KS], (o / KS) & 1, abort_flag, p.err);
         if (ok) {
-          const uint8_t* tile = smem + L::OFF_Q + (q + 1) % QS * L::TILE + r * 128;
+          uint8_t* ot = smem + L::OFF_KV + o % KS * L::TILE;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const int x = half * (D / 16) + i;
-            const uint4 y = *reinterpret_cast<const uint4*>(tile + x / 8 * CH + ((x % 8) ^ (r & 7)) * 16);
-            const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, yw[4] = {y.x, y.y, y.z, y.w};
+            const uint4 u = *tile_word(ot, r, x), y = *tile_word(tile, r, x);
+            const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               del = fmaf(__uint_as_float(uw[e] << 16), __uint_as_float(yw[e] << 16), del);
@@ -364,9 +367,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         del += mine[(half ^ 1) * 128 + r];
         if (lane == 0) {
           mbar_arrive(&q_empty[q % QS]);
-          mbar_arrive(&q_empty[(q + 1) % QS]);
+          if (leaving) {                   // the dQ before this one has left the dO tile before this one
+            bulk_wait_read0();
+            mbar_arrive(&q_empty[(q - 1) % QS]);
+          }
         }
+        if (threadIdx.x == 0) mbar_arrive(&kv_empty[o % KS]);
         if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
+        kv += 2 * it.nt + 1;
       }
       for (int j = 0; ok && j < it.nt; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
@@ -380,14 +388,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           reg_fence32(v[0]);
           reg_fence32(v[1]);
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i) e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -z));
         }
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
+        // the next S may run from here on, not before: products of two warps share the tensor cores, and dP is what
+        // these threads wait for (S runs while they form dS)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         tc_fence_after();
         const int keep = it.len - j * BN - 64 * half;
         uint32_t pk[32];
@@ -418,31 +428,62 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      // the next item's o sets out before this one's dQ is awaited
-      const bool keys = it.nt > 0, here = valid;
+      // the next item's lse sets out before this one's dQ is awaited
+      const ItemQ was = it;
+      const bool here = valid;
       __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
       w.next();
       more = w.at(a, it, false);
       if (more) fetch(it);
-      if (!keys) {
+      if (was.nt == 0) {
         if (here)
           for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
         continue;
       }
       ok = ok && mbar_wait(dq_done, items & 1, abort_flag, p.err);
       ++items;
-      if (!ok) continue;
-      tc_fence_after();
+      if (ok) {
+        tc_fence_after();
+        // rows by themselves would be 32 places a store: they go through the dO tile's place to boxes of 32 rows
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        uint32_t v[32];
-        tmem_ld32(lane_base + COL_DQ + half * (D / 2) + 32 * q, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-        if (here) store32(dst + 32 * q, v, p.scale, a.dq32);
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t v[32];
+          tmem_ld32(lane_base + COL_DQ + half * (D / 2) + 32 * q, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+          if (a.heads > 1) {
+            if (here) store32(dst + 32 * q, v, p.scale, a.dq32);
+          } else {
+            const float f = p.scale;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pk[i] = pack2(__uint_as_float(v[8 * e + 2 * i]) * f, __uint_as_float(v[8 * e + 2 * i + 1]) * f);
+              *tile_word(tile, r, half * (D / 16) + 4 * q + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
       }
-      tc_fence_before();
+      __syncwarp();
+      if (D == 64) named_bar(2 + quad, 64);          // both halves of a row are in one box
+      if (lane == 0) {
+        int g, n;
+        divide(was.tile, a.per_head, g, n);
+        n = n * BM + 32 * quad;
+        if (ok && a.heads == 1 && n < p.Nq && (D == 128 || half == 0)) {
+          tma_heads_store(a.dq, tile + (D == 128 ? half * CH : 0) + quad * 32 * 128, D == 128 ? 64 * half : 0, n,
+                          was.hk * G + g, was.b);
+          bulk_commit();
+        }
+      }
+      __syncwarp();
+      leaving = true;
     }
+    if (lane == 0) bulk_wait_read0();
   }
   tc_fence_before();
   __syncthreads();
@@ -459,7 +500,7 @@ struct SmemK {
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_R = 2 * TILE;
   static constexpr int OFF_ST = OFF_R + RS * TILE;          // [2] x (lse log2 e [128], D [128])
   static constexpr int OFF_BAR = OFF_ST + 2 * 1024;
-  static constexpr int NBAR = 4 + 2 * RS + 4 + 6;
+  static constexpr int NBAR = 4 + 2 * RS + 4 + 7;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 64;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -567,7 +608,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   uint64_t* st_full = r_empty + RS;      // [2]
   uint64_t* st_empty = st_full + 2;
   uint64_t* s_full = st_empty + 2;
-  uint64_t* p_full = s_full + 1;         // P^T is there
+  uint64_t* s_seen = s_full + 1;         // the step's threads have seen s_full
+  uint64_t* p_full = s_seen + 1;         // P^T is there
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;       // dS^T is there
   uint64_t* acc_done = ds_full + 1;      // the line's dV and dK are there
@@ -583,6 +625,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
     for (int s = 0; s < RS; ++s) { mbar_init(&r_full[s], 1); mbar_init(&r_empty[s], 2); }
     for (int s = 0; s < 2; ++s) { mbar_init(&st_full[s], 1); mbar_init(&st_empty[s], 8); }
     mbar_init(s_full, 1);
+    mbar_init(s_seen, 1);
     mbar_init(p_full, 8);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 8);
@@ -730,6 +773,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         const int seq = 2 * n + 1 - x;       // dO for dV, Q for dK (it has arrived: the step's scores are there)
         ok = mbar_wait(&r_full[seq % RS], (seq / RS) & 1, abort_flag, p.err) &&
              mbar_wait(ready, n & 1, abort_flag, p.err);
+        // products of the two warps share the tensor cores, and the next S^T is what the key's threads wait for
+        // first.  (They say that they have it: s_full itself may be a phase further by now.  At a line's end they are
+        // waiting for its dK before they look at the next S^T.)
+        if (x == 1 && !last) ok = ok && mbar_wait(s_seen, (n + 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t b = smem_u32(smem + L::OFF_R + seq % RS * L::TILE);
@@ -765,6 +812,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           ok = false;
           break;
         }
+        if (threadIdx.x == 0) mbar_arrive(s_seen);
         tc_fence_after();
         float e[2][32];
         {
@@ -988,14 +1036,16 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   }
   Params a;
   a.p = p;
-  plan(a, p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.q.h != 0 && p.dout.h != 0);
+  plan(a, p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.q.h != 0 && p.dout.h != 0 && p.o.h != 0);
   a.dq32 = wide(p.dq); a.dk32 = wide(p.dk); a.dv32 = wide(p.dv);
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
   const int rows = a.heads > 1 ? p.Nq : BM;
   if (!heads_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.dout, p.dout, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
-      !heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, BN, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, BN, 1))
+      !heads_map(&a.o, p.o, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
+      !heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, BN, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, BN, 1) ||
+      !heads_map(&a.dq, p.dq, p.B, p.Hq, p.Nq, p.d, 32, 1))
     return cudaErrorInvalidValue;
   const int sms = sm_count();
   const dim3 gq(a.items < sms ? a.items : sms), gk(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 2, JOIN_PARTS);
