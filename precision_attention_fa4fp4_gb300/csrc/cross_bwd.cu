@@ -14,11 +14,13 @@
 // 64 rows); a key tile is 128 keys.
 //
 // cross_dq_kernel: persistent, a query tile at a time.  Warps 0-7: a thread per
-//   row and half of the keys: P from S while dP runs, dS as bf16 into tensor memory
-//   (the A operand of dQ).  S of the next key tile runs as soon as S has been read.
-//   D is summed by the same threads from the o and dO tiles, and kept in the
-//   workspace; dQ leaves through the dO tile's place.  Two warps issue the products:
-//   S; dP and dQ.
+//   row and half of the keys: P from S, dS from P and dP, as bf16 into tensor memory
+//   (the A operand of dQ).  Q is in tensor memory too (the A operand of S), so that its
+//   place in shared memory takes the next item's Q, then this one's dQ on its way
+//   out, and K and V have room to be two steps ahead.  S and dP of the next key tile
+//   run as soon as these have been read.  D is summed by the same threads from the o
+//   and dO tiles, and kept in the workspace.  Two warps issue the products: S; dP and
+//   dQ.
 // cross_dkv_kernel: persistent over the steps (key tile, query tile), cut into
 //   equal ranges.  Rows are keys: P^T and dS^T go over S^T and dP^T as A operands of
 //   dV and dK, which are summed in tensor memory (512 columns in all).  Two warps
@@ -93,11 +95,11 @@ FA4_DEV void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float f, bool 
 template <int D>
 struct SmemQ {
   static constexpr int TILE = (D / 64) * CH;
-  static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
-  static constexpr int OFF_Q = 0, OFF_KV = QS * TILE;
+  static constexpr int KS = D == 128 ? 5 : 8;
+  static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_KV = 2 * TILE;
   static constexpr int OFF_DEL = OFF_KV + KS * TILE;        // [2 items][2 halves][128]: shares of D
   static constexpr int OFF_BAR = OFF_DEL + 2 * 1024;
-  static constexpr int NBAR = 2 * QS + 2 * KS + 6;
+  static constexpr int NBAR = 2 * KS + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -135,8 +137,8 @@ struct WalkQ {
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_constant__ Params a) {
   using L = SmemQ<D>;
-  constexpr int QS = L::QS, KS = L::KS;
-  constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DS = 384;
+  constexpr int KS = L::KS;
+  constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DS = 384, COL_Q = 448;
   const CrossParams& p = a.p;
   // (no room to align it by hand: nothing else is in shared memory, so it begins on its alignment)
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -145,27 +147,39 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     return;
   }
   float* shares = reinterpret_cast<float*>(smem + L::OFF_DEL);
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_empty = q_full + QS;
-  uint64_t* kv_full = q_empty + QS;
+  uint8_t *q_tile = smem + L::OFF_Q, *do_tile = smem + L::OFF_DO;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* kv_empty = kv_full + KS;
-  uint64_t* s_full = kv_empty + KS;      // S is there
-  uint64_t* s_free = s_full + 1;         // S has been read, and dP is there
+  uint64_t* q_full = kv_empty + KS;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* do_full = q_empty + 1;
+  uint64_t* do_empty = do_full + 1;
+  uint64_t* qt_full = do_empty + 1;      // Q is in tensor memory
+  uint64_t* s_full = qt_full + 1;        // S is there
+  uint64_t* s_free = s_full + 1;         // S has been read
   uint64_t* dp_full = s_free + 1;        // dP is there
-  uint64_t* ds_full = dp_full + 1;       // dS is there, dP has been read
-  uint64_t* dq_done = ds_full + 1;       // the item's dQ is there
+  uint64_t* dp_free = dp_full + 1;       // dP has been read
+  uint64_t* ds_full = dp_free + 1;       // dS is there
+  uint64_t* ds_free = ds_full + 1;       // dS has gone into dQ
+  uint64_t* dq_done = ds_free + 1;       // the item's dQ is there
   uint64_t* mma_done = dq_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 9); }
     for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 8);
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 9);
+    mbar_init(qt_full, 8);
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
     mbar_init(dp_full, 1);
+    mbar_init(dp_free, 8);
     mbar_init(ds_full, 8);
+    mbar_init(ds_free, 1);
     mbar_init(dq_done, 1);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -184,62 +198,60 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       if (lane == 0) {
         tma_prefetch_desc(&a.q.map);
         tma_prefetch_desc(&a.dout.map);
+        tma_prefetch_desc(&a.o.map);
         tma_prefetch_desc(&a.k.map);
         tma_prefetch_desc(&a.v.map);
-        int qn = 0, kn = 0;
-        auto load_q = [&](const HeadsMap& m, const ItemQ& it) -> bool {
-          const int st = qn % QS;
-          if (qn >= QS && !mbar_wait(&q_empty[st], (qn / QS - 1) & 1, abort_flag, p.err)) return false;
-          mbar_arrive_expect_tx(&q_full[st], a.box * 2 * D);
-          int g, n;
-          divide(it.tile, a.per_head, g, n);
-          const int h = it.hk * G + g * a.heads;
-          n *= BM;
-          for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_Q + st * L::TILE + c * CH, m, &q_full[st], 64 * c, n, h, it.b);
-          ++qn;
-          return true;
+        int qn = 0, dn = 0, kn = 0;          // tiles issued
+        auto load = [&](const HeadsMap& m, uint8_t* dst, uint64_t* full, int rows, int n, int h, int b) {
+          mbar_arrive_expect_tx(full, rows * 2 * D);
+          for (int c = 0; c < D / 64; ++c) tma_heads(dst + c * CH, m, full, 64 * c, n, h, b);
         };
         auto load_kv = [&](const HeadsMap& m, int rows, int n, int h, int b) -> bool {
           const int st = kn % KS;
           if (kn >= KS && !mbar_wait(&kv_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
-          mbar_arrive_expect_tx(&kv_full[st], rows * 2 * D);
-          for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_KV + st * L::TILE + c * CH, m, &kv_full[st], 64 * c, n, h, b);
+          load(m, smem + L::OFF_KV + st * L::TILE, &kv_full[st], rows, n, h, b);
           ++kn;
           return true;
         };
         WalkQ w;
         ItemQ it;
-        bool ok = true;
-        for (; ok && w.with_keys(a, it, true); w.next()) {
+        for (bool ok = true; ok && w.with_keys(a, it, true); w.next()) {
           int g, n;
           divide(it.tile, a.per_head, g, n);
-          ok = load_q(a.q, it) && load_kv(a.k, BN, 0, it.hk, it.b) && load_q(a.dout, it) &&
-               load_kv(a.o, a.box, n * BM, it.hk * G + g * a.heads, it.b) && load_kv(a.v, BN, 0, it.hk, it.b);
+          const int h = it.hk * G + g * a.heads;
+          n *= BM;
+          // Q, K_0 | dO, o, V_0 | K_1, V_1, ...: in the order of the K, V ring o, K_0, V_0, K_1, ...
+          if (qn > 0 && !mbar_wait(q_empty, (qn - 1) & 1, abort_flag, p.err)) break;
+          load(a.q, q_tile, q_full, a.box, n, h, it.b);
+          ++qn;
+          if (!load_kv(a.o, a.box, n, h, it.b) || !load_kv(a.k, BN, 0, it.hk, it.b)) break;
+          if (dn > 0 && !mbar_wait(do_empty, (dn - 1) & 1, abort_flag, p.err)) break;
+          load(a.dout, do_tile, do_full, a.box, n, h, it.b);
+          ++dn;
+          ok = load_kv(a.v, BN, 0, it.hk, it.b);
           for (int j = 1; ok && j < it.nt; ++j)
             ok = load_kv(a.k, BN, j * BN, it.hk, it.b) && load_kv(a.v, BN, j * BN, it.hk, it.b);
         }
         if (*abort_flag) {
           volatile int no_abort = 0;
-          for (int i = max(0, qn - QS); i < qn; ++i) mbar_wait(&q_full[i % QS], (i / QS) & 1, &no_abort, p.err);
+          if (qn > 0) mbar_wait(q_full, (qn - 1) & 1, &no_abort, p.err);
+          if (dn > 0) mbar_wait(do_full, (dn - 1) & 1, &no_abort, p.err);
           for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait(&kv_full[i % KS], (i / KS) & 1, &no_abort, p.err);
         }
       }
       __syncwarp();
     } else if (warp == W_MMA) {
-      // S of every step, once the one before has been read and dP of that step is there
+      // S of every step, once the one before has been read
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       WalkQ w;
       ItemQ it;
-      int kv = 0, q = 0, n = 0;
+      int kv = 0, n = 0;
       bool ok = true;
-      for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
-        const uint32_t sq = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
-        ok = mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
-        // (an item's tiles in the K, V ring: K_0, o, V_0, K_1, V_1, ...)
-        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += j == 1 ? 3 : 2) {
+      for (int i = 0; ok && w.with_keys(a, it, false); w.next(), ++i) {
+        ok = mbar_wait(qt_full, i & 1, abort_flag, p.err);
+        ++kv;                              // (o)
+        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += 2) {
           ok = mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err) &&
                (n == 0 || mbar_wait(s_free, (n - 1) & 1, abort_flag, p.err));
           if (!ok) break;
@@ -247,10 +259,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           uint8_t* k = smem + L::OFF_KV + kv % KS * L::TILE;
           if (it.len - j * BN < BN && it.len < p.Nk) clear_rows<D>(k, it.len - j * BN, lane);
           tc_fence_after();
+          const uint32_t b = desc_rows(smem_u32(k));
           if (leader) {
-            product_rows<D>(tbase + COL_S, sq, smem_u32(k), idesc_s);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              mma_ts(tbase + COL_S, tbase + COL_Q + 8 * x, b + (((x / 4) * CH + (x % 4) * 32) >> 4), idesc_s, x > 0);
             mma_commit(s_full);
-            if (j == it.nt - 1) mma_commit(&q_empty[q % QS]);
           }
           __syncwarp();
         }
@@ -261,21 +275,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       mbar_wait(mma_done, 0, &no_abort, p.err);
       __syncwarp();
     } else if (warp == W_MMA_B) {
-      // dP of every step; dQ of the step before it first
+      // dP of every step, once the one before has been read; then dQ of that one
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_q = idesc_f16(BM, D, true, false, true);
+      const uint32_t sdo = smem_u32(do_tile);
       WalkQ w;
       ItemQ it;
-      int k = 0, k_before = 0, q = 1, n = 0;   // K of this step and of the one before it
+      int k = 0, k_before = 0, n = 0;      // K of this step and of the one before it
       bool ok = true, add = false;
-      // dQ += dS K of step n - 1, whose K is at ring position k; last: of its item
-      auto issue_dq = [&](int k, bool last) -> bool {
-        if (!mbar_wait(ds_full, (n - 1) & 1, abort_flag, p.err)) return false;
+      // dQ += dS K of step m, whose K is at ring position k; last: of its item
+      auto issue_dq = [&](int m, int k, bool last) -> bool {
+        if (!mbar_wait(ds_full, m & 1, abort_flag, p.err)) return false;
         tc_fence_after();
         const uint32_t sk = smem_u32(smem + L::OFF_KV + k % KS * L::TILE);
         if (leader) {
           product_cols(tbase + COL_DQ, tbase + COL_DS, tbase + COL_DS + 32, sk, idesc_q, add);
+          mma_commit(ds_free);
           mma_commit(&kv_empty[k % KS]);
           if (last) mma_commit(dq_done);
         }
@@ -283,12 +299,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         add = !last;
         return true;
       };
-      for (; ok && w.with_keys(a, it, false); w.next(), q += 2) {
-        const uint32_t sdo = smem_u32(smem + L::OFF_Q + q % QS * L::TILE);
+      for (int i = 0; ok && w.with_keys(a, it, false); w.next(), ++i) {
         for (int j = 0; ok && j < it.nt; ++j) {
-          const int v = k + (j == 0 ? 2 : 1);
-          if (n > 0) ok = issue_dq(k_before, j == 0);
-          if (j == 0) ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err);
+          if (j == 0) ++k;                 // (o)
+          const int v = k + 1;
+          if (j == 0 && n > 0) ok = issue_dq(n - 1, k_before, true);
+          if (n > 0) ok = ok && mbar_wait(dp_free, (n - 1) & 1, abort_flag, p.err);
+          if (j == 0) ok = ok && mbar_wait(do_full, i & 1, abort_flag, p.err);
           ok = ok && mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
@@ -297,15 +314,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
             product_rows<D>(tbase + COL_DP, sdo, sv, idesc_s);
             mma_commit(dp_full);
             mma_commit(&kv_empty[v % KS]);
-            if (j == it.nt - 1) mma_commit(&q_empty[q % QS]);
+            if (j == it.nt - 1) mma_commit(do_empty);
           }
           __syncwarp();
+          if (j > 0) ok = issue_dq(n - 1, k_before, false);
           ++n;
           k_before = k;
           k = v + 1;
         }
       }
-      if (ok && n > 0) issue_dq(k_before, true);
+      if (ok && n > 0) issue_dq(n - 1, k_before, true);
       if (leader) mma_commit(mma_done);
       __syncwarp();
       volatile int no_abort = 0;
@@ -317,13 +335,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     const int half = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
-    int n = 0, items = 0;                  // key tiles, items with keys so far
-    bool ok = true;
+    int n = 0, items = 0;                  // key tiles, items so far
+    int kv = 0;                            // ring position of the item's o
+    bool ok = true, leaving = false;       // leaving: a dQ is on its way out of shared memory
     WalkQ w;
     ItemQ it;
-    int kv = 0;                            // ring position of the item's K_0
-    bool leaving = false;                  // a dQ is on its way out of shared memory
-    // an item's row: its lse is on its way while the item before ends
+    if (p.lens)                            // queries without a key
+      for (; w.at(a, it, false); w.next()) {
+        int g, row;
+        tile_row(a, it.tile, r, G, g, row);
+        if (it.nt > 0 || g >= G) continue;
+        uint4* dst = reinterpret_cast<uint4*>(at(p.dq, it.b, it.hk * G + g, row) + half * (D / 2));
+        for (int i = 0; i < D / 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+    w = WalkQ();
+    // the item's row and its lse
     bool valid = false;
     int h = 0, row = 0;
     float lse = INFINITY;
@@ -334,48 +360,64 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       h = x.hk * G + g;
       lse = valid ? p.lse[((long long)x.b * p.Hq + h) * p.Nq + row] : INFINITY;
     };
-    bool more = w.at(a, it, false);
-    if (more) fetch(it);
+    // this half of the item's Q row into tensor memory
+    auto take_q = [&](int i) -> bool {
+      if (!mbar_wait(q_full, i & 1, abort_flag, p.err)) return false;
+      uint32_t v[D / 4];
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const uint4 u = *tile_word(q_tile, r, half * (D / 16) + x);
+        v[4 * x] = u.x; v[4 * x + 1] = u.y; v[4 * x + 2] = u.z; v[4 * x + 3] = u.w;
+      }
+      if constexpr (D == 128) tmem_st32(lane_base + COL_Q + 32 * half, v);
+      else tmem_st16(lane_base + COL_Q + 16 * half, v);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qt_full);
+      return true;
+    };
+    bool more = w.with_keys(a, it, false);
+    if (more) {
+      fetch(it);
+      ok = take_q(0);
+      if (lane == 0) mbar_arrive(q_empty);
+    }
+    // (A warp whose wait ran out still meets the others at the barriers.)
     while (more) {
+      // D: this half's share from the o and dO tiles, then both halves'
       float del = 0.f, z = INFINITY;       // (a row without keys: P = 2^-inf = 0)
       if (lse > -INFINITY) z = lse * L2E;
-      const int q = 2 * items, o = kv + 1;
-      uint8_t* tile = smem + L::OFF_Q + (q + 1) % QS * L::TILE;      // dO, in the end dQ
-      if (it.nt > 0) {
-        // D: this half's share from the o and dO tiles, then both halves'.  (A warp whose wait ran out still meets the
-        // others at the barriers.)
-        ok = ok && mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err) &&
-             mbar_wait(&q_full[(q + 1) % QS], ((q + 1) / QS) & 1, abort_flag, p.err) &&
-             mbar_wait(&kv_full[o % KS], (o / KS) & 1, abort_flag, p.err);
-        if (ok) {
-          uint8_t* ot = smem + L::OFF_KV + o % KS * L::TILE;
+      ok = ok && mbar_wait(do_full, items & 1, abort_flag, p.err) &&
+           mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err);
+      if (ok) {
+        uint8_t* ot = smem + L::OFF_KV + kv % KS * L::TILE;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const int x = half * (D / 16) + i;
-            const uint4 u = *tile_word(ot, r, x), y = *tile_word(tile, r, x);
-            const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int i = 0; i < D / 16; ++i) {
+          const int x = half * (D / 16) + i;
+          const uint4 u = *tile_word(ot, r, x), y = *tile_word(do_tile, r, x);
+          const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              del = fmaf(__uint_as_float(uw[e] << 16), __uint_as_float(yw[e] << 16), del);
-              del = fmaf(__uint_as_float(uw[e] & 0xffff0000u), __uint_as_float(yw[e] & 0xffff0000u), del);
-            }
+          for (int e = 0; e < 4; ++e) {
+            del = fmaf(__uint_as_float(uw[e] << 16), __uint_as_float(yw[e] << 16), del);
+            del = fmaf(__uint_as_float(uw[e] & 0xffff0000u), __uint_as_float(yw[e] & 0xffff0000u), del);
           }
         }
-        float* mine = shares + (items & 1) * 256;
-        mine[half * 128 + r] = del;
-        named_bar(1, 256);
-        del += mine[(half ^ 1) * 128 + r];
-        if (lane == 0) {
-          mbar_arrive(&q_empty[q % QS]);
-          if (leaving) {                   // the dQ before this one has left the dO tile before this one
-            bulk_wait_read0();
-            mbar_arrive(&q_empty[(q - 1) % QS]);
-          }
-        }
-        if (threadIdx.x == 0) mbar_arrive(&kv_empty[o % KS]);
-        if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
-        kv += 2 * it.nt + 1;
       }
+      float* mine = shares + (items & 1) * 256;
+      mine[half * 128 + r] = del;
+      named_bar(1, 256);
+      del += mine[(half ^ 1) * 128 + r];
+      if (lane == 0) {
+        mbar_arrive(do_empty);
+        if (leaving) {                     // the dQ before this one has left the place of Q
+          bulk_wait_read0();
+          mbar_arrive(q_empty);
+        }
+      }
+      if (threadIdx.x == 0) mbar_arrive(&kv_empty[kv % KS]);
+      if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
+      kv += 2 * it.nt + 1;
       for (int j = 0; ok && j < it.nt; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
@@ -388,16 +430,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           reg_fence32(v[0]);
           reg_fence32(v[1]);
           tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 32; ++i) e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -z));
         }
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
-        // the next S may run from here on, not before: products of two warps share the tensor cores, and dP is what
-        // these threads wait for (S runs while they form dS)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
         tc_fence_after();
         const int keep = it.len - j * BN - 64 * half;
         uint32_t pk[32];
@@ -408,6 +448,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           tmem_ld_wait();
           reg_fence32(v[0]);
           reg_fence32(v[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dp_free);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -422,29 +465,30 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) pk[i] = pack2(e[i / 16][2 * (i % 16)], e[i / 16][2 * (i % 16) + 1]);
+        if (n >= 1 && !mbar_wait(ds_free, (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
         tmem_st32(lane_base + COL_DS + 32 * half, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      // the next item's lse sets out before this one's dQ is awaited
+      // the next item's Q goes into tensor memory before this one's dQ is awaited, and dQ then into Q's place
       const ItemQ was = it;
       const bool here = valid;
       __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
       w.next();
-      more = w.at(a, it, false);
-      if (more) fetch(it);
-      if (was.nt == 0) {
-        if (here)
-          for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-        continue;
+      more = w.with_keys(a, it, false);
+      if (more) {
+        fetch(it);
+        ok = ok && take_q(items + 1);
       }
+      named_bar(1, 256);
       ok = ok && mbar_wait(dq_done, items & 1, abort_flag, p.err);
       ++items;
       if (ok) {
         tc_fence_after();
-        // rows by themselves would be 32 places a store: they go through the dO tile's place to boxes of 32 rows
+        // (rows by themselves would be 32 places a store: they leave in boxes of 32 rows)
 #pragma unroll
         for (int q = 0; q < D / 64; ++q) {
           uint32_t v[32];
@@ -461,7 +505,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 pk[i] = pack2(__uint_as_float(v[8 * e + 2 * i]) * f, __uint_as_float(v[8 * e + 2 * i + 1]) * f);
-              *tile_word(tile, r, half * (D / 16) + 4 * q + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *tile_word(q_tile, r, half * (D / 16) + 4 * q + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
         }
@@ -471,11 +515,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       __syncwarp();
       if (D == 64) named_bar(2 + quad, 64);          // both halves of a row are in one box
       if (lane == 0) {
-        int g, n;
-        divide(was.tile, a.per_head, g, n);
-        n = n * BM + 32 * quad;
-        if (ok && a.heads == 1 && n < p.Nq && (D == 128 || half == 0)) {
-          tma_heads_store(a.dq, tile + (D == 128 ? half * CH : 0) + quad * 32 * 128, D == 128 ? 64 * half : 0, n,
+        int g, m;
+        divide(was.tile, a.per_head, g, m);
+        m = m * BM + 32 * quad;
+        if (ok && a.heads == 1 && m < p.Nq && (D == 128 || half == 0)) {
+          tma_heads_store(a.dq, q_tile + (D == 128 ? half * CH : 0) + quad * 32 * 128, D == 128 ? 64 * half : 0, m,
                           was.hk * G + g, was.b);
           bulk_commit();
         }
