@@ -3,14 +3,9 @@
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "cross.h"
+#include "divide.cuh"
 
 namespace fa4 {
-
-FA4_DEV int divide(int n, const Divisor& by) { return (int)((__umulhi((uint32_t)n, by.m) + (uint32_t)n) >> by.s); }
-FA4_DEV void divide(int n, const Divisor& by, int& q, int& r) {
-  q = divide(n, by);
-  r = n - q * by.d;
-}
 
 // Row (b, h, n) of a strided tensor.
 FA4_DEV __nv_bfloat16* at(const Strided& t, int b, int h, int n) {

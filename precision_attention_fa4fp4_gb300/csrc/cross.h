@@ -9,17 +9,6 @@
 
 namespace fa4 {
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1: (umulhi(n, m) + n) >> s.
-struct Divisor {
-  uint32_t m = 0;
-  int s = 0, d = 1;
-  Divisor() = default;
-  explicit Divisor(int d_) : d(d_) {
-    while ((1ll << s) < d) ++s;
-    m = (uint32_t)((((1ull << s) - (uint64_t)d) << 32) / (uint64_t)d + 1);
-  }
-};
-
 struct CrossParams {
   Strided q, k, v, o, dout, dq, dk, dv;   // the last four: backward only
   float* lse;                             // [B][Hq][Nq]; nullable forward

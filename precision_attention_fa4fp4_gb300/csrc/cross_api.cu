@@ -44,7 +44,7 @@ fa4fp4_status check_dims(int B, int Hq, int Hkv, int N, int d) {
   if (B < 0 || Hq < 0 || Hkv < 0 || N < 0) return FA4FP4_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA4FP4_ERR_UNSUPPORTED;
   // (sums of) head counts and token counts stay within 32 bits
-  if (Hq > (1 << 20) || Hkv > (1 << 20) || (long long)B * N > (1LL << 31) - 1) return FA4FP4_ERR_UNSUPPORTED;
+  if (Hq > (1 << 20) || Hkv > (1 << 20) || (long long)B * N > (1LL << 30)) return FA4FP4_ERR_UNSUPPORTED;
   if ((long long)B * N * (Hq + Hkv) > (1LL << 40)) return FA4FP4_ERR_UNSUPPORTED;
   return FA4FP4_OK;
 }

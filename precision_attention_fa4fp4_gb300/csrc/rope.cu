@@ -22,6 +22,7 @@
 // there).  The native sine and cosine are off by 2^-21 there, against bf16's 2^-9.
 #include <cuda_bf16.h>
 #include "common.cuh"
+#include "divide.cuh"
 #include <type_traits>
 #include "rope.h"
 
@@ -30,18 +31,19 @@ namespace {
 
 constexpr int WARPS = 8;
 
-// Two 16-byte words of bf16 -> first and second channels of 8 pairs.
+// Two 16-byte words of bf16 -> first and second channels of 8 pairs, two pairs to
+// a float2 (packed FP32 arithmetic: an instruction for two).
 template <bool PAIRS>
-FA4_DEV void unpack(const uint4& u, const uint4& v, float (&a)[8], float (&b)[8]) {
+FA4_DEV void unpack(const uint4& u, const uint4& v, float2 (&a)[4], float2 (&b)[4]) {
   const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
     if (PAIRS) {
-      a[i] = lo; b[i] = hi;
+      a[i] = make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+      b[i] = make_float2(__uint_as_float(w[2 * i] & 0xffff0000u), __uint_as_float(w[2 * i + 1] & 0xffff0000u));
     } else {
-      (i < 4 ? a : b)[(2 * i) & 7] = lo;
-      (i < 4 ? a : b)[(2 * i + 1) & 7] = hi;
+      a[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      b[i] = make_float2(__uint_as_float(w[4 + i] << 16), __uint_as_float(w[4 + i] & 0xffff0000u));
     }
   }
 }
@@ -52,16 +54,33 @@ FA4_DEV uint32_t pack2(float lo, float hi) {
 }
 
 template <bool PAIRS>
-FA4_DEV void pack(const float (&a)[8], const float (&b)[8], uint4& u, uint4& v) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (PAIRS) w[i] = pack2(a[i], b[i]);
-    else w[i] = i < 4 ? pack2(a[2 * i], a[2 * i + 1]) : pack2(b[2 * i - 8], b[2 * i - 7]);
+FA4_DEV void pack(const float2 (&a)[4], const float2 (&b)[4], uint4& u, uint4& v) {
+  if (PAIRS) {
+    u = make_uint4(pack2(a[0].x, b[0].x), pack2(a[0].y, b[0].y), pack2(a[1].x, b[1].x), pack2(a[1].y, b[1].y));
+    v = make_uint4(pack2(a[2].x, b[2].x), pack2(a[2].y, b[2].y), pack2(a[3].x, b[3].x), pack2(a[3].y, b[3].y));
+  } else {
+    u = make_uint4(pack2(a[0].x, a[0].y), pack2(a[1].x, a[1].y), pack2(a[2].x, a[2].y), pack2(a[3].x, a[3].y));
+    v = make_uint4(pack2(b[0].x, b[0].y), pack2(b[1].x, b[1].y), pack2(b[2].x, b[2].y), pack2(b[3].x, b[3].y));
   }
-  u = make_uint4(w[0], w[1], w[2], w[3]);
-  v = make_uint4(w[4], w[5], w[6], w[7]);
 }
+
+// 16 FP32 values of a lane's channels, laid out as a row's: the same.
+template <bool PAIRS>
+FA4_DEV void unpack(const float4 (&f)[4], float2 (&a)[4], float2 (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (PAIRS) {
+      a[i] = make_float2(f[i].x, f[i].z);
+      b[i] = make_float2(f[i].y, f[i].w);
+    } else {
+      a[i] = i % 2 ? make_float2(f[i / 2].z, f[i / 2].w) : make_float2(f[i / 2].x, f[i / 2].y);
+      b[i] = i % 2 ? make_float2(f[2 + i / 2].z, f[2 + i / 2].w) : make_float2(f[2 + i / 2].x, f[2 + i / 2].y);
+    }
+  }
+}
+
+FA4_DEV float2 both(float x) { return make_float2(x, x); }
+FA4_DEV float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
 // Where a lane's two words of a row start, in channels.
 template <int D, bool PAIRS>
@@ -70,11 +89,11 @@ template <int D, bool PAIRS>
 FA4_DEV int word1(int l) { return PAIRS ? 16 * l + 8 : D / 2 + 8 * l; }
 
 // Sines and cosines of a lane's 8 pairs at one token.
-FA4_DEV void angles(const RopeParams& p, const uint64_t* turn, const uint8_t* axis, int b, int n, int l, float (&c)[8],
-                    float (&s)[8]) {
+FA4_DEV void angles(const RopeParams& p, const uint64_t* turn, const uint8_t* axis, int b, int n, int l,
+                    float2 (&c)[4], float2 (&s)[4]) {
   if (!p.pos) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
+    for (int i = 0; i < 4; ++i) { c[i] = both(1.f); s[i] = both(0.f); }
     return;
   }
   const int* at = p.pos + b * p.pos_b + n;
@@ -83,8 +102,8 @@ FA4_DEV void angles(const RopeParams& p, const uint64_t* turn, const uint8_t* ax
     const int64_t where = __ldg(at + (long long)axis[8 * l + i] * p.N);
     const int rest = (int)(((uint64_t)where * turn[8 * l + i]) >> 32);   // of a turn, times 2^32
     const float th = (float)rest * 1.46291807926715968e-9f;              // 2 pi / 2^32
-    c[i] = __cosf(th);
-    s[i] = __sinf(th);
+    (i % 2 ? c[i / 2].y : c[i / 2].x) = __cosf(th);
+    (i % 2 ? s[i / 2].y : s[i / 2].x) = __sinf(th);
   }
 }
 
@@ -112,31 +131,39 @@ struct Tables {
     }
     __syncthreads();
   }
+  // the weights of a lane's channels, which begin at c0 and c1
+  template <bool PAIRS>
+  FA4_DEV void weights(int t, int c0, int c1, float2 (&a)[4], float2 (&b)[4]) const {
+    const float4 f[4] = {*reinterpret_cast<const float4*>(&w[t][c0]), *reinterpret_cast<const float4*>(&w[t][c0 + 4]),
+                         *reinterpret_cast<const float4*>(&w[t][c1]), *reinterpret_cast<const float4*>(&w[t][c1 + 4])};
+    unpack<PAIRS>(f, a, b);
+  }
 };
 
 
-// U rows of a lane group are on their way at a time.
+// U rows of a lane group are on their way at a time: 3, with 3 CTAs on a
+// multiprocessor and as many in the grid (24 + 24 heads of 32760 tokens: 134 us, 0.90
+// of measured HBM; 4 rows and 2 CTAs 144, 2 and 4 150; a CTA for every 8 tokens 145).
+constexpr int FWD_CTAS = 3;
 template <int D, bool PAIRS, int U>
-__global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const __grid_constant__ RopeParams p, int chunk, int nq,
-                                                               int nk) {
+__global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
+    norm_rope_kernel(const __grid_constant__ RopeParams p, int chunk, int nq, int nk, Divisor by_tokens, Divisor by_n) {
   constexpr int LANES = D / 16, ROWS = 32 / LANES;
   __shared__ Tables<D> tab;
   tab.load(p);
   const int lane = threadIdx.x % 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
-  const long long tokens = (long long)p.B * p.N;
-  const long long tasks = tokens * (nq + nk);
-  for (long long task = (long long)blockIdx.x * WARPS + threadIdx.x / 32; task < tasks;
-       task += (long long)gridDim.x * WARPS) {
-    const int part = (int)(task / tokens);
-    const long long m = task % tokens;
-    const int b = (int)(m / p.N), n = (int)(m % p.N);
+  const int tasks = by_tokens.d * (nq + nk);
+  for (int task = blockIdx.x * WARPS + threadIdx.x / 32; task < tasks; task += gridDim.x * WARPS) {
+    int part, m, b, n;
+    divide(task, by_tokens, part, m);
+    divide(m, by_n, b, n);
     const int t = part >= nq;
     const RopeTensor& T = p.t[t];
     const int h0 = (t ? part - nq : part) * chunk, h1 = min(T.H, h0 + chunk);
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(T.out.p) + b * T.out.b + n * T.out.n;
-    float c[8], s[8];
+    float2 c[4], s[4], wa[4], wb[4];
     bool first = true;
     for (int h = h0 + sub; h - sub < h1; h += ROWS * U) {
       uint4 u[U], v[U];
@@ -149,25 +176,28 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const __grid_cons
           v[i] = *reinterpret_cast<const uint4*>(row + c1);
         }
       }
-      if (first) angles(p, tab.turn, tab.axis, b, n, l, c, s);
-      first = false;
+      if (first) {
+        angles(p, tab.turn, tab.axis, b, n, l, c, s);
+        tab.template weights<PAIRS>(t, c0, c1, wa, wb);
+        first = false;
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        float fa[8], fb[8];
+        float2 fa[4], fb[4];
         unpack<PAIRS>(u[i], v[i], fa, fb);
         float r = 1.f;
         if (p.norm) {
-          float q = 0.f;
+          float2 q = fmul2(fa[0], fa[0]);
+          q = ffma2(fb[0], fb[0], q);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], q));
-          r = rsqrtf(row_sum<LANES>(q) * (1.f / D) + p.eps);
+          for (int j = 1; j < 4; ++j) q = ffma2(fb[j], fb[j], ffma2(fa[j], fa[j], q));
+          r = rsqrtf(row_sum<LANES>(q.x + q.y) * (1.f / D) + p.eps);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float na = fa[j] * r * tab.w[t][PAIRS ? c0 + 2 * j : c0 + j];
-          const float nb = fb[j] * r * tab.w[t][PAIRS ? c0 + 2 * j + 1 : c1 + j];
-          fa[j] = na * c[j] - nb * s[j];
-          fb[j] = nb * c[j] + na * s[j];
+        for (int j = 0; j < 4; ++j) {
+          const float2 na = fmul2(fmul2(fa[j], both(r)), wa[j]), nb = fmul2(fmul2(fb[j], both(r)), wb[j]);
+          fa[j] = ffma2(neg(nb), s[j], fmul2(na, c[j]));
+          fb[j] = ffma2(na, s[j], fmul2(nb, c[j]));
         }
         if (h + i * ROWS < h1) {
           pack<PAIRS>(fa, fb, u[i], v[i]);
@@ -182,10 +212,16 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_kernel(const __grid_cons
 
 // Gradients.  The CTAs [0, ctas[0]) work on q, the others on k; every lane adds
 // its 16 channels of the weight's gradient over its tasks, the CTA joins them in
-// a fixed order and leaves one row of partials.
+// a fixed order and leaves one row of partials.  A row's x and gradient are on their
+// way while the row before is at work.  2 CTAs on a multiprocessor: a lane's sums,
+// weights, sines and cosines and two rows take 128 registers (at 85, for 3 CTAs, they
+// spill: 132 -> 210 us for 2 x 8192 tokens of 32 + 8 heads with f32 gradients; rows
+// ahead by asynchronous copies to shared memory 157).
+constexpr int BWD_CTAS = 2;
 template <int D, bool PAIRS, bool F32>
-__global__ void __launch_bounds__(WARPS * 32) norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, int chunk,
-                                                                   int nq, int nk) {
+__global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
+    norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, int chunk, int nq, int nk, Divisor by_tokens,
+                         Divisor by_n) {
   constexpr int LANES = D / 16, ROWS = 32 / LANES;
   __shared__ Tables<D> tab;
   __shared__ float join[WARPS][D];
@@ -195,102 +231,97 @@ __global__ void __launch_bounds__(WARPS * 32) norm_rope_bwd_kernel(const __grid_
   const int t = (int)blockIdx.x >= p.ctas[0];
   const int cta = t ? (int)blockIdx.x - p.ctas[0] : (int)blockIdx.x;
   const RopeTensor& T = p.t[t];
-  const long long tokens = (long long)p.B * p.N;
-  const long long tasks = tokens * (t ? nk : nq);
-  float da[8], db[8];
+  const int tasks = by_tokens.d * (t ? nk : nq);
+  float2 da[4], db[4], wa[4], wb[4];
+  tab.template weights<PAIRS>(t, c0, c1, wa, wb);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) da[j] = db[j] = 0.f;
-  for (long long task = (long long)cta * WARPS + warp; task < tasks; task += (long long)p.ctas[t] * WARPS) {
-    const long long m = task % tokens;
-    const int b = (int)(m / p.N), n = (int)(m % p.N);
-    const int h0 = (int)(task / tokens) * chunk, h1 = min(T.H, h0 + chunk);
+  for (int j = 0; j < 4; ++j) da[j] = db[j] = both(0.f);
+  for (int task = cta * WARPS + warp; task < tasks; task += p.ctas[t] * WARPS) {
+    int part, m, b, n;
+    divide(task, by_tokens, part, m);
+    divide(m, by_n, b, n);
+    const int h0 = part * chunk, h1 = min(T.H, h0 + chunk);
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;
     const long long dy = b * T.dy.b + n * T.dy.n;
     __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(T.out.p) + b * T.out.b + n * T.out.n;
-    float c[8], s[8];
+    float2 c[4], s[4];
+    uint4 u, v;
+    float4 g[F32 ? 4 : 2];
+    auto fetch = [&](int h) {
+      u = v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < (F32 ? 4 : 2); ++i) g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h >= h1) return;
+      const __nv_bfloat16* row = x + h * T.x.h;
+      u = *reinterpret_cast<const uint4*>(row + c0);
+      v = *reinterpret_cast<const uint4*>(row + c1);
+      if (F32) {
+        const float* from = static_cast<const float*>(T.dy.p) + dy + h * T.dy.h;
+        g[0] = *reinterpret_cast<const float4*>(from + c0);
+        g[1] = *reinterpret_cast<const float4*>(from + c0 + 4);
+        g[F32 ? 2 : 0] = *reinterpret_cast<const float4*>(from + c1);
+        g[F32 ? 3 : 0] = *reinterpret_cast<const float4*>(from + c1 + 4);
+      } else {
+        const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(T.dy.p) + dy + h * T.dy.h;
+        g[0] = *reinterpret_cast<const float4*>(from + c0);
+        g[1] = *reinterpret_cast<const float4*>(from + c1);
+      }
+    };
+    fetch(h0 + sub);
     angles(p, tab.turn, tab.axis, b, n, l, c, s);
     for (int h = h0 + sub; h - sub < h1; h += ROWS) {
       const bool on = h < h1;
-      uint4 u = make_uint4(0, 0, 0, 0), v = u;
-      float ga[8], gb[8], fa[8], fb[8];
-      if (on) {
-        const __nv_bfloat16* row = x + h * T.x.h;
-        u = *reinterpret_cast<const uint4*>(row + c0);
-        v = *reinterpret_cast<const uint4*>(row + c1);
-      }
-      if (F32) {
-        float4 g[4] = {};
-        if (on) {
-          const float* row = static_cast<const float*>(T.dy.p) + dy + h * T.dy.h;
-          g[0] = *reinterpret_cast<const float4*>(row + c0);
-          g[1] = *reinterpret_cast<const float4*>(row + c0 + 4);
-          g[2] = *reinterpret_cast<const float4*>(row + c1);
-          g[3] = *reinterpret_cast<const float4*>(row + c1 + 4);
-        }
-        const float f[16] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w,
-                             g[2].x, g[2].y, g[2].z, g[2].w, g[3].x, g[3].y, g[3].z, g[3].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ga[j] = PAIRS ? f[2 * j] : f[j];
-          gb[j] = PAIRS ? f[2 * j + 1] : f[8 + j];
-        }
-      } else {
-        uint4 gu = make_uint4(0, 0, 0, 0), gv = gu;
-        if (on) {
-          const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(T.dy.p) + dy + h * T.dy.h;
-          gu = *reinterpret_cast<const uint4*>(row + c0);
-          gv = *reinterpret_cast<const uint4*>(row + c1);
-        }
-        unpack<PAIRS>(gu, gv, ga, gb);
-      }
+      float2 ga[4], gb[4], fa[4], fb[4];
       unpack<PAIRS>(u, v, fa, fb);
-      float xx = 0.f, ux = 0.f;
+      if constexpr (F32) unpack<PAIRS>(g, ga, gb);
+      else unpack<PAIRS>(*reinterpret_cast<const uint4*>(&g[0]), *reinterpret_cast<const uint4*>(&g[1]), ga, gb);
+      fetch(h + ROWS);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = ga[j] * c[j] + gb[j] * s[j], e = gb[j] * c[j] - ga[j] * s[j];
-        ga[j] = a;
-        gb[j] = e;
+      for (int j = 0; j < 4; ++j) {
+        const float2 e = ga[j];
+        ga[j] = ffma2(gb[j], s[j], fmul2(e, c[j]));
+        gb[j] = ffma2(neg(e), s[j], fmul2(gb[j], c[j]));
       }
       if (p.norm) {
+        float2 xx = both(0.f), ux = both(0.f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wa = tab.w[t][PAIRS ? c0 + 2 * j : c0 + j], wb = tab.w[t][PAIRS ? c0 + 2 * j + 1 : c1 + j];
-          xx = fmaf(fa[j], fa[j], fmaf(fb[j], fb[j], xx));
-          ux = fmaf(ga[j] * wa, fa[j], fmaf(gb[j] * wb, fb[j], ux));
+        for (int j = 0; j < 4; ++j) {
+          xx = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], xx));
+          ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
         }
-        xx = row_sum<LANES>(xx);
-        ux = row_sum<LANES>(ux);
+        const float sx = row_sum<LANES>(xx.x + xx.y), su = row_sum<LANES>(ux.x + ux.y);
         // rows that are not there add nothing (with eps = 0 their r is infinite)
-        const float r = on ? rsqrtf(xx * (1.f / D) + p.eps) : 0.f;
-        const float k = r * r * ux * (1.f / D);
+        const float r = on ? rsqrtf(sx * (1.f / D) + p.eps) : 0.f;
+        const float k = r * r * su * (1.f / D);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wa = tab.w[t][PAIRS ? c0 + 2 * j : c0 + j], wb = tab.w[t][PAIRS ? c0 + 2 * j + 1 : c1 + j];
-          da[j] = fmaf(ga[j], fa[j] * r, da[j]);
-          db[j] = fmaf(gb[j], fb[j] * r, db[j]);
-          ga[j] = r * (ga[j] * wa - fa[j] * k);
-          gb[j] = r * (gb[j] * wb - fb[j] * k);
+        for (int j = 0; j < 4; ++j) {
+          da[j] = ffma2(ga[j], fmul2(fa[j], both(r)), da[j]);
+          db[j] = ffma2(gb[j], fmul2(fb[j], both(r)), db[j]);
+          ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
+          gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
         }
       }
       if (on) {
-        pack<PAIRS>(ga, gb, u, v);
+        uint4 yu, yv;
+        pack<PAIRS>(ga, gb, yu, yv);
         __nv_bfloat16* row = dx + h * T.out.h;
-        *reinterpret_cast<uint4*>(row + c0) = u;
-        *reinterpret_cast<uint4*>(row + c1) = v;
+        *reinterpret_cast<uint4*>(row + c0) = yu;
+        *reinterpret_cast<uint4*>(row + c1) = yv;
       }
     }
   }
   if (!T.dw) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
+    float ya = j % 2 ? da[j / 2].y : da[j / 2].x, yb = j % 2 ? db[j / 2].y : db[j / 2].x;
 #pragma unroll
     for (int o = LANES; o < 32; o *= 2) {
-      da[j] += __shfl_xor_sync(0xffffffffu, da[j], o);
-      db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+      ya += __shfl_xor_sync(0xffffffffu, ya, o);
+      yb += __shfl_xor_sync(0xffffffffu, yb, o);
     }
     if (sub == 0) {
-      join[warp][PAIRS ? c0 + 2 * j : c0 + j] = da[j];
-      join[warp][PAIRS ? c0 + 2 * j + 1 : c1 + j] = db[j];
+      join[warp][PAIRS ? c0 + 2 * j : c0 + j] = ya;
+      join[warp][PAIRS ? c0 + 2 * j + 1 : c1 + j] = yb;
     }
   }
   __syncthreads();
@@ -344,15 +375,13 @@ int parts_of(int H, int chunk) { return (H + chunk - 1) / chunk; }
 
 cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t st) {
   const int rows = 32 / (p.d / 16);
-  const long long tokens = (long long)p.B * p.N;
+  const int tokens = p.B * p.N;
   const int chunk = chunk_of(tokens, p.t[0].H > p.t[1].H ? p.t[0].H : p.t[1].H, rows);
   const int nq = parts_of(p.t[0].H, chunk), nk = parts_of(p.t[1].H, chunk);
-  const long long tasks = tokens * (nq + nk);
-  const long long need = (tasks + WARPS - 1) / WARPS;
-  const int grid = (int)(need < (1 << 30) ? need : (1 << 30));
-  auto k = p.d == 128 ? (p.pairs ? norm_rope_kernel<128, true, 4> : norm_rope_kernel<128, false, 4>)
-                      : (p.pairs ? norm_rope_kernel<64, true, 4> : norm_rope_kernel<64, false, 4>);
-  k<<<grid, WARPS * 32, 0, st>>>(p, chunk, nq, nk);
+  const int need = (int)(((long long)tokens * (nq + nk) + WARPS - 1) / WARPS), room = FWD_CTAS * sms();
+  auto k = p.d == 128 ? (p.pairs ? norm_rope_kernel<128, true, 3> : norm_rope_kernel<128, false, 3>)
+                      : (p.pairs ? norm_rope_kernel<64, true, 3> : norm_rope_kernel<64, false, 3>);
+  k<<<need < room ? need : room, WARPS * 32, 0, st>>>(p, chunk, nq, nk, Divisor(tokens), Divisor(p.N));
   return cudaGetLastError();
 }
 
@@ -360,7 +389,7 @@ void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas) {
   const int rows = 32 / (d / 16);
   const long long tokens = (long long)B * N;
   const int chunk = chunk_of(tokens, Hq > Hkv ? Hq : Hkv, rows);
-  const long long room = (long long)sms() * 4;
+  const long long room = (long long)sms() * BWD_CTAS;
   const int H[2] = {Hq, Hkv};
   for (int t = 0; t < 2; ++t) {
     const long long need = (tokens * parts_of(H[t], chunk) + WARPS - 1) / WARPS;
@@ -374,13 +403,14 @@ cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st) {
   const int rows = 32 / (p.d / 16);
   const int chunk = chunk_of((long long)p.B * p.N, p.t[0].H > p.t[1].H ? p.t[0].H : p.t[1].H, rows);
   const int nq = parts_of(p.t[0].H, chunk), nk = parts_of(p.t[1].H, chunk);
+  const Divisor by_tokens(p.B * p.N), by_n(p.N);
   auto pick = [&](auto f32) {
     constexpr bool F = decltype(f32)::value;
     return p.d == 128 ? (p.pairs ? norm_rope_bwd_kernel<128, true, F> : norm_rope_bwd_kernel<128, false, F>)
                       : (p.pairs ? norm_rope_bwd_kernel<64, true, F> : norm_rope_bwd_kernel<64, false, F>);
   };
   auto k = p.dy_f32 ? pick(std::true_type()) : pick(std::false_type());
-  k<<<p.ctas[0] + p.ctas[1], WARPS * 32, 0, st>>>(p, chunk, nq, nk);
+  k<<<p.ctas[0] + p.ctas[1], WARPS * 32, 0, st>>>(p, chunk, nq, nk, by_tokens, by_n);
   if (p.t[0].dw || p.t[1].dw) norm_rope_dw_kernel<<<2 * (p.d / 32), 256, 0, st>>>(p);
   return cudaGetLastError();
 }

@@ -13,6 +13,17 @@ struct Strided {
   long long b, h, n;
 };
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: (umulhi(n, m) + n) >> s.
+struct Divisor {
+  uint32_t m = 0;
+  int s = 0, d = 1;
+  Divisor() = default;
+  explicit Divisor(int d_) : d(d_) {
+    while ((1ll << s) < d) ++s;
+    m = (uint32_t)((((1ull << s) - (uint64_t)d) << 32) / (uint64_t)d + 1);
+  }
+};
+
 struct RopeTensor {            // q or k
   Strided x, dy, out;          // dy: backward only
   const void* w;               // norm weight [d] or nullptr
