@@ -5,19 +5,20 @@
 // the heads have up to 64 rows, as many of its query heads as fit.  A work item is two
 // neighbouring tiles A and B, which share K and V.  The CTAs take the items in turn
 // (item i goes to CTA i mod grid), so that those at work at a time read the
-// same K and V.  12 warps:
-//   warps 0-3  softmax of tile A, warps 4-7 of tile B: a thread per row.  P =
-//              2^(c s - c m) rounded to bf16 into tensor memory over S, the
-//              normalizer from P before the rounding; the reference m follows the
-//              running maximum only when that passes it by 2^8 (P stays within
-//              bf16's range and relative precision), and only then O is rescaled.
-//              Then O / l to the row's place, 32 bytes at a time.
-//   warp 8     producer: Q tiles through one ring, K and V tiles through another,
-//              ahead of the item at work.
-//   warps 9-10 issue the products of tile A and of tile B: S = Q K^T, O += P V (P
-//              from tensor memory, V MN-major).  The next S of a tile follows its
-//              P V, across items too.  (One warp for both tiles was the bound: a
-//              product takes 512 cycles, its waits, instructions and commits 600.)
+// same K and V.  16 warps in four groups:
+//   warps 0-3    softmax of tile A, warps 4-7 of tile B: a thread per row.  P =
+//                2^(c s - c m) rounded to bf16 into tensor memory over S, in two
+//                halves of the keys, so that P V sets out on the first while the second
+//                is formed; the normalizer from P before the rounding.  The reference m
+//                follows the running maximum only when that passes it by 2^8 (P stays
+//                within bf16's range and relative precision), and only then O is
+//                rescaled.
+//   warp 8       producer: Q tiles through one ring, K and V tiles through another,
+//                ahead of the item at work.
+//   warp 9       issues the products: S = Q K^T, O += P V (P from tensor memory, V
+//                MN-major).  The next S of a tile follows its P V, across items too.
+//   warps 12-15  take O / l to the rows' places, tile A's and tile B's in turn, while
+//                the softmax of the next item runs.
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).
 #include <cuda_bf16.h>
 #include "common.cuh"
@@ -28,9 +29,9 @@ namespace fa4 {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int NTHREADS = 384;
-constexpr int W_PROD = 8, W_MMA = 9, W_MMA_B = 10;
-constexpr int REG_SOFT = 208, REG_MISC = 88;   // 2 x 208 + 88 = 504 of 512
+constexpr int NTHREADS = 512;
+constexpr int W_PROD = 8, W_MMA = 9, W_OUT = 12;
+constexpr int REG_SOFT = 192, REG_MISC = 64;   // 2 x 192 + 2 x 64 = 512, the launch's
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
 constexpr float TAU = 8.f;                     // log2 units
@@ -53,10 +54,11 @@ struct Smem {
   static constexpr int TILE = (D / 64) * CH;
   static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0, OFF_KV = OFF_Q + QS * TILE;
-  static constexpr int OFF_BAR = OFF_KV + KS * TILE;
-  static constexpr int NBAR = 2 * QS + 2 * KS + 6 + 1;
+  static constexpr int OFF_SUM = OFF_KV + KS * TILE;         // float2 [2 tiles][128]: c m and l of the rows
+  static constexpr int OFF_BAR = OFF_SUM + 2 * 1024;
+  static constexpr int NBAR = 2 * QS + 2 * KS + 14 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -112,25 +114,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
   using L = Smem<D>;
   constexpr int QS = L::QS, KS = L::KS;
   const CrossParams& p = a.p;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (no room to align it by hand: nothing else is in shared memory, so it begins on its alignment)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023) {
+    atomicOr(p.err, FA4_DEVERR_TIMEOUT);
+    return;
+  }
+  float2* sums = reinterpret_cast<float2*>(smem + L::OFF_SUM);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_empty = q_full + QS;
   uint64_t* kv_full = q_empty + QS;
   uint64_t* kv_empty = kv_full + KS;
   uint64_t* s_full = kv_empty + KS;          // [X]: S_X is there
-  uint64_t* p_full = s_full + 2;             // [X]: P_X is there, O_X rescaled
-  uint64_t* o_done = p_full + 2;             // [X]: P_X V is in O_X
-  uint64_t* mma_done = o_done + 2;
+  uint64_t* p_full = s_full + 2;             // [X][half]: that half of P_X is there (the first: O_X rescaled)
+  uint64_t* o_done = p_full + 4;             // [X]: the item's O_X is there
+  uint64_t* o_free = o_done + 2;             // [X]: it has been read
+  uint64_t* l_full = o_free + 2;             // [X]: the item's c m and l are there
+  uint64_t* l_free = l_full + 2;             // [X]: they have been read
+  uint64_t* mma_done = l_free + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < QS; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
-    for (int x = 0; x < 2; ++x) { mbar_init(&s_full[x], 1); mbar_init(&p_full[x], 4); mbar_init(&o_done[x], 1); }
-    mbar_init(mma_done, 2);
+    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1); mbar_init(&p_full[2 * x], 4); mbar_init(&p_full[2 * x + 1], 4);
+      mbar_init(&o_done[x], 1); mbar_init(&o_free[x], 4); mbar_init(&l_full[x], 4); mbar_init(&l_free[x], 4);
+    }
+    mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -187,83 +200,168 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
         }
       }
       __syncwarp();
-    } else if (warp == W_MMA || warp == W_MMA_B) {
+    } else if (warp == W_MMA) {
       // ---------------------------------------------------------- products
-      const int x = warp == W_MMA ? 0 : 1;
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_o = idesc_f16(BM, D, true, false, true);
-      const uint32_t col_s = tbase + COL_S0 + 128 * x, col_o = tbase + COL_O0 + D * x;
-      auto tile_q = [&](int seq) { return smem_u32(smem + L::OFF_Q + seq % QS * L::TILE); };
-      auto tile_kv = [&](int seq) { return smem + L::OFF_KV + seq % KS * L::TILE; };
-      auto arrived = [&](int seq) { return mbar_wait(&kv_full[seq % KS], (seq / KS) & 1, abort_flag, p.err); };
+      // a key tile of an item, and where its operands are
+      struct Step {
+        Item it;
+        int j, kv, q;                        // key tile; ring positions of its K, and of the item's Q tiles
+      };
       Walk w;
-      Item it;
-      int kv = 0, qn = 0, n = 0;             // ring positions of K_j and of the item's Q_A; tiles done
-      bool ok = true, ahead = false;         // ahead: S of this item's first key tile is issued
-      // S = Q K_j^T; the item's last one lets go of Q
-      auto issue_s = [&](int q, int k, bool first, bool last) -> bool {
-        if (first && !mbar_wait(&q_full[q % QS], (q / QS) & 1, abort_flag, p.err)) return false;
-        if (!arrived(k)) return false;
+      int qn = 0, kn = 0;
+      auto first = [&](Step& s) -> bool {
+        if (!w.with_keys(a, s.it, false)) return false;
+        s.j = 0;
+        s.kv = kn;
+        s.q = qn;
+        return true;
+      };
+      auto after = [&](const Step& s, Step& n) -> bool {
+        kn = s.kv + 2;
+        if (s.j + 1 < s.it.nt) {
+          n = s;
+          ++n.j;
+          n.kv = kn;
+          return true;
+        }
+        qn = s.q + (s.it.two ? 2 : 1);
+        w.next();
+        return first(n);
+      };
+      int pn[2] = {0, 0}, in[2] = {0, 0};    // of each tile: P V issued; items begun
+      auto issue_s = [&](int x, const Step& s) -> bool {
+        const int ks = s.kv % KS, q = s.q + x, qs = q % QS;
+        if (s.j == 0 && !mbar_wait(&q_full[qs], (q / QS) & 1, abort_flag, p.err)) return false;
+        if (x == 0 && !mbar_wait(&kv_full[ks], (s.kv / KS) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
-        const uint32_t sq = tile_q(q), sk = smem_u32(tile_kv(k));
+        const uint32_t sq = smem_u32(smem + L::OFF_Q + qs * L::TILE), sk = smem_u32(smem + L::OFF_KV + ks * L::TILE);
         if (leader) {
-          product_rows<D>(col_s, sq, sk, idesc_s);
+          product_rows<D>(tbase + COL_S0 + 128 * x, sq, sk, idesc_s);
           mma_commit(&s_full[x]);
-          mma_commit(&kv_empty[k % KS]);
-          if (last) mma_commit(&q_empty[q % QS]);
+          if (x == 1 || !s.it.two) mma_commit(&kv_empty[ks]);
+          if (s.j == s.it.nt - 1) mma_commit(&q_empty[qs]);
         }
         __syncwarp();
         return true;
       };
-      bool more = w.with_keys(a, it, false);
-      while (ok && more) {
-        const int nt = it.nt, len = it.len;
-        const bool mine = x == 0 || it.two;
-        const int q = qn + x, k0 = kv;
-        if (mine && !ahead) ok = issue_s(q, k0, true, nt == 1);
-        ahead = false;
-        qn += it.two ? 2 : 1;
-        kv += 2 * nt;
-        w.next();
-        for (int j = 0; ok && j < nt; ++j) {
-          const int k = k0 + 2 * j, v = k + 1;
-          if (!mine) {                       // tile A alone: only let go of K and V
-            ok = arrived(k) && arrived(v);
-            if (leader) { mbar_arrive(&kv_empty[k % KS]); mbar_arrive(&kv_empty[v % KS]); }
-            __syncwarp();
-            continue;
-          }
-          ok = arrived(v);
-          if (!ok) break;
-          // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not (both issuing
-          // warps write the same zeros)
-          if (len - j * BN < BN && len < p.Nk) clear_rows<D>(tile_kv(v), len - j * BN, lane);
-          ok = mbar_wait(&p_full[x], n & 1, abort_flag, p.err);
-          if (!ok) break;
-          ++n;
+      auto issue_pv = [&](int x, const Step& s) -> bool {
+        const int seq = s.kv + 1, st = seq % KS;
+        uint8_t* v = smem + L::OFF_KV + st * L::TILE;
+        if (x == 0) {
+          if (!mbar_wait(&kv_full[st], (seq / KS) & 1, abort_flag, p.err)) return false;
+          // rows of V behind the sequence's keys may be anything: P is 0 there, and 0 x NaN is not
+          const int keep = s.it.len - s.j * BN;
+          if (keep < BN && s.it.len < p.Nk) clear_rows<D>(v, keep, lane);
+        }
+        if (s.j == 0) {                      // O_X of the item before has been read
+          if (in[x] > 0 && !mbar_wait(&o_free[x], (in[x] - 1) & 1, abort_flag, p.err)) return false;
+          ++in[x];
+        }
+        const uint32_t b = desc_cols(smem_u32(v)), acc = tbase + COL_O0 + D * x, pc = tbase + COL_S0 + 128 * x;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(&p_full[2 * x + half], pn[x] & 1, abort_flag, p.err)) return false;
           tc_fence_after();
-          const uint32_t sv = smem_u32(tile_kv(v));
-          if (leader) {
-            product_cols(col_o, col_s, col_s + 32, sv, idesc_o, j > 0);
-            mma_commit(&o_done[x]);
-            mma_commit(&kv_empty[v % KS]);
-          }
+          if (leader)
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k) mma_ts(acc, pc + 8 * k, b + k * 128, idesc_o, s.j > 0 || k > 0);
           __syncwarp();
-          if (j + 1 < nt) ok = issue_s(q, k + 2, false, j + 2 == nt);
         }
-        // the next item's first S, while this one's last tile is at its softmax's end
-        more = ok && w.with_keys(a, it, false);
-        if (more && mine && (x == 0 || it.two)) {
-          ok = issue_s(qn + x, kv, true, it.nt == 1);
-          ahead = true;
+        ++pn[x];
+        if (leader) {
+          if (x == 1 || !s.it.two) mma_commit(&kv_empty[st]);
+          if (s.j == s.it.nt - 1) mma_commit(&o_done[x]);
         }
+        __syncwarp();
+        return true;
+      };
+      Step cur, nxt;
+      bool more = first(cur);
+      bool ok = !more || (issue_s(0, cur) && (!cur.it.two || issue_s(1, cur)));
+      while (ok && more) {
+        const bool then = after(cur, nxt);
+        ok = issue_pv(0, cur) && (!then || issue_s(0, nxt)) && (!cur.it.two || issue_pv(1, cur)) &&
+             (!then || !nxt.it.two || issue_s(1, nxt));
+        more = then;
+        cur = nxt;
       }
       if (leader) mma_commit(mma_done);
       __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(mma_done, 0, &no_abort, p.err);
       __syncwarp();
+    } else if (warp >= W_OUT) {
+      // ---------------------------------------------------------- O
+      const int quad = warp & 3, r = quad * 32 + lane;
+      const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
+      const int G = p.Hq / p.Hkv;
+      int in[2] = {0, 0};                    // items of each tile
+      bool ok = true;
+      Walk w;
+      Item it;
+      for (; ok && w.at(a, it, false); w.next()) {
+        for (int x = 0; ok && x < (it.two ? 2 : 1); ++x) {
+          const int tile = it.tile0 + x;
+          int g, row;
+          if (a.heads > 1) {
+            divide(r, a.nq, g, row);
+            g = r < a.heads * p.Nq ? tile * a.heads + g : G;
+          } else {
+            divide(tile, a.per_head, g, row);
+            row = row * BM + r;
+          }
+          const bool valid = g < G && row < p.Nq;
+          const int h = it.hk * G + g;
+          float* lse = valid && p.lse ? p.lse + ((long long)it.b * p.Hq + h) * p.Nq + row : nullptr;
+          __nv_bfloat16* dst = valid ? at(p.o, it.b, h, row) : nullptr;
+          if (it.nt == 0) {
+            if (lse) *lse = -INFINITY;
+            if (valid)
+              for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          if (!mbar_wait(&l_full[x], in[x] & 1, abort_flag, p.err)) { ok = false; break; }
+          const float2 ml = sums[128 * x + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_free[x]);
+          if (lse) *lse = (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+          const float inv = 1.f / ml.y;
+          if (!mbar_wait(&o_done[x], in[x] & 1, abort_flag, p.err)) { ok = false; break; }
+          ++in[x];
+          tc_fence_after();
+          const uint32_t col = lane_base + COL_O0 + D * x;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(col + 32 * q, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              __nv_bfloat162 t =
+                  __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+              pk[i] = *reinterpret_cast<uint32_t*>(&t);
+            }
+            if (q == D / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&o_free[x]);
+            }
+            if (valid && a.o32) {
+              st_global_v8(dst + 32 * q, pk);
+              st_global_v8(dst + 32 * q + 16, pk + 8);
+            } else if (valid) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(dst + 32 * q)[i] =
+                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            }
+          }
+        }
+      }
     }
   } else {
     setmaxnreg_inc<REG_SOFT>();
@@ -273,23 +371,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const uint32_t col_s = COL_S0 + 128 * x, col_o = COL_O0 + D * x;
     const float c = p.c;
-    const int G = p.Hq / p.Hkv;
-    int n = 0;                               // key tiles of this warp's tile so far
+    int n = 0, items = 0;                    // key tiles and items of this warp's tile so far
     bool ok = true;
     Walk w;
     Item it;
-    for (; ok && w.at(a, it, false); w.next()) {
+    for (; ok && w.with_keys(a, it, false); w.next()) {
       if (x == 1 && !it.two) continue;
-      const int tile = it.tile0 + x;
-      int g, row;
-      if (a.heads > 1) {
-        divide(r, a.nq, g, row);
-        g = r < a.heads * p.Nq ? tile * a.heads + g : G;
-      } else {
-        divide(tile, a.per_head, g, row);
-        row = row * BM + r;
-      }
-      const bool valid = g < G && row < p.Nq;
       float m = 0.f, mc = 0.f, l = 0.f;
       for (int j = 0; j < it.nt; ++j, ++n) {
         if (!mbar_wait(&s_full[x], n & 1, abort_flag, p.err)) { ok = false; break; }
@@ -323,6 +410,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           m = top > -INFINITY ? top : 0.f;
           mc = m * c;
         }
+        if (j > 0 && __any_sync(0xffffffffu, lift)) {
+          // (S of this tile came after P V of the one before: O is at rest)
+          const float f = lift ? ex2_approx(was - mc) : 1.f;
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t ov[16];
+            tmem_ld16(lane_base + col_o + 16 * q, ov);
+            tmem_ld_wait();
+            reg_fence16(ov);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+            tmem_st16(lane_base + col_o + 16 * q, ov);
+          }
+          l *= f;
+        }
         float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -336,64 +438,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
             pk[i] = *reinterpret_cast<uint32_t*>(&t);
           }
           tmem_st16(lane_base + col_s + 16 * q, pk);
-        }
-        if (j > 0 && __any_sync(0xffffffffu, lift)) {
-          const float f = lift ? ex2_approx(was - mc) : 1.f;
-          if (!mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t ov[32];
-            tmem_ld32(lane_base + col_o + 32 * q, ov);
-            tmem_ld_wait();
-            reg_fence32(ov);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-            tmem_st32(lane_base + col_o + 32 * q, ov);
+          if (q & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * x + q / 2]);
           }
-          l *= f;
         }
         l += ls.x + ls.y;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      const int h = it.hk * G + g;
-      if (valid && p.lse)
-        p.lse[((long long)it.b * p.Hq + h) * p.Nq + row] =
-            it.nt > 0 ? (mc + log2f(l)) * 0.69314718055994531f : -INFINITY;
-      __nv_bfloat16* dst = valid ? at(p.o, it.b, h, row) : nullptr;
-      if (it.nt == 0) {
-        if (valid)
-          for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      if (!mbar_wait(&o_done[x], (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
-      tc_fence_after();
-      const float inv = 1.f / l;
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t v[32], pk[16];
-        tmem_ld32(lane_base + col_o + 32 * q, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          __nv_bfloat162 t = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
-          pk[i] = *reinterpret_cast<uint32_t*>(&t);
-        }
-        if (valid && a.o32) {
-          st_global_v8(dst + 32 * q, pk);
-          st_global_v8(dst + 32 * q + 16, pk + 8);
-        } else if (valid) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(dst + 32 * q)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        }
-      }
-      tc_fence_before();
+      if (items > 0 && !mbar_wait(&l_free[x], (items - 1) & 1, abort_flag, p.err)) { ok = false; break; }
+      ++items;
+      sums[128 * x + r] = make_float2(mc, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&l_full[x]);
     }
   }
   tc_fence_before();
