@@ -98,16 +98,29 @@ struct Walk {
   }
 };
 
-FA4_DEV float rowmax128(const float (&s)[4][32]) {
+FA4_DEV float rowmax128(const uint32_t (&s)[4][32]) {
   float a[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) a[i] = fmax3(s[0][i], s[1][i], fmaxf(s[2][i], s[3][i]));
+  for (int i = 0; i < 32; ++i)
+    a[i] = fmax3(__uint_as_float(s[0][i]), __uint_as_float(s[1][i]),
+                 fmaxf(__uint_as_float(s[2][i]), __uint_as_float(s[3][i])));
 #pragma unroll
   for (int n = 32; n > 1; n /= 2)
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) a[i] = fmaxf(a[i], a[i + n / 2]);
   return a[0];
 }
+FA4_DEV float max32(const uint32_t (&s)[32]) {
+  float a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 16]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], a[i + 4], fmaxf(a[i + 8], a[i + 12]));
+  return fmax3(a[0], a[1], fmaxf(a[2], a[3]));
+}
+
+// Groups of 32 keys of key tile j that hold keys: the others are not scored, exponentiated or multiplied.
+FA4_DEV int groups_of(int len, int j) { return (min(len - j * BN, BN) + 31) / 32; }
 
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_constant__ Params a) {
@@ -203,7 +216,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
     } else if (warp == W_MMA) {
       // ---------------------------------------------------------- products
       const bool leader = elect_one();
-      const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_o = idesc_f16(BM, D, true, false, true);
       // a key tile of an item, and where its operands are
       struct Step {
@@ -238,6 +250,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
         if (x == 0 && !mbar_wait(&kv_full[ks], (s.kv / KS) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
         const uint32_t sq = smem_u32(smem + L::OFF_Q + qs * L::TILE), sk = smem_u32(smem + L::OFF_KV + ks * L::TILE);
+        const uint32_t idesc_s = idesc_f16(BM, 32 * groups_of(s.it.len, s.j), true, false, false);
         if (leader) {
           product_rows<D>(tbase + COL_S0 + 128 * x, sq, sk, idesc_s);
           mma_commit(&s_full[x]);
@@ -261,13 +274,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           ++in[x];
         }
         const uint32_t b = desc_cols(smem_u32(v)), acc = tbase + COL_O0 + D * x, pc = tbase + COL_S0 + 128 * x;
+        const int steps = 2 * groups_of(s.it.len, s.j);            // of 16 keys
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait(&p_full[2 * x + half], pn[x] & 1, abort_flag, p.err)) return false;
           tc_fence_after();
           if (leader)
 #pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k) mma_ts(acc, pc + 8 * k, b + k * 128, idesc_o, s.j > 0 || k > 0);
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              if (k < steps) mma_ts(acc, pc + 8 * k, b + k * 128, idesc_o, s.j > 0 || k > 0);
           __syncwarp();
         }
         ++pn[x];
@@ -381,69 +396,95 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
       for (int j = 0; j < it.nt; ++j, ++n) {
         if (!mbar_wait(&s_full[x], n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
-        float s[4][32];
-        {
-          uint32_t v[4][32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(lane_base + col_s + 32 * q, v[q]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            reg_fence32(v[q]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[q][i] = __uint_as_float(v[q][i]);
-          }
-        }
         const int keep = it.len - j * BN;
-        if (keep < BN) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * q + i >= keep) s[q][i] = -INFINITY;
-        }
-        const float top = rowmax128(s);
-        // the reference: the first tile's maximum, then only where a maximum passes it by far
-        const bool lift = j == 0 || (top - m) * c > TAU;
-        const float was = mc;
-        if (lift) {
-          m = top > -INFINITY ? top : 0.f;
-          mc = m * c;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, lift)) {
-          // (S of this tile came after P V of the one before: O is at rest)
-          const float f = lift ? ex2_approx(was - mc) : 1.f;
-#pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t ov[16];
-            tmem_ld16(lane_base + col_o + 16 * q, ov);
-            tmem_ld_wait();
-            reg_fence16(ov);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-            tmem_st16(lane_base + col_o + 16 * q, ov);
-          }
-          l *= f;
-        }
         float2 ls = make_float2(0.f, 0.f);
+        // the reference: the first tile's maximum, then only where a maximum passes it by far
+        auto refer = [&](float top) {
+          const bool lift = j == 0 || (top - m) * c > TAU;
+          const float was = mc;
+          if (lift) {
+            m = top > -INFINITY ? top : 0.f;
+            mc = m * c;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, lift)) {
+            // (S of this tile came after P V of the one before: O is at rest)
+            const float f = lift ? ex2_approx(was - mc) : 1.f;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t ov[16];
+              tmem_ld16(lane_base + col_o + 16 * q, ov);
+              tmem_ld_wait();
+              reg_fence16(ov);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+              tmem_st16(lane_base + col_o + 16 * q, ov);
+            }
+            l *= f;
+          }
+        };
+        // P of 32 keys, from their scores, over the place of keys that have been read
+        auto weigh = [&](const uint32_t (&s)[32], int q) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 y = ffma2(make_float2(s[q][2 * i], s[q][2 * i + 1]), make_float2(c, c), make_float2(-mc, -mc));
+            const float2 y = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                   make_float2(c, c), make_float2(-mc, -mc));
             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             ls = fadd2(ls, e);
             __nv_bfloat162 t = __floats2bfloat162_rn(e.x, e.y);
             pk[i] = *reinterpret_cast<uint32_t*>(&t);
           }
           tmem_st16(lane_base + col_s + 16 * q, pk);
-          if (q & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * x + q / 2]);
+        };
+        auto ready = [&](int half) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
+        };
+        if (keep >= BN) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(lane_base + col_s + 32 * q, s[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_fence32(s[q]);
+          refer(rowmax128(s));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            weigh(s[q], q);
+            if (q & 1) ready(q / 2);
           }
+        } else {
+          // a sequence's last tile, a group of 32 keys at a time, twice
+          const int groups = groups_of(it.len, j);
+          float top = -INFINITY;
+          auto scores = [&](int q, uint32_t (&s)[32]) {
+            tmem_ld32(lane_base + col_s + 32 * q, s);
+            tmem_ld_wait();
+            reg_fence32(s);
+            if (keep < 32 * q + 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * q + i >= keep) s[i] = 0xff800000u;          // -inf
+            }
+          };
+#pragma unroll 1
+          for (int q = 0; q < groups; ++q) {
+            uint32_t s[32];
+            scores(q, s);
+            top = fmaxf(top, max32(s));
+          }
+          refer(top);
+#pragma unroll 1
+          for (int q = 0; q < groups; ++q) {
+            uint32_t s[32];
+            scores(q, s);
+            weigh(s, q);
+            if (q == 1 && groups > 2) ready(0);
+          }
+          if (groups <= 2) ready(0);
+          ready(1);
         }
         l += ls.x + ls.y;
       }
