@@ -5,6 +5,8 @@
 #include <structmember.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -107,9 +109,20 @@ int* ints(PyObject* x, const char* name, int index, at::IntArrayRef shape) {
   return given(x) ? static_cast<int*>(expect(x, name, index, at::kInt, shape).data_ptr()) : nullptr;
 }
 
+// A tensor of the caching allocator, made without the dispatcher: 0.7 us instead of
+// at::empty's 1.8, where a call makes up to five.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index, bool zero = false) {
-  const auto o = at::TensorOptions().dtype(type).device(at::kCUDA, index);
-  return zero ? at::zeros(shape, o) : at::empty(shape, o);
+  if (zero) return at::zeros(shape, at::TensorOptions().dtype(type).device(at::kCUDA, index));
+  const int now = c10::cuda::current_device();
+  if (now != index) c10::cuda::set_device((c10::DeviceIndex)index);
+  struct Back {
+    int now, index;
+    ~Back() {
+      if (now != index) c10::cuda::set_device((c10::DeviceIndex)now);
+    }
+  } back{now, index};
+  return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                   c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 // The caller's workspace, or a fresh one of `need` bytes (none for 0).

@@ -26,7 +26,6 @@ struct HeadsMap {
   int own_h, own_b;
 };
 bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads);
-int sm_count();
 
 // Up to CROSS_TOKEN_ROWS query rows of a kv head (Hq / Hkv * Nq).
 constexpr int CROSS_TOKEN_ROWS = 32;

@@ -1093,15 +1093,18 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int sms = sm_count();
   const dim3 gq(a.items < sms ? a.items : sms), gk(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 2, JOIN_PARTS);
+  // no range ends inside a key tile's steps, and no key is without one?
+  const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
+  const bool join = p.lens || (a.tiles > 1 && (steps % a.ctas != 0 || steps / a.ctas % a.tiles != 0));
   cudaError_t e;
   if (p.d == 128) {
     e = start(cross_dq_kernel<128>, gq, SmemQ<128>::BYTES, a, st);
     if (e == cudaSuccess) e = start(cross_dkv_kernel<128>, gk, SmemK<128>::BYTES, a, st);
-    if (e == cudaSuccess) cross_join_kernel<128><<<gj, 256, 0, st>>>(a);
+    if (e == cudaSuccess && join) cross_join_kernel<128><<<gj, 256, 0, st>>>(a);
   } else {
     e = start(cross_dq_kernel<64>, gq, SmemQ<64>::BYTES, a, st);
     if (e == cudaSuccess) e = start(cross_dkv_kernel<64>, gk, SmemK<64>::BYTES, a, st);
-    if (e == cudaSuccess) cross_join_kernel<64><<<gj, 256, 0, st>>>(a);
+    if (e == cudaSuccess && join) cross_join_kernel<64><<<gj, 256, 0, st>>>(a);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -20,6 +20,7 @@
 //   warps 12-15  take O / l to the rows' places, tile A's and tile B's in turn, while
 //                the softmax of the next item runs.
 // Tensor memory: S_A, S_B, O_A, O_B (512 columns at d = 128).
+#include <atomic>
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "cross.cuh"
@@ -512,10 +513,13 @@ bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int ro
 }
 
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {

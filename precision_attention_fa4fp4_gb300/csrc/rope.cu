@@ -334,34 +334,29 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
 }
 
 // dw = sum of the CTAs' partials: one CTA per tensor and 32 channels.
-__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const __grid_constant__ RopeParams p) {
+constexpr int DW_WARPS = 32;
+__global__ void __launch_bounds__(DW_WARPS * 32) norm_rope_dw_kernel(const __grid_constant__ RopeParams p) {
   const int per = p.d / 32, t = blockIdx.x / per, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int i = (blockIdx.x % per) * 32 + lane;
   const RopeTensor& T = p.t[t];
   if (!T.dw) return;
-  __shared__ float join[8][32];
+  __shared__ float join[DW_WARPS][32];
   float sum = 0.f;
-  for (int c = warp; c < p.ctas[t]; c += 8) sum += T.part[(long long)c * p.d + i];
+#pragma unroll 4
+  for (int c = warp; c < p.ctas[t]; c += DW_WARPS) sum += T.part[(long long)c * p.d + i];
   join[warp][lane] = sum;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < 8; ++w) sum += join[w][lane];
+    for (int w = 1; w < DW_WARPS; ++w) sum += join[w][lane];
     T.dw[i] = sum;
   }
-}
-
-int sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
 }
 
 // Heads of a warp's task: all of a tensor's where there are tokens enough to fill
 // the GPU with one warp each, else as few as one round of its lanes.
 int chunk_of(long long tokens, int H, int rows) {
-  const long long want = (long long)sms() * 16;
+  const long long want = (long long)sm_count() * 16;
   if (H <= rows || tokens >= want) return H > 0 ? H : 1;
   const long long parts = (want + tokens - 1) / tokens;
   const long long rounds = (H + rows - 1) / rows;
@@ -378,7 +373,7 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t st) {
   const int tokens = p.B * p.N;
   const int chunk = chunk_of(tokens, p.t[0].H > p.t[1].H ? p.t[0].H : p.t[1].H, rows);
   const int nq = parts_of(p.t[0].H, chunk), nk = parts_of(p.t[1].H, chunk);
-  const int need = (int)(((long long)tokens * (nq + nk) + WARPS - 1) / WARPS), room = FWD_CTAS * sms();
+  const int need = (int)(((long long)tokens * (nq + nk) + WARPS - 1) / WARPS), room = FWD_CTAS * sm_count();
   auto k = p.d == 128 ? (p.pairs ? norm_rope_kernel<128, true, 3> : norm_rope_kernel<128, false, 3>)
                       : (p.pairs ? norm_rope_kernel<64, true, 3> : norm_rope_kernel<64, false, 3>);
   k<<<need < room ? need : room, WARPS * 32, 0, st>>>(p, chunk, nq, nk, Divisor(tokens), Divisor(p.N));
@@ -389,7 +384,7 @@ void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas) {
   const int rows = 32 / (d / 16);
   const long long tokens = (long long)B * N;
   const int chunk = chunk_of(tokens, Hq > Hkv ? Hq : Hkv, rows);
-  const long long room = (long long)sms() * BWD_CTAS;
+  const long long room = (long long)sm_count() * BWD_CTAS;
   const int H[2] = {Hq, Hkv};
   for (int t = 0; t < 2; ++t) {
     const long long need = (tokens * parts_of(H[t], chunk) + WARPS - 1) / WARPS;
@@ -411,7 +406,7 @@ cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st) {
   };
   auto k = p.dy_f32 ? pick(std::true_type()) : pick(std::false_type());
   k<<<p.ctas[0] + p.ctas[1], WARPS * 32, 0, st>>>(p, chunk, nq, nk, by_tokens, by_n);
-  if (p.t[0].dw || p.t[1].dw) norm_rope_dw_kernel<<<2 * (p.d / 32), 256, 0, st>>>(p);
+  if (p.t[0].dw || p.t[1].dw) norm_rope_dw_kernel<<<2 * (p.d / 32), DW_WARPS * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -13,6 +13,9 @@ struct Strided {
   long long b, h, n;
 };
 
+// Multiprocessors of the current device (1 where there is none).
+int sm_count();
+
 // Division of 0 <= n < 2^31 by a fixed d >= 1: (umulhi(n, m) + n) >> s.
 struct Divisor {
   uint32_t m = 0;
