@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     atomicOr(p.err, FA4_DEVERR_TIMEOUT);
     return;
   }
+  next_may_start();
   float* shares = reinterpret_cast<float*>(smem + L::OFF_DEL);
   uint8_t *q_tile = smem + L::OFF_Q, *do_tile = smem + L::OFF_DO;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -643,6 +644,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
     atomicOr(p.err, FA4_DEVERR_TIMEOUT);
     return;
   }
+  next_may_start();
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* k_empty = k_full + 1;
   uint64_t* v_full = k_empty + 1;
@@ -746,6 +748,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       }
       __syncwarp();
     } else if (warp == W_STAT) {
+      // (D is the first kernel's; every CTA waits for it, so that this kernel does not end before it)
+      wait_for_previous();
       // lse log2 e and D of each step's queries (infinite lse where there is none: P = 0)
       float z[4], d4[4];
       auto fetch = [&]() {
@@ -965,6 +969,7 @@ constexpr int JOIN_PARTS = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
   const CrossParams& p = a.p;
+  wait_for_previous();
   const int which = blockIdx.y;
   const Strided& out = which ? p.dk : p.dv;
   if ((int)blockIdx.x >= a.ctas) {
@@ -1052,14 +1057,11 @@ void plan(Params& a, int B, int Hq, int Hkv, int Nq, int Nk, bool share) {
 
 size_t del_bytes(int B, int Hq, int Nq) { return ((size_t)B * Hq * Nq * sizeof(float) + 127) / 128 * 128; }
 
-bool wide(const Strided& t) { return (reinterpret_cast<uintptr_t>(t.p) & 31) == 0 && ((t.b | t.h | t.n) & 15) == 0; }
+bool on_words(const Strided& t) { return (reinterpret_cast<uintptr_t>(t.p) & 31) == 0 && ((t.b | t.h | t.n) & 15) == 0; }
 
-template <class K>
-cudaError_t start(K kernel, dim3 grid, int smem, const Params& a, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<grid, NTHREADS, smem, st>>>(a);
-  return cudaGetLastError();
+cudaError_t start(void (*kernel)(const Params), dim3 grid, int smem, bool early, const Params& a, cudaStream_t st) {
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+  return e != cudaSuccess ? e : launch(kernel, grid, NTHREADS, smem, early, st, a);
 }
 
 }  // namespace
@@ -1081,7 +1083,7 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   Params a;
   a.p = p;
   plan(a, p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.q.h != 0 && p.dout.h != 0 && p.o.h != 0);
-  a.dq32 = wide(p.dq); a.dk32 = wide(p.dk); a.dv32 = wide(p.dv);
+  a.dq32 = on_words(p.dq); a.dk32 = on_words(p.dk); a.dv32 = on_words(p.dv);
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
   const int rows = a.heads > 1 ? p.Nq : BM;
@@ -1096,17 +1098,14 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   // no range ends inside a key tile's steps, and no key is without one?
   const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
   const bool join = p.lens || (a.tiles > 1 && (steps % a.ctas != 0 || steps / a.ctas % a.tiles != 0));
-  cudaError_t e;
-  if (p.d == 128) {
-    e = start(cross_dq_kernel<128>, gq, SmemQ<128>::BYTES, a, st);
-    if (e == cudaSuccess) e = start(cross_dkv_kernel<128>, gk, SmemK<128>::BYTES, a, st);
-    if (e == cudaSuccess && join) cross_join_kernel<128><<<gj, 256, 0, st>>>(a);
-  } else {
-    e = start(cross_dq_kernel<64>, gq, SmemQ<64>::BYTES, a, st);
-    if (e == cudaSuccess) e = start(cross_dkv_kernel<64>, gk, SmemK<64>::BYTES, a, st);
-    if (e == cudaSuccess && join) cross_join_kernel<64><<<gj, 256, 0, st>>>(a);
-  }
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const bool wide = p.d == 128;
+  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, gq, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
+                        false, a, st);
+  if (e == cudaSuccess)
+    e = start(wide ? cross_dkv_kernel<128> : cross_dkv_kernel<64>, gk, wide ? SmemK<128>::BYTES : SmemK<64>::BYTES,
+              true, a, st);
+  if (e == cudaSuccess && join) e = launch(wide ? cross_join_kernel<128> : cross_join_kernel<64>, gj, 256, 0, true, st, a);
+  return e;
 }
 
 }  // namespace fa4

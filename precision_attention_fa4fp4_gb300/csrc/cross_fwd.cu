@@ -522,6 +522,32 @@ int sm_count() {
   return n;
 }
 
+cudaError_t allow_smem(const void* kernel, int bytes, bool clusters) {
+  struct Known {
+    std::atomic<const void*> kernel;
+    std::atomic<uint64_t> devices;
+  };
+  static Known known[32];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Known* at = nullptr;
+  for (Known& k : known) {
+    const void* none = nullptr;
+    if (k.kernel.load(std::memory_order_acquire) == kernel ||
+        k.kernel.compare_exchange_strong(none, kernel, std::memory_order_acq_rel) || none == kernel) {
+      at = &k;
+      break;
+    }
+  }
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (at && (at->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && at) at->devices.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {
   Params a;
   a.p = p;
@@ -546,10 +572,8 @@ cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {
   const int sms = sm_count(), grid = a.items < sms ? a.items : sms;
   const int smem = p.d == 128 ? Smem<128>::BYTES : Smem<64>::BYTES;
   auto k = p.d == 128 ? cross_fwd_kernel<128> : cross_fwd_kernel<64>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  k<<<grid, NTHREADS, smem, st>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
+  return e != cudaSuccess ? e : launch(k, dim3(grid), NTHREADS, smem, false, st, a);
 }
 
 }  // namespace fa4

@@ -339,8 +339,7 @@ cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st) {
                       : (two ? cross_token_kernel<64, 2> : cross_token_kernel<64, 1>);
   const int smem = p.d == 128 ? (two ? Smem<128, 2>::BYTES : Smem<128, 1>::BYTES)
                               : (two ? Smem<64, 2>::BYTES : Smem<64, 1>::BYTES);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess && a.splits > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(heads * a.splits));

@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
   constexpr int LANES = D / 16, ROWS = 32 / LANES;
   __shared__ Tables<D> tab;
   __shared__ float join[WARPS][D];
+  next_may_start();
   tab.load(p);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(DW_WARPS * 32) norm_rope_dw_kernel(const __gri
   const int per = p.d / 32, t = blockIdx.x / per, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int i = (blockIdx.x % per) * 32 + lane;
   const RopeTensor& T = p.t[t];
+  wait_for_previous();
   if (!T.dw) return;
   __shared__ float join[DW_WARPS][32];
   float sum = 0.f;
@@ -406,8 +408,9 @@ cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st) {
   };
   auto k = p.dy_f32 ? pick(std::true_type()) : pick(std::false_type());
   k<<<p.ctas[0] + p.ctas[1], WARPS * 32, 0, st>>>(p, chunk, nq, nk, by_tokens, by_n);
-  if (p.t[0].dw || p.t[1].dw) norm_rope_dw_kernel<<<2 * (p.d / 32), DW_WARPS * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !(p.t[0].dw || p.t[1].dw)) return e;
+  return launch(norm_rope_dw_kernel, dim3(2 * (p.d / 32)), DW_WARPS * 32, 0, true, st, p);
 }
 
 }  // namespace fa4

@@ -16,6 +16,27 @@ struct Strided {
 // Multiprocessors of the current device (1 where there is none).
 int sm_count();
 
+// cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device (and
+// the leave for clusters of 16).
+cudaError_t allow_smem(const void* kernel, int bytes, bool clusters = false);
+
+// Launches a kernel; `early`: it may start while its predecessor runs, and waits for it
+// itself (griddepcontrol.wait) before it reads what that writes.
+template <class... P>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, bool early, cudaStream_t st, const P&... p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p...);
+}
+
 // Division of 0 <= n < 2^31 by a fixed d >= 1: (umulhi(n, m) + n) >> s.
 struct Divisor {
   uint32_t m = 0;
