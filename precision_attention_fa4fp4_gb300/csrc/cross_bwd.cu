@@ -146,7 +146,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     atomicOr(p.err, FA4_DEVERR_TIMEOUT);
     return;
   }
-  next_may_start();
   float* shares = reinterpret_cast<float*>(smem + L::OFF_DEL);
   uint8_t *q_tile = smem + L::OFF_Q, *do_tile = smem + L::OFF_DO;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -187,6 +186,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     fence_barrier_init();
   }
   if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
+  // (in this order: the next kernel reads its inputs before it waits for this one)
+  wait_for_previous();
+  next_may_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -748,7 +750,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       }
       __syncwarp();
     } else if (warp == W_STAT) {
-      // (D is the first kernel's; every CTA waits for it, so that this kernel does not end before it)
+      // (D is the first kernel's, which let this one start when the grids before it had ended; every CTA waits for it,
+      // so that this kernel does not end before it)
       wait_for_previous();
       // lse log2 e and D of each step's queries (infinite lse where there is none: P = 0)
       float z[4], d4[4];
@@ -1100,7 +1103,7 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   const bool join = p.lens || (a.tiles > 1 && (steps % a.ctas != 0 || steps / a.ctas % a.tiles != 0));
   const bool wide = p.d == 128;
   cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, gq, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
-                        false, a, st);
+                        true, a, st);
   if (e == cudaSuccess)
     e = start(wide ? cross_dkv_kernel<128> : cross_dkv_kernel<64>, gk, wide ? SmemK<128>::BYTES : SmemK<64>::BYTES,
               true, a, st);

@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
     fence_barrier_init();
   }
   if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
+  next_may_start();
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -573,7 +575,7 @@ cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st) {
   const int smem = p.d == 128 ? Smem<128>::BYTES : Smem<64>::BYTES;
   auto k = p.d == 128 ? cross_fwd_kernel<128> : cross_fwd_kernel<64>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
-  return e != cudaSuccess ? e : launch(k, dim3(grid), NTHREADS, smem, false, st, a);
+  return e != cudaSuccess ? e : launch(k, dim3(grid), NTHREADS, smem, true, st, a);
 }
 
 }  // namespace fa4

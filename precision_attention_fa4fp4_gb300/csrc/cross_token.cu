@@ -37,17 +37,14 @@ FA4_DEV uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-FA4_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-// A float in the shared memory of CTA `rank` of the cluster, at this CTA's place `x`.
-FA4_DEV float peer_float(const float* x, uint32_t rank) {
-  float v;
-  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-               : "=f"(v)
-               : "r"(smem_u32(x)), "r"(rank)
+FA4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+FA4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Two floats into the shared memory of CTA `rank` of the cluster, at this CTA's place `x`.
+FA4_DEV void give(const float2* x, int rank, float a, float b) {
+  asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n st.shared::cluster.v2.f32 [r], {%2, %3};\n}\n" ::"r"(
+                   smem_u32(x)),
+               "r"(rank), "f"(a), "f"(b)
                : "memory");
-  return v;
 }
 
 FA4_DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -74,14 +71,17 @@ struct Smem {
   static constexpr int CHUNK = KEYS<D> * 128;              // [keys][64 channels], 128-byte swizzle
   static constexpr int TILE = (D / 64) * CHUNK;            // 4 KB
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int RING = WARPS * STAGES * STAGE;      // 96 KB
-  // after the loop the rings' place holds the warps' (m, l) and O, then the CTA's
+  static constexpr int RING = WARPS * STAGES * STAGE;      // 24 KB a warp
+  // after the loop the rings' place holds the warps' O, m and l
   static constexpr int ROWS = 16 * MT;
   static constexpr int WARP_F = ROWS * (D + 2);            // floats of one warp: O [ROWS][D], m, l
-  static constexpr int OFF_CTA = WARPS * WARP_F * 4;
-  static_assert(OFF_CTA + WARP_F * 4 <= RING, "join fits the rings");
+  static_assert(WARPS * WARP_F * 4 <= RING, "join fits the rings");
   static constexpr int OFF_BAR = RING;
-  static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8 + 16 + 1024;
+  // what the cluster's CTAs give this one: (m, l) of all rows, and their O of its share of the outputs
+  static constexpr int OFF_ML = OFF_BAR + WARPS * STAGES * 8 + 32;
+  static constexpr int OFF_O = OFF_ML + 16 * ROWS * 8;
+  static constexpr int share(int splits) { return (ROWS * (D / 2) + splits - 1) / splits; }   // pairs of outputs
+  static constexpr int bytes(int splits) { return (splits > 1 ? OFF_O + splits * share(splits) * 8 : OFF_ML) + 1024; }
 };
 
 template <int D, int MT>
@@ -105,6 +105,9 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
     fence_barrier_init();
   }
   __syncthreads();
+  if (a.splits > 1) cluster_arrive();          // (this CTA is there to be given to)
+  next_may_start();
+  wait_for_previous();
   const int len = key_count(p, b, threadIdx.x == 0 && rank == 0);
   const int blocks = (len + NK - 1) / NK;
   // this warp's blocks: me, me + step, ...
@@ -161,11 +164,14 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
       __syncwarp();
     }
     const uint32_t ks = smem_u32(kt), vs = smem_u32(vt);
-    float s[MT][NK / 8][4];
+    // two sums over every other 16 channels: chains of products half as long
+    float s[MT][NK / 8][4], s2[MT][NK / 8][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int n = 0; n < NK / 8; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+      for (int n = 0; n < NK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][n][e] = s2[t][n][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -175,13 +181,18 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
         ldsm4(ks + (k / 4) * L::CHUNK + row * 128 + ((2 * (k % 4) + kcol) ^ (row & 7)) * 16, kf);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          mma_bf16(s[t][2 * n], qf[t][k], kf[0], kf[1]);
-          mma_bf16(s[t][2 * n + 1], qf[t][k], kf[2], kf[3]);
+          const bool second = MT == 1 && k % 2;      // (32 rows have chains enough, and no registers)
+          mma_bf16(second ? s2[t][2 * n] : s[t][2 * n], qf[t][k], kf[0], kf[1]);
+          mma_bf16(second ? s2[t][2 * n + 1] : s[t][2 * n + 1], qf[t][k], kf[2], kf[3]);
         }
       }
     uint32_t pf[MT][NK / 16][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int n = 0; n < NK / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][n][e] += s2[t][n][e];
       if (keep < NK) {
 #pragma unroll
         for (int n = 0; n < NK / 8; ++n)
@@ -189,17 +200,29 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
           for (int e = 0; e < 4; ++e)
             if (8 * n + 2 * (lane % 4) + (e & 1) >= keep) s[t][n][e] = -INFINITY;
       }
+      // both rows of the lane side by side
+      float now[2], ref[2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float top = -INFINITY;
+        now[half] = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NK / 8; ++n) top = fmaxf(top, fmaxf(s[t][n][2 * half], s[t][n][2 * half + 1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float now = fmaxf(m[t][half], top * p.c);
-        const float ref = now > -INFINITY ? now : 0.f;
-        if (__any_sync(0xffffffffu, now != m[t][half])) {
-          const float f = ex2_approx(m[t][half] - ref);
+        for (int n = 0; n < NK / 8; ++n)
+          now[half] = fmaxf(now[half], fmaxf(s[t][n][2 * half], s[t][n][2 * half + 1]));
+      }
+#pragma unroll
+      for (int x = 1; x < 4; x *= 2)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          now[half] = fmaxf(now[half], __shfl_xor_sync(0xffffffffu, now[half], x));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        now[half] = fmaxf(m[t][half], now[half] * p.c);
+        ref[half] = now[half] > -INFINITY ? now[half] : 0.f;
+      }
+      if (__any_sync(0xffffffffu, now[0] != m[t][0] || now[1] != m[t][1])) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float f = ex2_approx(m[t][half] - ref[half]);
           l[t][half] *= f;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) {
@@ -207,12 +230,15 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
             o[t][n][2 * half + 1] *= f;
           }
         }
-        m[t][half] = now;
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        m[t][half] = now[half];
         float sum = 0.f;
 #pragma unroll
         for (int n = 0; n < NK / 8; ++n) {
-          const float e0 = ex2_approx(fmaf(s[t][n][2 * half], p.c, -ref));
-          const float e1 = ex2_approx(fmaf(s[t][n][2 * half + 1], p.c, -ref));
+          const float e0 = ex2_approx(fmaf(s[t][n][2 * half], p.c, -ref[half]));
+          const float e1 = ex2_approx(fmaf(s[t][n][2 * half + 1], p.c, -ref[half]));
           sum += e0 + e1;
           pf[t][n / 2][(n & 1) * 2 + half] = pack2(e0, e1);
         }
@@ -262,19 +288,21 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
             make_float2(o[t][n][2 * half], o[t][n][2 * half + 1]);
     }
   __syncthreads();
-  // this CTA's O (not divided), m and l
-  float* cta = a.splits > 1 ? reinterpret_cast<float*>(smem + L::OFF_CTA) : nullptr;
   auto store = [&](int r, int i, float v0, float v1, float top, float sum) {
-    if (r >= R) return;
     const int h = hk * G + r / p.Nq, n = r % p.Nq;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *reinterpret_cast<uint32_t*>(at(p.o, b, h, n) + i) = pack2(v0 * inv, v1 * inv);
     if (i == 0 && p.lse)
       p.lse[((long long)b * p.Hq + h) * p.Nq + n] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   };
-  for (int x = threadIdx.x; x < L::ROWS * (D / 2); x += WARPS * 32) {
+  // of a cluster, each CTA takes an equal share of the outputs, and is given the others' parts of it: stores to
+  // another CTA's memory are not waited for, loads are (16 CTAs: 24.6 -> 18 us where they read)
+  float2* ml = reinterpret_cast<float2*>(smem + L::OFF_ML);        // [splits][ROWS]
+  float2* part = reinterpret_cast<float2*>(smem + L::OFF_O);       // [splits][share]
+  const int share = L::share(a.splits);
+  if (a.splits > 1) cluster_wait();
+  for (int x = threadIdx.x; x < R * (D / 2); x += WARPS * 32) {
     const int r = x / (D / 2), i = x % (D / 2) * 2;
-    if (r >= R) break;
     float top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) top = fmaxf(top, mem[w * L::WARP_F + L::ROWS * D + r]);
@@ -287,32 +315,34 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
       v0 = fmaf(v.x, f, v0);
       v1 = fmaf(v.y, f, v1);
     }
-    if (!cta) {
+    if (a.splits == 1) {
       store(r, i, v0, v1, top, sum);
     } else {
-      *reinterpret_cast<float2*>(cta + r * D + i) = make_float2(v0, v1);
-      if (i == 0) {
-        cta[L::ROWS * D + r] = top;
-        cta[L::ROWS * D + L::ROWS + r] = sum;
-      }
+      const int to = x / share;
+      give(part + rank * share + (x - to * share), to, v0, v1);
+      if (x % (D / 2) < a.splits) give(ml + rank * L::ROWS + r, x % (D / 2), top, sum);
     }
   }
-  if (!cta) return;
-  cluster_sync();
-  // the cluster's: pairs of outputs in turn
-  for (int x = rank * WARPS * 32 + threadIdx.x; x < R * (D / 2); x += a.splits * WARPS * 32) {
+  if (a.splits == 1) return;
+  cluster_arrive();
+  cluster_wait();
+  for (int y = threadIdx.x; y < share; y += WARPS * 32) {
+    const int x = rank * share + y;
+    if (x >= R * (D / 2)) break;
     const int r = x / (D / 2), i = x % (D / 2) * 2;
     float top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
-    for (int c = 0; c < a.splits; ++c) top = fmaxf(top, peer_float(cta + L::ROWS * D + r, c));
+#pragma unroll 4
+    for (int c = 0; c < a.splits; ++c) top = fmaxf(top, ml[c * L::ROWS + r].x);
+#pragma unroll 4
     for (int c = 0; c < a.splits; ++c) {
-      const float f = top > -INFINITY ? ex2_approx(peer_float(cta + L::ROWS * D + r, c) - top) : 0.f;
-      sum = fmaf(peer_float(cta + L::ROWS * D + L::ROWS + r, c), f, sum);
-      v0 = fmaf(peer_float(cta + r * D + i, c), f, v0);
-      v1 = fmaf(peer_float(cta + r * D + i + 1, c), f, v1);
+      const float2 e = ml[c * L::ROWS + r], v = part[c * share + y];
+      const float f = top > -INFINITY ? ex2_approx(e.x - top) : 0.f;
+      sum = fmaf(e.y, f, sum);
+      v0 = fmaf(v.x, f, v0);
+      v1 = fmaf(v.y, f, v1);
     }
     store(r, i, v0, v1, top, sum);
   }
-  cluster_sync();          // no CTA leaves while another reads its memory
 }
 
 }  // namespace
@@ -334,24 +364,27 @@ cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st) {
   const int sms = sm_count();
   a.splits = 1;
   while (a.splits < 16 && heads * a.splits * 2 <= 2LL * sms && p.Nk >= a.splits * 2 * WARPS * 2 * nk) a.splits *= 2;
-  const bool two = p.Hq / p.Hkv * p.Nq > 16;
-  auto k = p.d == 128 ? (two ? cross_token_kernel<128, 2> : cross_token_kernel<128, 1>)
-                      : (two ? cross_token_kernel<64, 2> : cross_token_kernel<64, 1>);
-  const int smem = p.d == 128 ? (two ? Smem<128, 2>::BYTES : Smem<128, 1>::BYTES)
-                              : (two ? Smem<64, 2>::BYTES : Smem<64, 1>::BYTES);
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, true);
+  const bool two = p.Hq / p.Hkv * p.Nq > 16, wide = p.d == 128;
+  const int n = a.splits;
+  auto k = wide ? (two ? cross_token_kernel<128, 2> : cross_token_kernel<128, 1>)
+                : (two ? cross_token_kernel<64, 2> : cross_token_kernel<64, 1>);
+  const int smem = wide ? (two ? Smem<128, 2>::bytes(n) : Smem<128, 1>::bytes(n))
+                        : (two ? Smem<64, 2>::bytes(n) : Smem<64, 1>::bytes(n));
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), Smem<128, 2>::bytes(16), true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(heads * a.splits));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 

@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
     norm_rope_kernel(const __grid_constant__ RopeParams p, int chunk, int nq, int nk, Divisor by_tokens, Divisor by_n) {
   constexpr int LANES = D / 16, ROWS = 32 / LANES;
   __shared__ Tables<D> tab;
+  next_may_start();
+  wait_for_previous();
   tab.load(p);
   const int lane = threadIdx.x % 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
@@ -226,6 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
   __shared__ Tables<D> tab;
   __shared__ float join[WARPS][D];
   next_may_start();
+  wait_for_previous();
   tab.load(p);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
@@ -378,8 +381,8 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t st) {
   const int need = (int)(((long long)tokens * (nq + nk) + WARPS - 1) / WARPS), room = FWD_CTAS * sm_count();
   auto k = p.d == 128 ? (p.pairs ? norm_rope_kernel<128, true, 3> : norm_rope_kernel<128, false, 3>)
                       : (p.pairs ? norm_rope_kernel<64, true, 3> : norm_rope_kernel<64, false, 3>);
-  k<<<need < room ? need : room, WARPS * 32, 0, st>>>(p, chunk, nq, nk, Divisor(tokens), Divisor(p.N));
-  return cudaGetLastError();
+  return launch(k, dim3(need < room ? need : room), WARPS * 32, 0, true, st, p, chunk, nq, nk, Divisor(tokens),
+                Divisor(p.N));
 }
 
 void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas) {
@@ -407,8 +410,8 @@ cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st) {
                       : (p.pairs ? norm_rope_bwd_kernel<64, true, F> : norm_rope_bwd_kernel<64, false, F>);
   };
   auto k = p.dy_f32 ? pick(std::true_type()) : pick(std::false_type());
-  k<<<p.ctas[0] + p.ctas[1], WARPS * 32, 0, st>>>(p, chunk, nq, nk, by_tokens, by_n);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch(k, dim3(p.ctas[0] + p.ctas[1]), WARPS * 32, 0, true, st, p, chunk, nq, nk, by_tokens, by_n);
   if (e != cudaSuccess || !(p.t[0].dw || p.t[1].dw)) return e;
   return launch(norm_rope_dw_kernel, dim3(2 * (p.d / 32)), DW_WARPS * 32, 0, true, st, p);
 }
