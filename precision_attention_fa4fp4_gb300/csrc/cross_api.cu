@@ -268,7 +268,8 @@ fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
       if ((s = check_heads(in[i], B, Hkv, Nk, 2, i >= 2)) != FA4FP4_OK) return s;
       *to[i] = strided(in[i], B, Hkv, Nk);
     }
-    if ((s = check_rows(p.k, Nk, d)) != FA4FP4_OK || (s = check_rows(p.v, Nk, d)) != FA4FP4_OK) return s;
+    for (const Strided* t : to)
+      if ((s = check_rows(*t, Nk, d)) != FA4FP4_OK) return s;
   }
   if (!aligned(kv_lens, 4) || !aligned(lse, 16)) return FA4FP4_ERR_ALIGNMENT;
   const size_t need = cross_bwd_workspace(B, Hq, Hkv, Nq, Nk, d);

@@ -13,7 +13,12 @@
 // A query tile is 128 rows as in the forward (several heads where they have up to
 // 64 rows); a key tile is 128 keys.
 //
-// cross_dq_kernel: persistent, a query tile at a time.  Warps 0-7: a thread per
+// Both kernels get equal ranges of steps (a key tile with a query tile) for as many
+// CTAs as the GPU has multiprocessors: few queries with many keys, or many with few,
+// keep it as busy as even shapes do.  A range that starts or ends inside an output
+// tile's steps leaves FP32 partials in the workspace.
+//
+// cross_dq_kernel: a query tile's key tiles in turn.  Warps 0-7: a thread per
 //   row and half of the keys: P from S, dS from P and dP, as bf16 into tensor memory
 //   (the A operand of dQ).  Q is in tensor memory too (the A operand of S), so that its
 //   place in shared memory takes the next item's Q, then this one's dQ on its way
@@ -21,13 +26,13 @@
 //   run as soon as these have been read.  D is summed by the same threads from the o
 //   and dO tiles, and kept in the workspace.  Two warps issue the products: S; dP and
 //   dQ.
-// cross_dkv_kernel: persistent over the steps (key tile, query tile), cut into
-//   equal ranges.  Rows are keys: P^T and dS^T go over S^T and dP^T as A operands of
-//   dV and dK, which are summed in tensor memory (512 columns in all).  Two warps
-//   issue the products, S^T and dV the one, dP^T and dK the other (one warp was the
-//   bound: a product takes 512 cycles, its waits, instructions and commits 700).  A range that starts or ends inside a key
-//   tile leaves FP32 partials in the workspace.
-// cross_join_kernel: sums those in the ranges' order; zeros for keys behind kv_lens.
+// cross_dkv_kernel: a key tile's query tiles in turn.  Rows are keys: P^T and dS^T go
+//   over S^T and dP^T as A operands of dV and dK, which are summed in tensor memory
+//   (512 columns in all).  Two warps issue the products, S^T and dV the one, dP^T and
+//   dK the other (one warp was the bound: a product takes 512 cycles, its waits,
+//   instructions and commits 700).
+// cross_join_kernel: sums the partials in the ranges' order; zeros for keys behind
+//   kv_lens.
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "cross.cuh"
@@ -46,15 +51,15 @@ constexpr float L2E = 1.4426950408889634f;
 struct Params {
   CrossParams p;
   HeadsMap q, dout, o, k, v;
-  HeadsMap dq;                                 // boxes of 32 rows, where heads share no tile
+  HeadsMap dq, dk, dv;                         // boxes of 32 rows (dq: where heads share no tile)
   int tiles, heads, box;                       // query tiles of a kv head, as in the forward
   Divisor per_head, per_kv, hkv, nq;           // (per_kv: tiles)
   int key_tiles;                               // of Nk
   int items;                                   // query tiles in all
-  int ctas;                                    // of the dK, dV kernel
-  int dq32, dk32, dv32;                        // rows begin on 32 bytes
+  int ctas;                                    // of both kernels
+  int dq32;                                    // dq's rows begin on 32 bytes
   float* del;                                  // D [B][Hq][Nq]
-  float* part;                                 // [2 ctas][dV, dK][128][d]
+  float *part, *part_q;                        // partial sums: [2 ctas][dV, dK] and [2 ctas] tiles of dQ
 };
 
 // Row r of a query tile: query head within the group (G: none) and position.
@@ -90,6 +95,103 @@ FA4_DEV void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float f, bool 
 }
 
 // ---------------------------------------------------------------------------
+// steps
+// ---------------------------------------------------------------------------
+// Both kernels' work is cut into steps, a key tile that holds keys with a query
+// tile each, and the CTAs get equal ranges of them: the first kernel's in the order
+// (sequence, kv head, query tile, key tile), the second's in the order (sequence, kv
+// head, key tile, query tile).  A line is the steps of one output tile.
+struct Range {
+  int b, hk, tile;             // sequence, kv head, the line's query (first kernel) or key tile
+  int nt, len;                 // the sequence's key tiles and keys
+  int t;                       // step within the line
+  int left;                    // steps of the range from here on
+  // the next line (the range has more), of `lines` for each kv head (0: the key tiles)
+  FA4_DEV void line(const Params& a, int lines) {
+    t = 0;
+    if (++tile < (lines ? lines : nt)) return;
+    tile = 0;
+    if (++hk < a.p.Hkv) return;
+    hk = 0;
+    do {
+      ++b;
+      len = key_count(a.p, b, false);
+      nt = (len + BN - 1) / BN;
+    } while (nt == 0);
+  }
+};
+
+FA4_DEV int tiles_of(const Params& a, int b, bool report = false) {
+  return (key_count(a.p, b, report) + BN - 1) / BN;
+}
+
+// Steps of all sequences (one warp).
+FA4_DEV long long all_steps(const Params& a, int lane, bool report = false) {
+  long long all = 0;
+  if (!a.p.lens) {
+    all = (long long)a.p.B * a.key_tiles;
+  } else {
+    for (int x = lane; x < a.p.B; x += 32) all += tiles_of(a, x, report);
+    for (int o = 16; o > 0; o /= 2) all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  return all * a.p.Hkv * a.tiles;
+}
+
+// The first step of CTA `cta` of `total` steps.
+FA4_DEV long long range_start(const Params& a, long long total, int cta) { return total * cta / a.ctas; }
+
+// The place of a step (one warp); rows: in the first kernel's order.
+FA4_DEV void find_step(const Params& a, long long step, bool rows, int lane, Range& x) {
+  x.b = 0;
+  const long long per = (long long)a.p.Hkv * a.tiles;      // steps of a key tile of a sequence
+  if (!a.p.lens) {
+    x.b = (int)(step / (per * a.key_tiles));
+    step -= per * a.key_tiles * x.b;
+  } else {
+    // 32 sequences at a time
+    for (int x0 = 0;; x0 += 32) {
+      const long long n = x0 + lane < a.p.B ? tiles_of(a, x0 + lane) * per : 0;
+      long long upto = n;
+      for (int o = 1; o < 32; o *= 2) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, upto > step);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        x.b = x0 + at;
+        step -= __shfl_sync(0xffffffffu, upto - n, at);
+        break;
+      }
+      step -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  x.len = key_count(a.p, x.b, false);
+  x.nt = (x.len + BN - 1) / BN;
+  const int line = (int)(step / (rows ? x.nt : a.tiles)), lines = rows ? a.tiles : x.nt;
+  x.t = (int)(step % (rows ? x.nt : a.tiles));
+  x.hk = line / lines;
+  x.tile = line % lines;
+}
+
+// This CTA's range (one warp).
+FA4_DEV Range find_range(const Params& a, bool rows, int lane) {
+  Range x;
+  const long long total = all_steps(a, lane, rows && blockIdx.x == 0);
+  const long long s0 = range_start(a, total, blockIdx.x), s1 = range_start(a, total, blockIdx.x + 1);
+  x.b = x.hk = x.tile = x.nt = x.len = x.t = 0;
+  x.left = (int)(s1 - s0);
+  if (x.left > 0) find_step(a, s0, rows, lane, x);
+  return x;
+}
+
+// The place of an output tile's partial sums: [D / 4][128 rows][4] FP32, so that
+// the threads of a warp, a row each, write lines.
+FA4_DEV float* partial(float* part, int D, int which, int row, int column) {
+  return part + (long long)which * 128 * D + (column / 4 * 128 + row) * 4;
+}
+
+// ---------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------
 template <int D>
@@ -101,36 +203,29 @@ struct SmemQ {
   static constexpr int OFF_BAR = OFF_DEL + 2 * 1024;
   static constexpr int NBAR = 2 * KS + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int BYTES = OFF_MISC + 48;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
+// The range's items: key tiles [j0, j1) of a query tile.
 struct ItemQ {
-  int b, hk, tile, len, nt;
+  int b, hk, tile, len, j0, j1;
+  bool whole;
 };
 struct WalkQ {
-  int i, b = -1, len = 0;
-  FA4_DEV WalkQ() : i(blockIdx.x) {}
-  FA4_DEV bool at(const Params& a, ItemQ& it, bool report) {
-    if (i >= a.items) return false;
-    int bh;
-    divide(i, a.per_kv, bh, it.tile);
-    divide(bh, a.hkv, it.b, it.hk);
-    if (it.b != b) {
-      b = it.b;
-      len = key_count(a.p, b, report);
-    }
-    it.len = len;
-    it.nt = (len + BN - 1) / BN;
+  Range x;
+  FA4_DEV explicit WalkQ(const Range& r) : x(r) {}
+  FA4_DEV bool get(ItemQ& it) const {
+    if (x.left == 0) return false;
+    it.b = x.b; it.hk = x.hk; it.tile = x.tile; it.len = x.len;
+    it.j0 = x.t;
+    it.j1 = min(x.nt, x.t + x.left);
+    it.whole = it.j0 == 0 && it.j1 == x.nt;
     return true;
   }
-  FA4_DEV void next() { i += gridDim.x; }
-  FA4_DEV bool with_keys(const Params& a, ItemQ& it, bool report) {
-    while (at(a, it, report)) {
-      if (it.nt > 0) return true;
-      next();
-    }
-    return false;
+  FA4_DEV void next(const Params& a) {
+    x.left -= min(x.nt, x.t + x.left) - x.t;
+    if (x.left > 0) x.line(a, a.tiles);
   }
 };
 
@@ -165,6 +260,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   uint64_t* mma_done = dq_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  Range* range = reinterpret_cast<Range*>(smem + L::OFF_MISC + 8);
+  static_assert(sizeof(Range) <= 40, "range's place");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -189,11 +286,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   // (in this order: the next kernel reads its inputs before it waits for this one)
   wait_for_previous();
   next_may_start();
+  if (warp == W_PROD) {
+    const Range x = find_range(a, true, lane);
+    if (lane == 0) *range = x;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
   const int G = p.Hq / p.Hkv;
+  WalkQ w(*range);
+  ItemQ it;
 
   if (warp >= W_PROD) {
     setmaxnreg_dec<REG_MISC>();
@@ -216,9 +319,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           ++kn;
           return true;
         };
-        WalkQ w;
-        ItemQ it;
-        for (bool ok = true; ok && w.with_keys(a, it, true); w.next()) {
+        for (bool ok = true; ok && w.get(it); w.next(a)) {
           int g, n;
           divide(it.tile, a.per_head, g, n);
           const int h = it.hk * G + g * a.heads;
@@ -227,12 +328,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           if (qn > 0 && !mbar_wait(q_empty, (qn - 1) & 1, abort_flag, p.err)) break;
           load(a.q, q_tile, q_full, a.box, n, h, it.b);
           ++qn;
-          if (!load_kv(a.o, a.box, n, h, it.b) || !load_kv(a.k, BN, 0, it.hk, it.b)) break;
+          if (!load_kv(a.o, a.box, n, h, it.b) || !load_kv(a.k, BN, it.j0 * BN, it.hk, it.b)) break;
           if (dn > 0 && !mbar_wait(do_empty, (dn - 1) & 1, abort_flag, p.err)) break;
           load(a.dout, do_tile, do_full, a.box, n, h, it.b);
           ++dn;
-          ok = load_kv(a.v, BN, 0, it.hk, it.b);
-          for (int j = 1; ok && j < it.nt; ++j)
+          ok = load_kv(a.v, BN, it.j0 * BN, it.hk, it.b);
+          for (int j = it.j0 + 1; ok && j < it.j1; ++j)
             ok = load_kv(a.k, BN, j * BN, it.hk, it.b) && load_kv(a.v, BN, j * BN, it.hk, it.b);
         }
         if (*abort_flag) {
@@ -247,14 +348,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       // S of every step, once the one before has been read
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
-      WalkQ w;
-      ItemQ it;
       int kv = 0, n = 0;
       bool ok = true;
-      for (int i = 0; ok && w.with_keys(a, it, false); w.next(), ++i) {
+      for (int i = 0; ok && w.get(it); w.next(a), ++i) {
         ok = mbar_wait(qt_full, i & 1, abort_flag, p.err);
         ++kv;                              // (o)
-        for (int j = 0; ok && j < it.nt; ++j, ++n, kv += 2) {
+        for (int j = it.j0; ok && j < it.j1; ++j, ++n, kv += 2) {
           ok = mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err) &&
                (n == 0 || mbar_wait(s_free, (n - 1) & 1, abort_flag, p.err));
           if (!ok) break;
@@ -283,8 +382,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_q = idesc_f16(BM, D, true, false, true);
       const uint32_t sdo = smem_u32(do_tile);
-      WalkQ w;
-      ItemQ it;
       int k = 0, k_before = 0, n = 0;      // K of this step and of the one before it
       bool ok = true, add = false;
       // dQ += dS K of step m, whose K is at ring position k; last: of its item
@@ -302,13 +399,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         add = !last;
         return true;
       };
-      for (int i = 0; ok && w.with_keys(a, it, false); w.next(), ++i) {
-        for (int j = 0; ok && j < it.nt; ++j) {
-          if (j == 0) ++k;                 // (o)
+      for (int i = 0; ok && w.get(it); w.next(a), ++i) {
+        for (int j = it.j0; ok && j < it.j1; ++j) {
+          const bool first = j == it.j0;
+          if (first) ++k;                  // (o)
           const int v = k + 1;
-          if (j == 0 && n > 0) ok = issue_dq(n - 1, k_before, true);
+          if (first && n > 0) ok = issue_dq(n - 1, k_before, true);
           if (n > 0) ok = ok && mbar_wait(dp_free, (n - 1) & 1, abort_flag, p.err);
-          if (j == 0) ok = ok && mbar_wait(do_full, i & 1, abort_flag, p.err);
+          if (first) ok = ok && mbar_wait(do_full, i & 1, abort_flag, p.err);
           ok = ok && mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
@@ -317,10 +415,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
             product_rows<D>(tbase + COL_DP, sdo, sv, idesc_s);
             mma_commit(dp_full);
             mma_commit(&kv_empty[v % KS]);
-            if (j == it.nt - 1) mma_commit(do_empty);
+            if (j == it.j1 - 1) mma_commit(do_empty);
           }
           __syncwarp();
-          if (j > 0) ok = issue_dq(n - 1, k_before, false);
+          if (!first) ok = issue_dq(n - 1, k_before, false);
           ++n;
           k_before = k;
           k = v + 1;
@@ -341,17 +439,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     int n = 0, items = 0;                  // key tiles, items so far
     int kv = 0;                            // ring position of the item's o
     bool ok = true, leaving = false;       // leaving: a dQ is on its way out of shared memory
-    WalkQ w;
-    ItemQ it;
     if (p.lens)                            // queries without a key
-      for (; w.at(a, it, false); w.next()) {
-        int g, row;
-        tile_row(a, it.tile, r, G, g, row);
-        if (it.nt > 0 || g >= G) continue;
-        uint4* dst = reinterpret_cast<uint4*>(at(p.dq, it.b, it.hk * G + g, row) + half * (D / 2));
-        for (int i = 0; i < D / 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+      for (int i = blockIdx.x; i < a.items; i += gridDim.x) {
+        int bh, b, hk, tile, g, row;
+        divide(i, a.per_kv, bh, tile);
+        divide(bh, a.hkv, b, hk);
+        tile_row(a, tile, r, G, g, row);
+        if (g >= G || key_count(p, b, false) > 0) continue;
+        uint4* dst = reinterpret_cast<uint4*>(at(p.dq, b, hk * G + g, row) + half * (D / 2));
+        for (int x = 0; x < D / 16; ++x) dst[x] = make_uint4(0, 0, 0, 0);
       }
-    w = WalkQ();
     // the item's row and its lse
     bool valid = false;
     int h = 0, row = 0;
@@ -380,7 +477,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(qt_full);
       return true;
     };
-    bool more = w.with_keys(a, it, false);
+    bool more = w.get(it);
     if (more) {
       fetch(it);
       ok = take_q(0);
@@ -420,8 +517,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       }
       if (threadIdx.x == 0) mbar_arrive(&kv_empty[kv % KS]);
       if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
-      kv += 2 * it.nt + 1;
-      for (int j = 0; ok && j < it.nt; ++j, ++n) {
+      kv += 2 * (it.j1 - it.j0) + 1;
+      for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         float e[2][32];
@@ -480,8 +577,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       const ItemQ was = it;
       const bool here = valid;
       __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
-      w.next();
-      more = w.with_keys(a, it, false);
+      w.next(a);
+      more = w.get(it);
       if (more) {
         fetch(it);
         ok = ok && take_q(items + 1);
@@ -498,7 +595,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           tmem_ld32(lane_base + COL_DQ + half * (D / 2) + 32 * q, v);
           tmem_ld_wait();
           reg_fence32(v);
-          if (a.heads > 1) {
+          if (!was.whole) {
+            // (the first item of the range in slot 0, its last one in slot 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(partial(a.part_q, D, 2 * blockIdx.x + (items > 1), r,
+                                                half * (D / 2) + 32 * q + 4 * e)) =
+                  make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else if (a.heads > 1) {
             if (here) store32(dst + 32 * q, v, p.scale, a.dq32);
           } else {
             const float f = p.scale;
@@ -521,7 +625,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         int g, m;
         divide(was.tile, a.per_head, g, m);
         m = m * BM + 32 * quad;
-        if (ok && a.heads == 1 && m < p.Nq && (D == 128 || half == 0)) {
+        if (ok && was.whole && a.heads == 1 && m < p.Nq && (D == 128 || half == 0)) {
           tma_heads_store(a.dq, q_tile + (D == 128 ? half * CH : 0) + quad * 32 * 128, D == 128 ? 64 * half : 0, m,
                           was.hk * G + g, was.b);
           bulk_commit();
@@ -543,96 +647,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
 template <int D>
 struct SmemK {
   static constexpr int TILE = (D / 64) * CH;
-  static constexpr int RS = D == 128 ? 5 : 10;              // ring: Q, dO, Q, dO, ...
+  static constexpr int RS = D == 128 ? 4 : 8;               // ring: Q, dO, Q, dO, ...
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_R = 2 * TILE;
-  static constexpr int OFF_ST = OFF_R + RS * TILE;          // [2] x (lse log2 e [128], D [128])
+  static constexpr int OFF_OUT = OFF_R + RS * TILE;         // 64 channels of dV and of dK on their way out
+  static constexpr int OFF_ST = OFF_OUT + 2 * CH;           // [2] x (lse log2 e [128], D [128])
   static constexpr int OFF_BAR = OFF_ST + 2 * 1024;
   static constexpr int NBAR = 4 + 2 * RS + 4 + 7;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 64;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
-
-// Lines: the key tiles that hold keys, by sequence, kv head and position; a
-// line's steps are the kv head's query tiles.  The CTAs get equal ranges of all
-// steps.
-struct Lines {
-  int b, hk, tile;             // sequence, kv head, key tile
-  int nt, len;                 // the sequence's key tiles and keys
-  int t;                       // step within the line
-  int left;                    // steps of the range from here on
-  // to the next line (the range has more)
-  FA4_DEV void line(const Params& a) {
-    t = 0;
-    if (++tile < nt) return;
-    tile = 0;
-    if (++hk < a.p.Hkv) return;
-    hk = 0;
-    do {
-      ++b;
-      len = key_count(a.p, b, false);
-      nt = (len + BN - 1) / BN;
-    } while (nt == 0);
-  }
-};
-
-FA4_DEV int tiles_of(const Params& a, int b) { return (key_count(a.p, b, false) + BN - 1) / BN; }
-
-// Key tiles that hold keys, of all sequences (one warp).
-FA4_DEV long long all_tiles(const Params& a, int lane) {
-  if (!a.p.lens) return (long long)a.p.B * a.key_tiles;
-  long long all = 0;
-  for (int x = lane; x < a.p.B; x += 32) all += tiles_of(a, x);
-  for (int o = 16; o > 0; o /= 2) all += __shfl_xor_sync(0xffffffffu, all, o);
-  return all;
-}
-
-// The first step of CTA `cta` of `total` steps.
-FA4_DEV long long range_start(const Params& a, long long total, int cta) { return total * cta / a.ctas; }
-
-// The sequence, kv head and key tile of a line (one warp).
-FA4_DEV void find_line(const Params& a, long long line, int lane, Lines& x) {
-  x.b = 0;
-  if (!a.p.lens) {
-    x.b = (int)(line / ((long long)a.p.Hkv * a.key_tiles));
-    line -= (long long)x.b * a.p.Hkv * a.key_tiles;
-  } else {
-    // 32 sequences at a time
-    for (int x0 = 0;; x0 += 32) {
-      const long long n = x0 + lane < a.p.B ? (long long)tiles_of(a, x0 + lane) * a.p.Hkv : 0;
-      long long upto = n;
-      for (int o = 1; o < 32; o *= 2) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, upto > line);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        x.b = x0 + at;
-        line -= __shfl_sync(0xffffffffu, upto - n, at);
-        break;
-      }
-      line -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
-  x.len = key_count(a.p, x.b, false);
-  x.nt = (x.len + BN - 1) / BN;
-  x.hk = (int)line / x.nt;
-  x.tile = (int)line % x.nt;
-}
-
-// This CTA's range (one warp).
-FA4_DEV Lines find_range(const Params& a, int lane) {
-  Lines x;
-  const long long total = all_tiles(a, lane) * a.p.Hkv * a.tiles;
-  const long long s0 = range_start(a, total, blockIdx.x), s1 = range_start(a, total, blockIdx.x + 1);
-  x.left = (int)(s1 - s0);
-  x.b = x.hk = x.tile = x.nt = x.t = x.len = 0;
-  if (x.left == 0) return x;
-  x.t = (int)(s0 % a.tiles);
-  find_line(a, s0 / a.tiles, lane, x);
-  return x;
-}
 
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_constant__ Params a) {
@@ -664,8 +688,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   uint64_t* mma_done = acc_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  Lines* range = reinterpret_cast<Lines*>(smem + L::OFF_MISC + 8);
-  static_assert(sizeof(Lines) <= 56, "range's place");
+  Range* range = reinterpret_cast<Range*>(smem + L::OFF_MISC + 8);
+  static_assert(sizeof(Range) <= 56, "range's place");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -688,7 +712,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       reinterpret_cast<uint4*>(smem + L::OFF_R)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == W_PROD) {
-    const Lines x = find_range(a, lane);
+    const Range x = find_range(a, false, lane);
     if (lane == 0) *range = x;
   }
   if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
@@ -697,7 +721,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
   const int G = p.Hq / p.Hkv;
-  Lines at_ = *range;
+  Range at_ = *range;
 
   if (warp >= W_PROD) {
     setmaxnreg_dec<REG_MISC>();
@@ -737,7 +761,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           fresh = false;
           --at_.left;
           if (++at_.t == a.tiles && at_.left > 0) {
-            at_.line(a);
+            at_.line(a, 0);
             fresh = true;
           }
         }
@@ -781,7 +805,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&st_full[st]);
         --at_.left;
         if (at_.left == 0) break;
-        if (++at_.t == a.tiles) at_.line(a);
+        if (++at_.t == a.tiles) at_.line(a, 0);
         fetch();
       }
     } else if (warp == W_MMA || warp == W_MMA_B) {
@@ -929,11 +953,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       tc_fence_after();
       const bool whole = s0 == 0 && s1 == a.tiles;
       const int key = at_.tile * BN + r;
-      const bool mine = key < p.Nk;
-      const float f = key < at_.len ? (half ? p.scale : 1.f) : 0.f;
-      __nv_bfloat16* dst = mine ? at(half ? p.dk : p.dv, at_.b, at_.hk, key) : nullptr;
-      // partials: slot 0 for the range's first line, 1 for its last
-      float* part = a.part + ((((long long)blockIdx.x * 2 + (lines > 0)) * 2 + half) * BN + r) * D;
+      const float f = half ? p.scale : 1.f;
+      uint8_t* out = smem + L::OFF_OUT + half * CH;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t v[32];
@@ -946,36 +967,61 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
         if (!whole) {
+          // (the first line of the range in slot 0, its last one in slot 1)
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(part + 32 * q + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else if (mine) {
-          store32(dst + 32 * q, v, f, half ? a.dk32 : a.dv32);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(partial(a.part, D, (2 * blockIdx.x + (lines > 0)) * 2 + half, r, 32 * q + 4 * e)) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          continue;
+        }
+        // rows by themselves would be 32 places a store: they leave in boxes of 32 rows and 64 channels
+        if (q % 2 == 0) {
+          if (lane == 0) bulk_wait_read0();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            pk[i] = pack2(__uint_as_float(v[8 * e + 2 * i]) * f, __uint_as_float(v[8 * e + 2 * i + 1]) * f);
+          *tile_word(out, r, q % 2 * 4 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (q % 2 == 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && at_.tile * BN + 32 * quad < p.Nk) {
+            tma_heads_store(half ? a.dk : a.dv, out + quad * 32 * 128, q / 2 * 64, at_.tile * BN + 32 * quad, at_.hk,
+                            at_.b);
+            bulk_commit();
+          }
         }
       }
       tc_fence_before();
       ++lines;
       at_.left -= s1 - s0;
-      if (at_.left > 0) at_.line(a);
+      if (at_.left > 0) at_.line(a, 0);
     }
+    if (lane == 0) bulk_wait_read0();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
-// dV (y = 0) and dK (y = 1) of the key tiles whose steps lie in several ranges: the x
-// below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside a key tile's steps
-// and began at or before their first.  Then, where sequences have lengths, zeros for the
-// key tiles behind them: an x for each sequence and kv head.
+// dV (y = 0), dK (y = 1) and dQ (y = 2) of the output tiles whose steps lie in
+// several ranges: the x below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside
+// a tile's steps and began at or before their first.  Then, where sequences have
+// lengths, zeros for the key tiles behind them: an x for each sequence and kv head.
 constexpr int JOIN_PARTS = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
   const CrossParams& p = a.p;
   wait_for_previous();
-  const int which = blockIdx.y;
-  const Strided& out = which ? p.dk : p.dv;
+  const int which = blockIdx.y, G = p.Hq / p.Hkv;
+  const Strided& out = which == 2 ? p.dq : which ? p.dk : p.dv;
   if ((int)blockIdx.x >= a.ctas) {
+    if (which == 2) return;
     int b, hk;
     divide((int)blockIdx.x - a.ctas, a.hkv, b, hk);
     const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
@@ -984,17 +1030,17 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     return;
   }
   const int c0 = blockIdx.x;
-  __shared__ Lines place;
+  __shared__ Range place;
   __shared__ long long sum;
   if (threadIdx.x < 32) {
-    const long long total = all_tiles(a, threadIdx.x) * p.Hkv * a.tiles;
-    const long long end = range_start(a, total, c0 + 1);
-    Lines x;
+    const long long total = all_steps(a, threadIdx.x);
+    const long long start = range_start(a, total, c0), end = range_start(a, total, c0 + 1);
+    Range x;
     x.left = 0;
-    // (a range that ends with its key tile's steps, or began inside them, joins nothing)
-    if (end > range_start(a, total, c0) && end % a.tiles != 0 && range_start(a, total, c0) <= end / a.tiles * a.tiles) {
-      x.left = 1;
-      find_line(a, end / a.tiles, threadIdx.x, x);
+    if (end > start && end < total) {
+      find_step(a, end, which == 2, threadIdx.x, x);
+      // (a range that ends with a tile's steps, or began inside them, joins nothing)
+      x.left = x.t > 0 && start <= end - x.t;
     }
     if (threadIdx.x == 0) {
       place = x;
@@ -1003,25 +1049,37 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   }
   __syncthreads();
   if (!place.left) return;
-  const long long total = sum, first = range_start(a, total, c0 + 1) / a.tiles * a.tiles;
-  for (int x = blockIdx.z * 256 + threadIdx.x; x < BN * (D / 8); x += JOIN_PARTS * 256) {
-    const int r = x / (D / 8), i = x % (D / 8) * 8, key = place.tile * BN + r;
-    if (key >= p.Nk) break;
+  const long long total = sum, first = range_start(a, total, c0 + 1) - place.t;
+  const long long last = first + (which == 2 ? place.nt : a.tiles);
+  const float f = which ? p.scale : 1.f;
+  for (int x = blockIdx.z * 256 + threadIdx.x; x < 128 * (D / 8); x += JOIN_PARTS * 256) {
+    const int r = x % 128, i = x / 128 * 8;
     float v[8] = {};
     for (int c = c0; c < a.ctas; ++c) {
       const long long s = range_start(a, total, c);
-      if (s >= first + a.tiles) break;
+      if (s >= last) break;
       if (range_start(a, total, c + 1) == s) continue;
-      // slot 0, unless the range began in a line before
-      const float* from = a.part + ((((long long)c * 2 + (s < first)) * 2 + which) * BN + r) * D + i;
-      const float4 u = *reinterpret_cast<const float4*>(from), w = *reinterpret_cast<const float4*>(from + 4);
+      // slot 0, unless the range began in a tile before
+      const int slot = 2 * c + (s < first);
+      float* part = which == 2 ? a.part_q : a.part;
+      const int at = which == 2 ? slot : 2 * slot + which;
+      const float4 u = *reinterpret_cast<const float4*>(partial(part, D, at, r, i));
+      const float4 w = *reinterpret_cast<const float4*>(partial(part, D, at, r, i + 4));
       v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
       v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
     }
-    const float f = which ? p.scale : 1.f;
-    *reinterpret_cast<uint4*>(at(out, place.b, place.hk, key) + i) =
-        make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
-                   pack2(v[6] * f, v[7] * f));
+    int h = place.hk, row = place.tile * BN + r;
+    bool valid = row < p.Nk;
+    if (which == 2) {
+      int g;
+      tile_row(a, place.tile, r, G, g, row);
+      valid = g < G;
+      h = place.hk * G + g;
+    }
+    if (valid)
+      *reinterpret_cast<uint4*>(at(out, place.b, h, row) + i) =
+          make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
+                     pack2(v[6] * f, v[7] * f));
   }
 }
 
@@ -1074,7 +1132,7 @@ size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   // (heads that share no tile make more tiles, never fewer CTAs)
   Params a;
   plan(a, B, Hq, Hkv, Nq, Nk, false);
-  return del_bytes(B, Hq, Nq) + (size_t)a.ctas * 4 * BN * d * sizeof(float);
+  return del_bytes(B, Hq, Nq) + (size_t)a.ctas * 6 * 128 * d * sizeof(float);
 }
 
 cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
@@ -1086,26 +1144,28 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   Params a;
   a.p = p;
   plan(a, p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.q.h != 0 && p.dout.h != 0 && p.o.h != 0);
-  a.dq32 = on_words(p.dq); a.dk32 = on_words(p.dk); a.dv32 = on_words(p.dv);
+  a.dq32 = on_words(p.dq);
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
+  a.part_q = a.part + (size_t)a.ctas * 4 * 128 * p.d;
   const int rows = a.heads > 1 ? p.Nq : BM;
   if (!heads_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.dout, p.dout, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.o, p.o, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.k, p.k, p.B, p.Hkv, p.Nk, p.d, BN, 1) || !heads_map(&a.v, p.v, p.B, p.Hkv, p.Nk, p.d, BN, 1) ||
-      !heads_map(&a.dq, p.dq, p.B, p.Hq, p.Nq, p.d, 32, 1))
+      !heads_map(&a.dq, p.dq, p.B, p.Hq, p.Nq, p.d, 32, 1) || !heads_map(&a.dk, p.dk, p.B, p.Hkv, p.Nk, p.d, 32, 1) ||
+      !heads_map(&a.dv, p.dv, p.B, p.Hkv, p.Nk, p.d, 32, 1))
     return cudaErrorInvalidValue;
-  const int sms = sm_count();
-  const dim3 gq(a.items < sms ? a.items : sms), gk(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 2, JOIN_PARTS);
-  // no range ends inside a key tile's steps, and no key is without one?
+  const dim3 grid(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 3, JOIN_PARTS);
+  // no range ends inside an output tile's steps, and no key is without one?
   const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
-  const bool join = p.lens || (a.tiles > 1 && (steps % a.ctas != 0 || steps / a.ctas % a.tiles != 0));
+  const auto apart = [&](int line) { return line == 1 || (steps % a.ctas == 0 && steps / a.ctas % line == 0); };
+  const bool join = p.lens || !apart(a.tiles) || !apart(a.key_tiles);
   const bool wide = p.d == 128;
-  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, gq, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
+  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
                         true, a, st);
   if (e == cudaSuccess)
-    e = start(wide ? cross_dkv_kernel<128> : cross_dkv_kernel<64>, gk, wide ? SmemK<128>::BYTES : SmemK<64>::BYTES,
+    e = start(wide ? cross_dkv_kernel<128> : cross_dkv_kernel<64>, grid, wide ? SmemK<128>::BYTES : SmemK<64>::BYTES,
               true, a, st);
   if (e == cudaSuccess && join) e = launch(wide ? cross_join_kernel<128> : cross_join_kernel<64>, gj, 256, 0, true, st, a);
   return e;
