@@ -57,7 +57,7 @@ struct Params {
   int key_tiles;                               // of Nk
   int items;                                   // query tiles in all
   int ctas;                                    // of both kernels
-  int dq32;                                    // dq's rows begin on 32 bytes
+  int dq32, dk32, dv32;                        // rows begin on 32 bytes
   float* del;                                  // D [B][Hq][Nq]
   float *part, *part_q;                        // partial sums: [2 ctas][dV, dK] and [2 ctas] tiles of dQ
 };
@@ -121,6 +121,12 @@ struct Range {
   }
 };
 
+// a / b for 0 <= a, 0 < b: in 32 bits where they fit (64-bit divisions take some
+// 500 cycles, and a kernel's start has several in a row).
+FA4_DEV long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 FA4_DEV int tiles_of(const Params& a, int b, bool report = false) {
   return (key_count(a.p, b, report) + BN - 1) / BN;
 }
@@ -138,14 +144,14 @@ FA4_DEV long long all_steps(const Params& a, int lane, bool report = false) {
 }
 
 // The first step of CTA `cta` of `total` steps.
-FA4_DEV long long range_start(const Params& a, long long total, int cta) { return total * cta / a.ctas; }
+FA4_DEV long long range_start(const Params& a, long long total, int cta) { return quotient(total * cta, a.ctas); }
 
 // The place of a step (one warp); rows: in the first kernel's order.
 FA4_DEV void find_step(const Params& a, long long step, bool rows, int lane, Range& x) {
   x.b = 0;
   const long long per = (long long)a.p.Hkv * a.tiles;      // steps of a key tile of a sequence
   if (!a.p.lens) {
-    x.b = (int)(step / (per * a.key_tiles));
+    x.b = (int)quotient(step, per * a.key_tiles);
     step -= per * a.key_tiles * x.b;
   } else {
     // 32 sequences at a time
@@ -168,10 +174,11 @@ FA4_DEV void find_step(const Params& a, long long step, bool rows, int lane, Ran
   }
   x.len = key_count(a.p, x.b, false);
   x.nt = (x.len + BN - 1) / BN;
-  const int line = (int)(step / (rows ? x.nt : a.tiles)), lines = rows ? a.tiles : x.nt;
-  x.t = (int)(step % (rows ? x.nt : a.tiles));
+  const int each = rows ? x.nt : a.tiles, lines = rows ? a.tiles : x.nt;
+  const int line = (int)quotient(step, each);
+  x.t = (int)(step - (long long)line * each);
   x.hk = line / lines;
-  x.tile = line % lines;
+  x.tile = line - x.hk * lines;
 }
 
 // This CTA's range (one warp).
@@ -644,13 +651,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // dK, dV
 // ---------------------------------------------------------------------------
-template <int D>
+// STAGED: dV and dK leave in boxes of 32 rows through shared memory (2 tiles of 64
+// channels).  At d = 128 that takes a place of the ring of five, which costs long lines
+// more than their ends gain: lines of up to STAGED_STEPS steps do so (24 heads of 2048
+// keys: 1 step 36.7 against 38.6 us, 8 steps 101.9 and 103.9, 16 steps 159 and 161, 64
+// steps 530 and 509).
+constexpr int STAGED_STEPS = 24;
+template <int D, bool STAGED>
 struct SmemK {
   static constexpr int TILE = (D / 64) * CH;
-  static constexpr int RS = D == 128 ? 4 : 8;               // ring: Q, dO, Q, dO, ...
+  static constexpr int RS = D == 128 ? (STAGED ? 4 : 5) : 8; // ring: Q, dO, Q, dO, ...
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_R = 2 * TILE;
   static constexpr int OFF_OUT = OFF_R + RS * TILE;         // 64 channels of dV and of dK on their way out
-  static constexpr int OFF_ST = OFF_OUT + 2 * CH;           // [2] x (lse log2 e [128], D [128])
+  static constexpr int OFF_ST = OFF_OUT + (STAGED ? 2 * CH : 0);   // [2] x (lse log2 e [128], D [128])
   static constexpr int OFF_BAR = OFF_ST + 2 * 1024;
   static constexpr int NBAR = 4 + 2 * RS + 4 + 7;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -658,9 +671,9 @@ struct SmemK {
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
-template <int D>
+template <int D, bool STAGED>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_constant__ Params a) {
-  using L = SmemK<D>;
+  using L = SmemK<D, STAGED>;
   constexpr int RS = L::RS;
   constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
   const CrossParams& p = a.p;
@@ -974,6 +987,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
                 make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           continue;
         }
+        if (!STAGED) {
+          if (key < p.Nk) store32(at(half ? p.dk : p.dv, at_.b, at_.hk, key) + 32 * q, v, f, half ? a.dk32 : a.dv32);
+          continue;
+        }
         // rows by themselves would be 32 places a store: they leave in boxes of 32 rows and 64 channels
         if (q % 2 == 0) {
           if (lane == 0) bulk_wait_read0();
@@ -1013,61 +1030,83 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
 // several ranges: the x below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside
 // a tile's steps and began at or before their first.  Then, where sequences have
 // lengths, zeros for the key tiles behind them: an x for each sequence and kv head.
-constexpr int JOIN_PARTS = 8;
+constexpr int JOIN_PARTS = 2;
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
   const CrossParams& p = a.p;
-  wait_for_previous();
   const int which = blockIdx.y, G = p.Hq / p.Hkv;
   const Strided& out = which == 2 ? p.dq : which ? p.dk : p.dv;
   if ((int)blockIdx.x >= a.ctas) {
-    if (which == 2) return;
+    wait_for_previous();
+    if (which == 2 || blockIdx.z > 0) return;
     int b, hk;
     divide((int)blockIdx.x - a.ctas, a.hkv, b, hk);
     const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
-    for (long long x = blockIdx.z * 256 + threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += JOIN_PARTS * 256)
+    for (long long x = threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += 256)
       *reinterpret_cast<uint4*>(at(out, b, hk, from + (int)(x / (D / 8))) + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
   const int c0 = blockIdx.x;
   __shared__ Range place;
+  __shared__ int slot0, c1, thin;
   __shared__ long long sum;
   if (threadIdx.x < 32) {
-    const long long total = all_steps(a, threadIdx.x);
+    const int lane = threadIdx.x;
+    const long long total = all_steps(a, lane);
     const long long start = range_start(a, total, c0), end = range_start(a, total, c0 + 1);
     Range x;
     x.left = 0;
     if (end > start && end < total) {
-      find_step(a, end, which == 2, threadIdx.x, x);
+      find_step(a, end, which == 2, lane, x);
       // (a range that ends with a tile's steps, or began inside them, joins nothing)
       x.left = x.t > 0 && start <= end - x.t;
     }
-    if (threadIdx.x == 0) {
-      place = x;
-      sum = total;
+    if (x.left) {
+      // the last range that meets the tile's steps
+      const long long last = end - x.t + (which == 2 ? x.nt : a.tiles);
+      int c = c0;
+      for (;;) {
+        const unsigned more =
+            __ballot_sync(0xffffffffu, c + 1 + lane < a.ctas && range_start(a, total, c + 1 + lane) < last);
+        c += __popc(more);
+        if (~more) break;
+      }
+      if (lane == 0) {
+        slot0 = 2 * c0 + (start < end - x.t);      // (slot 1 where the range began in a tile before)
+        c1 = c;
+        thin = total < a.ctas;                     // some ranges are empty: each has a step at most
+        sum = total;
+      }
     }
+    if (lane == 0) place = x;
   }
+  // (where the sums lie follows from the shapes and lengths: the partials are waited for after that, by every CTA,
+  // so that this kernel does not end before the ones before it)
+  wait_for_previous();
   __syncthreads();
   if (!place.left) return;
-  const long long total = sum, first = range_start(a, total, c0 + 1) - place.t;
-  const long long last = first + (which == 2 ? place.nt : a.tiles);
   const float f = which ? p.scale : 1.f;
-  for (int x = blockIdx.z * 256 + threadIdx.x; x < 128 * (D / 8); x += JOIN_PARTS * 256) {
-    const int r = x % 128, i = x / 128 * 8;
-    float v[8] = {};
-    for (int c = c0; c < a.ctas; ++c) {
-      const long long s = range_start(a, total, c);
-      if (s >= last) break;
-      if (range_start(a, total, c + 1) == s) continue;
-      // slot 0, unless the range began in a tile before
-      const int slot = 2 * c + (s < first);
-      float* part = which == 2 ? a.part_q : a.part;
-      const int at = which == 2 ? slot : 2 * slot + which;
-      const float4 u = *reinterpret_cast<const float4*>(partial(part, D, at, r, i));
-      const float4 w = *reinterpret_cast<const float4*>(partial(part, D, at, r, i + 4));
-      v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
-      v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+  float* part = which == 2 ? a.part_q : a.part;
+  constexpr int EACH = 128 * (D / 8) / (256 * JOIN_PARTS);      // of a thread: rows' 8 columns
+  const int x0 = blockIdx.z * 256 + threadIdx.x;
+  float v[EACH][8] = {};
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    if (thin && range_start(a, sum, c + 1) == range_start(a, sum, c)) continue;
+    const int slot = c == c0 ? slot0 : 2 * c;
+    const int at = which == 2 ? slot : 2 * slot + which;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const int x = x0 + e * 256 * JOIN_PARTS;
+      const float4 u = *reinterpret_cast<const float4*>(partial(part, D, at, x % 128, x / 128 * 8));
+      const float4 w = *reinterpret_cast<const float4*>(partial(part, D, at, x % 128, x / 128 * 8 + 4));
+      v[e][0] += u.x; v[e][1] += u.y; v[e][2] += u.z; v[e][3] += u.w;
+      v[e][4] += w.x; v[e][5] += w.y; v[e][6] += w.z; v[e][7] += w.w;
     }
+  }
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int x = x0 + e * 256 * JOIN_PARTS, r = x % 128, i = x / 128 * 8;
     int h = place.hk, row = place.tile * BN + r;
     bool valid = row < p.Nk;
     if (which == 2) {
@@ -1077,9 +1116,9 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
       h = place.hk * G + g;
     }
     if (valid)
-      *reinterpret_cast<uint4*>(at(out, place.b, h, row) + i) =
-          make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
-                     pack2(v[6] * f, v[7] * f));
+      *reinterpret_cast<uint4*>(fa4::at(out, place.b, h, row) + i) =
+          make_uint4(pack2(v[e][0] * f, v[e][1] * f), pack2(v[e][2] * f, v[e][3] * f), pack2(v[e][4] * f, v[e][5] * f),
+                     pack2(v[e][6] * f, v[e][7] * f));
   }
 }
 
@@ -1144,7 +1183,7 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   Params a;
   a.p = p;
   plan(a, p.B, p.Hq, p.Hkv, p.Nq, p.Nk, p.q.h != 0 && p.dout.h != 0 && p.o.h != 0);
-  a.dq32 = on_words(p.dq);
+  a.dq32 = on_words(p.dq); a.dk32 = on_words(p.dk); a.dv32 = on_words(p.dv);
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
   a.part_q = a.part + (size_t)a.ctas * 4 * 128 * p.d;
@@ -1164,9 +1203,11 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   const bool wide = p.d == 128;
   cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
                         true, a, st);
+  const bool staged = !wide || a.tiles <= STAGED_STEPS;
   if (e == cudaSuccess)
-    e = start(wide ? cross_dkv_kernel<128> : cross_dkv_kernel<64>, grid, wide ? SmemK<128>::BYTES : SmemK<64>::BYTES,
-              true, a, st);
+    e = start(!wide ? cross_dkv_kernel<64, true> : staged ? cross_dkv_kernel<128, true> : cross_dkv_kernel<128, false>,
+              grid, !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a,
+              st);
   if (e == cudaSuccess && join) e = launch(wide ? cross_join_kernel<128> : cross_join_kernel<64>, gj, 256, 0, true, st, a);
   return e;
 }
