@@ -27,8 +27,8 @@ struct HeadsMap {
 };
 bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads);
 
-// Up to CROSS_TOKEN_ROWS query rows of a kv head (Hq / Hkv * Nq).
-constexpr int CROSS_TOKEN_ROWS = 32;
+// Few query rows: keys shared among clusters, products of 16 rows.
+bool cross_few_rows(const CrossParams& p);
 cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st);
 cudaError_t launch_cross_fwd(const CrossParams& p, cudaStream_t st);
 size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d);

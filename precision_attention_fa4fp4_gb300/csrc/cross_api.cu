@@ -228,8 +228,7 @@ fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.d = d;
   p.scale = softmax_scale_of(softmax_scale, d);
   p.c = (float)((double)p.scale * 1.4426950408889634);
-  const bool few = (long long)(Hq / Hkv) * Nq <= CROSS_TOKEN_ROWS;
-  return status_of((few ? launch_cross_token : launch_cross_fwd)(p, static_cast<cudaStream_t>(stream)));
+  return status_of((cross_few_rows(p) ? launch_cross_token : launch_cross_fwd)(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fa4bf16_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {

@@ -1,5 +1,5 @@
-// cross_token.cu -- cross attention of few query rows (up to 32 per kv head: the
-// new tokens of a decoding step, all query heads of a kv head together).
+// cross_token.cu -- cross attention of few query rows (the new tokens of a decoding
+// step, all query heads of a kv head together; a CTA has up to 32 of them).
 //
 // Bound by reading K and V once.  A CTA (4 warps) works on one (sequence, kv head)
 // or on a part of its keys: a cluster of up to 16 CTAs shares them where there are
@@ -20,12 +20,17 @@
 namespace fa4 {
 namespace {
 
-constexpr int WARPS = 4, STAGES = 3;
+constexpr int WARPS = 4;
+// Stages of a warp's ring: with two of them, 32 rows of d = 128 leave room for 2 CTAs
+// on a multiprocessor.
+template <int D, int MT>
+constexpr int STAGES_OF = D == 128 && MT == 2 ? 2 : 3;
 
 struct Params {
   CrossParams p;
   HeadsMap k, v;
   int splits;                    // CTAs of a cluster
+  Divisor groups, hkv, nq;       // groups of 16 MT query rows of a (sequence, kv head)
 };
 
 // 8 KB of K and V a block: 16 keys at d = 128, 32 at d = 64.
@@ -70,13 +75,13 @@ template <int D, int MT>
 struct Smem {
   static constexpr int CHUNK = KEYS<D> * 128;              // [keys][64 channels], 128-byte swizzle
   static constexpr int TILE = (D / 64) * CHUNK;            // 4 KB
-  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STAGE = 2 * TILE, STAGES = STAGES_OF<D, MT>;
   static constexpr int RING = WARPS * STAGES * STAGE;      // 24 KB a warp
   // after the loop the rings' place holds the warps' O, m and l
   static constexpr int ROWS = 16 * MT;
   static constexpr int WARP_F = ROWS * (D + 2);            // floats of one warp: O [ROWS][D], m, l
-  static_assert(WARPS * WARP_F * 4 <= RING, "join fits the rings");
-  static constexpr int OFF_BAR = RING;
+  static constexpr int JOIN = WARPS * WARP_F * 4;
+  static constexpr int OFF_BAR = RING > JOIN ? RING : JOIN;
   // what the cluster's CTAs give this one: (m, l) of all rows, and their O of its share of the outputs
   static constexpr int OFF_ML = OFF_BAR + WARPS * STAGES * 8 + 32;
   static constexpr int OFF_O = OFF_ML + 16 * ROWS * 8;
@@ -87,7 +92,7 @@ struct Smem {
 template <int D, int MT>
 __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_constant__ Params a) {
   using L = Smem<D, MT>;
-  constexpr int NK = KEYS<D>;
+  constexpr int NK = KEYS<D>, STAGES = L::STAGES;
   const CrossParams& p = a.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -95,8 +100,10 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + WARPS * STAGES);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = a.splits > 1 ? (int)cluster_rank() : 0;
-  const int bh = blockIdx.x / a.splits, b = bh / p.Hkv, hk = bh % p.Hkv;
-  const int G = p.Hq / p.Hkv, R = G * p.Nq;
+  int bh, group, b, hk;
+  divide((int)blockIdx.x / a.splits, a.groups, bh, group);
+  divide(bh, a.hkv, b, hk);
+  const int G = p.Hq / p.Hkv, r0 = group * L::ROWS, R = min(G * p.Nq - r0, L::ROWS);
   uint64_t* full = bars + warp * STAGES;
   uint8_t* ring = smem + warp * STAGES * L::STAGE;
   if (lane == 0) {
@@ -131,7 +138,9 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = 16 * t + lane / 4 + 8 * half;
-      const __nv_bfloat16* q = r < R ? at(p.q, b, hk * G + r / p.Nq, r % p.Nq) + 2 * (lane % 4) : nullptr;
+      int g, n;
+      divide(r0 + r, a.nq, g, n);
+      const __nv_bfloat16* q = r < R ? at(p.q, b, hk * G + g, n) + 2 * (lane % 4) : nullptr;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         qf[t][k][half] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
@@ -289,7 +298,9 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
     }
   __syncthreads();
   auto store = [&](int r, int i, float v0, float v1, float top, float sum) {
-    const int h = hk * G + r / p.Nq, n = r % p.Nq;
+    int g, n;
+    divide(r0 + r, a.nq, g, n);
+    const int h = hk * G + g;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *reinterpret_cast<uint32_t*>(at(p.o, b, h, n) + i) = pack2(v0 * inv, v1 * inv);
     if (i == 0 && p.lse)
@@ -347,6 +358,47 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
 
 }  // namespace
 
+namespace {
+
+// CTAs that share a (sequence, kv head, row group)'s keys: a cluster, while there are
+// more multiprocessors than CTAs (2 fit on one) and at least two blocks for each warp.
+int splits_of(long long heads, int Nk, int d) {
+  const int sms = sm_count(), nk = 2048 / d;
+  int n = 1;
+  while (n < 16 && heads * n * 2 <= 2LL * sms && Nk >= n * 2 * WARPS * 2 * nk) n *= 2;
+  return n;
+}
+
+}  // namespace
+
+// Which of the two kernels is quicker, by what 376 shapes (heads of 64 and 128, 1 to
+// 128 of them, 8 to 256 rows, 50 to 8000 keys) took, in ns.  This kernel: a start,
+// 0.6 us for a cluster's join, and a time for each block in a warp's turn, times the
+// waves of CTAs (within 12% on average).  The kernel of 128-row tiles: a start, and for
+// each wave of CTAs a start and a time per key tile (within 5%).  The quicker by this
+// rule is the quicker one but for 0.6% on average and 21% at most; 32 rows as the border
+// loses 19% on average.  One sequence of 8000 keys, 8 heads of 64: 12.8 us here for 32
+// rows each and 27.4 for 256, 75 and 100 there; of 100 keys 6.6 here, 5.9 there.
+bool cross_few_rows(const CrossParams& p) {
+  const int G = p.Hq / p.Hkv, sms = sm_count(), d = p.d;
+  const long long H = (long long)p.B * p.Hkv, rows = (long long)G * p.Nq;
+  const bool two = rows > 16;
+  const long long heads = H * (two ? (rows + 31) / 32 : 1);
+  if (heads > (1 << 24)) return false;
+  const int n = splits_of(heads, p.Nk, d), nk = 2048 / d;
+  const long long blocks = ((p.Nk + nk - 1) / nk + WARPS * n - 1) / (WARPS * n);
+  const double start = d == 128 ? (two ? 9000 : 4300) : (two ? 5000 : 3700);
+  const double block = d == 128 ? (two ? 1350 : 1090) : (two ? 1440 : 860);
+  const double waves = (double)heads * n / (2.0 * sms);
+  const double here = start + (n > 1 ? 600 : 0) + block * blocks * (waves > 1 ? waves : 1);
+  const int share = p.Nq <= 64 ? (128 / p.Nq < G ? 128 / p.Nq : G) : 1;
+  const long long tiles = share > 1 ? (G + share - 1) / share : (long long)G * ((p.Nq + 127) / 128);
+  const double turns = (double)((H * ((tiles + 1) / 2) + sms - 1) / sms);
+  const double tile = d == 128 ? (tiles > 1 ? 1900 : 1250) : (tiles > 1 ? 1550 : 1120);
+  const double there = 2300 + turns * (2300 + tile * ((p.Nk + 127) / 128));
+  return here < there;
+}
+
 cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st) {
   Params a;
   a.p = p;
@@ -358,19 +410,19 @@ cudaError_t launch_cross_token(const CrossParams& p, cudaStream_t st) {
     memset(&a.k, 0, sizeof(a.k));          // never loaded from
     a.v = a.k;
   }
-  // a cluster shares a head's keys while there are more multiprocessors than CTAs
-  // and at least two blocks for each of its warps
-  const long long heads = (long long)p.B * p.Hkv;
-  const int sms = sm_count();
-  a.splits = 1;
-  while (a.splits < 16 && heads * a.splits * 2 <= 2LL * sms && p.Nk >= a.splits * 2 * WARPS * 2 * nk) a.splits *= 2;
-  const bool two = p.Hq / p.Hkv * p.Nq > 16, wide = p.d == 128;
+  const int rows = p.Hq / p.Hkv * p.Nq;
+  const bool two = rows > 16, wide = p.d == 128;
+  a.groups = Divisor((rows + 31) / 32);
+  a.hkv = Divisor(p.Hkv);
+  a.nq = Divisor(p.Nq);
+  const long long heads = (long long)p.B * p.Hkv * a.groups.d;
+  a.splits = splits_of(heads, p.Nk, p.d);
   const int n = a.splits;
   auto k = wide ? (two ? cross_token_kernel<128, 2> : cross_token_kernel<128, 1>)
                 : (two ? cross_token_kernel<64, 2> : cross_token_kernel<64, 1>);
   const int smem = wide ? (two ? Smem<128, 2>::bytes(n) : Smem<128, 1>::bytes(n))
                         : (two ? Smem<64, 2>::bytes(n) : Smem<64, 1>::bytes(n));
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), Smem<128, 2>::bytes(16), true);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), 112 * 1024, true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(heads * a.splits));
