@@ -73,6 +73,61 @@ def test_backward(fa, d, B, Hq, Hkv, Nq, Nk, lens):
     check_bwd(fa, *make(B, Hq, Hkv, Nq, Nk, d, lens))
 
 
+# shapes where the work of one head is spread over the GPU: clusters of every size, row groups, query tiles and key
+# tiles whose steps lie in several ranges
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk,lens", [
+    (1, 1, 1, 1, 4100, None), (1, 8, 1, 2, 16000, None), (1, 6, 2, 33, 2500, None), (2, 1, 1, 40, 5000, [4999, 17]),
+    (1, 1, 1, 100, 3001, None), (1, 1, 1, 256, 9000, [8999]), (5, 3, 3, 9, 1100, [1100, 0, 1, 513, 512]),
+    (1, 1, 1, 13, 6000, None), (1, 2, 1, 1500, 257, [129]), (3, 2, 1, 700, 900, [900, 300, 601])])
+def test_spread(fa, d, B, Hq, Hkv, Nq, Nk, lens):
+    q, k, v, lens, g = make(B, Hq, Hkv, Nq, Nk, d, lens)
+    check_fwd(fa, q, k, v, lens)
+    check_bwd(fa, q, k, v, lens, g)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fewer_steps_than_room(fa, d):
+    """Most sequences are empty: there are more multiprocessors than steps, and ranges without any."""
+    for lens in ([0] * 39 + [130], [0] * 40, [1] + [0] * 38 + [600]):
+        q, k, v, lens, g = make(40, 4, 2, 300, 600, d, lens)
+        check_fwd(fa, q, k, v, lens)
+        dq, dk, dv = check_bwd(fa, q, k, v, lens, g)
+        assert (dk[1:39] == 0).all() and (dv[1:39] == 0).all() and (dq[1:39] == 0).all()
+
+
+def test_one_key(fa):
+    """One key: o is its value, and dQ and dK are zero but for roundings of P = 1 (dS = dP - D)."""
+    q, k, v, _, g = make(2, 2, 2, 150, 1, 64)
+    o, lse = check_fwd(fa, q, k, v, None)
+    assert torch.equal(o, v.expand(-1, -1, 150, -1))
+    check_bwd(fa, q, k, v, None, g)
+
+
+def test_refusals(fa):
+    q, k, v, _, _ = make(1, 2, 2, 4, 8, 64)
+    c = k.contiguous()
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.cross_fwd(q, c.as_strided((1, 2, 8, 64), (1024, 512, 32, 1)), v)        # rows on each other
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.cross_fwd(q, k, v, out=q.new_empty((1, 1, 4, 64)).expand(-1, 2, -1, -1))   # outputs on each other
+    for bad in (dict(kv_lens=torch.zeros(2, device="cuda", dtype=torch.int32)), dict(kv_lens=torch.zeros(1, device="cuda")),
+                dict(out=q.float()), dict(lse=q)):
+        with pytest.raises(ValueError):
+            fa.cross_fwd(q, k, v, **bad)
+    with pytest.raises(ValueError):
+        fa.cross_fwd(q, k, v[:, :1])
+    with pytest.raises(ValueError):
+        fa.cross_fwd(q, k.transpose(2, 3).contiguous().transpose(2, 3), v)
+    o, lse = fa.cross_fwd(q, k, v)
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.cross_bwd(q, k, v, o, q, lse, workspace=torch.empty(16, device="cuda", dtype=torch.uint8))
+    w = torch.empty(fa.cross_bwd_workspace_bytes(1, 2, 2, 4, 8, 64), device="cuda", dtype=torch.uint8)
+    for a, b in zip(fa.cross_bwd(q, k, v, o, q, lse, workspace=w), fa.cross_bwd(q, k, v, o, q, lse)):
+        assert torch.equal(a, b)
+    fa.sync_status()
+
+
 @pytest.mark.parametrize("Nq", [1, 4, 200])
 def test_scores_of_every_size(fa, Nq):
     """Peaked, flat and negative rows; the largest score in the first, last and a middle key."""

@@ -204,3 +204,43 @@ def test_streams_and_graph(fa):
     graph.replay()
     for a, b in zip((*y, *d), (*fa.qk_norm_rope(q, k, pos, freqs, *w), *fa.qk_norm_rope_bwd(*dy, q, k, pos, freqs, *w))):
         assert torch.equal(a, b)
+
+
+def test_refusals(fa):
+    q, k, w, pos, _ = make(1, 2, 2, 8, 64)
+    f = fa.rope_freqs(64)
+    for args, kw in (((q, k, pos), {}), ((q, k, None, f), {}), ((q, k, pos, f.float()), {}), ((q, k, pos, f.cuda()), {}),
+                     ((q, k, pos.long(), f), {}), ((q, k, pos, f), dict(sections=(16, 15))),
+                     ((q, k, pos, f), dict(sections=(16, 16))), ((q, k, pos, f), dict(sections=(32, 0, 0, 0, 0))),
+                     ((q, k, pos, f, w[0], w[1].to(torch.bfloat16)), {}), ((q, k, pos, f, w[0]), dict(norm=False)),
+                     ((q, k), dict(norm=False)), ((q, None, pos, f, None, w[0]), {}), ((q, k[:, :, :7], pos, f), {}),
+                     ((q.float(), k, pos, f), {})):
+        with pytest.raises(ValueError):
+            fa.qk_norm_rope(*args, **kw)
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.qk_norm_rope(q, k, pos, f, eps=-1.0)
+    odd = torch.empty(1 * 8 * 2 * 64 + 4, device="cuda", dtype=torch.bfloat16)[4:].view(1, 2, 8, 64)
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.qk_norm_rope(odd, k, pos, f)
+    dy = [x.contiguous() for x in (q, k)]
+    with pytest.raises(ValueError):
+        fa.qk_norm_rope_bwd(dy[0], dy[1].float(), q, k, pos, f)
+    with pytest.raises(fa.api.Fa4Fp4Error):
+        fa.qk_norm_rope_bwd(*dy, q, k, pos, f, *w, workspace=torch.empty(16, device="cuda", dtype=torch.uint8))
+    ws = torch.empty(fa.qk_norm_rope_bwd_workspace_bytes(1, 2, 2, 8, 64), device="cuda", dtype=torch.uint8)
+    for a, b in zip(fa.qk_norm_rope_bwd(*dy, q, k, pos, f, *w, workspace=ws), fa.qk_norm_rope_bwd(*dy, q, k, pos, f, *w)):
+        assert torch.equal(a, b)
+    fa.sync_status()
+
+
+def test_far_offsets(fa):
+    """Element offsets that pass 32 bits."""
+    room = torch.empty(2 ** 31 + 2 ** 20, device="cuda", dtype=torch.bfloat16)
+    q, k = (room[at:].as_strided((2, 2, 100, 64), (2 ** 31, 6400, 64, 1)) for at in (0, 2 ** 16))
+    q0, k0, w, pos, _ = make(2, 2, 2, 100, 64, fused=False)
+    q.copy_(q0)
+    k.copy_(k0)
+    f = fa.rope_freqs(64)
+    assert all(torch.equal(a, b) for a, b in zip(fa.qk_norm_rope(q, k, pos, f, *w), fa.qk_norm_rope(q0, k0, pos, f, *w)))
+    out = fa.qk_norm_rope_bwd(q0, k0, q, k, pos, f, *w, dq=q, dk=k)
+    assert all(torch.equal(a, b) for a, b in zip(out, fa.qk_norm_rope_bwd(q0, k0, q0, k0, pos, f, *w)))
