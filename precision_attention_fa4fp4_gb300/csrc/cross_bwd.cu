@@ -79,6 +79,11 @@ FA4_DEV uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&t);
 }
 
+// Columns 2 i and 2 i + 1 of a thread's row.
+FA4_DEV float2 pair(const uint32_t (&v)[32], int i) {
+  return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+
 // 32 FP32 columns of a row, times f, to bf16 in global memory.
 FA4_DEV void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float f, bool wide) {
   uint32_t pk[16];
@@ -528,7 +533,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
-        float e[2][32];
+        // (two elements an instruction)
+        float2 e[32];
         {
           uint32_t v[2][32];
           tmem_ld32(lane_base + COL_S + 64 * half, v[0]);
@@ -540,9 +546,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -z));
+          for (int i = 0; i < 32; ++i) {
+            const float2 y = ffma2(pair(v[i / 16], i % 16), make_float2(c, c), make_float2(-z, -z));
+            e[i] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          }
         }
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
@@ -559,19 +566,19 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) mbar_arrive(dp_free);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) e[q][i] *= __uint_as_float(v[q][i]) - del;
+          for (int i = 0; i < 32; ++i) {
+            e[i] = fmul2(e[i], fadd2(pair(v[i / 16], i % 16), make_float2(-del, -del)));
+            pk[i] = pack2(e[i].x, e[i].y);
+          }
         }
         if (keep < 64) {
+          // (what masked keys gave may be NaN: dS is 0 there)
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * q + i >= keep) e[q][i] = 0.f;
+          for (int i = 0; i < 32; ++i) {
+            if (2 * i >= keep) pk[i] = 0;
+            else if (2 * i + 1 >= keep) pk[i] &= 0xffffu;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack2(e[i / 16][2 * (i % 16)], e[i / 16][2 * (i % 16) + 1]);
         if (n >= 1 && !mbar_wait(ds_free, (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         tmem_st32(lane_base + COL_DS + 32 * half, pk);
@@ -663,7 +670,7 @@ struct SmemK {
   static constexpr int RS = D == 128 ? (STAGED ? 4 : 5) : 8; // ring: Q, dO, Q, dO, ...
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_R = 2 * TILE;
   static constexpr int OFF_OUT = OFF_R + RS * TILE;         // 64 channels of dV and of dK on their way out
-  static constexpr int OFF_ST = OFF_OUT + (STAGED ? 2 * CH : 0);   // [2] x (lse log2 e [128], D [128])
+  static constexpr int OFF_ST = OFF_OUT + (STAGED ? 2 * CH : 0);   // [2] x (-lse log2 e [128], -D [128])
   static constexpr int OFF_BAR = OFF_ST + 2 * 1024;
   static constexpr int NBAR = 4 + 2 * RS + 4 + 7;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -790,20 +797,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       // (D is the first kernel's, which let this one start when the grids before it had ended; every CTA waits for it,
       // so that this kernel does not end before it)
       wait_for_previous();
-      // lse log2 e and D of each step's queries (infinite lse where there is none: P = 0)
+      // -lse log2 e and -D of each step's queries (infinite lse where there is none: P = 0)
       float z[4], d4[4];
       auto fetch = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           int g, n;
           tile_row(a, at_.t, 4 * lane + i, G, g, n);
-          z[i] = INFINITY;
+          z[i] = -INFINITY;
           d4[i] = 0.f;
           if (g < G) {
             const long long flat = ((long long)at_.b * p.Hq + at_.hk * G + g) * p.Nq + n;
             const float v = p.lse[flat];
-            if (v > -INFINITY) z[i] = v * L2E;
-            d4[i] = a.del[flat];
+            if (v > -INFINITY) z[i] = -v * L2E;
+            d4[i] = -a.del[flat];
           }
         }
       };
@@ -902,7 +909,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         }
         if (threadIdx.x == 0) mbar_arrive(s_seen);
         tc_fence_after();
-        float e[2][32];
+        float2 e[32];
+        uint32_t pk[32];
         {
           uint32_t v[2][32];
           tmem_ld32(lane_base + COL_S + 64 * half, v[0]);
@@ -911,19 +919,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           reg_fence32(v[0]);
           reg_fence32(v[1]);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 z = *reinterpret_cast<const float4*>(stat + 32 * q + i);
-              e[q][i] = ex2_approx(fmaf(__uint_as_float(v[q][i]), c, -z.x));
-              e[q][i + 1] = ex2_approx(fmaf(__uint_as_float(v[q][i + 1]), c, -z.y));
-              e[q][i + 2] = ex2_approx(fmaf(__uint_as_float(v[q][i + 2]), c, -z.z));
-              e[q][i + 3] = ex2_approx(fmaf(__uint_as_float(v[q][i + 3]), c, -z.w));
-            }
+          for (int i = 0; i < 32; i += 2) {
+            const float4 z = *reinterpret_cast<const float4*>(stat + 2 * i);
+            const float2 x = ffma2(pair(v[i / 16], i % 16), make_float2(c, c), make_float2(z.x, z.y));
+            const float2 y = ffma2(pair(v[i / 16], i % 16 + 1), make_float2(c, c), make_float2(z.z, z.w));
+            e[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            e[i + 1] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            pk[i] = pack2(e[i].x, e[i].y);
+            pk[i + 1] = pack2(e[i + 1].x, e[i + 1].y);
+          }
         }
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack2(e[i / 16][2 * (i % 16)], e[i / 16][2 * (i % 16) + 1]);
         tmem_st32(lane_base + COL_S + 64 * half, pk);
         tmem_st_wait();
         tc_fence_before();
@@ -939,18 +944,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           reg_fence32(v[0]);
           reg_fence32(v[1]);
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 z = *reinterpret_cast<const float4*>(stat + 128 + 32 * q + i);
-              e[q][i] *= __uint_as_float(v[q][i]) - z.x;
-              e[q][i + 1] *= __uint_as_float(v[q][i + 1]) - z.y;
-              e[q][i + 2] *= __uint_as_float(v[q][i + 2]) - z.z;
-              e[q][i + 3] *= __uint_as_float(v[q][i + 3]) - z.w;
-            }
+          for (int i = 0; i < 32; i += 2) {
+            const float4 z = *reinterpret_cast<const float4*>(stat + 128 + 2 * i);
+            const float2 x = fmul2(e[i], fadd2(pair(v[i / 16], i % 16), make_float2(z.x, z.y)));
+            const float2 y = fmul2(e[i + 1], fadd2(pair(v[i / 16], i % 16 + 1), make_float2(z.z, z.w)));
+            pk[i] = pack2(x.x, x.y);
+            pk[i + 1] = pack2(y.x, y.y);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack2(e[i / 16][2 * (i % 16)], e[i / 16][2 * (i % 16) + 1]);
         tmem_st32(lane_base + COL_DP + 64 * half, pk);
         tmem_st_wait();
         tc_fence_before();
