@@ -209,11 +209,12 @@ FA4_DEV float* partial(float* part, int D, int which, int row, int column) {
 template <int D>
 struct SmemQ {
   static constexpr int TILE = (D / 64) * CH;
-  static constexpr int KS = D == 128 ? 5 : 8;
-  static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_KV = 2 * TILE;
-  static constexpr int OFF_DEL = OFF_KV + KS * TILE;        // [2 items][2 halves][128]: shares of D
+  // K is held from S to dQ, V for dP alone: rings of their own (o goes through V's)
+  static constexpr int KS = D == 128 ? 3 : 5, VS = D == 128 ? 2 : 4;
+  static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE;
+  static constexpr int OFF_DEL = OFF_V + VS * TILE;         // [2 items][2 halves][128]: shares of D
   static constexpr int OFF_BAR = OFF_DEL + 2 * 1024;
-  static constexpr int NBAR = 2 * KS + 13;
+  static constexpr int NBAR = 2 * KS + 2 * VS + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 48;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -244,7 +245,7 @@ struct WalkQ {
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_constant__ Params a) {
   using L = SmemQ<D>;
-  constexpr int KS = L::KS;
+  constexpr int KS = L::KS, VS = L::VS;
   constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DS = 384, COL_Q = 448;
   const CrossParams& p = a.p;
   // (no room to align it by hand: nothing else is in shared memory, so it begins on its alignment)
@@ -255,9 +256,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   }
   float* shares = reinterpret_cast<float*>(smem + L::OFF_DEL);
   uint8_t *q_tile = smem + L::OFF_Q, *do_tile = smem + L::OFF_DO;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* kv_empty = kv_full + KS;
-  uint64_t* q_full = kv_empty + KS;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* v_full = k_empty + KS;
+  uint64_t* v_empty = v_full + VS;
+  uint64_t* q_full = v_empty + VS;
   uint64_t* q_empty = q_full + 1;
   uint64_t* do_full = q_empty + 1;
   uint64_t* do_empty = do_full + 1;
@@ -277,7 +280,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < KS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 8);
     mbar_init(do_full, 1);
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   const uint32_t tbase = *tmem_holder;
   const int G = p.Hq / p.Hkv;
   WalkQ w(*range);
-  ItemQ it;
+  ItemQ it{};
 
   if (warp >= W_PROD) {
     setmaxnreg_dec<REG_MISC>();
@@ -319,16 +323,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         tma_prefetch_desc(&a.o.map);
         tma_prefetch_desc(&a.k.map);
         tma_prefetch_desc(&a.v.map);
-        int qn = 0, dn = 0, kn = 0;          // tiles issued
+        int qn = 0, dn = 0, kn = 0, vn = 0;  // tiles issued
         auto load = [&](const HeadsMap& m, uint8_t* dst, uint64_t* full, int rows, int n, int h, int b) {
           mbar_arrive_expect_tx(full, rows * 2 * D);
           for (int c = 0; c < D / 64; ++c) tma_heads(dst + c * CH, m, full, 64 * c, n, h, b);
         };
-        auto load_kv = [&](const HeadsMap& m, int rows, int n, int h, int b) -> bool {
+        auto load_k = [&](int j) -> bool {
           const int st = kn % KS;
-          if (kn >= KS && !mbar_wait(&kv_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
-          load(m, smem + L::OFF_KV + st * L::TILE, &kv_full[st], rows, n, h, b);
+          if (kn >= KS && !mbar_wait(&k_empty[st], (kn / KS - 1) & 1, abort_flag, p.err)) return false;
+          load(a.k, smem + L::OFF_K + st * L::TILE, &k_full[st], BN, j * BN, it.hk, it.b);
           ++kn;
+          return true;
+        };
+        auto load_v = [&](const HeadsMap& m, int rows, int n, int h) -> bool {
+          const int st = vn % VS;
+          if (vn >= VS && !mbar_wait(&v_empty[st], (vn / VS - 1) & 1, abort_flag, p.err)) return false;
+          load(m, smem + L::OFF_V + st * L::TILE, &v_full[st], rows, n, h, it.b);
+          ++vn;
           return true;
         };
         for (bool ok = true; ok && w.get(it); w.next(a)) {
@@ -336,23 +347,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           divide(it.tile, a.per_head, g, n);
           const int h = it.hk * G + g * a.heads;
           n *= BM;
-          // Q, K_0 | dO, o, V_0 | K_1, V_1, ...: in the order of the K, V ring o, K_0, V_0, K_1, ...
           if (qn > 0 && !mbar_wait(q_empty, (qn - 1) & 1, abort_flag, p.err)) break;
           load(a.q, q_tile, q_full, a.box, n, h, it.b);
           ++qn;
-          if (!load_kv(a.o, a.box, n, h, it.b) || !load_kv(a.k, BN, it.j0 * BN, it.hk, it.b)) break;
+          if (!load_k(it.j0) || !load_v(a.o, a.box, n, h)) break;
           if (dn > 0 && !mbar_wait(do_empty, (dn - 1) & 1, abort_flag, p.err)) break;
           load(a.dout, do_tile, do_full, a.box, n, h, it.b);
           ++dn;
-          ok = load_kv(a.v, BN, it.j0 * BN, it.hk, it.b);
-          for (int j = it.j0 + 1; ok && j < it.j1; ++j)
-            ok = load_kv(a.k, BN, j * BN, it.hk, it.b) && load_kv(a.v, BN, j * BN, it.hk, it.b);
+          ok = load_v(a.v, BN, it.j0 * BN, it.hk);
+          for (int j = it.j0 + 1; ok && j < it.j1; ++j) ok = load_k(j) && load_v(a.v, BN, j * BN, it.hk);
         }
         if (*abort_flag) {
           volatile int no_abort = 0;
           if (qn > 0) mbar_wait(q_full, (qn - 1) & 1, &no_abort, p.err);
           if (dn > 0) mbar_wait(do_full, (dn - 1) & 1, &no_abort, p.err);
-          for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait(&kv_full[i % KS], (i / KS) & 1, &no_abort, p.err);
+          for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait(&k_full[i % KS], (i / KS) & 1, &no_abort, p.err);
+          for (int i = max(0, vn - VS); i < vn; ++i) mbar_wait(&v_full[i % VS], (i / VS) & 1, &no_abort, p.err);
         }
       }
       __syncwarp();
@@ -360,17 +370,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       // S of every step, once the one before has been read
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
-      int kv = 0, n = 0;
+      int n = 0;
       bool ok = true;
       for (int i = 0; ok && w.get(it); w.next(a), ++i) {
         ok = mbar_wait(qt_full, i & 1, abort_flag, p.err);
-        ++kv;                              // (o)
-        for (int j = it.j0; ok && j < it.j1; ++j, ++n, kv += 2) {
-          ok = mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err) &&
+        for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
+          ok = mbar_wait(&k_full[n % KS], (n / KS) & 1, abort_flag, p.err) &&
                (n == 0 || mbar_wait(s_free, (n - 1) & 1, abort_flag, p.err));
           if (!ok) break;
           // rows of K behind the sequence's keys may be anything: dS is 0 there, and 0 x NaN is not
-          uint8_t* k = smem + L::OFF_KV + kv % KS * L::TILE;
+          uint8_t* k = smem + L::OFF_K + n % KS * L::TILE;
           if (it.len - j * BN < BN && it.len < p.Nk) clear_rows<D>(k, it.len - j * BN, lane);
           tc_fence_after();
           const uint32_t b = desc_rows(smem_u32(k));
@@ -394,17 +403,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_q = idesc_f16(BM, D, true, false, true);
       const uint32_t sdo = smem_u32(do_tile);
-      int k = 0, k_before = 0, n = 0;      // K of this step and of the one before it
+      int v = 0, n = 0;                    // ring position of V; steps whose dP is issued
       bool ok = true, add = false;
-      // dQ += dS K of step m, whose K is at ring position k; last: of its item
-      auto issue_dq = [&](int m, int k, bool last) -> bool {
+      // dQ += dS K of step m; last: of its item
+      auto issue_dq = [&](int m, bool last) -> bool {
         if (!mbar_wait(ds_full, m & 1, abort_flag, p.err)) return false;
         tc_fence_after();
-        const uint32_t sk = smem_u32(smem + L::OFF_KV + k % KS * L::TILE);
+        const uint32_t sk = smem_u32(smem + L::OFF_K + m % KS * L::TILE);
         if (leader) {
           product_cols(tbase + COL_DQ, tbase + COL_DS, tbase + COL_DS + 32, sk, idesc_q, add);
           mma_commit(ds_free);
-          mma_commit(&kv_empty[k % KS]);
+          mma_commit(&k_empty[m % KS]);
           if (last) mma_commit(dq_done);
         }
         __syncwarp();
@@ -414,29 +423,27 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       for (int i = 0; ok && w.get(it); w.next(a), ++i) {
         for (int j = it.j0; ok && j < it.j1; ++j) {
           const bool first = j == it.j0;
-          if (first) ++k;                  // (o)
-          const int v = k + 1;
-          if (first && n > 0) ok = issue_dq(n - 1, k_before, true);
+          if (first) ++v;                  // (o)
+          if (first && n > 0) ok = issue_dq(n - 1, true);
           if (n > 0) ok = ok && mbar_wait(dp_free, (n - 1) & 1, abort_flag, p.err);
           if (first) ok = ok && mbar_wait(do_full, i & 1, abort_flag, p.err);
-          ok = ok && mbar_wait(&kv_full[v % KS], (v / KS) & 1, abort_flag, p.err);
+          ok = ok && mbar_wait(&v_full[v % VS], (v / VS) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sv = smem_u32(smem + L::OFF_KV + v % KS * L::TILE);
+          const uint32_t sv = smem_u32(smem + L::OFF_V + v % VS * L::TILE);
           if (leader) {
             product_rows<D>(tbase + COL_DP, sdo, sv, idesc_s);
             mma_commit(dp_full);
-            mma_commit(&kv_empty[v % KS]);
+            mma_commit(&v_empty[v % VS]);
             if (j == it.j1 - 1) mma_commit(do_empty);
           }
           __syncwarp();
-          if (!first) ok = issue_dq(n - 1, k_before, false);
+          if (!first) ok = issue_dq(n - 1, false);
           ++n;
-          k_before = k;
-          k = v + 1;
+          ++v;
         }
       }
-      if (ok && n > 0) issue_dq(n - 1, k_before, true);
+      if (ok && n > 0) issue_dq(n - 1, true);
       if (leader) mma_commit(mma_done);
       __syncwarp();
       volatile int no_abort = 0;
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
     int n = 0, items = 0;                  // key tiles, items so far
-    int kv = 0;                            // ring position of the item's o
+    int o = 0;                             // ring position of the item's o
     bool ok = true, leaving = false;       // leaving: a dQ is on its way out of shared memory
     if (p.lens)                            // queries without a key
       for (int i = blockIdx.x; i < a.items; i += gridDim.x) {
@@ -501,9 +508,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       float del = 0.f, z = INFINITY;       // (a row without keys: P = 2^-inf = 0)
       if (lse > -INFINITY) z = lse * L2E;
       ok = ok && mbar_wait(do_full, items & 1, abort_flag, p.err) &&
-           mbar_wait(&kv_full[kv % KS], (kv / KS) & 1, abort_flag, p.err);
+           mbar_wait(&v_full[o % VS], (o / VS) & 1, abort_flag, p.err);
       if (ok) {
-        uint8_t* ot = smem + L::OFF_KV + kv % KS * L::TILE;
+        uint8_t* ot = smem + L::OFF_V + o % VS * L::TILE;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int x = half * (D / 16) + i;
@@ -527,9 +534,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           mbar_arrive(q_empty);
         }
       }
-      if (threadIdx.x == 0) mbar_arrive(&kv_empty[kv % KS]);
+      if (threadIdx.x == 0) mbar_arrive(&v_empty[o % VS]);
       if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
-      kv += 2 * (it.j1 - it.j0) + 1;
+      o += it.j1 - it.j0 + 1;
       for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
