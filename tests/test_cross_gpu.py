@@ -313,3 +313,14 @@ def test_gradients_against_differences():
                 f.append(float((ref.cross(q, k, v, lens)[0] * dout).sum()))
             x[at] = was
             assert abs((f[0] - f[1]) / 2e-5 - float(grads[i][0][at])) < 1e-7
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", [
+    (1, 3, 3, 2500, 256), (2, 4, 2, 1200, 300), (1, 5, 5, 900, 512), (3, 2, 1, 700, 640), (1, 7, 7, 300, 768),
+    (2, 6, 3, 520, 1000), (1, 1, 1, 3000, 1900), (5, 8, 2, 20, 257)])
+def test_key_tiles_side_by_side(fa, B, Hq, Hkv, Nq, Nk):
+    """Two to eight key tiles of a head go through its queries at the same time, and their ranges end inside lines;
+    with lengths (all keys) each goes by itself."""
+    q, k, v, _, g = make(B, Hq, Hkv, Nq, Nk, 128)
+    check_bwd(fa, q, k, v, None, g)
+    check_bwd(fa, q, k, v, torch.full((B,), Nk, device="cuda", dtype=torch.int32), g)
