@@ -86,6 +86,16 @@ FA4_DEV void product_cols(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, u
   for (int k = 0; k < 8; ++k) mma_ts(acc, (k < 4 ? a0 : a1) + 8 * (k % 4), b + k * 128, idesc, add || k > 0);
 }
 
+// Half of that product: the first or the last 32 of A's columns from a0 and from a1.
+FA4_DEV void product_quarters(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t idesc, int part, bool add) {
+  const uint32_t b = desc_cols(sb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = 2 * part + i % 2;
+    mma_ts(acc, (i < 2 ? a0 : a1) + 8 * k, b + (i / 2 * 4 + k) * 128, idesc, add || i > 0);
+  }
+}
+
 // Rows [keep, 128) of a tile to zeros (one warp).
 template <int D>
 FA4_DEV void clear_rows(uint8_t* tile, int keep, int lane) {

@@ -691,7 +691,7 @@ struct SmemK {
   static constexpr int OFF_OUT = OFF_R + RS * TILE;         // 64 channels of dV and of dK on their way out
   static constexpr int OFF_ST = OFF_OUT + (STAGED ? 2 * CH : 0);   // [2] x (-lse log2 e [128], -D [128])
   static constexpr int OFF_BAR = OFF_ST + 2 * 1024;
-  static constexpr int NBAR = 4 + 2 * RS + 4 + 7;
+  static constexpr int NBAR = 4 + 2 * RS + 4 + 9;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int BYTES = OFF_MISC + 64;
   static_assert(BYTES <= 227 * 1024, "shared memory budget");
@@ -720,10 +720,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   uint64_t* st_empty = st_full + 2;
   uint64_t* s_full = st_empty + 2;
   uint64_t* s_seen = s_full + 1;         // the step's threads have seen s_full
-  uint64_t* p_full = s_seen + 1;         // P^T is there
-  uint64_t* dp_full = p_full + 1;
-  uint64_t* ds_full = dp_full + 1;       // dS^T is there
-  uint64_t* acc_done = ds_full + 1;      // the line's dV and dK are there
+  uint64_t* p_full = s_seen + 1;         // [2] halves: P^T is there
+  uint64_t* dp_full = p_full + 2;
+  uint64_t* ds_full = dp_full + 1;       // [2] halves: dS^T is there
+  uint64_t* acc_done = ds_full + 2;      // the line's dV and dK are there
   uint64_t* mma_done = acc_done + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -737,9 +737,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
     for (int s = 0; s < 2; ++s) { mbar_init(&st_full[s], 1); mbar_init(&st_empty[s], 8); }
     mbar_init(s_full, 1);
     mbar_init(s_seen, 1);
-    mbar_init(p_full, 8);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    for (int s = 0; s < 2; ++s) { mbar_init(&p_full[s], 8); mbar_init(&ds_full[s], 8); }
     mbar_init(acc_done, 2);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -892,10 +891,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         // waiting for its dK before they look at the next S^T.)
         if (x == 1 && !last) ok = ok && mbar_wait(s_seen, (n + 1) & 1, abort_flag, p.err);
         if (!ok) break;
-        tc_fence_after();
         const uint32_t b = smem_u32(smem + L::OFF_R + seq % RS * L::TILE);
+        tc_fence_after();
+        if (leader) product_quarters(sum, col, col + 64, b, idesc_a, 0, !first);
+        __syncwarp();
+        if (!mbar_wait(&ready[1], n & 1, abort_flag, p.err)) { ok = false; break; }
+        tc_fence_after();
         if (leader) {
-          product_cols(sum, col, col + 64, b, idesc_a, !first);
+          product_quarters(sum, col, col + 64, b, idesc_a, 1, true);
           mma_commit(&r_empty[seq % RS]);
           if (last) mma_commit(acc_done);
         }
@@ -915,6 +918,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
     const int half = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
+    // half of the thread's P^T or dS^T: its product begins with it
+    auto give = [&](uint32_t column, const uint32_t (&w)[16], uint64_t* bar) {
+      tmem_st16(lane_base + column + 64 * half, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     int n = 0, lines = 0;
     bool ok = true;
     while (ok && at_.left > 0) {
@@ -929,7 +940,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         if (threadIdx.x == 0) mbar_arrive(s_seen);
         tc_fence_after();
         float2 e[32];
-        uint32_t pk[32];
+        uint32_t pk[2][16];
         {
           uint32_t v[2][32];
           tmem_ld32(lane_base + COL_S + 64 * half, v[0]);
@@ -939,20 +950,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           reg_fence32(v[1]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
+            if (i == 16) give(COL_S, pk[0], p_full);
             const float4 z = *reinterpret_cast<const float4*>(stat + 2 * i);
             const float2 x = ffma2(pair(v[i / 16], i % 16), make_float2(c, c), make_float2(z.x, z.y));
             const float2 y = ffma2(pair(v[i / 16], i % 16 + 1), make_float2(c, c), make_float2(z.z, z.w));
             e[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             e[i + 1] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            pk[i] = pack2(e[i].x, e[i].y);
-            pk[i + 1] = pack2(e[i + 1].x, e[i + 1].y);
+            pk[i / 16][i % 16] = pack2(e[i].x, e[i].y);
+            pk[i / 16][i % 16 + 1] = pack2(e[i + 1].x, e[i + 1].y);
           }
         }
-        tmem_st32(lane_base + COL_S + 64 * half, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        give(COL_S + 16, pk[1], p_full + 1);
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         {
@@ -964,21 +972,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           reg_fence32(v[1]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
+            if (i == 16) give(COL_DP, pk[0], ds_full);
             const float4 z = *reinterpret_cast<const float4*>(stat + 128 + 2 * i);
             const float2 x = fmul2(e[i], fadd2(pair(v[i / 16], i % 16), make_float2(z.x, z.y)));
             const float2 y = fmul2(e[i + 1], fadd2(pair(v[i / 16], i % 16 + 1), make_float2(z.z, z.w)));
-            pk[i] = pack2(x.x, x.y);
-            pk[i + 1] = pack2(y.x, y.y);
+            pk[i / 16][i % 16] = pack2(x.x, x.y);
+            pk[i / 16][i % 16 + 1] = pack2(y.x, y.y);
           }
         }
-        tmem_st32(lane_base + COL_DP + 64 * half, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(ds_full);
-          mbar_arrive(&st_empty[st]);
-        }
+        give(COL_DP + 16, pk[1], ds_full + 1);
+        if (lane == 0) mbar_arrive(&st_empty[st]);
       }
       if (!ok) break;
       // the line's sums: warps 0-3 dV, warps 4-7 dK, a key each
