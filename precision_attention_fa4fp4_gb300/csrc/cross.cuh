@@ -78,16 +78,15 @@ FA4_DEV void product_rows(uint32_t acc, uint32_t sa, uint32_t sb, uint32_t idesc
     mma_ss(acc, a + off, b + off, idesc, k > 0);
   }
 }
-// acc (+)= A B over B's 128 rows, A packed in tensor memory: its first 64 columns
-// in [a0, a0 + 32), the others in [a1, a1 + 32).
-FA4_DEV void product_cols(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t idesc, bool add) {
+// acc (+)= A B over B's 128 rows, A packed in tensor memory.
+FA4_DEV void product_cols(uint32_t acc, uint32_t a, uint32_t sb, uint32_t idesc, bool add) {
   const uint32_t b = desc_cols(sb);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) mma_ts(acc, (k < 4 ? a0 : a1) + 8 * (k % 4), b + k * 128, idesc, add || k > 0);
+  for (int k = 0; k < 8; ++k) mma_ts(acc, a + 8 * k, b + k * 128, idesc, add || k > 0);
 }
-
-// Half of that product: the first or the last 32 of A's columns from a0 and from a1.
-FA4_DEV void product_quarters(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t idesc, int part, bool add) {
+// Half of that product: the first or the last 32 of A's columns from a0 and from a1
+// (64 columns, packed, each).
+FA4_DEV void product_half(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t sb, uint32_t idesc, int part, bool add) {
   const uint32_t b = desc_cols(sb);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -18,19 +18,27 @@
 // keep it as busy as even shapes do.  A range that starts or ends inside an output
 // tile's steps leaves FP32 partials in the workspace.
 //
-// cross_dq_kernel: a query tile's key tiles in turn.  Warps 0-7: a thread per
-//   row and half of the keys: P from S, dS from P and dP, as bf16 into tensor memory
+// cross_dq_kernel: a query tile's key tiles in turn.  Warps 0-15: a thread per
+//   row and quarter of the keys: P from S, dS from P and dP, as bf16 into tensor memory
 //   (the A operand of dQ).  Q is in tensor memory too (the A operand of S), so that its
 //   place in shared memory takes the next item's Q, then this one's dQ on its way
-//   out, and K and V have room to be two steps ahead.  S and dP of the next key tile
-//   run as soon as these have been read.  D is summed by the same threads from the o
-//   and dO tiles, and kept in the workspace.  Two warps issue the products: S; dP and
-//   dQ.
+//   out, and K has three places and V two.  S and dP of the next key tile run as soon
+//   as these have been read.  D is summed by the same threads from the o and dO tiles,
+//   and kept in the workspace.  Two warps issue the products: S; dP and dQ.  What bounds
+//   it: with many key tiles what comes in (64 KB a step at 30 B a cycle, where the
+//   products take 1536 of 2240 cycles), with one or two the item's own chain (Q to
+//   tensor memory, D, dQ out), which is why there are sixteen warps: eight took 219
+//   where these take 203 us (6 heads, 76,666 queries, 188 keys; 1024 queries over 4100
+//   keys 323 with either).
 // cross_dkv_kernel: a key tile's query tiles in turn.  Rows are keys: P^T and dS^T go
 //   over S^T and dP^T as A operands of dV and dK, which are summed in tensor memory
 //   (512 columns in all).  Two warps issue the products, S^T and dV the one, dP^T and
 //   dK the other (one warp was the bound: a product takes 512 cycles, its waits,
-//   instructions and commits 700).
+//   instructions and commits 700).  Eight warps of threads with a key and half of the
+//   queries each (sixteen: 175 -> 191 us of the 4100 keys).  What bounds it at d = 128:
+//   shared memory, of which a step's products read 192 KB, TMA writes 64 KB and the
+//   threads take 256 words of -lse and -D: 2304 cycles of 128 B, with the waits between
+//   them 2800, where the products alone take 2048.
 // cross_join_kernel: sums the partials in the ranges' order; zeros for keys behind
 //   kv_lens.
 #include <cuda_bf16.h>
@@ -42,9 +50,15 @@ namespace fa4 {
 namespace {
 
 constexpr int BM = 128, BN = 128;
-constexpr int NTHREADS = 384;
-constexpr int W_PROD = 8, W_MMA = 9, W_MMA_B = 10, W_STAT = 11;
-constexpr int REG_SOFT = 208, REG_MISC = 88;   // 2 x 208 + 88 = 504 of 512
+// Warps of a kernel with N that do the element-wise work, behind them four that load and
+// issue; registers are moved between the two.
+template <int N>
+struct Roles {
+  static constexpr int SOFT = 32 * N, NTHREADS = SOFT + 128;
+  static constexpr int W_PROD = N, W_MMA = N + 1, W_MMA_B = N + 2;
+  // (of 168 and of 96 that a thread starts with: 2 x 208 + 88 = 3 x 168, 4 x 104 + 64 = 5 x 96)
+  static constexpr int REG_SOFT = N == 8 ? 208 : 104, REG_MISC = N == 8 ? 88 : 64;
+};
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float L2E = 1.4426950408889634f;
 
@@ -81,23 +95,35 @@ FA4_DEV uint32_t pack2(float lo, float hi) {
 }
 
 // Columns 2 i and 2 i + 1 of a thread's row.
-FA4_DEV float2 pair(const uint32_t (&v)[32], int i) {
+template <int N>
+FA4_DEV float2 pair(const uint32_t (&v)[N], int i) {
   return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
 }
 
-// 32 FP32 columns of a row, times f, to bf16 in global memory.
-FA4_DEV void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float f, bool wide) {
-  uint32_t pk[16];
+// N FP32 columns of a row, times f, to bf16 in global memory.
+template <int N>
+FA4_DEV void store_row(__nv_bfloat16* dst, const uint32_t (&v)[N], float f, bool wide) {
+  uint32_t pk[N / 2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) pk[i] = pack2(__uint_as_float(v[2 * i]) * f, __uint_as_float(v[2 * i + 1]) * f);
+  for (int i = 0; i < N / 2; ++i) pk[i] = pack2(pair(v, i).x * f, pair(v, i).y * f);
   if (wide) {
-    st_global_v8(dst, pk);
-    st_global_v8(dst + 16, pk + 8);
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) st_global_v8(dst + 16 * i, pk + 8 * i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N / 8; ++i)
       reinterpret_cast<uint4*>(dst)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
   }
+}
+
+// N columns of tensor memory (a thread's row).
+template <int N>
+FA4_DEV void load_columns(uint32_t taddr, uint32_t (&v)[N]) {
+  if constexpr (N == 32) tmem_ld32(taddr, v);
+  else tmem_ld16(taddr, v);
+  tmem_ld_wait();
+  if constexpr (N == 32) reg_fence32(v);
+  else reg_fence16(v);
 }
 
 // ---------------------------------------------------------------------------
@@ -224,7 +250,7 @@ struct SmemQ {
   // K is held from S to dQ, V for dP alone: rings of their own (o goes through V's)
   static constexpr int KS = D == 128 ? 3 : 5, VS = D == 128 ? 2 : 4;
   static constexpr int OFF_Q = 0, OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE;
-  static constexpr int OFF_DEL = OFF_V + VS * TILE;         // [2 items][2 halves][128]: shares of D
+  static constexpr int OFF_DEL = OFF_V + VS * TILE;         // [4 quarters][128]: shares of D
   static constexpr int OFF_BAR = OFF_DEL + 2 * 1024;
   static constexpr int NBAR = 2 * KS + 2 * VS + 13;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -255,8 +281,9 @@ struct WalkQ {
 };
 
 template <int D>
-__global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_constant__ Params a) {
+__global__ void __launch_bounds__(Roles<16>::NTHREADS, 1) cross_dq_kernel(const __grid_constant__ Params a) {
   using L = SmemQ<D>;
+  using R = Roles<16>;
   constexpr int KS = L::KS, VS = L::VS;
   constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DS = 384, COL_Q = 448;
   const CrossParams& p = a.p;
@@ -295,26 +322,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     for (int s = 0; s < KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 8);
+    mbar_init(q_empty, R::W_PROD);
     mbar_init(do_full, 1);
-    mbar_init(do_empty, 9);
-    mbar_init(qt_full, 8);
+    mbar_init(do_empty, R::W_PROD + 1);
+    mbar_init(qt_full, R::W_PROD);
     mbar_init(s_full, 1);
-    mbar_init(s_free, 8);
+    mbar_init(s_free, R::W_PROD);
     mbar_init(dp_full, 1);
-    mbar_init(dp_free, 8);
-    mbar_init(ds_full, 8);
+    mbar_init(dp_free, R::W_PROD);
+    mbar_init(ds_full, R::W_PROD);
     mbar_init(ds_free, 1);
     mbar_init(dq_done, 1);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
+  if (warp == R::W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
   // (in this order: the next kernel reads its inputs before it waits for this one)
   wait_for_previous();
   next_may_start();
-  if (warp == W_PROD) {
+  if (warp == R::W_PROD) {
     const Range x = find_range(a, true, lane);
     if (lane == 0) *range = x;
   }
@@ -326,9 +353,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   WalkQ w(*range);
   ItemQ it{};
 
-  if (warp >= W_PROD) {
-    setmaxnreg_dec<REG_MISC>();
-    if (warp == W_PROD) {
+  if (warp >= R::W_PROD) {
+    setmaxnreg_dec<R::REG_MISC>();
+    if (warp == R::W_PROD) {
       if (lane == 0) {
         tma_prefetch_desc(&a.q.map);
         tma_prefetch_desc(&a.dout.map);
@@ -378,7 +405,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         }
       }
       __syncwarp();
-    } else if (warp == W_MMA) {
+    } else if (warp == R::W_MMA) {
       // S of every step, once the one before has been read
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
@@ -409,7 +436,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       volatile int no_abort = 0;
       mbar_wait(mma_done, 0, &no_abort, p.err);
       __syncwarp();
-    } else if (warp == W_MMA_B) {
+    } else if (warp == R::W_MMA_B) {
       // dP of every step, once the one before has been read; then dQ of that one
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
@@ -423,7 +450,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         tc_fence_after();
         const uint32_t sk = smem_u32(smem + L::OFF_K + m % KS * L::TILE);
         if (leader) {
-          product_cols(tbase + COL_DQ, tbase + COL_DS, tbase + COL_DS + 32, sk, idesc_q, add);
+          product_cols(tbase + COL_DQ, tbase + COL_DS, sk, idesc_q, add);
           mma_commit(ds_free);
           mma_commit(&k_empty[m % KS]);
           if (last) mma_commit(dq_done);
@@ -463,8 +490,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       __syncwarp();
     }
   } else {
-    setmaxnreg_inc<REG_SOFT>();
-    const int half = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    setmaxnreg_inc<R::REG_SOFT>();
+    const int part = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
     int n = 0, items = 0;                  // key tiles, items so far
@@ -477,8 +504,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         divide(bh, a.hkv, b, hk);
         tile_row(a, tile, r, G, g, row);
         if (g >= G || key_count(p, b, false) > 0) continue;
-        uint4* dst = reinterpret_cast<uint4*>(at(p.dq, b, hk * G + g, row) + half * (D / 2));
-        for (int x = 0; x < D / 16; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+        uint4* dst = reinterpret_cast<uint4*>(at(p.dq, b, hk * G + g, row) + part * (D / 4));
+        for (int x = 0; x < D / 32; ++x) dst[x] = make_uint4(0, 0, 0, 0);
       }
     // the item's row and its lse
     bool valid = false;
@@ -491,17 +518,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       h = x.hk * G + g;
       lse = valid ? p.lse[((long long)x.b * p.Hq + h) * p.Nq + row] : INFINITY;
     };
-    // this half of the item's Q row into tensor memory
+    // this quarter of the item's Q row into tensor memory
     auto take_q = [&](int i) -> bool {
       if (!mbar_wait(q_full, i & 1, abort_flag, p.err)) return false;
-      uint32_t v[D / 4];
+      uint32_t v[D / 8];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint4 u = *tile_word(q_tile, r, half * (D / 16) + x);
+      for (int x = 0; x < D / 32; ++x) {
+        const uint4 u = *tile_word(q_tile, r, part * (D / 32) + x);
         v[4 * x] = u.x; v[4 * x + 1] = u.y; v[4 * x + 2] = u.z; v[4 * x + 3] = u.w;
       }
-      if constexpr (D == 128) tmem_st32(lane_base + COL_Q + 32 * half, v);
-      else tmem_st16(lane_base + COL_Q + 16 * half, v);
+      if constexpr (D == 128) tmem_st16(lane_base + COL_Q + 16 * part, v);
+      else tmem_st8(lane_base + COL_Q + 8 * part, v);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -516,7 +543,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
     }
     // (A warp whose wait ran out still meets the others at the barriers.)
     while (more) {
-      // D: this half's share from the o and dO tiles, then both halves'
+      // D: this quarter's share from the o and dO tiles, then all of them in their order
       float del = 0.f, z = INFINITY;       // (a row without keys: P = 2^-inf = 0)
       if (lse > -INFINITY) z = lse * L2E;
       ok = ok && mbar_wait(do_full, items & 1, abort_flag, p.err) &&
@@ -524,8 +551,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       if (ok) {
         uint8_t* ot = smem + L::OFF_V + o % VS * L::TILE;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int x = half * (D / 16) + i;
+        for (int i = 0; i < D / 32; ++i) {
+          const int x = part * (D / 32) + i;
           const uint4 u = *tile_word(ot, r, x), y = *tile_word(do_tile, r, x);
           const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -535,10 +562,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
           }
         }
       }
-      float* mine = shares + (items & 1) * 256;
-      mine[half * 128 + r] = del;
-      named_bar(1, 256);
-      del += mine[(half ^ 1) * 128 + r];
+      shares[part * 128 + r] = del;
+      named_bar(1, R::SOFT);
+      del = (shares[r] + shares[128 + r]) + (shares[256 + r] + shares[384 + r]);
       if (lane == 0) {
         mbar_arrive(do_empty);
         if (leaving) {                     // the dQ before this one has left the place of Q
@@ -547,60 +573,52 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
         }
       }
       if (threadIdx.x == 0) mbar_arrive(&v_empty[o % VS]);
-      if (ok && valid && half == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
+      if (ok && valid && part == 0) a.del[((long long)it.b * p.Hq + h) * p.Nq + row] = del;
       o += it.j1 - it.j0 + 1;
       for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
         if (!mbar_wait(s_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         // (two elements an instruction)
-        float2 e[32];
+        float2 e[16];
         {
-          uint32_t v[2][32];
-          tmem_ld32(lane_base + COL_S + 64 * half, v[0]);
-          tmem_ld32(lane_base + COL_S + 64 * half + 32, v[1]);
-          tmem_ld_wait();
-          reg_fence32(v[0]);
-          reg_fence32(v[1]);
+          uint32_t v[32];
+          load_columns(lane_base + COL_S + 32 * part, v);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 y = ffma2(pair(v[i / 16], i % 16), make_float2(c, c), make_float2(-z, -z));
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = ffma2(pair(v, i), make_float2(c, c), make_float2(-z, -z));
             e[i] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
           }
         }
         if (!mbar_wait(dp_full, n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
-        const int keep = it.len - j * BN - 64 * half;
-        uint32_t pk[32];
+        const int keep = it.len - j * BN - 32 * part;
+        uint32_t pk[16];
         {
-          uint32_t v[2][32];
-          tmem_ld32(lane_base + COL_DP + 64 * half, v[0]);
-          tmem_ld32(lane_base + COL_DP + 64 * half + 32, v[1]);
-          tmem_ld_wait();
-          reg_fence32(v[0]);
-          reg_fence32(v[1]);
+          uint32_t v[32];
+          load_columns(lane_base + COL_DP + 32 * part, v);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(dp_free);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            e[i] = fmul2(e[i], fadd2(pair(v[i / 16], i % 16), make_float2(-del, -del)));
+          for (int i = 0; i < 16; ++i) {
+            e[i] = fmul2(e[i], fadd2(pair(v, i), make_float2(-del, -del)));
             pk[i] = pack2(e[i].x, e[i].y);
           }
         }
-        if (keep < 64) {
+        if (keep < 32) {
           // (what masked keys gave may be NaN: dS is 0 there)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             if (2 * i >= keep) pk[i] = 0;
             else if (2 * i + 1 >= keep) pk[i] &= 0xffffu;
           }
         }
         if (n >= 1 && !mbar_wait(ds_free, (n - 1) & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
-        tmem_st32(lane_base + COL_DS + 32 * half, pk);
+        tmem_st16(lane_base + COL_DS + 16 * part, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -609,58 +627,52 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
       // the next item's Q goes into tensor memory before this one's dQ is awaited, and dQ then into Q's place
       const ItemQ was = it;
       const bool here = valid;
-      __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + half * (D / 2) : nullptr;
+      __nv_bfloat16* dst = here ? at(p.dq, it.b, h, row) + part * (D / 4) : nullptr;
       w.next(a);
       more = w.get(it);
       if (more) {
         fetch(it);
         ok = ok && take_q(items + 1);
       }
-      named_bar(1, 256);
+      named_bar(1, R::SOFT);
       ok = ok && mbar_wait(dq_done, items & 1, abort_flag, p.err);
       ++items;
       if (ok) {
         tc_fence_after();
         // (rows by themselves would be 32 places a store: they leave in boxes of 32 rows)
+        uint32_t v[D / 4];
+        load_columns(lane_base + COL_DQ + part * (D / 4), v);
+        if (!was.whole) {
+          // (the first item of the range in slot 0, its last one in slot 1)
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          uint32_t v[32];
-          tmem_ld32(lane_base + COL_DQ + half * (D / 2) + 32 * q, v);
-          tmem_ld_wait();
-          reg_fence32(v);
-          if (!was.whole) {
-            // (the first item of the range in slot 0, its last one in slot 1)
+          for (int e = 0; e < D / 16; ++e)
+            *reinterpret_cast<uint4*>(partial(a.part_q, D, 2 * blockIdx.x + (items > 1), r, part * (D / 4) + 4 * e)) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else if (a.heads > 1) {
+          if (here) store_row(dst, v, p.scale, a.dq32);
+        } else {
+          const float f = p.scale;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(partial(a.part_q, D, 2 * blockIdx.x + (items > 1), r,
-                                                half * (D / 2) + 32 * q + 4 * e)) =
-                  make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          } else if (a.heads > 1) {
-            if (here) store32(dst + 32 * q, v, p.scale, a.dq32);
-          } else {
-            const float f = p.scale;
+          for (int e = 0; e < D / 32; ++e) {
+            uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                pk[i] = pack2(__uint_as_float(v[8 * e + 2 * i]) * f, __uint_as_float(v[8 * e + 2 * i + 1]) * f);
-              *tile_word(q_tile, r, half * (D / 16) + 4 * q + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
+            for (int i = 0; i < 4; ++i) pk[i] = pack2(pair(v, 4 * e + i).x * f, pair(v, 4 * e + i).y * f);
+            *tile_word(q_tile, r, part * (D / 32) + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         }
         tc_fence_before();
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (D == 64) named_bar(2 + quad, 64);          // both halves of a row are in one box
+      // (all quarters of a box of 64 channels)
+      const int box = part * (D / 4) / 64;
+      named_bar(2 + quad * (D / 64) + box, 8192 / D);
       if (lane == 0) {
         int g, m;
         divide(was.tile, a.per_head, g, m);
         m = m * BM + 32 * quad;
-        if (ok && was.whole && a.heads == 1 && m < p.Nq && (D == 128 || half == 0)) {
-          tma_heads_store(a.dq, q_tile + (D == 128 ? half * CH : 0) + quad * 32 * 128, D == 128 ? 64 * half : 0, m,
-                          was.hk * G + g, was.b);
+        if (ok && was.whole && a.heads == 1 && m < p.Nq && part * (D / 4) % 64 == 0) {
+          tma_heads_store(a.dq, q_tile + box * CH + quad * 32 * 128, 64 * box, m, was.hk * G + g, was.b);
           bulk_commit();
         }
       }
@@ -671,7 +683,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dq_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
+  if (warp == R::W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
 // ---------------------------------------------------------------------------
@@ -698,8 +710,9 @@ struct SmemK {
 };
 
 template <int D, bool STAGED>
-__global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_constant__ Params a) {
+__global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const __grid_constant__ Params a) {
   using L = SmemK<D, STAGED>;
+  using K = Roles<8>;
   constexpr int RS = L::RS;
   constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
   const CrossParams& p = a.p;
@@ -746,14 +759,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   }
   // rows of a ring slot that no box brings are zeros: P and dS are 0 there
   if (a.box < BM)
-    for (int i = threadIdx.x; i < RS * L::TILE / 16; i += NTHREADS)
+    for (int i = threadIdx.x; i < RS * L::TILE / 16; i += K::NTHREADS)
       reinterpret_cast<uint4*>(smem + L::OFF_R)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (warp == W_PROD) {
+  if (warp == K::W_PROD) {
     const Range x = find_range(a, false, lane);
     if (lane == 0) *range = x;
   }
-  if (warp == W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
+  if (warp == K::W_MMA) tmem_alloc(tmem_holder, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -761,9 +774,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   const int G = p.Hq / p.Hkv;
   Range at_ = *range;
 
-  if (warp >= W_PROD) {
-    setmaxnreg_dec<REG_MISC>();
-    if (warp == W_PROD) {
+  if (warp >= K::W_PROD) {
+    setmaxnreg_dec<K::REG_MISC>();
+    if (warp == K::W_PROD) {
       if (lane == 0) {
         tma_prefetch_desc(&a.q.map);
         tma_prefetch_desc(&a.dout.map);
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         }
       }
       __syncwarp();
-    } else if (warp == W_STAT) {
+    } else if (warp == K::W_MMA_B + 1) {
       // (D is the first kernel's, which let this one start when the grids before it had ended; every CTA waits for it,
       // so that this kernel does not end before it)
       wait_for_previous();
@@ -846,10 +859,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         if (++at_.t == a.tiles) at_.line(a, false);
         fetch();
       }
-    } else if (warp == W_MMA || warp == W_MMA_B) {
+    } else if (warp == K::W_MMA || warp == K::W_MMA_B) {
       // the first warp issues S^T and dV, the second dP^T and dK.  Each overwrites, in its own order, what its own
       // product before has read: S^T the P^T, dP^T the dS^T.
-      const int x = warp == W_MMA ? 0 : 1;
+      const int x = warp == K::W_MMA ? 0 : 1;
       const bool leader = elect_one();
       const uint32_t idesc_s = idesc_f16(BM, BN, true, false, false);
       const uint32_t idesc_a = idesc_f16(BM, D, true, false, true);
@@ -893,12 +906,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
         if (!ok) break;
         const uint32_t b = smem_u32(smem + L::OFF_R + seq % RS * L::TILE);
         tc_fence_after();
-        if (leader) product_quarters(sum, col, col + 64, b, idesc_a, 0, !first);
+        if (leader) product_half(sum, col, col + 64, b, idesc_a, 0, !first);
         __syncwarp();
         if (!mbar_wait(&ready[1], n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         if (leader) {
-          product_quarters(sum, col, col + 64, b, idesc_a, 1, true);
+          product_half(sum, col, col + 64, b, idesc_a, 1, true);
           mma_commit(&r_empty[seq % RS]);
           if (last) mma_commit(acc_done);
         }
@@ -914,7 +927,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
       __syncwarp();
     }
   } else {
-    setmaxnreg_inc<REG_SOFT>();
+    setmaxnreg_inc<K::REG_SOFT>();
     const int half = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const float c = p.c;
@@ -1011,7 +1024,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
           continue;
         }
         if (!STAGED) {
-          if (key < p.Nk) store32(at(half ? p.dk : p.dv, at_.b, at_.hk, key) + 32 * q, v, f, half ? a.dk32 : a.dv32);
+          if (key < p.Nk) store_row(at(half ? p.dk : p.dv, at_.b, at_.hk, key) + 32 * q, v, f, half ? a.dk32 : a.dv32);
           continue;
         }
         // rows by themselves would be 32 places a store: they leave in boxes of 32 rows and 64 channels
@@ -1046,7 +1059,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_dkv_kernel(const __grid_con
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == W_MMA) tmem_dealloc(tbase, TMEM_COLS);
+  if (warp == K::W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
 // dV (y = 0), dK (y = 1) and dQ (y = 2) of the output tiles whose steps lie in
@@ -1190,9 +1203,9 @@ size_t del_bytes(int B, int Hq, int Nq) { return ((size_t)B * Hq * Nq * sizeof(f
 
 bool on_words(const Strided& t) { return (reinterpret_cast<uintptr_t>(t.p) & 31) == 0 && ((t.b | t.h | t.n) & 15) == 0; }
 
-cudaError_t start(void (*kernel)(const Params), dim3 grid, int smem, bool early, const Params& a, cudaStream_t st) {
+cudaError_t start(void (*kernel)(const Params), dim3 grid, int threads, int smem, bool early, const Params& a, cudaStream_t st) {
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
-  return e != cudaSuccess ? e : launch(kernel, grid, NTHREADS, smem, early, st, a);
+  return e != cudaSuccess ? e : launch(kernel, grid, threads, smem, early, st, a);
 }
 
 }  // namespace
@@ -1235,12 +1248,12 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   };
   const bool join = p.lens || !apart(steps, a.ctas, a.key_tiles) || !apart(steps / a.side, a.ranges, a.tiles);
   const bool wide = p.d == 128;
-  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
+  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, Roles<16>::NTHREADS, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
                         true, a, st);
   const bool staged = !wide || a.tiles <= STAGED_STEPS;
   if (e == cudaSuccess)
     e = start(!wide ? cross_dkv_kernel<64, true> : staged ? cross_dkv_kernel<128, true> : cross_dkv_kernel<128, false>,
-              dim3(a.ranges * a.side), !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a,
+              dim3(a.ranges * a.side), Roles<8>::NTHREADS, !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a,
               st);
   if (e == cudaSuccess && join) e = launch(wide ? cross_join_kernel<128> : cross_join_kernel<64>, gj, 256, 0, true, st, a);
   return e;
