@@ -1066,8 +1066,11 @@ __global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const 
 // several ranges: the x below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside
 // a tile's steps and began at or before their first.  Then, where sequences have
 // lengths, zeros for the key tiles behind them: an x for each sequence and kv head.
-constexpr int JOIN_PARTS = 2;
-template <int D>
+// More parts make shorter sums and more CTAs that find nothing to do: with eight partials
+// and more of a tile a thread takes 8 columns of one row (6 heads, 76,666 queries, 188
+// keys 202 -> 167 us; where 6 sequences of 24 heads have a query over 230 keys 23.4
+// becomes 25.4, so otherwise two).
+template <int D, int JOIN_PARTS>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
   const CrossParams& p = a.p;
   const int which = blockIdx.y, G = p.Hq / p.Hkv;
@@ -1127,7 +1130,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   constexpr int EACH = 128 * (D / 8) / (256 * JOIN_PARTS);      // of a thread: rows' 8 columns
   const int x0 = blockIdx.z * 256 + threadIdx.x;
   float v[EACH][8] = {};
-#pragma unroll 2
+#pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     if (thin && range_start(sum, c + 1, ranges) == range_start(sum, c, ranges)) continue;
     const int slot = 2 * (c * side + lane_tile) + (c == c0 ? slot0 : 0);
@@ -1240,14 +1243,17 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
       !heads_map(&a.dq, p.dq, p.B, p.Hq, p.Nq, p.d, 32, 1) || !heads_map(&a.dk, p.dk, p.B, p.Hkv, p.Nk, p.d, 32, 1) ||
       !heads_map(&a.dv, p.dv, p.B, p.Hkv, p.Nk, p.d, 32, 1))
     return cudaErrorInvalidValue;
-  const dim3 grid(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 3, JOIN_PARTS);
+  const bool wide = p.d == 128;
+  const long long lines = (long long)p.B * p.Hkv * min(a.key_tiles, a.tiles);
+  const bool many = a.ctas >= 8 * lines;
+  const int parts = many ? wide ? 8 : 4 : 2;
+  const dim3 grid(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 3, parts);
   // no range ends inside an output tile's steps, and no key is without one?
   const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
   const auto apart = [](long long steps, int ranges, int line) {
     return line == 1 || (steps % ranges == 0 && steps / ranges % line == 0);
   };
   const bool join = p.lens || !apart(steps, a.ctas, a.key_tiles) || !apart(steps / a.side, a.ranges, a.tiles);
-  const bool wide = p.d == 128;
   cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, Roles<16>::NTHREADS, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
                         true, a, st);
   const bool staged = !wide || a.tiles <= STAGED_STEPS;
@@ -1255,7 +1261,10 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
     e = start(!wide ? cross_dkv_kernel<64, true> : staged ? cross_dkv_kernel<128, true> : cross_dkv_kernel<128, false>,
               dim3(a.ranges * a.side), Roles<8>::NTHREADS, !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a,
               st);
-  if (e == cudaSuccess && join) e = launch(wide ? cross_join_kernel<128> : cross_join_kernel<64>, gj, 256, 0, true, st, a);
+  if (e == cudaSuccess && join)
+    e = launch(many ? wide ? cross_join_kernel<128, 8> : cross_join_kernel<64, 4>
+                    : wide ? cross_join_kernel<128, 2> : cross_join_kernel<64, 2>,
+               gj, 256, 0, true, st, a);
   return e;
 }
 

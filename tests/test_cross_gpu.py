@@ -324,3 +324,12 @@ def test_key_tiles_side_by_side(fa, B, Hq, Hkv, Nq, Nk):
     q, k, v, _, g = make(B, Hq, Hkv, Nq, Nk, 128)
     check_bwd(fa, q, k, v, None, g)
     check_bwd(fa, q, k, v, torch.full((B,), Nk, device="cuda", dtype=torch.int32), g)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk,lens", [
+    (1, 2, 1, 9000, 200, None), (1, 1, 1, 20000, 40, [39]), (1, 4, 1, 20, 16000, None), (2, 1, 1, 7, 9000, [9000, 1])])
+def test_many_ranges_of_a_tile(fa, d, B, Hq, Hkv, Nq, Nk, lens):
+    """One or two output tiles, whose sums come from most of the GPU."""
+    q, k, v, lens, g = make(B, Hq, Hkv, Nq, Nk, d, lens)
+    check_bwd(fa, q, k, v, lens, g)
