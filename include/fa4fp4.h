@@ -442,7 +442,10 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_evict(const fa4fp4_cache* cache, const int
  * stride_n + i, strides in elements.  The last dimension is dense; ptr is 16-byte
  * aligned, and so is every row: strides (of dimensions larger than 1) are
  * multiples of 16 bytes, at least 0 and at most 2^40 bytes.  An input may have
- * strides of 0 (a broadcast).  The rows of an output do not overlap. */
+ * strides of 0 (a broadcast).  The rows of an output overlap neither each other nor,
+ * where not said otherwise, anything else of the call.  d is 64 or 128; B N is at
+ * most 2^30, heads are at most 2^20, and for the attention B Hq Nq and B Hkv Nk are
+ * below 2^31, B Hq at most 2^24 (FA4FP4_ERR_UNSUPPORTED). */
 typedef struct {
   void* ptr;
   int64_t stride_b, stride_h, stride_n;
@@ -496,7 +499,7 @@ FA4FP4_API fa4fp4_status fa4fp4_norm_rope(const fa4fp4_heads* q, const fa4fp4_he
  * fa4fp4_norm_rope_bwd_workspace_bytes(...) bytes of device memory (its size is 0,
  * and it may be NULL, for an empty problem), for this call alone while it runs; it
  * needs no initialisation.  Without a dq_weight or dk_weight it is not used and may
- * be NULL. */
+ * be NULL.  dq may be q, and dk may be k. */
 FA4FP4_API size_t fa4fp4_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
 FA4FP4_API fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const fa4fp4_heads* dk_out, int dout_dtype,
                                               const fa4fp4_heads* q, const fa4fp4_heads* k, int B, int Hq, int Hkv,

@@ -11,6 +11,12 @@
 // maximum, sum and O.  The warps' results are joined in shared memory, the
 // cluster's through distributed shared memory, each CTA taking a share of the
 // outputs.
+//
+// Measured: 64 sequences of 16 heads of 64, a query over 1..1500 keys 37 us, 0.88 of
+// the measured copy bandwidth.  One sequence of 8 kv heads of 128, 12 rows each over
+// 16,383 keys 19 us, 0.52: a share of 3.6 us of reading on each of 128 CTAs, the rest a
+// launch, the first boxes' way (2 us), the cluster's join (3 us) and the drain.  Eight
+// warps a CTA there: 31 us when four took 23.
 #include <cstring>
 #include <cuda_bf16.h>
 #include "common.cuh"

@@ -244,3 +244,15 @@ def test_far_offsets(fa):
     assert all(torch.equal(a, b) for a, b in zip(fa.qk_norm_rope(q, k, pos, f, *w), fa.qk_norm_rope(q0, k0, pos, f, *w)))
     out = fa.qk_norm_rope_bwd(q0, k0, q, k, pos, f, *w, dq=q, dk=k)
     assert all(torch.equal(a, b) for a, b in zip(out, fa.qk_norm_rope_bwd(q0, k0, q0, k0, pos, f, *w)))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_backward_in_place(fa, f32):
+    """dq in q's place, and dk in k's: more tokens than the GPU has warps."""
+    q, k, w, pos, g = make(3, 6, 2, 5000, 64)
+    freqs = fa.rope_freqs(64)
+    dy = [torch.randn(x.shape, generator=g, device="cuda").to(torch.float32 if f32 else torch.bfloat16) for x in (q, k)]
+    want = fa.qk_norm_rope_bwd(*dy, q, k, pos, freqs, *w)
+    got = fa.qk_norm_rope_bwd(*dy, q, k, pos, freqs, *w, dq=q, dk=k)
+    assert got[0] is q and got[1] is k
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
