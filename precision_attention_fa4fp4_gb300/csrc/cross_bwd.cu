@@ -70,11 +70,12 @@ struct Params {
   Divisor per_head, per_kv, hkv, nq;           // (per_kv: tiles)
   int key_tiles;                               // of Nk
   int items;                                   // query tiles in all
-  int ctas;                                    // of both kernels (the second: ranges * side)
-  int side, ranges;                            // second kernel: key tiles side by side, ranges of steps
+  int slots;                                   // CTAs at most, of either kernel
+  int ctas;                                    // of the first kernel
+  int side, ranges;                            // second kernel: key tiles side by side, ranges of steps (side CTAs each)
   int dq32, dk32, dv32;                        // rows begin on 32 bytes
   float* del;                                  // D [B][Hq][Nq]
-  float *part, *part_q;                        // partial sums: [2 ctas][dV, dK] and [2 ctas] tiles of dQ
+  float *part, *part_q;                        // partial sums: [2 slots][dV, dK] and [2 slots] tiles of dQ
 };
 
 // Row r of a query tile: query head within the group (G: none) and position.
@@ -1063,7 +1064,7 @@ __global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const 
 }
 
 // dV (y = 0), dK (y = 1) and dQ (y = 2) of the output tiles whose steps lie in
-// several ranges: the x below a.ctas, JOIN_PARTS CTAs (z) for each range that ends inside
+// several ranges: the x below a.slots, JOIN_PARTS CTAs (z) for each range that ends inside
 // a tile's steps and began at or before their first.  Then, where sequences have
 // lengths, zeros for the key tiles behind them: an x for each sequence and kv head.
 // More parts make shorter sums and more CTAs that find nothing to do: with eight partials
@@ -1075,11 +1076,11 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   const CrossParams& p = a.p;
   const int which = blockIdx.y, G = p.Hq / p.Hkv;
   const Strided& out = which == 2 ? p.dq : which ? p.dk : p.dv;
-  if ((int)blockIdx.x >= a.ctas) {
+  if ((int)blockIdx.x >= a.slots) {
     wait_for_previous();
     if (which == 2 || blockIdx.z > 0) return;
     int b, hk;
-    divide((int)blockIdx.x - a.ctas, a.hkv, b, hk);
+    divide((int)blockIdx.x - a.slots, a.hkv, b, hk);
     const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
     for (long long x = threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += 256)
       *reinterpret_cast<uint4*>(at(out, b, hk, from + (int)(x / (D / 8))) + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
@@ -1193,13 +1194,21 @@ void plan(Params& a, int B, int Hq, int Hkv, int Nq, int Nk, bool share, bool le
   a.key_tiles = (Nk + BN - 1) / BN;
   const long long steps = (long long)B * Hkv * a.key_tiles * a.tiles;
   const int sms = sm_count();
-  a.ctas = (int)(steps < sms ? steps : sms);
+  a.slots = (int)(steps < sms ? steps : sms);
   // as many key tiles side by side as divide them and leave no more than a fiftieth of the CTAs over
   a.side = 1;
   if (!lens)
     for (int n = 2; n <= SIDE_MAX; ++n)
-      if (a.key_tiles % n == 0 && a.ctas % n * 50 <= a.ctas) a.side = n;
-  a.ranges = a.ctas / a.side;
+      if (a.key_tiles % n == 0 && a.slots % n * 50 <= a.slots) a.side = n;
+  // short ranges: no more of them than the longest needs, and fewer partials (182 steps are 91 ranges of two, not 152
+  // of one or two: 7 heads, 241 queries, 1590 keys 34.1 -> 30.4 us; 24 heads, 5 queries, 6943 keys 31.4 -> 25.8;
+  // ranges of 111 steps gain nothing: 324 -> 332).  With lengths the steps are fewer, nobody here knows how many.
+  const auto ranges = [lens](long long n, int most) {
+    const long long each = (n + most - 1) / most;
+    return lens || each < 2 || each > 8 ? most : (int)((n + each - 1) / each);
+  };
+  a.ctas = ranges(steps, a.slots);
+  a.ranges = ranges(steps / a.side, a.slots / a.side);
 }
 
 size_t del_bytes(int B, int Hq, int Nq) { return ((size_t)B * Hq * Nq * sizeof(float) + 127) / 128 * 128; }
@@ -1218,7 +1227,7 @@ size_t cross_bwd_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   // (heads that share no tile make more tiles, never fewer CTAs)
   Params a;
   plan(a, B, Hq, Hkv, Nq, Nk, false, true);
-  return del_bytes(B, Hq, Nq) + (size_t)a.ctas * 6 * 128 * d * sizeof(float);
+  return del_bytes(B, Hq, Nq) + (size_t)a.slots * 6 * 128 * d * sizeof(float);
 }
 
 cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
@@ -1234,7 +1243,7 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   a.dq32 = on_words(p.dq); a.dk32 = on_words(p.dk); a.dv32 = on_words(p.dv);
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
-  a.part_q = a.part + (size_t)a.ctas * 4 * 128 * p.d;
+  a.part_q = a.part + (size_t)a.slots * 4 * 128 * p.d;
   const int rows = a.heads > 1 ? p.Nq : BM;
   if (!heads_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.dout, p.dout, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
@@ -1245,9 +1254,9 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const bool wide = p.d == 128;
   const long long lines = (long long)p.B * p.Hkv * min(a.key_tiles, a.tiles);
-  const bool many = a.ctas >= 8 * lines;
+  const bool many = a.slots >= 8 * lines;
   const int parts = many ? wide ? 8 : 4 : 2;
-  const dim3 grid(a.ctas), gj(a.ctas + (p.lens ? p.B * p.Hkv : 0), 3, parts);
+  const dim3 grid(a.ctas), gj(a.slots + (p.lens ? p.B * p.Hkv : 0), 3, parts);
   // no range ends inside an output tile's steps, and no key is without one?
   const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
   const auto apart = [](long long steps, int ranges, int line) {
@@ -1259,8 +1268,8 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   const bool staged = !wide || a.tiles <= STAGED_STEPS;
   if (e == cudaSuccess)
     e = start(!wide ? cross_dkv_kernel<64, true> : staged ? cross_dkv_kernel<128, true> : cross_dkv_kernel<128, false>,
-              dim3(a.ranges * a.side), Roles<8>::NTHREADS, !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a,
-              st);
+              dim3(a.ranges * a.side), Roles<8>::NTHREADS,
+              !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a, st);
   if (e == cudaSuccess && join)
     e = launch(many ? wide ? cross_join_kernel<128, 8> : cross_join_kernel<64, 4>
                     : wide ? cross_join_kernel<128, 2> : cross_join_kernel<64, 2>,
