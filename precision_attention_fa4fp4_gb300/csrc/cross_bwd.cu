@@ -72,6 +72,8 @@ struct Params {
   int items;                                   // query tiles in all
   int slots;                                   // CTAs at most, of either kernel
   int ctas;                                    // of the first kernel
+  int joins, by_query_tile, by_key_tile;       // third kernel: x that join, and what an x is
+  int parts_q, parts_k;                        // CTAs of a sum
   int side, ranges;                            // second kernel: key tiles side by side, ranges of steps (side CTAs each)
   int dq32, dk32, dv32;                        // rows begin on 32 bytes
   float* del;                                  // D [B][Hq][Nq]
@@ -1063,94 +1065,45 @@ __global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const 
   if (warp == K::W_MMA) tmem_dealloc(tbase, TMEM_COLS);
 }
 
-// dV (y = 0), dK (y = 1) and dQ (y = 2) of the output tiles whose steps lie in
-// several ranges: the x below a.slots, JOIN_PARTS CTAs (z) for each range that ends inside
-// a tile's steps and began at or before their first.  Then, where sequences have
-// lengths, zeros for the key tiles behind them: an x for each sequence and kv head.
-// More parts make shorter sums and more CTAs that find nothing to do: with eight partials
-// and more of a tile a thread takes 8 columns of one row (6 heads, 76,666 queries, 188
-// keys 202 -> 167 us; where 6 sequences of 24 heads have a query over 230 keys 23.4
-// becomes 25.4, so otherwise two).
-template <int D, int JOIN_PARTS>
-__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ Params a) {
+// The sum of a tile's partials, EACH times 8 columns of a row for a thread; thin: the steps, where some ranges are
+// empty.
+template <int D, int EACH>
+FA4_DEV void join(const Params& a, const Strided& out, const Range& place, int slot0, int c0, int c1, long long thin) {
   const CrossParams& p = a.p;
   const int which = blockIdx.y, G = p.Hq / p.Hkv;
-  const Strided& out = which == 2 ? p.dq : which ? p.dk : p.dv;
-  if ((int)blockIdx.x >= a.slots) {
-    wait_for_previous();
-    if (which == 2 || blockIdx.z > 0) return;
-    int b, hk;
-    divide((int)blockIdx.x - a.slots, a.hkv, b, hk);
-    const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
-    for (long long x = threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += 256)
-      *reinterpret_cast<uint4*>(at(out, b, hk, from + (int)(x / (D / 8))) + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int side = which == 2 ? 1 : a.side, ranges = which == 2 ? a.ctas : a.ranges;
-  const int c0 = blockIdx.x / side, lane_tile = blockIdx.x % side;     // (c0 may be behind the last range)
-  __shared__ Range place;
-  __shared__ int slot0, c1, thin;
-  __shared__ long long sum;
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    const long long total = all_steps(a, which == 2, lane);
-    const long long start = range_start(total, c0, ranges), end = range_start(total, c0 + 1, ranges);
-    Range x;
-    x.left = 0;
-    if (end > start && end < total) {
-      find_step(a, end, which == 2, lane_tile, lane, x);
-      // (a range that ends with a tile's steps, or began inside them, joins nothing)
-      x.left = x.t > 0 && start <= end - x.t;
-    }
-    if (x.left) {
-      // the last range that meets the tile's steps
-      const long long last = end - x.t + (which == 2 ? x.nt : a.tiles);
-      int c = c0;
-      for (;;) {
-        const unsigned more =
-            __ballot_sync(0xffffffffu, c + 1 + lane < ranges && range_start(total, c + 1 + lane, ranges) < last);
-        c += __popc(more);
-        if (~more) break;
-      }
-      if (lane == 0) {
-        slot0 = start < end - x.t;                 // (slot 1 where the range began in a tile before)
-        c1 = c;
-        thin = total < ranges;                     // some ranges are empty: each has a step at most
-        sum = total;
-      }
-    }
-    if (lane == 0) place = x;
-  }
-  // (where the sums lie follows from the shapes and lengths: the partials are waited for after that, by every CTA,
-  // so that this kernel does not end before the ones before it)
-  wait_for_previous();
-  __syncthreads();
-  if (!place.left) return;
+  const bool rows = which == 2;
+  const int side = rows ? 1 : a.side, ranges = rows ? a.ctas : a.ranges;
   const float f = which ? p.scale : 1.f;
-  float* part = which == 2 ? a.part_q : a.part;
-  constexpr int EACH = 128 * (D / 8) / (256 * JOIN_PARTS);      // of a thread: rows' 8 columns
+  float* part = rows ? a.part_q : a.part;
+  constexpr int STRIDE = 128 * (D / 8) / EACH;    // threads of all parts
   const int x0 = blockIdx.z * 256 + threadIdx.x;
   float v[EACH][8] = {};
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    if (thin && range_start(sum, c + 1, ranges) == range_start(sum, c, ranges)) continue;
-    const int slot = 2 * (c * side + lane_tile) + (c == c0 ? slot0 : 0);
-    const int at = which == 2 ? slot : 2 * slot + which;
+  const auto add = [&](int c) {
+    const int slot = 2 * (c * side + place.tile % side) + (c == c0 ? slot0 : 0);
+    const int at = rows ? slot : 2 * slot + which;
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
-      const int x = x0 + e * 256 * JOIN_PARTS;
+      const int x = x0 + e * STRIDE;
       const float4 u = *reinterpret_cast<const float4*>(partial(part, D, at, x % 128, x / 128 * 8));
       const float4 w = *reinterpret_cast<const float4*>(partial(part, D, at, x % 128, x / 128 * 8 + 4));
       v[e][0] += u.x; v[e][1] += u.y; v[e][2] += u.z; v[e][3] += u.w;
       v[e][4] += w.x; v[e][5] += w.y; v[e][6] += w.z; v[e][7] += w.w;
     }
+  };
+  if (!thin) {
+    constexpr int AHEAD = EACH == 1 ? 8 : 4;
+#pragma unroll AHEAD
+    for (int c = c0; c <= c1; ++c) add(c);
+  } else {
+    for (int c = c0; c <= c1; ++c)
+      if (range_start(thin, c + 1, ranges) > range_start(thin, c, ranges)) add(c);
   }
 #pragma unroll
   for (int e = 0; e < EACH; ++e) {
-    const int x = x0 + e * 256 * JOIN_PARTS, r = x % 128, i = x / 128 * 8;
+    const int x = x0 + e * STRIDE, r = x % 128, i = x / 128 * 8;
     int h = place.hk, row = place.tile * BN + r;
     bool valid = row < p.Nk;
-    if (which == 2) {
+    if (rows) {
       int g;
       tile_row(a, place.tile, r, G, g, row);
       valid = g < G;
@@ -1161,6 +1114,90 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
           make_uint4(pack2(v[e][0] * f, v[e][1] * f), pack2(v[e][2] * f, v[e][3] * f), pack2(v[e][4] * f, v[e][5] * f),
                      pack2(v[e][6] * f, v[e][7] * f));
   }
+}
+
+// dV (y = 0), dK (y = 1) and dQ (y = 2) of the output tiles whose steps lie in
+// several ranges: a few CTAs (z) for each x below a.joins.  That is an output tile, where
+// there are fewer of them than ranges, or else a range that ends inside a tile's steps
+// and began at or before their first.  Then, where sequences have lengths, zeros for
+// the key tiles behind them: an x for each sequence and kv head.
+// Tiles of four ranges and more are shared by D / 16 CTAs, a row's 8 columns a thread, the
+// others by two (6 heads, 76,666 queries, 188 keys 202 -> 167 us).  An x for every
+// range and all parts for every sum were 3600 CTAs of which 50 found something (7
+// heads, 241 queries, 1..1590 keys 38.0 -> 31.7 us; 6 heads, 5985 queries, 87 keys 40 -> 35).
+// FEW: are there such tiles?  (Their sums take more registers.)
+template <int D, bool FEW>
+__global__ void __launch_bounds__(256, FEW ? 2 : 3) cross_join_kernel(const __grid_constant__ Params a) {
+  const CrossParams& p = a.p;
+  const int which = blockIdx.y;
+  const Strided& out = which == 2 ? p.dq : which ? p.dk : p.dv;
+  if ((int)blockIdx.x >= a.joins) {
+    wait_for_previous();
+    if (which == 2 || blockIdx.z > 0) return;
+    int b, hk;
+    divide((int)blockIdx.x - a.joins, a.hkv, b, hk);
+    const int from = (key_count(p, b, false) + BN - 1) / BN * BN;
+    for (long long x = threadIdx.x; x < (long long)(p.Nk - from) * (D / 8); x += 256)
+      *reinterpret_cast<uint4*>(at(out, b, hk, from + (int)(x / (D / 8))) + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const bool rows = which == 2;
+  const int parts = rows ? a.parts_q : a.parts_k;
+  if ((int)blockIdx.z >= parts) return;
+  const int side = rows ? 1 : a.side, ranges = rows ? a.ctas : a.ranges;
+  __shared__ Range place;                         // (left: is there anything to join?)
+  __shared__ int slot0, c0, c1, thin;
+  __shared__ long long sum;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const long long total = all_steps(a, rows, lane);
+    long long start = 0;                          // the tile's first step
+    Range x;
+    x.left = 0;
+    if (rows ? a.by_query_tile : a.by_key_tile) {
+      const int each = rows ? a.tiles : a.key_tiles, bh = blockIdx.x / each;
+      x.tile = blockIdx.x - bh * each;
+      divide(bh, a.hkv, x.b, x.hk);
+      if (x.b < p.B) {
+        x.nt = tiles_of(a, x.b);
+        x.left = rows ? x.nt > 0 : x.tile < x.nt;
+        start = (long long)x.b * a.key_tiles;     // key tiles of the sequences before
+        if (p.lens) {
+          start = 0;
+          for (int b = lane; b < x.b; b += 32) start += tiles_of(a, b);
+          for (int o = 16; o > 0; o /= 2) start += __shfl_xor_sync(0xffffffffu, start, o);
+        }
+        start = start / side * p.Hkv * a.tiles +
+                (rows ? (long long)(x.hk * a.tiles + x.tile) * x.nt
+                      : (long long)(x.hk * (x.nt / side) + x.tile / side) * a.tiles);
+      }
+    } else {
+      const int c = blockIdx.x / side;            // (may be behind the last range)
+      const long long begin = range_start(total, c, ranges), end = range_start(total, c + 1, ranges);
+      if (end > begin && end < total) {
+        find_step(a, end, rows, blockIdx.x % side, lane, x);
+        start = end - x.t;
+        x.left = x.t > 0 && begin <= start;
+      }
+    }
+    if (x.left && lane == 0) {
+      // the ranges of its first and last step
+      c0 = (int)quotient((start + 1) * ranges - 1, total);
+      c1 = (int)quotient((start + (rows ? x.nt : a.tiles)) * ranges - 1, total);
+      slot0 = range_start(total, c0, ranges) < start;      // (slot 1 where the range began in a tile before)
+      thin = total < ranges;                               // some ranges are empty: each has a step at most
+      sum = total;
+      x.left = c0 < c1;
+    }
+    if (lane == 0) place = x;
+  }
+  // (where the sums lie follows from the shapes and lengths: the partials are waited for after that, by every CTA,
+  // so that this kernel does not end before the ones before it)
+  wait_for_previous();
+  __syncthreads();
+  if (!place.left) return;
+  if (!FEW || parts == 2) join<D, D / 32>(a, out, place, slot0, c0, c1, thin ? sum : 0);
+  else join<D, 1>(a, out, place, slot0, c0, c1, thin ? sum : 0);
 }
 
 // Zeros where there is no partner at all.
@@ -1253,26 +1290,31 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
       !heads_map(&a.dv, p.dv, p.B, p.Hkv, p.Nk, p.d, 32, 1))
     return cudaErrorInvalidValue;
   const bool wide = p.d == 128;
-  const long long lines = (long long)p.B * p.Hkv * min(a.key_tiles, a.tiles);
-  const bool many = a.slots >= 8 * lines;
-  const int parts = many ? wide ? 8 : 4 : 2;
-  const dim3 grid(a.ctas), gj(a.slots + (p.lens ? p.B * p.Hkv : 0), 3, parts);
-  // no range ends inside an output tile's steps, and no key is without one?
+  // does a range end inside an output tile's steps?
   const long long steps = (long long)p.B * p.Hkv * a.key_tiles * a.tiles;
   const auto apart = [](long long steps, int ranges, int line) {
     return line == 1 || (steps % ranges == 0 && steps / ranges % line == 0);
   };
-  const bool join = p.lens || !apart(steps, a.ctas, a.key_tiles) || !apart(steps / a.side, a.ranges, a.tiles);
-  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, Roles<16>::NTHREADS, wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES,
-                        true, a, st);
+  const bool join_q = p.lens ? a.key_tiles > 1 : !apart(steps, a.ctas, a.key_tiles);
+  const bool join_k = p.lens ? a.tiles > 1 : !apart(steps / a.side, a.ranges, a.tiles);
+  const long long query_tiles = a.items, key_tiles = (long long)p.B * p.Hkv * a.key_tiles;
+  a.by_query_tile = query_tiles < a.slots;
+  a.by_key_tile = key_tiles < a.slots;
+  a.joins = max(join_q ? (int)min(query_tiles, (long long)a.slots) : 0,
+                join_k ? (int)min(key_tiles, (long long)a.slots) : 0);
+  a.parts_q = !join_q ? 0 : 4 * query_tiles <= a.slots ? p.d / 16 : 2;
+  a.parts_k = !join_k ? 0 : 4 * key_tiles <= a.slots ? p.d / 16 : 2;
+  const dim3 grid(a.ctas), gj(a.joins + (p.lens ? p.B * p.Hkv : 0), 3, max(max(a.parts_q, a.parts_k), 1));
+  cudaError_t e = start(wide ? cross_dq_kernel<128> : cross_dq_kernel<64>, grid, Roles<16>::NTHREADS,
+                        wide ? SmemQ<128>::BYTES : SmemQ<64>::BYTES, true, a, st);
   const bool staged = !wide || a.tiles <= STAGED_STEPS;
   if (e == cudaSuccess)
     e = start(!wide ? cross_dkv_kernel<64, true> : staged ? cross_dkv_kernel<128, true> : cross_dkv_kernel<128, false>,
               dim3(a.ranges * a.side), Roles<8>::NTHREADS,
               !wide ? SmemK<64, true>::BYTES : staged ? SmemK<128, true>::BYTES : SmemK<128, false>::BYTES, true, a, st);
-  if (e == cudaSuccess && join)
-    e = launch(many ? wide ? cross_join_kernel<128, 8> : cross_join_kernel<64, 4>
-                    : wide ? cross_join_kernel<128, 2> : cross_join_kernel<64, 2>,
+  if (e == cudaSuccess && gj.x > 0)
+    e = launch(gj.z > 2 ? wide ? cross_join_kernel<128, true> : cross_join_kernel<64, true>
+                        : wide ? cross_join_kernel<128, false> : cross_join_kernel<64, false>,
                gj, 256, 0, true, st, a);
   return e;
 }

@@ -333,3 +333,13 @@ def test_many_ranges_of_a_tile(fa, d, B, Hq, Hkv, Nq, Nk, lens):
     """One or two output tiles, whose sums come from most of the GPU."""
     q, k, v, lens, g = make(B, Hq, Hkv, Nq, Nk, d, lens)
     check_bwd(fa, q, k, v, lens, g)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk,lens", [
+    (1, 7, 1, 241, 1590, [1234]), (3, 2, 1, 5985, 87, None), (7, 4, 1, 500, 66, [66, 1, 0, 65, 20, 0, 3]),
+    (40, 2, 2, 130, 129, None), (40, 2, 2, 130, 129, [129, 0, 128, 5] * 10), (9, 7, 1, 33, 271, None)])
+def test_joins(fa, d, B, Hq, Hkv, Nq, Nk, lens):
+    """Output tiles of a few ranges and of many, fewer of them than ranges and more, sequences without keys between."""
+    q, k, v, lens, g = make(B, Hq, Hkv, Nq, Nk, d, lens)
+    check_bwd(fa, q, k, v, lens, g)
