@@ -109,16 +109,19 @@ bool make_rows_map(CUtensorMap* m, const void* base, int row_bytes, uint64_t row
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, row_bytes, rows, 1, row_bytes, box_rows,
                   row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
-bool make_heads_map(CUtensorMap* m, const void* base, int d, const uint64_t (&dims)[3], const int64_t (&strides)[3],
+bool make_heads_map(CUtensorMap* m, const void* base, int d, int rank, const uint64_t* dims, const int64_t* strides,
                     uint32_t rows, uint32_t heads) {
   EncodeTiledFn enc = encoder();
   if (!enc) return false;
-  const cuuint64_t size[4] = {(cuuint64_t)d, dims[0], dims[1], dims[2]};
+  cuuint64_t size[5] = {(cuuint64_t)d};
   // (a dimension of one element needs some stride that the encoder takes)
-  cuuint64_t bytes[3];
-  for (int i = 0; i < 3; ++i) bytes[i] = dims[i] > 1 ? (cuuint64_t)strides[i] * 2 : (cuuint64_t)d * 2;
-  const cuuint32_t box[4] = {64, rows, heads, 1}, es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), size, bytes, box, es,
+  cuuint64_t bytes[4];
+  for (int i = 0; i < rank - 1; ++i) {
+    size[i + 1] = dims[i];
+    bytes[i] = dims[i] > 1 ? (cuuint64_t)strides[i] * 2 : (cuuint64_t)d * 2;
+  }
+  const cuuint32_t box[5] = {64, rows, heads, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), size, bytes, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

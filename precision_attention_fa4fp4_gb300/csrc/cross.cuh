@@ -31,6 +31,15 @@ FA4_DEV void tma_heads(void* dst, const HeadsMap& m, uint64_t* bar, int c, int n
       : "memory");
 }
 
+// A box of a group_map at channel c, row n, head g of kv head hk, sequence b.
+FA4_DEV void tma_group(void* dst, const HeadsMap& m, uint64_t* bar, int c, int n, int g, int hk, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(&m.map)), "r"(smem_u32(bar)), "r"(c), "r"(n), "r"(g), "r"(hk), "r"(b * m.own_b)
+      : "memory");
+}
+
 // A box from shared memory, by one lane; rows behind the tensor's are left out.
 FA4_DEV void tma_heads_store(const HeadsMap& m, const void* src, int c, int n, int h, int b) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(

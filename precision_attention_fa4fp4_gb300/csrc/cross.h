@@ -26,6 +26,8 @@ struct HeadsMap {
   int own_h, own_b;
 };
 bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int rows, int heads);
+// ... whose boxes end with their kv head's G heads: zeros behind them (tma_group).
+bool group_map(HeadsMap* m, const Strided& t, int B, int Hkv, int G, int N, int d, int rows, int heads);
 
 // Few query rows: keys shared among clusters, products of 16 rows.
 bool cross_few_rows(const CrossParams& p);

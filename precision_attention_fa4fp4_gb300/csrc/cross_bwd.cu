@@ -65,6 +65,7 @@ constexpr float L2E = 1.4426950408889634f;
 struct Params {
   CrossParams p;
   HeadsMap q, dout, o, k, v;
+  HeadsMap group_q, group_dout;                // second kernel, where heads share a tile
   HeadsMap dq, dk, dv;                         // boxes of 32 rows (dq: where heads share no tile)
   int tiles, heads, box;                       // query tiles of a kv head, as in the forward
   Divisor per_head, per_kv, hkv, nq;           // (per_kv: tiles)
@@ -760,7 +761,8 @@ __global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const 
     *abort_flag = 0;
     fence_barrier_init();
   }
-  // rows of a ring slot that no box brings are zeros: P and dS are 0 there
+  // rows of a ring slot that no box brings are zeros, and so are those that it brings from behind the kv head's heads:
+  // P and dS are 0 there, and 0 x NaN is not
   if (a.box < BM)
     for (int i = threadIdx.x; i < RS * L::TILE / 16; i += K::NTHREADS)
       reinterpret_cast<uint4*>(smem + L::OFF_R)[i] = make_uint4(0, 0, 0, 0);
@@ -794,22 +796,24 @@ __global__ void __launch_bounds__(Roles<8>::NTHREADS, 1) cross_dkv_kernel(const 
           ++count;
           return true;
         };
-        auto load_r = [&](const HeadsMap& m) -> bool {
+        auto load_r = [&](const HeadsMap& m, const HeadsMap& group) -> bool {
           const int st = rn % RS;
           if (rn >= RS && !mbar_wait(&r_empty[st], (rn / RS - 1) & 1, abort_flag, p.err)) return false;
           mbar_arrive_expect_tx(&r_full[st], a.box * 2 * D);
           int g, n;
           divide(at_.t, a.per_head, g, n);
-          const int h = at_.hk * G + g * a.heads;
           n *= BM;
-          for (int c = 0; c < D / 64; ++c)
-            tma_heads(smem + L::OFF_R + st * L::TILE + c * CH, m, &r_full[st], 64 * c, n, h, at_.b);
+          for (int c = 0; c < D / 64; ++c) {
+            uint8_t* dst = smem + L::OFF_R + st * L::TILE + c * CH;
+            if (a.heads > 1) tma_group(dst, group, &r_full[st], 64 * c, n, g * a.heads, at_.hk, at_.b);
+            else tma_heads(dst, m, &r_full[st], 64 * c, n, at_.hk * G + g, at_.b);
+          }
           ++rn;
           return true;
         };
         bool ok = true, fresh = true;
         while (ok && at_.left > 0) {
-          ok = load_r(a.q) && (!fresh || load_kv(a.k, k_full, k_empty, L::OFF_K, kn)) && load_r(a.dout) &&
+          ok = load_r(a.q, a.group_q) && (!fresh || load_kv(a.k, k_full, k_empty, L::OFF_K, kn)) && load_r(a.dout, a.group_dout) &&
                (!fresh || load_kv(a.v, v_full, v_empty, L::OFF_V, vn));
           if (fresh) ++ln;
           fresh = false;
@@ -1281,7 +1285,10 @@ cudaError_t launch_cross_bwd(const CrossParams& p, cudaStream_t st) {
   a.del = reinterpret_cast<float*>(p.work);
   a.part = reinterpret_cast<float*>(p.work + del_bytes(p.B, p.Hq, p.Nq));
   a.part_q = a.part + (size_t)a.slots * 4 * 128 * p.d;
-  const int rows = a.heads > 1 ? p.Nq : BM;
+  const int rows = a.heads > 1 ? p.Nq : BM, G = p.Hq / p.Hkv;
+  if (a.heads > 1 && (!group_map(&a.group_q, p.q, p.B, p.Hkv, G, p.Nq, p.d, rows, a.heads) ||
+                      !group_map(&a.group_dout, p.dout, p.B, p.Hkv, G, p.Nq, p.d, rows, a.heads)))
+    return cudaErrorInvalidValue;
   if (!heads_map(&a.q, p.q, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.dout, p.dout, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||
       !heads_map(&a.o, p.o, p.B, p.Hq, p.Nq, p.d, rows, a.heads) ||

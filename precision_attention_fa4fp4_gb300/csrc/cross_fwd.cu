@@ -519,7 +519,15 @@ bool heads_map(HeadsMap* m, const Strided& t, int B, int H, int N, int d, int ro
   m->own_h = t.h != 0;
   const uint64_t dims[3] = {(uint64_t)N, m->own_h ? (uint64_t)H : 1, m->own_b ? (uint64_t)B : 1};
   const int64_t strides[3] = {t.n, t.h, t.b};
-  return make_heads_map(&m->map, t.p, d, dims, strides, (uint32_t)rows, (uint32_t)heads);
+  return make_heads_map(&m->map, t.p, d, 4, dims, strides, (uint32_t)rows, (uint32_t)heads);
+}
+
+bool group_map(HeadsMap* m, const Strided& t, int B, int Hkv, int G, int N, int d, int rows, int heads) {
+  m->own_b = t.b != 0;
+  m->own_h = 1;
+  const uint64_t dims[4] = {(uint64_t)N, (uint64_t)G, (uint64_t)Hkv, m->own_b ? (uint64_t)B : 1};
+  const int64_t strides[4] = {t.n, t.h, G * t.h, t.b};
+  return make_heads_map(&m->map, t.p, d, 5, dims, strides, (uint32_t)rows, (uint32_t)heads);
 }
 
 int sm_count() {

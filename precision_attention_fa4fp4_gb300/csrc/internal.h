@@ -8,9 +8,9 @@
 
 namespace fa4 {
 
-// Tiled map of a strided bf16 [B][H][N][d] tensor: boxes of 64 channels (128-byte
-// swizzle) x `rows` x `heads`; dims, strides (elements): N, H, B.
-bool make_heads_map(CUtensorMap* m, const void* base, int d, const uint64_t (&dims)[3], const int64_t (&strides)[3],
+// Tiled map of a strided bf16 tensor: boxes of 64 channels (128-byte swizzle) x `rows` x
+// `heads`; dims, strides (elements) without d's: N, H, B (rank 4) or N, G, Hkv, B (5).
+bool make_heads_map(CUtensorMap* m, const void* base, int d, int rank, const uint64_t* dims, const int64_t* strides,
                     uint32_t rows, uint32_t heads);
 
 struct Thresh { float v[7]; };

@@ -1,0 +1,68 @@
+"""Norm and rotation, and cross attention, at the ends of what their calls allow."""
+import pytest
+import torch
+
+import layer_ref as ref
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def fa():
+    return require_gpu()
+
+
+def make(B, Hq, Hkv, Nq, Nk, d, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    new = lambda H, N: torch.randn((B, H, N, d), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    return new(Hq, Nq), new(Hkv, Nk), new(Hkv, Nk), new(Hq, Nq)
+
+
+def check_fwd(fa, q, k, v):
+    o, lse = fa.cross_fwd(q, k, v)
+    want, bound, wl, bl = ref.cross(q, k, v)
+    ref.assert_within(o, want, bound, "o")
+    ref.assert_within(lse, wl, bl, "lse")
+    return o, lse
+
+
+# query heads that share a tile and do not fill their kv head's last one
+SHARED = [(1, 14, 2, 20, 300), (2, 21, 3, 33, 129), (1, 10, 2, 64, 64), (2, 14, 2, 1, 40), (1, 12, 4, 50, 1000)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", SHARED)
+def test_gradients_of_tiles_not_filled(fa, d, B, Hq, Hkv, Nq, Nk):
+    q, k, v, dout = make(B, Hq, Hkv, Nq, Nk, d)
+    o, lse = check_fwd(fa, q, k, v)
+    for name, x, (want, bound) in zip(("dq", "dk", "dv"), fa.cross_bwd(q, k, v, o, dout, lse),
+                                      ref.cross_bwd(q, k, v, o, dout, lse)):
+        ref.assert_within(x, want, bound, name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), INF, 3e38])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk", SHARED)
+def test_kv_heads_stay_apart(fa, d, bad, B, Hq, Hkv, Nq, Nk):
+    """What is not finite in one kv head, its queries or their gradients, changes nothing in the others."""
+    q, k, v, dout = make(B, Hq, Hkv, Nq, Nk, d)
+    G = Hq // Hkv
+    o, lse = fa.cross_fwd(q, k, v)
+    want = fa.cross_bwd(q, k, v, o, dout, lse)
+    for h in (1, Hkv - 1):
+        q2, k2, v2, g2 = (x.clone() for x in (q, k, v, dout))
+        others = [x for x in range(Hkv) if x != h]
+        heads = [x for x in range(Hq) if x // G != h]
+        for x in (q2, g2):
+            x[:, h * G: (h + 1) * G, ::3] = bad
+        k2[:, h, ::2], v2[:, h, 1::2] = bad, bad
+        for a, b, e in ((q2, k2, g2), (q2, k, dout), (q, k, g2)):
+            o2, lse2 = fa.cross_fwd(a, b, v2)
+            assert torch.equal(o2[:, heads], o[:, heads]) and torch.equal(lse2[:, heads], lse[:, heads])
+            dq, dk, dv = fa.cross_bwd(a, b, v2, o2, e, lse2)
+            assert torch.equal(dq[:, heads], want[0][:, heads])
+            assert torch.equal(dk[:, others], want[1][:, others]) and torch.equal(dv[:, others], want[2][:, others])
+    fa.sync_status()
