@@ -99,7 +99,7 @@ FA4_DEV void angles(const RopeParams& p, const uint64_t* turn, const uint8_t* ax
   const int* at = p.pos + b * p.pos_b + n;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t where = __ldg(at + (long long)axis[8 * l + i] * p.N);
+    const int64_t where = at[(long long)axis[8 * l + i] * p.N];   // (plainly: the launch before may have written it)
     const int rest = (int)(((uint64_t)where * turn[8 * l + i]) >> 32);   // of a turn, times 2^32
     const float th = (float)rest * 1.46291807926715968e-9f;              // 2 pi / 2^32
     (i % 2 ? c[i / 2].y : c[i / 2].x) = __cosf(th);

@@ -66,3 +66,43 @@ def test_kv_heads_stay_apart(fa, d, bad, B, Hq, Hkv, Nq, Nk):
             assert torch.equal(dq[:, heads], want[0][:, heads])
             assert torch.equal(dk[:, others], want[1][:, others]) and torch.equal(dv[:, others], want[2][:, others])
     fa.sync_status()
+
+
+@pytest.mark.parametrize("B,H,N,axes", [(64, 8, 1, 1), (2, 4, 600, 3)])
+def test_positions_of_the_launch_before(fa, B, H, N, axes):
+    """Positions, weights and rows that the launch right before the call writes, over and over."""
+    d = 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((B, H, N, d), generator=g, device="cuda").to(torch.bfloat16)
+    dy = torch.randn((B, H, N, d), generator=g, device="cuda").to(torch.bfloat16)
+    sections = [d // 2 - (axes - 1) * (d // 2 // axes)] + [d // 2 // axes] * (axes - 1)
+    freqs = fa.rope_freqs(d, sections)
+    start = torch.randint(0, 1000, (B, axes, N), generator=g, device="cuda").int()
+    steps = 60
+    want = []
+    for i in range(steps):
+        pos = start + 7 * i
+        torch.cuda.synchronize()
+        want.append((fa.qk_norm_rope(x, None, pos, freqs, sections=sections)[0],
+                     fa.qk_norm_rope_bwd(dy, None, x, None, pos, freqs, sections=sections)[0]))
+        torch.cuda.synchronize()
+    pos = start.clone()
+
+    def run():
+        got = []
+        for i in range(steps):
+            y = fa.qk_norm_rope(x, None, pos, freqs, sections=sections)[0]
+            got.append((y, fa.qk_norm_rope_bwd(dy, None, x, None, pos, freqs, sections=sections)[0]))
+            pos.add_(7)
+        return got
+
+    eager = run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for _ in range(5):
+        pos.copy_(start)
+        graph.replay()
+        for got in (eager, captured):
+            for a, b in zip(want, got):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
