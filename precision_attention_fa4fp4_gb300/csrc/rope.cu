@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
   tab.load(p);
   const int lane = threadIdx.x % 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
-  const int tasks = by_tokens.d * (nq + nk);
-  for (int task = blockIdx.x * WARPS + threadIdx.x / 32; task < tasks; task += gridDim.x * WARPS) {
+  for (Tasks task{blockIdx.x * WARPS + threadIdx.x / 32, gridDim.x * WARPS, (uint32_t)by_tokens.d * (nq + nk)};
+       task.more(); task.next()) {
     int part, m, b, n;
-    divide(task, by_tokens, part, m);
+    divide((int)task.now, by_tokens, part, m);
     divide(m, by_n, b, n);
     const int t = part >= nq;
     const RopeTensor& T = p.t[t];
@@ -235,14 +235,14 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
   const int t = (int)blockIdx.x >= p.ctas[0];
   const int cta = t ? (int)blockIdx.x - p.ctas[0] : (int)blockIdx.x;
   const RopeTensor& T = p.t[t];
-  const int tasks = by_tokens.d * (t ? nk : nq);
   float2 da[4], db[4], wa[4], wb[4];
   tab.template weights<PAIRS>(t, c0, c1, wa, wb);
 #pragma unroll
   for (int j = 0; j < 4; ++j) da[j] = db[j] = both(0.f);
-  for (int task = cta * WARPS + warp; task < tasks; task += p.ctas[t] * WARPS) {
+  for (Tasks task{(uint32_t)(cta * WARPS + warp), (uint32_t)(p.ctas[t] * WARPS), (uint32_t)by_tokens.d * (t ? nk : nq)};
+       task.more(); task.next()) {
     int part, m, b, n;
-    divide(task, by_tokens, part, m);
+    divide((int)task.now, by_tokens, part, m);
     divide(m, by_n, b, n);
     const int h0 = part * chunk, h1 = min(T.H, h0 + chunk);
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;

@@ -5,6 +5,12 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#ifdef __CUDACC__
+#define FA4_BOTH __host__ __device__ __forceinline__
+#else
+#define FA4_BOTH inline
+#endif
+
 namespace fa4 {
 
 // A strided [B][H][N][d] tensor: element strides, the last dimension dense.
@@ -46,6 +52,14 @@ struct Divisor {
     while ((1ll << s) < d) ++s;
     m = (uint32_t)((((1ull << s) - (uint64_t)d) << 32) / (uint64_t)d + 1);
   }
+};
+
+// A warp's tasks: every `step`th of `all` from `now` on.  Counted without a sign: 2^30 tokens with heads of q
+// and of k are 2^31 tasks, and a warp's last step goes behind them.
+struct Tasks {
+  uint32_t now, step, all;
+  FA4_BOTH bool more() const { return now < all; }
+  FA4_BOTH void next() { now += step; }
 };
 
 struct RopeTensor {            // q or k
