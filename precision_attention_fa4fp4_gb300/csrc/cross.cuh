@@ -22,6 +22,12 @@ FA4_DEV int key_count(const CrossParams& p, int b, bool report = true) {
   return len < 0 ? 0 : p.Nk;
 }
 
+// lse of a row whose weights 2^(c s - ref) add up to l; ref holds `down` (0 to 126), which is taken out of both before
+// the logarithm: what little l differs from 2^-down by is not rounded away beside it.
+FA4_DEV float lse_of(float ref, float l, int down) {
+  return ((ref - (float)down) + log2f(l * __uint_as_float((uint32_t)(127 + down) << 23))) * 0.69314718055994531f;
+}
+
 // A box at channel c, row n, head h, sequence b.
 FA4_DEV void tma_heads(void* dst, const HeadsMap& m, uint64_t* bar, int c, int n, int h, int b) {
   asm volatile(

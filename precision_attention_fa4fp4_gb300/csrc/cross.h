@@ -16,6 +16,7 @@ struct CrossParams {
   unsigned* err;
   int B, Hq, Hkv, Nq, Nk, d;
   float scale, c;                         // softmax scale, fl32(scale * log2 e)
+  int keys_log2;                          // forward: Nk <= 2^it
   uint8_t* work;                          // backward workspace
 };
 

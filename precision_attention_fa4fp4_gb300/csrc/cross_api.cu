@@ -228,6 +228,7 @@ fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Nq = Nq; p.Nk = Nk; p.d = d;
   p.scale = softmax_scale_of(softmax_scale, d);
   p.c = (float)((double)p.scale * 1.4426950408889634);
+  while ((1LL << p.keys_log2) < Nk) ++p.keys_log2;
   return status_of((cross_few_rows(p) ? launch_cross_token : launch_cross_fwd)(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -7,12 +7,15 @@
 // (item i goes to CTA i mod grid), so that those at work at a time read the
 // same K and V.  16 warps in four groups:
 //   warps 0-3    softmax of tile A, warps 4-7 of tile B: a thread per row.  P =
-//                2^(c s - c m) rounded to bf16 into tensor memory over S, in two
+//                2^(c s - c m - down) rounded to bf16 into tensor memory over S, in two
 //                halves of the keys, so that P V sets out on the first while the second
 //                is formed; the normalizer from P before the rounding.  The reference m
-//                follows the running maximum only when that passes it by 2^8 (P stays
-//                within bf16's range and relative precision), and only then O is
-//                rescaled.
+//                follows the running maximum only when that passes it by 2^8 (P keeps
+//                bf16's relative precision), and only then O is rescaled.  2^down is
+//                that 2^8 times the number of keys or more: no sum of P |v| passes the
+//                largest |v|.  (It costs no instruction; the exponent is then rounded
+//                to 2^-20, of the order of the native exponential's error.  Scaling
+//                the rounded P instead: 177 -> 181 us.)
 //   warp 8       producer: Q tiles through one ring, K and V tiles through another,
 //                ahead of the item at work.
 //   warp 9       issues the products: S = Q K^T, O += P V (P from tensor memory, V
@@ -43,7 +46,7 @@ constexpr int W_PROD = 8, W_MMA = 9, W_OUT = 12;
 constexpr int REG_SOFT = 192, REG_MISC = 64;   // 2 x 192 + 2 x 64 = 512, the launch's
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
-constexpr float TAU = 8.f;                     // log2 units
+constexpr int TAU = 8;                         // log2 units
 
 struct Params {
   CrossParams p;
@@ -63,7 +66,7 @@ struct Smem {
   static constexpr int TILE = (D / 64) * CH;
   static constexpr int QS = D == 128 ? 3 : 5, KS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0, OFF_KV = OFF_Q + QS * TILE;
-  static constexpr int OFF_SUM = OFF_KV + KS * TILE;         // float2 [2 tiles][128]: c m and l of the rows
+  static constexpr int OFF_SUM = OFF_KV + KS * TILE;         // float2 [2 tiles][128]: c m + down and l of the rows
   static constexpr int OFF_BAR = OFF_SUM + 2 * 1024;
   static constexpr int NBAR = 2 * QS + 2 * KS + 14 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
   uint64_t* p_full = s_full + 2;             // [X][half]: that half of P_X is there (the first: O_X rescaled)
   uint64_t* o_done = p_full + 4;             // [X]: the item's O_X is there
   uint64_t* o_free = o_done + 2;             // [X]: it has been read
-  uint64_t* l_full = o_free + 2;             // [X]: the item's c m and l are there
+  uint64_t* l_full = o_free + 2;             // [X]: the item's c m + down and l are there
   uint64_t* l_free = l_full + 2;             // [X]: they have been read
   uint64_t* mma_done = l_free + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           const float2 ml = sums[128 * x + r];
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_free[x]);
-          if (lse) *lse = (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+          if (lse) *lse = lse_of(ml.x, ml.y, p.keys_log2 + TAU);
           const float inv = 1.f / ml.y;
           if (!mbar_wait(&o_done[x], in[x] & 1, abort_flag, p.err)) { ok = false; break; }
           ++in[x];
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quad * 32) << 16);
     const uint32_t col_s = COL_S0 + 128 * x, col_o = COL_O0 + D * x;
-    const float c = p.c;
+    const float c = p.c, down = (float)(p.keys_log2 + TAU);
     int n = 0, items = 0;                    // key tiles and items of this warp's tile so far
     bool ok = true;
     Walk w;
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           const float was = mc;
           if (lift) {
             m = top > -INFINITY ? top : 0.f;
-            mc = m * c;
+            mc = fmaf(m, c, down);
           }
           if (j > 0 && __any_sync(0xffffffffu, lift)) {
             // (S of this tile came after P V of the one before: O is at rest)

@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
         qf[t][k][2 + half] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
       }
     }
+  // (m stands above the maximum by the number of keys: no sum of P |v| passes the largest |v|)
+  const float down = (float)p.keys_log2;
   float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
           now[half] = fmaxf(now[half], __shfl_xor_sync(0xffffffffu, now[half], x));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        now[half] = fmaxf(m[t][half], now[half] * p.c);
+        now[half] = fmaxf(m[t][half], fmaf(now[half], p.c, down));
         ref[half] = now[half] > -INFINITY ? now[half] : 0.f;
       }
       if (__any_sync(0xffffffffu, now[0] != m[t][0] || now[1] != m[t][1])) {
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *reinterpret_cast<uint32_t*>(at(p.o, b, h, n) + i) = pack2(v0 * inv, v1 * inv);
     if (i == 0 && p.lse)
-      p.lse[((long long)b * p.Hq + h) * p.Nq + n] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      p.lse[((long long)b * p.Hq + h) * p.Nq + n] = sum > 0.f ? lse_of(top, sum, p.keys_log2) : -INFINITY;
   };
   // of a cluster, each CTA takes an equal share of the outputs, and is given the others' parts of it: stores to
   // another CTA's memory are not waited for, loads are (16 CTAs: 24.6 -> 18 us where they read)

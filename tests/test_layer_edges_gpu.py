@@ -106,3 +106,19 @@ def test_positions_of_the_launch_before(fa, B, H, N, axes):
         for got in (eager, captured):
             for a, b in zip(want, got):
                 assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [3, 200])
+@pytest.mark.parametrize("Nk", [1, 100, 1000, 6000])
+def test_values_near_the_end(fa, d, Nq, Nk):
+    """Values up to the largest of bf16, whose sums before the division would pass FP32's, and very small ones."""
+    q, k, v, _ = make(1, 4, 2, Nq, Nk, d)
+    most = torch.finfo(torch.bfloat16).max
+    u = torch.rand(v.shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    q[:, :, 0] = 0                                     # a row of equal weights
+    for values in ((0.5 + 0.5 * u) * most, torch.full_like(u, most), v.float() / 8 * most):
+        values = values.to(torch.bfloat16)
+        values = torch.where(values.isinf(), torch.full_like(values, most), values)
+        check_fwd(fa, q, k, values)
+        check_fwd(fa, q, k, (values.float() * 2.0 ** -228).to(torch.bfloat16))
