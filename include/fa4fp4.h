@@ -521,8 +521,9 @@ FA4FP4_API fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const 
  * and sequences may be broadcast.
  * Products are exact, sums FP32; P is rounded to bf16 (half a step: 2^-9) for the
  * product with V, its sum is taken before that.  No sum of P V passes FP32's range
- * on its way to o, whatever the values and the number of keys.  Nq and Nk may be 0
- * (k and v are then not read; no query is an empty problem). */
+ * on its way to o, whatever the values and the number of keys.  Scores below
+ * FP32's range have no weight; a row without any other is one without a key.  Nq and
+ * Nk may be 0 (k and v are then not read; no query is an empty problem). */
 FA4FP4_API fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, const fa4fp4_heads* v,
                                            const int* kv_lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
                                            float softmax_scale, const fa4fp4_heads* o, float* lse, void* stream);

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_free[x]);
           if (lse) *lse = lse_of(ml.x, ml.y, p.keys_log2 + TAU);
-          const float inv = 1.f / ml.y;
+          const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;      // (no score within FP32's range)
           if (!mbar_wait(&o_done[x], in[x] & 1, abort_flag, p.err)) { ok = false; break; }
           ++in[x];
           tc_fence_after();
@@ -406,23 +406,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) cross_fwd_kernel(const __grid_con
     Item it;
     for (; ok && w.with_keys(a, it, false); w.next()) {
       if (x == 1 && !it.two) continue;
-      float m = 0.f, mc = 0.f, l = 0.f;
+      float m = -INFINITY, mc = 0.f, l = 0.f;
       for (int j = 0; j < it.nt; ++j, ++n) {
         if (!mbar_wait(&s_full[x], n & 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         const int keep = it.len - j * BN;
         float2 ls = make_float2(0.f, 0.f);
-        // the reference: the first tile's maximum, then only where a maximum passes it by far
+        // the reference: the first maximum (of tiles whose scores are all -inf there is none, and P is 0), then only
+        // where a maximum passes it by far
         auto refer = [&](float top) {
-          const bool lift = j == 0 || (top - m) * c > TAU;
-          const float was = mc;
+          const bool lift = (top - m) * c > TAU;
+          float f = 1.f;
           if (lift) {
-            m = top > -INFINITY ? top : 0.f;
+            const float was = mc;
+            const bool first = m == -INFINITY;
+            m = top;
             mc = fmaf(m, c, down);
+            if (!first) f = ex2_approx(was - mc);
           }
           if (j > 0 && __any_sync(0xffffffffu, lift)) {
             // (S of this tile came after P V of the one before: O is at rest)
-            const float f = lift ? ex2_approx(was - mc) : 1.f;
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
               uint32_t ov[16];

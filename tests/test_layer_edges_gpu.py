@@ -122,3 +122,42 @@ def test_values_near_the_end(fa, d, Nq, Nk):
         values = torch.where(values.isinf(), torch.full_like(values, most), values)
         check_fwd(fa, q, k, values)
         check_fwd(fa, q, k, (values.float() * 2.0 ** -228).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [3, 200, 700])
+@pytest.mark.parametrize("Nk,lost", [(300, 128), (1000, 900), (40, 32)])
+def test_scores_past_the_range(fa, d, Nq, Nk, lost):
+    """Scores that pass FP32's range below, in the first keys: those keys have no weight, the others all of it."""
+    q, k, v, dout = make(1, 2, 2, Nq, Nk, d)
+    q[..., 0] = 1e20
+    k[..., 0] = 0
+    k[:, :, :lost] = 0
+    k[:, :, :lost, 0] = -1e20
+    q[..., 1:] = 1.0
+    k[:, :, lost:, 1:] -= 30.0                         # scores of some hundred below zero
+    o, lse = fa.cross_fwd(q, k, v)
+    want, bound, wl, bl = ref.cross(q, k[:, :, lost:], v[:, :, lost:])
+    ref.assert_within(o, want, bound, "o")
+    ref.assert_within(lse, wl, bl, "lse")
+    dq, dk, dv = fa.cross_bwd(q, k, v, o, dout, lse)
+    assert (dk[:, :, :lost] == 0).all() and (dv[:, :, :lost] == 0).all()
+    assert torch.isfinite(dq).all() and torch.isfinite(dk).all() and torch.isfinite(dv).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [3, 200, 700])
+@pytest.mark.parametrize("Nk", [20, 300])
+def test_no_score_within_the_range(fa, d, Nq, Nk):
+    """All scores of a row past FP32's range below: as a row without a key."""
+    q, k, v, dout = make(1, 2, 2, Nq, Nk, d)
+    q[:, :, 1] = 0
+    q[:, :, 1, 0] = 1e20
+    k[..., 0] = -1e20
+    q[:, :, [0, 2], 0] = 0
+    o, lse = fa.cross_fwd(q, k, v)
+    assert (lse[:, :, 1] == -INF).all() and (o[:, :, 1] == 0).all()
+    want, bound, wl, bl = ref.cross(q[:, :, [0, 2]], k, v)
+    ref.assert_within(o[:, :, [0, 2]], want, bound, "o")
+    dq = fa.cross_bwd(q, k, v, o, dout, lse)[0]
+    assert (dq[:, :, 1] == 0).all()
