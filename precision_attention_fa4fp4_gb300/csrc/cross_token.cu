@@ -82,7 +82,7 @@ struct Smem {
   static constexpr int CHUNK = KEYS<D> * 128;              // [keys][64 channels], 128-byte swizzle
   static constexpr int TILE = (D / 64) * CHUNK;            // 4 KB
   static constexpr int STAGE = 2 * TILE, STAGES = STAGES_OF<D, MT>;
-  static constexpr int RING = WARPS * STAGES * STAGE;      // 24 KB a warp
+  static constexpr int RING = WARPS * STAGES * STAGE;      // 24 KB a warp (16 with two stages)
   // after the loop the rings' place holds the warps' O, m and l
   static constexpr int ROWS = 16 * MT;
   static constexpr int WARP_F = ROWS * (D + 2);            // floats of one warp: O [ROWS][D], m, l
@@ -309,10 +309,11 @@ __global__ void __launch_bounds__(WARPS * 32) cross_token_kernel(const __grid_co
     int g, n;
     divide(r0 + r, a.nq, g, n);
     const int h = hk * G + g;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const bool none = sum == 0.f;        // (a sum that is NaN is no row without a key)
+    const float inv = none ? 0.f : 1.f / sum;
     *reinterpret_cast<uint32_t*>(at(p.o, b, h, n) + i) = pack2(v0 * inv, v1 * inv);
     if (i == 0 && p.lse)
-      p.lse[((long long)b * p.Hq + h) * p.Nq + n] = sum > 0.f ? lse_of(top, sum, p.keys_log2) : -INFINITY;
+      p.lse[((long long)b * p.Hq + h) * p.Nq + n] = none ? -INFINITY : lse_of(top, sum, p.keys_log2);
   };
   // of a cluster, each CTA takes an equal share of the outputs, and is given the others' parts of it: stores to
   // another CTA's memory are not waited for, loads are (16 CTAs: 24.6 -> 18 us where they read)

@@ -161,3 +161,20 @@ def test_no_score_within_the_range(fa, d, Nq, Nk):
     ref.assert_within(o[:, :, [0, 2]], want, bound, "o")
     dq = fa.cross_bwd(q, k, v, o, dout, lse)[0]
     assert (dq[:, :, 1] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nk", [(2, 20), (2, 5000), (40, 60), (300, 500)])
+def test_rows_that_are_not_finite(fa, d, Nq, Nk):
+    """A query that is not finite has neither o nor lse, and is no row without a key; the others are as they were."""
+    q, k, v, _ = make(2, 4, 2, Nq, Nk, d)
+    lens = torch.tensor([Nk, 0], device="cuda", dtype=torch.int32)
+    o, lse = fa.cross_fwd(q, k, v, lens)
+    q[:, 1, 0] = float("nan")
+    q[:, 2, 1, 3] = INF
+    o2, lse2 = fa.cross_fwd(q, k, v, lens)
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[0, 1, 0] = bad[0, 2, 1] = True
+    assert lse2[bad].isnan().all() and o2[bad].isnan().all()
+    assert torch.equal(lse2[~bad], lse[~bad]) and torch.equal(o2[~bad], o[~bad])
+    assert (lse2[1] == -INF).all() and (o2[1] == 0).all()
