@@ -537,8 +537,8 @@ FA4FP4_API fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_h
  * that depends on the shapes and the GPU's number of multiprocessors alone.
  * `workspace`: at least fa4bf16_cross_bwd_workspace_bytes(...) bytes of device
  * memory (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs; it
- * needs no initialisation.  Nq == 0 gives zeros for dk and dv, Nk == 0 zeros for
- * dq. */
+ * needs no initialisation.  Nq == 0 or Hq == 0 gives zeros for dk and dv, Nk == 0
+ * zeros for dq. */
 FA4FP4_API size_t fa4bf16_cross_bwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 FA4FP4_API fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, const fa4fp4_heads* v,
                                            const fa4fp4_heads* o, const fa4fp4_heads* dout, const float* lse,

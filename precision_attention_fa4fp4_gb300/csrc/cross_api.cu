@@ -244,7 +244,8 @@ fa4fp4_status fa4bf16_cross_bwd(const fa4fp4_heads* q, const fa4fp4_heads* k, co
                                 const fa4fp4_heads* dv, void* workspace, size_t workspace_bytes, void* stream) {
   fa4fp4_status s = check_cross(B, Hq, Hkv, Nq, Nk, d);
   if (s != FA4FP4_OK) return s;
-  if (B == 0 || Hq == 0 || (Nq == 0 && Nk == 0)) return FA4FP4_OK;
+  if (Hq == 0) Nq = 0;                   // no queries: zeros for dk and dv
+  if (B == 0 || (Nq == 0 && (Nk == 0 || Hkv == 0))) return FA4FP4_OK;
   CrossParams p;
   memset(&p, 0, sizeof(p));
   if (Nq > 0) {

@@ -1,11 +1,12 @@
 """What holds of the norm and rotation and of cross attention without a GPU."""
+import ctypes
 import os
 import re
 import subprocess
 
 import pytest
 
-from precision_attention_fa4fp4_gb300 import build
+from precision_attention_fa4fp4_gb300 import api, build
 
 
 @pytest.mark.parametrize("name", sorted(f for f in os.listdir(build.CSRC) if f.endswith((".cu", ".cuh"))))
@@ -57,3 +58,13 @@ def test_tasks_of_the_largest_calls(tmp_path):
     assert run.returncode == 0, run.stdout
     with open(os.path.join(build.CSRC, "rope.cu")) as f:
         assert f.read().count("Tasks task{") == 2          # both kernels count so
+
+
+def test_no_query_heads_is_checked():
+    """Without a query head dk and dv are still outputs: they are checked (here they are missing)."""
+    build.build()
+    lib = api.load_library()
+    call = lambda Hkv, Nk: lib.fa4bf16_cross_bwd(  # noqa: E731
+        None, None, None, None, None, None, None, 1, 0, Hkv, 4, Nk, 64, ctypes.c_float(0.0), None, None, None, None,
+        ctypes.c_size_t(0), None)
+    assert call(2, 8) == 1 and call(0, 8) == 0 and call(2, 0) == 0

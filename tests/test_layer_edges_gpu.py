@@ -178,3 +178,14 @@ def test_rows_that_are_not_finite(fa, d, Nq, Nk):
     assert lse2[bad].isnan().all() and o2[bad].isnan().all()
     assert torch.equal(lse2[~bad], lse[~bad]) and torch.equal(o2[~bad], o[~bad])
     assert (lse2[1] == -INF).all() and (o2[1] == 0).all()
+
+
+def test_no_query_heads(fa):
+    """Keys that no head attends to have gradients of zeros."""
+    q = torch.zeros((2, 0, 5, 64), device="cuda", dtype=torch.bfloat16)
+    k = torch.ones((2, 3, 9, 64), device="cuda", dtype=torch.bfloat16)
+    o, lse = fa.cross_fwd(q, k, k)
+    outs = [torch.full_like(k, 7.0) for _ in range(2)]
+    dq, dk, dv = fa.cross_bwd(q, k, k, o, q, lse, dk=outs[0], dv=outs[1])
+    assert o.shape == dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+    fa.sync_status()
