@@ -458,8 +458,9 @@ typedef struct {
  * [B][axes][N], or [axes][N] for all sequences when shared, 4-byte aligned, of any
  * sign.  sections and freqs (64-bit, d / 2 of them, finite) are HOST arrays, read
  * during the call only.  Angles are reduced to a turn in 64-bit integers, so they
- * are as exact at far positions as at near ones: for |freqs[i]| <= 2 pi they are
- * off by |position| 2^-52 and 2^-30 at most. */
+ * are as exact at far positions as at near ones: for |freqs[i]| up to 2^40 an angle
+ * in [-pi, pi] is off by 2^-21 at most (its roundings to FP32), and its sine and
+ * cosine by another 2^-21 (the native functions). */
 typedef struct {
   const int* positions;
   int shared;

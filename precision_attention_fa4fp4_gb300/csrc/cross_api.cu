@@ -71,6 +71,16 @@ fa4fp4_status check_rotation(const fa4fp4_rotation* r, int d) {
   return aligned(r->positions, 4) ? FA4FP4_OK : FA4FP4_ERR_ALIGNMENT;
 }
 
+// f / (2 pi) modulo 1, times 2^64.  One product of 53 bits would be off by 2^-54 of itself, times the position: so the
+// product with 1 / (2 pi) in two parts, and what its own rounding leaves.
+uint64_t turn_of(double f) {
+  constexpr double HI = 0x1.45f306dc9c883p-3, LO = -0x1.6b01ec5417056p-57;   // 1 / (2 pi) to 2^-110
+  // (this product too by fma: a compiler may make a plain one and the subtraction below one fma, which rounds elsewhere)
+  const double hi = std::fma(f, HI, 0.0), lo = std::fma(f, LO, std::fma(f, HI, -hi));
+  const auto turn = [](double x) { return (uint64_t)(int64_t)((x - std::rint(x)) * 9223372036854775808.0) * 2; };
+  return turn(hi) + turn(lo);
+}
+
 void set_rotation(RopeParams* p, const fa4fp4_norm* norm, const fa4fp4_rotation* r) {
   if (norm) {
     p->norm = 1;
@@ -86,9 +96,7 @@ void set_rotation(RopeParams* p, const fa4fp4_norm* norm, const fa4fp4_rotation*
   for (int a = 0, i = 0; a < r->axes; ++a)
     for (int j = 0; j < r->sections[a]; ++j, ++i) {
       p->axis[i] = (uint8_t)a;
-      const double turns = r->freqs[i] * 0.15915494309189535;             // 1 / (2 pi)
-      const double rest = turns - std::floor(turns);                      // in [0, 1]
-      p->turn[i] = rest >= 1.0 ? 0 : (uint64_t)(rest * 18446744073709551616.0);
+      p->turn[i] = turn_of(r->freqs[i]);
     }
 }
 

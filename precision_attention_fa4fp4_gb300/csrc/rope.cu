@@ -17,9 +17,10 @@
 // cosines are taken once and serve every head of the token.
 //
 // Angles: f_i / 2 pi is held as a fraction of a turn in 64 bits; position times
-// it modulo 2^64 is the exact remainder, whose upper 32 bits give th in [-pi,
-// pi) within 2^-30, at position 10^6 as at 1 (an FP32 product is off by 0.03
-// there).  The native sine and cosine are off by 2^-21 there, against bf16's 2^-9.
+// it modulo 2^64 is the remainder, whose upper 32 bits give th in [-pi, pi] within
+// 2^-21 (two roundings to FP32 and a constant's, 3.0e-7), at position 2^31 as at 1
+// (an FP32 product is off by 0.03 at 10^6).  The native sine and cosine are off by
+// 2^-21 there, against bf16's 2^-8.
 #include <cuda_bf16.h>
 #include "common.cuh"
 #include "divide.cuh"

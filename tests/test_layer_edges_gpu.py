@@ -1,4 +1,6 @@
 """Norm and rotation, and cross attention, at the ends of what their calls allow."""
+import math
+
 import pytest
 import torch
 
@@ -189,3 +191,48 @@ def test_no_query_heads(fa):
     dq, dk, dv = fa.cross_bwd(q, k, k, o, q, lse, dk=outs[0], dv=outs[1])
     assert o.shape == dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
     fa.sync_status()
+
+
+def turn_exactly(freq):
+    """The angle of a position, position * freq modulo 2 pi, in whole numbers."""
+    two_pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239)) * 2      # times 2^BITS (Machin)
+    num, den = freq.as_integer_ratio()
+    return lambda p: ((p * num << BITS) // den % two_pi) / (1 << BITS)
+
+
+BITS = 200
+
+
+def arctan_inverse(n):
+    total = term = (1 << BITS) // n
+    i, sign = 3, -1
+    while term:
+        term //= n * n
+        total += sign * (term // i)
+        i, sign = i + 2, -sign
+    return total
+
+
+def test_exact_turns():
+    assert abs(turn_exactly(1.0)(7) - math.fmod(7.0, 2 * math.pi)) < 1e-15
+    assert abs(turn_exactly(0.5)(-1) - (2 * math.pi - 0.5)) < 1e-15
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_far_positions_of_high_frequencies(fa, interleaved):
+    """Angles do not worsen with the position.  A sine or cosine is off by 3.0e-7 for its angle's roundings to FP32 and by
+    2^-21.2 for the native function, the sum of two products by another 1.2e-7 of their sizes: below 2^-20 of them."""
+    d, N, H = 64, 512, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((1, H, N, d), generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(2 ** 31 - 2 ** 20, 2 ** 31, (1, 1, N), generator=g, device="cuda").int()
+    pos[:, :, ::2] *= -1
+    freqs = torch.linspace(-2 * math.pi, 2 * math.pi, d // 2 + 1, dtype=torch.float64)[1:] * 0.999
+    freqs[0], freqs[1] = 1e-9, 1e6 + 0.37
+    places = pos[0, 0].tolist()
+    th = torch.stack([torch.tensor([t(p) for p in places], dtype=torch.float64)
+                      for t in (turn_exactly(float(f)) for f in freqs)], -1)[None, None].cuda()
+    y, _ = fa.qk_norm_rope(x, None, pos, freqs, norm=False, interleaved=interleaved)
+    want = ref.turn(x.double(), th, interleaved)
+    a, b = ref.split(x.double().abs(), interleaved)
+    ref.assert_within(y, want, ref.U * want.abs() + 2.0 ** -20 * ref.join(a + b, a + b, interleaved), "q")
