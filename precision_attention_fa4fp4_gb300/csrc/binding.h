@@ -5,7 +5,9 @@
 #include <structmember.h>
 
 #include <ATen/ATen.h>
+#include <ATen/Context.h>
 #include <ATen/EmptyTensor.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -109,10 +111,21 @@ int* ints(PyObject* x, const char* name, int index, at::IntArrayRef shape) {
   return given(x) ? static_cast<int*>(expect(x, name, index, at::kInt, shape).data_ptr()) : nullptr;
 }
 
-// A tensor of the caching allocator, made without the dispatcher: about 1 us instead of
-// at::empty's 1.8, where a call makes up to five.
+// Does anything look at the tensors that torch makes: a dispatch or function mode, a transform, or the filling of
+// uninitialised memory?
+bool watched() {
+  const c10::DispatchKeySet keys = c10::impl::tls_local_dispatch_key_set().included_;
+  const at::Context& torch = at::globalContext();
+  return !(keys - c10::default_included_set).empty() ||
+         (torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory());
+}
+
+// A tensor of the caching allocator, made without the dispatcher where nothing there would see it: about 1 us
+// instead of at::empty's 1.8, where a call makes up to five.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index, bool zero = false) {
-  if (zero) return at::zeros(shape, at::TensorOptions().dtype(type).device(at::kCUDA, index));
+  const at::TensorOptions how = at::TensorOptions().dtype(type).device(at::kCUDA, index);
+  if (zero) return at::zeros(shape, how);
+  if (watched()) return at::empty(shape, how);
   const int now = c10::cuda::current_device();
   if (now != index) c10::cuda::set_device((c10::DeviceIndex)index);
   struct Back {

@@ -236,3 +236,50 @@ def test_far_positions_of_high_frequencies(fa, interleaved):
     want = ref.turn(x.double(), th, interleaved)
     a, b = ref.split(x.double().abs(), interleaved)
     ref.assert_within(y, want, ref.U * want.abs() + 2.0 ** -20 * ref.join(a + b, a + b, interleaved), "q")
+
+
+class Watch(torch.utils._python_dispatch.TorchDispatchMode):
+    def __init__(self):
+        super().__init__()
+        self.shapes = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if func is torch.ops.aten.empty.memory_format:
+            self.shapes.append(tuple(out.shape))
+        return out
+
+
+def test_outputs_are_seen_by_torch(fa):
+    """The tensors that a call makes go through torch's dispatcher where something there looks at them: a dispatch mode, or
+    the filling of uninitialised memory."""
+    q, k, v, dout = make(1, 2, 2, 4, 8, 64)
+    cache = fa.cache_alloc(1, 2, 64, page=16)
+    table = torch.zeros((1, 1), device="cuda", dtype=torch.int32)
+    lens = torch.zeros(1, device="cuda", dtype=torch.int32)
+    fa.cache_append(cache, k, v, table, lens)
+    lens += 8
+
+    def calls():
+        o, lse = fa.cross_fwd(q, k, v)
+        return (o, lse, *fa.cross_bwd(q, k, v, o, dout, lse), *fa.qk_norm_rope(q, dout),
+                *fa.cache_fwd(q, cache, table, lens))
+
+    want = calls()
+    with Watch() as seen:
+        got = calls()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for x in want:
+        assert tuple(x.shape) in seen.shapes
+    assert sum(s == tuple(q.shape) for s in seen.shapes) >= 4
+    was = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        assert torch.utils.deterministic.fill_uninitialized_memory
+        with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
+            got = calls()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    finally:
+        torch.use_deterministic_algorithms(was)
+    fills = sum(e.count for e in prof.key_averages() if e.key == "aten::fill_")
+    assert fills >= len(want)
