@@ -472,7 +472,8 @@ typedef struct {
 
 /* The norm of every row of d channels: n = x w / sqrt(mean(x^2) + eps), w the
  * weight of its tensor ([d], f32 or bf16 by weight_dtype (fa4fp4_out_dtype), device
- * memory, 16-byte aligned; NULL: ones).  eps >= 0. */
+ * memory, 16-byte aligned; NULL: ones).  eps >= 0.  Rows of any size: squares that
+ * would pass FP32's range at either end are formed in other units. */
 typedef struct {
   const void* q_weight;
   const void* k_weight;

@@ -80,6 +80,9 @@ FA4_DEV void unpack(const float4 (&f)[4], float2 (&a)[4], float2 (&b)[4]) {
   }
 }
 
+// Rows that are not there: their norm is no special case.
+FA4_DEV uint4 ones() { return make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u); }
+
 FA4_DEV float2 both(float x) { return make_float2(x, x); }
 FA4_DEV float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
@@ -114,6 +117,27 @@ FA4_DEV float row_sum(float v) {
   for (int o = LANES / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+
+// Rows whose squares come near an end of FP32's range (values from 2^50 on, or, with an eps that is smaller still,
+// below 2^-50) are seldom: they are formed anew in units of 2^100 or 2^-100, and normalized before they go on.
+FA4_DEV bool far(float ms) { return !(ms > 0x1p-100f && ms < 0x1p100f); }
+struct Unit {
+  float unit;
+  FA4_DEV explicit Unit(float ms) : unit(ms < 1.f ? 0x1p100f : 0x1p-100f) {}
+  FA4_DEV float squares(const float2 (&a)[4], const float2 (&b)[4]) const {
+    float2 q = both(0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = fmul2(a[j], both(unit)), y = fmul2(b[j], both(unit));
+      q = ffma2(y, y, ffma2(x, x, q));
+    }
+    return q.x + q.y;
+  }
+  // 1 / sqrt(mean(x^2) + eps) over the unit
+  FA4_DEV float root(float sum, float per, float eps) const { return rsqrtf(fmaf(sum, per, eps * unit * unit)); }
+  // x r (the root first: a channel far smaller than its row keeps its bits)
+  FA4_DEV float2 apply(float2 x, float root) const { return fmul2(fmul2(x, both(root)), both(unit)); }
+};
 
 // What a CTA needs of the rotation and the weights, in shared memory.
 template <int D>
@@ -172,7 +196,7 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
       uint4 u[U], v[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        u[i] = v[i] = make_uint4(0, 0, 0, 0);
+        u[i] = v[i] = ones();
         if (h + i * ROWS < h1) {
           const __nv_bfloat16* row = x + (h + i * ROWS) * T.x.h;
           u[i] = *reinterpret_cast<const uint4*>(row + c0);
@@ -194,7 +218,20 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
           q = ffma2(fb[0], fb[0], q);
 #pragma unroll
           for (int j = 1; j < 4; ++j) q = ffma2(fb[j], fb[j], ffma2(fa[j], fa[j], q));
-          r = rsqrtf(row_sum<LANES>(q.x + q.y) * (1.f / D) + p.eps);
+          const float ms = row_sum<LANES>(q.x + q.y) * (1.f / D) + p.eps;
+          r = rsqrtf(ms);
+          if (__builtin_expect(__any_sync(0xffffffffu, far(ms)), 0)) {
+            const Unit by(ms);
+            const float root = by.root(row_sum<LANES>(by.squares(fa, fb)), 1.f / D, p.eps);
+            if (far(ms)) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                fa[j] = by.apply(fa[j], root);
+                fb[j] = by.apply(fb[j], root);
+              }
+              r = 1.f;
+            }
+          }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -220,6 +257,8 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
 // weights, sines and cosines and two rows take 128 registers (at 85, for 3 CTAs, they
 // spill: 132 -> 210 us for 2 x 8192 tokens of 32 + 8 heads with f32 gradients; rows
 // ahead by asynchronous copies to shared memory 157).
+// Far rows are left to a second pass over the tasks of a warp that met any: formed where they are met, they took 126
+// -> 138 us of calls without any, in registers.
 constexpr int BWD_CTAS = 2;
 template <int D, bool PAIRS, bool F32>
 __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
@@ -228,11 +267,14 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
   constexpr int LANES = D / 16, ROWS = 32 / LANES;
   __shared__ Tables<D> tab;
   __shared__ float join[WARPS][D];
+  __shared__ int again[WARPS];                 // has the warp met rows that are far?
   next_may_start();
   wait_for_previous();
   tab.load(p);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % LANES, sub = lane / LANES;
   const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
+  if (lane == 0) again[warp] = 0;
+  __syncwarp();
   const int t = (int)blockIdx.x >= p.ctas[0];
   const int cta = t ? (int)blockIdx.x - p.ctas[0] : (int)blockIdx.x;
   const RopeTensor& T = p.t[t];
@@ -240,81 +282,115 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
   tab.template weights<PAIRS>(t, c0, c1, wa, wb);
 #pragma unroll
   for (int j = 0; j < 4; ++j) da[j] = db[j] = both(0.f);
-  for (Tasks task{(uint32_t)(cta * WARPS + warp), (uint32_t)(p.ctas[t] * WARPS), (uint32_t)by_tokens.d * (t ? nk : nq)};
-       task.more(); task.next()) {
-    int part, m, b, n;
-    divide((int)task.now, by_tokens, part, m);
-    divide(m, by_n, b, n);
-    const int h0 = part * chunk, h1 = min(T.H, h0 + chunk);
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;
-    const long long dy = b * T.dy.b + n * T.dy.n;
-    __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(T.out.p) + b * T.out.b + n * T.out.n;
-    float2 c[4], s[4];
-    uint4 u, v;
-    float4 g[F32 ? 4 : 2];
-    auto fetch = [&](int h) {
-      u = v = make_uint4(0, 0, 0, 0);
+  const auto pass = [&](auto only_far) {
+    constexpr bool FAR = decltype(only_far)::value;
+    for (Tasks task{(uint32_t)(cta * WARPS + warp), (uint32_t)(p.ctas[t] * WARPS), (uint32_t)by_tokens.d * (t ? nk : nq)};
+         task.more(); task.next()) {
+      int part, m, b, n;
+      divide((int)task.now, by_tokens, part, m);
+      divide(m, by_n, b, n);
+      const int h0 = part * chunk, h1 = min(T.H, h0 + chunk);
+      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;
+      const long long dy = b * T.dy.b + n * T.dy.n;
+      __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(T.out.p) + b * T.out.b + n * T.out.n;
+      float2 c[4], s[4];
+      uint4 u, v;
+      float4 g[F32 ? 4 : 2];
+      auto fetch = [&](int h) {
+        u = v = ones();
 #pragma unroll
-      for (int i = 0; i < (F32 ? 4 : 2); ++i) g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h >= h1) return;
-      const __nv_bfloat16* row = x + h * T.x.h;
-      u = *reinterpret_cast<const uint4*>(row + c0);
-      v = *reinterpret_cast<const uint4*>(row + c1);
-      if (F32) {
-        const float* from = static_cast<const float*>(T.dy.p) + dy + h * T.dy.h;
-        g[0] = *reinterpret_cast<const float4*>(from + c0);
-        g[1] = *reinterpret_cast<const float4*>(from + c0 + 4);
-        g[F32 ? 2 : 0] = *reinterpret_cast<const float4*>(from + c1);
-        g[F32 ? 3 : 0] = *reinterpret_cast<const float4*>(from + c1 + 4);
-      } else {
-        const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(T.dy.p) + dy + h * T.dy.h;
-        g[0] = *reinterpret_cast<const float4*>(from + c0);
-        g[1] = *reinterpret_cast<const float4*>(from + c1);
-      }
-    };
-    fetch(h0 + sub);
-    angles(p, tab.turn, tab.axis, b, n, l, c, s);
-    for (int h = h0 + sub; h - sub < h1; h += ROWS) {
-      const bool on = h < h1;
-      float2 ga[4], gb[4], fa[4], fb[4];
-      unpack<PAIRS>(u, v, fa, fb);
-      if constexpr (F32) unpack<PAIRS>(g, ga, gb);
-      else unpack<PAIRS>(*reinterpret_cast<const uint4*>(&g[0]), *reinterpret_cast<const uint4*>(&g[1]), ga, gb);
-      fetch(h + ROWS);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 e = ga[j];
-        ga[j] = ffma2(gb[j], s[j], fmul2(e, c[j]));
-        gb[j] = ffma2(neg(e), s[j], fmul2(gb[j], c[j]));
-      }
-      if (p.norm) {
-        float2 xx = both(0.f), ux = both(0.f);
+        for (int i = 0; i < (F32 ? 4 : 2); ++i) g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h >= h1) return;
+        const __nv_bfloat16* row = x + h * T.x.h;
+        u = *reinterpret_cast<const uint4*>(row + c0);
+        v = *reinterpret_cast<const uint4*>(row + c1);
+        if (F32) {
+          const float* from = static_cast<const float*>(T.dy.p) + dy + h * T.dy.h;
+          g[0] = *reinterpret_cast<const float4*>(from + c0);
+          g[1] = *reinterpret_cast<const float4*>(from + c0 + 4);
+          g[F32 ? 2 : 0] = *reinterpret_cast<const float4*>(from + c1);
+          g[F32 ? 3 : 0] = *reinterpret_cast<const float4*>(from + c1 + 4);
+        } else {
+          const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(T.dy.p) + dy + h * T.dy.h;
+          g[0] = *reinterpret_cast<const float4*>(from + c0);
+          g[1] = *reinterpret_cast<const float4*>(from + c1);
+        }
+      };
+      fetch(h0 + sub);
+      angles(p, tab.turn, tab.axis, b, n, l, c, s);
+      for (int h = h0 + sub; h - sub < h1; h += ROWS) {
+        bool on = h < h1;
+        float2 ga[4], gb[4], fa[4], fb[4];
+        unpack<PAIRS>(u, v, fa, fb);
+        if constexpr (F32) unpack<PAIRS>(g, ga, gb);
+        else unpack<PAIRS>(*reinterpret_cast<const uint4*>(&g[0]), *reinterpret_cast<const uint4*>(&g[1]), ga, gb);
+        fetch(h + ROWS);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          xx = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], xx));
-          ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
+          const float2 e = ga[j];
+          ga[j] = ffma2(gb[j], s[j], fmul2(e, c[j]));
+          gb[j] = ffma2(neg(e), s[j], fmul2(gb[j], c[j]));
         }
-        const float sx = row_sum<LANES>(xx.x + xx.y), su = row_sum<LANES>(ux.x + ux.y);
-        // rows that are not there add nothing (with eps = 0 their r is infinite)
-        const float r = on ? rsqrtf(sx * (1.f / D) + p.eps) : 0.f;
-        const float k = r * r * su * (1.f / D);
+        if (p.norm) {
+          float2 xx = both(0.f), ux = both(0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          da[j] = ffma2(ga[j], fmul2(fa[j], both(r)), da[j]);
-          db[j] = ffma2(gb[j], fmul2(fb[j], both(r)), db[j]);
-          ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
-          gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
+          for (int j = 0; j < 4; ++j) {
+            xx = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], xx));
+            ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
+          }
+          const float sx = row_sum<LANES>(xx.x + xx.y), su = row_sum<LANES>(ux.x + ux.y);
+          // the rows of the other pass add nothing (nor do those that are not there: their gradient is 0)
+          const float ms = sx * (1.f / D) + p.eps;
+          const bool here = far(ms) == FAR;
+          if (!here) {
+            if (!FAR) again[warp] = 1;
+            on = false;
+          }
+          if constexpr (FAR) {
+            const Unit by(ms);
+            const float root = by.root(row_sum<LANES>(by.squares(fa, fb)), 1.f / D, p.eps);
+            ux = both(0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              fa[j] = by.apply(fa[j], root);
+              fb[j] = by.apply(fb[j], root);
+              ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
+            }
+            const float r = root * by.unit, k = row_sum<LANES>(ux.x + ux.y) * (1.f / D);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (on) {
+                da[j] = ffma2(ga[j], fa[j], da[j]);
+                db[j] = ffma2(gb[j], fb[j], db[j]);
+              }
+              ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
+              gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
+            }
+          } else {
+            const float r = here ? rsqrtf(ms) : 0.f;
+            const float k = r * r * su * (1.f / D);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              da[j] = ffma2(ga[j], fmul2(fa[j], both(r)), da[j]);
+              db[j] = ffma2(gb[j], fmul2(fb[j], both(r)), db[j]);
+              ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
+              gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
+            }
+          }
         }
-      }
-      if (on) {
-        uint4 yu, yv;
-        pack<PAIRS>(ga, gb, yu, yv);
-        __nv_bfloat16* row = dx + h * T.out.h;
-        *reinterpret_cast<uint4*>(row + c0) = yu;
-        *reinterpret_cast<uint4*>(row + c1) = yv;
+        if (on) {
+          uint4 yu, yv;
+          pack<PAIRS>(ga, gb, yu, yv);
+          __nv_bfloat16* row = dx + h * T.out.h;
+          *reinterpret_cast<uint4*>(row + c0) = yu;
+          *reinterpret_cast<uint4*>(row + c1) = yv;
+        }
       }
     }
-  }
+  };
+  pass(std::false_type());
+  __syncwarp();
+  if (again[warp]) pass(std::true_type());
   if (!T.dw) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

@@ -283,3 +283,31 @@ def test_outputs_are_seen_by_torch(fa):
         torch.use_deterministic_algorithms(was)
     fills = sum(e.count for e in prof.key_averages() if e.key == "aten::fill_")
     assert fills >= len(want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_of_every_size(fa, d, interleaved, eps):
+    """Rows whose squares pass FP32's range at either end, beside others, and rows of large and small channels."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    B, H, N = 2, 5, 9
+    new = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    sizes = torch.tensor([0, 126, 100, 64, 60, 51, 40, -40, -60, -75, -100, -120], device="cuda").float()
+    if eps:
+        sizes = sizes.clamp(min=0)
+    rows = 2.0 ** sizes[torch.randint(0, 12, (B, H, N, 1), generator=g, device="cuda")]
+    x = (new(B, H, N, d).clamp(-1.9, 1.9) * rows).to(torch.bfloat16)
+    x[0, 0, :, : d // 4] *= 2.0 ** -30
+    w = 1 + 0.2 * new(d)
+    pos = torch.randint(0, 5000, (B, 1, N), generator=g, device="cuda").int()
+    freqs = fa.rope_freqs(d)
+    th = ref.turns(pos, freqs, [d // 2])
+    y, _ = fa.qk_norm_rope(x, None, pos, freqs, w, interleaved=interleaved, eps=eps)
+    ref.assert_within(y, *ref.norm_rope(x, w, th, interleaved, True, eps), "y")
+    dy = new(B, H, N, d)
+    for dt in (torch.float32, torch.bfloat16):
+        dx, _, dw, _ = fa.qk_norm_rope_bwd(dy.to(dt), None, x, None, pos, freqs, w, interleaved=interleaved, eps=eps)
+        want, bound, want_w, bound_w = ref.norm_rope_bwd(dy.to(dt), x, w, th, interleaved, True, eps)
+        ref.assert_within(dx, want, bound, "dx")
+        ref.assert_within(dw, want_w, bound_w, "dw")
