@@ -26,7 +26,9 @@
  *     (key n is visible to query i iff n <= i).
  *   - An empty problem (B == 0, or H == 0 / Hq == 0) is a no-op: the call
  *     checks its shape and options, then returns FA4FP4_OK without inspecting
- *     its pointers (they may be NULL) and without launching anything.
+ *     its pointers (they may be NULL) and without launching anything.  (Sums
+ *     over an empty problem that are outputs, fa4fp4_norm_rope_bwd's weight
+ *     gradients and fa4bf16_cross_bwd's dk and dv, are written: zeros.)
  *   - softmax_scale <= 0 selects 1/sqrt(d).
  *   - No C++ exception crosses this boundary; there is no CPU fallback.
  *
@@ -521,11 +523,14 @@ FA4FP4_API fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const 
  * o: bf16; lse: f32 [B][Hq][Nq], dense.  Without a key o = 0 and lse = -inf.  The
  * rows of q, k and v do not overlap (stride_n >= d; FA4FP4_ERR_UNSUPPORTED); heads
  * and sequences may be broadcast.
- * Products are exact, sums FP32; P is rounded to bf16 (half a step: 2^-9) for the
+ * Products are exact, sums FP32; P is rounded to bf16 (half a step: 2^-8) for the
  * product with V, its sum is taken before that.  No sum of P V passes FP32's range
- * on its way to o, whatever the values and the number of keys.  Scores below
- * FP32's range have no weight; a row without any other is one without a key.  Nq and
- * Nk may be 0 (k and v are then not read; no query is an empty problem). */
+ * on its way to o, whatever the values and the number of keys; weights below 2^-117
+ * Nk of a row's largest may count as 0.  Scores below FP32's range have no weight; a
+ * row without any other is one without a key.  Scores that are NaN, or above FP32's
+ * range, give NaN for the row's o and lse.  A row's largest score is good up to 2^30
+ * in magnitude: FP32's steps are 64 there.  Nq and Nk may be 0 (k and v are then
+ * not read; no query is an empty problem). */
 FA4FP4_API fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_heads* k, const fa4fp4_heads* v,
                                            const int* kv_lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
                                            float softmax_scale, const fa4fp4_heads* o, float* lse, void* stream);
@@ -536,7 +541,10 @@ FA4FP4_API fa4fp4_status fa4bf16_cross_fwd(const fa4fp4_heads* q, const fa4fp4_h
  * dV and dK summed over the query heads of their kv head.  dq, dk, dv: bf16, fully
  * written (zeros for keys behind kv_lens and for queries without a key).  P and dS
  * are rounded to bf16 for the products, the sums are FP32 and are added in an order
- * that depends on the shapes and the GPU's number of multiprocessors alone.
+ * that depends on the shapes and the GPU's number of multiprocessors alone.  lse is
+ * FP32, and P is off by about 2^-22 |lse| of itself for it: rows of |lse| above 2^20
+ * have no use for gradients, and may make them infinite or NaN above 2^28.  The rows
+ * of o and dout do not overlap either; their heads and sequences may be broadcast.
  * `workspace`: at least fa4bf16_cross_bwd_workspace_bytes(...) bytes of device
  * memory (FA4FP4_ERR_WORKSPACE otherwise), for this call alone while it runs; it
  * needs no initialisation.  Nq == 0 or Hq == 0 gives zeros for dk and dv, Nk == 0

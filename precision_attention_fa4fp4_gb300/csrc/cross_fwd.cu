@@ -13,9 +13,10 @@
 //                follows the running maximum only when that passes it by 2^8 (P keeps
 //                bf16's relative precision), and only then O is rescaled.  2^down is
 //                that 2^8 times the number of keys or more: no sum of P |v| passes the
-//                largest |v|.  (It costs no instruction; the exponent is then rounded
-//                to 2^-20, of the order of the native exponential's error.  Scaling
-//                the rounded P instead: 177 -> 181 us.)
+//                largest |v|, and weights below 2^(down - 126) of the largest are lost.
+//                (It costs no instruction; the exponent is rounded to 2^-20, of the
+//                order of the native exponential's error.  Scaling the rounded P
+//                instead: 177 -> 181 us.)
 //   warp 8       producer: Q tiles through one ring, K and V tiles through another,
 //                ahead of the item at work.
 //   warp 9       issues the products: S = Q K^T, O += P V (P from tensor memory, V

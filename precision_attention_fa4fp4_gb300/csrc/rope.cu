@@ -167,7 +167,7 @@ struct Tables {
 
 
 // U rows of a lane group are on their way at a time: 3, with 3 CTAs on a
-// multiprocessor and as many in the grid (24 + 24 heads of 32760 tokens: 134 us, 0.90
+// multiprocessor and as many in the grid (24 + 24 heads of 32760 tokens: 137 us, 0.88
 // of measured HBM; 4 rows and 2 CTAs 144, 2 and 4 150; a CTA for every 8 tokens 145).
 constexpr int FWD_CTAS = 3;
 template <int D, bool PAIRS, int U>
