@@ -446,8 +446,8 @@ FA4FP4_API fa4fp4_status fa4fp4_cache_evict(const fa4fp4_cache* cache, const int
  * multiples of 16 bytes, at least 0 and at most 2^40 bytes.  An input may have
  * strides of 0 (a broadcast).  The rows of an output overlap neither each other nor,
  * where not said otherwise, anything else of the call.  d is 64 or 128; B N is at
- * most 2^30, heads are at most 2^20, and for the attention B Hq Nq and B Hkv Nk are
- * below 2^31, B Hq at most 2^24 (FA4FP4_ERR_UNSUPPORTED). */
+ * most 2^30, heads are at most 2^20, rows in all at most 2^36, and for the attention B
+ * Hq Nq and B Hkv Nk are below 2^31, B Hq at most 2^24 (FA4FP4_ERR_UNSUPPORTED). */
 typedef struct {
   void* ptr;
   int64_t stride_b, stride_h, stride_n;

@@ -49,6 +49,13 @@ fa4fp4_status check_dims(int B, int Hq, int Hkv, int N, int d) {
   return FA4FP4_OK;
 }
 
+// Of the norm and rotation: tasks of 128 rows and more, and one for each token, stay within 31 bits.
+fa4fp4_status check_rows_in_all(int B, int Hq, int Hkv, int N, int d) {
+  const fa4fp4_status s = check_dims(B, Hq, Hkv, N, d);
+  if (s != FA4FP4_OK) return s;
+  return (long long)B * N * (Hq + Hkv) > (1LL << 36) ? FA4FP4_ERR_UNSUPPORTED : FA4FP4_OK;
+}
+
 fa4fp4_status check_norm(const fa4fp4_norm* norm) {
   if (!norm) return FA4FP4_OK;
   if (norm->weight_dtype != FA4FP4_OUT_F32 && norm->weight_dtype != FA4FP4_OUT_BF16) return FA4FP4_ERR_INVALID_ARG;
@@ -127,7 +134,7 @@ extern "C" {
 fa4fp4_status fa4fp4_norm_rope(const fa4fp4_heads* q, const fa4fp4_heads* k, int B, int Hq, int Hkv, int N, int d,
                                const fa4fp4_norm* norm, const fa4fp4_rotation* rotation, const fa4fp4_heads* q_out,
                                const fa4fp4_heads* k_out, void* stream) {
-  fa4fp4_status s = check_dims(B, Hq, Hkv, N, d);
+  fa4fp4_status s = check_rows_in_all(B, Hq, Hkv, N, d);
   if (s != FA4FP4_OK) return s;
   if ((!norm && !rotation) || (!k && Hkv != 0)) return FA4FP4_ERR_INVALID_ARG;
   if (B == 0 || N == 0 || Hq + Hkv == 0) return FA4FP4_OK;
@@ -150,7 +157,7 @@ fa4fp4_status fa4fp4_norm_rope(const fa4fp4_heads* q, const fa4fp4_heads* k, int
 }
 
 size_t fa4fp4_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int d) {
-  if (check_dims(B, Hq, Hkv, N, d) != FA4FP4_OK || B == 0 || N == 0 || Hq + Hkv == 0) return 0;
+  if (check_rows_in_all(B, Hq, Hkv, N, d) != FA4FP4_OK || B == 0 || N == 0 || Hq + Hkv == 0) return 0;
   int ctas[2];
   rope_bwd_ctas(B, Hq, Hkv, N, d, ctas);
   return (size_t)(ctas[0] + ctas[1]) * d * sizeof(float);
@@ -161,7 +168,7 @@ fa4fp4_status fa4fp4_norm_rope_bwd(const fa4fp4_heads* dq_out, const fa4fp4_head
                                    const fa4fp4_norm* norm, const fa4fp4_rotation* rotation, const fa4fp4_heads* dq,
                                    const fa4fp4_heads* dk, float* dq_weight, float* dk_weight, void* workspace,
                                    size_t workspace_bytes, void* stream) {
-  fa4fp4_status s = check_dims(B, Hq, Hkv, N, d);
+  fa4fp4_status s = check_rows_in_all(B, Hq, Hkv, N, d);
   if (s != FA4FP4_OK) return s;
   if (dout_dtype != FA4FP4_OUT_F32 && dout_dtype != FA4FP4_OUT_BF16) return FA4FP4_ERR_INVALID_ARG;
   if ((!norm && !rotation) || (!k && Hkv != 0)) return FA4FP4_ERR_INVALID_ARG;

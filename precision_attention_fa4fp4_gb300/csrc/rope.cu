@@ -250,148 +250,64 @@ __global__ void __launch_bounds__(WARPS * 32, FWD_CTAS)
   }
 }
 
-// Gradients.  The CTAs [0, ctas[0]) work on q, the others on k; every lane adds
-// its 16 channels of the weight's gradient over its tasks, the CTA joins them in
-// a fixed order and leaves one row of partials.  A row's x and gradient are on their
-// way while the row before is at work.  2 CTAs on a multiprocessor: a lane's sums,
-// weights, sines and cosines and two rows take 128 registers (at 85, for 3 CTAs, they
-// spill: 132 -> 210 us for 2 x 8192 tokens of 32 + 8 heads with f32 gradients; rows
-// ahead by asynchronous copies to shared memory 157).
-// Far rows are left to a second pass over the tasks of a warp that met any: formed where they are met, they took 126
-// -> 138 us of calls without any, in registers.
-constexpr int BWD_CTAS = 2;
-template <int D, bool PAIRS, bool F32>
-__global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
-    norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, int chunk, int nq, int nk, Divisor by_tokens,
-                         Divisor by_n) {
-  constexpr int LANES = D / 16, ROWS = 32 / LANES;
-  __shared__ Tables<D> tab;
-  __shared__ float join[WARPS][D];
-  __shared__ int again[WARPS];                 // has the warp met rows that are far?
-  next_may_start();
-  wait_for_previous();
-  tab.load(p);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % LANES, sub = lane / LANES;
-  const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
-  if (lane == 0) again[warp] = 0;
-  __syncwarp();
-  const int t = (int)blockIdx.x >= p.ctas[0];
-  const int cta = t ? (int)blockIdx.x - p.ctas[0] : (int)blockIdx.x;
-  const RopeTensor& T = p.t[t];
-  float2 da[4], db[4], wa[4], wb[4];
-  tab.template weights<PAIRS>(t, c0, c1, wa, wb);
+// What a lane holds of a row of x and of the output's gradient on their way.
+template <bool F32>
+struct RowPair {
+  uint4 u, v;
+  float4 g[F32 ? 4 : 2];
+
+  // (a row that is not there: its gradient is 0)
+  FA4_DEV void none() {
+    u = v = ones();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) da[j] = db[j] = both(0.f);
-  const auto pass = [&](auto only_far) {
-    constexpr bool FAR = decltype(only_far)::value;
-    for (Tasks task{(uint32_t)(cta * WARPS + warp), (uint32_t)(p.ctas[t] * WARPS), (uint32_t)by_tokens.d * (t ? nk : nq)};
-         task.more(); task.next()) {
-      int part, m, b, n;
-      divide((int)task.now, by_tokens, part, m);
-      divide(m, by_n, b, n);
-      const int h0 = part * chunk, h1 = min(T.H, h0 + chunk);
-      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(T.x.p) + b * T.x.b + n * T.x.n;
-      const long long dy = b * T.dy.b + n * T.dy.n;
-      __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(T.out.p) + b * T.out.b + n * T.out.n;
-      float2 c[4], s[4];
-      uint4 u, v;
-      float4 g[F32 ? 4 : 2];
-      auto fetch = [&](int h) {
-        u = v = ones();
-#pragma unroll
-        for (int i = 0; i < (F32 ? 4 : 2); ++i) g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h >= h1) return;
-        const __nv_bfloat16* row = x + h * T.x.h;
-        u = *reinterpret_cast<const uint4*>(row + c0);
-        v = *reinterpret_cast<const uint4*>(row + c1);
-        if (F32) {
-          const float* from = static_cast<const float*>(T.dy.p) + dy + h * T.dy.h;
-          g[0] = *reinterpret_cast<const float4*>(from + c0);
-          g[1] = *reinterpret_cast<const float4*>(from + c0 + 4);
-          g[F32 ? 2 : 0] = *reinterpret_cast<const float4*>(from + c1);
-          g[F32 ? 3 : 0] = *reinterpret_cast<const float4*>(from + c1 + 4);
-        } else {
-          const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(T.dy.p) + dy + h * T.dy.h;
-          g[0] = *reinterpret_cast<const float4*>(from + c0);
-          g[1] = *reinterpret_cast<const float4*>(from + c1);
-        }
-      };
-      fetch(h0 + sub);
-      angles(p, tab.turn, tab.axis, b, n, l, c, s);
-      for (int h = h0 + sub; h - sub < h1; h += ROWS) {
-        bool on = h < h1;
-        float2 ga[4], gb[4], fa[4], fb[4];
-        unpack<PAIRS>(u, v, fa, fb);
-        if constexpr (F32) unpack<PAIRS>(g, ga, gb);
-        else unpack<PAIRS>(*reinterpret_cast<const uint4*>(&g[0]), *reinterpret_cast<const uint4*>(&g[1]), ga, gb);
-        fetch(h + ROWS);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 e = ga[j];
-          ga[j] = ffma2(gb[j], s[j], fmul2(e, c[j]));
-          gb[j] = ffma2(neg(e), s[j], fmul2(gb[j], c[j]));
-        }
-        if (p.norm) {
-          float2 xx = both(0.f), ux = both(0.f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            xx = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], xx));
-            ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
-          }
-          const float sx = row_sum<LANES>(xx.x + xx.y), su = row_sum<LANES>(ux.x + ux.y);
-          // the rows of the other pass add nothing (nor do those that are not there: their gradient is 0)
-          const float ms = sx * (1.f / D) + p.eps;
-          const bool here = far(ms) == FAR;
-          if (!here) {
-            if (!FAR) again[warp] = 1;
-            on = false;
-          }
-          if constexpr (FAR) {
-            const Unit by(ms);
-            const float root = by.root(row_sum<LANES>(by.squares(fa, fb)), 1.f / D, p.eps);
-            ux = both(0.f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              fa[j] = by.apply(fa[j], root);
-              fb[j] = by.apply(fb[j], root);
-              ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
-            }
-            const float r = root * by.unit, k = row_sum<LANES>(ux.x + ux.y) * (1.f / D);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (on) {
-                da[j] = ffma2(ga[j], fa[j], da[j]);
-                db[j] = ffma2(gb[j], fb[j], db[j]);
-              }
-              ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
-              gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
-            }
-          } else {
-            const float r = here ? rsqrtf(ms) : 0.f;
-            const float k = r * r * su * (1.f / D);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              da[j] = ffma2(ga[j], fmul2(fa[j], both(r)), da[j]);
-              db[j] = ffma2(gb[j], fmul2(fb[j], both(r)), db[j]);
-              ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
-              gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
-            }
-          }
-        }
-        if (on) {
-          uint4 yu, yv;
-          pack<PAIRS>(ga, gb, yu, yv);
-          __nv_bfloat16* row = dx + h * T.out.h;
-          *reinterpret_cast<uint4*>(row + c0) = yu;
-          *reinterpret_cast<uint4*>(row + c1) = yv;
-        }
-      }
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  FA4_DEV void fetch(const __nv_bfloat16* x, const void* dy, long long at, int c0, int c1) {
+    u = *reinterpret_cast<const uint4*>(x + c0);
+    v = *reinterpret_cast<const uint4*>(x + c1);
+    if (F32) {
+      const float* from = static_cast<const float*>(dy) + at;
+      g[0] = *reinterpret_cast<const float4*>(from + c0);
+      g[1] = *reinterpret_cast<const float4*>(from + c0 + 4);
+      g[F32 ? 2 : 0] = *reinterpret_cast<const float4*>(from + c1);
+      g[F32 ? 3 : 0] = *reinterpret_cast<const float4*>(from + c1 + 4);
+    } else {
+      const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(dy) + at;
+      g[0] = *reinterpret_cast<const float4*>(from + c0);
+      g[1] = *reinterpret_cast<const float4*>(from + c1);
     }
-  };
-  pass(std::false_type());
-  __syncwarp();
-  if (again[warp]) pass(std::true_type());
-  if (!T.dw) return;
+  }
+  template <bool PAIRS>
+  FA4_DEV void take(float2 (&fa)[4], float2 (&fb)[4], float2 (&ga)[4], float2 (&gb)[4]) const {
+    unpack<PAIRS>(u, v, fa, fb);
+    if constexpr (F32) unpack<PAIRS>(g, ga, gb);
+    else unpack<PAIRS>(*reinterpret_cast<const uint4*>(&g[0]), *reinterpret_cast<const uint4*>(&g[1]), ga, gb);
+  }
+};
+
+// A gradient turned back.
+FA4_DEV void turn_back(float2 (&ga)[4], float2 (&gb)[4], const float2 (&c)[4], const float2 (&s)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 e = ga[j];
+    ga[j] = ffma2(gb[j], s[j], fmul2(e, c[j]));
+    gb[j] = ffma2(neg(e), s[j], fmul2(gb[j], c[j]));
+  }
+}
+
+template <bool PAIRS>
+FA4_DEV void put(__nv_bfloat16* row, int c0, int c1, const float2 (&a)[4], const float2 (&b)[4]) {
+  uint4 u, v;
+  pack<PAIRS>(a, b, u, v);
+  *reinterpret_cast<uint4*>(row + c0) = u;
+  *reinterpret_cast<uint4*>(row + c1) = v;
+}
+
+// A warp's sums of the weight's gradient, over its rows of lanes, by channels.
+template <int D, bool PAIRS, class F>
+FA4_DEV void by_channel(const float2 (&da)[4], const float2 (&db)[4], F to) {
+  constexpr int LANES = D / 16;
+  const int lane = threadIdx.x % 32, c0 = word0<D, PAIRS>(lane % LANES), c1 = word1<D, PAIRS>(lane % LANES);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float ya = j % 2 ? da[j / 2].y : da[j / 2].x, yb = j % 2 ? db[j / 2].y : db[j / 2].x;
@@ -400,11 +316,162 @@ __global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
       ya += __shfl_xor_sync(0xffffffffu, ya, o);
       yb += __shfl_xor_sync(0xffffffffu, yb, o);
     }
-    if (sub == 0) {
-      join[warp][PAIRS ? c0 + 2 * j : c0 + j] = ya;
-      join[warp][PAIRS ? c0 + 2 * j + 1 : c1 + j] = yb;
+    if (lane < LANES) {
+      to(PAIRS ? c0 + 2 * j : c0 + j, ya);
+      to(PAIRS ? c0 + 2 * j + 1 : c1 + j, yb);
     }
   }
+}
+
+// Gradients.  The CTAs [0, ctas[0]) work on q, the others on k; every lane adds
+// its 16 channels of the weight's gradient over its tasks, the CTA joins them in
+// a fixed order and leaves one row of partials.  A row's x and gradient are on their
+// way while the row before is at work.  2 CTAs on a multiprocessor: a lane's sums,
+// weights, sines and cosines and two rows take 128 registers (at 85, for 3 CTAs, they
+// spill: 132 -> 210 us for 2 x 8192 tokens of 32 + 8 heads with f32 gradients; rows
+// ahead by asynchronous copies to shared memory 157).
+// Far rows are left out and told to shared memory; behind a task that had some the loop
+// over the tasks is left for them.  (dx may lie in x's place: theirs is not written before.)
+// Formed inside that loop they cost calls without such rows a tenth, in registers (126
+// -> 138 us), as a call of their own 154.
+constexpr int BWD_CTAS = 2;
+template <int D, bool PAIRS, bool F32>
+__global__ void __launch_bounds__(WARPS * 32, BWD_CTAS)
+    norm_rope_bwd_kernel(const __grid_constant__ RopeParams p, int chunk, int nq, int nk, Divisor by_tokens,
+                         Divisor by_n) {
+  constexpr int LANES = D / 16, ROWS = 32 / LANES;
+  __shared__ Tables<D> tab;
+  __shared__ float join[WARPS][D];
+  __shared__ uint32_t left_out[WARPS][ROWS];   // rounds whose row is far
+  next_may_start();
+  wait_for_previous();
+  tab.load(p);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % LANES, sub = lane / LANES;
+  const int c0 = word0<D, PAIRS>(l), c1 = word1<D, PAIRS>(l);
+  if (l == 0) left_out[warp][sub] = 0;
+  __syncwarp();
+  const int t = (int)blockIdx.x >= p.ctas[0];
+  const int cta = t ? (int)blockIdx.x - p.ctas[0] : (int)blockIdx.x;
+  const RopeTensor& T = p.t[t];
+  float2 da[4], db[4], wa[4], wb[4];
+  tab.template weights<PAIRS>(t, c0, c1, wa, wb);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) da[j] = db[j] = both(0.f);
+  // a task's heads and where its rows lie
+  struct Place {
+    int b, n, h0, h1;
+    const __nv_bfloat16* x;
+    __nv_bfloat16* dx;
+    long long dy;
+  };
+  const auto place = [&](uint32_t task) {
+    Place a;
+    int part, m;
+    divide((int)task, by_tokens, part, m);
+    divide(m, by_n, a.b, a.n);
+    a.h0 = part * chunk;
+    a.h1 = min(T.H, a.h0 + chunk);
+    a.x = static_cast<const __nv_bfloat16*>(T.x.p) + a.b * T.x.b + a.n * T.x.n;
+    a.dx = static_cast<__nv_bfloat16*>(T.out.p) + a.b * T.out.b + a.n * T.out.n;
+    a.dy = a.b * T.dy.b + a.n * T.dy.n;
+    return a;
+  };
+  const auto fetch = [&](const Place& a, int h, RowPair<F32>& row) {
+    row.none();
+    if (h < a.h1) row.fetch(a.x + h * T.x.h, T.dy.p, a.dy + h * T.dy.h, c0, c1);
+  };
+  Tasks task{(uint32_t)(cta * WARPS + warp), (uint32_t)(p.ctas[t] * WARPS), (uint32_t)by_tokens.d * (t ? nk : nq)};
+  while (task.more()) {
+    uint32_t mine = 0, last = 0;
+    for (; task.more(); task.next()) {
+      const Place a = place(task.now);
+      float2 c[4], s[4];
+      RowPair<F32> next;
+      fetch(a, a.h0 + sub, next);
+      angles(p, tab.turn, tab.axis, a.b, a.n, l, c, s);
+      for (int h = a.h0 + sub; h - sub < a.h1; h += ROWS) {
+        bool on = h < a.h1;
+        float2 ga[4], gb[4], fa[4], fb[4];
+        next.template take<PAIRS>(fa, fb, ga, gb);
+        fetch(a, h + ROWS, next);
+        turn_back(ga, gb, c, s);
+        if (p.norm) {
+          float2 xx = both(0.f), ux = both(0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            xx = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], xx));
+            ux = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], ux));
+          }
+          const float sx = row_sum<LANES>(xx.x + xx.y), su = row_sum<LANES>(ux.x + ux.y);
+          const float ms = sx * (1.f / D) + p.eps;
+          const bool wait = far(ms);
+          if (wait) {
+            left_out[warp][sub] |= 1u << (h - a.h0) / ROWS;      // (the same by all lanes of the row)
+            on = false;
+          }
+          // (rows that are left out add nothing)
+          const float r = wait ? 0.f : rsqrtf(ms);
+          const float k = r * r * su * (1.f / D);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            da[j] = ffma2(ga[j], fmul2(fa[j], both(r)), da[j]);
+            db[j] = ffma2(gb[j], fmul2(fb[j], both(r)), db[j]);
+            ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
+            gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
+          }
+        }
+        if (on) put<PAIRS>(a.dx + h * T.out.h, c0, c1, ga, gb);
+      }
+      __syncwarp();
+      mine = left_out[warp][sub];
+      if (__any_sync(0xffffffffu, mine)) {
+        last = task.now;
+        task.next();
+        break;
+      }
+    }
+    uint32_t all = __reduce_or_sync(0xffffffffu, mine);
+    if (!all) break;
+    // the far rows of the last task
+    const Place a = place(last);
+    float2 c[4], s[4];
+    angles(p, tab.turn, tab.axis, a.b, a.n, l, c, s);
+    for (; all; all &= all - 1) {
+      const int round = __ffs(all) - 1, h = a.h0 + round * ROWS + sub;
+      const bool on = (mine >> round & 1) && h < a.h1;
+      RowPair<F32> row;
+      fetch(a, on ? h : a.h1, row);
+      float2 ga[4], gb[4], fa[4], fb[4];
+      row.template take<PAIRS>(fa, fb, ga, gb);
+      turn_back(ga, gb, c, s);
+      float2 q = both(0.f), un = both(0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q = ffma2(fa[j], fa[j], ffma2(fb[j], fb[j], q));
+      const Unit by(row_sum<LANES>(q.x + q.y) * (1.f / D) + p.eps);
+      const float root = by.root(row_sum<LANES>(by.squares(fa, fb)), 1.f / D, p.eps);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        fa[j] = by.apply(fa[j], root);
+        fb[j] = by.apply(fb[j], root);
+        un = ffma2(fmul2(ga[j], wa[j]), fa[j], ffma2(fmul2(gb[j], wb[j]), fb[j], un));
+      }
+      const float r = root * by.unit, k = row_sum<LANES>(un.x + un.y) * (1.f / D);
+      if (!on) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        da[j] = ffma2(ga[j], fa[j], da[j]);
+        db[j] = ffma2(gb[j], fb[j], db[j]);
+        ga[j] = fmul2(ffma2(fa[j], both(-k), fmul2(ga[j], wa[j])), both(r));
+        gb[j] = fmul2(ffma2(fb[j], both(-k), fmul2(gb[j], wb[j])), both(r));
+      }
+      put<PAIRS>(a.dx + h * T.out.h, c0, c1, ga, gb);
+    }
+    __syncwarp();
+    left_out[warp][sub] = 0;
+    __syncwarp();
+  }
+  if (!T.dw) return;
+  by_channel<D, PAIRS>(da, db, [&](int i, float y) { join[warp][i] = y; });
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += WARPS * 32) {
     float sum = 0.f;
@@ -437,6 +504,8 @@ __global__ void __launch_bounds__(DW_WARPS * 32) norm_rope_dw_kernel(const __gri
 
 // Heads of a warp's task: all of a tensor's where there are tokens enough to fill
 // the GPU with one warp each, else as few as one round of its lanes.
+// A task of the gradients has 32 rounds at most.
+constexpr int BWD_ROUNDS = 32;
 int chunk_of(long long tokens, int H, int rows) {
   const long long want = (long long)sm_count() * 16;
   if (H <= rows || tokens >= want) return H > 0 ? H : 1;
@@ -444,6 +513,11 @@ int chunk_of(long long tokens, int H, int rows) {
   const long long rounds = (H + rows - 1) / rows;
   const long long per = (rounds + parts - 1) / parts;
   return (int)(per * rows);
+}
+
+int bwd_chunk_of(long long tokens, int H, int rows) {
+  const int chunk = chunk_of(tokens, H, rows);
+  return chunk < BWD_ROUNDS * rows ? chunk : BWD_ROUNDS * rows;
 }
 
 int parts_of(int H, int chunk) { return (H + chunk - 1) / chunk; }
@@ -465,7 +539,7 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t st) {
 void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas) {
   const int rows = 32 / (d / 16);
   const long long tokens = (long long)B * N;
-  const int chunk = chunk_of(tokens, Hq > Hkv ? Hq : Hkv, rows);
+  const int chunk = bwd_chunk_of(tokens, Hq > Hkv ? Hq : Hkv, rows);
   const long long room = (long long)sm_count() * BWD_CTAS;
   const int H[2] = {Hq, Hkv};
   for (int t = 0; t < 2; ++t) {
@@ -478,7 +552,7 @@ void rope_bwd_ctas(int B, int Hq, int Hkv, int N, int d, int* ctas) {
 
 cudaError_t launch_norm_rope_bwd(const RopeParams& p, cudaStream_t st) {
   const int rows = 32 / (p.d / 16);
-  const int chunk = chunk_of((long long)p.B * p.N, p.t[0].H > p.t[1].H ? p.t[0].H : p.t[1].H, rows);
+  const int chunk = bwd_chunk_of((long long)p.B * p.N, p.t[0].H > p.t[1].H ? p.t[0].H : p.t[1].H, rows);
   const int nq = parts_of(p.t[0].H, chunk), nk = parts_of(p.t[1].H, chunk);
   const Divisor by_tokens(p.B * p.N), by_n(p.N);
   auto pick = [&](auto f32) {

@@ -68,3 +68,13 @@ def test_no_query_heads_is_checked():
         None, None, None, None, None, None, None, 1, 0, Hkv, 4, Nk, 64, ctypes.c_float(0.0), None, None, None, None,
         ctypes.c_size_t(0), None)
     assert call(2, 8) == 1 and call(0, 8) == 0 and call(2, 0) == 0
+
+
+def test_rows_are_counted_in_32_bits():
+    """Sizes whose tasks would not be: refused before anything is looked at."""
+    build.build()
+    lib = api.load_library()
+    for B, H, N, status in ((1 << 15, 64, 1 << 15, 2), (1 << 10, 1 << 20, 1 << 10, 2), (1 << 10, 1 << 19, 1 << 6, 1)):
+        assert lib.fa4fp4_norm_rope(None, None, B, H, H, N, 64, None, None, None, None, None) == status
+        assert lib.fa4fp4_norm_rope_bwd(None, None, 0, None, None, B, H, H, N, 64, None, None, None, None, None, None, None,
+                                        ctypes.c_size_t(0), None) == status

@@ -311,3 +311,53 @@ def test_rows_of_every_size(fa, d, interleaved, eps):
         want, bound, want_w, bound_w = ref.norm_rope_bwd(dy.to(dt), x, w, th, interleaved, True, eps)
         ref.assert_within(dx, want, bound, "dx")
         ref.assert_within(dw, want_w, bound_w, "dw")
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_of_every_size_in_place(fa, f32, eps):
+    """Gradients in their rows' places, among which are rows beyond FP32's squares and others whose gradients are far too
+    small or large: what a row's place holds by then is not taken for the row."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    B, H, N, d = 2, 150, 40, 64
+    new = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    sizes = torch.tensor([0, 0, 0, 100, -40, 45] + ([-70] if eps == 0 else [60]), device="cuda").float()
+    x = (new(B, H, N, d) * 2.0 ** sizes[torch.randint(0, 7, (B, H, N, 1), generator=g, device="cuda")]).to(torch.bfloat16)
+    dy = new(B, H, N, d) * 2.0 ** sizes[torch.randint(0, 6, (B, H, N, 1), generator=g, device="cuda")].clamp(-60, 45)
+    dy[:, ::5] = 0.0
+    dy = dy.to(torch.float32 if f32 else torch.bfloat16)
+    w = 1 + 0.2 * new(d)
+    pos = torch.randint(0, 5000, (B, 1, N), generator=g, device="cuda").int()
+    args = (pos, fa.rope_freqs(d), w)
+    want = fa.qk_norm_rope_bwd(dy, None, x, None, *args, eps=eps)
+    dx, bound, _, _ = ref.norm_rope_bwd(dy, x, w, ref.turns(pos, args[1], [d // 2]), False, True, eps)
+    ref.assert_within(want[0], dx, bound, "dx")
+    got = fa.qk_norm_rope_bwd(dy, None, x, None, *args, eps=eps, dq=x)
+    assert got[0] is x and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    y = fa.qk_norm_rope(x, None, *args, eps=1e-6)[0]
+    assert torch.equal(fa.qk_norm_rope(x, None, *args, eps=1e-6, q_out=x)[0], y)
+
+
+@pytest.mark.parametrize("d,H", [(64, 300), (128, 131)])
+def test_many_heads_of_many_tokens(fa, d, H):
+    """More heads than a warp takes at a time, with tokens enough for every warp; every row of some tokens beyond FP32's
+    squares."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    N = 3001
+    x = torch.randn((1, N, H, d), generator=g, device="cuda")
+    x[:, 5::700] *= 2.0 ** 70
+    x = x.to(torch.bfloat16).transpose(1, 2)
+    dy = torch.randn((1, N, H, d), generator=g, device="cuda").to(torch.bfloat16).transpose(1, 2)
+    w = 1 + 0.2 * torch.randn(d, generator=g, device="cuda")
+    pos = torch.arange(N, device="cuda", dtype=torch.int32)[None]
+    freqs = fa.rope_freqs(d)
+    th = ref.turns(pos[None], freqs, [d // 2])
+    y, _ = fa.qk_norm_rope(x, None, pos, freqs, w)
+    dx, _, dw, _ = fa.qk_norm_rope_bwd(dy, None, x, None, pos, freqs, w)
+    for h in range(0, H, 50):
+        at = slice(h, min(H, h + 50))
+        ref.assert_within(y[:, at], *ref.norm_rope(x[:, at], w, th, False, True, 1e-6), "y")
+        want, bound, _, _ = ref.norm_rope_bwd(dy[:, at], x[:, at], w, th, False, True, 1e-6)
+        ref.assert_within(dx[:, at], want, bound, "dx")
+    parts = [ref.norm_rope_bwd(dy[:, h: h + 50], x[:, h: h + 50], w, th, False, True, 1e-6)[2:] for h in range(0, H, 50)]
+    ref.assert_within(dw, sum(a for a, _ in parts), sum(b for _, b in parts), "dw")
